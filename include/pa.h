@@ -361,6 +361,100 @@ pa_status pa_decode_shared_prefix_fp8(void *out, const void *query,
                                       int32_t dtype, void *stream);
 
 /*
+ * FP4 KV cache.  The cache stores 4 bits per element and a scale for every 16
+ * of them: an element is an E2M1 code (1 sign, 2 exponent bits with bias 1, 1
+ * fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; no infinities,
+ * no NaN), 16 consecutive elements of a head_dim row share one E4M3 scale (the
+ * codes of "FP8 KV cache", sign clear), and each cache has one fp32 scale
+ * (k_scale, v_scale): code c under scale s stands for k_scale * s * e2m1(c).
+ * 4.5 bits per element: 9/32 of the bytes of a 16-bit cache.
+ * Layout: uint8 [num_blocks, num_kv_heads, block_size * head_dim * 9 / 16].
+ * The bytes of one (block, head) are the codes of its tokens, [block_size,
+ * head_dim / 2], two codes a byte with the even element in the low nibble,
+ * followed by their scales, [block_size, head_dim / 16].  Blocks are copied
+ * (copy-on-write forks) and swapped by pa_swap_blocks, with block_bytes =
+ * num_kv_heads * block_size * head_dim * 9 / 16; a fork within one pool passes
+ * it as src and dst.
+ * For all calls: k_scale, v_scale between 2^-100 and 2^100 (PA_ERR_INVALID_ARG
+ * otherwise); head_dim 64 or 128; block_size 16 or 32; dtype PA_FP16 or
+ * PA_BF16 is the type of the 16-bit tensors.
+ */
+
+/*
+ * pa_reshape_and_cache_fp4 -- pa_reshape_and_cache into FP4 caches.  For every
+ * 16 elements x of a new row, with g the cache's scale and every operation an
+ * IEEE fp32 one:
+ *   s = e4m3(max|x| / (6 g)),   z = s g,   code = e2m1(x * (1 / z)),
+ * both conversions to the nearest value (ties to the even code), magnitudes
+ * beyond 448 and 6 clamped to them.  A group with s = 0 stores zeros; a group
+ * with a NaN in it stores the NaN scale (0x7f) and zero codes, so that it
+ * reads back as NaN; an infinity is stored as 6 * 448 * g.
+ * Other arguments as pa_reshape_and_cache.
+ */
+pa_status pa_reshape_and_cache_fp4(const void *key, const void *value,
+                                   int64_t key_stride, int64_t value_stride,
+                                   void *k_cache, void *v_cache,
+                                   const int64_t *slot_mapping,
+                                   int32_t num_tokens, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                   int32_t src_dtype, float k_scale, float v_scale,
+                                   void *stream);
+
+/*
+ * pa_gather_cache_fp4 -- read cached tokens back as 16-bit rows (the input of a
+ * 16-bit kernel, a transfer to another engine):
+ *
+ *   for every t < num_tokens with slot = slot_mapping[t] >= 0, every h:
+ *     key[t, h, :]   = the K row of head h at that slot, value[t, h, :] its V row
+ *
+ * each element e2m1(code) * (s * k_scale) in fp32 (v_scale for V), rounded once
+ * to dtype.
+ * key, value       device, written: [num_tokens, num_kv_heads, head_dim], row
+ *                  t at element t * key_stride (value_stride), strides as
+ *                  pa_reshape_and_cache's; they must not overlap the caches.
+ * slot_mapping     device int64 [num_tokens]; a negative slot leaves its row
+ *                  as it was; a slot >= num_blocks * block_size does too and
+ *                  sets PA_DEVERR_BAD_SLOT.  Slots may repeat.
+ * Pointers 16-byte aligned.
+ */
+pa_status pa_gather_cache_fp4(void *key, void *value, int64_t key_stride, int64_t value_stride,
+                              const void *k_cache, const void *v_cache,
+                              const int64_t *slot_mapping,
+                              int32_t num_tokens, int32_t num_kv_heads,
+                              int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                              int32_t dtype, float k_scale, float v_scale, void *stream);
+
+/*
+ * pa_decode_fp4 -- pa_decode over FP4 caches.  s * e2m1(c) is exact in fp16
+ * (at most 6 significant bits); both products run in fp16 with fp32
+ * accumulation, k_scale joins the softmax scale and v_scale multiplies the
+ * output; bf16 queries are carried in fp16 as pa_decode_fp8 does.  Other
+ * arguments, partitions and workspace as pa_decode.
+ */
+pa_status pa_decode_fp4(void *out, const void *query,
+                        const void *k_cache, const void *v_cache,
+                        const int32_t *block_tables, int32_t max_blocks_per_seq,
+                        const int32_t *context_lens,
+                        int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                        int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                        float scale, float k_scale, float v_scale,
+                        int32_t max_context_len, int32_t partition_size,
+                        void *workspace, size_t workspace_bytes,
+                        int32_t dtype, void *stream);
+
+/*
+ * pa_prefill_fp4 -- pa_prefill over FP4 caches, the values as in pa_decode_fp4.
+ * Arguments, shapes and error behaviour as pa_prefill_fp8.
+ */
+pa_status pa_prefill_fp4(void *out, const void *query, const int32_t *query_start,
+                         const void *k_cache, const void *v_cache,
+                         const int32_t *block_tables, int32_t max_blocks_per_seq,
+                         const int32_t *context_lens, int32_t num_seqs, int32_t max_q_len,
+                         int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                         int32_t block_size, int64_t num_blocks, float scale,
+                         float k_scale, float v_scale, int32_t dtype, void *stream);
+
+/*
  * pa_copy_blocks -- copy-on-write fork of whole physical blocks ("Serving
  * engines", How vLLM works: sequences share physical blocks until one writes;
  * the write forks only the block being written).

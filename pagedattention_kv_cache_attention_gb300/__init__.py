@@ -28,7 +28,8 @@ __all__ = [
     "PaError", "DEVERR_BAD_BLOCK", "DEVERR_BAD_SLOT", "DEVERR_BAD_LEN", "DEVERR_TIMEOUT",
     "DEVERR_WORKSPACE", "DEVERR_PREFIX", "DECODE_COUNTER_BYTES", "new_decode_workspace",
     "pa_decode_shared_prefix", "pa_decode_shared_prefix_fp8", "pa_prefill_fp8",
-    "pa_copy_blocks_fp8",
+    "pa_copy_blocks_fp8", "new_fp4_cache", "fp4_block_size", "pa_reshape_and_cache_fp4",
+    "pa_gather_cache_fp4", "pa_decode_fp4", "pa_prefill_fp4",
 ]
 
 PA_FP16, PA_BF16 = 0, 1
@@ -96,6 +97,13 @@ def _stream(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _torch_stream(stream):
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = _stream(stream)
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
 
 
 def _check(call: str, status: int) -> None:
@@ -517,6 +525,153 @@ def pa_prefill_fp8(out: torch.Tensor, query: torch.Tensor, query_start: torch.Te
     fp16 or bf16 queries and output."""
     return _prefill("pa_prefill_fp8", out, query, query_start, k_cache, v_cache, block_tables,
                     context_lens, scale, (k_scale, v_scale), max_q_len, stream)
+
+
+def new_fp4_cache(num_blocks: int, num_kv_heads: int, block_size: int, head_dim: int,
+                  device=None) -> torch.Tensor:
+    """A zero-filled FP4 cache (K or V): uint8 [num_blocks, num_kv_heads,
+    block_size * head_dim * 9 / 16], each (block, head) holding its tokens'
+    E2M1 codes [block_size, head_dim / 2] (the even element of a byte in the
+    low nibble) and then their E4M3 scales [block_size, head_dim / 16]."""
+    return torch.zeros(num_blocks, num_kv_heads, block_size * head_dim * 9 // 16,
+                       dtype=torch.uint8,
+                       device=device if device is not None else torch.cuda.current_device())
+
+
+def fp4_block_size(cache: torch.Tensor, head_dim: int) -> int:
+    """Tokens per block of an FP4 cache for heads of ``head_dim``."""
+    if cache.dim() != 3 or cache.shape[2] * 16 % (9 * head_dim):
+        raise ValueError(f"an FP4 cache is uint8 [NB, Hkv, block_size * d * 9 / 16]; "
+                         f"{tuple(cache.shape)} is none for d = {head_dim}")
+    return cache.shape[2] * 16 // (9 * head_dim)
+
+
+def _fp4_caches(k_cache, v_cache, head_dim) -> int:
+    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _cuda(n, t, torch.uint8)
+        if not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache shapes differ")
+    return fp4_block_size(k_cache, head_dim)
+
+
+def _cache_fp4(name, key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, stream):
+    P, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+    f = _blocks_fn(name, [P, P, i64, i64, P, P, P, i32, i32, i32, i32, i64, i32, f32, f32, P])
+    for n, t in (("key", key), ("value", value)):
+        _cuda(n, t, key.dtype)
+        if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+            raise ValueError(f"{n} must be [T, Hkv, d] with heads contiguous inside a token row")
+    T, Hkv, d = key.shape
+    bs = _fp4_caches(k_cache, v_cache, d)
+    if value.shape != key.shape or k_cache.shape[1] != Hkv:
+        raise ValueError("key/value/cache shapes disagree")
+    _cuda("slot_mapping", slot_mapping, torch.int64)
+    if slot_mapping.numel() != T or not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be contiguous, with one entry per token")
+    row = Hkv * d  # the stride of a single row is not looked at
+    _check(name, f(key.data_ptr(), value.data_ptr(), key.stride(0) if T > 1 else row,
+                   value.stride(0) if T > 1 else row, k_cache.data_ptr(), v_cache.data_ptr(),
+                   slot_mapping.data_ptr(), T, Hkv, d, bs, k_cache.shape[0], _dtype_code(key),
+                   float(k_scale), float(v_scale), _stream(stream)))
+
+
+def pa_reshape_and_cache_fp4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
+                             v_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                             k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
+    """Write key/value [T, Hkv, d] (fp16/bf16) into FP4 caches (new_fp4_cache)
+    at slot_mapping[t] (int64; negative = skip), quantised in groups of 16."""
+    _cache_fp4("pa_reshape_and_cache_fp4", key, value, k_cache, v_cache, slot_mapping, k_scale,
+               v_scale, stream)
+
+
+def pa_gather_cache_fp4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
+                        v_cache: torch.Tensor, slot_mapping: torch.Tensor, k_scale: float = 1.0,
+                        v_scale: float = 1.0, stream=None) -> None:
+    """Read cached tokens back: row t of ``key`` and ``value`` (fp16/bf16 [T,
+    Hkv, d], written in place) becomes the values cached at slot_mapping[t]
+    (int64; a negative slot leaves its row as it was)."""
+    _cache_fp4("pa_gather_cache_fp4", key, value, k_cache, v_cache, slot_mapping, k_scale,
+               v_scale, stream)
+
+
+def pa_decode_fp4(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor,
+                  v_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                  scale: float, k_scale: float, v_scale: float, max_context_len: int,
+                  partition_size: int = 0, workspace: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """Paged decode attention over FP4 caches into ``out`` [B, Hq, d] (fp16 or
+    bf16 queries and output).  ``workspace`` as for pa_decode."""
+    P, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+    f = _blocks_fn("pa_decode_fp4", [P, P, P, P, P, i32, P, i32, i32, i32, i32, i32, i64, f32,
+                                     f32, f32, i32, i32, P, sz, i32, P])
+    for n, t in (("out", out), ("query", query)):
+        _cuda(n, t, query.dtype)
+        if not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+    B, Hq, d = query.shape
+    bs = _fp4_caches(k_cache, v_cache, d)
+    for n, t in (("block_tables", block_tables), ("context_lens", context_lens)):
+        _cuda(n, t, torch.int32)
+        if not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+    if out.shape != query.shape:
+        raise ValueError("out and query shapes differ")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.numel() != B:
+        raise ValueError("block_tables must be [B, MB] and context_lens [B]")
+    need = pa_decode_workspace_size(B, Hq, d, max_context_len, partition_size)
+    ws_ptr, ws_bytes = None, 0
+    if need:
+        if workspace is None:
+            # made on the call's own stream: its zeros come before the kernels, and its
+            # memory is not handed on before they are done
+            with torch.cuda.stream(_torch_stream(stream)):
+                workspace = torch.zeros(need, dtype=torch.uint8, device=query.device)
+        _cuda("workspace", workspace)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check("pa_decode_fp4", f(
+        out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, Hq,
+        k_cache.shape[1], d, bs, k_cache.shape[0], float(scale), float(k_scale), float(v_scale),
+        int(max_context_len), int(partition_size), ws_ptr, ws_bytes, _dtype_code(query),
+        _stream(stream)))
+    return out
+
+
+def pa_prefill_fp4(out: torch.Tensor, query: torch.Tensor, query_start: torch.Tensor,
+                   k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                   context_lens: torch.Tensor, scale: float, k_scale: float, v_scale: float,
+                   max_q_len: int, stream=None) -> torch.Tensor:
+    """pa_prefill over FP4 caches, fp16 or bf16 queries and output."""
+    P, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+    f = _blocks_fn("pa_prefill_fp4", [P, P, P, P, P, P, i32, P, i32, i32, i32, i32, i32, i32,
+                                      i64, f32, f32, f32, i32, P])
+    for n, t in (("out", out), ("query", query)):
+        _cuda(n, t, query.dtype)
+        if not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+    total_q, Hq, d = query.shape
+    bs = _fp4_caches(k_cache, v_cache, d)
+    for n, t in (("query_start", query_start), ("block_tables", block_tables),
+                 ("context_lens", context_lens)):
+        _cuda(n, t, torch.int32)
+        if not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+    B = context_lens.numel()
+    if query_start.numel() != B + 1 or out.shape != query.shape:
+        raise ValueError("query_start must have num_seqs + 1 entries; out must match query")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be [B, MB]")
+    _check("pa_prefill_fp4", f(
+        out.data_ptr(), query.data_ptr(), query_start.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+        context_lens.data_ptr(), B, int(max_q_len), Hq, k_cache.shape[1], d, bs,
+        k_cache.shape[0], float(scale), float(k_scale), float(v_scale), _dtype_code(query),
+        _stream(stream)))
+    return out
 
 
 def pa_selftest_bounded_wait(stream=None) -> None:

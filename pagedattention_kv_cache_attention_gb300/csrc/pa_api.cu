@@ -43,6 +43,11 @@ bool dtype_ok(int32_t d) { return d == PA_FP16 || d == PA_BF16; }
 bool fp8_scales_ok(float k_scale, float v_scale) {
   return std::isfinite(k_scale) && std::isfinite(v_scale) && k_scale > 0.f && v_scale > 0.f;
 }
+// FP4 caches: 6 * 448 * scale, scale * 2^-9 and the reciprocals stay normal fp32 numbers.
+bool fp4_scales_ok(float k_scale, float v_scale) {
+  const float lo = 0x1p-100f, hi = 0x1p100f;
+  return k_scale >= lo && k_scale <= hi && v_scale >= lo && v_scale <= hi;
+}
 bool head_dim_ok(int32_t d) { return d == 64 || d == 128; }
 bool block_size_ok(int32_t b) { return b == 16 || b == 32; }
 
@@ -443,28 +448,44 @@ pa_status pa_reshape_and_cache_fp8(const void *key, const void *value, int64_t k
 
 namespace {
 
-pa_status prefill_impl(void *out, const void *query, const int32_t *query_start,
-                       const void *k_cache, const void *v_cache, const int32_t *block_tables,
-                       int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
-                       int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads,
-                       int32_t head_dim, int32_t block_size, int64_t num_blocks, float scale,
-                       int32_t dtype, bool kv_fp8, float k_scale, float v_scale, void *stream) {
+// Every host-side check of the prefill calls but those of the cache scales.
+pa_status prefill_check_args(const void *out, const void *query, const int32_t *query_start,
+                             const void *k_cache, const void *v_cache,
+                             const int32_t *block_tables, int32_t max_blocks_per_seq,
+                             const int32_t *context_lens, int32_t num_seqs, int32_t max_q_len,
+                             int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                             int32_t block_size, int64_t num_blocks, float scale, int32_t dtype) {
   if (num_seqs < 0 || max_q_len < 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
       num_blocks <= 0 || max_blocks_per_seq <= 0 || !dtype_ok(dtype) || !std::isfinite(scale) ||
       !(scale > 0.f))
     return PA_ERR_INVALID_ARG;
   if (num_q_heads % num_kv_heads) return PA_ERR_INVALID_ARG;
-  const int32_t group = num_q_heads / num_kv_heads;
-  if (!head_dim_ok(head_dim) || !block_size_ok(block_size) || group > 8)
+  if (!head_dim_ok(head_dim) || !block_size_ok(block_size) || num_q_heads / num_kv_heads > 8)
     return PA_ERR_UNSUPPORTED;
   if (num_seqs == 0 || max_q_len == 0) return PA_OK;
   if (!out || !query || !query_start || !k_cache || !v_cache || !block_tables || !context_lens)
     return PA_ERR_INVALID_ARG;
   if (!aligned16(out) || !aligned16(query) || !aligned16(k_cache) || !aligned16(v_cache))
     return PA_ERR_INVALID_ARG;
-  const int64_t pool_rows = num_blocks * num_kv_heads * block_size;
-  if (pool_rows >= (int64_t(1) << 31) || num_seqs > 65535 || num_kv_heads > 65535)
+  if (num_blocks * num_kv_heads * block_size >= (int64_t(1) << 31) || num_seqs > 65535 ||
+      num_kv_heads > 65535)
     return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+pa_status prefill_impl(void *out, const void *query, const int32_t *query_start,
+                       const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                       int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+                       int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads,
+                       int32_t head_dim, int32_t block_size, int64_t num_blocks, float scale,
+                       int32_t dtype, bool kv_fp8, float k_scale, float v_scale, void *stream) {
+  const pa_status st = prefill_check_args(
+      out, query, query_start, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+      num_seqs, max_q_len, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+      dtype);
+  if (st != PA_OK || num_seqs == 0 || max_q_len == 0) return st;
+  const int32_t group = num_q_heads / num_kv_heads;
+  const int64_t pool_rows = num_blocks * num_kv_heads * block_size;
   unsigned int *err = nullptr;
   if (error_word(&err) != cudaSuccess) return PA_ERR_CUDA;
   pa::PrefillArgs a{};
@@ -517,6 +538,156 @@ pa_status pa_prefill_fp8(void *out, const void *query, const int32_t *query_star
   return prefill_impl(out, query, query_start, k_cache, v_cache, block_tables, max_blocks_per_seq,
                       context_lens, num_seqs, max_q_len, num_q_heads, num_kv_heads, head_dim,
                       block_size, num_blocks, scale, dtype, true, k_scale, v_scale, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// The FP4 write (write = true) and read-back share their arguments and checks.
+pa_status cache_fp4_impl(bool write, void *key, void *value, int64_t key_stride,
+                         int64_t value_stride, void *k_cache, void *v_cache,
+                         const int64_t *slot_mapping, int32_t num_tokens, int32_t num_kv_heads,
+                         int32_t head_dim, int32_t block_size, int64_t num_blocks, int32_t dtype,
+                         float k_scale, float v_scale, void *stream) {
+  if (num_tokens < 0 || num_kv_heads <= 0 || num_blocks <= 0 || !dtype_ok(dtype) ||
+      !fp4_scales_ok(k_scale, v_scale))
+    return PA_ERR_INVALID_ARG;
+  if (!head_dim_ok(head_dim) || !block_size_ok(block_size)) return PA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return PA_OK;
+  if (!key || !value || !k_cache || !v_cache || !slot_mapping) return PA_ERR_INVALID_ARG;
+  if (!aligned16(key) || !aligned16(value) || !aligned16(k_cache) || !aligned16(v_cache))
+    return PA_ERR_INVALID_ARG;
+  const int64_t row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (key_stride < row || value_stride < row || key_stride % 8 || value_stride % 8)
+    return PA_ERR_INVALID_ARG;
+  // the launch is one-dimensional over the groups of 16, at least 128 to a CTA
+  if (num_kv_heads > 65535 || num_tokens * (row / 16) > (int64_t(1) << 37))
+    return PA_ERR_UNSUPPORTED;
+  unsigned int *err = nullptr;
+  if (error_word(&err) != cudaSuccess) return PA_ERR_CUDA;
+  pa::Fp4CacheArgs a;
+  a.key = key;
+  a.value = value;
+  a.key_stride = key_stride;
+  a.value_stride = value_stride;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.slot_mapping = slot_mapping;
+  a.num_tokens = num_tokens;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.bs_log2 = block_size == 16 ? 4 : 5;
+  a.num_blocks = num_blocks;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.err = err;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  return (write ? pa::launch_cache_fp4_write(a, dtype, cs)
+                : pa::launch_cache_fp4_read(a, dtype, cs)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+pa_status attn_fp4_impl(void *out, const void *query, const int32_t *query_start,
+                        const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                        int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
+                        int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads,
+                        int32_t head_dim, int32_t block_size, int64_t num_blocks, float scale,
+                        float k_scale, float v_scale, int32_t max_context_len, int32_t dtype,
+                        void *stream) {
+  unsigned int *err = nullptr;
+  if (error_word(&err) != cudaSuccess) return PA_ERR_CUDA;
+  pa::Fp4AttnArgs a{};
+  a.out = out;
+  a.query = query;
+  a.query_start = query_start;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.group = num_q_heads / num_kv_heads;
+  a.bs_log2 = block_size == 16 ? 4 : 5;
+  a.max_q_len = max_q_len;
+  a.max_context_len = max_context_len;
+  a.num_blocks = num_blocks;
+  a.scale_log2 = scale * 1.4426950408889634f * k_scale;
+  a.out_scale = v_scale;
+  a.err = err;
+  return pa::launch_attn_fp4(a, head_dim, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_reshape_and_cache_fp4(const void *key, const void *value, int64_t key_stride,
+                                   int64_t value_stride, void *k_cache, void *v_cache,
+                                   const int64_t *slot_mapping, int32_t num_tokens,
+                                   int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                   int64_t num_blocks, int32_t src_dtype, float k_scale,
+                                   float v_scale, void *stream) {
+  return cache_fp4_impl(true, const_cast<void *>(key), const_cast<void *>(value), key_stride,
+                        value_stride, k_cache, v_cache, slot_mapping, num_tokens, num_kv_heads,
+                        head_dim, block_size, num_blocks, src_dtype, k_scale, v_scale, stream);
+}
+
+pa_status pa_gather_cache_fp4(void *key, void *value, int64_t key_stride, int64_t value_stride,
+                              const void *k_cache, const void *v_cache,
+                              const int64_t *slot_mapping, int32_t num_tokens,
+                              int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                              int64_t num_blocks, int32_t dtype, float k_scale, float v_scale,
+                              void *stream) {
+  return cache_fp4_impl(false, key, value, key_stride, value_stride, const_cast<void *>(k_cache),
+                        const_cast<void *>(v_cache), slot_mapping, num_tokens, num_kv_heads,
+                        head_dim, block_size, num_blocks, dtype, k_scale, v_scale, stream);
+}
+
+pa_status pa_decode_fp4(void *out, const void *query, const void *k_cache, const void *v_cache,
+                        const int32_t *block_tables, int32_t max_blocks_per_seq,
+                        const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads,
+                        int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                        int64_t num_blocks, float scale, float k_scale, float v_scale,
+                        int32_t max_context_len, int32_t partition_size, void *workspace,
+                        size_t workspace_bytes, int32_t dtype, void *stream) {
+  if (!fp4_scales_ok(k_scale, v_scale)) return PA_ERR_INVALID_ARG;
+  const int32_t st = pa::decode_check_args(
+      out, query, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs,
+      num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, max_context_len,
+      partition_size, dtype);
+  if (st != PA_OK || num_seqs == 0) return static_cast<pa_status>(st);
+  const size_t need = pa_decode_workspace_size(num_seqs, num_q_heads, head_dim, max_context_len,
+                                               partition_size);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return PA_ERR_INVALID_ARG;
+  return attn_fp4_impl(out, query, nullptr, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                       context_lens, num_seqs, 1, num_q_heads, num_kv_heads, head_dim, block_size,
+                       num_blocks, scale, k_scale, v_scale, max_context_len, dtype, stream);
+}
+
+pa_status pa_prefill_fp4(void *out, const void *query, const int32_t *query_start,
+                         const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                         int32_t max_blocks_per_seq, const int32_t *context_lens,
+                         int32_t num_seqs, int32_t max_q_len, int32_t num_q_heads,
+                         int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                         int64_t num_blocks, float scale, float k_scale, float v_scale,
+                         int32_t dtype, void *stream) {
+  if (!fp4_scales_ok(k_scale, v_scale)) return PA_ERR_INVALID_ARG;
+  const pa_status st = prefill_check_args(
+      out, query, query_start, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+      num_seqs, max_q_len, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+      dtype);
+  if (st != PA_OK || num_seqs == 0 || max_q_len == 0) return st;
+  return attn_fp4_impl(out, query, query_start, k_cache, v_cache, block_tables,
+                       max_blocks_per_seq, context_lens, num_seqs, max_q_len, num_q_heads,
+                       num_kv_heads, head_dim, block_size, num_blocks, scale, k_scale, v_scale,
+                       INT32_MAX, dtype, stream);
 }
 
 }  // extern "C"

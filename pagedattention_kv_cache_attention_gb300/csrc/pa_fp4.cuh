@@ -1,0 +1,68 @@
+// pa_fp4.cuh -- the FP4 KV cache's number format and tile layout.
+//
+// A cached element is an E2M1 code (1 sign, 2 exponent bits with bias 1, 1
+// fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives); 16
+// consecutive elements of a head_dim row share one E4M3 scale, and a cache has
+// one fp32 scale g: code c under scale s stands for g * s * e2m1(c).
+//
+// The tile of one (physical block, KV head) is block_size * head_dim * 9 / 16
+// consecutive bytes: the codes of its tokens row by row (head_dim / 2 bytes a
+// token, the even element of a byte in its low nibble), then their scales row
+// by row (head_dim / 16 bytes a token).  Codes and scales of a tile are so
+// fetched in one copy.
+//
+// e2m1 * E4M3 has at most 2 + 4 significant bits and is 0 or lies between
+// 2^-10 and 2688 in magnitude, so s * e2m1(c) is exact in fp16: the attention
+// kernels form it there (one fp16x2 product for two elements) and fold g into
+// the softmax scale or the output.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+#include "pa_device.cuh"
+
+namespace pa {
+
+constexpr int kFp4Group = 16;           // elements that share a scale
+constexpr uint32_t kFp4NanScale = 0x7f;  // E4M3 NaN: the scale of a group with a NaN in it
+
+// Bytes of one (block, KV head) tile, and of its codes.
+__host__ __device__ constexpr int fp4_tile_bytes(int bs, int d) { return bs * d * 9 / 16; }
+__host__ __device__ constexpr int fp4_code_bytes(int bs, int d) { return bs * d / 2; }
+
+// Eight E2M1 codes (element 0 in the lowest nibble) to four fp16 pairs.
+__device__ __forceinline__ void e2m1x8_to_half(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+// Eight fp32 values to E2M1 codes (nearest, ties to the even code, magnitudes
+// beyond 6 to 6), value 0 in the lowest nibble.
+__device__ __forceinline__ uint32_t float8_to_e2m1x8(const float (&y)[8]) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  return w;
+}
+
+// E4M3 code (low byte of b) to fp32, exact.
+__device__ __forceinline__ float e4m3_to_float(uint32_t b) {
+  const uint32_t h = e4m3x2_lo_to_f16x2(b & 0xffu);
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
+}
+
+// fp32 to the nearest E4M3 code (ties to even, at most 448; NaN stays NaN).
+__device__ __forceinline__ uint32_t float_to_e4m3(float x) {
+  return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+}
+
+}  // namespace pa

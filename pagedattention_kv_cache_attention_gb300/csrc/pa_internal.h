@@ -95,6 +95,31 @@ struct ReshapeArgs {
   unsigned *err;
 };
 
+// The FP4 cache's write (key, value are read) and read-back (they are written).
+struct Fp4CacheArgs {
+  void *key, *value;
+  int64_t key_stride, value_stride;  // elements
+  void *k_cache, *v_cache;
+  const int64_t *slot_mapping;
+  int num_tokens, num_kv_heads, head_dim, bs_log2;
+  int64_t num_blocks;
+  float k_scale, v_scale;
+  unsigned *err;
+};
+
+// Attention over the FP4 cache; query_start null: one query a sequence.
+struct Fp4AttnArgs {
+  void *out;
+  const void *query;
+  const int32_t *query_start, *block_tables, *context_lens;
+  const void *k_cache, *v_cache;
+  int max_blocks_per_seq;
+  int num_seqs, num_q_heads, num_kv_heads, group, bs_log2, max_q_len, max_context_len;
+  int64_t num_blocks;
+  float scale_log2, out_scale;
+  unsigned *err;
+};
+
 struct PrefillArgs {
   void *out;                    // [total_q, Hq, D]
   const void *query;            // [total_q, Hq, D]
@@ -169,6 +194,9 @@ cudaError_t launch_shared_prefix(const DecodeArgs &a, const void *k_cache, const
 // Sequences of one group that a shared-prefix CTA serves at query group size G.
 int shared_prefix_members_per_cta(int group);
 cudaError_t launch_reshape(const ReshapeArgs &a, cudaStream_t stream);
+cudaError_t launch_cache_fp4_write(const Fp4CacheArgs &a, int dtype, cudaStream_t stream);
+cudaError_t launch_cache_fp4_read(const Fp4CacheArgs &a, int dtype, cudaStream_t stream);
+cudaError_t launch_attn_fp4(const Fp4AttnArgs &a, int head_dim, int dtype, cudaStream_t stream);
 cudaError_t launch_block_copy(const BlockCopyArgs &a, int num_tensors, cudaStream_t stream);
 cudaError_t launch_prefill(const PrefillArgs &a, const void *k_cache, const void *v_cache,
                            int64_t pool_rows, int head_dim, int dtype, bool kv_fp8,
