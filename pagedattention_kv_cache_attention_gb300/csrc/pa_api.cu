@@ -48,6 +48,15 @@ bool fp4_scales_ok(float k_scale, float v_scale) {
   const float lo = 0x1p-100f, hi = 0x1p100f;
   return k_scale >= lo && k_scale <= hi && v_scale >= lo && v_scale <= hi;
 }
+// TMA row coordinates of an FP4 pool (9 rows for 8 tokens) are 32-bit, and so
+// is the arithmetic on token indexes, a step or two past the table's end.
+bool fp4_pool_ok(int64_t num_blocks, int32_t num_kv_heads, int32_t block_size,
+                 int32_t max_blocks_per_seq) {
+  if (num_blocks <= 0 || num_kv_heads <= 0 || block_size <= 0) return true;  // refused elsewhere
+  return num_blocks < (int64_t(1) << 31) &&
+         num_blocks * num_kv_heads < (int64_t(1) << 31) / (block_size * 9 / 8 + 1) &&
+         static_cast<int64_t>(max_blocks_per_seq) * block_size < (int64_t(1) << 31) - 8192;
+}
 bool head_dim_ok(int32_t d) { return d == 64 || d == 128; }
 bool block_size_ok(int32_t b) { return b == 16 || b == 32; }
 
@@ -252,7 +261,7 @@ pa_status decode_impl(void *out, const void *query, const void *k_cache, const v
                       int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                       int64_t num_blocks, float scale, int32_t max_context_len,
                       int32_t partition_size, void *workspace, size_t workspace_bytes,
-                      int32_t dtype, bool kv_fp8, float k_scale, float v_scale, void *stream,
+                      int32_t dtype, pa::Kv kv, float k_scale, float v_scale, void *stream,
                       const SharedPrefix *sp = nullptr) {
   const int32_t st = pa::decode_check_args(
       out, query, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs,
@@ -320,12 +329,16 @@ pa_status decode_impl(void *out, const void *query, const void *k_cache, const v
     a.max_group_size = sp->max_group_size;
     a.members_per_cta = pa::shared_prefix_members_per_cta(group);
     a.chunks = chunks;
-    if (pa::launch_shared_prefix(a, k_cache, v_cache, pool_rows, head_dim, dtype, kv_fp8, cs,
-                                 &map_failed) != cudaSuccess)
+    if (pa::launch_shared_prefix(a, k_cache, v_cache, pool_rows, head_dim, dtype,
+                                 kv == pa::Kv::kFp8, cs, &map_failed) != cudaSuccess)
       return map_failed ? PA_ERR_INVALID_ARG : PA_ERR_CUDA;
   }
-  if (pa::launch_decode(a, k_cache, v_cache, pool_rows, head_dim, dtype, kv_fp8, cs,
-                        &map_failed) != cudaSuccess)
+  const cudaError_t launched =
+      kv == pa::Kv::kFp4
+          ? pa::launch_decode_fp4(a, k_cache, v_cache, head_dim, dtype, cs, &map_failed)
+          : pa::launch_decode(a, k_cache, v_cache, pool_rows, head_dim, dtype,
+                              kv == pa::Kv::kFp8, cs, &map_failed);
+  if (launched != cudaSuccess)
     return map_failed ? PA_ERR_INVALID_ARG : PA_ERR_CUDA;
   if (P > 1 && !fuse)
     return reduce_impl(out, workspace, context_lens, num_seqs, num_q_heads, head_dim,
@@ -348,7 +361,7 @@ pa_status pa_decode(void *out, const void *query, const void *k_cache, const voi
   return decode_impl(out, query, k_cache, v_cache, block_tables, max_blocks_per_seq,
                      context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                      num_blocks, scale, max_context_len, partition_size, workspace,
-                     workspace_bytes, dtype, false, 1.f, 1.f, stream);
+                     workspace_bytes, dtype, pa::Kv::k16, 1.f, 1.f, stream);
 }
 
 pa_status pa_decode_shared_prefix(void *out, const void *query, const void *k_cache,
@@ -365,7 +378,7 @@ pa_status pa_decode_shared_prefix(void *out, const void *query, const void *k_ca
   return decode_impl(out, query, k_cache, v_cache, block_tables, max_blocks_per_seq,
                      context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                      num_blocks, scale, max_context_len, partition_size, workspace,
-                     workspace_bytes, dtype, false, 1.f, 1.f, stream, &sp);
+                     workspace_bytes, dtype, pa::Kv::k16, 1.f, 1.f, stream, &sp);
 }
 
 pa_status pa_decode_shared_prefix_fp8(void *out, const void *query, const void *k_cache,
@@ -384,7 +397,7 @@ pa_status pa_decode_shared_prefix_fp8(void *out, const void *query, const void *
   return decode_impl(out, query, k_cache, v_cache, block_tables, max_blocks_per_seq,
                      context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                      num_blocks, scale, max_context_len, partition_size, workspace,
-                     workspace_bytes, dtype, true, k_scale, v_scale, stream, &sp);
+                     workspace_bytes, dtype, pa::Kv::kFp8, k_scale, v_scale, stream, &sp);
 }
 
 pa_status pa_decode_fp8(void *out, const void *query, const void *k_cache, const void *v_cache,
@@ -400,7 +413,7 @@ pa_status pa_decode_fp8(void *out, const void *query, const void *k_cache, const
   return decode_impl(out, query, k_cache, v_cache, block_tables, max_blocks_per_seq,
                      context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                      num_blocks, scale, max_context_len, partition_size, workspace,
-                     workspace_bytes, dtype, true, k_scale, v_scale, stream);
+                     workspace_bytes, dtype, pa::Kv::kFp8, k_scale, v_scale, stream);
 }
 
 pa_status pa_reshape_and_cache_fp8(const void *key, const void *value, int64_t key_stride,
@@ -657,18 +670,12 @@ pa_status pa_decode_fp4(void *out, const void *query, const void *k_cache, const
                         int32_t max_context_len, int32_t partition_size, void *workspace,
                         size_t workspace_bytes, int32_t dtype, void *stream) {
   if (!fp4_scales_ok(k_scale, v_scale)) return PA_ERR_INVALID_ARG;
-  const int32_t st = pa::decode_check_args(
-      out, query, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs,
-      num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, max_context_len,
-      partition_size, dtype);
-  if (st != PA_OK || num_seqs == 0) return static_cast<pa_status>(st);
-  const size_t need = pa_decode_workspace_size(num_seqs, num_q_heads, head_dim, max_context_len,
-                                               partition_size);
-  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
-    return PA_ERR_INVALID_ARG;
-  return attn_fp4_impl(out, query, nullptr, k_cache, v_cache, block_tables, max_blocks_per_seq,
-                       context_lens, num_seqs, 1, num_q_heads, num_kv_heads, head_dim, block_size,
-                       num_blocks, scale, k_scale, v_scale, max_context_len, dtype, stream);
+  if (!fp4_pool_ok(num_blocks, num_kv_heads, block_size, max_blocks_per_seq))
+    return PA_ERR_UNSUPPORTED;
+  return decode_impl(out, query, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                     context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                     num_blocks, scale, max_context_len, partition_size, workspace,
+                     workspace_bytes, dtype, pa::Kv::kFp4, k_scale, v_scale, stream);
 }
 
 pa_status pa_prefill_fp4(void *out, const void *query, const int32_t *query_start,
@@ -679,6 +686,8 @@ pa_status pa_prefill_fp4(void *out, const void *query, const int32_t *query_star
                          int64_t num_blocks, float scale, float k_scale, float v_scale,
                          int32_t dtype, void *stream) {
   if (!fp4_scales_ok(k_scale, v_scale)) return PA_ERR_INVALID_ARG;
+  if (!fp4_pool_ok(num_blocks, num_kv_heads, block_size, max_blocks_per_seq))
+    return PA_ERR_UNSUPPORTED;
   const pa_status st = prefill_check_args(
       out, query, query_start, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
       num_seqs, max_q_len, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,

@@ -13,6 +13,9 @@ namespace pa {
 
 constexpr int kMaxDevices = 64;
 
+// What the caches hold: fp16 / bf16 elements, E4M3 codes, or FP4 tiles (pa_fp4.cuh).
+enum class Kv { k16, kFp8, kFp4 };
+
 // Raises one kernel's dynamic shared-memory limit once per device.  Safe when
 // several host threads make their first call at the same time: the attribute
 // is set under a lock, and later calls only read an atomic flag.  Each
@@ -181,10 +184,16 @@ constexpr int kMaxSharedPrefixPartition = 8192;
 bool encode_pool_map(CUtensorMap *map, const void *pool, int64_t rows, int head_dim, int dtype,
                      bool fp8);
 
+// An FP4 cache of `tiles` (block, head) tiles, viewed for TMA loads of whole tiles.
+bool encode_fp4_map(CUtensorMap *map, const void *pool, int64_t tiles, int block_size,
+                    int head_dim);
+
 // kv_fp8: the caches hold FP8 E4M3 codes (queries and output fp16).
 cudaError_t launch_decode(const DecodeArgs &a, const void *k_cache, const void *v_cache,
                           int64_t pool_rows, int head_dim, int dtype, bool kv_fp8,
                           cudaStream_t stream, bool *map_failed);
+cudaError_t launch_decode_fp4(const DecodeArgs &a, const void *k_cache, const void *v_cache,
+                              int head_dim, int dtype, cudaStream_t stream, bool *map_failed);
 cudaError_t launch_reduce(const ReduceArgs &a, int head_dim, int dtype, cudaStream_t stream);
 // The shared-prefix pass of pa_decode_shared_prefix (16-bit or FP8 caches);
 // the decode launch with a.prefix_lens set follows it on the same stream.
