@@ -491,7 +491,7 @@ pa_status prefill_impl(void *out, const void *query, const int32_t *query_start,
                        int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
                        int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads,
                        int32_t head_dim, int32_t block_size, int64_t num_blocks, float scale,
-                       int32_t dtype, bool kv_fp8, float k_scale, float v_scale, void *stream) {
+                       int32_t dtype, pa::Kv kv, float k_scale, float v_scale, void *stream) {
   const pa_status st = prefill_check_args(
       out, query, query_start, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
       num_seqs, max_q_len, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
@@ -519,7 +519,7 @@ pa_status prefill_impl(void *out, const void *query, const int32_t *query_start,
   a.out_scale = v_scale;
   a.err = err;
   bool map_failed = false;
-  if (pa::launch_prefill(a, k_cache, v_cache, pool_rows, head_dim, dtype, kv_fp8,
+  if (pa::launch_prefill(a, k_cache, v_cache, pool_rows, head_dim, dtype, kv,
                          static_cast<cudaStream_t>(stream), &map_failed) != cudaSuccess)
     return map_failed ? PA_ERR_INVALID_ARG : PA_ERR_CUDA;
   return PA_OK;
@@ -537,7 +537,7 @@ pa_status pa_prefill(void *out, const void *query, const int32_t *query_start,
                      int32_t dtype, void *stream) {
   return prefill_impl(out, query, query_start, k_cache, v_cache, block_tables, max_blocks_per_seq,
                       context_lens, num_seqs, max_q_len, num_q_heads, num_kv_heads, head_dim,
-                      block_size, num_blocks, scale, dtype, false, 1.f, 1.f, stream);
+                      block_size, num_blocks, scale, dtype, pa::Kv::k16, 1.f, 1.f, stream);
 }
 
 pa_status pa_prefill_fp8(void *out, const void *query, const int32_t *query_start,
@@ -550,7 +550,8 @@ pa_status pa_prefill_fp8(void *out, const void *query, const int32_t *query_star
   if (!fp8_scales_ok(k_scale, v_scale)) return PA_ERR_INVALID_ARG;
   return prefill_impl(out, query, query_start, k_cache, v_cache, block_tables, max_blocks_per_seq,
                       context_lens, num_seqs, max_q_len, num_q_heads, num_kv_heads, head_dim,
-                      block_size, num_blocks, scale, dtype, true, k_scale, v_scale, stream);
+                      block_size, num_blocks, scale, dtype, pa::Kv::kFp8, k_scale, v_scale,
+                      stream);
 }
 
 }  // extern "C"
@@ -598,40 +599,6 @@ pa_status cache_fp4_impl(bool write, void *key, void *value, int64_t key_stride,
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   return (write ? pa::launch_cache_fp4_write(a, dtype, cs)
                 : pa::launch_cache_fp4_read(a, dtype, cs)) == cudaSuccess
-             ? PA_OK
-             : PA_ERR_CUDA;
-}
-
-pa_status attn_fp4_impl(void *out, const void *query, const int32_t *query_start,
-                        const void *k_cache, const void *v_cache, const int32_t *block_tables,
-                        int32_t max_blocks_per_seq, const int32_t *context_lens, int32_t num_seqs,
-                        int32_t max_q_len, int32_t num_q_heads, int32_t num_kv_heads,
-                        int32_t head_dim, int32_t block_size, int64_t num_blocks, float scale,
-                        float k_scale, float v_scale, int32_t max_context_len, int32_t dtype,
-                        void *stream) {
-  unsigned int *err = nullptr;
-  if (error_word(&err) != cudaSuccess) return PA_ERR_CUDA;
-  pa::Fp4AttnArgs a{};
-  a.out = out;
-  a.query = query;
-  a.query_start = query_start;
-  a.block_tables = block_tables;
-  a.context_lens = context_lens;
-  a.k_cache = k_cache;
-  a.v_cache = v_cache;
-  a.max_blocks_per_seq = max_blocks_per_seq;
-  a.num_seqs = num_seqs;
-  a.num_q_heads = num_q_heads;
-  a.num_kv_heads = num_kv_heads;
-  a.group = num_q_heads / num_kv_heads;
-  a.bs_log2 = block_size == 16 ? 4 : 5;
-  a.max_q_len = max_q_len;
-  a.max_context_len = max_context_len;
-  a.num_blocks = num_blocks;
-  a.scale_log2 = scale * 1.4426950408889634f * k_scale;
-  a.out_scale = v_scale;
-  a.err = err;
-  return pa::launch_attn_fp4(a, head_dim, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
 }
@@ -688,15 +655,10 @@ pa_status pa_prefill_fp4(void *out, const void *query, const int32_t *query_star
   if (!fp4_scales_ok(k_scale, v_scale)) return PA_ERR_INVALID_ARG;
   if (!fp4_pool_ok(num_blocks, num_kv_heads, block_size, max_blocks_per_seq))
     return PA_ERR_UNSUPPORTED;
-  const pa_status st = prefill_check_args(
-      out, query, query_start, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
-      num_seqs, max_q_len, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
-      dtype);
-  if (st != PA_OK || num_seqs == 0 || max_q_len == 0) return st;
-  return attn_fp4_impl(out, query, query_start, k_cache, v_cache, block_tables,
-                       max_blocks_per_seq, context_lens, num_seqs, max_q_len, num_q_heads,
-                       num_kv_heads, head_dim, block_size, num_blocks, scale, k_scale, v_scale,
-                       INT32_MAX, dtype, stream);
+  return prefill_impl(out, query, query_start, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                      context_lens, num_seqs, max_q_len, num_q_heads, num_kv_heads, head_dim,
+                      block_size, num_blocks, scale, dtype, pa::Kv::kFp4, k_scale, v_scale,
+                      stream);
 }
 
 }  // extern "C"

@@ -749,9 +749,9 @@ bool encode_pool_map(CUtensorMap *map, const void *pool, int64_t rows, int head_
 
 // An FP4 cache viewed as a 2-D tensor of rows of head_dim / 2 bytes, 18 for
 // every 16 tokens of a tile (the last two of them scales), loaded one tile at a
-// time with the swizzle of the row's length.
+// time, with the swizzle of the row's length or as they are.
 bool encode_fp4_map(CUtensorMap *map, const void *pool, int64_t tiles, int block_size,
-                    int head_dim) {
+                    int head_dim, bool swizzle) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   const int row = head_dim / 2, rows = block_size * 9 / 8;
@@ -761,7 +761,8 @@ bool encode_fp4_map(CUtensorMap *map, const void *pool, int64_t tiles, int block
   cuuint32_t estr[2] = {1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(pool), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+             !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE
+                      : (row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B),
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -66,12 +66,6 @@ template <int D> __device__ __forceinline__ int token_of(int r) {
   return D == 128 ? r ^ ((r >> 1) & 1) : r ^ ((r >> 2) & 1);
 }
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  const __half2 p = __hmul2(*reinterpret_cast<const __half2 *>(&a),
-                            *reinterpret_cast<const __half2 *>(&b));
-  return *reinterpret_cast<const uint32_t *>(&p);
-}
-
 // T: query and output type.  NW warps, S stages each, U 32-token units per
 // step.  WP: each warp takes a whole partition and writes its partial itself
 // (partitions joined by the reduce kernel), as in the 16-bit kernel.
@@ -312,10 +306,10 @@ __global__ void __launch_bounds__(NW * 32)
           uint32_t ha[4], hb[4];
           e2m1x8_to_half(word_of(wa, w), ha);
           e2m1x8_to_half(word_of(wb, w), hb);
-          Elem<__half>::mma(x[h], hmul2(ha[0], ga), hmul2(hb[0], gb), hmul2(ha[1], ga),
-                            hmul2(hb[1], gb), qf[w].x, qf[w].y);
-          Elem<__half>::mma(x[h], hmul2(ha[2], ga), hmul2(hb[2], gb), hmul2(ha[3], ga),
-                            hmul2(hb[3], gb), qf[w].z, qf[w].w);
+          Elem<__half>::mma(x[h], f16x2_mul(ha[0], ga), f16x2_mul(hb[0], gb), f16x2_mul(ha[1], ga),
+                            f16x2_mul(hb[1], gb), qf[w].x, qf[w].y);
+          Elem<__half>::mma(x[h], f16x2_mul(ha[2], ga), f16x2_mul(hb[2], gb), f16x2_mul(ha[3], ga),
+                            f16x2_mul(hb[3], gb), qf[w].z, qf[w].w);
         }
       } else {
         const uint2 wa = *reinterpret_cast<const uint2 *>(Ks);
@@ -327,10 +321,10 @@ __global__ void __launch_bounds__(NW * 32)
           uint32_t ha[4], hb[4];
           e2m1x8_to_half(w == 0 ? wa.x : wa.y, ha);
           e2m1x8_to_half(w == 0 ? wb.x : wb.y, hb);
-          Elem<__half>::mma(x[h], hmul2(ha[0], ga), hmul2(hb[0], gb), hmul2(ha[1], ga),
-                            hmul2(hb[1], gb), qf[w].x, qf[w].y);
-          Elem<__half>::mma(x[h], hmul2(ha[2], ga), hmul2(hb[2], gb), hmul2(ha[3], ga),
-                            hmul2(hb[3], gb), qf[w].z, qf[w].w);
+          Elem<__half>::mma(x[h], f16x2_mul(ha[0], ga), f16x2_mul(hb[0], gb), f16x2_mul(ha[1], ga),
+                            f16x2_mul(hb[1], gb), qf[w].x, qf[w].y);
+          Elem<__half>::mma(x[h], f16x2_mul(ha[2], ga), f16x2_mul(hb[2], gb), f16x2_mul(ha[3], ga),
+                            f16x2_mul(hb[3], gb), qf[w].z, qf[w].w);
         }
       }
     }
@@ -426,9 +420,9 @@ __global__ void __launch_bounds__(NW * 32)
         pairs(v2.y, v3.y, a3[0], a3[1]);
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt)
-          Elem<__half>::mma(acc[mt], hmul2(a0[mt & 1][mt >> 1], g01),
-                            hmul2(a1[mt & 1][mt >> 1], g01), hmul2(a2[mt & 1][mt >> 1], g23),
-                            hmul2(a3[mt & 1][mt >> 1], g23), pb0[h], pb1[h]);
+          Elem<__half>::mma(acc[mt], f16x2_mul(a0[mt & 1][mt >> 1], g01),
+                            f16x2_mul(a1[mt & 1][mt >> 1], g01), f16x2_mul(a2[mt & 1][mt >> 1], g23),
+                            f16x2_mul(a3[mt & 1][mt >> 1], g23), pb0[h], pb1[h]);
       } else {
         uint32_t a0[2][4], a2[2][4];
         pairs(*reinterpret_cast<const uint32_t *>(Vs + v_at0),
@@ -437,9 +431,9 @@ __global__ void __launch_bounds__(NW * 32)
               *reinterpret_cast<const uint32_t *>(Vs + v_at1 + 8 * Sh::kRow), a2[0], a2[1]);
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
-          Elem<__half>::mma(acc[mt], hmul2(a0[mt & 1][mt >> 1], g01),
-                            hmul2(a0[mt & 1][2 + (mt >> 1)], g01), hmul2(a2[mt & 1][mt >> 1], g23),
-                            hmul2(a2[mt & 1][2 + (mt >> 1)], g23), pb0[h], pb1[h]);
+          Elem<__half>::mma(acc[mt], f16x2_mul(a0[mt & 1][mt >> 1], g01),
+                            f16x2_mul(a0[mt & 1][2 + (mt >> 1)], g01), f16x2_mul(a2[mt & 1][mt >> 1], g23),
+                            f16x2_mul(a2[mt & 1][2 + (mt >> 1)], g23), pb0[h], pb1[h]);
       }
     }
 
@@ -598,8 +592,8 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, const void *k_cache, const vo
                               int head_dim, int dtype, cudaStream_t stream, bool *map_failed) {
   CUtensorMap km, vm;
   const int64_t tiles = a.num_blocks * a.num_kv_heads;
-  *map_failed = !encode_fp4_map(&km, k_cache, tiles, 1 << a.bs_log2, head_dim) ||
-                !encode_fp4_map(&vm, v_cache, tiles, 1 << a.bs_log2, head_dim);
+  *map_failed = !encode_fp4_map(&km, k_cache, tiles, 1 << a.bs_log2, head_dim, true) ||
+                !encode_fp4_map(&vm, v_cache, tiles, 1 << a.bs_log2, head_dim, true);
   if (*map_failed) return cudaErrorInvalidValue;
   if (dtype == 0)
     return head_dim == 128 ? launch_t<__half, 128>(a, km, vm, stream)

@@ -54,6 +54,13 @@ __device__ __forceinline__ uint32_t float8_to_e2m1x8(const float (&y)[8]) {
   return w;
 }
 
+// Product of two fp16 pairs.
+__device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
+  const __half2 p = __hmul2(*reinterpret_cast<const __half2 *>(&a),
+                            *reinterpret_cast<const __half2 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&p);
+}
+
 // E4M3 code (low byte of b) to fp32, exact.
 __device__ __forceinline__ float e4m3_to_float(uint32_t b) {
   const uint32_t h = e4m3x2_lo_to_f16x2(b & 0xffu);

@@ -110,19 +110,6 @@ struct Fp4CacheArgs {
   unsigned *err;
 };
 
-// Attention over the FP4 cache; query_start null: one query a sequence.
-struct Fp4AttnArgs {
-  void *out;
-  const void *query;
-  const int32_t *query_start, *block_tables, *context_lens;
-  const void *k_cache, *v_cache;
-  int max_blocks_per_seq;
-  int num_seqs, num_q_heads, num_kv_heads, group, bs_log2, max_q_len, max_context_len;
-  int64_t num_blocks;
-  float scale_log2, out_scale;
-  unsigned *err;
-};
-
 struct PrefillArgs {
   void *out;                    // [total_q, Hq, D]
   const void *query;            // [total_q, Hq, D]
@@ -186,7 +173,7 @@ bool encode_pool_map(CUtensorMap *map, const void *pool, int64_t rows, int head_
 
 // An FP4 cache of `tiles` (block, head) tiles, viewed for TMA loads of whole tiles.
 bool encode_fp4_map(CUtensorMap *map, const void *pool, int64_t tiles, int block_size,
-                    int head_dim);
+                    int head_dim, bool swizzle);
 
 // kv_fp8: the caches hold FP8 E4M3 codes (queries and output fp16).
 cudaError_t launch_decode(const DecodeArgs &a, const void *k_cache, const void *v_cache,
@@ -205,10 +192,9 @@ int shared_prefix_members_per_cta(int group);
 cudaError_t launch_reshape(const ReshapeArgs &a, cudaStream_t stream);
 cudaError_t launch_cache_fp4_write(const Fp4CacheArgs &a, int dtype, cudaStream_t stream);
 cudaError_t launch_cache_fp4_read(const Fp4CacheArgs &a, int dtype, cudaStream_t stream);
-cudaError_t launch_attn_fp4(const Fp4AttnArgs &a, int head_dim, int dtype, cudaStream_t stream);
 cudaError_t launch_block_copy(const BlockCopyArgs &a, int num_tensors, cudaStream_t stream);
 cudaError_t launch_prefill(const PrefillArgs &a, const void *k_cache, const void *v_cache,
-                           int64_t pool_rows, int head_dim, int dtype, bool kv_fp8,
+                           int64_t pool_rows, int head_dim, int dtype, Kv kv,
                            cudaStream_t stream, bool *map_failed);
 
 // The host-side checks of pa_decode that come before the workspace check;

@@ -24,6 +24,7 @@
 #include <type_traits>
 
 #include "pa_device.cuh"
+#include "pa_fp4.cuh"
 #include "pa_internal.h"
 
 namespace pa {
@@ -131,23 +132,39 @@ constexpr int kPairKvAtom = kPairKeys * 128;   // one 64-dim atom of a K or V st
 
 // TILES query tiles per CTA: softmax warps 0 .. 4 TILES - 1, issuing warps
 // 4 TILES .. 6 TILES - 1 (Q K^T and P V of each tile), then the K and V warps.
-// Over FP8 caches at head_dim 128 the two-tile kernel has two more warps that
-// widen half of each step's K and V codes, so the widening is spread over all
-// four schedulers of the SM.
-template <int TILES, int D = 128, bool F8 = false>
-__host__ __device__ constexpr bool f8_helpers() { return F8 && TILES == 2 && D == 128; }
-template <int TILES, int D = 128, bool F8 = false>
-constexpr int pair_threads() { return 32 * (6 * TILES + 2 + (f8_helpers<TILES, D, F8>() ? 2 : 0)); }
+// Over FP8 caches at head_dim 128, and over FP4 caches, the two-tile kernel has
+// two more warps that widen half of each step's K and V codes, so the widening
+// is spread over all four schedulers of the SM.
+template <int TILES, int D = 128, Kv KV = Kv::k16>
+__host__ __device__ constexpr bool has_helpers() {
+  return TILES == 2 && ((KV == Kv::kFp8 && D == 128) || KV == Kv::kFp4);
+}
+template <int TILES, int D = 128, Kv KV = Kv::k16>
+constexpr int pair_threads() { return 32 * (6 * TILES + 2 + (has_helpers<TILES, D, KV>() ? 2 : 0)); }
 
-template <int SK, int SV, int TILES, int D>
+// FP4: steps of raw tiles in flight for each of K and V.  One tile per CTA has
+// room for one beside its widened stages (two CTAs share the SM's memory).
+template <int TILES, int D, Kv KV>
+constexpr int raw_stages() {
+  return KV != Kv::kFp4 ? 0 : TILES == 2 ? 6 : (D == 128 ? 1 : 4);
+}
+// Place of a raw 16-token FP4 tile (TMA copies start on 128 bytes); a 32-token
+// tile takes two.
+template <int D> constexpr int kRawSlot16 = D == 128 ? 1152 : 640;
+
+template <int SK, int SV, int TILES, int D, Kv KV>
 struct PairLayout {
   static constexpr int kAtoms = D / 64;
+  static constexpr int kRaw = raw_stages<TILES, D, KV>();
+  static constexpr int kRawStep = kPairKeys / 16 * kRawSlot16<D>;   // K or V of a step
   static constexpr int kQOff = 0;                                   // Q: [TILES][atoms]
   static constexpr int kKOff = TILES * kAtoms * kPairQAtom;         // K ring: [SK][atoms]
   static constexpr int kVOff = kKOff + SK * kAtoms * kPairKvAtom;   // V ring: [SV][atoms]
-  static constexpr int kBarOff = kVOff + SV * kAtoms * kPairKvAtom;
-  // + the FP8 landing barriers (SK + SV) and the V sub-tile masks (SV words)
-  static constexpr int kBars = 2 * SK + 2 * SV + 1 + 2 + 2 + 4 + 4 + 1 + SK + SV;
+  static constexpr int kRawOff = kVOff + SV * kAtoms * kPairKvAtom;  // FP4: [K, V][kRaw]
+  static constexpr int kBarOff = kRawOff + 2 * kRaw * kRawStep;
+  // + the landing barriers (FP8: SK + SV; FP4: kRaw for each of four warps)
+  // and the V sub-tile masks (SV words)
+  static constexpr int kBars = 2 * SK + 2 * SV + 1 + 2 + 2 + 4 + 4 + 1 + SK + SV + 4 * kRaw;
   static constexpr size_t kSmem = 1024 + kBarOff + kBars * 8 + SV * 4 + 16;
 };
 
@@ -210,31 +227,90 @@ __device__ __forceinline__ void f8_stage_to_f16(uint8_t *st, int lane, int pass_
   }
 }
 
-// F8: the caches hold FP8 E4M3 codes, widened to fp16 in shared memory; the
+// FP4 caches: rows [row0, row1) of a step's raw tiles (unswizzled) become the
+// fp16 tile that the MMA reads, every value s * e2m1(code) exact there.  A lane
+// takes 32 dimensions of a row, four words of eight codes, each one 16-byte
+// store.  Its words are taken in an order i = t ^ f that differs between lanes:
+// with it the 32 word loads of a step t hit 32 banks, and the eight stores of
+// a phase (two rows of four lanes, or four rows of two) eight different
+// 16-byte bank groups of the swizzled rows.  Rows that keep() refuses get a
+// zero scale, and with it zeros: a code is always finite.
+template <int D, typename Keep>
+__device__ __forceinline__ void f4_widen(const uint8_t *raw, uint8_t *st, int lane, int row0,
+                                         int row1, int bs_log2, Keep keep) {
+  constexpr int kPerRow = D / 32;          // lanes per row
+  constexpr int kRows = 32 / kPerRow;      // rows per pass
+  constexpr int kGroup = 2;                // passes read before their stores
+  const int u = lane % kPerRow, bs = 1 << bs_log2;
+#pragma unroll 1
+  for (int r0 = row0; r0 < row1; r0 += kGroup * kRows) {
+    uint32_t w[kGroup][4], sc[kGroup];
+#pragma unroll
+    for (int p = 0; p < kGroup; ++p) {
+      const int r = r0 + p * kRows + lane / kPerRow;
+      const int f = D == 128 ? ((r >> 1) & 3) ^ (u >> 1) ^ ((r & 1) << 1) : (r >> 2) & 3;
+      const uint8_t *tile = raw + (r >> bs_log2) * (kRawSlot16<D> << (bs_log2 - 4));
+      const int rr = r & (bs - 1);
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        w[p][t] = *reinterpret_cast<const uint32_t *>(tile + rr * (D / 2) + u * 16 + ((t ^ f) << 2));
+      sc[p] = *reinterpret_cast<const uint16_t *>(tile + bs * (D / 2) + rr * (D / 16) + 2 * u);
+    }
+#pragma unroll
+    for (int p = 0; p < kGroup; ++p) {
+      const int r = r0 + p * kRows + lane / kPerRow;
+      const int f = D == 128 ? ((r >> 1) & 3) ^ (u >> 1) ^ ((r & 1) << 1) : (r >> 2) & 3;
+      const uint32_t s2 = e4m3x2_lo_to_f16x2(keep(r) ? sc[p] : 0u);  // the lane's two scales
+      const uint32_t s_lo = __byte_perm(s2, 0, 0x1010), s_hi = __byte_perm(s2, 0, 0x3232);
+      uint8_t *row = st + (u >> 1) * kPairKvAtom + r * 128;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int i = t ^ f;
+        const uint32_t g = (i & 2) ? s_hi : s_lo;
+        uint32_t h[4];
+        e2m1x8_to_half(w[p][t], h);
+        *reinterpret_cast<uint4 *>(row + ((((u & 1) * 4 + i) ^ (r & 7)) << 4)) =
+            make_uint4(f16x2_mul(h[0], g), f16x2_mul(h[1], g), f16x2_mul(h[2], g),
+                       f16x2_mul(h[3], g));
+      }
+    }
+  }
+}
+
+// KV = kFp8: the caches hold FP8 E4M3 codes, widened to fp16 in shared memory; the
 // products then run in fp16 whatever T is (bf16 queries are carried in fp16,
-// see the Q load).
-template <typename T, int D, int SK, int SV, bool SPLIT, int TILES, bool PX, bool F8>
-__global__ void __launch_bounds__(pair_threads<TILES, D, F8>(), TILES == 1 ? 2 : 1)
+// see the Q load).  KV = kFp4: the same with FP4 tiles, which land in a ring of
+// their own.
+template <typename T, int D, int SK, int SV, bool SPLIT, int TILES, bool PX, Kv KV>
+__global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 : 1)
     pa_prefill_tc_pair_kernel(const __grid_constant__ CUtensorMap kmap,
                               const __grid_constant__ CUtensorMap vmap, const PrefillArgs a) {
   static_assert(TILES == 1 || TILES == 2, "one or two query tiles per CTA");
   static_assert(!PX || TILES == 1, "the shared-prefix pass runs one tile per CTA");
   static_assert(D == 64 || D == 128, "head_dim 64 or 128");
-  static_assert(!F8 || !SPLIT, "FP8 caches: the products run in fp16 (no split P)");
-  using L = PairLayout<SK, SV, TILES, D>;
+  constexpr bool F8 = KV == Kv::kFp8, F4 = KV == Kv::kFp4;
+  constexpr bool kWide = F8 || F4;  // codes widened to fp16 in shared memory
+  static_assert(!kWide || !SPLIT, "widened caches: the products run in fp16 (no split P)");
+  static_assert(!F4 || !PX, "the shared-prefix pass has no FP4 form");
+  using L = PairLayout<SK, SV, TILES, D, KV>;
   constexpr int kAtoms = L::kAtoms;
   constexpr int kIssue0 = 4 * TILES;      // first MMA-issuing warp
   constexpr int kLoad0 = 6 * TILES;       // K producer warp (V: kLoad0 + 1)
-  // FP8 widening helpers (K: kLoad0 + 2, V: kLoad0 + 3); a stage is handed
+  // widening helpers (K: kLoad0 + 2, V: kLoad0 + 3); a stage is handed
   // over by every warp that widens part of it
-  constexpr bool kHelpers = f8_helpers<TILES, D, F8>();
+  constexpr bool kHelpers = has_helpers<TILES, D, KV>();
   constexpr int kWideners = kHelpers ? 2 : 1;
   constexpr int kSub = kPairKeys / 16;         // 16-row sub-tiles per step
   constexpr uint32_t kAllSub = (1u << kSub) - 1;
   constexpr bool kBf16 = sizeof(T) == 2 && !std::is_same<T, __half>::value;
-  // MMA operand type (P included): T, or fp16 over FP8 caches
-  using MT = typename std::conditional<F8, __half, T>::type;
-  constexpr bool kMmaBf16 = kBf16 && !F8;
+  // MMA operand type (P included): T, or fp16 over widened caches
+  using MT = typename std::conditional<kWide, __half, T>::type;
+  constexpr bool kMmaBf16 = kBf16 && !kWide;
+  // FP4: P is held times 2^11 with the running maximum at most 2^4 behind, so
+  // that it stays below 2^15 and keeps fp16's precision down to 2^-25 of the
+  // maximum: a long context's faint tail keeps its mass
+  constexpr float kGrowth = F4 ? 4.f : kRescaleLog2;
+  constexpr float kPShift = F4 ? 11.f : 0.f;
   // TMEM columns of a tile: scores 0..63, P 64..127, O from 128.  fp16 P: two
   // buffers of 32 columns (step n in buffer n % 2); bf16 P: one buffer, hi
   // parts in 64..95 and lo parts in 96..127.
@@ -256,7 +332,8 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, F8>(), TILES == 1 ? 2 :
   uint64_t *q_ready = pv_done + 4;
   uint64_t *k_land = q_ready + 1;      // [SK] FP8: a K step's codes are in
   uint64_t *v_land = k_land + SK;      // [SV] FP8: a V step's codes are in
-  uint32_t *v_masks = reinterpret_cast<uint32_t *>(v_land + SV);  // [SV] FP8: loaded sub-tiles
+  uint64_t *raw_land = v_land + SV;    // [4 warps][kRaw] FP4: a warp's raw tiles of a step are in
+  uint32_t *v_masks = reinterpret_cast<uint32_t *>(raw_land + 4 * L::kRaw);  // [SV] FP8: loaded sub-tiles
   uint32_t *tmem_slot = v_masks + SV;
 
   const int kvh = blockIdx.y;
@@ -270,11 +347,11 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, F8>(), TILES == 1 ? 2 :
 
   if (tid == 0) {
     for (int s = 0; s < SK; ++s) {
-      mbar_init(&k_full[s], F8 ? kWideners : 1);
+      mbar_init(&k_full[s], kWide ? kWideners : 1);
       mbar_init(&k_empty[s], TILES);  // released by every Q K^T issuer
     }
     for (int s = 0; s < SV; ++s) {
-      mbar_init(&v_full[s], F8 ? kWideners : 1);
+      mbar_init(&v_full[s], kWide ? kWideners : 1);
       mbar_init(&v_empty[s], TILES);  // and every P V issuer
     }
     mbar_init(v_tail, 1);
@@ -289,6 +366,7 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, F8>(), TILES == 1 ? 2 :
     mbar_init(q_ready, TILES * kTcRows);
     for (int s = 0; s < SK; ++s) mbar_init(&k_land[s], 1);
     for (int s = 0; s < SV; ++s) mbar_init(&v_land[s], 1);
+    for (int s = 0; s < 4 * L::kRaw; ++s) mbar_init(&raw_land[s], 1);
     fence_barrier_init();
   }
   if (warp == kIssue0) tmem_alloc(tmem_slot, 256 * TILES);
@@ -417,13 +495,13 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, F8>(), TILES == 1 ? 2 :
                       (static_cast<int64_t>(q0 + (row_ok ? tok : 0)) * a.num_q_heads + kvh * G +
                        rc % G) * D;
       uint8_t *qt = smem + L::kQOff + t * kAtoms * kPairQAtom;
-      // bf16 queries over FP8 caches: the row is scaled by 2^e so that its
+      // bf16 queries over widened caches: the row is scaled by 2^e so that its
       // largest magnitude lands in [2^14, 2^15), then rounded to fp16 (exact
       // for every value down to 2^-31 of the largest: bf16 carries 8
       // significant bits, and fp16 holds 8 bits at every magnitude from 2^-17
       // up), and 2^-e joins the row's softmax scale
       float qf = 1.f;
-      if constexpr (F8 && kBf16) {
+      if constexpr (kWide && kBf16) {
         float mx = 0.f;
         if (row_ok) {
 #pragma unroll 4
@@ -445,7 +523,7 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, F8>(), TILES == 1 ? 2 :
       for (int ch = 0; ch < D / 8; ++ch) {
         uint4 v = row_ok ? *reinterpret_cast<const uint4 *>(qrow + ch * 8)
                          : make_uint4(0, 0, 0, 0);
-        if constexpr (F8 && kBf16) {
+        if constexpr (kWide && kBf16) {
           uint32_t w4[4];
 #pragma unroll
           for (int w2 = 0; w2 < 4; ++w2) {
@@ -529,13 +607,13 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, F8>(), TILES == 1 ? 2 :
                                    fmaxf(t8[6], t8[7]));
       const float tmax = tmax_raw * sl2;  // the scale is positive: same order
       const float m_new = fmaxf(m_ref, tmax);
-      const bool move = m_new > m_ref + kRescaleLog2;  // includes the first finite max
+      const bool move = m_new > m_ref + kGrowth;  // includes the first finite max
       const float alpha = !move ? 1.f : (m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m_new));
       if (move) {
         l *= alpha;
         m_ref = m_new;
       }
-      const float neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
+      const float neg_m = m_ref == -INFINITY ? 0.f : kPShift - m_ref;
       // P for the whole step in registers first (s scale - m and the row sum on
       // packed fp32 pairs), so the wait for its buffer below overlaps the math
       const uint64_t scale2 = f2_pack(sl2, sl2);
@@ -763,9 +841,86 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, F8>(), TILES == 1 ? 2 :
     };
     const uint64_t policy = l2_policy_evict_first();
     int win_base = 0;
-    int win = helper ? -1 : block_of(lane);
+    int win = helper || F4 ? -1 : block_of(lane);
     bool ok_run = true;
-    if constexpr (F8) {
+    if constexpr (F4) {
+      // Each widening warp has its share of every step (64 tokens, or with a
+      // helper 32), which its own copies bring into its part of the raw ring,
+      // kRaw steps ahead; it widens a share into the fp16 stage, hands its
+      // part of the stage over and refills the raw place it has just read.
+      constexpr int kShare = kPairKeys / kWideners, kRaw = L::kRaw;
+      const int share0 = helper ? kShare : 0;  // the share's first row in the step
+      const int tsh = a.bs_log2 == 4 ? (kShare == 64 ? 2 : 1) : (kShare == 64 ? 1 : 0);
+      const int tiles = 1 << tsh;              // tiles of a share
+      const uint32_t tile_bytes = fp4_tile_bytes(1 << a.bs_log2, D);
+      const int tile_rows = 18 << (a.bs_log2 - 4);
+      const int S = k_role ? SK : SV;
+      uint64_t *full = k_role ? k_full : v_full;
+      uint64_t *empty = k_role ? k_empty : v_empty;
+      uint64_t *land = raw_land + (warp - kLoad0) * kRaw;
+      uint8_t *ring = smem + (k_role ? L::kKOff : L::kVOff);
+      uint8_t *raw = smem + L::kRawOff + (k_role ? 0 : kRaw * L::kRawStep);
+      const CUtensorMap *map = k_role ? &kmap : &vmap;
+      // block of the warp's tile l (its tiles are numbered over all steps)
+      auto tile_block = [&](int l) -> int {
+        const int key = (l >> tsh) * kPairKeys + share0 + ((l & (tiles - 1)) << a.bs_log2);
+        if (key >= n_keys) return -1;
+        const int phys = bt_row[key >> a.bs_log2];
+        if (phys < 0 || static_cast<int64_t>(phys) >= a.num_blocks) {
+          atomicOr(a.err, kErrBadBlock);
+          return -1;
+        }
+        return phys;
+      };
+      win = tile_block(lane);
+      uint32_t loaded = 0;  // bit 4 rs + i: tile i of the share in raw place rs
+      auto fetch = [&](int m) {
+        const int rs = m % kRaw;
+        if ((m << tsh) >= win_base + 32) {
+          win_base += 32;
+          win = tile_block(win_base + lane);
+        }
+        const int phys = __shfl_sync(kFullMask, win, (m << tsh) + (lane & (tiles - 1)) - win_base);
+        const uint32_t mask = __ballot_sync(kFullMask, lane < tiles && phys >= 0);
+        loaded = (loaded & ~(15u << (4 * rs))) | (mask << (4 * rs));
+        if (lane == 0) {
+          if (mask == 0)
+            mbar_arrive(&land[rs]);
+          else
+            mbar_arrive_expect_tx(&land[rs], __popc(mask) * tile_bytes);
+        }
+        __syncwarp();
+        if (lane < tiles && phys >= 0)
+          tma_load_2d(raw + rs * L::kRawStep + (share0 / 16) * kRawSlot16<D> +
+                          lane * (kRawSlot16<D> << (a.bs_log2 - 4)),
+                      map, 0, (phys * a.num_kv_heads + kvh) * tile_rows, &land[rs], policy);
+      };
+      for (int m = 0; m < min(kRaw, n_steps); ++m) fetch(m);
+      int m = 0;
+      for (; m < n_steps; ++m) {
+        const int rs = m % kRaw, s = m % S;
+        if (!__all_sync(kFullMask, mbar_wait_bounded(&land[rs], (m / kRaw) & 1) &&
+                                       (m < S || mbar_wait_bounded(&empty[s], ((m / S) - 1) & 1)))) {
+          ok_run = false;
+          break;
+        }
+        const uint32_t ok = (loaded >> (4 * rs)) & 15u;
+        const int past = n_keys - m * kPairKeys;  // first row that must not contribute
+        // K rows that must not contribute are masked by the softmax
+        const bool all = k_role || (ok == (1u << tiles) - 1 && past >= share0 + kShare);
+        f4_widen<D>(raw + rs * L::kRawStep, ring + s * kAtoms * kPairKvAtom, lane, share0,
+                    share0 + kShare, a.bs_log2, [&](int r) {
+                      return all || (r < past && ((ok >> ((r - share0) >> a.bs_log2)) & 1u));
+                    });
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
+        if (m + kRaw < n_steps) fetch(m + kRaw);
+      }
+      // let copies already in flight land before the CTA leaves (bounded again)
+      for (int k = m; !ok_run && k < min(m + kRaw, n_steps); ++k)
+        (void)mbar_wait_bounded(&land[k % kRaw], (k / kRaw) & 1);
+    } else if constexpr (F8) {
       // A step's copies (16 rows of head_dim codes per sub-tile) land in the
       // upper half of its stage; the warp widens them to fp16 there, clears
       // what V must not contribute and hands the stage over.  Copies and
@@ -986,14 +1141,14 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, F8>(), TILES == 1 ? 2 :
 }
 
 template <typename T, int D, int SK, int SV, bool SPLIT, int TILES, bool PX = false,
-          bool F8 = false>
+          Kv KV = Kv::k16>
 cudaError_t launch_prefill_tc_pair_t(const PrefillArgs &a, const CUtensorMap &km,
                                      const CUtensorMap &vm, cudaStream_t stream) {
   // the shared-prefix pass keeps each member's first partition and the pass's
   // control words after the barriers
-  constexpr size_t smem = PairLayout<SK, SV, TILES, D>::kSmem + (PX ? (kTcRows + 8) * 4 : 0);
+  constexpr size_t smem = PairLayout<SK, SV, TILES, D, KV>::kSmem + (PX ? (kTcRows + 8) * 4 : 0);
   static_assert(smem <= (TILES == 1 ? 113 : 227) * 1024, "shared memory");
-  auto kern = pa_prefill_tc_pair_kernel<T, D, SK, SV, SPLIT, TILES, PX, F8>;
+  auto kern = pa_prefill_tc_pair_kernel<T, D, SK, SV, SPLIT, TILES, PX, KV>;
   static SmemLimitOnce smem_limit;
   const cudaError_t e = smem_limit.ensure(kern, smem);
   if (e != cudaSuccess) return e;
@@ -1002,12 +1157,12 @@ cudaError_t launch_prefill_tc_pair_t(const PrefillArgs &a, const CUtensorMap &km
         kern,
         dim3(static_cast<unsigned>(a.num_parts * a.chunks), static_cast<unsigned>(a.num_kv_heads),
              static_cast<unsigned>(a.num_groups)),
-        dim3(pair_threads<TILES, D, F8>()), smem, stream, km, vm, a);
+        dim3(pair_threads<TILES, D, KV>()), smem, stream, km, vm, a);
   }
   const int tpc = TILES * kTcRows / a.group;
   const int tiles = (a.max_q_len + tpc - 1) / tpc;
   return launch_dependent(kern, dim3(tiles, a.num_kv_heads, a.num_seqs),
-                          dim3(pair_threads<TILES, D, F8>()), smem,
+                          dim3(pair_threads<TILES, D, KV>()), smem,
                           stream, km, vm, a);
 }
 
@@ -1026,6 +1181,12 @@ cudaError_t launch_prefill_tc_pair_t(const PrefillArgs &a, const CUtensorMap &km
 #define PA_PREFILL_PAIR_VSTAGES 4
 #endif
 
+// Widened stages of the two-tile kernel over FP4 caches; its raw ring is what
+// runs ahead.
+#ifndef PA_PREFILL_FP4_STAGES
+#define PA_PREFILL_FP4_STAGES 3
+#endif
+
 bool prefill_tc_supported(int head_dim, int group) {
   return (head_dim == 64 || head_dim == 128) && group >= 1 && group <= 8;
 }
@@ -1034,20 +1195,31 @@ namespace {
 
 template <int D>
 cudaError_t launch_prefill_tc_d(const PrefillArgs &a, const CUtensorMap &km,
-                                const CUtensorMap &vm, int dtype, bool kv_fp8,
-                                cudaStream_t stream) {
+                                const CUtensorMap &vm, int dtype, Kv kv, cudaStream_t stream) {
   const bool pair = static_cast<int64_t>(a.max_q_len) * a.group > kTcRows;
   constexpr int PK = PA_PREFILL_PAIR_KSTAGES, PV = PA_PREFILL_PAIR_VSTAGES;
   constexpr int SK = PA_PREFILL_SOLO_KSTAGES, SV = PA_PREFILL_SOLO_VSTAGES;
-  if (kv_fp8) {
+  if (kv == Kv::kFp4) {
+    constexpr int FS = PA_PREFILL_FP4_STAGES;
     if (dtype == 0)
-      return pair ? launch_prefill_tc_pair_t<__half, D, PK, PV, false, 2, false, true>(a, km, vm,
-                                                                                       stream)
-                  : launch_prefill_tc_pair_t<__half, D, SK, SV, false, 1, false, true>(a, km, vm,
-                                                                                       stream);
-    return pair ? launch_prefill_tc_pair_t<__nv_bfloat16, D, PK, PV, false, 2, false, true>(
+      return pair ? launch_prefill_tc_pair_t<__half, D, FS, FS, false, 2, false, Kv::kFp4>(
+                        a, km, vm, stream)
+                  : launch_prefill_tc_pair_t<__half, D, SK, SV, false, 1, false, Kv::kFp4>(
+                        a, km, vm, stream);
+    return pair ? launch_prefill_tc_pair_t<__nv_bfloat16, D, FS, FS, false, 2, false, Kv::kFp4>(
                       a, km, vm, stream)
-                : launch_prefill_tc_pair_t<__nv_bfloat16, D, SK, SV, false, 1, false, true>(
+                : launch_prefill_tc_pair_t<__nv_bfloat16, D, SK, SV, false, 1, false, Kv::kFp4>(
+                      a, km, vm, stream);
+  }
+  if (kv == Kv::kFp8) {
+    if (dtype == 0)
+      return pair ? launch_prefill_tc_pair_t<__half, D, PK, PV, false, 2, false, Kv::kFp8>(a, km, vm,
+                                                                                       stream)
+                  : launch_prefill_tc_pair_t<__half, D, SK, SV, false, 1, false, Kv::kFp8>(a, km, vm,
+                                                                                       stream);
+    return pair ? launch_prefill_tc_pair_t<__nv_bfloat16, D, PK, PV, false, 2, false, Kv::kFp8>(
+                      a, km, vm, stream)
+                : launch_prefill_tc_pair_t<__nv_bfloat16, D, SK, SV, false, 1, false, Kv::kFp8>(
                       a, km, vm, stream);
   }
   if (dtype == 0) {
@@ -1070,19 +1242,21 @@ cudaError_t launch_prefill_tc_d(const PrefillArgs &a, const CUtensorMap &km,
 // 128-row tile run with two tiles per CTA (one CTA per SM); shorter ones
 // (short chunks, decode-like rows) with one tile per CTA, two CTAs per SM.
 cudaError_t launch_prefill(const PrefillArgs &a, const void *k_cache, const void *v_cache,
-                           int64_t pool_rows, int head_dim, int dtype, bool kv_fp8,
+                           int64_t pool_rows, int head_dim, int dtype, Kv kv,
                            cudaStream_t stream, bool *map_failed) {
   CUtensorMap km, vm;
-  *map_failed = false;
-  if (!encode_pool_map(&km, k_cache, pool_rows, head_dim, dtype, kv_fp8) ||
-      !encode_pool_map(&vm, v_cache, pool_rows, head_dim, dtype, kv_fp8)) {
-    *map_failed = true;
-    return cudaErrorInvalidValue;
-  }
+  auto encode = [&](CUtensorMap *map, const void *cache) {
+    return kv == Kv::kFp4 ? encode_fp4_map(map, cache, a.num_blocks * a.num_kv_heads,
+                                           1 << a.bs_log2, head_dim, /*swizzle=*/false)
+                          : encode_pool_map(map, cache, pool_rows, head_dim, dtype,
+                                            kv == Kv::kFp8);
+  };
+  *map_failed = !encode(&km, k_cache) || !encode(&vm, v_cache);
+  if (*map_failed) return cudaErrorInvalidValue;
   if (a.max_q_len == 0) return cudaSuccess;
   if (!prefill_tc_supported(head_dim, a.group)) return cudaErrorInvalidValue;
-  return head_dim == 128 ? launch_prefill_tc_d<128>(a, km, vm, dtype, kv_fp8, stream)
-                         : launch_prefill_tc_d<64>(a, km, vm, dtype, kv_fp8, stream);
+  return head_dim == 128 ? launch_prefill_tc_d<128>(a, km, vm, dtype, kv, stream)
+                         : launch_prefill_tc_d<64>(a, km, vm, dtype, kv, stream);
 }
 
 // The shared-prefix pass of pa_decode_shared_prefix on the same kernel: one
@@ -1131,14 +1305,14 @@ cudaError_t launch_shared_prefix(const DecodeArgs &d, const void *k_cache, const
   if (kv_fp8) {
     if (dtype == 0)
       return head_dim == 128
-                 ? launch_prefill_tc_pair_t<__half, 128, KS, VS, false, 1, true, true>(a, km, vm,
+                 ? launch_prefill_tc_pair_t<__half, 128, KS, VS, false, 1, true, Kv::kFp8>(a, km, vm,
                                                                                        stream)
-                 : launch_prefill_tc_pair_t<__half, 64, KS, VS, false, 1, true, true>(a, km, vm,
+                 : launch_prefill_tc_pair_t<__half, 64, KS, VS, false, 1, true, Kv::kFp8>(a, km, vm,
                                                                                       stream);
     return head_dim == 128
-               ? launch_prefill_tc_pair_t<__nv_bfloat16, 128, KS, VS, false, 1, true, true>(
+               ? launch_prefill_tc_pair_t<__nv_bfloat16, 128, KS, VS, false, 1, true, Kv::kFp8>(
                      a, km, vm, stream)
-               : launch_prefill_tc_pair_t<__nv_bfloat16, 64, KS, VS, false, 1, true, true>(
+               : launch_prefill_tc_pair_t<__nv_bfloat16, 64, KS, VS, false, 1, true, Kv::kFp8>(
                      a, km, vm, stream);
   }
   if (dtype == 0)
