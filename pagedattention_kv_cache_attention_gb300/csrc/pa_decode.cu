@@ -747,22 +747,22 @@ bool encode_pool_map(CUtensorMap *map, const void *pool, int64_t rows, int head_
   return r == CUDA_SUCCESS;
 }
 
-// An FP4 cache viewed as a 2-D tensor of rows of head_dim / 2 bytes, 18 for
-// every 16 tokens of a tile (the last two of them scales), loaded one tile at a
-// time, with the swizzle of the row's length or as they are.
+// An FP4 cache viewed as a 2-D tensor of lines of head_dim bytes (the codes of
+// two tokens), 9 for every 16 tokens of a tile (the last of them scales),
+// loaded one tile at a time, with the swizzle of the line's length or as they are.
 bool encode_fp4_map(CUtensorMap *map, const void *pool, int64_t tiles, int block_size,
                     int head_dim, bool swizzle) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
-  const int row = head_dim / 2, rows = block_size * 9 / 8;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(row), static_cast<cuuint64_t>(tiles * rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(row)};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(row), static_cast<cuuint32_t>(rows)};
+  const int lines = block_size * 9 / 16;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(tiles * lines)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(head_dim)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(head_dim), static_cast<cuuint32_t>(lines)};
   cuuint32_t estr[2] = {1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(pool), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
              !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE
-                      : (row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B),
+                      : (head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B),
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

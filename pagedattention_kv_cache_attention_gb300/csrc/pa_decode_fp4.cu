@@ -8,9 +8,9 @@
 //  * One CTA per (KV head, sequence, partition) serves all G query heads of
 //    the KV head, so a tile leaves HBM once per group.  Its warps take 32-token
 //    steps in turn, each with its own ring of S shared-memory stages.
-//  * A tile (codes and scales of one block and head, 18 or 36 rows of
-//    head_dim / 2 bytes) is one 2-D TMA copy with the swizzle of its row
-//    length, so that both products read shared memory without conflicts.
+//  * A tile (codes and scales of one block and head, 9 or 18 lines of head_dim
+//    bytes) is one 2-D TMA copy with the swizzle of its line length, so that
+//    both products read shared memory without conflicts.
 //  * S^T[16 tokens, 8 heads] = K Q^T on mma.sync m16n8k16.  A lane reads 16
 //    (or 8) bytes of a K row, which lie within one or two scale groups:
 //    cvt.f16x2.e2m1x2 makes fp16 pairs of a byte and one fp16x2 product with
@@ -20,10 +20,11 @@
 //    instructions for eight codes, so that a converted pair is already (token,
 //    next token) of one dimension, and its scale pair is shared by the lane's
 //    dimensions.
-//  * fp32 online softmax in base 2.  P is carried as fp16 (11 bits; the output
-//    has at most 11) scaled by 2^15, so that only probabilities below 2^-29 of
-//    the running maximum lose bits and below 2^-39 vanish: a long context's
-//    faint tail keeps its mass.
+//  * fp32 online softmax in base 2 against a reference that moves only when a
+//    score passes it by more than 4.  P is carried as fp16 (11 bits; the output
+//    has at most 11) times 2^11, so that only probabilities below 2^-25 of the
+//    maximum lose bits and below 2^-35 vanish: a long context's faint tail
+//    keeps its mass.
 //  * Tokens that must not count get logit -inf and a V scale of zero; a code is
 //    always finite, so nothing a masked slot holds (NaN scales among it)
 //    reaches the output.
@@ -45,37 +46,70 @@ namespace pa {
 
 namespace {
 
-constexpr float kPShift = 15.f;  // P is held times 2^15
+#ifndef PA_DECODE_FP4_WARPS
+#define PA_DECODE_FP4_WARPS 4
+#endif
+#ifndef PA_DECODE_FP4_STAGES
+#define PA_DECODE_FP4_STAGES 2
+#endif
+#ifndef PA_DECODE_FP4_CTAS
+#define PA_DECODE_FP4_CTAS 4
+#endif
 
-// Geometry of a tile in shared memory: rows of D / 2 bytes in the swizzle of
-// that row length (64 bytes: 16-byte unit u of row r at u ^ ((r >> 1) & 3);
-// 32 bytes: u ^ ((r >> 2) & 1)), the scales in the rows after the codes.
-template <int D> struct Fp4Shape {
-  static constexpr int kRow = D / 2;                   // bytes of a token's codes
-  static constexpr int kScales = D / 16;               // bytes of a token's scales
-  static constexpr int kSwizzle = D == 128 ? 3 : 1;    // units that a row's XOR reaches
-  static constexpr int kSlot16 = D == 128 ? 1536 : 768;  // a 16-token tile, on a swizzle period
-  static constexpr int kUnit = 2 * kSlot16;            // 32 tokens of K or V (one or two tiles)
+// P is held times 2^11, against a reference that is at most 2^4 below the
+// running maximum: below 2^15 then, and in fp16's normal range down to 2^-25 of
+// the maximum.
+constexpr float kPShift = 11.f, kGrowth = 4.f;
+
+// Geometry of a tile in shared memory.  TMA brings it in lines of D bytes (the
+// codes of two tokens; 9 lines for 16 tokens, the last of them scales) with the
+// swizzle of that line length: byte address bits 4.. ^= bits 7.. (three bits at
+// 128-byte lines, two at 64).  A 16-token tile takes a place of 12 lines, so
+// that the second tile of a 32-token unit (and of no other pair of places)
+// starts half a swizzle period off: all its addresses are XORed with kOdd.
+template <int D, int BS> struct Fp4Shape {
+  static constexpr int kRow = D / 2;                     // bytes of a token's codes
+  static constexpr int kScales = D / 16;                 // bytes of a token's scales
+  static constexpr int kSlot16 = 12 * D;
+  static constexpr int kUnit = 2 * kSlot16;              // 32 tokens of K or V
+  static constexpr int kTiles = 32 / BS;                 // tiles of a unit
+  static constexpr int kLines = BS * 9 / 16;             // lines of a tile
+  static constexpr int kTileBytes = fp4_tile_bytes(BS, D);
+  static constexpr int kOdd = BS == 16 ? D / 2 : 0;
+  // codes and scales of the unit's 16-token half h
+  __host__ __device__ static constexpr int codes(int h) { return h * (BS == 16 ? kSlot16 : 16 * kRow); }
+  __host__ __device__ static constexpr int scales(int h) {
+    return BS == 16 ? h * kSlot16 + 16 * kRow : 32 * kRow + h * 16 * kScales;
+  }
+  __host__ __device__ static constexpr int flip_codes(int h) { return h * kOdd; }
+  // (the second half's scales of a 32-token tile lie in the line that the
+  // 128-byte swizzle XORs with one 16-byte unit)
+  __host__ __device__ static constexpr int flip_scales(int h) { return h * (BS == 16 ? kOdd : (D == 128 ? 16 : 0)); }
   static constexpr int kMTiles = D / 16;
   static constexpr int kQChunks = D / 32;
 };
 
-// Row of a 16-token sub-tile that MMA row r stands for: a permutation that
-// puts the four V rows 2c (c = 0..3) into different banks.
+// Row of a 16-token half that MMA row r stands for: a permutation that puts
+// the four V rows 2c (c = 0..3) into different banks.
 template <int D> __device__ __forceinline__ int token_of(int r) {
   return D == 128 ? r ^ ((r >> 1) & 1) : r ^ ((r >> 2) & 1);
 }
+// Byte `b` of the codes of token r in a half, in the swizzle of its lines.
+template <int D> __device__ __forceinline__ int code_at(int r, int b) {
+  const int at = r * (D / 2) + b;
+  return at ^ (((at >> 7) & (D == 128 ? 7 : 3)) << 4);
+}
 
-// T: query and output type.  NW warps, S stages each, U 32-token units per
-// step.  WP: each warp takes a whole partition and writes its partial itself
-// (partitions joined by the reduce kernel), as in the 16-bit kernel.
-template <typename T, int D, int NW, int S, int U, bool WP>
-__global__ void __launch_bounds__(NW * 32)
+// T: query and output type.  NW warps, S stages each.  WP: each warp takes a
+// whole partition and writes its partial itself (partitions joined by the
+// reduce kernel), as in the 16-bit kernel.
+template <typename T, int D, int BS, int NW, int S, bool WP>
+__global__ void __launch_bounds__(NW * 32, PA_DECODE_FP4_CTAS)
     pa_decode_fp4_kernel(const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap, const DecodeArgs a) {
-  using Sh = Fp4Shape<D>;
-  constexpr int kStep = 2 * U * Sh::kUnit;  // K then V of a step
-  constexpr int kSubs = 2 * U;              // 16-token sub-tiles of a step
+  using Sh = Fp4Shape<D, BS>;
+  constexpr int kStep = 2 * Sh::kUnit;  // K then V of a 32-token step
+  constexpr int kTiles = Sh::kTiles;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -96,18 +130,14 @@ __global__ void __launch_bounds__(NW * 32)
   __syncwarp();
   grid_dependency_wait();  // the pool may come from the kernel before
 
-  // Units are 32-token windows of the sequence from the one that holds the
+  // Steps are 32-token windows of the sequence from the one that holds the
   // partition's first token on: a block never straddles two.  A warp's tiles
-  // (tpu = 32 / block_size of them a unit) are numbered l in its own order; 32
-  // lanes hold the block ids of a window of them.
+  // are numbered l in its own order; 32 lanes hold a window of 32 of them.
   const int t_begin = part * a.part_tokens;
   const int base = t_begin & ~31;
-  const int tsh = 5 - a.bs_log2, tpu = 1 << tsh;  // 1 or 2 tiles a unit
   const int32_t *bt_row = a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq;
-  auto unit_of = [&](int lu) {  // the warp's local unit -> the partition's
-    return WP ? lu : (warp + (lu / U) * NW) * U + lu % U;
-  };
-  auto block_of = [&](int l) { return (base >> a.bs_log2) + (unit_of(l >> tsh) << tsh) + (l & (tpu - 1)); };
+  auto step_token = [&](int k) { return base + (WP ? k : warp + k * NW) * 32; };
+  auto block_of = [&](int l) { return step_token(l / kTiles) / BS + l % kTiles; };
   auto table_entry = [&](int l) -> int {
     const int lb = block_of(l);
     return lb < a.max_blocks_per_seq ? bt_row[lb] : -1;
@@ -115,75 +145,55 @@ __global__ void __launch_bounds__(NW * 32)
   int win = table_entry(lane);  // read before the length arrives; entries past it are not used
 
   int ctx = a.context_lens[seq];
-  if (ctx < 0 || ctx > (a.max_blocks_per_seq << a.bs_log2) || ctx > a.max_context_len) {
+  if (ctx < 0 || ctx > a.max_blocks_per_seq * BS || ctx > a.max_context_len) {
     if (threadIdx.x == 0 && part == 0 && kvh == 0) atomicOr(a.err, kErrBadLen);
     ctx = 0;
   }
   if (part > 0 && t_begin >= ctx) return;
   const int np_seq = ctx > 0 ? (ctx + a.part_tokens - 1) / a.part_tokens : 1;
   const int t_end = min(ctx, t_begin + a.part_tokens);
-  const int n_unit = t_end > base ? (t_end - base + 31) / 32 : 0;
-  const int n_grp = (n_unit + U - 1) / U;
-  const int my_n = WP ? n_grp : (n_grp > warp ? (n_grp - warp + NW - 1) / NW : 0);
+  const int n_step = t_end > base ? (t_end - base + 31) / 32 : 0;
+  const int my_n = WP ? n_step : (n_step > warp ? (n_step - warp + NW - 1) / NW : 0);
 
-  // block id of the warp's tile l; -1 if it holds no token of the partition or is invalid
-  auto checked = [&](int l, int phys) -> int {
+  // First line of the warp's tile l in the pool.  Every step loads all its
+  // tiles: in place of one without a token of the partition, and of an invalid
+  // block id, block 0 is read and nothing of it used.
+  bool bad = false;  // an invalid id was met (the same in all lanes)
+  auto line_of = [&](int l, int phys) -> int {
     const int lb = block_of(l);
-    if (l >= ((my_n * U) << tsh) || lb > ((t_end - 1) >> a.bs_log2) || lb < (t_begin >> a.bs_log2))
-      return -1;
-    if (phys < 0 || static_cast<int64_t>(phys) >= a.num_blocks) {
-      atomicOr(a.err, kErrBadBlock);
-      return -1;
-    }
-    return phys;
+    const bool used = l < my_n * kTiles && lb <= (t_end - 1) / BS && lb >= t_begin / BS;
+    const bool ok = phys >= 0 && static_cast<int64_t>(phys) < a.num_blocks;
+    if (used && !ok) atomicOr(a.err, kErrBadBlock);
+    bad = bad || __any_sync(kFull, used && !ok);
+    return ((used && ok ? phys : 0) * a.num_kv_heads + kvh) * Sh::kLines;
   };
+  int win_base = 0;
+  win = line_of(lane, win);
+  int win_next = my_n * kTiles > 32 ? line_of(32 + lane, table_entry(32 + lane)) : 0;
 
   const uint64_t policy = l2_policy_evict_first();
-  const uint32_t tile_bytes = fp4_tile_bytes(1 << a.bs_log2, D);
-  const int tile_rows = 18 << (a.bs_log2 - 4);
-  // lane 0: load the tiles of a step (phys of tile i in unit-tile order) into stage s
-  auto issue = [&](const int (&phys)[kSubs], int s) {
-    uint64_t *bar = &my_bars[s];
-    uint32_t bytes = 0;
-#pragma unroll
-    for (int i = 0; i < kSubs; ++i) bytes += i < (U << tsh) && phys[i] >= 0 ? 2 * tile_bytes : 0;
-    if (bytes == 0) {
-      mbar_arrive(bar);
-      return;
+  auto fill = [&](int k, int s) {  // called for k = 0, 1, 2, ...
+    if (k * kTiles >= win_base + 32) {
+      win_base += 32;
+      win = win_next;
+      win_next = line_of(win_base + 32 + lane, table_entry(win_base + 32 + lane));
     }
-    mbar_arrive_expect_tx(bar, bytes);
-    uint8_t *st = my_stages + s * kStep;
-#pragma unroll
-    for (int i = 0; i < kSubs; ++i) {
-      if (i >= (U << tsh) || phys[i] < 0) continue;
-      const int y = (phys[i] * a.num_kv_heads + kvh) * tile_rows;
-      uint8_t *dst = st + (i >> tsh) * Sh::kUnit + (i & (tpu - 1)) * Sh::kSlot16;
-      tma_load_2d(dst, &kmap, 0, y, bar, policy);
-      tma_load_2d(dst + U * Sh::kUnit, &vmap, 0, y, bar, policy);
-    }
-  };
-
-  int win_base = 0;
-  win = checked(lane, win);
-  const int my_tiles = (my_n * U) << tsh;
-  int win_next = my_tiles > 32 ? checked(32 + lane, table_entry(32 + lane)) : -1;
-  uint32_t stage_ok = 0;  // bit s kSubs + i: tile i of stage s is loaded
-  auto tiles_of = [&](int k, int s, int (&phys)[kSubs]) {
-#pragma unroll
-    for (int i = 0; i < kSubs; ++i) {
-      phys[i] = __shfl_sync(kFull, win, (((k * U) << tsh) + i - win_base) & 31);
-      const uint32_t bit = 1u << (s * kSubs + i);
-      stage_ok = phys[i] >= 0 && i < (U << tsh) ? stage_ok | bit : stage_ok & ~bit;
+    const int y0 = __shfl_sync(kFull, win, (k * kTiles) & 31);
+    const int y1 = kTiles == 2 ? __shfl_sync(kFull, win, (k * kTiles + 1) & 31) : 0;
+    if (lane == 0) {
+      uint8_t *st = my_stages + s * kStep;
+      fence_proxy_async_smem();
+      mbar_arrive_expect_tx(&my_bars[s], 2 * kTiles * Sh::kTileBytes);
+      tma_load_2d(st, &kmap, 0, y0, &my_bars[s], policy);
+      if (kTiles == 2) tma_load_2d(st + Sh::kSlot16, &kmap, 0, y1, &my_bars[s], policy);
+      tma_load_2d(st + Sh::kUnit, &vmap, 0, y0, &my_bars[s], policy);
+      if (kTiles == 2)
+        tma_load_2d(st + Sh::kUnit + Sh::kSlot16, &vmap, 0, y1, &my_bars[s], policy);
     }
   };
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    if (s < my_n) {
-      int phys[kSubs];
-      tiles_of(s, s, phys);
-      if (lane == 0) issue(phys, s);
-    }
-  }
+  for (int s = 0; s < S; ++s)
+    if (s < my_n) fill(s, s);
 
   // query fragments of head g, in the order of the K bytes a lane reads
   const int G = a.group;
@@ -228,140 +238,140 @@ __global__ void __launch_bounds__(NW * 32)
     }
   }
 
-  // The lane's places in a sub-tile: K rows token_of(g) and + 8, V rows
-  // t0 = token_of(2c), t1 = token_of(2c + 1) and + 8 (rows 8 apart share their
-  // swizzle and lie 8 kRow bytes apart).
+  // The lane's places in a half: K rows token_of(g) and + 8, V rows t0 =
+  // token_of(2c), t1 = token_of(2c + 1) and + 8.  Row r + 8 lies 8 kRow bytes
+  // on, in lines whose 128-byte swizzle differs in unit bit 2 (a 64-byte line's
+  // in none).
   const int kr = token_of<D>(g), t0 = token_of<D>(2 * c), t1 = token_of<D>(2 * c + 1);
-  int k_at, v_at0, v_at1;
-  if constexpr (D == 128) {
-    k_at = kr * 64 + ((c ^ ((kr >> 1) & 3)) << 4);
-    const int in_row = (((g >> 1) ^ c) << 4) + (g & 1) * 8;  // (t0 >> 1) & 3 = (t1 >> 1) & 3 = c
-    v_at0 = t0 * 64 + in_row;
-    v_at1 = t1 * 64 + in_row;
-  } else {
-    k_at = kr * 32 + (((c >> 1) ^ ((kr >> 2) & 1)) << 4) + (c & 1) * 8;
-    const int in_row = (((g >> 2) ^ (c >> 1)) << 4) + (g & 3) * 4;  // (t0 >> 2) & 1 = c >> 1
-    v_at0 = t0 * 32 + in_row;
-    v_at1 = t1 * 32 + in_row;
-  }
-  const int kb = D == 128 ? 2 * c : c, vb = D == 128 ? g : g >> 1;  // scale groups of the lane
-  // a 16-token sub-tile h of a unit: its codes and its scales.  The scales of
-  // the upper half of a 32-token tile lie in rows whose swizzle flips unit 0.
-  const bool bs16 = a.bs_log2 == 4;
-  const int sub_step = bs16 ? Sh::kSlot16 : 16 * Sh::kRow;
-  const int sc_base = bs16 ? 16 * Sh::kRow : 32 * Sh::kRow;
-  const int sc_step = bs16 ? Sh::kSlot16 : 16 * Sh::kScales;
-  const int sc_flip = D == 128 && !bs16 ? 16 : 0;
+  constexpr int kBytes = D == 128 ? 16 : 8;  // of a K row; of a V row half of them
+  const int k_a = code_at<D>(kr, c * kBytes), k_b = code_at<D>(kr + 8, c * kBytes);
+  const int v_0 = code_at<D>(t0, g * kBytes / 2), v_1 = code_at<D>(t1, g * kBytes / 2);
+  const int v_2 = code_at<D>(t0 + 8, g * kBytes / 2), v_3 = code_at<D>(t1 + 8, g * kBytes / 2);
+  // scale groups of the lane: 2c and 2c + 1 (or c) of K, g (or g / 2) of V
+  const int ks_a = kr * Sh::kScales + (D == 128 ? 2 * c : c), ks_b = ks_a + 8 * Sh::kScales;
+  const int vs_0 = t0 * Sh::kScales + (D == 128 ? g : g >> 1);
+  const int vs_1 = t1 * Sh::kScales + (D == 128 ? g : g >> 1);
 
   const float NEG_INF = -INFINITY;
-  float m0 = NEG_INF, m1 = NEG_INF, l0 = 0.f, l1 = 0.f;  // heads 2c, 2c + 1
+  // online softmax of the lane's heads 2c and 2c + 1 in base 2: c0 = kPShift -
+  // the reference of head 2c, so that probabilities are held as 2^(x + c0);
+  // before the first token the reference is far below any score
+  float c0 = 1e30f, c1 = 1e30f, l0 = 0.f, l1 = 0.f;
   float acc[Sh::kMTiles][4];
 #pragma unroll
   for (int mt = 0; mt < Sh::kMTiles; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
 
   bool timed_out = false;
-  int k_stop = my_n;
+  int k = 0;
 #pragma unroll 1
-  for (int k = 0; k < my_n; ++k) {
+  for (; k < my_n; ++k) {
     const int s = k % S;
     if (!__all_sync(kFull, mbar_wait_bounded(&my_bars[s], (k / S) & 1))) {
       if (lane == 0) atomicOr(a.err, kErrTimeout);
       timed_out = true;
-      k_stop = k;
       break;
     }
     const uint8_t *stage = my_stages + s * kStep;
-    // valid tokens [lo, hi) of each sub-tile
-    int lo[kSubs], hi[kSubs];
-    bool whole = true;
-#pragma unroll
-    for (int h = 0; h < kSubs; ++h) {
-      const int tile = bs16 ? h : h >> 1;
-      const int tok = base + unit_of(k * U + (h >> 1)) * 32 + (h & 1) * 16;
-      const bool ok = (stage_ok >> (s * kSubs + tile)) & 1u;
-      lo[h] = max(0, t_begin - tok);
-      hi[h] = ok ? max(0, min(16, t_end - tok)) : 0;
-      whole = whole && lo[h] == 0 && hi[h] == 16;
-    }
 
     // ---- S^T = K Q^T
-    float x[kSubs][4];
+    float x[2][4];
 #pragma unroll
-    for (int h = 0; h < kSubs; ++h) {
-      const uint8_t *unit = stage + (h >> 1) * Sh::kUnit;
-      const uint8_t *Ks = unit + (h & 1) * sub_step + k_at;
-      const uint8_t *sc = unit + sc_base + (h & 1) * sc_step;
-      const int flip = (h & 1) * sc_flip;
-      const int sa = ((kr * Sh::kScales) ^ flip) + kb, sb = (((kr + 8) * Sh::kScales) ^ flip) + kb;
-      x[h][0] = x[h][1] = x[h][2] = x[h][3] = 0.f;
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t *Ks = stage + Sh::codes(h);
+      const uint8_t *sc = stage + Sh::scales(h);
+      // two chains of products, so that half of them wait for one another
+      float y[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      const int ca = k_a ^ Sh::flip_codes(h), cb = k_b ^ Sh::flip_codes(h);
+      const int sa = ks_a ^ Sh::flip_scales(h), sb = ks_b ^ Sh::flip_scales(h);
+      uint32_t pa, pb;  // the scales of rows a and b as fp16 pairs
+      uint32_t wa[D / 32], wb[D / 32];
       if constexpr (D == 128) {
-        const uint4 wa = *reinterpret_cast<const uint4 *>(Ks);
-        const uint4 wb = *reinterpret_cast<const uint4 *>(Ks + 8 * Sh::kRow);
-        const uint32_t pa = e4m3x2_lo_to_f16x2(*reinterpret_cast<const uint16_t *>(sc + sa));
-        const uint32_t pb = e4m3x2_lo_to_f16x2(*reinterpret_cast<const uint16_t *>(sc + sb));
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t ga = __byte_perm(pa, 0, w < 2 ? 0x1010 : 0x3232);
-          const uint32_t gb = __byte_perm(pb, 0, w < 2 ? 0x1010 : 0x3232);
-          uint32_t ha[4], hb[4];
-          e2m1x8_to_half(word_of(wa, w), ha);
-          e2m1x8_to_half(word_of(wb, w), hb);
-          Elem<__half>::mma(x[h], f16x2_mul(ha[0], ga), f16x2_mul(hb[0], gb), f16x2_mul(ha[1], ga),
-                            f16x2_mul(hb[1], gb), qf[w].x, qf[w].y);
-          Elem<__half>::mma(x[h], f16x2_mul(ha[2], ga), f16x2_mul(hb[2], gb), f16x2_mul(ha[3], ga),
-                            f16x2_mul(hb[3], gb), qf[w].z, qf[w].w);
-        }
+        const uint4 va = *reinterpret_cast<const uint4 *>(Ks + ca);
+        const uint4 vb = *reinterpret_cast<const uint4 *>(Ks + cb);
+        wa[0] = va.x, wa[1] = va.y, wa[2] = va.z, wa[3] = va.w;
+        wb[0] = vb.x, wb[1] = vb.y, wb[2] = vb.z, wb[3] = vb.w;
+        pa = e4m3x2_lo_to_f16x2(*reinterpret_cast<const uint16_t *>(sc + sa));
+        pb = e4m3x2_lo_to_f16x2(*reinterpret_cast<const uint16_t *>(sc + sb));
       } else {
-        const uint2 wa = *reinterpret_cast<const uint2 *>(Ks);
-        const uint2 wb = *reinterpret_cast<const uint2 *>(Ks + 8 * Sh::kRow);
-        const uint32_t p = e4m3x2_lo_to_f16x2(sc[sa] | (static_cast<uint32_t>(sc[sb]) << 8));
-        const uint32_t ga = __byte_perm(p, 0, 0x1010), gb = __byte_perm(p, 0, 0x3232);
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          uint32_t ha[4], hb[4];
-          e2m1x8_to_half(w == 0 ? wa.x : wa.y, ha);
-          e2m1x8_to_half(w == 0 ? wb.x : wb.y, hb);
-          Elem<__half>::mma(x[h], f16x2_mul(ha[0], ga), f16x2_mul(hb[0], gb), f16x2_mul(ha[1], ga),
-                            f16x2_mul(hb[1], gb), qf[w].x, qf[w].y);
-          Elem<__half>::mma(x[h], f16x2_mul(ha[2], ga), f16x2_mul(hb[2], gb), f16x2_mul(ha[3], ga),
-                            f16x2_mul(hb[3], gb), qf[w].z, qf[w].w);
-        }
+        const uint2 va = *reinterpret_cast<const uint2 *>(Ks + ca);
+        const uint2 vb = *reinterpret_cast<const uint2 *>(Ks + cb);
+        wa[0] = va.x, wa[1] = va.y;
+        wb[0] = vb.x, wb[1] = vb.y;
+        pa = e4m3x2_lo_to_f16x2(sc[sa] * 0x101u);
+        pb = e4m3x2_lo_to_f16x2(sc[sb] * 0x101u);
       }
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) {
+        const uint32_t ga = D == 64 ? pa : __byte_perm(pa, 0, w < 2 ? 0x1010 : 0x3232);
+        const uint32_t gb = D == 64 ? pb : __byte_perm(pb, 0, w < 2 ? 0x1010 : 0x3232);
+        uint32_t ha[4], hb[4];
+        e2m1x8_to_half(wa[w], ha);
+        e2m1x8_to_half(wb[w], hb);
+        Elem<__half>::mma(y[0], f16x2_mul(ha[0], ga), f16x2_mul(hb[0], gb), f16x2_mul(ha[1], ga),
+                          f16x2_mul(hb[1], gb), qf[w].x, qf[w].y);
+        Elem<__half>::mma(y[1], f16x2_mul(ha[2], ga), f16x2_mul(hb[2], gb), f16x2_mul(ha[3], ga),
+                          f16x2_mul(hb[3], gb), qf[w].z, qf[w].w);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[h][e] = y[0][e] + y[1][e];
     }
 
-    // ---- online softmax in base 2, one reduction for the step's tokens
-#pragma unroll
-    for (int h = 0; h < kSubs; ++h) {
-      x[h][0] *= sl0;
-      x[h][1] *= sl1;
-      x[h][2] *= sl0;
-      x[h][3] *= sl1;
-    }
+    // whole: every token of the step counts; otherwise those that the mask has
+    // (bit i: token step_tok + i)
+    const int step_tok = step_token(k);
+    const bool whole = !bad && step_tok >= t_begin && step_tok + 32 <= t_end;
+    uint32_t mask = 0xffffffffu;
     if (!whole) {
-#pragma unroll
-      for (int h = 0; h < kSubs; ++h) {
-        const bool va = kr >= lo[h] && kr < hi[h], vz = kr + 8 >= lo[h] && kr + 8 < hi[h];
-        x[h][0] = va ? x[h][0] : NEG_INF;
-        x[h][1] = va ? x[h][1] : NEG_INF;
-        x[h][2] = vz ? x[h][2] : NEG_INF;
-        x[h][3] = vz ? x[h][3] : NEG_INF;
+      const int tok = step_tok + lane;
+      bool in = tok >= t_begin && tok < t_end;
+      if (bad && in) {
+        const int phys = bt_row[tok / BS];
+        in = phys >= 0 && static_cast<int64_t>(phys) < a.num_blocks;
       }
+      mask = __ballot_sync(kFull, in);
     }
-    float mx0 = m0, mx1 = m1;
+    // z = scores + (b0, b1); tokens that do not count get -inf
+    auto logits = [&](float (&z)[2][4], float b0, float b1) {
 #pragma unroll
-    for (int h = 0; h < kSubs; ++h) {
-      mx0 = fmaxf(mx0, fmaxf(x[h][0], x[h][2]));
-      mx1 = fmaxf(mx1, fmaxf(x[h][1], x[h][3]));
-    }
+      for (int h = 0; h < 2; ++h) {
+        z[h][0] = fmaf(x[h][0], sl0, b0);
+        z[h][1] = fmaf(x[h][1], sl1, b1);
+        z[h][2] = fmaf(x[h][2], sl0, b0);
+        z[h][3] = fmaf(x[h][3], sl1, b1);
+        if (!whole) {
+          const bool va = (mask >> (16 * h + kr)) & 1u, vz = (mask >> (16 * h + kr + 8)) & 1u;
+          z[h][0] = va ? z[h][0] : NEG_INF;
+          z[h][1] = va ? z[h][1] : NEG_INF;
+          z[h][2] = vz ? z[h][2] : NEG_INF;
+          z[h][3] = vz ? z[h][3] : NEG_INF;
+        }
+      }
+    };
+    // 2^y are the probabilities; the reference moves only when one of them
+    // passes 2^(kPShift + kGrowth), so most steps need a vote and no shuffles
+    float y[2][4];
+    logits(y, c0, c1);
+    float top = NEG_INF;
 #pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
-      mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, off));
-      mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, off));
-    }
-    const float r0 = mx0 == NEG_INF ? 0.f : mx0 - kPShift;  // no valid token yet: any reference
-    const float r1 = mx1 == NEG_INF ? 0.f : mx1 - kPShift;
-    if (__any_sync(kFull, mx0 != m0 || mx1 != m1)) {
-      const float al0 = ex2_approx(m0 - kPShift - r0), al1 = ex2_approx(m1 - kPShift - r1);
+    for (int h = 0; h < 2; ++h)
+      top = fmaxf(top, fmaxf(fmaxf(y[h][0], y[h][1]), fmaxf(y[h][2], y[h][3])));
+    if (__any_sync(kFull, top > kPShift + kGrowth)) {
+      logits(y, 0.f, 0.f);
+      float mx0 = kPShift - c0, mx1 = kPShift - c1;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mx0 = fmaxf(mx0, fmaxf(y[h][0], y[h][2]));
+        mx1 = fmaxf(mx1, fmaxf(y[h][1], y[h][3]));
+      }
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, off));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, off));
+      }
+      const float n0 = kPShift - mx0, n1 = kPShift - mx1;
+      const float al0 = ex2_approx(n0 - c0), al1 = ex2_approx(n1 - c1);
+      c0 = n0;
+      c1 = n1;
       l0 *= al0;
       l1 *= al1;
 #pragma unroll
@@ -371,14 +381,13 @@ __global__ void __launch_bounds__(NW * 32)
         acc[mt][2] *= al0;
         acc[mt][3] *= al1;
       }
-      m0 = mx0;
-      m1 = mx1;
+      logits(y, c0, c1);
     }
-    uint32_t pb0[kSubs], pb1[kSubs];
+    uint32_t pb0[2], pb1[2];
 #pragma unroll
-    for (int h = 0; h < kSubs; ++h) {
-      const float p0 = ex2_approx(x[h][0] - r0), p1 = ex2_approx(x[h][1] - r1);
-      const float p2 = ex2_approx(x[h][2] - r0), p3 = ex2_approx(x[h][3] - r1);
+    for (int h = 0; h < 2; ++h) {
+      const float p0 = ex2_approx(y[h][0]), p1 = ex2_approx(y[h][1]);
+      const float p2 = ex2_approx(y[h][2]), p3 = ex2_approx(y[h][3]);
       l0 += p0 + p2;
       l1 += p1 + p3;
       // P^T as the B operand: an 8x8 transpose of the accumulator's layout
@@ -388,18 +397,17 @@ __global__ void __launch_bounds__(NW * 32)
 
     // ---- O^T += V^T P^T
 #pragma unroll
-    for (int h = 0; h < kSubs; ++h) {
-      const uint8_t *unit = stage + (U + (h >> 1)) * Sh::kUnit;
-      const uint8_t *Vs = unit + (h & 1) * sub_step;
-      const uint8_t *sc = unit + sc_base + (h & 1) * sc_step + vb;
-      const int flip = (h & 1) * sc_flip;
-      uint32_t s0 = sc[(t0 * Sh::kScales) ^ flip], s1 = sc[(t1 * Sh::kScales) ^ flip];
-      uint32_t s2 = sc[((t0 + 8) * Sh::kScales) ^ flip], s3 = sc[((t1 + 8) * Sh::kScales) ^ flip];
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t *Vs = stage + Sh::kUnit + Sh::codes(h);
+      const uint8_t *sc = stage + Sh::kUnit + Sh::scales(h);
+      uint32_t s0 = sc[vs_0 ^ Sh::flip_scales(h)], s1 = sc[vs_1 ^ Sh::flip_scales(h)];
+      uint32_t s2 = sc[(vs_0 + 8 * Sh::kScales) ^ Sh::flip_scales(h)];
+      uint32_t s3 = sc[(vs_1 + 8 * Sh::kScales) ^ Sh::flip_scales(h)];
       if (!whole) {
-        s0 = t0 >= lo[h] && t0 < hi[h] ? s0 : 0;
-        s1 = t1 >= lo[h] && t1 < hi[h] ? s1 : 0;
-        s2 = t0 + 8 >= lo[h] && t0 + 8 < hi[h] ? s2 : 0;
-        s3 = t1 + 8 >= lo[h] && t1 + 8 < hi[h] ? s3 : 0;
+        s0 = (mask >> (16 * h + t0)) & 1u ? s0 : 0;
+        s1 = (mask >> (16 * h + t1)) & 1u ? s1 : 0;
+        s2 = (mask >> (16 * h + t0 + 8)) & 1u ? s2 : 0;
+        s3 = (mask >> (16 * h + t1 + 8)) & 1u ? s3 : 0;
       }
       const uint32_t g01 = e4m3x2_lo_to_f16x2(s0 | (s1 << 8));
       const uint32_t g23 = e4m3x2_lo_to_f16x2(s2 | (s3 << 8));
@@ -408,58 +416,47 @@ __global__ void __launch_bounds__(NW * 32)
         e2m1x8_to_half((A & 0x0f0f0f0fu) | ((B << 4) & 0xf0f0f0f0u), even);
         e2m1x8_to_half(((A >> 4) & 0x0f0f0f0fu) | (B & 0xf0f0f0f0u), odd);
       };
+      const int c_0 = v_0 ^ Sh::flip_codes(h), c_1 = v_1 ^ Sh::flip_codes(h);
+      const int c_2 = v_2 ^ Sh::flip_codes(h), c_3 = v_3 ^ Sh::flip_codes(h);
       if constexpr (D == 128) {
-        const uint2 v0 = *reinterpret_cast<const uint2 *>(Vs + v_at0);
-        const uint2 v1 = *reinterpret_cast<const uint2 *>(Vs + v_at1);
-        const uint2 v2 = *reinterpret_cast<const uint2 *>(Vs + v_at0 + 8 * Sh::kRow);
-        const uint2 v3 = *reinterpret_cast<const uint2 *>(Vs + v_at1 + 8 * Sh::kRow);
+        const uint2 w0 = *reinterpret_cast<const uint2 *>(Vs + c_0);
+        const uint2 w1 = *reinterpret_cast<const uint2 *>(Vs + c_1);
+        const uint2 w2 = *reinterpret_cast<const uint2 *>(Vs + c_2);
+        const uint2 w3 = *reinterpret_cast<const uint2 *>(Vs + c_3);
         uint32_t a0[2][4], a1[2][4], a2[2][4], a3[2][4];
-        pairs(v0.x, v1.x, a0[0], a0[1]);
-        pairs(v0.y, v1.y, a1[0], a1[1]);
-        pairs(v2.x, v3.x, a2[0], a2[1]);
-        pairs(v2.y, v3.y, a3[0], a3[1]);
+        pairs(w0.x, w1.x, a0[0], a0[1]);
+        pairs(w0.y, w1.y, a1[0], a1[1]);
+        pairs(w2.x, w3.x, a2[0], a2[1]);
+        pairs(w2.y, w3.y, a3[0], a3[1]);
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt)
           Elem<__half>::mma(acc[mt], f16x2_mul(a0[mt & 1][mt >> 1], g01),
-                            f16x2_mul(a1[mt & 1][mt >> 1], g01), f16x2_mul(a2[mt & 1][mt >> 1], g23),
+                            f16x2_mul(a1[mt & 1][mt >> 1], g01),
+                            f16x2_mul(a2[mt & 1][mt >> 1], g23),
                             f16x2_mul(a3[mt & 1][mt >> 1], g23), pb0[h], pb1[h]);
       } else {
         uint32_t a0[2][4], a2[2][4];
-        pairs(*reinterpret_cast<const uint32_t *>(Vs + v_at0),
-              *reinterpret_cast<const uint32_t *>(Vs + v_at1), a0[0], a0[1]);
-        pairs(*reinterpret_cast<const uint32_t *>(Vs + v_at0 + 8 * Sh::kRow),
-              *reinterpret_cast<const uint32_t *>(Vs + v_at1 + 8 * Sh::kRow), a2[0], a2[1]);
+        pairs(*reinterpret_cast<const uint32_t *>(Vs + c_0),
+              *reinterpret_cast<const uint32_t *>(Vs + c_1), a0[0], a0[1]);
+        pairs(*reinterpret_cast<const uint32_t *>(Vs + c_2),
+              *reinterpret_cast<const uint32_t *>(Vs + c_3), a2[0], a2[1]);
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
           Elem<__half>::mma(acc[mt], f16x2_mul(a0[mt & 1][mt >> 1], g01),
-                            f16x2_mul(a0[mt & 1][2 + (mt >> 1)], g01), f16x2_mul(a2[mt & 1][mt >> 1], g23),
+                            f16x2_mul(a0[mt & 1][2 + (mt >> 1)], g01),
+                            f16x2_mul(a2[mt & 1][mt >> 1], g23),
                             f16x2_mul(a2[mt & 1][2 + (mt >> 1)], g23), pb0[h], pb1[h]);
       }
     }
 
     // ---- refill this stage with step k + S
     __syncwarp();
-    const int nk = k + S;
-    if (nk < my_n) {
-      if (((nk * U) << tsh) >= win_base + 32) {
-        win_base += 32;
-        win = win_next;
-        win_next = checked(win_base + 32 + lane, table_entry(win_base + 32 + lane));
-      }
-      int phys[kSubs];
-      tiles_of(nk, s, phys);
-      if (lane == 0) {
-        fence_proxy_async_smem();
-        issue(phys, s);
-      }
-    }
+    if (k + S < my_n) fill(k + S, s);
   }
-
-  if (timed_out) {
-    // let copies already in flight land before the CTA leaves (bounded again)
-    for (int kk = k_stop; kk < min(k_stop + S, my_n); ++kk)
-      (void)mbar_wait_bounded(&my_bars[kk % S], (kk / S) & 1);
-  }
+  // after a wait that ran out, copies already in flight land before the CTA
+  // leaves (bounded again)
+  for (const int filled = min(k + S, my_n); timed_out && k < filled; ++k)
+    (void)mbar_wait_bounded(&my_bars[k % S], (k / S) & 1);
 
   // row sums over the 8 token rows; l and acc are both held times 2^kPShift
   const float unshift = exp2f(-kPShift);
@@ -470,6 +467,7 @@ __global__ void __launch_bounds__(NW * 32)
   }
   l0 *= unshift;
   l1 *= unshift;
+  const float m0 = kPShift - c0, m1 = kPShift - c1;  // the references
 
   if constexpr (WP) {
     const int64_t row0 = static_cast<int64_t>(seq) * a.num_q_heads + kvh * G;
@@ -550,26 +548,15 @@ __global__ void __launch_bounds__(NW * 32)
   grid_launch_dependents();
 }
 
-#ifndef PA_DECODE_FP4_WARPS
-#define PA_DECODE_FP4_WARPS 4
-#endif
-#ifndef PA_DECODE_FP4_STAGES
-#define PA_DECODE_FP4_STAGES 2
-#endif
-#ifndef PA_DECODE_FP4_UNITS
-#define PA_DECODE_FP4_UNITS 1
-#endif
-
-template <typename T, int D, bool WP>
+template <typename T, int D, int BS, bool WP>
 cudaError_t launch_w(const DecodeArgs &a, const CUtensorMap &km, const CUtensorMap &vm,
                      cudaStream_t stream) {
-  constexpr int NW = PA_DECODE_FP4_WARPS, S = PA_DECODE_FP4_STAGES, U = PA_DECODE_FP4_UNITS;
-  constexpr size_t stages = static_cast<size_t>(NW) * S * 2 * U * Fp4Shape<D>::kUnit;
+  constexpr int NW = PA_DECODE_FP4_WARPS, S = PA_DECODE_FP4_STAGES;
+  constexpr size_t stages = static_cast<size_t>(NW) * S * 2 * Fp4Shape<D, BS>::kUnit;
   constexpr size_t smem = 1024 + stages + NW * S * 8;
   static_assert(static_cast<size_t>(NW) * 8 * D * 4 + NW * 8 * 2 * 4 + 16 <= stages,
                 "merge buffers and the join flag must fit in the stage area");
-  static_assert(S * 2 * U <= 32, "stage bits");
-  auto kern = pa_decode_fp4_kernel<T, D, NW, S, U, WP>;
+  auto kern = pa_decode_fp4_kernel<T, D, BS, NW, S, WP>;
   static SmemLimitOnce smem_limit;
   const cudaError_t e = smem_limit.ensure(kern, smem);
   if (e != cudaSuccess) return e;
@@ -582,8 +569,12 @@ cudaError_t launch_w(const DecodeArgs &a, const CUtensorMap &km, const CUtensorM
 template <typename T, int D>
 cudaError_t launch_t(const DecodeArgs &a, const CUtensorMap &km, const CUtensorMap &vm,
                      cudaStream_t stream) {
-  return a.num_parts > 1 && !a.fuse_join ? launch_w<T, D, true>(a, km, vm, stream)
-                                         : launch_w<T, D, false>(a, km, vm, stream);
+  const bool wp = a.num_parts > 1 && !a.fuse_join;
+  if (a.bs_log2 == 4)
+    return wp ? launch_w<T, D, 16, true>(a, km, vm, stream)
+              : launch_w<T, D, 16, false>(a, km, vm, stream);
+  return wp ? launch_w<T, D, 32, true>(a, km, vm, stream)
+            : launch_w<T, D, 32, false>(a, km, vm, stream);
 }
 
 }  // namespace

@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
       const int tsh = a.bs_log2 == 4 ? (kShare == 64 ? 2 : 1) : (kShare == 64 ? 1 : 0);
       const int tiles = 1 << tsh;              // tiles of a share
       const uint32_t tile_bytes = fp4_tile_bytes(1 << a.bs_log2, D);
-      const int tile_rows = 18 << (a.bs_log2 - 4);
+      const int tile_lines = 9 << (a.bs_log2 - 4);
       const int S = k_role ? SK : SV;
       uint64_t *full = k_role ? k_full : v_full;
       uint64_t *empty = k_role ? k_empty : v_empty;
@@ -893,7 +893,7 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
         if (lane < tiles && phys >= 0)
           tma_load_2d(raw + rs * L::kRawStep + (share0 / 16) * kRawSlot16<D> +
                           lane * (kRawSlot16<D> << (a.bs_log2 - 4)),
-                      map, 0, (phys * a.num_kv_heads + kvh) * tile_rows, &land[rs], policy);
+                      map, 0, (phys * a.num_kv_heads + kvh) * tile_lines, &land[rs], policy);
       };
       for (int m = 0; m < min(kRaw, n_steps); ++m) fetch(m);
       int m = 0;
