@@ -261,18 +261,10 @@ __global__ void __launch_bounds__(NW * 32, PA_DECODE_FP4_CTAS)
 #pragma unroll
   for (int mt = 0; mt < Sh::kMTiles; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
 
-  bool timed_out = false;
-  int k = 0;
-#pragma unroll 1
-  for (; k < my_n; ++k) {
-    const int s = k % S;
-    if (!__all_sync(kFull, mbar_wait_bounded(&my_bars[s], (k / S) & 1))) {
-      if (lane == 0) atomicOr(a.err, kErrTimeout);
-      timed_out = true;
-      break;
-    }
-    const uint8_t *stage = my_stages + s * kStep;
-
+  // One step, its K and V at `stage`.  masked: only the tokens that `mask` has
+  // count (bit i: token i of the step); the code of whole steps is apart, as
+  // the selects cost a seventh of a step's instructions.
+  auto step = [&](const uint8_t *stage, bool masked, uint32_t mask) {
     // ---- S^T = K Q^T
     float x[2][4];
 #pragma unroll
@@ -316,20 +308,6 @@ __global__ void __launch_bounds__(NW * 32, PA_DECODE_FP4_CTAS)
       for (int e = 0; e < 4; ++e) x[h][e] = y[0][e] + y[1][e];
     }
 
-    // whole: every token of the step counts; otherwise those that the mask has
-    // (bit i: token step_tok + i)
-    const int step_tok = step_token(k);
-    const bool whole = !bad && step_tok >= t_begin && step_tok + 32 <= t_end;
-    uint32_t mask = 0xffffffffu;
-    if (!whole) {
-      const int tok = step_tok + lane;
-      bool in = tok >= t_begin && tok < t_end;
-      if (bad && in) {
-        const int phys = bt_row[tok / BS];
-        in = phys >= 0 && static_cast<int64_t>(phys) < a.num_blocks;
-      }
-      mask = __ballot_sync(kFull, in);
-    }
     // z = scores + (b0, b1); tokens that do not count get -inf
     auto logits = [&](float (&z)[2][4], float b0, float b1) {
 #pragma unroll
@@ -338,7 +316,7 @@ __global__ void __launch_bounds__(NW * 32, PA_DECODE_FP4_CTAS)
         z[h][1] = fmaf(x[h][1], sl1, b1);
         z[h][2] = fmaf(x[h][2], sl0, b0);
         z[h][3] = fmaf(x[h][3], sl1, b1);
-        if (!whole) {
+        if (masked) {
           const bool va = (mask >> (16 * h + kr)) & 1u, vz = (mask >> (16 * h + kr + 8)) & 1u;
           z[h][0] = va ? z[h][0] : NEG_INF;
           z[h][1] = va ? z[h][1] : NEG_INF;
@@ -403,7 +381,7 @@ __global__ void __launch_bounds__(NW * 32, PA_DECODE_FP4_CTAS)
       uint32_t s0 = sc[vs_0 ^ Sh::flip_scales(h)], s1 = sc[vs_1 ^ Sh::flip_scales(h)];
       uint32_t s2 = sc[(vs_0 + 8 * Sh::kScales) ^ Sh::flip_scales(h)];
       uint32_t s3 = sc[(vs_1 + 8 * Sh::kScales) ^ Sh::flip_scales(h)];
-      if (!whole) {
+      if (masked) {
         s0 = (mask >> (16 * h + t0)) & 1u ? s0 : 0;
         s1 = (mask >> (16 * h + t1)) & 1u ? s1 : 0;
         s2 = (mask >> (16 * h + t0 + 8)) & 1u ? s2 : 0;
@@ -411,10 +389,13 @@ __global__ void __launch_bounds__(NW * 32, PA_DECODE_FP4_CTAS)
       }
       const uint32_t g01 = e4m3x2_lo_to_f16x2(s0 | (s1 << 8));
       const uint32_t g23 = e4m3x2_lo_to_f16x2(s2 | (s3 << 8));
-      // words of eight codes of tokens (A, B) -> even dimensions' pairs, odd dimensions' pairs
-      auto pairs = [](uint32_t A, uint32_t B, uint32_t (&even)[4], uint32_t (&odd)[4]) {
-        e2m1x8_to_half((A & 0x0f0f0f0fu) | ((B << 4) & 0xf0f0f0f0u), even);
-        e2m1x8_to_half(((A >> 4) & 0x0f0f0f0fu) | (B & 0xf0f0f0f0u), odd);
+      // words of eight codes of tokens A and B -> (A, B) pairs of the even or the odd dimensions
+      auto pairs = [](uint32_t A, uint32_t B, int odd, uint32_t s, uint32_t (&out)[4]) {
+        e2m1x8_to_half(odd ? ((A >> 4) & 0x0f0f0f0fu) | (B & 0xf0f0f0f0u)
+                           : (A & 0x0f0f0f0fu) | ((B << 4) & 0xf0f0f0f0u),
+                       out);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = f16x2_mul(out[i], s);
       };
       const int c_0 = v_0 ^ Sh::flip_codes(h), c_1 = v_1 ^ Sh::flip_codes(h);
       const int c_2 = v_2 ^ Sh::flip_codes(h), c_3 = v_3 ^ Sh::flip_codes(h);
@@ -423,30 +404,58 @@ __global__ void __launch_bounds__(NW * 32, PA_DECODE_FP4_CTAS)
         const uint2 w1 = *reinterpret_cast<const uint2 *>(Vs + c_1);
         const uint2 w2 = *reinterpret_cast<const uint2 *>(Vs + c_2);
         const uint2 w3 = *reinterpret_cast<const uint2 *>(Vs + c_3);
-        uint32_t a0[2][4], a1[2][4], a2[2][4], a3[2][4];
-        pairs(w0.x, w1.x, a0[0], a0[1]);
-        pairs(w0.y, w1.y, a1[0], a1[1]);
-        pairs(w2.x, w3.x, a2[0], a2[1]);
-        pairs(w2.y, w3.y, a3[0], a3[1]);
 #pragma unroll
-        for (int mt = 0; mt < 8; ++mt)
-          Elem<__half>::mma(acc[mt], f16x2_mul(a0[mt & 1][mt >> 1], g01),
-                            f16x2_mul(a1[mt & 1][mt >> 1], g01),
-                            f16x2_mul(a2[mt & 1][mt >> 1], g23),
-                            f16x2_mul(a3[mt & 1][mt >> 1], g23), pb0[h], pb1[h]);
+        for (int odd = 0; odd < 2; ++odd) {  // m-tiles 0, 2, 4, 6, then 1, 3, 5, 7
+          uint32_t a0[4], a1[4], a2[4], a3[4];
+          pairs(w0.x, w1.x, odd, g01, a0);
+          pairs(w0.y, w1.y, odd, g01, a1);
+          pairs(w2.x, w3.x, odd, g23, a2);
+          pairs(w2.y, w3.y, odd, g23, a3);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            Elem<__half>::mma(acc[2 * i + odd], a0[i], a1[i], a2[i], a3[i], pb0[h], pb1[h]);
+        }
       } else {
-        uint32_t a0[2][4], a2[2][4];
-        pairs(*reinterpret_cast<const uint32_t *>(Vs + c_0),
-              *reinterpret_cast<const uint32_t *>(Vs + c_1), a0[0], a0[1]);
-        pairs(*reinterpret_cast<const uint32_t *>(Vs + c_2),
-              *reinterpret_cast<const uint32_t *>(Vs + c_3), a2[0], a2[1]);
+        const uint32_t w0 = *reinterpret_cast<const uint32_t *>(Vs + c_0);
+        const uint32_t w1 = *reinterpret_cast<const uint32_t *>(Vs + c_1);
+        const uint32_t w2 = *reinterpret_cast<const uint32_t *>(Vs + c_2);
+        const uint32_t w3 = *reinterpret_cast<const uint32_t *>(Vs + c_3);
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-          Elem<__half>::mma(acc[mt], f16x2_mul(a0[mt & 1][mt >> 1], g01),
-                            f16x2_mul(a0[mt & 1][2 + (mt >> 1)], g01),
-                            f16x2_mul(a2[mt & 1][mt >> 1], g23),
-                            f16x2_mul(a2[mt & 1][2 + (mt >> 1)], g23), pb0[h], pb1[h]);
+        for (int odd = 0; odd < 2; ++odd) {  // m-tiles 0, 2, then 1, 3
+          uint32_t a0[4], a2[4];
+          pairs(w0, w1, odd, g01, a0);
+          pairs(w2, w3, odd, g23, a2);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            Elem<__half>::mma(acc[2 * i + odd], a0[i], a0[2 + i], a2[i], a2[2 + i], pb0[h],
+                              pb1[h]);
+        }
       }
+    }
+  };
+
+  bool timed_out = false;
+  int k = 0;
+#pragma unroll 1
+  for (; k < my_n; ++k) {
+    const int s = k % S;
+    if (!__all_sync(kFull, mbar_wait_bounded(&my_bars[s], (k / S) & 1))) {
+      if (lane == 0) atomicOr(a.err, kErrTimeout);
+      timed_out = true;
+      break;
+    }
+    const uint8_t *stage = my_stages + s * kStep;
+    const int step_tok = step_token(k);
+    if (!bad && step_tok >= t_begin && step_tok + 32 <= t_end) {
+      step(stage, false, 0xffffffffu);
+    } else {
+      const int tok = step_tok + lane;
+      bool in = tok >= t_begin && tok < t_end;
+      if (bad && in) {
+        const int phys = bt_row[tok / BS];
+        in = phys >= 0 && static_cast<int64_t>(phys) < a.num_blocks;
+      }
+      step(stage, true, __ballot_sync(kFull, in));
     }
 
     // ---- refill this stage with step k + S
