@@ -99,13 +99,6 @@ def _stream(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _torch_stream(stream):
-    if stream is None or isinstance(stream, torch.cuda.Stream):
-        return stream
-    handle = _stream(stream)
-    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
-
-
 def _check(call: str, status: int) -> None:
     if status != 0:
         raise PaError(call, status)
@@ -546,35 +539,81 @@ def fp4_block_size(cache: torch.Tensor, head_dim: int) -> int:
     return cache.shape[2] * 16 // (9 * head_dim)
 
 
-def _fp4_caches(k_cache, v_cache, head_dim) -> int:
-    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _cuda(n, t, torch.uint8)
-        if not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous")
+# The FP4 calls check their arguments in one pass and look nothing up twice: for
+# a decode step of a few short sequences the host's share of a call is longer
+# than the kernel (16 us a call with the checks of the calls above, 8 with these).
+_fp4_fns = {}
+_FP4_ARGS = {
+    "cache": "PPllPPPiiiiliffP",                  # write and read-back
+    "decode": "PPPPPiPiiiiilfffiiPziP",
+    "prefill": "PPPPPPiPiiiiiilfffiP",
+}
+_CT = {"P": ctypes.c_void_p, "i": ctypes.c_int32, "l": ctypes.c_int64, "f": ctypes.c_float,
+       "z": ctypes.c_size_t}
+
+
+def _fp4_fn(name: str, kind: str):
+    f = getattr(_load(), name)
+    f.argtypes, f.restype = [_CT[c] for c in _FP4_ARGS[kind]], ctypes.c_int32
+    _fp4_fns[name] = f
+    return f
+
+
+def _fits(name: str, t, dtype, dev: int) -> None:
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev
+            and t.is_contiguous()):
+        return
+    _cuda(name, t, dtype)
+    raise ValueError(f"{name} must be contiguous")
+
+
+# the current stream's handle without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _device_of(name: str, t) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev = torch.cuda.current_device()
+    if t.get_device() != dev:
+        _cuda(name, t)
+    return dev
+
+
+def _fp4_caches(k_cache, v_cache, head_dim: int, dev: int) -> int:
+    _fits("k_cache", k_cache, torch.uint8, dev)
+    _fits("v_cache", v_cache, torch.uint8, dev)
     if v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache shapes differ")
     return fp4_block_size(k_cache, head_dim)
 
 
 def _cache_fp4(name, key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, stream):
-    P, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
-    f = _blocks_fn(name, [P, P, i64, i64, P, P, P, i32, i32, i32, i32, i64, i32, f32, f32, P])
-    for n, t in (("key", key), ("value", value)):
-        _cuda(n, t, key.dtype)
-        if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
-            raise ValueError(f"{n} must be [T, Hkv, d] with heads contiguous inside a token row")
-    T, Hkv, d = key.shape
-    bs = _fp4_caches(k_cache, v_cache, d)
-    if value.shape != key.shape or k_cache.shape[1] != Hkv:
+    f = _fp4_fns.get(name) or _fp4_fn(name, "cache")
+    dev = _device_of("key", key)
+    shape, dtype = key.shape, key.dtype
+    if len(shape) != 3 or value.shape != shape:
+        raise ValueError("key and value must be [T, Hkv, d], alike")
+    T, Hkv, d = shape
+    if not value.is_cuda or value.get_device() != dev or value.dtype is not dtype:
+        _cuda("value", value, dtype)
+    ks, vs = key.stride(), value.stride()
+    if ks[2] != 1 or ks[1] != d or vs[2] != 1 or vs[1] != d:
+        raise ValueError("key, value: heads must be contiguous inside a token row")
+    bs = _fp4_caches(k_cache, v_cache, d, dev)
+    if k_cache.shape[1] != Hkv:
         raise ValueError("key/value/cache shapes disagree")
-    _cuda("slot_mapping", slot_mapping, torch.int64)
-    if slot_mapping.numel() != T or not slot_mapping.is_contiguous():
-        raise ValueError("slot_mapping must be contiguous, with one entry per token")
+    _fits("slot_mapping", slot_mapping, torch.int64, dev)
+    if slot_mapping.numel() != T:
+        raise ValueError("slot_mapping must have one entry per token")
     row = Hkv * d  # the stride of a single row is not looked at
-    _check(name, f(key.data_ptr(), value.data_ptr(), key.stride(0) if T > 1 else row,
-                   value.stride(0) if T > 1 else row, k_cache.data_ptr(), v_cache.data_ptr(),
-                   slot_mapping.data_ptr(), T, Hkv, d, bs, k_cache.shape[0], _dtype_code(key),
-                   float(k_scale), float(v_scale), _stream(stream)))
+    st = f(key.data_ptr(), value.data_ptr(), ks[0] if T > 1 else row, vs[0] if T > 1 else row,
+           k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T, Hkv, d, bs,
+           k_cache.shape[0], _dtype_code(key), float(k_scale), float(v_scale),
+           _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise PaError(name, st)
 
 
 def pa_reshape_and_cache_fp4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
@@ -603,41 +642,38 @@ def pa_decode_fp4(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor,
                   stream=None) -> torch.Tensor:
     """Paged decode attention over FP4 caches into ``out`` [B, Hq, d] (fp16 or
     bf16 queries and output).  ``workspace`` as for pa_decode."""
-    P, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
-    f = _blocks_fn("pa_decode_fp4", [P, P, P, P, P, i32, P, i32, i32, i32, i32, i32, i64, f32,
-                                     f32, f32, i32, i32, P, sz, i32, P])
-    for n, t in (("out", out), ("query", query)):
-        _cuda(n, t, query.dtype)
-        if not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous")
+    f = _fp4_fns.get("pa_decode_fp4") or _fp4_fn("pa_decode_fp4", "decode")
+    dev = _device_of("query", query)
+    _fits("query", query, query.dtype, dev)
+    _fits("out", out, query.dtype, dev)
     B, Hq, d = query.shape
-    bs = _fp4_caches(k_cache, v_cache, d)
-    for n, t in (("block_tables", block_tables), ("context_lens", context_lens)):
-        _cuda(n, t, torch.int32)
-        if not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous")
+    bs = _fp4_caches(k_cache, v_cache, d, dev)
+    _fits("block_tables", block_tables, torch.int32, dev)
+    _fits("context_lens", context_lens, torch.int32, dev)
     if out.shape != query.shape:
         raise ValueError("out and query shapes differ")
     if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.numel() != B:
         raise ValueError("block_tables must be [B, MB] and context_lens [B]")
-    need = pa_decode_workspace_size(B, Hq, d, max_context_len, partition_size)
     ws_ptr, ws_bytes = None, 0
-    if need:
+    if 0 < partition_size < max_context_len:
         if workspace is None:
             # made on the call's own stream: its zeros come before the kernels, and its
             # memory is not handed on before they are done
-            with torch.cuda.stream(_torch_stream(stream)):
-                workspace = torch.zeros(need, dtype=torch.uint8, device=query.device)
+            handle = _raw_stream(dev) if stream is None else _stream(stream)
+            on = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+            with torch.cuda.stream(on):
+                workspace = new_decode_workspace(B, Hq, d, max_context_len, partition_size, dev)
         _cuda("workspace", workspace)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check("pa_decode_fp4", f(
-        out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-        block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, Hq,
-        k_cache.shape[1], d, bs, k_cache.shape[0], float(scale), float(k_scale), float(v_scale),
-        int(max_context_len), int(partition_size), ws_ptr, ws_bytes, _dtype_code(query),
-        _stream(stream)))
+    st = f(out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+           block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, Hq,
+           k_cache.shape[1], d, bs, k_cache.shape[0], float(scale), float(k_scale), float(v_scale),
+           int(max_context_len), int(partition_size), ws_ptr, ws_bytes, _dtype_code(query),
+           _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise PaError("pa_decode_fp4", st)
     return out
 
 
@@ -646,31 +682,27 @@ def pa_prefill_fp4(out: torch.Tensor, query: torch.Tensor, query_start: torch.Te
                    context_lens: torch.Tensor, scale: float, k_scale: float, v_scale: float,
                    max_q_len: int, stream=None) -> torch.Tensor:
     """pa_prefill over FP4 caches, fp16 or bf16 queries and output."""
-    P, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
-    f = _blocks_fn("pa_prefill_fp4", [P, P, P, P, P, P, i32, P, i32, i32, i32, i32, i32, i32,
-                                      i64, f32, f32, f32, i32, P])
-    for n, t in (("out", out), ("query", query)):
-        _cuda(n, t, query.dtype)
-        if not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous")
+    f = _fp4_fns.get("pa_prefill_fp4") or _fp4_fn("pa_prefill_fp4", "prefill")
+    dev = _device_of("query", query)
+    _fits("query", query, query.dtype, dev)
+    _fits("out", out, query.dtype, dev)
     total_q, Hq, d = query.shape
-    bs = _fp4_caches(k_cache, v_cache, d)
-    for n, t in (("query_start", query_start), ("block_tables", block_tables),
-                 ("context_lens", context_lens)):
-        _cuda(n, t, torch.int32)
-        if not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous")
+    bs = _fp4_caches(k_cache, v_cache, d, dev)
+    _fits("query_start", query_start, torch.int32, dev)
+    _fits("block_tables", block_tables, torch.int32, dev)
+    _fits("context_lens", context_lens, torch.int32, dev)
     B = context_lens.numel()
     if query_start.numel() != B + 1 or out.shape != query.shape:
         raise ValueError("query_start must have num_seqs + 1 entries; out must match query")
     if block_tables.dim() != 2 or block_tables.shape[0] != B:
         raise ValueError("block_tables must be [B, MB]")
-    _check("pa_prefill_fp4", f(
-        out.data_ptr(), query.data_ptr(), query_start.data_ptr(), k_cache.data_ptr(),
-        v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
-        context_lens.data_ptr(), B, int(max_q_len), Hq, k_cache.shape[1], d, bs,
-        k_cache.shape[0], float(scale), float(k_scale), float(v_scale), _dtype_code(query),
-        _stream(stream)))
+    st = f(out.data_ptr(), query.data_ptr(), query_start.data_ptr(), k_cache.data_ptr(),
+           v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+           context_lens.data_ptr(), B, int(max_q_len), Hq, k_cache.shape[1], d, bs,
+           k_cache.shape[0], float(scale), float(k_scale), float(v_scale), _dtype_code(query),
+           _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise PaError("pa_prefill_fp4", st)
     return out
 
 
