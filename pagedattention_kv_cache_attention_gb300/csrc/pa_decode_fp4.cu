@@ -55,6 +55,12 @@ namespace {
 #ifndef PA_DECODE_FP4_CTAS
 #define PA_DECODE_FP4_CTAS 4
 #endif
+#ifndef PA_CHUNK_FP4_WARPS
+#define PA_CHUNK_FP4_WARPS 8
+#endif
+#ifndef PA_CHUNK_FP4_STAGES
+#define PA_CHUNK_FP4_STAGES 3
+#endif
 
 // P is held times 2^11, against a reference that is at most 2^4 below the
 // running maximum: below 2^15 then, and in fp16's normal range down to 2^-25 of
@@ -100,14 +106,24 @@ template <int D> __device__ __forceinline__ int code_at(int r, int b) {
   return at ^ (((at >> 7) & (D == 128 ? 7 : 3)) << 4);
 }
 
-// T: query and output type.  NW warps, S stages each.  WP: each warp takes a
-// whole partition and writes its partial itself (partitions joined by the
-// reduce kernel), as in the 16-bit kernel.
-template <typename T, int D, int BS, int NW, int S, bool WP>
-__global__ void __launch_bounds__(NW * 32, PA_DECODE_FP4_CTAS)
+enum class Rows { kDecode, kDecodeWarps, kChunk };
+
+// T: query and output type.  NW warps, S stages each.  What the 8 NT columns of
+// the products are:
+//  kDecode       the heads of one query (NT = 1); the warps share a partition
+//  kDecodeWarps  the same, but each warp takes a whole partition and writes its
+//                partial itself (partitions joined by the reduce kernel), as in
+//                the 16-bit kernel
+//  kChunk        rows of a short chunk, (token, head) pairs with token = row /
+//                G, the CTA's from row 8 NT blockIdx.x on; the warps share the
+//                keys up to its last row's
+template <typename T, int D, int BS, int NW, int S, Rows ROWS, int NT>
+__global__ void __launch_bounds__(NW * 32, ROWS == Rows::kChunk ? 1 : PA_DECODE_FP4_CTAS)
     pa_decode_fp4_kernel(const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap, const DecodeArgs a) {
   using Sh = Fp4Shape<D, BS>;
+  constexpr bool WP = ROWS == Rows::kDecodeWarps, kChunk = ROWS == Rows::kChunk;
+  static_assert(kChunk || NT == 1, "a decode query's heads are one tile of columns");
   constexpr int kStep = 2 * Sh::kUnit;  // K then V of a 32-token step
   constexpr int kTiles = Sh::kTiles;
   extern __shared__ uint8_t smem_raw[];
@@ -117,7 +133,7 @@ __global__ void __launch_bounds__(NW * 32, PA_DECODE_FP4_CTAS)
 
   const int kvh = blockIdx.y, seq = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int part = WP ? blockIdx.x * NW + warp : blockIdx.x;
+  const int part = WP ? blockIdx.x * NW + warp : kChunk ? 0 : blockIdx.x;
   if (WP && part >= a.num_parts) return;  // the last CTA's spare warps
   const int g = lane >> 2, c = lane & 3;
   uint8_t *my_stages = smem + warp * S * kStep;
@@ -144,14 +160,28 @@ __global__ void __launch_bounds__(NW * 32, PA_DECODE_FP4_CTAS)
   };
   int win = table_entry(lane);  // read before the length arrives; entries past it are not used
 
+  const int G = a.group;
   int ctx = a.context_lens[seq];
-  if (ctx < 0 || ctx > a.max_blocks_per_seq * BS || ctx > a.max_context_len) {
+  int q0 = seq, row0 = 0, n_rows = G, base_pos = 0;  // the chunk's first row and rows, its position
+  if constexpr (kChunk) {
+    q0 = a.query_start[seq];
+    const int q_len = a.query_start[seq + 1] - q0;
+    row0 = 8 * NT * blockIdx.x;
+    n_rows = q_len * G;
+    base_pos = ctx - q_len;
+    if (q_len < 0 || ctx < q_len || ctx > a.max_blocks_per_seq * BS || q_len > a.max_q_len) {
+      if (threadIdx.x == 0 && row0 == 0 && kvh == 0) atomicOr(a.err, kErrBadLen);
+      return;
+    }
+    if (row0 >= n_rows) return;
+    ctx = base_pos + (min(n_rows, row0 + 8 * NT) - 1) / G + 1;  // keys of the CTA's last row
+  } else if (ctx < 0 || ctx > a.max_blocks_per_seq * BS || ctx > a.max_context_len) {
     if (threadIdx.x == 0 && part == 0 && kvh == 0) atomicOr(a.err, kErrBadLen);
     ctx = 0;
   }
   if (part > 0 && t_begin >= ctx) return;
-  const int np_seq = ctx > 0 ? (ctx + a.part_tokens - 1) / a.part_tokens : 1;
-  const int t_end = min(ctx, t_begin + a.part_tokens);
+  const int np_seq = !kChunk && ctx > 0 ? (ctx + a.part_tokens - 1) / a.part_tokens : 1;
+  const int t_end = kChunk ? ctx : min(ctx, t_begin + a.part_tokens);
   const int n_step = t_end > base ? (t_end - base + 31) / 32 : 0;
   const int my_n = WP ? n_step : (n_step > warp ? (n_step - warp + NW - 1) / NW : 0);
 
@@ -195,28 +225,32 @@ __global__ void __launch_bounds__(NW * 32, PA_DECODE_FP4_CTAS)
   for (int s = 0; s < S; ++s)
     if (s < my_n) fill(s, s);
 
-  // query fragments of head g, in the order of the K bytes a lane reads
-  const int G = a.group;
-  uint4 qf[Sh::kQChunks];
-  float sl0 = a.scale_log2, sl1 = a.scale_log2;  // of the lane's columns 2c and 2c + 1
-  {
+  // query fragments of column g of every tile, in the order of the K bytes a lane reads
+  uint4 qf[NT][Sh::kQChunks];
+  float sl[NT][2];  // softmax scale of the lane's columns 2c and 2c + 1
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int col = row0 + 8 * nt + g;
     const T *qrow = static_cast<const T *>(a.query) +
-                    (static_cast<int64_t>(seq) * a.num_q_heads + kvh * G + g) * D;
+                    (static_cast<int64_t>(q0 + (kChunk ? col / G : 0)) * a.num_q_heads + kvh * G +
+                     (kChunk ? col % G : col)) * D;
 #pragma unroll
     for (int i = 0; i < Sh::kQChunks; ++i)
-      qf[i] = g < G ? *reinterpret_cast<const uint4 *>(qrow + (c * Sh::kQChunks + i) * 8)
-                    : make_uint4(0, 0, 0, 0);
+      qf[nt][i] = col < n_rows
+                      ? *reinterpret_cast<const uint4 *>(qrow + (c * Sh::kQChunks + i) * 8)
+                      : make_uint4(0, 0, 0, 0);
+    sl[nt][0] = sl[nt][1] = a.scale_log2;
     if constexpr (!std::is_same<T, __half>::value) {
-      // bf16 queries: each head is scaled by 2^e so that its largest magnitude
+      // bf16 queries: each row is scaled by 2^e so that its largest magnitude
       // lies in [2^14, 2^15), then rounded to fp16 (exact for every value down
       // to 2^-31 of the largest: bf16 carries 8 bits, and fp16 holds 8 bits at
-      // every magnitude from 2^-17 up); 2^-e joins the head's softmax scale
+      // every magnitude from 2^-17 up); 2^-e joins the row's softmax scale
       float mx = 0.f;
 #pragma unroll
       for (int i = 0; i < Sh::kQChunks; ++i)
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const float2 v = Elem<T>::unpack(word_of(qf[i], w));
+          const float2 v = Elem<T>::unpack(word_of(qf[nt][i], w));
           mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
         }
       mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
@@ -228,13 +262,13 @@ __global__ void __launch_bounds__(NW * 32, PA_DECODE_FP4_CTAS)
         uint32_t w4[4];
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const float2 v = Elem<T>::unpack(word_of(qf[i], w));
+          const float2 v = Elem<T>::unpack(word_of(qf[nt][i], w));
           w4[w] = Elem<__half>::pack(v.x * f, v.y * f);
         }
-        qf[i] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+        qf[nt][i] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
       }
-      sl0 = ldexpf(sl0, -__shfl_sync(kFull, e, 8 * c));      // a lane of head 2c
-      sl1 = ldexpf(sl1, -__shfl_sync(kFull, e, 8 * c + 4));  // of head 2c + 1
+      sl[nt][0] = ldexpf(sl[nt][0], -__shfl_sync(kFull, e, 8 * c));      // a lane of column 2c
+      sl[nt][1] = ldexpf(sl[nt][1], -__shfl_sync(kFull, e, 8 * c + 4));  // of column 2c + 1
     }
   }
 
@@ -253,26 +287,34 @@ __global__ void __launch_bounds__(NW * 32, PA_DECODE_FP4_CTAS)
   const int vs_1 = t1 * Sh::kScales + (D == 128 ? g : g >> 1);
 
   const float NEG_INF = -INFINITY;
-  // online softmax of the lane's heads 2c and 2c + 1 in base 2: c0 = kPShift -
-  // the reference of head 2c, so that probabilities are held as 2^(x + c0);
+  // online softmax of the lane's columns 2c and 2c + 1 in base 2: c0 = kPShift -
+  // the reference of the first, so that probabilities are held as 2^(x + c0);
   // before the first token the reference is far below any score
-  float c0 = 1e30f, c1 = 1e30f, l0 = 0.f, l1 = 0.f;
-  float acc[Sh::kMTiles][4];
+  float cr[NT][2], l[NT][2], acc[NT][Sh::kMTiles][4];
 #pragma unroll
-  for (int mt = 0; mt < Sh::kMTiles; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
+  for (int nt = 0; nt < NT; ++nt) {
+    cr[nt][0] = cr[nt][1] = 1e30f;
+    l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < Sh::kMTiles; ++mt)
+      acc[nt][mt][0] = acc[nt][mt][1] = acc[nt][mt][2] = acc[nt][mt][3] = 0.f;
+  }
 
   // One step, its K and V at `stage`.  masked: only the tokens that `mask` has
-  // count (bit i: token i of the step); the code of whole steps is apart, as
-  // the selects cost a seventh of a step's instructions.
-  auto step = [&](const uint8_t *stage, bool masked, uint32_t mask) {
+  // count (bit i: token i of the step), and in a chunk only those up to a
+  // row's own, which is token `own` + row / G; the code of whole steps is
+  // apart, as the selects cost a seventh of a step's instructions.
+  auto step = [&](const uint8_t *stage, bool masked, uint32_t mask, int own) {
     // ---- S^T = K Q^T
-    float x[2][4];
+    float x[NT][2][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint8_t *Ks = stage + Sh::codes(h);
       const uint8_t *sc = stage + Sh::scales(h);
       // two chains of products, so that half of them wait for one another
-      float y[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      // (several tiles of columns are chains enough)
+      constexpr int kChains = NT == 1 ? 2 : 1;
+      float y[NT][kChains][4] = {};
       const int ca = k_a ^ Sh::flip_codes(h), cb = k_b ^ Sh::flip_codes(h);
       const int sa = ks_a ^ Sh::flip_scales(h), sb = ks_b ^ Sh::flip_scales(h);
       uint32_t pa, pb;  // the scales of rows a and b as fp16 pairs
@@ -299,78 +341,96 @@ __global__ void __launch_bounds__(NW * 32, PA_DECODE_FP4_CTAS)
         uint32_t ha[4], hb[4];
         e2m1x8_to_half(wa[w], ha);
         e2m1x8_to_half(wb[w], hb);
-        Elem<__half>::mma(y[0], f16x2_mul(ha[0], ga), f16x2_mul(hb[0], gb), f16x2_mul(ha[1], ga),
-                          f16x2_mul(hb[1], gb), qf[w].x, qf[w].y);
-        Elem<__half>::mma(y[1], f16x2_mul(ha[2], ga), f16x2_mul(hb[2], gb), f16x2_mul(ha[3], ga),
-                          f16x2_mul(hb[3], gb), qf[w].z, qf[w].w);
-      }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[h][e] = y[0][e] + y[1][e];
-    }
-
-    // z = scores + (b0, b1); tokens that do not count get -inf
-    auto logits = [&](float (&z)[2][4], float b0, float b1) {
+        for (int i = 0; i < 4; ++i) {
+          ha[i] = f16x2_mul(ha[i], ga);
+          hb[i] = f16x2_mul(hb[i], gb);
+        }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        z[h][0] = fmaf(x[h][0], sl0, b0);
-        z[h][1] = fmaf(x[h][1], sl1, b1);
-        z[h][2] = fmaf(x[h][2], sl0, b0);
-        z[h][3] = fmaf(x[h][3], sl1, b1);
-        if (masked) {
-          const bool va = (mask >> (16 * h + kr)) & 1u, vz = (mask >> (16 * h + kr + 8)) & 1u;
-          z[h][0] = va ? z[h][0] : NEG_INF;
-          z[h][1] = va ? z[h][1] : NEG_INF;
-          z[h][2] = vz ? z[h][2] : NEG_INF;
-          z[h][3] = vz ? z[h][3] : NEG_INF;
+        for (int nt = 0; nt < NT; ++nt) {
+          Elem<__half>::mma(y[nt][0], ha[0], hb[0], ha[1], hb[1], qf[nt][w].x, qf[nt][w].y);
+          Elem<__half>::mma(y[nt][kChains - 1], ha[2], hb[2], ha[3], hb[3], qf[nt][w].z,
+                            qf[nt][w].w);
         }
       }
-    };
-    // 2^y are the probabilities; the reference moves only when one of them
-    // passes 2^(kPShift + kGrowth), so most steps need a vote and no shuffles
-    float y[2][4];
-    logits(y, c0, c1);
-    float top = NEG_INF;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      top = fmaxf(top, fmaxf(fmaxf(y[h][0], y[h][1]), fmaxf(y[h][2], y[h][3])));
-    if (__any_sync(kFull, top > kPShift + kGrowth)) {
-      logits(y, 0.f, 0.f);
-      float mx0 = kPShift - c0, mx1 = kPShift - c1;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[nt][h][e] = kChains == 2 ? y[nt][0][e] + y[nt][kChains - 1][e] : y[nt][0][e];
+    }
+
+    uint32_t pb0[NT][2], pb1[NT][2];  // P^T as the B operand
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      // a row's own token (of columns 2c and 2c + 1) within the step
+      const int col = row0 + 8 * nt + 2 * c;
+      const int own0 = kChunk && masked ? own + col / G : 0;
+      const int own1 = kChunk && masked ? own + (col + 1) / G : 0;
+      // z = scores + (b0, b1); tokens that do not count get -inf
+      auto logits = [&](float (&z)[2][4], float b0, float b1) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          z[h][0] = fmaf(x[nt][h][0], sl[nt][0], b0);
+          z[h][1] = fmaf(x[nt][h][1], sl[nt][1], b1);
+          z[h][2] = fmaf(x[nt][h][2], sl[nt][0], b0);
+          z[h][3] = fmaf(x[nt][h][3], sl[nt][1], b1);
+          if (masked) {
+            const int ta = 16 * h + kr, tb = ta + 8;
+            const bool va = (mask >> ta) & 1u, vb = (mask >> tb) & 1u;
+            z[h][0] = va && (!kChunk || ta <= own0) ? z[h][0] : NEG_INF;
+            z[h][1] = va && (!kChunk || ta <= own1) ? z[h][1] : NEG_INF;
+            z[h][2] = vb && (!kChunk || tb <= own0) ? z[h][2] : NEG_INF;
+            z[h][3] = vb && (!kChunk || tb <= own1) ? z[h][3] : NEG_INF;
+          }
+        }
+      };
+      // 2^y are the probabilities; the reference moves only when one of them
+      // passes 2^(kPShift + kGrowth), so most steps need a vote and no shuffles
+      float y[2][4];
+      logits(y, cr[nt][0], cr[nt][1]);
+      float top = NEG_INF;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        top = fmaxf(top, fmaxf(fmaxf(y[h][0], y[h][1]), fmaxf(y[h][2], y[h][3])));
+      if (__any_sync(kFull, top > kPShift + kGrowth)) {
+        logits(y, 0.f, 0.f);
+        float mx0 = kPShift - cr[nt][0], mx1 = kPShift - cr[nt][1];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          mx0 = fmaxf(mx0, fmaxf(y[h][0], y[h][2]));
+          mx1 = fmaxf(mx1, fmaxf(y[h][1], y[h][3]));
+        }
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, off));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, off));
+        }
+        const float n0 = kPShift - mx0, n1 = kPShift - mx1;
+        const float al0 = ex2_approx(n0 - cr[nt][0]), al1 = ex2_approx(n1 - cr[nt][1]);
+        cr[nt][0] = n0;
+        cr[nt][1] = n1;
+        l[nt][0] *= al0;
+        l[nt][1] *= al1;
+#pragma unroll
+        for (int mt = 0; mt < Sh::kMTiles; ++mt) {
+          acc[nt][mt][0] *= al0;
+          acc[nt][mt][1] *= al1;
+          acc[nt][mt][2] *= al0;
+          acc[nt][mt][3] *= al1;
+        }
+        logits(y, cr[nt][0], cr[nt][1]);
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        mx0 = fmaxf(mx0, fmaxf(y[h][0], y[h][2]));
-        mx1 = fmaxf(mx1, fmaxf(y[h][1], y[h][3]));
+        const float p0 = ex2_approx(y[h][0]), p1 = ex2_approx(y[h][1]);
+        const float p2 = ex2_approx(y[h][2]), p3 = ex2_approx(y[h][3]);
+        l[nt][0] += p0 + p2;
+        l[nt][1] += p1 + p3;
+        // an 8x8 transpose of the accumulator's layout
+        pb0[nt][h] = movmatrix_trans(Elem<__half>::pack(p0, p1));
+        pb1[nt][h] = movmatrix_trans(Elem<__half>::pack(p2, p3));
       }
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, off));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, off));
-      }
-      const float n0 = kPShift - mx0, n1 = kPShift - mx1;
-      const float al0 = ex2_approx(n0 - c0), al1 = ex2_approx(n1 - c1);
-      c0 = n0;
-      c1 = n1;
-      l0 *= al0;
-      l1 *= al1;
-#pragma unroll
-      for (int mt = 0; mt < Sh::kMTiles; ++mt) {
-        acc[mt][0] *= al0;
-        acc[mt][1] *= al1;
-        acc[mt][2] *= al0;
-        acc[mt][3] *= al1;
-      }
-      logits(y, c0, c1);
-    }
-    uint32_t pb0[2], pb1[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float p0 = ex2_approx(y[h][0]), p1 = ex2_approx(y[h][1]);
-      const float p2 = ex2_approx(y[h][2]), p3 = ex2_approx(y[h][3]);
-      l0 += p0 + p2;
-      l1 += p1 + p3;
-      // P^T as the B operand: an 8x8 transpose of the accumulator's layout
-      pb0[h] = movmatrix_trans(Elem<__half>::pack(p0, p1));
-      pb1[h] = movmatrix_trans(Elem<__half>::pack(p2, p3));
     }
 
     // ---- O^T += V^T P^T
@@ -413,7 +473,10 @@ __global__ void __launch_bounds__(NW * 32, PA_DECODE_FP4_CTAS)
           pairs(w2.y, w3.y, odd, g23, a3);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            Elem<__half>::mma(acc[2 * i + odd], a0[i], a1[i], a2[i], a3[i], pb0[h], pb1[h]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              Elem<__half>::mma(acc[nt][2 * i + odd], a0[i], a1[i], a2[i], a3[i], pb0[nt][h],
+                                pb1[nt][h]);
         }
       } else {
         const uint32_t w0 = *reinterpret_cast<const uint32_t *>(Vs + c_0);
@@ -427,8 +490,10 @@ __global__ void __launch_bounds__(NW * 32, PA_DECODE_FP4_CTAS)
           pairs(w2, w3, odd, g23, a2);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            Elem<__half>::mma(acc[2 * i + odd], a0[i], a0[2 + i], a2[i], a2[2 + i], pb0[h],
-                              pb1[h]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              Elem<__half>::mma(acc[nt][2 * i + odd], a0[i], a0[2 + i], a2[i], a2[2 + i],
+                                pb0[nt][h], pb1[nt][h]);
         }
       }
     }
@@ -446,8 +511,10 @@ __global__ void __launch_bounds__(NW * 32, PA_DECODE_FP4_CTAS)
     }
     const uint8_t *stage = my_stages + s * kStep;
     const int step_tok = step_token(k);
-    if (!bad && step_tok >= t_begin && step_tok + 32 <= t_end) {
-      step(stage, false, 0xffffffffu);
+    // (in a chunk every row sees the step's last token if its first row does)
+    if (!bad && step_tok >= t_begin &&
+        step_tok + 32 <= (kChunk ? base_pos + row0 / G + 1 : t_end)) {
+      step(stage, false, 0xffffffffu, 0);
     } else {
       const int tok = step_tok + lane;
       bool in = tok >= t_begin && tok < t_end;
@@ -455,7 +522,7 @@ __global__ void __launch_bounds__(NW * 32, PA_DECODE_FP4_CTAS)
         const int phys = bt_row[tok / BS];
         in = phys >= 0 && static_cast<int64_t>(phys) < a.num_blocks;
       }
-      step(stage, true, __ballot_sync(kFull, in));
+      step(stage, true, __ballot_sync(kFull, in), base_pos - step_tok);
     }
 
     // ---- refill this stage with step k + S
@@ -470,120 +537,150 @@ __global__ void __launch_bounds__(NW * 32, PA_DECODE_FP4_CTAS)
   // row sums over the 8 token rows; l and acc are both held times 2^kPShift
   const float unshift = exp2f(-kPShift);
 #pragma unroll
-  for (int off = 4; off < 32; off <<= 1) {
-    l0 += __shfl_xor_sync(kFull, l0, off);
-    l1 += __shfl_xor_sync(kFull, l1, off);
-  }
-  l0 *= unshift;
-  l1 *= unshift;
-  const float m0 = kPShift - c0, m1 = kPShift - c1;  // the references
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1)
+        l[nt][e] += __shfl_xor_sync(kFull, l[nt][e], off);
+      l[nt][e] *= unshift;
+      cr[nt][e] = kPShift - cr[nt][e];  // from here on the reference itself
+    }
 
   if constexpr (WP) {
-    const int64_t row0 = static_cast<int64_t>(seq) * a.num_q_heads + kvh * G;
+    const int64_t first = static_cast<int64_t>(seq) * a.num_q_heads + kvh * G;
     const int h0 = 2 * c, h1 = 2 * c + 1;
-    const float inv0 = l0 > 0.f ? a.out_scale * unshift / l0 : 0.f;
-    const float inv1 = l1 > 0.f ? a.out_scale * unshift / l1 : 0.f;
-    const int64_t pr0 = (row0 + h0) * a.num_parts + part, pr1 = (row0 + h1) * a.num_parts + part;
+    const float inv0 = l[0][0] > 0.f ? a.out_scale * unshift / l[0][0] : 0.f;
+    const float inv1 = l[0][1] > 0.f ? a.out_scale * unshift / l[0][1] : 0.f;
+    const int64_t pr0 = (first + h0) * a.num_parts + part, pr1 = (first + h1) * a.num_parts + part;
     if (g == 0) {
       if (h0 < G) {
-        a.ws_m[pr0] = m0;
-        a.ws_l[pr0] = l0;
+        a.ws_m[pr0] = cr[0][0];
+        a.ws_l[pr0] = l[0][0];
       }
       if (h1 < G) {
-        a.ws_m[pr1] = m1;
-        a.ws_l[pr1] = l1;
+        a.ws_m[pr1] = cr[0][1];
+        a.ws_l[pr1] = l[0][1];
       }
     }
-    store_partial_o<D, true>(a.ws_o + pr0 * D, a.ws_o + pr1 * D, h0 < G, h1 < G, acc, inv0, inv1,
-                             g);
+    store_partial_o<D, true>(a.ws_o + pr0 * D, a.ws_o + pr1 * D, h0 < G, h1 < G, acc[0], inv0,
+                             inv1, g);
     grid_launch_dependents();
     return;
   }
 
-  // ---- merge warps through shared memory (stages are idle now)
-  __syncthreads();
+  // ---- merge warps through shared memory (stages are idle now), a tile of
+  // columns at a time
   float *wacc = reinterpret_cast<float *>(smem);  // [NW][8][D]
   float *wml = wacc + NW * 8 * D;                 // [NW][8][2]
-  if (g == 0) {
-    wml[(warp * 8 + 2 * c) * 2 + 0] = m0;
-    wml[(warp * 8 + 2 * c) * 2 + 1] = l0;
-    wml[(warp * 8 + 2 * c + 1) * 2 + 0] = m1;
-    wml[(warp * 8 + 2 * c + 1) * 2 + 1] = l1;
-  }
-  {
-    float *h0 = wacc + (warp * 8 + 2 * c) * D;
-    store_partial_o<D, true>(h0, h0 + D, true, true, acc, unshift, unshift, g);
-  }
-  __syncthreads();
-  constexpr int kChunks = D / 8;
-  for (int item = threadIdx.x; item < G * kChunks; item += NW * 32) {
-    const int h = item / kChunks, ch = item % kChunks;
-    float M = NEG_INF;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) M = fmaxf(M, wml[(w * 8 + h) * 2]);
-    float L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const float mw = wml[(w * 8 + h) * 2];
-      const float f = mw == NEG_INF ? 0.f : exp2f(mw - M);
-      L += wml[(w * 8 + h) * 2 + 1] * f;
-      const float *src = wacc + (w * 8 + h) * D + ch * 8;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] += src[e] * f;
+  for (int nt = 0; nt < NT; ++nt) {
+    __syncthreads();
+    if (g == 0) {
+      wml[(warp * 8 + 2 * c) * 2 + 0] = cr[nt][0];
+      wml[(warp * 8 + 2 * c) * 2 + 1] = l[nt][0];
+      wml[(warp * 8 + 2 * c + 1) * 2 + 0] = cr[nt][1];
+      wml[(warp * 8 + 2 * c + 1) * 2 + 1] = l[nt][1];
     }
-    const int64_t row = static_cast<int64_t>(seq) * a.num_q_heads + kvh * G + h;
-    const float inv = L > 0.f ? a.out_scale / L : 0.f;
+    float *mine = wacc + (warp * 8 + 2 * c) * D;
+    store_partial_o<D, true>(mine, mine + D, true, true, acc[nt], unshift, unshift, g);
+    __syncthreads();
+    constexpr int kChunks = D / 8;
+    const int cols = min(8, n_rows - row0 - 8 * nt);
+    for (int item = threadIdx.x; item < cols * kChunks; item += NW * 32) {
+      const int h = item / kChunks, ch = item % kChunks;
+      float M = NEG_INF;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] *= inv;
-    if (a.num_parts == 1 || (a.fuse_join && np_seq == 1)) {
-      *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row * D + ch * 8) =
-          make_uint4(Elem<T>::pack(o[0], o[1]), Elem<T>::pack(o[2], o[3]),
-                     Elem<T>::pack(o[4], o[5]), Elem<T>::pack(o[6], o[7]));
-    } else {
-      const int64_t pr = row * a.num_parts + part;
-      float4 *dst = reinterpret_cast<float4 *>(a.ws_o + pr * D + ch * 8);
-      dst[0] = make_float4(o[0], o[1], o[2], o[3]);
-      dst[1] = make_float4(o[4], o[5], o[6], o[7]);
-      if (ch == 0) {
-        a.ws_m[pr] = M;
-        a.ws_l[pr] = L;
+      for (int w = 0; w < NW; ++w) M = fmaxf(M, wml[(w * 8 + h) * 2]);
+      float L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float f = exp2f(wml[(w * 8 + h) * 2] - M);
+        L += wml[(w * 8 + h) * 2 + 1] * f;
+        const float *src = wacc + (w * 8 + h) * D + ch * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] += src[e] * f;
+      }
+      const int col = row0 + 8 * nt + h;
+      const int64_t row = static_cast<int64_t>(q0 + (kChunk ? col / G : 0)) * a.num_q_heads +
+                          kvh * G + (kChunk ? col % G : col);
+      const float inv = L > 0.f ? a.out_scale / L : 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] *= inv;
+      if (kChunk || a.num_parts == 1 || (a.fuse_join && np_seq == 1)) {
+        *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row * D + ch * 8) =
+            make_uint4(Elem<T>::pack(o[0], o[1]), Elem<T>::pack(o[2], o[3]),
+                       Elem<T>::pack(o[4], o[5]), Elem<T>::pack(o[6], o[7]));
+      } else {
+        const int64_t pr = row * a.num_parts + part;
+        float4 *dst = reinterpret_cast<float4 *>(a.ws_o + pr * D + ch * 8);
+        dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+        if (ch == 0) {
+          a.ws_m[pr] = M;
+          a.ws_l[pr] = L;
+        }
       }
     }
   }
-  if (a.fuse_join && np_seq > 1) {
+  if (!kChunk && a.fuse_join && np_seq > 1) {
     if (last_to_arrive(a, seq, kvh, np_seq, reinterpret_cast<uint32_t *>(wml + NW * 8 * 2)))
       join_partitions<T, D, NW>(a, seq, kvh, np_seq);
   }
   grid_launch_dependents();
 }
 
-template <typename T, int D, int BS, bool WP>
-cudaError_t launch_w(const DecodeArgs &a, const CUtensorMap &km, const CUtensorMap &vm,
-                     cudaStream_t stream) {
-  constexpr int NW = PA_DECODE_FP4_WARPS, S = PA_DECODE_FP4_STAGES;
+template <typename T, int D, int BS, int NW, int S, Rows ROWS, int NT>
+cudaError_t launch_rows(const DecodeArgs &a, const CUtensorMap &km, const CUtensorMap &vm,
+                        unsigned grid_x, cudaStream_t stream) {
   constexpr size_t stages = static_cast<size_t>(NW) * S * 2 * Fp4Shape<D, BS>::kUnit;
   constexpr size_t smem = 1024 + stages + NW * S * 8;
   static_assert(static_cast<size_t>(NW) * 8 * D * 4 + NW * 8 * 2 * 4 + 16 <= stages,
                 "merge buffers and the join flag must fit in the stage area");
-  auto kern = pa_decode_fp4_kernel<T, D, BS, NW, S, WP>;
+  static_assert(smem <= 227 * 1024, "shared memory");
+  auto kern = pa_decode_fp4_kernel<T, D, BS, NW, S, ROWS, NT>;
   static SmemLimitOnce smem_limit;
   const cudaError_t e = smem_limit.ensure(kern, smem);
   if (e != cudaSuccess) return e;
-  const unsigned gx = WP ? static_cast<unsigned>((a.num_parts + NW - 1) / NW)
-                         : static_cast<unsigned>(a.num_parts);
-  return launch_dependent(kern, dim3(gx, a.num_kv_heads, a.num_seqs), dim3(NW * 32), smem, stream,
-                          km, vm, a);
+  return launch_dependent(kern, dim3(grid_x, a.num_kv_heads, a.num_seqs), dim3(NW * 32), smem,
+                          stream, km, vm, a);
 }
 
-template <typename T, int D>
-cudaError_t launch_t(const DecodeArgs &a, const CUtensorMap &km, const CUtensorMap &vm,
-                     cudaStream_t stream) {
-  const bool wp = a.num_parts > 1 && !a.fuse_join;
-  if (a.bs_log2 == 4)
-    return wp ? launch_w<T, D, 16, true>(a, km, vm, stream)
-              : launch_w<T, D, 16, false>(a, km, vm, stream);
-  return wp ? launch_w<T, D, 32, true>(a, km, vm, stream)
-            : launch_w<T, D, 32, false>(a, km, vm, stream);
+template <typename T, int D, int BS>
+cudaError_t launch_decode_t(const DecodeArgs &a, const CUtensorMap &km, const CUtensorMap &vm,
+                            cudaStream_t stream) {
+  constexpr int NW = PA_DECODE_FP4_WARPS, S = PA_DECODE_FP4_STAGES;
+  if (a.num_parts > 1 && !a.fuse_join)
+    return launch_rows<T, D, BS, NW, S, Rows::kDecodeWarps, 1>(a, km, vm,
+                                                               (a.num_parts + NW - 1) / NW, stream);
+  return launch_rows<T, D, BS, NW, S, Rows::kDecode, 1>(a, km, vm, a.num_parts, stream);
+}
+
+template <typename T, int D, int BS>
+cudaError_t launch_chunk_t(const DecodeArgs &a, const CUtensorMap &km, const CUtensorMap &vm,
+                           cudaStream_t stream) {
+  constexpr int NW = PA_CHUNK_FP4_WARPS, S = PA_CHUNK_FP4_STAGES;
+  const int rows = a.max_q_len * a.group;
+  if (rows <= 8) return launch_rows<T, D, BS, NW, S, Rows::kChunk, 1>(a, km, vm, 1, stream);
+  if (rows <= 16) return launch_rows<T, D, BS, NW, S, Rows::kChunk, 2>(a, km, vm, 1, stream);
+  return launch_rows<T, D, BS, NW, S, Rows::kChunk, 3>(a, km, vm, (rows + 23) / 24, stream);
+}
+
+// f(head_dim, block_size) with both as compile-time constants
+template <typename F> cudaError_t by_shape(int head_dim, int bs_log2, F &&f) {
+  using D128 = std::integral_constant<int, 128>;
+  using D64 = std::integral_constant<int, 64>;
+  using B16 = std::integral_constant<int, 16>;
+  using B32 = std::integral_constant<int, 32>;
+  if (head_dim == 128) return bs_log2 == 4 ? f(D128{}, B16{}) : f(D128{}, B32{});
+  return bs_log2 == 4 ? f(D64{}, B16{}) : f(D64{}, B32{});
+}
+
+bool encode_maps(CUtensorMap *km, CUtensorMap *vm, const DecodeArgs &a, const void *k_cache,
+                 const void *v_cache, int head_dim) {
+  const int64_t tiles = a.num_blocks * a.num_kv_heads;
+  return encode_fp4_map(km, k_cache, tiles, 1 << a.bs_log2, head_dim, true) &&
+         encode_fp4_map(vm, v_cache, tiles, 1 << a.bs_log2, head_dim, true);
 }
 
 }  // namespace
@@ -591,15 +688,23 @@ cudaError_t launch_t(const DecodeArgs &a, const CUtensorMap &km, const CUtensorM
 cudaError_t launch_decode_fp4(const DecodeArgs &a, const void *k_cache, const void *v_cache,
                               int head_dim, int dtype, cudaStream_t stream, bool *map_failed) {
   CUtensorMap km, vm;
-  const int64_t tiles = a.num_blocks * a.num_kv_heads;
-  *map_failed = !encode_fp4_map(&km, k_cache, tiles, 1 << a.bs_log2, head_dim, true) ||
-                !encode_fp4_map(&vm, v_cache, tiles, 1 << a.bs_log2, head_dim, true);
+  *map_failed = !encode_maps(&km, &vm, a, k_cache, v_cache, head_dim);
   if (*map_failed) return cudaErrorInvalidValue;
-  if (dtype == 0)
-    return head_dim == 128 ? launch_t<__half, 128>(a, km, vm, stream)
-                           : launch_t<__half, 64>(a, km, vm, stream);
-  return head_dim == 128 ? launch_t<__nv_bfloat16, 128>(a, km, vm, stream)
-                         : launch_t<__nv_bfloat16, 64>(a, km, vm, stream);
+  return by_shape(head_dim, a.bs_log2, [&](auto d, auto bs) {
+    return dtype == 0 ? launch_decode_t<__half, d(), bs()>(a, km, vm, stream)
+                      : launch_decode_t<__nv_bfloat16, d(), bs()>(a, km, vm, stream);
+  });
+}
+
+cudaError_t launch_chunk_fp4(const DecodeArgs &a, const void *k_cache, const void *v_cache,
+                             int head_dim, int dtype, cudaStream_t stream, bool *map_failed) {
+  CUtensorMap km, vm;
+  *map_failed = !encode_maps(&km, &vm, a, k_cache, v_cache, head_dim);
+  if (*map_failed) return cudaErrorInvalidValue;
+  return by_shape(head_dim, a.bs_log2, [&](auto d, auto bs) {
+    return dtype == 0 ? launch_chunk_t<__half, d(), bs()>(a, km, vm, stream)
+                      : launch_chunk_t<__nv_bfloat16, d(), bs()>(a, km, vm, stream);
+  });
 }
 
 }  // namespace pa

@@ -69,6 +69,10 @@ struct DecodeArgs {
   const int32_t *group_start;
   int num_groups, max_group_size;
   int members_per_cta, chunks;  // sequences per shared-prefix CTA, CTAs per group
+  // A chunk of few rows over FP4 caches (launch_chunk_fp4; nullptr otherwise):
+  // sequence i's rows start at query_start[i], as in PrefillArgs.
+  const int32_t *query_start;
+  int max_q_len;
 };
 
 struct ReduceArgs {
@@ -181,6 +185,10 @@ cudaError_t launch_decode(const DecodeArgs &a, const void *k_cache, const void *
                           cudaStream_t stream, bool *map_failed);
 cudaError_t launch_decode_fp4(const DecodeArgs &a, const void *k_cache, const void *v_cache,
                               int head_dim, int dtype, cudaStream_t stream, bool *map_failed);
+// pa_prefill_fp4 for chunks of at most kMaxChunkRows (token, head) rows a KV head.
+constexpr int kMaxChunkRows = 24;
+cudaError_t launch_chunk_fp4(const DecodeArgs &a, const void *k_cache, const void *v_cache,
+                             int head_dim, int dtype, cudaStream_t stream, bool *map_failed);
 cudaError_t launch_reduce(const ReduceArgs &a, int head_dim, int dtype, cudaStream_t stream);
 // The shared-prefix pass of pa_decode_shared_prefix (16-bit or FP8 caches);
 // the decode launch with a.prefix_lens set follows it on the same stream.

@@ -127,38 +127,43 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 // sub-tile whose block id is out of range) are zeroed by the V loader before
 // the stage is handed over; the softmax warps mask those keys.
 constexpr int kPairKeys = 64;                  // keys per step
-constexpr int kPairQAtom = kTcRows * 128;      // one 64-dim atom of a Q tile (bytes)
 constexpr int kPairKvAtom = kPairKeys * 128;   // one 64-dim atom of a K or V stage (bytes)
 
 // TILES query tiles per CTA: softmax warps 0 .. 4 TILES - 1, issuing warps
 // 4 TILES .. 6 TILES - 1 (Q K^T and P V of each tile), then the K and V warps.
 // Over FP8 caches at head_dim 128, and over FP4 caches, the two-tile kernel has
 // two more warps that widen half of each step's K and V codes, so the widening
-// is spread over all four schedulers of the SM.
-template <int TILES, int D = 128, Kv KV = Kv::k16>
+// is spread over all four schedulers of the SM.  The one-tile kernel over FP4
+// caches with at most 64 rows (ROWS = 64) has its helpers in warps 2 and 3,
+// whose rows would be empty, and half the Q tile: the products still run over
+// 128 rows, those past the 64th of whatever lies behind, and nobody reads them.
+template <int TILES, int D = 128, Kv KV = Kv::k16, int ROWS = kTcRows>
 __host__ __device__ constexpr bool has_helpers() {
-  return TILES == 2 && ((KV == Kv::kFp8 && D == 128) || KV == Kv::kFp4);
+  return (TILES == 2 && KV == Kv::kFp8 && D == 128) ||
+         (KV == Kv::kFp4 && (TILES == 2 || ROWS == 64));
 }
 template <int TILES, int D = 128, Kv KV = Kv::k16>
 constexpr int pair_threads() { return 32 * (6 * TILES + 2 + (has_helpers<TILES, D, KV>() ? 2 : 0)); }
 
-// FP4: steps of raw tiles in flight for each of K and V.  One tile per CTA has
-// room for one beside its widened stages (two CTAs share the SM's memory).
-template <int TILES, int D, Kv KV>
+// FP4: steps of raw tiles in flight for each of K and V.  One 128-row tile per
+// CTA has room for one beside its widened stages (two CTAs share the SM's
+// memory), a 64-row tile for three.
+template <int TILES, int D, Kv KV, int ROWS>
 constexpr int raw_stages() {
-  return KV != Kv::kFp4 ? 0 : TILES == 2 ? 6 : (D == 128 ? 1 : 4);
+  return KV != Kv::kFp4 ? 0 : TILES == 2 ? 6 : (D == 64 ? 4 : ROWS == 64 ? 3 : 1);
 }
 // Place of a raw 16-token FP4 tile (TMA copies start on 128 bytes); a 32-token
 // tile takes two.
 template <int D> constexpr int kRawSlot16 = D == 128 ? 1152 : 640;
 
-template <int SK, int SV, int TILES, int D, Kv KV>
+template <int SK, int SV, int TILES, int D, Kv KV, int ROWS>
 struct PairLayout {
   static constexpr int kAtoms = D / 64;
-  static constexpr int kRaw = raw_stages<TILES, D, KV>();
+  static constexpr int kQAtom = ROWS * 128;                         // one 64-dim atom of a Q tile
+  static constexpr int kRaw = raw_stages<TILES, D, KV, ROWS>();
   static constexpr int kRawStep = kPairKeys / 16 * kRawSlot16<D>;   // K or V of a step
   static constexpr int kQOff = 0;                                   // Q: [TILES][atoms]
-  static constexpr int kKOff = TILES * kAtoms * kPairQAtom;         // K ring: [SK][atoms]
+  static constexpr int kKOff = TILES * kAtoms * kQAtom;             // K ring: [SK][atoms]
   static constexpr int kVOff = kKOff + SK * kAtoms * kPairKvAtom;   // V ring: [SV][atoms]
   static constexpr int kRawOff = kVOff + SV * kAtoms * kPairKvAtom;  // FP4: [K, V][kRaw]
   static constexpr int kBarOff = kRawOff + 2 * kRaw * kRawStep;
@@ -281,7 +286,7 @@ __device__ __forceinline__ void f4_widen(const uint8_t *raw, uint8_t *st, int la
 // products then run in fp16 whatever T is (bf16 queries are carried in fp16,
 // see the Q load).  KV = kFp4: the same with FP4 tiles, which land in a ring of
 // their own.
-template <typename T, int D, int SK, int SV, bool SPLIT, int TILES, bool PX, Kv KV>
+template <typename T, int D, int SK, int SV, bool SPLIT, int TILES, bool PX, Kv KV, int ROWS>
 __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 : 1)
     pa_prefill_tc_pair_kernel(const __grid_constant__ CUtensorMap kmap,
                               const __grid_constant__ CUtensorMap vmap, const PrefillArgs a) {
@@ -292,13 +297,15 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
   constexpr bool kWide = F8 || F4;  // codes widened to fp16 in shared memory
   static_assert(!kWide || !SPLIT, "widened caches: the products run in fp16 (no split P)");
   static_assert(!F4 || !PX, "the shared-prefix pass has no FP4 form");
-  using L = PairLayout<SK, SV, TILES, D, KV>;
+  static_assert(ROWS == kTcRows || (ROWS == 64 && F4 && TILES == 1), "128 rows, or 64 over FP4");
+  using L = PairLayout<SK, SV, TILES, D, KV, ROWS>;
   constexpr int kAtoms = L::kAtoms;
+  constexpr int kSoft = ROWS / 32 * TILES;  // softmax warps
   constexpr int kIssue0 = 4 * TILES;      // first MMA-issuing warp
   constexpr int kLoad0 = 6 * TILES;       // K producer warp (V: kLoad0 + 1)
-  // widening helpers (K: kLoad0 + 2, V: kLoad0 + 3); a stage is handed
-  // over by every warp that widens part of it
-  constexpr bool kHelpers = has_helpers<TILES, D, KV>();
+  // widening helpers (K: kLoad0 + 2, V: kLoad0 + 3; with 64 rows warps 2 and
+  // 3); a stage is handed over by every warp that widens part of it
+  constexpr bool kHelpers = has_helpers<TILES, D, KV, ROWS>();
   constexpr int kWideners = kHelpers ? 2 : 1;
   constexpr int kSub = kPairKeys / 16;         // 16-row sub-tiles per step
   constexpr uint32_t kAllSub = (1u << kSub) - 1;
@@ -339,7 +346,7 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
   const int kvh = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.group;
-  const int tpc = TILES * kTcRows / G; // tokens per CTA (members, in the shared-prefix pass)
+  const int tpc = TILES * ROWS / G;    // tokens per CTA (members, in the shared-prefix pass)
   // shared-prefix pass: first_m of each member of the CTA, then the source
   // member, the member count and the first member's sequence
   int *px_first = reinterpret_cast<int *>(tmem_slot + 4);
@@ -357,13 +364,13 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
     mbar_init(v_tail, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
-      mbar_init(&s_free[t], kTcRows);
+      mbar_init(&s_free[t], ROWS);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&p_full[i], kTcRows);
+      mbar_init(&p_full[i], ROWS);
       mbar_init(&pv_done[i], 1);
     }
-    mbar_init(q_ready, TILES * kTcRows);
+    mbar_init(q_ready, TILES * ROWS);
     for (int s = 0; s < SK; ++s) mbar_init(&k_land[s], 1);
     for (int s = 0; s < SV; ++s) mbar_init(&v_land[s], 1);
     for (int s = 0; s < 4 * L::kRaw; ++s) mbar_init(&raw_land[s], 1);
@@ -480,7 +487,7 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
   // table entry of the 16-key sub-tile u of the key range
   auto table_entry = [&](int u) { return bt_row[(key_base + u * 16) >> a.bs_log2]; };
 
-  if (active && warp < kIssue0) {
+  if (active && warp < kSoft) {
     // ------------------------------------------------------------ softmax warps
     const int t = warp >> 2;
     const int r = tid & (kTcRows - 1);                 // row within the tile = TMEM lane
@@ -494,7 +501,7 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
       const T *qrow = static_cast<const T *>(a.query) +
                       (static_cast<int64_t>(q0 + (row_ok ? tok : 0)) * a.num_q_heads + kvh * G +
                        rc % G) * D;
-      uint8_t *qt = smem + L::kQOff + t * kAtoms * kPairQAtom;
+      uint8_t *qt = smem + L::kQOff + t * kAtoms * L::kQAtom;
       // bf16 queries over widened caches: the row is scaled by 2^e so that its
       // largest magnitude lands in [2^14, 2^15), then rounded to fp16 (exact
       // for every value down to 2^-31 of the largest: bf16 carries 8
@@ -532,7 +539,7 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
           }
           v = make_uint4(w4[0], w4[1], w4[2], w4[3]);
         }
-        *reinterpret_cast<uint4 *>(qt + (ch >> 3) * kPairQAtom + r * 128 +
+        *reinterpret_cast<uint4 *>(qt + (ch >> 3) * L::kQAtom + r * 128 +
                                    (((ch & 7) ^ (r & 7)) << 4)) = v;
       }
       fence_proxy_async_smem();
@@ -752,7 +759,7 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
       bool ok_run = true;
       if (qk_role) {
         const uint32_t id_qk = umma_idesc_f16(kMmaBf16 ? 1 : 0, false, kTcRows, kPairKeys);
-        const uint32_t qb = smem_addr(smem + L::kQOff) + t * kAtoms * kPairQAtom;
+        const uint32_t qb = smem_addr(smem + L::kQOff) + t * kAtoms * L::kQAtom;
         const uint32_t sk0 = smem_addr(smem + L::kKOff);
         // descriptors of the tile's Q and of K stage 0; every other operand
         // is these plus a byte offset / 16 in the address field (shared
@@ -773,7 +780,7 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
           const uint64_t dkn = dk0 + static_cast<uint64_t>(((n % SK) * kAtoms * kPairKvAtom) >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint64_t da = dq0 + static_cast<uint64_t>(((k >> 2) * kPairQAtom + (k & 3) * 32) >> 4);
+            const uint64_t da = dq0 + static_cast<uint64_t>(((k >> 2) * L::kQAtom + (k & 3) * 32) >> 4);
             const uint64_t db = dkn + static_cast<uint64_t>(((k >> 2) * kPairKvAtom + (k & 3) * 32) >> 4);
             umma_f16(tt, da, db, id_qk, k > 0);
           }
@@ -823,12 +830,12 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
       }
       if (!ok_run) atomicOr(a.err, kErrTimeout);
     }
-  } else if (active && warp >= kLoad0) {
+  } else if (active && (warp >= kLoad0 || (ROWS == 64 && warp < kIssue0))) {
     // ---------------------------------------------------- TMA producers (K, V)
     // (and, over FP8 caches at head_dim 128 with two tiles, the K and V
     // widening helpers)
-    const bool k_role = ((warp - kLoad0) & 1) == 0;
-    const bool helper = warp - kLoad0 >= 2;
+    const bool k_role = (warp & 1) == 0;  // kLoad0 is even
+    const bool helper = ROWS == 64 ? warp < kIssue0 : warp - kLoad0 >= 2;
     const int bs_mask = (1 << a.bs_log2) - 1;
     auto block_of = [&](int u) -> int {
       if (u >= n_sub) return -1;
@@ -857,7 +864,7 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
       const int S = k_role ? SK : SV;
       uint64_t *full = k_role ? k_full : v_full;
       uint64_t *empty = k_role ? k_empty : v_empty;
-      uint64_t *land = raw_land + (warp - kLoad0) * kRaw;
+      uint64_t *land = raw_land + ((warp & 1) + (helper ? 2 : 0)) * kRaw;
       uint8_t *ring = smem + (k_role ? L::kKOff : L::kVOff);
       uint8_t *raw = smem + L::kRawOff + (k_role ? 0 : kRaw * L::kRawStep);
       const CUtensorMap *map = k_role ? &kmap : &vmap;
@@ -1141,14 +1148,14 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
 }
 
 template <typename T, int D, int SK, int SV, bool SPLIT, int TILES, bool PX = false,
-          Kv KV = Kv::k16>
+          Kv KV = Kv::k16, int ROWS = kTcRows>
 cudaError_t launch_prefill_tc_pair_t(const PrefillArgs &a, const CUtensorMap &km,
                                      const CUtensorMap &vm, cudaStream_t stream) {
   // the shared-prefix pass keeps each member's first partition and the pass's
   // control words after the barriers
-  constexpr size_t smem = PairLayout<SK, SV, TILES, D, KV>::kSmem + (PX ? (kTcRows + 8) * 4 : 0);
+  constexpr size_t smem = PairLayout<SK, SV, TILES, D, KV, ROWS>::kSmem + (PX ? (kTcRows + 8) * 4 : 0);
   static_assert(smem <= (TILES == 1 ? 113 : 227) * 1024, "shared memory");
-  auto kern = pa_prefill_tc_pair_kernel<T, D, SK, SV, SPLIT, TILES, PX, KV>;
+  auto kern = pa_prefill_tc_pair_kernel<T, D, SK, SV, SPLIT, TILES, PX, KV, ROWS>;
   static SmemLimitOnce smem_limit;
   const cudaError_t e = smem_limit.ensure(kern, smem);
   if (e != cudaSuccess) return e;
@@ -1159,7 +1166,7 @@ cudaError_t launch_prefill_tc_pair_t(const PrefillArgs &a, const CUtensorMap &km
              static_cast<unsigned>(a.num_groups)),
         dim3(pair_threads<TILES, D, KV>()), smem, stream, km, vm, a);
   }
-  const int tpc = TILES * kTcRows / a.group;
+  const int tpc = TILES * ROWS / a.group;
   const int tiles = (a.max_q_len + tpc - 1) / tpc;
   return launch_dependent(kern, dim3(tiles, a.num_kv_heads, a.num_seqs),
                           dim3(pair_threads<TILES, D, KV>()), smem,
@@ -1201,15 +1208,17 @@ cudaError_t launch_prefill_tc_d(const PrefillArgs &a, const CUtensorMap &km,
   constexpr int SK = PA_PREFILL_SOLO_KSTAGES, SV = PA_PREFILL_SOLO_VSTAGES;
   if (kv == Kv::kFp4) {
     constexpr int FS = PA_PREFILL_FP4_STAGES;
-    if (dtype == 0)
-      return pair ? launch_prefill_tc_pair_t<__half, D, FS, FS, false, 2, false, Kv::kFp4>(
-                        a, km, vm, stream)
-                  : launch_prefill_tc_pair_t<__half, D, SK, SV, false, 1, false, Kv::kFp4>(
-                        a, km, vm, stream);
-    return pair ? launch_prefill_tc_pair_t<__nv_bfloat16, D, FS, FS, false, 2, false, Kv::kFp4>(
-                      a, km, vm, stream)
-                : launch_prefill_tc_pair_t<__nv_bfloat16, D, SK, SV, false, 1, false, Kv::kFp4>(
-                      a, km, vm, stream);
+    const bool few = static_cast<int64_t>(a.max_q_len) * a.group <= 64;
+    auto launch = [&](auto type) {
+      using T = decltype(type);
+      return pair  ? launch_prefill_tc_pair_t<T, D, FS, FS, false, 2, false, Kv::kFp4>(a, km, vm,
+                                                                                       stream)
+             : few ? launch_prefill_tc_pair_t<T, D, SK, SV, false, 1, false, Kv::kFp4, 64>(
+                         a, km, vm, stream)
+                   : launch_prefill_tc_pair_t<T, D, SK, SV, false, 1, false, Kv::kFp4>(a, km, vm,
+                                                                                       stream);
+    };
+    return dtype == 0 ? launch(__half{}) : launch(__nv_bfloat16{});
   }
   if (kv == Kv::kFp8) {
     if (dtype == 0)
@@ -1244,6 +1253,26 @@ cudaError_t launch_prefill_tc_d(const PrefillArgs &a, const CUtensorMap &km,
 cudaError_t launch_prefill(const PrefillArgs &a, const void *k_cache, const void *v_cache,
                            int64_t pool_rows, int head_dim, int dtype, Kv kv,
                            cudaStream_t stream, bool *map_failed) {
+  if (kv == Kv::kFp4 && static_cast<int64_t>(a.max_q_len) * a.group <= kMaxChunkRows) {
+    DecodeArgs d{};
+    d.out = a.out;
+    d.query = a.query;
+    d.query_start = a.query_start;
+    d.max_q_len = a.max_q_len;
+    d.block_tables = a.block_tables;
+    d.context_lens = a.context_lens;
+    d.max_blocks_per_seq = a.max_blocks_per_seq;
+    d.num_seqs = a.num_seqs;
+    d.num_q_heads = a.num_q_heads;
+    d.num_kv_heads = a.num_kv_heads;
+    d.group = a.group;
+    d.bs_log2 = a.bs_log2;
+    d.num_blocks = a.num_blocks;
+    d.scale_log2 = a.scale_log2;
+    d.out_scale = a.out_scale;
+    d.err = a.err;
+    return launch_chunk_fp4(d, k_cache, v_cache, head_dim, dtype, stream, map_failed);
+  }
   CUtensorMap km, vm;
   auto encode = [&](CUtensorMap *map, const void *cache) {
     return kv == Kv::kFp4 ? encode_fp4_map(map, cache, a.num_blocks * a.num_kv_heads,
