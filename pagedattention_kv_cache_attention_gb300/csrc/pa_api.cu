@@ -575,9 +575,8 @@ pa_status cache_fp4_impl(bool write, void *key, void *value, int64_t key_stride,
   const int64_t row = static_cast<int64_t>(num_kv_heads) * head_dim;
   if (key_stride < row || value_stride < row || key_stride % 8 || value_stride % 8)
     return PA_ERR_INVALID_ARG;
-  // the launch is one-dimensional over the groups of 16, at least 128 to a CTA
-  if (num_kv_heads > 65535 || num_tokens * (row / 16) > (int64_t(1) << 37))
-    return PA_ERR_UNSUPPORTED;
+  // offsets within a block (all heads) are 32-bit
+  if (num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
   unsigned int *err = nullptr;
   if (error_word(&err) != cudaSuccess) return PA_ERR_CUDA;
   pa::Fp4CacheArgs a;
