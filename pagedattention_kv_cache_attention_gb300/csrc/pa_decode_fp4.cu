@@ -70,30 +70,42 @@ constexpr float kPShift = 11.f, kGrowth = 4.f;
 // Geometry of a tile in shared memory.  TMA brings it in lines of D bytes (the
 // codes of two tokens; 9 lines for 16 tokens, the last of them scales) with the
 // swizzle of that line length: byte address bits 4.. ^= bits 7.. (three bits at
-// 128-byte lines, two at 64).  A 16-token tile takes a place of 12 lines, so
-// that the second tile of a 32-token unit (and of no other pair of places)
-// starts half a swizzle period off: all its addresses are XORed with kOdd.
+// 128-byte lines, two at 64).  Rows 8 apart, and the two 16-token tiles of a
+// 32-token unit (which start 12 lines apart), differ by half a swizzle period:
+// their addresses are the same but for an offset and an XOR with kHalf.  So an
+// address is one of two values of the lane (its offset, or that XOR kHalf) and
+// a constant.
 template <int D, int BS> struct Fp4Shape {
   static constexpr int kRow = D / 2;                     // bytes of a token's codes
   static constexpr int kScales = D / 16;                 // bytes of a token's scales
+  static constexpr int kHalf = D / 2;
   static constexpr int kSlot16 = 12 * D;
   static constexpr int kUnit = 2 * kSlot16;              // 32 tokens of K or V
   static constexpr int kTiles = 32 / BS;                 // tiles of a unit
   static constexpr int kLines = BS * 9 / 16;             // lines of a tile
   static constexpr int kTileBytes = fp4_tile_bytes(BS, D);
-  static constexpr int kOdd = BS == 16 ? D / 2 : 0;
-  // codes and scales of the unit's 16-token half h
-  __host__ __device__ static constexpr int codes(int h) { return h * (BS == 16 ? kSlot16 : 16 * kRow); }
-  __host__ __device__ static constexpr int scales(int h) {
-    return BS == 16 ? h * kSlot16 + 16 * kRow : 32 * kRow + h * 16 * kScales;
-  }
-  __host__ __device__ static constexpr int flip_codes(int h) { return h * kOdd; }
-  // (the second half's scales of a 32-token tile lie in the line that the
-  // 128-byte swizzle XORs with one 16-byte unit)
-  __host__ __device__ static constexpr int flip_scales(int h) { return h * (BS == 16 ? kOdd : (D == 128 ? 16 : 0)); }
   static constexpr int kMTiles = D / 16;
   static constexpr int kQChunks = D / 32;
 };
+
+// The lane's offset `at` (a byte of the codes of a row below 8 of a unit's
+// first half), or of the unit's half h and 8 up rows on.  (at_x = at ^ kHalf)
+template <int D, int BS>
+__device__ __forceinline__ int code_place(int at, int at_x, int h, int up) {
+  using Sh = Fp4Shape<D, BS>;
+  return BS == 16 ? ((h ^ up) ? at_x : at) + h * Sh::kSlot16 + up * 8 * Sh::kRow
+                  : (up ? at_x : at) + (16 * h + 8 * up) * Sh::kRow;
+}
+// The same for a scale byte (at: row * kScales + group, row below 8).  The
+// scales of a 32-token tile's second half lie in a line of their own at 128
+// bytes, whose swizzle flips unit 0.
+template <int D, int BS> __device__ __forceinline__ int scale_place(int at, int h, int up) {
+  using Sh = Fp4Shape<D, BS>;
+  if constexpr (BS == 16)
+    return at + 16 * Sh::kRow + h * Sh::kSlot16 + ((h ^ up) ? Sh::kHalf : 0);
+  else
+    return (D == 128 && h ? at ^ 16 : at) + (32 * Sh::kRow + (16 * h + 8 * up) * Sh::kScales);
+}
 
 // Row of a 16-token half that MMA row r stands for: a permutation that puts
 // the four V rows 2c (c = 0..3) into different banks.
@@ -272,17 +284,15 @@ __global__ void __launch_bounds__(NW * 32, ROWS == Rows::kChunk ? 1 : PA_DECODE_
     }
   }
 
-  // The lane's places in a half: K rows token_of(g) and + 8, V rows t0 =
-  // token_of(2c), t1 = token_of(2c + 1) and + 8.  Row r + 8 lies 8 kRow bytes
-  // on, in lines whose 128-byte swizzle differs in unit bit 2 (a 64-byte line's
-  // in none).
+  // The lane's places in a unit's first half: K row token_of(g), V rows t0 =
+  // token_of(2c) and t1 = token_of(2c + 1), all below 8; the scale groups 2c
+  // and 2c + 1 (or c) of K, g (or g / 2) of V.
   const int kr = token_of<D>(g), t0 = token_of<D>(2 * c), t1 = token_of<D>(2 * c + 1);
   constexpr int kBytes = D == 128 ? 16 : 8;  // of a K row; of a V row half of them
-  const int k_a = code_at<D>(kr, c * kBytes), k_b = code_at<D>(kr + 8, c * kBytes);
-  const int v_0 = code_at<D>(t0, g * kBytes / 2), v_1 = code_at<D>(t1, g * kBytes / 2);
-  const int v_2 = code_at<D>(t0 + 8, g * kBytes / 2), v_3 = code_at<D>(t1 + 8, g * kBytes / 2);
-  // scale groups of the lane: 2c and 2c + 1 (or c) of K, g (or g / 2) of V
-  const int ks_a = kr * Sh::kScales + (D == 128 ? 2 * c : c), ks_b = ks_a + 8 * Sh::kScales;
+  const int k_at = code_at<D>(kr, c * kBytes), k_ax = k_at ^ Sh::kHalf;
+  const int v_0 = code_at<D>(t0, g * kBytes / 2), v_0x = v_0 ^ Sh::kHalf;
+  const int v_1 = code_at<D>(t1, g * kBytes / 2), v_1x = v_1 ^ Sh::kHalf;
+  const int ks_at = kr * Sh::kScales + (D == 128 ? 2 * c : c);
   const int vs_0 = t0 * Sh::kScales + (D == 128 ? g : g >> 1);
   const int vs_1 = t1 * Sh::kScales + (D == 128 ? g : g >> 1);
 
@@ -309,30 +319,30 @@ __global__ void __launch_bounds__(NW * 32, ROWS == Rows::kChunk ? 1 : PA_DECODE_
     float x[NT][2][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint8_t *Ks = stage + Sh::codes(h);
-      const uint8_t *sc = stage + Sh::scales(h);
       // two chains of products, so that half of them wait for one another
       // (several tiles of columns are chains enough)
       constexpr int kChains = NT == 1 ? 2 : 1;
       float y[NT][kChains][4] = {};
-      const int ca = k_a ^ Sh::flip_codes(h), cb = k_b ^ Sh::flip_codes(h);
-      const int sa = ks_a ^ Sh::flip_scales(h), sb = ks_b ^ Sh::flip_scales(h);
+      const uint8_t *ka = stage + code_place<D, BS>(k_at, k_ax, h, 0);
+      const uint8_t *kb = stage + code_place<D, BS>(k_at, k_ax, h, 1);
+      const uint8_t *sa = stage + scale_place<D, BS>(ks_at, h, 0);
+      const uint8_t *sb = stage + scale_place<D, BS>(ks_at, h, 1);
       uint32_t pa, pb;  // the scales of rows a and b as fp16 pairs
       uint32_t wa[D / 32], wb[D / 32];
       if constexpr (D == 128) {
-        const uint4 va = *reinterpret_cast<const uint4 *>(Ks + ca);
-        const uint4 vb = *reinterpret_cast<const uint4 *>(Ks + cb);
+        const uint4 va = *reinterpret_cast<const uint4 *>(ka);
+        const uint4 vb = *reinterpret_cast<const uint4 *>(kb);
         wa[0] = va.x, wa[1] = va.y, wa[2] = va.z, wa[3] = va.w;
         wb[0] = vb.x, wb[1] = vb.y, wb[2] = vb.z, wb[3] = vb.w;
-        pa = e4m3x2_lo_to_f16x2(*reinterpret_cast<const uint16_t *>(sc + sa));
-        pb = e4m3x2_lo_to_f16x2(*reinterpret_cast<const uint16_t *>(sc + sb));
+        pa = e4m3x2_lo_to_f16x2(*reinterpret_cast<const uint16_t *>(sa));
+        pb = e4m3x2_lo_to_f16x2(*reinterpret_cast<const uint16_t *>(sb));
       } else {
-        const uint2 va = *reinterpret_cast<const uint2 *>(Ks + ca);
-        const uint2 vb = *reinterpret_cast<const uint2 *>(Ks + cb);
+        const uint2 va = *reinterpret_cast<const uint2 *>(ka);
+        const uint2 vb = *reinterpret_cast<const uint2 *>(kb);
         wa[0] = va.x, wa[1] = va.y;
         wb[0] = vb.x, wb[1] = vb.y;
-        pa = e4m3x2_lo_to_f16x2(sc[sa] * 0x101u);
-        pb = e4m3x2_lo_to_f16x2(sc[sb] * 0x101u);
+        pa = e4m3x2_lo_to_f16x2(*sa * 0x101u);
+        pb = e4m3x2_lo_to_f16x2(*sb * 0x101u);
       }
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {
@@ -436,11 +446,9 @@ __global__ void __launch_bounds__(NW * 32, ROWS == Rows::kChunk ? 1 : PA_DECODE_
     // ---- O^T += V^T P^T
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint8_t *Vs = stage + Sh::kUnit + Sh::codes(h);
-      const uint8_t *sc = stage + Sh::kUnit + Sh::scales(h);
-      uint32_t s0 = sc[vs_0 ^ Sh::flip_scales(h)], s1 = sc[vs_1 ^ Sh::flip_scales(h)];
-      uint32_t s2 = sc[(vs_0 + 8 * Sh::kScales) ^ Sh::flip_scales(h)];
-      uint32_t s3 = sc[(vs_1 + 8 * Sh::kScales) ^ Sh::flip_scales(h)];
+      const uint8_t *Vs = stage + Sh::kUnit;
+      uint32_t s0 = Vs[scale_place<D, BS>(vs_0, h, 0)], s1 = Vs[scale_place<D, BS>(vs_1, h, 0)];
+      uint32_t s2 = Vs[scale_place<D, BS>(vs_0, h, 1)], s3 = Vs[scale_place<D, BS>(vs_1, h, 1)];
       if (masked) {
         s0 = (mask >> (16 * h + t0)) & 1u ? s0 : 0;
         s1 = (mask >> (16 * h + t1)) & 1u ? s1 : 0;
@@ -457,13 +465,15 @@ __global__ void __launch_bounds__(NW * 32, ROWS == Rows::kChunk ? 1 : PA_DECODE_
 #pragma unroll
         for (int i = 0; i < 4; ++i) out[i] = f16x2_mul(out[i], s);
       };
-      const int c_0 = v_0 ^ Sh::flip_codes(h), c_1 = v_1 ^ Sh::flip_codes(h);
-      const int c_2 = v_2 ^ Sh::flip_codes(h), c_3 = v_3 ^ Sh::flip_codes(h);
+      const uint8_t *p0 = Vs + code_place<D, BS>(v_0, v_0x, h, 0);
+      const uint8_t *p1 = Vs + code_place<D, BS>(v_1, v_1x, h, 0);
+      const uint8_t *p2 = Vs + code_place<D, BS>(v_0, v_0x, h, 1);
+      const uint8_t *p3 = Vs + code_place<D, BS>(v_1, v_1x, h, 1);
       if constexpr (D == 128) {
-        const uint2 w0 = *reinterpret_cast<const uint2 *>(Vs + c_0);
-        const uint2 w1 = *reinterpret_cast<const uint2 *>(Vs + c_1);
-        const uint2 w2 = *reinterpret_cast<const uint2 *>(Vs + c_2);
-        const uint2 w3 = *reinterpret_cast<const uint2 *>(Vs + c_3);
+        const uint2 w0 = *reinterpret_cast<const uint2 *>(p0);
+        const uint2 w1 = *reinterpret_cast<const uint2 *>(p1);
+        const uint2 w2 = *reinterpret_cast<const uint2 *>(p2);
+        const uint2 w3 = *reinterpret_cast<const uint2 *>(p3);
 #pragma unroll
         for (int odd = 0; odd < 2; ++odd) {  // m-tiles 0, 2, 4, 6, then 1, 3, 5, 7
           uint32_t a0[4], a1[4], a2[4], a3[4];
@@ -479,10 +489,10 @@ __global__ void __launch_bounds__(NW * 32, ROWS == Rows::kChunk ? 1 : PA_DECODE_
                                 pb1[nt][h]);
         }
       } else {
-        const uint32_t w0 = *reinterpret_cast<const uint32_t *>(Vs + c_0);
-        const uint32_t w1 = *reinterpret_cast<const uint32_t *>(Vs + c_1);
-        const uint32_t w2 = *reinterpret_cast<const uint32_t *>(Vs + c_2);
-        const uint32_t w3 = *reinterpret_cast<const uint32_t *>(Vs + c_3);
+        const uint32_t w0 = *reinterpret_cast<const uint32_t *>(p0);
+        const uint32_t w1 = *reinterpret_cast<const uint32_t *>(p1);
+        const uint32_t w2 = *reinterpret_cast<const uint32_t *>(p2);
+        const uint32_t w3 = *reinterpret_cast<const uint32_t *>(p3);
 #pragma unroll
         for (int odd = 0; odd < 2; ++odd) {  // m-tiles 0, 2, then 1, 3
           uint32_t a0[4], a2[4];

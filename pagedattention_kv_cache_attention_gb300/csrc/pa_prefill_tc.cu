@@ -31,6 +31,9 @@ namespace pa {
 
 namespace {
 
+#ifndef PA_PREFILL_FP4_RAW
+#define PA_PREFILL_FP4_RAW 3
+#endif
 constexpr int kTcRows = 128;     // query rows per tile = TMEM lanes
 constexpr float kRescaleLog2 = 8.f;         // move the running max only past this growth
 constexpr unsigned kFullMask = 0xffffffffu;
@@ -150,7 +153,7 @@ constexpr int pair_threads() { return 32 * (6 * TILES + 2 + (has_helpers<TILES, 
 // memory), a 64-row tile for three.
 template <int TILES, int D, Kv KV, int ROWS>
 constexpr int raw_stages() {
-  return KV != Kv::kFp4 ? 0 : TILES == 2 ? 6 : (D == 64 ? 4 : ROWS == 64 ? 3 : 1);
+  return KV != Kv::kFp4 ? 0 : TILES == 2 ? PA_PREFILL_FP4_RAW : (D == 64 ? 4 : ROWS == 64 ? 3 : 1);
 }
 // Place of a raw 16-token FP4 tile (TMA copies start on 128 bytes); a 32-token
 // tile takes two.
