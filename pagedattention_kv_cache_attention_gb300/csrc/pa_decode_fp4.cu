@@ -55,11 +55,8 @@ namespace {
 #ifndef PA_DECODE_FP4_CTAS
 #define PA_DECODE_FP4_CTAS 4
 #endif
-#ifndef PA_CHUNK_FP4_WARPS
-#define PA_CHUNK_FP4_WARPS 8
-#endif
-#ifndef PA_CHUNK_FP4_STAGES
-#define PA_CHUNK_FP4_STAGES 3
+#ifndef PA_CHUNK_FP4_CTAS2
+#define PA_CHUNK_FP4_CTAS2 3
 #endif
 
 // P is held times 2^11, against a reference that is at most 2^4 below the
@@ -118,23 +115,60 @@ template <int D> __device__ __forceinline__ int code_at(int r, int b) {
   return at ^ (((at >> 7) & (D == 128 ? 7 : 3)) << 4);
 }
 
-enum class Rows { kDecode, kDecodeWarps, kChunk };
+// A warp's accumulators laid out in shared memory, 8 columns of kAccStride
+// floats, so that the 32 lanes of each store write 32 banks (lane row g holds
+// dimensions D/8 g .. D/8 g + D/8 - 1 of columns 2c and 2c + 1: in their own
+// order a store would hit two banks).
+template <int D> constexpr int kAccHalf = D / 2 + 8;       // from a first half-row to its second
+template <int D> constexpr int kAccStride = D + 12;
+template <int D> __device__ __forceinline__ int acc_place(int d) {  // of dimension d in a column
+  const int g = d / (D / 8), r = d % (D / 8), mt = r % (D / 16);
+  return (r >= D / 16 ? kAccHalf<D> : 0) + mt * 8 + g;
+}
+template <int D>
+__device__ __forceinline__ void put_acc(float *dst, const float (&acc)[D / 16][4], float s0,
+                                        float s1, int g, int c) {
+  float *d0 = dst + 2 * c * kAccStride<D> + g, *d1 = d0 + kAccStride<D>;
+#pragma unroll
+  for (int mt = 0; mt < D / 16; ++mt) {
+    d0[mt * 8] = acc[mt][0] * s0;
+    d1[mt * 8] = acc[mt][1] * s1;
+    d0[kAccHalf<D> + mt * 8] = acc[mt][2] * s0;
+    d1[kAccHalf<D> + mt * 8] = acc[mt][3] * s1;
+  }
+}
+
+enum class Rows { kDecode, kDecodeWarps, kWhole, kChunk };
+
+// CTAs that share an SM: 16, 12 or 8 warps in all, by the accumulators that a
+// thread holds (32, 64 or 96 registers at head_dim 128).
+constexpr int ctas_per_sm(int tiles) {
+  return tiles == 1 ? PA_DECODE_FP4_CTAS : tiles == 2 ? PA_CHUNK_FP4_CTAS2 : 2;
+}
 
 // T: query and output type.  NW warps, S stages each.  What the 8 NT columns of
 // the products are:
-//  kDecode       the heads of one query (NT = 1); the warps share a partition
+//  kDecode       the heads of one query (NT = 1); the warps share a partition,
+//                and the last CTA of a row joins them
 //  kDecodeWarps  the same, but each warp takes a whole partition and writes its
 //                partial itself (partitions joined by the reduce kernel), as in
 //                the 16-bit kernel
+//  kWhole        the heads of one query over its whole context, no partitions
 //  kChunk        rows of a short chunk, (token, head) pairs with token = row /
-//                G, the CTA's from row 8 NT blockIdx.x on; the warps share the
-//                keys up to its last row's
+//                G, the CTA's from row 8 NT group on; the warps share the keys
+//                up to its last row's
+// In a call without partitions (kWhole, kChunk) the warps of a.cluster CTAs share
+// the keys, and the CTAs join through one another's
+// shared memory: a long context then takes a cluster's time and not a CTA's,
+// and CTAs of unequal contexts fill the SMs more evenly.
 template <typename T, int D, int BS, int NW, int S, Rows ROWS, int NT>
-__global__ void __launch_bounds__(NW * 32, ROWS == Rows::kChunk ? 1 : PA_DECODE_FP4_CTAS)
+__global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
     pa_decode_fp4_kernel(const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap, const DecodeArgs a) {
   using Sh = Fp4Shape<D, BS>;
   constexpr bool WP = ROWS == Rows::kDecodeWarps, kChunk = ROWS == Rows::kChunk;
+  constexpr bool kParts = ROWS == Rows::kDecode || WP;  // a context is cut into partitions
+  const int cluster = kParts ? 1 : a.cluster;
   static_assert(kChunk || NT == 1, "a decode query's heads are one tile of columns");
   constexpr int kStep = 2 * Sh::kUnit;  // K then V of a 32-token step
   constexpr int kTiles = Sh::kTiles;
@@ -145,7 +179,8 @@ __global__ void __launch_bounds__(NW * 32, ROWS == Rows::kChunk ? 1 : PA_DECODE_
 
   const int kvh = blockIdx.y, seq = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int part = WP ? blockIdx.x * NW + warp : kChunk ? 0 : blockIdx.x;
+  const int rank = kParts ? 0 : static_cast<int>(blockIdx.x) % cluster;  // in the cluster
+  const int part = WP ? blockIdx.x * NW + warp : kParts ? blockIdx.x : 0;
   if (WP && part >= a.num_parts) return;  // the last CTA's spare warps
   const int g = lane >> 2, c = lane & 3;
   uint8_t *my_stages = smem + warp * S * kStep;
@@ -161,10 +196,11 @@ __global__ void __launch_bounds__(NW * 32, ROWS == Rows::kChunk ? 1 : PA_DECODE_
   // Steps are 32-token windows of the sequence from the one that holds the
   // partition's first token on: a block never straddles two.  A warp's tiles
   // are numbered l in its own order; 32 lanes hold a window of 32 of them.
-  const int t_begin = part * a.part_tokens;
+  const int t_begin = kParts ? part * a.part_tokens : 0;
   const int base = t_begin & ~31;
   const int32_t *bt_row = a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq;
-  auto step_token = [&](int k) { return base + (WP ? k : warp + k * NW) * 32; };
+  const int wid = rank * NW + warp, n_warps = NW * cluster;
+  auto step_token = [&](int k) { return base + (WP ? k : wid + k * n_warps) * 32; };
   auto block_of = [&](int l) { return step_token(l / kTiles) / BS + l % kTiles; };
   auto table_entry = [&](int l) -> int {
     const int lb = block_of(l);
@@ -178,12 +214,12 @@ __global__ void __launch_bounds__(NW * 32, ROWS == Rows::kChunk ? 1 : PA_DECODE_
   if constexpr (kChunk) {
     q0 = a.query_start[seq];
     const int q_len = a.query_start[seq + 1] - q0;
-    row0 = 8 * NT * blockIdx.x;
+    row0 = 8 * NT * (blockIdx.x / cluster);
     n_rows = q_len * G;
     base_pos = ctx - q_len;
     if (q_len < 0 || ctx < q_len || ctx > a.max_blocks_per_seq * BS || q_len > a.max_q_len) {
       if (threadIdx.x == 0 && row0 == 0 && kvh == 0) atomicOr(a.err, kErrBadLen);
-      return;
+      return;  // (the whole cluster)
     }
     if (row0 >= n_rows) return;
     ctx = base_pos + (min(n_rows, row0 + 8 * NT) - 1) / G + 1;  // keys of the CTA's last row
@@ -192,10 +228,10 @@ __global__ void __launch_bounds__(NW * 32, ROWS == Rows::kChunk ? 1 : PA_DECODE_
     ctx = 0;
   }
   if (part > 0 && t_begin >= ctx) return;
-  const int np_seq = !kChunk && ctx > 0 ? (ctx + a.part_tokens - 1) / a.part_tokens : 1;
-  const int t_end = kChunk ? ctx : min(ctx, t_begin + a.part_tokens);
+  const int np_seq = kParts && ctx > 0 ? (ctx + a.part_tokens - 1) / a.part_tokens : 1;
+  const int t_end = kParts ? min(ctx, t_begin + a.part_tokens) : ctx;
   const int n_step = t_end > base ? (t_end - base + 31) / 32 : 0;
-  const int my_n = WP ? n_step : (n_step > warp ? (n_step - warp + NW - 1) / NW : 0);
+  const int my_n = WP ? n_step : (n_step > wid ? (n_step - wid + n_warps - 1) / n_warps : 0);
 
   // First line of the warp's tile l in the pool.  Every step loads all its
   // tiles: in place of one without a token of the partition, and of an invalid
@@ -573,16 +609,28 @@ __global__ void __launch_bounds__(NW * 32, ROWS == Rows::kChunk ? 1 : PA_DECODE_
         a.ws_l[pr1] = l[0][1];
       }
     }
-    store_partial_o<D, true>(a.ws_o + pr0 * D, a.ws_o + pr1 * D, h0 < G, h1 < G, acc[0], inv0,
-                             inv1, g);
+    // out through the warp's idle stages, in whole lines
+    float *mine = reinterpret_cast<float *>(my_stages);
+    put_acc<D>(mine, acc[0], inv0, inv1, g, c);
+    __syncwarp();
+#pragma unroll 1
+    for (int i = lane; i < G * (D / 4); i += 32) {
+      const int h = i / (D / 4), d = i % (D / 4) * 4;
+      const float *src = mine + h * kAccStride<D>;
+      *reinterpret_cast<float4 *>(a.ws_o + ((first + h) * a.num_parts + part) * D + d) =
+          make_float4(src[acc_place<D>(d)], src[acc_place<D>(d + 1)], src[acc_place<D>(d + 2)],
+                      src[acc_place<D>(d + 3)]);
+    }
     grid_launch_dependents();
     return;
   }
 
   // ---- merge warps through shared memory (stages are idle now), a tile of
   // columns at a time
-  float *wacc = reinterpret_cast<float *>(smem);  // [NW][8][D]
-  float *wml = wacc + NW * 8 * D;                 // [NW][8][2]
+  float *wacc = reinterpret_cast<float *>(smem);  // [NW][8][kAccStride]
+  float *wml = wacc + NW * 8 * kAccStride<D>;     // [NW][8][2]
+  float *cl_o = wml + NW * 8 * 2 + 4;             // [NT][8][D]: the CTA's, for its cluster
+  float *cl_ml = cl_o + NT * 8 * D;               // [NT][8][2]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     __syncthreads();
@@ -592,8 +640,7 @@ __global__ void __launch_bounds__(NW * 32, ROWS == Rows::kChunk ? 1 : PA_DECODE_
       wml[(warp * 8 + 2 * c + 1) * 2 + 0] = cr[nt][1];
       wml[(warp * 8 + 2 * c + 1) * 2 + 1] = l[nt][1];
     }
-    float *mine = wacc + (warp * 8 + 2 * c) * D;
-    store_partial_o<D, true>(mine, mine + D, true, true, acc[nt], unshift, unshift, g);
+    put_acc<D>(wacc + warp * 8 * kAccStride<D>, acc[nt], unshift, unshift, g, c);
     __syncthreads();
     constexpr int kChunks = D / 8;
     const int cols = min(8, n_rows - row0 - 8 * nt);
@@ -607,9 +654,19 @@ __global__ void __launch_bounds__(NW * 32, ROWS == Rows::kChunk ? 1 : PA_DECODE_
       for (int w = 0; w < NW; ++w) {
         const float f = exp2f(wml[(w * 8 + h) * 2] - M);
         L += wml[(w * 8 + h) * 2 + 1] * f;
-        const float *src = wacc + (w * 8 + h) * D + ch * 8;
+        const float *src = wacc + (w * 8 + h) * kAccStride<D>;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] += src[e] * f;
+        for (int e = 0; e < 8; ++e) o[e] += src[acc_place<D>(ch * 8 + e)] * f;
+      }
+      if (!kParts && cluster > 1) {
+        float4 *dst = reinterpret_cast<float4 *>(cl_o + (nt * 8 + h) * D + ch * 8);
+        dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+        if (ch == 0) {
+          cl_ml[(nt * 8 + h) * 2] = M;
+          cl_ml[(nt * 8 + h) * 2 + 1] = L;
+        }
+        continue;
       }
       const int col = row0 + 8 * nt + h;
       const int64_t row = static_cast<int64_t>(q0 + (kChunk ? col / G : 0)) * a.num_q_heads +
@@ -617,7 +674,7 @@ __global__ void __launch_bounds__(NW * 32, ROWS == Rows::kChunk ? 1 : PA_DECODE_
       const float inv = L > 0.f ? a.out_scale / L : 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] *= inv;
-      if (kChunk || a.num_parts == 1 || (a.fuse_join && np_seq == 1)) {
+      if (!kParts || (a.fuse_join && np_seq == 1)) {
         *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row * D + ch * 8) =
             make_uint4(Elem<T>::pack(o[0], o[1]), Elem<T>::pack(o[2], o[3]),
                        Elem<T>::pack(o[4], o[5]), Elem<T>::pack(o[6], o[7]));
@@ -633,7 +690,44 @@ __global__ void __launch_bounds__(NW * 32, ROWS == Rows::kChunk ? 1 : PA_DECODE_
       }
     }
   }
-  if (!kChunk && a.fuse_join && np_seq > 1) {
+  if (!kParts && cluster > 1) {
+    // the cluster's CTAs share the rows of the join out
+    cluster_sync();
+    constexpr int kChunks = D / 8;
+    const int cols = min(8 * NT, n_rows - row0);
+    for (int item = threadIdx.x + rank * NW * 32; item < cols * kChunks;
+         item += NW * 32 * cluster) {
+      const int j = item / kChunks, ch = item % kChunks;
+      float M = NEG_INF;
+      for (int r = 0; r < cluster; ++r)
+        M = fmaxf(M, ld_cluster_f2(cluster_addr(cl_ml + j * 2, r)).x);
+      float L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int r = 0; r < cluster; ++r) {
+        const float2 ml = ld_cluster_f2(cluster_addr(cl_ml + j * 2, r));
+        const uint32_t src = cluster_addr(cl_o + j * D + ch * 8, r);
+        const float4 x = ld_cluster_f4(src), y = ld_cluster_f4(src + 16);
+        const float f = exp2f(ml.x - M);
+        L += ml.y * f;
+        o[0] += x.x * f;
+        o[1] += x.y * f;
+        o[2] += x.z * f;
+        o[3] += x.w * f;
+        o[4] += y.x * f;
+        o[5] += y.y * f;
+        o[6] += y.z * f;
+        o[7] += y.w * f;
+      }
+      const int col = row0 + j;
+      const int64_t row = static_cast<int64_t>(q0 + (kChunk ? col / G : 0)) * a.num_q_heads +
+                          kvh * G + (kChunk ? col % G : col);
+      const float inv = L > 0.f ? a.out_scale / L : 0.f;
+      *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row * D + ch * 8) = make_uint4(
+          Elem<T>::pack(o[0] * inv, o[1] * inv), Elem<T>::pack(o[2] * inv, o[3] * inv),
+          Elem<T>::pack(o[4] * inv, o[5] * inv), Elem<T>::pack(o[6] * inv, o[7] * inv));
+    }
+    cluster_sync();  // nobody leaves while its memory is read
+  }
+  if (kParts && a.fuse_join && np_seq > 1) {
     if (last_to_arrive(a, seq, kvh, np_seq, reinterpret_cast<uint32_t *>(wml + NW * 8 * 2)))
       join_partitions<T, D, NW>(a, seq, kvh, np_seq);
   }
@@ -645,35 +739,59 @@ cudaError_t launch_rows(const DecodeArgs &a, const CUtensorMap &km, const CUtens
                         unsigned grid_x, cudaStream_t stream) {
   constexpr size_t stages = static_cast<size_t>(NW) * S * 2 * Fp4Shape<D, BS>::kUnit;
   constexpr size_t smem = 1024 + stages + NW * S * 8;
-  static_assert(static_cast<size_t>(NW) * 8 * D * 4 + NW * 8 * 2 * 4 + 16 <= stages,
+  static_assert((static_cast<size_t>(NW) * (kAccStride<D> + 2) + NT * (D + 2)) * 32 + 16 <= stages,
                 "merge buffers and the join flag must fit in the stage area");
   static_assert(smem <= 227 * 1024, "shared memory");
   auto kern = pa_decode_fp4_kernel<T, D, BS, NW, S, ROWS, NT>;
   static SmemLimitOnce smem_limit;
   const cudaError_t e = smem_limit.ensure(kern, smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kern, dim3(grid_x, a.num_kv_heads, a.num_seqs), dim3(NW * 32), smem,
-                          stream, km, vm, a);
+  return launch_clusters(a.cluster, kern, dim3(grid_x, a.num_kv_heads, a.num_seqs),
+                         dim3(NW * 32), smem, stream, km, vm, a);
+}
+
+// How many CTAs share a row group's keys in a call without partitions: as many
+// as the SMs still have room for, while a warp keeps two steps of the longest
+// context that the table can hold.  Few sequences gain (one of 8,000 tokens and
+// one KV head 20 us, with one CTA 93; eight KV heads of 4,096 tokens 11 against
+// 33), and beyond that room a CTA's 4 to 6 us of start and join cost more than
+// the evener load gives (64 sequences of 512 to 4,096 tokens, 20 rows: 82 us
+// alone, 88 in pairs, 115 in fours).
+int cluster_of(const DecodeArgs &a, int64_t ctas, int warps, int per_sm) {
+  const int64_t steps = (static_cast<int64_t>(a.max_blocks_per_seq) << a.bs_log2) / 32;
+  int n = 1;
+  while (n < 8 && 2 * n * ctas <= 152 * per_sm && steps >= 4 * n * warps) n *= 2;
+  return n;
 }
 
 template <typename T, int D, int BS>
-cudaError_t launch_decode_t(const DecodeArgs &a, const CUtensorMap &km, const CUtensorMap &vm,
+cudaError_t launch_decode_t(DecodeArgs a, const CUtensorMap &km, const CUtensorMap &vm,
                             cudaStream_t stream) {
+  a.cluster = 1;
   constexpr int NW = PA_DECODE_FP4_WARPS, S = PA_DECODE_FP4_STAGES;
   if (a.num_parts > 1 && !a.fuse_join)
     return launch_rows<T, D, BS, NW, S, Rows::kDecodeWarps, 1>(a, km, vm,
                                                                (a.num_parts + NW - 1) / NW, stream);
-  return launch_rows<T, D, BS, NW, S, Rows::kDecode, 1>(a, km, vm, a.num_parts, stream);
+  if (a.num_parts > 1)
+    return launch_rows<T, D, BS, NW, S, Rows::kDecode, 1>(a, km, vm, a.num_parts, stream);
+  a.cluster = cluster_of(a, static_cast<int64_t>(a.num_seqs) * a.num_kv_heads, NW, ctas_per_sm(1));
+  return launch_rows<T, D, BS, NW, S, Rows::kWhole, 1>(a, km, vm, a.cluster, stream);
 }
 
 template <typename T, int D, int BS>
-cudaError_t launch_chunk_t(const DecodeArgs &a, const CUtensorMap &km, const CUtensorMap &vm,
+cudaError_t launch_chunk_t(DecodeArgs a, const CUtensorMap &km, const CUtensorMap &vm,
                            cudaStream_t stream) {
-  constexpr int NW = PA_CHUNK_FP4_WARPS, S = PA_CHUNK_FP4_STAGES;
   const int rows = a.max_q_len * a.group;
-  if (rows <= 8) return launch_rows<T, D, BS, NW, S, Rows::kChunk, 1>(a, km, vm, 1, stream);
-  if (rows <= 16) return launch_rows<T, D, BS, NW, S, Rows::kChunk, 2>(a, km, vm, 1, stream);
-  return launch_rows<T, D, BS, NW, S, Rows::kChunk, 3>(a, km, vm, (rows + 23) / 24, stream);
+  const int groups = (rows + 23) / 24;
+  auto launch = [&](auto tiles) {
+    constexpr int NT = decltype(tiles)::value;
+    a.cluster = cluster_of(a, static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * groups, 4,
+                           ctas_per_sm(NT));
+    return launch_rows<T, D, BS, 4, 2, Rows::kChunk, NT>(a, km, vm, groups * a.cluster, stream);
+  };
+  if (rows <= 8) return launch(std::integral_constant<int, 1>{});
+  if (rows <= 16) return launch(std::integral_constant<int, 2>{});
+  return launch(std::integral_constant<int, 3>{});
 }
 
 // f(head_dim, block_size) with both as compile-time constants

@@ -73,6 +73,8 @@ struct DecodeArgs {
   // sequence i's rows start at query_start[i], as in PrefillArgs.
   const int32_t *query_start;
   int max_q_len;
+  // CTAs of a cluster that share the keys of an unsplit call over FP4 caches
+  int cluster;
 };
 
 struct ReduceArgs {
@@ -150,20 +152,29 @@ struct BlockCopyArgs {
 // Launch `kern` on `stream` as a programmatic dependent of the work before it:
 // it may start while the previous kernel finishes, and must call
 // griddepcontrol.wait before reading anything that kernel writes.
+// launch_clusters: the same, in clusters of `cluster` CTAs along x.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                             cudaStream_t stream, Args &&...args) {
+cudaError_t launch_clusters(int cluster, void (*kern)(KArgs...), dim3 grid, dim3 block,
+                            size_t smem, cudaStream_t stream, Args &&...args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Args &&>(args)...);
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                             cudaStream_t stream, Args &&...args) {
+  return launch_clusters(1, kern, grid, block, smem, stream, static_cast<Args &&>(args)...);
 }
 
 // Largest partition size the shared-prefix kernel takes (its shared-memory
