@@ -24,81 +24,14 @@
 #include <type_traits>
 
 #include "pa_device.cuh"
-#include "pa_fp4.cuh"
 #include "pa_internal.h"
+#include "pa_tc.cuh"
 
 namespace pa {
 
 namespace {
 
-#ifndef PA_PREFILL_FP4_RAW
-#define PA_PREFILL_FP4_RAW 3
-#endif
-constexpr int kTcRows = 128;     // query rows per tile = TMEM lanes
 constexpr float kRescaleLog2 = 8.f;         // move the running max only past this growth
-constexpr unsigned kFullMask = 0xffffffffu;
-
-// D (TMEM) [+]= A (TMEM, K-major: lane = row, column c = elements 2c, 2c+1) * B (smem)
-__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b_desc,
-                                            uint32_t idesc, bool accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1 : 0)
-      : "memory");
-}
-
-// 16 consecutive 32-bit columns of this thread's TMEM lane
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
-}
-
-// Packed fp32 pairs (sm_100 and later): two IEEE fp32 operations per instruction,
-// each rounded exactly as the scalar one.
-// Non-blocking look at an mbarrier phase (acquire, CTA scope): true once the
-// phase with the given parity has completed.
-__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
-__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 f2_unpack(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 
 // ---------------------------------------------------------------------------
 // Query tiles per CTA, 64-key steps, scores and P in separate TMEM columns.
@@ -129,21 +62,19 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 // own warp.  V rows a product must not use (past the keys in use, or in a
 // sub-tile whose block id is out of range) are zeroed by the V loader before
 // the stage is handed over; the softmax warps mask those keys.
-constexpr int kPairKeys = 64;                  // keys per step
 constexpr int kPairKvAtom = kPairKeys * 128;   // one 64-dim atom of a K or V stage (bytes)
 
 // TILES query tiles per CTA: softmax warps 0 .. 4 TILES - 1, issuing warps
 // 4 TILES .. 6 TILES - 1 (Q K^T and P V of each tile), then the K and V warps.
-// Over FP8 caches at head_dim 128, and over FP4 caches, the two-tile kernel has
-// two more warps that widen half of each step's K and V codes, so the widening
-// is spread over all four schedulers of the SM.  The one-tile kernel over FP4
-// caches with at most 64 rows (ROWS = 64) has its helpers in warps 2 and 3,
+// Over FP8 caches at head_dim 128 the two-tile kernel has two more warps that
+// widen half of each step's K and V codes, so the widening is spread over all
+// four schedulers of the SM.  The one-tile kernel over FP4 caches (two tiles
+// run in pa_prefill_fp4.cu) with at most 64 rows (ROWS = 64) has its helpers in warps 2 and 3,
 // whose rows would be empty, and half the Q tile: the products still run over
 // 128 rows, those past the 64th of whatever lies behind, and nobody reads them.
 template <int TILES, int D = 128, Kv KV = Kv::k16, int ROWS = kTcRows>
 __host__ __device__ constexpr bool has_helpers() {
-  return (TILES == 2 && KV == Kv::kFp8 && D == 128) ||
-         (KV == Kv::kFp4 && (TILES == 2 || ROWS == 64));
+  return (TILES == 2 && KV == Kv::kFp8 && D == 128) || (KV == Kv::kFp4 && ROWS == 64);
 }
 template <int TILES, int D = 128, Kv KV = Kv::k16>
 constexpr int pair_threads() { return 32 * (6 * TILES + 2 + (has_helpers<TILES, D, KV>() ? 2 : 0)); }
@@ -153,12 +84,8 @@ constexpr int pair_threads() { return 32 * (6 * TILES + 2 + (has_helpers<TILES, 
 // memory), a 64-row tile for three.
 template <int TILES, int D, Kv KV, int ROWS>
 constexpr int raw_stages() {
-  return KV != Kv::kFp4 ? 0 : TILES == 2 ? PA_PREFILL_FP4_RAW : (D == 64 ? 4 : ROWS == 64 ? 3 : 1);
+  return KV != Kv::kFp4 ? 0 : (D == 64 ? 4 : ROWS == 64 ? 3 : 1);
 }
-// Place of a raw 16-token FP4 tile (TMA copies start on 128 bytes); a 32-token
-// tile takes two.
-template <int D> constexpr int kRawSlot16 = D == 128 ? 1152 : 640;
-
 template <int SK, int SV, int TILES, int D, Kv KV, int ROWS>
 struct PairLayout {
   static constexpr int kAtoms = D / 64;
@@ -235,78 +162,6 @@ __device__ __forceinline__ void f8_stage_to_f16(uint8_t *st, int lane, int pass_
   }
 }
 
-// FP4 caches: 32 rows of raw tiles (unswizzled) at a time become rows of the
-// fp16 tile that the MMA reads, every value s * e2m1(code) exact there.  A lane
-// takes 32 dimensions of a row, four words of eight codes, each one 16-byte
-// store.  Its words are taken in an order i = t ^ f that differs between lanes:
-// with it the 32 word loads of a step t hit 32 banks, and the eight stores of
-// a phase (two rows of four lanes, or four rows of two) eight different
-// 16-byte bank groups of the swizzled rows.  f and every offset depend on the
-// lane alone and are worked out once: worked out for each row, the widening took
-// as long as the whole step (2,030 of 2,100 cycles, measured), and with them it
-// takes 1,400.
-template <int D> struct F4Widen {
-  static constexpr int kPerRow = D / 32;          // lanes per row
-  static constexpr int kRows = 32 / kPerRow;      // rows per pass: 8 or 16
-  static constexpr int kPasses = 16 / kRows;      // passes of a 16-row group
-  int row, read[4], write[4], scale;
-  uint32_t sel_lo, sel_hi;  // the scale pair's halves for words t < 2 and t >= 2
-  int group1, scale0, scale1;  // second 16-row group, scales of the first and of the second
-
-  __device__ __forceinline__ F4Widen(int lane, int bs_log2) {
-    const int u = lane % kPerRow;
-    row = lane / kPerRow;
-    const int f = D == 128 ? ((row >> 1) & 3) ^ (u >> 1) ^ ((row & 1) << 1) : (row >> 2) & 3;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int i = t ^ f;
-      read[t] = row * (D / 2) + u * 16 + (i << 2);
-      write[t] = (u >> 1) * kPairKvAtom + row * 128 + ((((u & 1) * 4 + i) ^ (row & 7)) << 4);
-    }
-    scale = row * (D / 16) + 2 * u;
-    sel_lo = f & 2 ? 0x3232 : 0x1010;
-    sel_hi = f & 2 ? 0x1010 : 0x3232;
-    const bool bs16 = bs_log2 == 4;
-    group1 = bs16 ? kRawSlot16<D> : 16 * (D / 2);
-    scale0 = (bs16 ? 16 : 32) * (D / 2);
-    scale1 = bs16 ? kRawSlot16<D> + 16 * (D / 2) : 32 * (D / 2) + D;
-  }
-
-  // rows 0..31 of raw to rows 0..31 at st; rows that keep(row) refuses get a
-  // zero scale, and with it zeros: a code is always finite
-  template <typename Keep>
-  __device__ __forceinline__ void operator()(const uint8_t *raw, uint8_t *st, Keep keep) const {
-    uint32_t w[2][kPasses][4], sc[2][kPasses];
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-      for (int p = 0; p < kPasses; ++p) {
-        const uint8_t *codes = raw + (q ? group1 : 0) + p * kRows * (D / 2);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) w[q][p][t] = *reinterpret_cast<const uint32_t *>(codes + read[t]);
-        sc[q][p] = *reinterpret_cast<const uint16_t *>(raw + (q ? scale1 : scale0) +
-                                                       p * kRows * (D / 16) + scale);
-      }
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-      for (int p = 0; p < kPasses; ++p) {
-        const int r0 = 16 * q + p * kRows;
-        const uint32_t s2 = e4m3x2_lo_to_f16x2(keep(r0 + row) ? sc[q][p] : 0u);
-        const uint32_t lo = __byte_perm(s2, 0, sel_lo), hi = __byte_perm(s2, 0, sel_hi);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint32_t g = t < 2 ? lo : hi;
-          uint32_t h[4];
-          e2m1x8_to_half(w[q][p][t], h);
-          *reinterpret_cast<uint4 *>(st + r0 * 128 + write[t]) =
-              make_uint4(f16x2_mul(h[0], g), f16x2_mul(h[1], g), f16x2_mul(h[2], g),
-                         f16x2_mul(h[3], g));
-        }
-      }
-  }
-};
-
 // KV = kFp8: the caches hold FP8 E4M3 codes, widened to fp16 in shared memory; the
 // products then run in fp16 whatever T is (bf16 queries are carried in fp16,
 // see the Q load).  KV = kFp4: the same with FP4 tiles, which land in a ring of
@@ -321,7 +176,7 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
   constexpr bool F8 = KV == Kv::kFp8, F4 = KV == Kv::kFp4;
   constexpr bool kWide = F8 || F4;  // codes widened to fp16 in shared memory
   static_assert(!kWide || !SPLIT, "widened caches: the products run in fp16 (no split P)");
-  static_assert(!F4 || !PX, "the shared-prefix pass has no FP4 form");
+  static_assert(!F4 || (!PX && TILES == 1), "FP4: one tile, no shared-prefix pass");
   static_assert(ROWS == kTcRows || (ROWS == 64 && F4 && TILES == 1), "128 rows, or 64 over FP4");
   using L = PairLayout<SK, SV, TILES, D, KV, ROWS>;
   constexpr int kAtoms = L::kAtoms;
@@ -904,7 +759,7 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
         }
         return phys;
       };
-      const F4Widen<D> widen(lane, a.bs_log2);
+      const F4Widen<D> widen(lane, a.bs_log2, kPairKvAtom);
       win = tile_block(lane);
       uint32_t loaded = 0;  // bit 4 rs + i: tile i of the share in raw place rs
       auto fetch = [&](int m) {
@@ -1222,12 +1077,6 @@ cudaError_t launch_prefill_tc_pair_t(const PrefillArgs &a, const CUtensorMap &km
 #define PA_PREFILL_PAIR_VSTAGES 4
 #endif
 
-// Widened stages of the two-tile kernel over FP4 caches; its raw ring is what
-// runs ahead.
-#ifndef PA_PREFILL_FP4_STAGES
-#define PA_PREFILL_FP4_STAGES 3
-#endif
-
 bool prefill_tc_supported(int head_dim, int group) {
   return (head_dim == 64 || head_dim == 128) && group >= 1 && group <= 8;
 }
@@ -1241,16 +1090,14 @@ cudaError_t launch_prefill_tc_d(const PrefillArgs &a, const CUtensorMap &km,
   constexpr int PK = PA_PREFILL_PAIR_KSTAGES, PV = PA_PREFILL_PAIR_VSTAGES;
   constexpr int SK = PA_PREFILL_SOLO_KSTAGES, SV = PA_PREFILL_SOLO_VSTAGES;
   if (kv == Kv::kFp4) {
-    constexpr int FS = PA_PREFILL_FP4_STAGES;
+    if (pair) return launch_prefill_fp4(a, km, vm, D, dtype, stream);
     const bool few = static_cast<int64_t>(a.max_q_len) * a.group <= 64;
     auto launch = [&](auto type) {
       using T = decltype(type);
-      return pair  ? launch_prefill_tc_pair_t<T, D, FS, FS, false, 2, false, Kv::kFp4>(a, km, vm,
-                                                                                       stream)
-             : few ? launch_prefill_tc_pair_t<T, D, SK, SV, false, 1, false, Kv::kFp4, 64>(
-                         a, km, vm, stream)
-                   : launch_prefill_tc_pair_t<T, D, SK, SV, false, 1, false, Kv::kFp4>(a, km, vm,
-                                                                                       stream);
+      return few ? launch_prefill_tc_pair_t<T, D, SK, SV, false, 1, false, Kv::kFp4, 64>(a, km, vm,
+                                                                                         stream)
+                 : launch_prefill_tc_pair_t<T, D, SK, SV, false, 1, false, Kv::kFp4>(a, km, vm,
+                                                                                     stream);
     };
     return dtype == 0 ? launch(__half{}) : launch(__nv_bfloat16{});
   }

@@ -1,0 +1,165 @@
+// pa_tc.cuh -- what the tcgen05 prefill kernels share: wrappers of the
+// instructions that they use beyond pa_device.cuh's, packed fp32 arithmetic, and
+// the widening of FP4 tiles to the fp16 stages of the matrix products.
+#pragma once
+
+#include <stdint.h>
+
+#include "pa_device.cuh"
+#include "pa_fp4.cuh"
+
+namespace pa {
+
+constexpr int kTcRows = 128;     // query rows per tile = TMEM lanes
+constexpr int kPairKeys = 64;                  // keys per step
+constexpr unsigned kFullMask = 0xffffffffu;
+
+// D (TMEM) [+]= A (TMEM, K-major: lane = row, column c = elements 2c, 2c+1) * B (smem)
+__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b_desc,
+                                            uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1 : 0)
+      : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// 16 consecutive 32-bit columns of this thread's TMEM lane
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// Packed fp32 pairs (sm_100 and later): two IEEE fp32 operations per instruction,
+// each rounded exactly as the scalar one.
+// Non-blocking look at an mbarrier phase (acquire, CTA scope): true once the
+// phase with the given parity has completed.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 f2_unpack(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Place of a raw 16-token FP4 tile (TMA copies start on 128 bytes); a 32-token
+// tile takes two.
+template <int D> constexpr int kRawSlot16 = D == 128 ? 1152 : 640;
+
+// FP4 caches: 32 rows of raw tiles (unswizzled) at a time become rows of the
+// fp16 tile that the MMA reads, every value s * e2m1(code) exact there.  A lane
+// takes 32 dimensions of a row, four words of eight codes, each one 16-byte
+// store.  Its words are taken in an order i = t ^ f that differs between lanes:
+// with it the 32 word loads of a step t hit 32 banks, and the eight stores of
+// a phase (two rows of four lanes, or four rows of two) eight different
+// 16-byte bank groups of the swizzled rows.  f and every offset depend on the
+// lane alone and are worked out once: worked out for each row, the widening took
+// as long as the whole step (2,030 of 2,100 cycles, measured), and with them it
+// takes 1,400.
+template <int D> struct F4Widen {
+  static constexpr int kPerRow = D / 32;          // lanes per row
+  static constexpr int kRows = 32 / kPerRow;      // rows per pass: 8 or 16
+  static constexpr int kPasses = 16 / kRows;      // passes of a 16-row group
+  int row, read[4], write[4], scale;
+  uint32_t sel_lo, sel_hi;  // the scale pair's halves for words t < 2 and t >= 2
+  int group1, scale0, scale1;  // second 16-row group, scales of the first and of the second
+
+  // atom_bytes: from one 64-dimension atom of the fp16 stage to the next
+  __device__ __forceinline__ F4Widen(int lane, int bs_log2, int atom_bytes) {
+    const int u = lane % kPerRow;
+    row = lane / kPerRow;
+    const int f = D == 128 ? ((row >> 1) & 3) ^ (u >> 1) ^ ((row & 1) << 1) : (row >> 2) & 3;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int i = t ^ f;
+      read[t] = row * (D / 2) + u * 16 + (i << 2);
+      write[t] = (u >> 1) * atom_bytes + row * 128 + ((((u & 1) * 4 + i) ^ (row & 7)) << 4);
+    }
+    scale = row * (D / 16) + 2 * u;
+    sel_lo = f & 2 ? 0x3232 : 0x1010;
+    sel_hi = f & 2 ? 0x1010 : 0x3232;
+    const bool bs16 = bs_log2 == 4;
+    group1 = bs16 ? kRawSlot16<D> : 16 * (D / 2);
+    scale0 = (bs16 ? 16 : 32) * (D / 2);
+    scale1 = bs16 ? kRawSlot16<D> + 16 * (D / 2) : 32 * (D / 2) + D;
+  }
+
+  // rows 0..31 of raw to rows 0..31 at st; rows that keep(row) refuses get a
+  // zero scale, and with it zeros: a code is always finite
+  template <typename Keep>
+  __device__ __forceinline__ void operator()(const uint8_t *raw, uint8_t *st, Keep keep) const {
+    uint32_t w[2][kPasses][4], sc[2][kPasses];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const uint8_t *codes = raw + (q ? group1 : 0) + p * kRows * (D / 2);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) w[q][p][t] = *reinterpret_cast<const uint32_t *>(codes + read[t]);
+        sc[q][p] = *reinterpret_cast<const uint16_t *>(raw + (q ? scale1 : scale0) +
+                                                       p * kRows * (D / 16) + scale);
+      }
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int p = 0; p < kPasses; ++p) {
+        const int r0 = 16 * q + p * kRows;
+        const uint32_t s2 = e4m3x2_lo_to_f16x2(keep(r0 + row) ? sc[q][p] : 0u);
+        const uint32_t lo = __byte_perm(s2, 0, sel_lo), hi = __byte_perm(s2, 0, sel_hi);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const uint32_t g = t < 2 ? lo : hi;
+          uint32_t h[4];
+          e2m1x8_to_half(w[q][p][t], h);
+          *reinterpret_cast<uint4 *>(st + r0 * 128 + write[t]) =
+              make_uint4(f16x2_mul(h[0], g), f16x2_mul(h[1], g), f16x2_mul(h[2], g),
+                         f16x2_mul(h[3], g));
+        }
+      }
+  }
+};
+
+}  // namespace pa
