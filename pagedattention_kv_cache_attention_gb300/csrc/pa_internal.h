@@ -135,6 +135,7 @@ struct PrefillArgs {
   // partials (m, l, o) into the decode workspace.  Unused by pa_prefill.
   float *ws_m, *ws_l, *ws_o;
   const int32_t *prefix_lens, *group_start;
+  // (chunks: in the FP4 two-tile kernel, the CTAs of a cluster)
   int num_groups, max_group_size, members_per_cta, chunks;
   int part_tokens, num_parts, max_context_len;
 };

@@ -26,6 +26,10 @@
 // a tile's next scores then wait for its last P V.  Two threads a row took
 // 1,207.
 //
+// Where the call has too few CTAs to fill the SMs, a cluster of up to eight
+// shares a tile pair's keys: each CTA takes a run of the steps, leaves its O,
+// maximum and sum in shared memory, and the CTAs share the rows of the join.
+//
 // Warp roles: warps 0 and 2 widen K, 1 and 3 V; 4-7 softmax of tile 0, 8-11 of
 // tile 1; 12-15 issue (Q K^T and P V of tile 0, of tile 1).
 #include <cuda.h>
@@ -81,6 +85,10 @@ template <int D> struct Layout {
   static constexpr int kBarOff = kRawOff + 2 * kRaw * kRawStep;
   static constexpr int kBars = 2 * kSK + 2 * kSV + 4 + 4 + 4 + 1 + 4 * kRaw;
   static constexpr size_t kSmem = 1024 + kBarOff + kBars * 8 + 16;
+  // join in a cluster: O [tile][row][D] fp32 over the idle Q and stages, 16-byte
+  // unit u of row r at u ^ (r & 7); then (maximum, sum) [tile][row]
+  static constexpr int kMlOff = 2 * kTcRows * D * 4;
+  static_assert(kMlOff + 2 * kTcRows * 8 <= kRawOff, "the join fits in Q and the stages");
 };
 
 template <typename T, int D>
@@ -145,9 +153,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (q_len < 0 || ctx < q_len || ctx > (a.max_blocks_per_seq << a.bs_log2) ||
       q_len > a.max_q_len) {
     if (tid == 0 && blockIdx.x == 0 && kvh == 0) atomicOr(a.err, kErrBadLen);
-    active = false;
+    active = false;  // (in the whole cluster, here and below)
   }
-  const int t_first = blockIdx.x * tpc;
+  const int cluster = a.chunks, rank = blockIdx.x % cluster;
+  const int t_first = blockIdx.x / cluster * tpc;
   if (t_first >= q_len) active = false;
   const int t_last = min(q_len, t_first + tpc) - 1;
   const int base_pos = ctx - q_len;
@@ -158,11 +167,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   // reach token (kTcRows - 1) / G; tile 1's begin at token kTcRows / G.
   const int last0 = min(t_last, t_first + (kTcRows - 1) / G);
   const int last1 = t_first + kTcRows / G <= t_last ? t_last : -1;
-  const int steps0 = active ? (base_pos + last0 + kPairKeys) / kPairKeys : 0;
-  const int steps1 = active && last1 >= 0 ? (n_keys + kPairKeys - 1) / kPairKeys : 0;
-  const int n_steps = max(steps0, steps1);
+  // In a cluster, from step_base on the CTA's share of them.
+  const int all0 = active ? (base_pos + last0 + kPairKeys) / kPairKeys : 0;
+  const int all1 = active && last1 >= 0 ? (n_keys + kPairKeys - 1) / kPairKeys : 0;
+  const int all = max(all0, all1);
+  const int step_base = static_cast<int>(static_cast<int64_t>(all) * rank / cluster);
+  const int n_steps = static_cast<int>(static_cast<int64_t>(all) * (rank + 1) / cluster) - step_base;
+  const int steps0 = max(0, min(n_steps, all0 - step_base));
+  const int steps1 = all1 > 0 ? n_steps : 0;
   const int n_sub = (n_keys + 15) / 16;
 
+  // the softmax threads' row, for the join in a cluster
+  float m_ref = -INFINITY, l = 0.f;
+  bool row_done = false;  // the row's O is in tensor memory
   if (active && warp >= kSoft0 && warp < kSoft0 + 8) {
     // ------------------------------------------------------------ softmax warps
     const int t = (warp - kSoft0) >> 2;
@@ -223,14 +240,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * 256;
     // table entry of sub-tile `lane` of step n; whether the loaders took it
     auto entry = [&](int n) -> int {
-      const int u = n * kSub + lane;
+      const int u = (step_base + n) * kSub + lane;
       return lane < kSub && u < n_sub ? bt_row[(u * 16) >> a.bs_log2] : -1;
     };
     auto valid = [&](int phys) -> uint32_t {
       return __ballot_sync(kFullMask, phys >= 0 && static_cast<int64_t>(phys) < a.num_blocks) &
              kAllSub;
     };
-    float m_ref = -INFINITY, l = 0.f;
     bool ok_run = true;
     uint32_t vmask_next = my_steps > 0 ? valid(entry(0)) : 0;
     for (int n = 0; n < my_steps; ++n) {
@@ -256,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // loaded now, used at the end of the step: its latency hides behind the softmax
       const int bt_next = n + 1 < my_steps ? entry(n + 1) : -1;
-      const int key0 = n * kPairKeys;
+      const int key0 = (step_base + n) * kPairKeys;
       if (!(row_ok && key0 + kPairKeys - 1 <= pos && vmask == kAllSub)) {
 #pragma unroll
         for (int c = 0; c < kPairKeys; ++c) {
@@ -325,7 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int last = my_steps - 1;
       ok_run = __all_sync(kFullMask,
                           mbar_wait_bounded(&pv_done[2 * t + (last & 1)], (last >> 1) & 1));
-      if (ok_run) {
+      row_done = ok_run;
+      if (ok_run && cluster == 1) {
         tc_fence_after();
         const float inv = l > 0.f ? a.out_scale / l : 0.f;  // times the V scale
         T *orow = static_cast<T *>(a.out) +
@@ -448,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t policy = l2_policy_evict_first();
     // block of the warp's tile l (its tiles are numbered over all steps)
     auto tile_block = [&](int l) -> int {
-      const int key = (l >> tsh) * kPairKeys + share0 + (tsh ? (l & 1) * 16 : 0);
+      const int key = (step_base + (l >> tsh)) * kPairKeys + share0 + (tsh ? (l & 1) * 16 : 0);
       if (key >= n_keys) return -1;
       const int phys = bt_row[key >> a.bs_log2];
       if (phys < 0 || static_cast<int64_t>(phys) >= a.num_blocks) {
@@ -493,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       const uint32_t ok = (loaded >> (2 * rs)) & 3u;
-      const int past = n_keys - m * kPairKeys - share0;  // the share's first row past the keys
+      const int past = n_keys - (step_base + m) * kPairKeys - share0;  // the share's first row past the keys
       uint8_t *st = (k_role ? smem + L::kKOff + s * kAtoms * L::kKAtom
                             : smem + L::kVOff + s * kAtoms * L::kVAtom) + share0 * 128;
       const uint8_t *from = raw + rs * L::kRawStep;
@@ -519,6 +536,63 @@ __global__ void __launch_bounds__(kThreads, 1)
   // before it), or the tile had no work
   tc_fence_before();
   __syncthreads();
+  if (cluster > 1 && active) {
+    float2 *ml = reinterpret_cast<float2 *>(smem + L::kMlOff);
+    if (warp >= kSoft0 && warp < kSoft0 + 8) {
+      const int t = (warp - kSoft0) >> 2, r = tid & (kTcRows - 1);
+      const uint32_t addr =
+          tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * 256 + kOCol;
+      float4 *row = reinterpret_cast<float4 *>(smem + (t * kTcRows + r) * D * 4);
+      tc_fence_after();
+#pragma unroll 1
+      for (int cb = 0; cb < D / 32; ++cb) {
+        float o[32];
+        tmem_ld32(addr + cb * 32, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          row[(cb * 8 + q) ^ (r & 7)] =
+              row_done ? make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3])
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      ml[t * kTcRows + r] = make_float2(row_done ? m_ref : -INFINITY, row_done ? l : 0.f);
+      tc_fence_before();
+    }
+    cluster_sync();
+    // the pair's 256 rows, an equal share of them for each CTA, 8 columns at a time
+    const int rows = 2 * kTcRows / cluster;
+    for (int i = tid; i < rows * (D / 8); i += kThreads) {
+      const int rc = rank * rows + i / (D / 8), ch = i % (D / 8);
+      const int tok = t_first + rc / G;
+      if (tok > t_last) continue;
+      float M = -INFINITY, sum = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < cluster; ++k) M = fmaxf(M, ld_cluster_f2(cluster_addr(ml + rc, k)).x);
+      const float ref = M == -INFINITY ? 0.f : M;
+      for (int k = 0; k < cluster; ++k) {
+        const float2 part = ld_cluster_f2(cluster_addr(ml + rc, k));
+        const uint32_t row = cluster_addr(smem + rc * D * 4, k);
+        const float4 x = ld_cluster_f4(row + (((2 * ch) ^ (rc & 7)) << 4));
+        const float4 y = ld_cluster_f4(row + (((2 * ch + 1) ^ (rc & 7)) << 4));
+        const float f = exp2f(part.x - ref);
+        sum += part.y * f;
+        o[0] += x.x * f;
+        o[1] += x.y * f;
+        o[2] += x.z * f;
+        o[3] += x.w * f;
+        o[4] += y.x * f;
+        o[5] += y.y * f;
+        o[6] += y.z * f;
+        o[7] += y.w * f;
+      }
+      const float inv = sum > 0.f ? a.out_scale / sum : 0.f;
+      T *orow = static_cast<T *>(a.out) +
+                (static_cast<int64_t>(q0 + tok) * a.num_q_heads + kvh * G + rc % G) * D;
+      *reinterpret_cast<uint4 *>(orow + ch * 8) = make_uint4(
+          Elem<T>::pack(o[0] * inv, o[1] * inv), Elem<T>::pack(o[2] * inv, o[3] * inv),
+          Elem<T>::pack(o[4] * inv, o[5] * inv), Elem<T>::pack(o[6] * inv, o[7] * inv));
+    }
+    cluster_sync();  // nobody leaves while its memory is read
+  }
   if (warp == kIssue0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -535,9 +609,16 @@ cudaError_t launch_t(const PrefillArgs &a, const CUtensorMap &km, const CUtensor
   static SmemLimitOnce smem_limit;
   const cudaError_t e = smem_limit.ensure(kern, smem);
   if (e != cudaSuccess) return e;
-  const int tpc = 2 * kTcRows / a.group;
-  return launch_dependent(kern, dim3((a.max_q_len + tpc - 1) / tpc, a.num_kv_heads, a.num_seqs),
-                          dim3(kThreads), smem, stream, km, vm, a);
+  // as many CTAs on a tile pair's keys as the SMs have room for, while each
+  // keeps four steps of the longest context that the table can hold
+  PrefillArgs b = a;
+  const int tpc = 2 * kTcRows / a.group, tiles = (a.max_q_len + tpc - 1) / tpc;
+  const int64_t ctas = static_cast<int64_t>(tiles) * a.num_kv_heads * a.num_seqs;
+  const int64_t steps = (static_cast<int64_t>(a.max_blocks_per_seq) << a.bs_log2) / kPairKeys;
+  b.chunks = 1;
+  while (b.chunks < 8 && 2 * b.chunks * ctas <= 152 && steps >= 8 * b.chunks) b.chunks *= 2;
+  return launch_clusters(b.chunks, kern, dim3(tiles * b.chunks, a.num_kv_heads, a.num_seqs),
+                         dim3(kThreads), smem, stream, km, vm, b);
 }
 
 }  // namespace

@@ -68,10 +68,11 @@ constexpr int kPairKvAtom = kPairKeys * 128;   // one 64-dim atom of a K or V st
 // 4 TILES .. 6 TILES - 1 (Q K^T and P V of each tile), then the K and V warps.
 // Over FP8 caches at head_dim 128 the two-tile kernel has two more warps that
 // widen half of each step's K and V codes, so the widening is spread over all
-// four schedulers of the SM.  The one-tile kernel over FP4 caches (two tiles
-// run in pa_prefill_fp4.cu) with at most 64 rows (ROWS = 64) has its helpers in warps 2 and 3,
-// whose rows would be empty, and half the Q tile: the products still run over
-// 128 rows, those past the 64th of whatever lies behind, and nobody reads them.
+// four schedulers of the SM.  Over FP4 caches the kernel serves at most 64 rows
+// (ROWS = 64; more run in pa_prefill_fp4.cu): its helpers are warps 2 and 3,
+// whose rows would be empty, and the Q tile is half: the products still run
+// over 128 rows, those past the 64th of whatever lies behind, and nobody reads
+// them.
 template <int TILES, int D = 128, Kv KV = Kv::k16, int ROWS = kTcRows>
 __host__ __device__ constexpr bool has_helpers() {
   return (TILES == 2 && KV == Kv::kFp8 && D == 128) || (KV == Kv::kFp4 && ROWS == 64);
@@ -79,18 +80,16 @@ __host__ __device__ constexpr bool has_helpers() {
 template <int TILES, int D = 128, Kv KV = Kv::k16>
 constexpr int pair_threads() { return 32 * (6 * TILES + 2 + (has_helpers<TILES, D, KV>() ? 2 : 0)); }
 
-// FP4: steps of raw tiles in flight for each of K and V.  One 128-row tile per
-// CTA has room for one beside its widened stages (two CTAs share the SM's
-// memory), a 64-row tile for three.
-template <int TILES, int D, Kv KV, int ROWS>
-constexpr int raw_stages() {
-  return KV != Kv::kFp4 ? 0 : (D == 64 ? 4 : ROWS == 64 ? 3 : 1);
-}
+// FP4: steps of raw tiles in flight for each of K and V, beside the widened
+// stages (two CTAs share the SM's memory).
+template <int D, Kv KV>
+constexpr int raw_stages() { return KV != Kv::kFp4 ? 0 : D == 64 ? 4 : 3; }
+
 template <int SK, int SV, int TILES, int D, Kv KV, int ROWS>
 struct PairLayout {
   static constexpr int kAtoms = D / 64;
   static constexpr int kQAtom = ROWS * 128;                         // one 64-dim atom of a Q tile
-  static constexpr int kRaw = raw_stages<TILES, D, KV, ROWS>();
+  static constexpr int kRaw = raw_stages<D, KV>();
   static constexpr int kRawStep = kPairKeys / 16 * kRawSlot16<D>;   // K or V of a step
   static constexpr int kQOff = 0;                                   // Q: [TILES][atoms]
   static constexpr int kKOff = TILES * kAtoms * kQAtom;             // K ring: [SK][atoms]
@@ -176,8 +175,8 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
   constexpr bool F8 = KV == Kv::kFp8, F4 = KV == Kv::kFp4;
   constexpr bool kWide = F8 || F4;  // codes widened to fp16 in shared memory
   static_assert(!kWide || !SPLIT, "widened caches: the products run in fp16 (no split P)");
-  static_assert(!F4 || (!PX && TILES == 1), "FP4: one tile, no shared-prefix pass");
-  static_assert(ROWS == kTcRows || (ROWS == 64 && F4 && TILES == 1), "128 rows, or 64 over FP4");
+  static_assert(!F4 || ROWS == 64, "FP4: up to 64 rows here");
+  static_assert(ROWS == kTcRows || (F4 && TILES == 1 && !PX), "a 64-row tile: FP4 chunks only");
   using L = PairLayout<SK, SV, TILES, D, KV, ROWS>;
   constexpr int kAtoms = L::kAtoms;
   constexpr int kSoft = ROWS / 32 * TILES;  // softmax warps
@@ -1090,16 +1089,19 @@ cudaError_t launch_prefill_tc_d(const PrefillArgs &a, const CUtensorMap &km,
   constexpr int PK = PA_PREFILL_PAIR_KSTAGES, PV = PA_PREFILL_PAIR_VSTAGES;
   constexpr int SK = PA_PREFILL_SOLO_KSTAGES, SV = PA_PREFILL_SOLO_VSTAGES;
   if (kv == Kv::kFp4) {
-    if (pair) return launch_prefill_fp4(a, km, vm, D, dtype, stream);
-    const bool few = static_cast<int64_t>(a.max_q_len) * a.group <= 64;
-    auto launch = [&](auto type) {
-      using T = decltype(type);
-      return few ? launch_prefill_tc_pair_t<T, D, SK, SV, false, 1, false, Kv::kFp4, 64>(a, km, vm,
-                                                                                         stream)
-                 : launch_prefill_tc_pair_t<T, D, SK, SV, false, 1, false, Kv::kFp4>(a, km, vm,
-                                                                                     stream);
-    };
-    return dtype == 0 ? launch(__half{}) : launch(__nv_bfloat16{});
+    // Up to 64 rows run two CTAs to an SM where there are enough of them (64
+    // sequences of 512 to 4,096 tokens, 8 KV heads, 28 to 64 rows: 110 to 122
+    // us against 145 with two tiles); more rows, and few CTAs, in the two-tile
+    // kernel, whose steps are shorter (80 rows of the same batch 146 us; in a
+    // one-tile kernel 176), and which shares a sequence's keys in a cluster.
+    if (static_cast<int64_t>(a.max_q_len) * a.group > 64 ||
+        static_cast<int64_t>(a.num_seqs) * a.num_kv_heads < 2 * 152)
+      return launch_prefill_fp4(a, km, vm, D, dtype, stream);
+    return dtype == 0
+               ? launch_prefill_tc_pair_t<__half, D, SK, SV, false, 1, false, Kv::kFp4, 64>(
+                     a, km, vm, stream)
+               : launch_prefill_tc_pair_t<__nv_bfloat16, D, SK, SV, false, 1, false, Kv::kFp4, 64>(
+                     a, km, vm, stream);
   }
   if (kv == Kv::kFp8) {
     if (dtype == 0)

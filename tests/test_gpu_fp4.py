@@ -362,6 +362,28 @@ def test_prefill_random_shapes(pa, i):
     assert pa.pa_device_errors() == 0
 
 
+@pytest.mark.parametrize("rows", [1, 7, 8, 9, 16, 17, 24, 25, 48, 63, 64, 65, 127, 128, 129, 255,
+                                  256, 257, 300])
+@pytest.mark.parametrize("G,d,bs,dtype", [(1, 128, 16, "fp16"), (8, 64, 32, "bf16"),
+                                          (3, 128, 32, "bf16")])
+def test_prefill_few_sequences_beside_a_long_one(pa, rows, G, d, bs, dtype):
+    """The table has room for the longest context, so the keys of the short ones
+    are fewer than the work is split for."""
+    q = -(-rows // G)
+    lens = [2600, q, q + 1, q + 40, q + 65]
+    b = Batch(900 + rows, lens, 2, G, d, bs, dtype, ks=0.5, vs=2.0, q_lens=[q, q, q, max(1, q // 2), q])
+    b.check(b.prefill(pa))
+    assert pa.pa_device_errors() == 0
+
+
+def test_prefill_more_sequences_than_multiprocessors(pa):
+    rng = np.random.default_rng(77)
+    lens = rng.integers(20, 400, 170)
+    b = Batch(54, lens, 2, 2, 128, 16, "fp16", q_lens=[20] * 170)
+    b.check(b.prefill(pa))
+    assert pa.pa_device_errors() == 0
+
+
 def test_prefill_keeps_the_mass_of_a_long_faint_tail(pa):
     n, d, bs = 9001, 64, 16
     b = Batch(52, [n], 1, 2, d, bs, "fp16", q_lens=[3])
