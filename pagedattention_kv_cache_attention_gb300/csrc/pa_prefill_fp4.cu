@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *raw_land = q_ready + 1;   // [4 warps][kRaw]: a warp's raw tiles of a step are in
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(raw_land + 4 * kRaw);
 
-  const int kvh = blockIdx.y, seq = blockIdx.z;
+  const int kvh = blockIdx.x / a.chunks, seq = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.group;
   const int tpc = 2 * kTcRows / G;  // tokens per CTA
@@ -152,11 +152,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool active = true;
   if (q_len < 0 || ctx < q_len || ctx > (a.max_blocks_per_seq << a.bs_log2) ||
       q_len > a.max_q_len) {
-    if (tid == 0 && blockIdx.x == 0 && kvh == 0) atomicOr(a.err, kErrBadLen);
+    if (tid == 0) atomicOr(a.err, kErrBadLen);
     active = false;  // (in the whole cluster, here and below)
   }
   const int cluster = a.chunks, rank = blockIdx.x % cluster;
-  const int t_first = blockIdx.x / cluster * tpc;
+  const int t_first = (gridDim.z - 1 - blockIdx.z) * tpc;
   if (t_first >= q_len) active = false;
   const int t_last = min(q_len, t_first + tpc) - 1;
   const int base_pos = ctx - q_len;
@@ -190,50 +190,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pos = base_pos + tok;     // keys up to pos are attended to
     const int my_steps = t == 0 ? steps0 : steps1;
     float sl2 = a.scale_log2;           // this row's softmax scale (base 2)
+    // Q and the output move in whole rows: lane ch of a group of kLanes holds
+    // unit ch of the row, kRowsAt rows at a time; the rows' offsets from the
+    // tile pair's first (in rows of D; -1: past the chunk) are asked of their
+    // threads.  A thread that walks its own row touches a line with every lane
+    // of every access instead: 3 us more a CTA (of 13 for one step of keys).
+    constexpr int kLanes = D / 8, kRowsAt = 32 / kLanes;
+    const int sub = lane / kLanes, ch = lane % kLanes;
+    const int row_off = row_ok ? (rc / G) * a.num_q_heads + rc % G : -1;
+    const int64_t tile_at =
+        (static_cast<int64_t>(q0 + t_first) * a.num_q_heads + kvh * G) * D;
+    // 16-byte unit c of row i of this warp in the swizzled Q tile
+    auto q_unit = [&](int i, int c) {
+      return reinterpret_cast<uint4 *>(smem + (t * kAtoms + (c >> 3)) * L::kQAtom +
+                                       ((warp & 3) * 32 + i) * 128 + (((c & 7) ^ (i & 7)) << 4));
+    };
     {
-      const T *qrow = static_cast<const T *>(a.query) +
-                      (static_cast<int64_t>(q0 + (row_ok ? tok : 0)) * a.num_q_heads + kvh * G +
-                       rc % G) * D;
-      uint8_t *qt = smem + t * kAtoms * L::kQAtom;
-      // bf16 queries: the row is scaled by 2^e so that its largest magnitude
-      // lies in [2^14, 2^15), then rounded to fp16 (exact for every value down
-      // to 2^-31 of the largest: bf16 carries 8 significant bits, and fp16
-      // holds 8 bits at every magnitude from 2^-17 up), and 2^-e joins the
-      // row's softmax scale
-      float qf = 1.f;
-      if constexpr (kBf16) {
-        float mx = 0.f;
-        if (row_ok) {
-#pragma unroll 4
-          for (int ch = 0; ch < D / 8; ++ch) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(qrow + ch * 8);
+      // A row is read by D / 8 neighbouring lanes.  bf16 queries: the row is
+      // scaled by 2^e so that its largest magnitude lies in [2^14, 2^15), then
+      // rounded to fp16 (exact for every value down to 2^-31 of the largest:
+      // bf16 carries 8 significant bits, and fp16 holds 8 bits at every
+      // magnitude from 2^-17 up), and 2^-e joins the row's softmax scale.
+      const T *qbase = static_cast<const T *>(a.query) + tile_at + ch * 8;
+      int e_row = 0;
+#pragma unroll 1
+      for (int b = 0; b < 32; b += 8 * kRowsAt) {
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int off = __shfl_sync(kFullMask, row_off, b + i * kRowsAt + sub);
+          v[i] = off >= 0 ? *reinterpret_cast<const uint4 *>(qbase + static_cast<int64_t>(off) * D)
+                          : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if constexpr (kBf16) {
+            // the largest exponent: of the magnitudes' bits, two at a time
+            uint32_t mx = __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                                   __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
+#pragma unroll
+            for (int x = kLanes / 2; x > 0; x >>= 1)
+              mx = __vmaxu2(mx, __shfl_xor_sync(kFullMask, mx, x));
+            const int e = min(120, 14 + 127 - static_cast<int>(max(mx >> 23, (mx >> 7) & 0xffu)));
+            const float qf = ldexpf(1.f, e);
+            uint32_t w4[4];
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              const float2 f = Elem<T>::unpack(word_of(v, w));
-              mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+              const float2 f = Elem<T>::unpack(word_of(v[i], w));
+              w4[w] = Elem<__half>::pack(f.x * qf, f.y * qf);
             }
+            v[i] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+            const int mine = __shfl_sync(kFullMask, e, (lane % kRowsAt) * kLanes);
+            if ((lane - b) / kRowsAt == i && lane >= b) e_row = mine;
           }
+          *q_unit(b + i * kRowsAt + sub, ch) = v[i];
         }
-        const int e = min(120, 14 + 127 - static_cast<int>((__float_as_uint(mx) >> 23) & 0xffu));
-        qf = ldexpf(1.f, e);
-        sl2 = ldexpf(sl2, -e);
       }
-#pragma unroll
-      for (int ch = 0; ch < D / 8; ++ch) {
-        uint4 v = row_ok ? *reinterpret_cast<const uint4 *>(qrow + ch * 8)
-                         : make_uint4(0, 0, 0, 0);
-        if constexpr (kBf16) {
-          uint32_t w4[4];
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const float2 f = Elem<T>::unpack(word_of(v, w));
-            w4[w] = Elem<__half>::pack(f.x * qf, f.y * qf);
-          }
-          v = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-        }
-        *reinterpret_cast<uint4 *>(qt + (ch >> 3) * L::kQAtom + r * 128 +
-                                   (((ch & 7) ^ (r & 7)) << 4)) = v;
-      }
+      if constexpr (kBf16) sl2 = ldexpf(sl2, -e_row);
       fence_proxy_async_smem();
       mbar_arrive(q_ready);
     }
@@ -345,22 +358,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok_run && cluster == 1) {
         tc_fence_after();
         const float inv = l > 0.f ? a.out_scale / l : 0.f;  // times the V scale
-        T *orow = static_cast<T *>(a.out) +
-                  (static_cast<int64_t>(q0 + tok) * a.num_q_heads + kvh * G + rc % G) * D;
+        // through the Q tile, whose readers are done
 #pragma unroll 1
         for (int cb = 0; cb < D / 32; ++cb) {
           float o[32];
           tmem_ld32(lane_addr + kOCol + cb * 32, o);
           tmem_wait_ld();
-          if (row_ok) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              *reinterpret_cast<uint4 *>(orow + cb * 32 + q * 8) =
-                  make_uint4(Elem<T>::pack(o[q * 8 + 0] * inv, o[q * 8 + 1] * inv),
-                             Elem<T>::pack(o[q * 8 + 2] * inv, o[q * 8 + 3] * inv),
-                             Elem<T>::pack(o[q * 8 + 4] * inv, o[q * 8 + 5] * inv),
-                             Elem<T>::pack(o[q * 8 + 6] * inv, o[q * 8 + 7] * inv));
-          }
+          for (int q = 0; q < 4; ++q)
+            *q_unit(lane, cb * 4 + q) =
+                make_uint4(Elem<T>::pack(o[q * 8 + 0] * inv, o[q * 8 + 1] * inv),
+                           Elem<T>::pack(o[q * 8 + 2] * inv, o[q * 8 + 3] * inv),
+                           Elem<T>::pack(o[q * 8 + 4] * inv, o[q * 8 + 5] * inv),
+                           Elem<T>::pack(o[q * 8 + 6] * inv, o[q * 8 + 7] * inv));
+        }
+        __syncwarp();
+        T *obase = static_cast<T *>(a.out) + tile_at + ch * 8;
+#pragma unroll 4
+        for (int i = 0; i < 32 / kRowsAt; ++i) {
+          const int off = __shfl_sync(kFullMask, row_off, i * kRowsAt + sub);
+          if (off >= 0)
+            *reinterpret_cast<uint4 *>(obase + static_cast<int64_t>(off) * D) =
+                *q_unit(i * kRowsAt + sub, ch);
         }
       }
     }
@@ -617,7 +636,8 @@ cudaError_t launch_t(const PrefillArgs &a, const CUtensorMap &km, const CUtensor
   const int64_t steps = (static_cast<int64_t>(a.max_blocks_per_seq) << a.bs_log2) / kPairKeys;
   b.chunks = 1;
   while (b.chunks < 8 && 2 * b.chunks * ctas <= 152 && steps >= 8 * b.chunks) b.chunks *= 2;
-  return launch_clusters(b.chunks, kern, dim3(tiles * b.chunks, a.num_kv_heads, a.num_seqs),
+  return launch_clusters(b.chunks, kern, dim3(a.num_kv_heads * b.chunks, a.num_seqs, tiles),
+
                          dim3(kThreads), smem, stream, km, vm, b);
 }
 
