@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *raw_land = q_ready + 1;   // [4 warps][kRaw]: a warp's raw tiles of a step are in
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(raw_land + 4 * kRaw);
 
-  const int kvh = blockIdx.x / a.chunks, seq = blockIdx.y;
+  const int cluster = a.chunks, cluster_log2 = 31 - __clz(cluster);  // a power of two
+  const int kvh = blockIdx.x >> cluster_log2, seq = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.group;
   const int tpc = 2 * kTcRows / G;  // tokens per CTA
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) atomicOr(a.err, kErrBadLen);
     active = false;  // (in the whole cluster, here and below)
   }
-  const int cluster = a.chunks, rank = blockIdx.x % cluster;
+  const int rank = blockIdx.x & (cluster - 1);
   const int t_first = (gridDim.z - 1 - blockIdx.z) * tpc;
   if (t_first >= q_len) active = false;
   const int t_last = min(q_len, t_first + tpc) - 1;
@@ -171,8 +172,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int all0 = active ? (base_pos + last0 + kPairKeys) / kPairKeys : 0;
   const int all1 = active && last1 >= 0 ? (n_keys + kPairKeys - 1) / kPairKeys : 0;
   const int all = max(all0, all1);
-  const int step_base = static_cast<int>(static_cast<int64_t>(all) * rank / cluster);
-  const int n_steps = static_cast<int>(static_cast<int64_t>(all) * (rank + 1) / cluster) - step_base;
+  const int step_base = (all * rank) >> cluster_log2;  // (all < 2^26, rank < 8)
+  const int n_steps = ((all * (rank + 1)) >> cluster_log2) - step_base;
   const int steps0 = max(0, min(n_steps, all0 - step_base));
   const int steps1 = all1 > 0 ? n_steps : 0;
   const int n_sub = (n_keys + 15) / 16;
@@ -206,47 +207,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        ((warp & 3) * 32 + i) * 128 + (((c & 7) ^ (i & 7)) << 4));
     };
     {
-      // A row is read by D / 8 neighbouring lanes.  bf16 queries: the row is
-      // scaled by 2^e so that its largest magnitude lies in [2^14, 2^15), then
-      // rounded to fp16 (exact for every value down to 2^-31 of the largest:
-      // bf16 carries 8 significant bits, and fp16 holds 8 bits at every
-      // magnitude from 2^-17 up), and 2^-e joins the row's softmax scale.
       const T *qbase = static_cast<const T *>(a.query) + tile_at + ch * 8;
-      int e_row = 0;
-#pragma unroll 1
-      for (int b = 0; b < 32; b += 8 * kRowsAt) {
-        uint4 v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int off = __shfl_sync(kFullMask, row_off, b + i * kRowsAt + sub);
-          v[i] = off >= 0 ? *reinterpret_cast<const uint4 *>(qbase + static_cast<int64_t>(off) * D)
-                          : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 32 / kRowsAt; ++i) {
+        const int off = __shfl_sync(kFullMask, row_off, i * kRowsAt + sub);
+        // rows past the chunk: zeros (nothing read)
+        cp_async16(q_unit(i * kRowsAt + sub, ch),
+                   qbase + static_cast<int64_t>(max(off, 0)) * D, off >= 0);
+      }
+      cp_async_wait_all();
+      // bf16 queries: the row is scaled by 2^e so that its largest magnitude
+      // lies in [2^14, 2^15), then rounded to fp16 (exact for every value down
+      // to 2^-31 of the largest: bf16 carries 8 significant bits, and fp16
+      // holds 8 bits at every magnitude from 2^-17 up), and 2^-e joins the
+      // row's softmax scale.  Each thread rewrites its own row: a third of the
+      // instructions of rewriting what it fetched, which needs a maximum over
+      // lanes for every unit (4,500 cycles a CTA more).
+      if constexpr (kBf16) {
+        __syncwarp();
+        uint32_t mx = 0;  // the largest exponent: of the magnitudes' bits, two at a time
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = *q_unit(lane, c);
+          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                     __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
         }
+        const int e = min(120, 14 + 127 - static_cast<int>(max(mx >> 23, (mx >> 7) & 0xffu)));
+        const float qf = ldexpf(1.f, e);
+        sl2 = ldexpf(sl2, -e);
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = *q_unit(lane, c);
+          uint32_t w4[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if constexpr (kBf16) {
-            // the largest exponent: of the magnitudes' bits, two at a time
-            uint32_t mx = __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
-                                   __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
-#pragma unroll
-            for (int x = kLanes / 2; x > 0; x >>= 1)
-              mx = __vmaxu2(mx, __shfl_xor_sync(kFullMask, mx, x));
-            const int e = min(120, 14 + 127 - static_cast<int>(max(mx >> 23, (mx >> 7) & 0xffu)));
-            const float qf = ldexpf(1.f, e);
-            uint32_t w4[4];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const float2 f = Elem<T>::unpack(word_of(v[i], w));
-              w4[w] = Elem<__half>::pack(f.x * qf, f.y * qf);
-            }
-            v[i] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-            const int mine = __shfl_sync(kFullMask, e, (lane % kRowsAt) * kLanes);
-            if ((lane - b) / kRowsAt == i && lane >= b) e_row = mine;
+          for (int w = 0; w < 4; ++w) {
+            const float2 f = Elem<T>::unpack(word_of(v, w));
+            w4[w] = Elem<__half>::pack(f.x * qf, f.y * qf);
           }
-          *q_unit(b + i * kRowsAt + sub, ch) = v[i];
+          *q_unit(lane, c) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
         }
       }
-      if constexpr (kBf16) sl2 = ldexpf(sl2, -e_row);
       fence_proxy_async_smem();
       mbar_arrive(q_ready);
     }
