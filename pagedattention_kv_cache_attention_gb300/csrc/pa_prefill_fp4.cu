@@ -225,23 +225,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       // lanes for every unit (4,500 cycles a CTA more).
       if constexpr (kBf16) {
         __syncwarp();
+        uint4 v[D / 8];
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) v[c] = *q_unit(lane, c);
         uint32_t mx = 0;  // the largest exponent: of the magnitudes' bits, two at a time
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = *q_unit(lane, c);
-          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                     __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-        }
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v[c].x & 0x7fff7fffu, v[c].y & 0x7fff7fffu),
+                                     __vmaxu2(v[c].z & 0x7fff7fffu, v[c].w & 0x7fff7fffu)));
         const int e = min(120, 14 + 127 - static_cast<int>(max(mx >> 23, (mx >> 7) & 0xffu)));
         const float qf = ldexpf(1.f, e);
         sl2 = ldexpf(sl2, -e);
-#pragma unroll 4
+#pragma unroll
         for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = *q_unit(lane, c);
           uint32_t w4[4];
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            const float2 f = Elem<T>::unpack(word_of(v, w));
+            const float2 f = Elem<T>::unpack(word_of(v[c], w));
             w4[w] = Elem<__half>::pack(f.x * qf, f.y * qf);
           }
           *q_unit(lane, c) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
@@ -374,12 +374,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         T *obase = static_cast<T *>(a.out) + tile_at + ch * 8;
-#pragma unroll 4
-        for (int i = 0; i < 32 / kRowsAt; ++i) {
-          const int off = __shfl_sync(kFullMask, row_off, i * kRowsAt + sub);
-          if (off >= 0)
-            *reinterpret_cast<uint4 *>(obase + static_cast<int64_t>(off) * D) =
-                *q_unit(i * kRowsAt + sub, ch);
+#pragma unroll
+        for (int b = 0; b < 32; b += 8 * kRowsAt) {
+          uint4 v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = *q_unit(b + i * kRowsAt + sub, ch);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int off = __shfl_sync(kFullMask, row_off, b + i * kRowsAt + sub);
+            if (off >= 0) *reinterpret_cast<uint4 *>(obase + static_cast<int64_t>(off) * D) = v[i];
+          }
         }
       }
     }
