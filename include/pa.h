@@ -429,7 +429,10 @@ pa_status pa_gather_cache_fp4(void *key, void *value, int64_t key_stride, int64_
  * (at most 6 significant bits); both products run in fp16 with fp32
  * accumulation, k_scale joins the softmax scale and v_scale multiplies the
  * output; bf16 queries are carried in fp16 as pa_decode_fp8 does.  Other
- * arguments, partitions and workspace as pa_decode.
+ * arguments, partitions and workspace as pa_decode; m of a partial is a value
+ * that the partition's largest logit passes by at most 4 (base 2) in place of
+ * that logit itself, and l and o are relative to it, so that the join is the
+ * same.
  */
 pa_status pa_decode_fp4(void *out, const void *query,
                         const void *k_cache, const void *v_cache,
@@ -444,7 +447,9 @@ pa_status pa_decode_fp4(void *out, const void *query,
 
 /*
  * pa_prefill_fp4 -- pa_prefill over FP4 caches, the values as in pa_decode_fp4.
- * Arguments, shapes and error behaviour as pa_prefill_fp8.
+ * Arguments, shapes and error behaviour as pa_prefill_fp8; max_q_len (or
+ * max_blocks_per_seq * block_size, if that is less) above 65535 * (256 / group)
+ * tokens, group = num_q_heads / num_kv_heads: PA_ERR_UNSUPPORTED.
  */
 pa_status pa_prefill_fp4(void *out, const void *query, const int32_t *query_start,
                          const void *k_cache, const void *v_cache,

@@ -35,6 +35,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -117,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(raw_land + 4 * kRaw);
 
   const int cluster = a.chunks, cluster_log2 = 31 - __clz(cluster);  // a power of two
-  const int kvh = blockIdx.x >> cluster_log2, seq = blockIdx.y;
+  const int kvh = blockIdx.x >> cluster_log2, seq = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.group;
   const int tpc = 2 * kTcRows / G;  // tokens per CTA
@@ -157,7 +158,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     active = false;  // (in the whole cluster, here and below)
   }
   const int rank = blockIdx.x & (cluster - 1);
-  const int t_first = (gridDim.z - 1 - blockIdx.z) * tpc;
+  // a sequence's tiles start together, those with the most keys first, so that
+  // its K and V come from L2
+  const int t_first = (gridDim.y - 1 - blockIdx.y) * tpc;
   if (t_first >= q_len) active = false;
   const int t_last = min(q_len, t_first + tpc) - 1;
   const int base_pos = ctx - q_len;
@@ -485,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    (share0 / 16) * kRawSlot16<D>;
     const CUtensorMap *map = k_role ? &kmap : &vmap;
     const F4Widen<D> widen(lane, a.bs_log2, k_role ? L::kKAtom : L::kVAtom);
-    const uint64_t policy = l2_policy_evict_first();
+    const uint64_t policy = l2_policy_evict_normal();  // the chunk's other tiles read it too
     // block of the warp's tile l (its tiles are numbered over all steps)
     auto tile_block = [&](int l) -> int {
       const int key = (step_base + (l >> tsh)) * kPairKeys + share0 + (tsh ? (l & 1) * 16 : 0);
@@ -635,13 +638,16 @@ cudaError_t launch_t(const PrefillArgs &a, const CUtensorMap &km, const CUtensor
   // as many CTAs on a tile pair's keys as the SMs have room for, while each
   // keeps four steps of the longest context that the table can hold
   PrefillArgs b = a;
-  const int tpc = 2 * kTcRows / a.group, tiles = (a.max_q_len + tpc - 1) / tpc;
-  const int64_t ctas = static_cast<int64_t>(tiles) * a.num_kv_heads * a.num_seqs;
-  const int64_t steps = (static_cast<int64_t>(a.max_blocks_per_seq) << a.bs_log2) / kPairKeys;
+  const int tpc = 2 * kTcRows / a.group;
+  // (no chunk is longer than what the table can hold)
+  const int64_t room = static_cast<int64_t>(a.max_blocks_per_seq) << a.bs_log2;
+  b.max_q_len = static_cast<int>(std::min<int64_t>(a.max_q_len, std::max<int64_t>(room, 1)));
+  const int64_t tiles = (b.max_q_len - 1) / tpc + 1;
+  const int64_t ctas = tiles * a.num_kv_heads * a.num_seqs, steps = room / kPairKeys;
   b.chunks = 1;
   while (b.chunks < 8 && 2 * b.chunks * ctas <= 152 && steps >= 8 * b.chunks) b.chunks *= 2;
-  return launch_clusters(b.chunks, kern, dim3(a.num_kv_heads * b.chunks, a.num_seqs, tiles),
-
+  return launch_clusters(b.chunks, kern,
+                         dim3(a.num_kv_heads * b.chunks, static_cast<unsigned>(tiles), a.num_seqs),
                          dim3(kThreads), smem, stream, km, vm, b);
 }
 
