@@ -210,19 +210,17 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
 
   const int G = a.group;
   int ctx = a.context_lens[seq];
-  int q0 = seq, row0 = 0, n_rows = G, base_pos = 0;  // the chunk's first row and rows, its position
+  int q0 = seq, n_rows = G, base_pos = 0;  // the chunk's first token, its rows, its position
   if constexpr (kChunk) {
     q0 = a.query_start[seq];
     const int q_len = a.query_start[seq + 1] - q0;
-    row0 = 8 * NT * (blockIdx.x / cluster);
     n_rows = q_len * G;
     base_pos = ctx - q_len;
     if (q_len < 0 || ctx < q_len || ctx > a.max_blocks_per_seq * BS || q_len > a.max_q_len) {
-      if (threadIdx.x == 0 && row0 == 0 && kvh == 0) atomicOr(a.err, kErrBadLen);
+      if (threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0) atomicOr(a.err, kErrBadLen);
       return;  // (the whole cluster)
     }
-    if (row0 >= n_rows) return;
-    ctx = base_pos + (min(n_rows, row0 + 8 * NT) - 1) / G + 1;  // keys of the CTA's last row
+    if (n_rows == 0) return;  // (n_rows <= 8 NT: the launch has NT for max_q_len)
   } else if (ctx < 0 || ctx > a.max_blocks_per_seq * BS || ctx > a.max_context_len) {
     if (threadIdx.x == 0 && part == 0 && kvh == 0) atomicOr(a.err, kErrBadLen);
     ctx = 0;
@@ -278,7 +276,7 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
   float sl[NT][2];  // softmax scale of the lane's columns 2c and 2c + 1
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int col = row0 + 8 * nt + g;
+    const int col = 8 * nt + g;
     const T *qrow = static_cast<const T *>(a.query) +
                     (static_cast<int64_t>(q0 + (kChunk ? col / G : 0)) * a.num_q_heads + kvh * G +
                      (kChunk ? col % G : col)) * D;
@@ -410,7 +408,7 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       // a row's own token (of columns 2c and 2c + 1) within the step
-      const int col = row0 + 8 * nt + 2 * c;
+      const int col = 8 * nt + 2 * c;
       const int own0 = kChunk && masked ? own + col / G : 0;
       const int own1 = kChunk && masked ? own + (col + 1) / G : 0;
       // z = scores + (b0, b1); tokens that do not count get -inf
@@ -559,7 +557,7 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
     const int step_tok = step_token(k);
     // (in a chunk every row sees the step's last token if its first row does)
     if (!bad && step_tok >= t_begin &&
-        step_tok + 32 <= (kChunk ? base_pos + row0 / G + 1 : t_end)) {
+        step_tok + 32 <= (kChunk ? base_pos + 1 : t_end)) {
       step(stage, false, 0xffffffffu, 0);
     } else {
       const int tok = step_tok + lane;
@@ -643,7 +641,7 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
     put_acc<D>(wacc + warp * 8 * kAccStride<D>, acc[nt], unshift, unshift, g, c);
     __syncthreads();
     constexpr int kChunks = D / 8;
-    const int cols = min(8, n_rows - row0 - 8 * nt);
+    const int cols = min(8, n_rows - 8 * nt);
     for (int item = threadIdx.x; item < cols * kChunks; item += NW * 32) {
       const int h = item / kChunks, ch = item % kChunks;
       float M = NEG_INF;
@@ -668,7 +666,7 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
         }
         continue;
       }
-      const int col = row0 + 8 * nt + h;
+      const int col = 8 * nt + h;
       const int64_t row = static_cast<int64_t>(q0 + (kChunk ? col / G : 0)) * a.num_q_heads +
                           kvh * G + (kChunk ? col % G : col);
       const float inv = L > 0.f ? a.out_scale / L : 0.f;
@@ -694,17 +692,17 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
     // the cluster's CTAs share the rows of the join out
     cluster_sync();
     constexpr int kChunks = D / 8;
-    const int cols = min(8 * NT, n_rows - row0);
+    const int cols = min(8 * NT, n_rows);
     for (int item = threadIdx.x + rank * NW * 32; item < cols * kChunks;
          item += NW * 32 * cluster) {
-      const int j = item / kChunks, ch = item % kChunks;
+      const int col = item / kChunks, ch = item % kChunks;
       float M = NEG_INF;
       for (int r = 0; r < cluster; ++r)
-        M = fmaxf(M, ld_cluster_f2(cluster_addr(cl_ml + j * 2, r)).x);
+        M = fmaxf(M, ld_cluster_f2(cluster_addr(cl_ml + col * 2, r)).x);
       float L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       for (int r = 0; r < cluster; ++r) {
-        const float2 ml = ld_cluster_f2(cluster_addr(cl_ml + j * 2, r));
-        const uint32_t src = cluster_addr(cl_o + j * D + ch * 8, r);
+        const float2 ml = ld_cluster_f2(cluster_addr(cl_ml + col * 2, r));
+        const uint32_t src = cluster_addr(cl_o + col * D + ch * 8, r);
         const float4 x = ld_cluster_f4(src), y = ld_cluster_f4(src + 16);
         const float f = exp2f(ml.x - M);
         L += ml.y * f;
@@ -717,7 +715,6 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
         o[6] += y.z * f;
         o[7] += y.w * f;
       }
-      const int col = row0 + j;
       const int64_t row = static_cast<int64_t>(q0 + (kChunk ? col / G : 0)) * a.num_q_heads +
                           kvh * G + (kChunk ? col % G : col);
       const float inv = L > 0.f ? a.out_scale / L : 0.f;
@@ -782,12 +779,11 @@ template <typename T, int D, int BS>
 cudaError_t launch_chunk_t(DecodeArgs a, const CUtensorMap &km, const CUtensorMap &vm,
                            cudaStream_t stream) {
   const int rows = a.max_q_len * a.group;
-  const int groups = (rows + 23) / 24;
   auto launch = [&](auto tiles) {
     constexpr int NT = decltype(tiles)::value;
-    a.cluster = cluster_of(a, static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * groups, 4,
+    a.cluster = cluster_of(a, static_cast<int64_t>(a.num_seqs) * a.num_kv_heads, 4,
                            ctas_per_sm(NT));
-    return launch_rows<T, D, BS, 4, 2, Rows::kChunk, NT>(a, km, vm, groups * a.cluster, stream);
+    return launch_rows<T, D, BS, 4, 2, Rows::kChunk, NT>(a, km, vm, a.cluster, stream);
   };
   if (rows <= 8) return launch(std::integral_constant<int, 1>{});
   if (rows <= 16) return launch(std::integral_constant<int, 2>{});

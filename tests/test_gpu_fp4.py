@@ -276,6 +276,18 @@ def test_decode_long_context_through_the_reduce(pa, dtype, bs):
     assert pa.pa_device_errors() == 0
 
 
+@pytest.mark.parametrize("G,d,bs,dtype", [(1, 128, 16, "fp16"), (4, 64, 32, "bf16"),
+                                          (8, 128, 32, "fp16"), (5, 64, 16, "bf16")])
+@pytest.mark.parametrize("long", [600, 1100, 4100])
+def test_decode_empty_and_short_sequences_beside_a_long_one(pa, G, d, bs, dtype, long):
+    """Unsplit: the work is split for the table's room, which most sequences do not fill."""
+    b = Batch(40 + G, [long, 0, 1, 33, 64, 257], 2, G, d, bs, dtype, ks=2.0, vs=0.3)
+    out = b.decode(pa, 0)
+    b.check(out)
+    assert (out[1] == 0).all()
+    assert pa.pa_device_errors() == 0
+
+
 def test_decode_workspace_reused_across_shapes(pa):
     a = Batch(33, [900, 1500, 3], 2, 4, 128, 16, "fp16")
     b = Batch(34, [700], 1, 8, 64, 32, "bf16")
@@ -560,6 +572,29 @@ def test_serving_steps_captured_and_replayed(pa):
         clear()
         g.replay()
         check()
+
+
+def test_calls_at_once_on_two_streams(pa):
+    """Two batches, each on a stream and with a workspace of its own."""
+    both = []
+    for i, (lens, ps) in enumerate((([3000, 700, 5, 1900], 256), ([900] * 12, 64))):
+        b = Batch(60 + i, lens, 2, 4, 128, 16, "fp16")
+        p = Batch(62 + i, [400, 1300, 300], 2, 4, 128, 16, "bf16", q_lens=[200, 6, 300])
+        dec, pre = b.gpu(), p.gpu()
+        ws = pa.new_decode_workspace(len(lens), 8, 128, 3000, ps)
+        outs = [torch.full_like(x.q, float("nan"), device="cuda") for x in (b, p)]
+        both.append((b, p, dec, pre, ws, ps, outs, b.q.cuda(), p.q.cuda(), dev(p.start),
+                     torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for b, p, dec, pre, ws, ps, outs, q, pq, start, st in both:
+            pa.pa_decode_fp4(outs[0], q, *dec, b.scale, 1.0, 1.0, 3000, ps, ws, st)
+            pa.pa_prefill_fp4(outs[1], pq, start, *pre, p.scale, 1.0, 1.0, 300, st)
+    torch.cuda.synchronize()
+    for b, p, dec, pre, ws, ps, outs, *_ in both:
+        b.check(outs[0])
+        p.check(outs[1])
+    assert pa.pa_device_errors() == 0
 
 
 def test_decode_makes_its_own_workspace_on_the_calls_stream(pa):
