@@ -17,14 +17,14 @@
 //  * The issuing warps run their loops whole and elect a lane for the tcgen05
 //    instructions: operands then stay in uniform registers (a product's issue
 //    took 113 cycles in a single-lane branch, 65 like this).
-// What bounds it: a step takes 1,790 cycles; the shared memory is busy for 1,430
+// What bounds it: a step takes 1,730 cycles; the shared memory is busy for 1,430
 // of them (Q's 64 KB, K's and V's 32 KB each, read by the products, 32 KB
 // written by the widening), a tile's softmax for 1,300.  Measured: 8,111-token
-// prompt, 64 query / 8 KV heads, head_dim 128, bf16: 975 us, 1.10 PFLOP/s (0.57
-// of cuBLAS bf16; the kernel with separate P columns 1,022 us).  Products of 128
-// keys (a third less of Q's traffic) with the scores' buffer whole took 1,144:
-// a tile's next scores then wait for its last P V.  Two threads a row took
-// 1,207.
+// prompt, 64 query / 8 KV heads, head_dim 128, bf16: 833 us, 1.29 PFLOP/s (0.67
+// of cuBLAS bf16).  In an earlier state of this kernel (975 us) separate columns
+// for P took 1,022; products of 128 keys (a third less of Q's traffic) with the
+// scores' buffer whole 1,144, since a tile's next scores then wait for its last
+// P V; two threads a row 1,207.
 //
 // Where the call has too few CTAs to fill the SMs, a cluster of up to eight
 // shares a tile pair's keys: each CTA takes a run of the steps, leaves its O,
@@ -67,7 +67,7 @@ constexpr float kPShift = 11.f, kGrowth = 4.f;
 #endif
 
 // First warps of the roles (the widening first, which the schedulers then
-// favour: 975 us against 983 with it last).
+// favour: 975 us against 983 with it last, then).
 constexpr int kLoad0 = 0, kSoft0 = 4, kIssue0 = 12;
 
 // Shared memory.  An atom is 64 dimensions of 128-byte rows.
@@ -289,10 +289,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // loaded now, used at the end of the step: its latency hides behind the softmax
       const int bt_next = n + 1 < my_steps ? entry(n + 1) : -1;
       const int key0 = (step_base + n) * kPairKeys;
-      if (!(row_ok && key0 + kPairKeys - 1 <= pos && vmask == kAllSub)) {
+      // rows past the chunk (zeros, never stored) attend like the last one, so that
+      // they do not send their warp through the masking at every step (255 of 256
+      // rows in use: 143 us became 118)
+      if (!(key0 + kPairKeys - 1 <= pos && vmask == kAllSub)) {
 #pragma unroll
         for (int c = 0; c < kPairKeys; ++c) {
-          const bool ok = row_ok && key0 + c <= pos && ((vmask >> (c >> 4)) & 1u);
+          const bool ok = key0 + c <= pos && ((vmask >> (c >> 4)) & 1u);
           sv[c] = ok ? sv[c] : -INFINITY;
         }
       }

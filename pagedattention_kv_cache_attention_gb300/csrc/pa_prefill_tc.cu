@@ -471,12 +471,17 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
         if (n + 1 < my_steps && lane < kSub && u < n_sub) bt_next = table_entry(u);
       }
       const int key0 = n * kPairKeys;
-      const bool full_step = row_ok && key0 + kPairKeys - 1 <= pos && vmask == kAllSub;
+      // FP4: rows past the chunk (zeros, never stored) attend like the last one,
+      // so that they do not send their warp through the masking at every step
+      // (64 sequences, 28 rows: 121 to 107 us;
+      // at head_dim 64 107 to 75)
+      const bool row_in = F4 || row_ok;
+      const bool full_step = row_in && key0 + kPairKeys - 1 <= pos && vmask == kAllSub;
       if (!full_step) {
 #pragma unroll
         for (int c = 0; c < kPairKeys; ++c) {
           const int key = key0 + c;
-          const bool ok = row_ok && key <= pos && ((vmask >> (c >> 4)) & 1u);
+          const bool ok = row_in && key <= pos && ((vmask >> (c >> 4)) & 1u);
           sv[c] = ok ? sv[c] : -INFINITY;
         }
       }
@@ -1090,10 +1095,10 @@ cudaError_t launch_prefill_tc_d(const PrefillArgs &a, const CUtensorMap &km,
   constexpr int SK = PA_PREFILL_SOLO_KSTAGES, SV = PA_PREFILL_SOLO_VSTAGES;
   if (kv == Kv::kFp4) {
     // Up to 64 rows run two CTAs to an SM where there are enough of them (64
-    // sequences of 512 to 4,096 tokens, 8 KV heads, 28 to 64 rows: 110 to 122
-    // us against 145 with two tiles); more rows, and few CTAs, in the two-tile
-    // kernel, whose steps are shorter (80 rows of the same batch 146 us; in a
-    // one-tile kernel 176), and which shares a sequence's keys in a cluster.
+    // sequences of 512 to 4,096 tokens, 8 KV heads, 28 to 64 rows: 107 to 111
+    // us, 127 with two tiles); more rows, and few CTAs, in the two-tile kernel,
+    // whose steps are shorter (80 rows of the same batch 127 us; a one-tile
+    // kernel took 176), and which shares a sequence's keys in a cluster.
     if (static_cast<int64_t>(a.max_q_len) * a.group > 64 ||
         static_cast<int64_t>(a.num_seqs) * a.num_kv_heads < 2 * 152)
       return launch_prefill_fp4(a, km, vm, D, dtype, stream);
