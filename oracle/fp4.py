@@ -114,7 +114,11 @@ def attend(q, K, V, scale: float, ends) -> np.ndarray:
         top = z.max(-1, keepdims=True, initial=-np.inf)
         e = np.exp(z - np.where(np.isinf(top), 0, top))
         l = e.sum(-1, keepdims=True)
-        out[:, h] = (e / np.where(l == 0, 1, l)) @ V[h // G]
+        v = V[h // G]
+        gone = np.isnan(v)
+        out[:, h] = (e / np.where(l == 0, 1, l)) @ np.where(gone, 0, v)
+        # a NaN of V reaches the rows that see its key, and no others
+        out[:, h][seen.astype(float) @ gone > 0] = np.nan
     return out
 
 

@@ -185,6 +185,11 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
   const int g = lane >> 2, c = lane & 3;
   uint8_t *my_stages = smem + warp * S * kStep;
   uint64_t *my_bars = bars + warp * S;
+  // kChunk: NaNs of V at keys that not every row attends to: zeros in the
+  // products, so that they do not reach the rows before them, and put back at
+  // the end.  [warp][group]: the least such key, from the chunk's first token on.
+  int *nan_key = reinterpret_cast<int *>(bars + NW * S);
+  if (kChunk && lane < 8) nan_key[warp * 8 + lane] = 0x7fffffff;
   if (lane == 0) {
 #pragma unroll
     for (int s = 0; s < S; ++s) mbar_init(&my_bars[s], 1);
@@ -488,6 +493,19 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
         s1 = (mask >> (16 * h + t1)) & 1u ? s1 : 0;
         s2 = (mask >> (16 * h + t0 + 8)) & 1u ? s2 : 0;
         s3 = (mask >> (16 * h + t1 + 8)) & 1u ? s3 : 0;
+        if constexpr (kChunk) {
+          auto drop_nan = [&](uint32_t &sc, int at) {
+            if ((sc & 0x7fu) == 0x7fu) {
+              sc = 0;
+              atomicMin(&nan_key[warp * 8 + (D == 128 ? g : g >> 1)], at - own);
+            }
+          };
+          drop_nan(s0, 16 * h + t0);
+          drop_nan(s1, 16 * h + t1);
+          drop_nan(s2, 16 * h + t0 + 8);
+          drop_nan(s3, 16 * h + t1 + 8);
+          __syncwarp();
+        }
       }
       const uint32_t g01 = e4m3x2_lo_to_f16x2(s0 | (s1 << 8));
       const uint32_t g23 = e4m3x2_lo_to_f16x2(s2 | (s3 << 8));
@@ -656,6 +674,15 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] += src[acc_place<D>(ch * 8 + e)] * f;
       }
+      if constexpr (kChunk) {
+        int first_nan = nan_key[ch / 2];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) first_nan = min(first_nan, nan_key[w * 8 + ch / 2]);
+        if (first_nan <= (8 * nt + h) / G) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = __int_as_float(0x7fffffff);
+        }
+      }
       if (!kParts && cluster > 1) {
         float4 *dst = reinterpret_cast<float4 *>(cl_o + (nt * 8 + h) * D + ch * 8);
         dst[0] = make_float4(o[0], o[1], o[2], o[3]);
@@ -735,7 +762,7 @@ template <typename T, int D, int BS, int NW, int S, Rows ROWS, int NT>
 cudaError_t launch_rows(const DecodeArgs &a, const CUtensorMap &km, const CUtensorMap &vm,
                         unsigned grid_x, cudaStream_t stream) {
   constexpr size_t stages = static_cast<size_t>(NW) * S * 2 * Fp4Shape<D, BS>::kUnit;
-  constexpr size_t smem = 1024 + stages + NW * S * 8;
+  constexpr size_t smem = 1024 + stages + NW * S * 8 + (ROWS == Rows::kChunk ? NW * 8 * 4 : 0);
   static_assert((static_cast<size_t>(NW) * (kAccStride<D> + 2) + NT * (D + 2)) * 32 + 16 <= stages,
                 "merge buffers and the join flag must fit in the stage area");
   static_assert(smem <= 227 * 1024, "shared memory");

@@ -20,7 +20,7 @@
 // What bounds it: a step takes 1,730 cycles; the shared memory is busy for 1,430
 // of them (Q's 64 KB, K's and V's 32 KB each, read by the products, 32 KB
 // written by the widening), a tile's softmax for 1,300.  Measured: 8,111-token
-// prompt, 64 query / 8 KV heads, head_dim 128, bf16: 833 us, 1.29 PFLOP/s (0.67
+// prompt, 64 query / 8 KV heads, head_dim 128, bf16: 841 us, 1.28 PFLOP/s (0.67
 // of cuBLAS bf16).  In an earlier state of this kernel (975 us) separate columns
 // for P took 1,022; products of 128 keys (a third less of Q's traffic) with the
 // scores' buffer whole 1,144, since a tile's next scores then wait for its last
@@ -85,7 +85,7 @@ template <int D> struct Layout {
   static constexpr int kRawOff = kVOff + kSV * kAtoms * kVAtom;
   static constexpr int kBarOff = kRawOff + 2 * kRaw * kRawStep;
   static constexpr int kBars = 2 * kSK + 2 * kSV + 4 + 4 + 4 + 1 + 4 * kRaw;
-  static constexpr size_t kSmem = 1024 + kBarOff + kBars * 8 + 16;
+  static constexpr size_t kSmem = 1024 + kBarOff + kBars * 8 + 16 + (D / 16 + 1) * 4;
   // join in a cluster: O [tile][row][D] fp32 over the idle Q and stages, 16-byte
   // unit u of row r at u ^ (r & 7); then (maximum, sum) [tile][row]
   static constexpr int kMlOff = 2 * kTcRows * D * 4;
@@ -116,6 +116,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *q_ready = pv_done + 4;
   uint64_t *raw_land = q_ready + 1;   // [4 warps][kRaw]: a warp's raw tiles of a step are in
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(raw_land + 4 * kRaw);
+  // NaNs of V at keys that not every row attends to: zeros in the products, so
+  // that they do not reach the rows before them, and put back at the end
+  int *nan_key = reinterpret_cast<int *>(tmem_slot + 4);
 
   const int cluster = a.chunks, cluster_log2 = 31 - __clz(cluster);  // a power of two
   const int kvh = blockIdx.x >> cluster_log2, seq = blockIdx.z;
@@ -140,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_ready, 2 * kTcRows);
     for (int s = 0; s < 4 * kRaw; ++s) mbar_init(&raw_land[s], 1);
     fence_barrier_init();
+    for (int i = 0; i <= D / 16; ++i) nan_key[i] = 0x7fffffff;
   }
   if (warp == kIssue0) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
@@ -370,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float o[32];
           tmem_ld32(lane_addr + kOCol + cb * 32, o);
           tmem_wait_ld();
+          if (nan_key[D / 16] <= pos) put_nans(o, nan_key, cb, pos);
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             *q_unit(lane, cb * 4 + q) =
@@ -543,11 +548,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint8_t *st = (k_role ? smem + L::kKOff + s * kAtoms * L::kKAtom
                             : smem + L::kVOff + s * kAtoms * L::kVAtom) + share0 * 128;
       const uint8_t *from = raw + rs * L::kRawStep;
+      const int key0 = (step_base + m) * kPairKeys;
       // V rows that must not contribute become zeros; K's are masked by the softmax
-      if (k_role || (ok == (1u << (1 << tsh)) - 1 && past >= kShare))
-        widen(from, st, [](int) { return true; });
+      if (k_role || (ok == (1u << (1 << tsh)) - 1 && key0 + kPairKeys - 1 <= base_pos + t_first))
+        widen(from, st, [](int, uint32_t sc) { return sc; });
       else
-        widen(from, st, [&](int r) { return r < past && ((ok >> (r >> a.bs_log2)) & 1u); });
+        widen(from, st, [&](int r, uint32_t sc) {
+          return r < past && ((ok >> (r >> a.bs_log2)) & 1u)
+                     ? F4Widen<D>::drop_nans(sc, lane, key0 + share0 + r, nan_key)
+                     : 0u;
+        });
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full);
@@ -572,12 +582,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t addr =
           tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * 256 + kOCol;
       float4 *row = reinterpret_cast<float4 *>(smem + (t * kTcRows + r) * D * 4);
+      const int pos = base_pos + t_first + (t * kTcRows + r) / G;
       tc_fence_after();
 #pragma unroll 1
       for (int cb = 0; cb < D / 32; ++cb) {
         float o[32];
         tmem_ld32(addr + cb * 32, o);
         tmem_wait_ld();
+        if (nan_key[D / 16] <= pos) put_nans(o, nan_key, cb, pos);
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           row[(cb * 8 + q) ^ (r & 7)] =

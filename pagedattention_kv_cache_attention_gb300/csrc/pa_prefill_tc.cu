@@ -99,7 +99,8 @@ struct PairLayout {
   // + the landing barriers (FP8: SK + SV; FP4: kRaw for each of four warps)
   // and the V sub-tile masks (SV words)
   static constexpr int kBars = 2 * SK + 2 * SV + 1 + 2 + 2 + 4 + 4 + 1 + SK + SV + 4 * kRaw;
-  static constexpr size_t kSmem = 1024 + kBarOff + kBars * 8 + SV * 4 + 16;
+  static constexpr size_t kSmem =
+      1024 + kBarOff + kBars * 8 + SV * 4 + 16 + (KV == Kv::kFp4 ? (D / 16 + 1) * 4 : 0);
 };
 
 // FP8 E4M3 caches: a step's codes (64 rows of D bytes, in the pool map's
@@ -230,6 +231,9 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
   // member, the member count and the first member's sequence
   int *px_first = reinterpret_cast<int *>(tmem_slot + 4);
   int *px_ctl = px_first + kTcRows;
+  // FP4: NaNs of V at keys that not every row attends to: zeros in the products,
+  // so that they do not reach the rows before them, and put back at the end
+  int *nan_key = reinterpret_cast<int *>(tmem_slot + 4);
 
   if (tid == 0) {
     for (int s = 0; s < SK; ++s) {
@@ -254,6 +258,8 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
     for (int s = 0; s < SV; ++s) mbar_init(&v_land[s], 1);
     for (int s = 0; s < 4 * L::kRaw; ++s) mbar_init(&raw_land[s], 1);
     fence_barrier_init();
+    if constexpr (F4)
+      for (int i = 0; i <= D / 16; ++i) nan_key[i] = 0x7fffffff;
   }
   if (warp == kIssue0) tmem_alloc(tmem_slot, 256 * TILES);
   tc_fence_before();
@@ -611,6 +617,8 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
           float o[32];
           tmem_ld32(lane_addr + kOCol + cb * 32, o);
           tmem_wait_ld();
+          if constexpr (F4)
+            if (nan_key[D / 16] <= pos) put_nans(o, nan_key, cb, pos);
           if (row_ok) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -798,18 +806,24 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
         }
         const uint32_t ok = (loaded >> (4 * rs)) & 15u;
         const int past = n_keys - m * kPairKeys;  // first row that must not contribute
+        const int key0 = m * kPairKeys;
         // K rows that must not contribute are masked by the softmax
-        const bool all = k_role || (ok == (1u << tiles) - 1 && past >= share0 + kShare);
+        const bool all = k_role || (ok == (1u << tiles) - 1 &&
+                                    key0 + kPairKeys - 1 <= base_pos + t_first);
         uint8_t *st = ring + s * kAtoms * kPairKvAtom + share0 * 128;
         const uint8_t *from = raw + rs * L::kRawStep + (share0 / 16) * kRawSlot16<D>;
 #pragma unroll 1
         for (int r0 = 0; r0 < kShare; r0 += 32) {
           const int first = r0;
           if (all)
-            widen(from + (r0 / 16) * kRawSlot16<D>, st + r0 * 128, [](int) { return true; });
+            widen(from + (r0 / 16) * kRawSlot16<D>, st + r0 * 128,
+                  [](int, uint32_t sc) { return sc; });
           else
-            widen(from + (r0 / 16) * kRawSlot16<D>, st + r0 * 128, [&](int r) {
-              return share0 + first + r < past && ((ok >> ((first + r) >> a.bs_log2)) & 1u);
+            widen(from + (r0 / 16) * kRawSlot16<D>, st + r0 * 128, [&](int r, uint32_t sc) {
+              const int at = share0 + first + r;
+              return at < past && ((ok >> ((first + r) >> a.bs_log2)) & 1u)
+                         ? F4Widen<D>::drop_nans(sc, lane, key0 + at, nan_key)
+                         : 0u;
             });
         }
         fence_proxy_async_smem();

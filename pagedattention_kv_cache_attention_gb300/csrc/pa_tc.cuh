@@ -127,10 +127,24 @@ template <int D> struct F4Widen {
     scale1 = bs16 ? kRawSlot16<D> + 16 * (D / 2) : 32 * (D / 2) + D;
   }
 
-  // rows 0..31 of raw to rows 0..31 at st; rows that keep(row) refuses get a
-  // zero scale, and with it zeros: a code is always finite
-  template <typename Keep>
-  __device__ __forceinline__ void operator()(const uint8_t *raw, uint8_t *st, Keep keep) const {
+  // The lane's pair of scales (of groups 2 u and 2 u + 1, u = lane % kPerRow)
+  // without NaNs, which are noted: nan[group] becomes the least key with a NaN
+  // scale in the group, nan[D / 16] that of all groups.
+  static __device__ __forceinline__ uint32_t drop_nans(uint32_t sc, int lane, int key, int *nan) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (((sc >> (8 * i)) & 0x7fu) == 0x7fu) {
+        sc &= ~(0xffu << (8 * i));
+        atomicMin(&nan[2 * (lane % kPerRow) + i], key);
+        atomicMin(&nan[D / 16], key);
+      }
+    return sc;
+  }
+
+  // rows 0..31 of raw to rows 0..31 at st, with the scales fix(row, pair); a
+  // scale of zero makes zeros: a code is always finite
+  template <typename Fix>
+  __device__ __forceinline__ void operator()(const uint8_t *raw, uint8_t *st, Fix fix) const {
     uint32_t w[2][kPasses][4], sc[2][kPasses];
 #pragma unroll
     for (int q = 0; q < 2; ++q)
@@ -147,7 +161,7 @@ template <int D> struct F4Widen {
 #pragma unroll
       for (int p = 0; p < kPasses; ++p) {
         const int r0 = 16 * q + p * kRows;
-        const uint32_t s2 = e4m3x2_lo_to_f16x2(keep(r0 + row) ? sc[q][p] : 0u);
+        const uint32_t s2 = e4m3x2_lo_to_f16x2(fix(r0 + row, sc[q][p]));
         const uint32_t lo = __byte_perm(s2, 0, sel_lo), hi = __byte_perm(s2, 0, sel_hi);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -161,5 +175,17 @@ template <int D> struct F4Widen {
       }
   }
 };
+
+// 32 output values of a row, from dimension 32 cb on: NaN where the row attends
+// to a key whose V has a NaN scale there (what drop_nans noted; pos: the row's
+// last key).
+__device__ __forceinline__ void put_nans(float (&o)[32], const int *nan, int cb, int pos) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (nan[2 * cb + i] <= pos) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[16 * i + e] = __int_as_float(0x7fffffff);
+    }
+}
 
 }  // namespace pa

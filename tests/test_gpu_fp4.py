@@ -411,6 +411,44 @@ def test_prefill_keeps_the_mass_of_a_long_faint_tail(pa):
     b.check(b.prefill(pa))
 
 
+@pytest.mark.parametrize("G,q,d,bs,dtype,n", [
+    (4, 2, 128, 16, "fp16", 3), (4, 5, 128, 32, "bf16", 3), (3, 7, 64, 16, "fp16", 3),
+    (2, 12, 64, 32, "bf16", 80), (1, 24, 128, 16, "bf16", 170),
+    (4, 12, 128, 16, "fp16", 160), (2, 30, 64, 32, "bf16", 160), (8, 8, 128, 32, "bf16", 155),
+    (4, 20, 128, 16, "bf16", 3), (8, 70, 64, 16, "fp16", 3), (2, 150, 128, 32, "fp16", 2),
+    (5, 60, 128, 16, "fp16", 100), (1, 300, 64, 32, "bf16", 80)])
+def test_prefill_nan_reaches_only_the_rows_that_attend_to_it(pa, G, q, d, bs, dtype, n):
+    """NaN groups of K and of V among the chunk's own tokens and before them:
+    the rows before a NaN keep their values, a row that attends to a NaN of V is
+    NaN in that group's dimensions alone, one that attends to a NaN of K in all."""
+    rng = np.random.default_rng(G * 1000 + q)
+    lens = rng.integers(q, q + 150, n)
+    lens[0] = 700 + q
+    b = Batch(56, lens, 2, G, d, bs, dtype, ks=0.5, vs=2.0, q_lens=[q] * n)
+    vs, ks = F.views(b.vc, bs, d)[1], F.views(b.kc, bs, d)[1]
+    for i in range(n):
+        at = lens[i] - q + rng.integers(0, q, 2)           # two of the chunk's tokens
+        for j, h, group in ((at[0], 0, rng.integers(d // 16)), (at[1], 0, rng.integers(d // 16))):
+            vs[b.tables[i, j // bs], h, j % bs, group] = NAN_SCALE
+        if i % 3 == 0 and lens[i] > q:                     # one before the chunk
+            j = rng.integers(0, lens[i] - q)
+            vs[b.tables[i, j // bs], 1, j % bs, rng.integers(d // 16)] = NAN_SCALE
+        if i % 4 == 1:                                     # a K of the chunk
+            j = lens[i] - 1 - rng.integers(0, q)
+            ks[b.tables[i, j // bs], 1, j % bs, 0] = NAN_SCALE
+    with np.errstate(invalid="ignore"):
+        ref, A = b.reference(), b.reference(True)
+    out = b.prefill(pa)
+    got = f64(out)
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    assert np.isnan(ref).any() and not np.isnan(ref).all()
+    eps = torch.finfo(TYPES[dtype]).eps / 2
+    tol = eps * np.abs(ref) * (1 + 2 ** -8) + A * (2 ** -11 + 2 ** -12) + 2.0 ** -24
+    live = ~np.isnan(ref)
+    assert (np.abs(got - ref)[live] <= tol[live]).all()
+    assert pa.pa_device_errors() == 0
+
+
 @pytest.mark.parametrize("q,d", [(300, 128), (20, 128), (200, 64), (10, 64)])
 def test_prefill_bad_block_and_bad_length(pa, q, d):
     b = Batch(53, [700, 1400, 900], 2, 4, d, 16, "fp16", q_lens=[q, q, q])
