@@ -320,6 +320,44 @@ def test_decode_keeps_the_mass_of_a_long_faint_tail(pa, dtype):
     b.check(b.decode(pa, 512))
 
 
+def same_with_nans(b, out):
+    """out against the reference, NaN where the reference is and nowhere else."""
+    with np.errstate(invalid="ignore"):
+        ref, A, got = b.reference(), b.reference(True), f64(out)
+    assert np.array_equal(np.isnan(got), np.isnan(ref))
+    live = ~np.isnan(ref)
+    eps = torch.finfo(TYPES[b.dtype]).eps / 2
+    tol = eps * np.abs(ref) * (1 + 2 ** -8) + A * (2 ** -11 + 2 ** -12) + 2.0 ** -24
+    assert (np.abs(got - ref)[live] <= tol[live]).all()
+    return np.isnan(ref)
+
+
+@pytest.mark.parametrize("ps", [0, 16, 64, 512])
+@pytest.mark.parametrize("G,d,bs,dtype", [(4, 128, 16, "fp16"), (3, 64, 32, "bf16")])
+def test_decode_nans_stay_where_they_belong(pa, ps, G, d, bs, dtype):
+    """A NaN group of V, of K, and a NaN in one head's query."""
+    b = Batch(37, [900, 1300, 40, 700], 2, G, d, bs, dtype)
+    for i, j, cache in ((0, 899, b.vc), (1, 5, b.kc), (1, 1290, b.vc), (2, 17, b.vc)):
+        F.views(cache, bs, d)[1][b.tables[i, j // bs], i % 2, j % bs, 1] = NAN_SCALE
+    b.q[3, G - 1, 7] = float("nan")
+    out = b.decode(pa, ps)
+    nans = same_with_nans(b, out)
+    assert nans.any() and not nans[0].all() and not nans[3, G].any()
+    assert pa.pa_device_errors() == 0
+
+
+@pytest.mark.parametrize("G,q,d,n", [(4, 3, 128, 3), (4, 6, 64, 90), (4, 14, 128, 160), (3, 100, 128, 3),
+                                     (8, 90, 64, 100)])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_prefill_nan_queries_stay_in_their_rows(pa, G, q, d, n, dtype):
+    b = Batch(38, np.full(n, 3 * q), 2, G, d, 16, dtype, q_lens=[q] * n)
+    b.q[q // 2, G, 3] = float("nan")
+    b.q[-1, 0, :] = float("nan")
+    nans = same_with_nans(b, b.prefill(pa))
+    assert nans.sum() == 2 * d
+    assert pa.pa_device_errors() == 0
+
+
 def test_decode_bad_block_and_bad_length(pa):
     b = Batch(36, [500, 900, 64], 2, 4, 128, 16, "fp16")
     good = b.tables.copy()
