@@ -34,7 +34,7 @@
 // KV heads, head_dim 128, fp16, 1,024-token partitions: 42.5 us for 161 MB (3.8
 // TB/s, 0.56 of the copy rate; bytes alone 24 us); 256 sequences of up to 16,384,
 // 64 query heads, bf16: 111 us, 4.9 TB/s; a chunk of 5 tokens x 4 heads for the
-// first batch: 77 to 90 us, its three row tiles' chain of latencies at two CTAs
+// first batch: 66 to 73 us, its three row tiles' chain of latencies at two CTAs
 // an SM.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + NW * S * kStep);
 
-  const int kvh = blockIdx.y, seq = blockIdx.z;
+  const int kvh = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = kParts ? 0 : static_cast<int>(blockIdx.x) % cluster;  // in the cluster
   const int part = WP ? blockIdx.x * NW + warp : kParts ? blockIdx.x : 0;
@@ -205,6 +205,19 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
   }
   __syncwarp();
   grid_dependency_wait();  // the pool may come from the kernel before
+  int place = blockIdx.z;
+  if constexpr (!kParts) {
+    if (a.by_length) {
+      int *at = nan_key + NW * 8;
+      if (warp == 0) {
+        place = seq_by_length(a.context_lens, a.num_seqs, place, lane);
+        if (lane == 0) *at = place;
+      }
+      __syncthreads();
+      place = *at;
+    }
+  }
+  const int seq = place;
 
   // Steps are 32-token windows of the sequence from the one that holds the
   // partition's first token on: a block never straddles two.  A warp's tiles
@@ -767,10 +780,11 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
 }
 
 template <typename T, int D, int BS, int NW, int S, Rows ROWS, int NT>
-cudaError_t launch_rows(const DecodeArgs &a, const CUtensorMap &km, const CUtensorMap &vm,
+cudaError_t launch_rows(DecodeArgs a, const CUtensorMap &km, const CUtensorMap &vm,
                         unsigned grid_x, cudaStream_t stream) {
   constexpr size_t stages = static_cast<size_t>(NW) * S * 2 * Fp4Shape<D, BS>::kUnit;
-  constexpr size_t smem = 1024 + stages + NW * S * 8 + (ROWS == Rows::kChunk ? NW * 8 * 4 : 0);
+  constexpr bool kParts = ROWS == Rows::kDecode || ROWS == Rows::kDecodeWarps;
+  constexpr size_t smem = 1024 + stages + NW * S * 8 + (kParts ? 0 : NW * 8 * 4 + 4);
   static_assert((static_cast<size_t>(NW) * (kAccStride<D> + 2) + NT * (D + 2)) * 32 + 16 <= stages,
                 "merge buffers and the join flag must fit in the stage area");
   static_assert(smem <= 227 * 1024, "shared memory");
@@ -778,6 +792,17 @@ cudaError_t launch_rows(const DecodeArgs &a, const CUtensorMap &km, const CUtens
   static SmemLimitOnce smem_limit;
   const cudaError_t e = smem_limit.ensure(kern, smem);
   if (e != cudaSuccess) return e;
+  // Longest contexts first where the CTAs are more than run at once and the
+  // table leaves room for unequal contexts: 64 sequences of 512 to 4,096 tokens,
+  // 20 rows: 66 us against 78 to 91; 256 of up to 4,096, one query: 118 against
+  // 132.  (256 of up to 300 tokens, 8 rows, under a table of 32,768: 27 against
+  // 26.)  Calls with partitions lose: 256 sequences of up to 16,384 152 us
+  // against 116, since every empty partition's CTA asks for its sequence too.
+  const int64_t ctas = static_cast<int64_t>(grid_x) * a.num_kv_heads * a.num_seqs;
+  a.by_length = !kParts && a.cluster == 1 &&
+                a.num_seqs > 1 && a.num_seqs <= kMaxByLength && ctas > 152 * ctas_per_sm(NT) &&
+                (static_cast<int64_t>(a.max_blocks_per_seq) << a.bs_log2) >= kMinByLength &&
+                (ROWS == Rows::kChunk || a.max_context_len >= kMinByLength);
   return launch_clusters(a.cluster, kern, dim3(grid_x, a.num_kv_heads, a.num_seqs),
                          dim3(NW * 32), smem, stream, km, vm, a);
 }
@@ -787,8 +812,8 @@ cudaError_t launch_rows(const DecodeArgs &a, const CUtensorMap &km, const CUtens
 // context that the table can hold.  Few sequences gain (one of 8,000 tokens and
 // one KV head 20 us, with one CTA 93; eight KV heads of 4,096 tokens 11 against
 // 33), and beyond that room a CTA's 4 to 6 us of start and join cost more than
-// the evener load gives (64 sequences of 512 to 4,096 tokens, 20 rows: 82 us
-// alone, 88 in pairs, 115 in fours).
+// the evener load gives (64 sequences of 512 to 4,096 tokens, 20 rows, taken
+// as they come: 82 us alone, 88 in pairs, 115 in fours).
 int cluster_of(const DecodeArgs &a, int64_t ctas, int warps, int per_sm) {
   const int64_t steps = (static_cast<int64_t>(a.max_blocks_per_seq) << a.bs_log2) / 32;
   int n = 1;

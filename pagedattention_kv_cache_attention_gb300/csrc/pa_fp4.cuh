@@ -72,4 +72,54 @@ __device__ __forceinline__ uint32_t float_to_e4m3(float x) {
   return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
 }
 
+constexpr int kMaxByLength = 256;
+constexpr int kMinByLength = 1024;  // tokens of the longest context
+
+// The sequence of place z when n <= kMaxByLength sequences are put in order of
+// their context lengths, longest first, in 16 to 32 classes of equal width (in a
+// class by index).  For a whole warp.  A grid of more CTAs than run at once ends
+// with its last CTAs: with the short contexts there it ends earlier.  Where no
+// context reaches kMinByLength the places stay as they are.  (A function of its
+// own: inlined, its registers cost the kernels up to 10 %.)
+static __device__ __noinline__ int seq_by_length(const int32_t *lens, int n, int z, int lane) {
+  constexpr int kWords = kMaxByLength / 32;
+  int c[kWords], top = 0;
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    c[i] = i * 32 + lane < n ? max(lens[i * 32 + lane], 0) : -1;
+    top = max(top, c[i]);
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (top < kMinByLength) return z;
+  const int shift = 27 - __clz(top);  // top >> shift is at most 31
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) c[i] >>= shift;  // (-1 stays)
+  int cls = 0, rem = z;
+#pragma unroll
+  for (int bit = 4; bit >= 0; --bit) {
+    const int want = (cls >> bit) | 1;
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      if (i * 32 < n) count += __popc(__ballot_sync(0xffffffffu, c[i] >> bit == want));
+    if (rem < count)
+      cls |= 1 << bit;
+    else
+      rem -= count;
+  }
+  int seq = 0;
+#pragma unroll
+  for (int i = 0; i < kWords; ++i)
+    if (i * 32 < n) {
+      const uint32_t in = __ballot_sync(0xffffffffu, c[i] == cls);
+      const int count = __popc(in);
+      if (rem >= 0 && rem < count)
+        seq = i * 32 + __ffs(__ballot_sync(0xffffffffu, ((in >> lane) & 1u) &&
+                                                            __popc(in & ((1u << lane) - 1)) == rem)) -
+              1;
+      rem -= count;
+    }
+  return seq;
+}
+
 }  // namespace pa

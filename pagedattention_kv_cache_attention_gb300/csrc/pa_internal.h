@@ -75,6 +75,7 @@ struct DecodeArgs {
   int max_q_len;
   // CTAs of a cluster that share the keys of an unsplit call over FP4 caches
   int cluster;
+  int by_length;  // FP4: CTAs take the longest contexts first (seq_by_length)
 };
 
 struct ReduceArgs {
@@ -138,6 +139,7 @@ struct PrefillArgs {
   // (chunks: in the FP4 two-tile kernel, the CTAs of a cluster)
   int num_groups, max_group_size, members_per_cta, chunks;
   int part_tokens, num_parts, max_context_len;
+  int by_length;  // FP4: CTAs take the longest contexts first (seq_by_length)
 };
 
 struct BlockCopyArgs {

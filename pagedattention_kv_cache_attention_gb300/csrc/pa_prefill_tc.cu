@@ -342,7 +342,17 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
       }
     }
   } else {
-    const int tile = blockIdx.x, seq = blockIdx.z;
+    const int tile = blockIdx.x;
+    int seq = blockIdx.z;
+    if constexpr (F4)
+      if (a.by_length) {
+        if (warp == 0) {
+          const int mine = seq_by_length(a.context_lens, a.num_seqs, seq, tid);
+          if (tid == 0) tmem_slot[1] = mine;
+        }
+        __syncthreads();
+        seq = tmem_slot[1];
+      }
     q0 = a.query_start[seq];
     q_len = a.query_start[seq + 1] - q0;
     const int ctx = a.context_lens[seq];
@@ -1075,6 +1085,15 @@ cudaError_t launch_prefill_tc_pair_t(const PrefillArgs &a, const CUtensorMap &km
   }
   const int tpc = TILES * ROWS / a.group;
   const int tiles = (a.max_q_len + tpc - 1) / tpc;
+  if constexpr (KV == Kv::kFp4) {
+    // longest contexts first (64 sequences of 512 to 4,096 tokens, 28 to 64 rows:
+    // 89 us against 107)
+    PrefillArgs b = a;
+    b.by_length = a.num_seqs <= kMaxByLength &&
+                  (static_cast<int64_t>(a.max_blocks_per_seq) << a.bs_log2) >= kMinByLength;
+    return launch_dependent(kern, dim3(tiles, a.num_kv_heads, a.num_seqs),
+                            dim3(pair_threads<TILES, D, KV>()), smem, stream, km, vm, b);
+  }
   return launch_dependent(kern, dim3(tiles, a.num_kv_heads, a.num_seqs),
                           dim3(pair_threads<TILES, D, KV>()), smem,
                           stream, km, vm, a);
@@ -1109,8 +1128,8 @@ cudaError_t launch_prefill_tc_d(const PrefillArgs &a, const CUtensorMap &km,
   constexpr int SK = PA_PREFILL_SOLO_KSTAGES, SV = PA_PREFILL_SOLO_VSTAGES;
   if (kv == Kv::kFp4) {
     // Up to 64 rows run two CTAs to an SM where there are enough of them (64
-    // sequences of 512 to 4,096 tokens, 8 KV heads, 28 to 64 rows: 107 to 111
-    // us, 127 with two tiles); more rows, and few CTAs, in the two-tile kernel,
+    // sequences of 512 to 4,096 tokens, 8 KV heads, 28 to 64 rows: 89 us,
+    // 127 with two tiles); more rows, and few CTAs, in the two-tile kernel,
     // whose steps are shorter (80 rows of the same batch 127 us; a one-tile
     // kernel took 176), and which shares a sequence's keys in a cluster.
     if (static_cast<int64_t>(a.max_q_len) * a.group > 64 ||

@@ -426,6 +426,26 @@ def test_prefill_few_sequences_beside_a_long_one(pa, rows, G, d, bs, dtype):
     assert pa.pa_device_errors() == 0
 
 
+@pytest.mark.parametrize("n", [39, 64, 200, 256, 257])
+@pytest.mark.parametrize("q,G,d,bs,dtype", [(0, 2, 64, 16, "fp16"), (3, 2, 64, 32, "bf16"),
+                                            (6, 4, 64, 16, "fp16"), (13, 4, 64, 16, "bf16")])
+@pytest.mark.parametrize("longest", [900, 1500])
+def test_many_sequences_of_unequal_contexts(pa, n, q, G, d, bs, dtype, longest):
+    """Every sequence is served once, in whichever order the kernels take them;
+    q = 0: decode.  Zero and equal lengths among them."""
+    rng = np.random.default_rng(n + q)
+    lens = rng.integers(0, 90, n)
+    lens[rng.integers(0, n, 5)] = rng.integers(500, longest, 5)
+    lens[n // 2], lens[::7] = longest, 33
+    if q == 0:
+        b = Batch(57, lens, 8, G, d, bs, dtype)
+        b.check(b.decode(pa, 0))
+    else:
+        b = Batch(58, lens, 8, G, d, bs, dtype, q_lens=np.minimum(lens, rng.integers(0, q + 1, n)))
+        b.check(b.prefill(pa))
+    assert pa.pa_device_errors() == 0
+
+
 def test_prefill_more_sequences_than_multiprocessors(pa):
     rng = np.random.default_rng(77)
     lens = rng.integers(20, 400, 170)
