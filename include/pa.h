@@ -450,7 +450,8 @@ pa_status pa_decode_fp4(void *out, const void *query,
  * pa_prefill_fp4 -- pa_prefill over FP4 caches, the values as in pa_decode_fp4.
  * Arguments, shapes and error behaviour as pa_prefill_fp8; max_q_len (or
  * max_blocks_per_seq * block_size, if that is less) above 65535 * (256 / group)
- * tokens, group = num_q_heads / num_kv_heads: PA_ERR_UNSUPPORTED.
+ * tokens, group = num_q_heads / num_kv_heads, or a table of 2^31 tokens or
+ * more: PA_ERR_UNSUPPORTED.
  */
 pa_status pa_prefill_fp4(void *out, const void *query, const int32_t *query_start,
                          const void *k_cache, const void *v_cache,

@@ -500,10 +500,10 @@ pa_status prefill_impl(void *out, const void *query, const int32_t *query_start,
   if (st != PA_OK || num_seqs == 0 || max_q_len == 0) return st;
   const int32_t group = num_q_heads / num_kv_heads;
   const int64_t pool_rows = num_blocks * num_kv_heads * block_size;
-  // FP4: the tiles of a chunk are the grid's second dimension
-  if (kv == pa::Kv::kFp4 &&
-      std::min<int64_t>(max_q_len, static_cast<int64_t>(max_blocks_per_seq) * block_size) >
-          int64_t{65535} * (256 / group))
+  // FP4: positions are 32-bit, and the tiles of a chunk the grid's second dimension
+  const int64_t room = static_cast<int64_t>(max_blocks_per_seq) * block_size;
+  if (kv == pa::Kv::kFp4 && (room > 0x7fffffff || std::min<int64_t>(max_q_len, room) >
+                                                      int64_t{65535} * (256 / group)))
     return PA_ERR_UNSUPPORTED;
   unsigned int *err = nullptr;
   if (error_word(&err) != cudaSuccess) return PA_ERR_CUDA;

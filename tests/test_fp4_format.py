@@ -139,7 +139,8 @@ SETS = {"pa_reshape_and_cache_fp4": ROWS, "pa_gather_cache_fp4": ROWS,
         "pa_prefill_fp4": ATTN + [(dict(mq=0), 0), (dict(mq=-1), 1), (dict(qs=None), 1),
                                   (dict(scale=0.0), 1),
                                   # tiles of a chunk beyond the grid's second dimension
-                                  (dict(mq=(1 << 22) + 1, mb=1 << 20), 2)]}
+                                  (dict(mq=(1 << 22) + 1, mb=1 << 20), 2),
+                                  (dict(mb=1 << 27), 2)]}
 
 
 @pytest.mark.parametrize("name,over,status",
