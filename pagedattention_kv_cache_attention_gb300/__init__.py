@@ -542,7 +542,10 @@ def fp4_block_size(cache: torch.Tensor, head_dim: int) -> int:
 # The FP4 calls check their arguments in one pass and look nothing up twice: for
 # a decode step of a few short sequences the host's share of a call is longer
 # than the kernel (16 us a call with the checks of the calls above, 8 with these).
+# What fits passes one expression; only what does not is gone through tensor by
+# tensor, to name it.
 _fp4_fns = {}
+_U8, _I32, _I64 = torch.uint8, torch.int32, torch.int64
 _FP4_ARGS = {
     "cache": "PPllPPPiiiiliffP",                  # write and read-back
     "decode": "PPPPPiPiiiiilfffiiPziP",
@@ -581,12 +584,10 @@ def _device_of(name: str, t) -> int:
     return dev
 
 
-def _fp4_caches(k_cache, v_cache, head_dim: int, dev: int) -> int:
-    _fits("k_cache", k_cache, torch.uint8, dev)
-    _fits("v_cache", v_cache, torch.uint8, dev)
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache shapes differ")
-    return fp4_block_size(k_cache, head_dim)
+def _all_fit(dev: int, **tensors) -> None:
+    """Each name=(tensor, dtype): dense on the current device; raises for the first that is not."""
+    for name, (t, dtype) in tensors.items():
+        _fits(name, t, dtype, dev)
 
 
 def _cache_fp4(name, key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, stream):
@@ -601,16 +602,28 @@ def _cache_fp4(name, key, value, k_cache, v_cache, slot_mapping, k_scale, v_scal
     ks, vs = key.stride(), value.stride()
     if ks[2] != 1 or ks[1] != d or vs[2] != 1 or vs[1] != d:
         raise ValueError("key, value: heads must be contiguous inside a token row")
-    bs = _fp4_caches(k_cache, v_cache, d, dev)
-    if k_cache.shape[1] != Hkv:
+    try:
+        fit = (k_cache.dtype is _U8 and v_cache.dtype is _U8 and slot_mapping.dtype is _I64
+               and k_cache.get_device() == dev == v_cache.get_device() == slot_mapping.get_device()
+               and k_cache.is_contiguous() and v_cache.is_contiguous()
+               and slot_mapping.is_contiguous())
+    except AttributeError:
+        fit = False
+    if not fit:
+        _all_fit(dev, k_cache=(k_cache, _U8), v_cache=(v_cache, _U8),
+                 slot_mapping=(slot_mapping, _I64))
+    cache = k_cache.shape
+    if v_cache.shape != cache:
+        raise ValueError("k_cache and v_cache shapes differ")
+    bs = fp4_block_size(k_cache, d)
+    if cache[1] != Hkv:
         raise ValueError("key/value/cache shapes disagree")
-    _fits("slot_mapping", slot_mapping, torch.int64, dev)
     if slot_mapping.numel() != T:
         raise ValueError("slot_mapping must have one entry per token")
     row = Hkv * d  # the stride of a single row is not looked at
     st = f(key.data_ptr(), value.data_ptr(), ks[0] if T > 1 else row, vs[0] if T > 1 else row,
            k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), T, Hkv, d, bs,
-           k_cache.shape[0], _dtype_code(key), float(k_scale), float(v_scale),
+           cache[0], _dtype_code(key), float(k_scale), float(v_scale),
            _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise PaError(name, st)
@@ -644,15 +657,29 @@ def pa_decode_fp4(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor,
     bf16 queries and output).  ``workspace`` as for pa_decode."""
     f = _fp4_fns.get("pa_decode_fp4") or _fp4_fn("pa_decode_fp4", "decode")
     dev = _device_of("query", query)
-    _fits("query", query, query.dtype, dev)
-    _fits("out", out, query.dtype, dev)
-    B, Hq, d = query.shape
-    bs = _fp4_caches(k_cache, v_cache, d, dev)
-    _fits("block_tables", block_tables, torch.int32, dev)
-    _fits("context_lens", context_lens, torch.int32, dev)
-    if out.shape != query.shape:
+    dtype = query.dtype
+    try:
+        fit = (out.dtype is dtype and k_cache.dtype is _U8 and v_cache.dtype is _U8
+               and block_tables.dtype is _I32 and context_lens.dtype is _I32
+               and out.get_device() == dev == k_cache.get_device() == v_cache.get_device()
+               and block_tables.get_device() == dev == context_lens.get_device()
+               and query.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous()
+               and v_cache.is_contiguous() and block_tables.is_contiguous()
+               and context_lens.is_contiguous())
+    except AttributeError:
+        fit = False
+    if not fit:
+        _all_fit(dev, query=(query, dtype), out=(out, dtype), k_cache=(k_cache, _U8),
+                 v_cache=(v_cache, _U8), block_tables=(block_tables, _I32),
+                 context_lens=(context_lens, _I32))
+    shape, cache, table = query.shape, k_cache.shape, block_tables.shape
+    B, Hq, d = shape
+    if v_cache.shape != cache:
+        raise ValueError("k_cache and v_cache shapes differ")
+    bs = fp4_block_size(k_cache, d)
+    if out.shape != shape:
         raise ValueError("out and query shapes differ")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.numel() != B:
+    if len(table) != 2 or table[0] != B or context_lens.numel() != B:
         raise ValueError("block_tables must be [B, MB] and context_lens [B]")
     ws_ptr, ws_bytes = None, 0
     if 0 < partition_size < max_context_len:
@@ -668,8 +695,8 @@ def pa_decode_fp4(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor,
             raise ValueError("workspace must be contiguous")
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     st = f(out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-           block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, Hq,
-           k_cache.shape[1], d, bs, k_cache.shape[0], float(scale), float(k_scale), float(v_scale),
+           block_tables.data_ptr(), table[1], context_lens.data_ptr(), B, Hq,
+           cache[1], d, bs, cache[0], float(scale), float(k_scale), float(v_scale),
            int(max_context_len), int(partition_size), ws_ptr, ws_bytes, _dtype_code(query),
            _raw_stream(dev) if stream is None else _stream(stream))
     if st:
@@ -684,22 +711,37 @@ def pa_prefill_fp4(out: torch.Tensor, query: torch.Tensor, query_start: torch.Te
     """pa_prefill over FP4 caches, fp16 or bf16 queries and output."""
     f = _fp4_fns.get("pa_prefill_fp4") or _fp4_fn("pa_prefill_fp4", "prefill")
     dev = _device_of("query", query)
-    _fits("query", query, query.dtype, dev)
-    _fits("out", out, query.dtype, dev)
-    total_q, Hq, d = query.shape
-    bs = _fp4_caches(k_cache, v_cache, d, dev)
-    _fits("query_start", query_start, torch.int32, dev)
-    _fits("block_tables", block_tables, torch.int32, dev)
-    _fits("context_lens", context_lens, torch.int32, dev)
+    dtype = query.dtype
+    try:
+        fit = (out.dtype is dtype and k_cache.dtype is _U8 and v_cache.dtype is _U8
+               and query_start.dtype is _I32 and block_tables.dtype is _I32
+               and context_lens.dtype is _I32
+               and out.get_device() == dev == k_cache.get_device() == v_cache.get_device()
+               and query_start.get_device() == dev == block_tables.get_device()
+               and context_lens.get_device() == dev
+               and query.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous()
+               and v_cache.is_contiguous() and query_start.is_contiguous()
+               and block_tables.is_contiguous() and context_lens.is_contiguous())
+    except AttributeError:
+        fit = False
+    if not fit:
+        _all_fit(dev, query=(query, dtype), out=(out, dtype), k_cache=(k_cache, _U8),
+                 v_cache=(v_cache, _U8), query_start=(query_start, _I32),
+                 block_tables=(block_tables, _I32), context_lens=(context_lens, _I32))
+    shape, cache, table = query.shape, k_cache.shape, block_tables.shape
+    total_q, Hq, d = shape
+    if v_cache.shape != cache:
+        raise ValueError("k_cache and v_cache shapes differ")
+    bs = fp4_block_size(k_cache, d)
     B = context_lens.numel()
-    if query_start.numel() != B + 1 or out.shape != query.shape:
+    if query_start.numel() != B + 1 or out.shape != shape:
         raise ValueError("query_start must have num_seqs + 1 entries; out must match query")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+    if len(table) != 2 or table[0] != B:
         raise ValueError("block_tables must be [B, MB]")
     st = f(out.data_ptr(), query.data_ptr(), query_start.data_ptr(), k_cache.data_ptr(),
-           v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
-           context_lens.data_ptr(), B, int(max_q_len), Hq, k_cache.shape[1], d, bs,
-           k_cache.shape[0], float(scale), float(k_scale), float(v_scale), _dtype_code(query),
+           v_cache.data_ptr(), block_tables.data_ptr(), table[1],
+           context_lens.data_ptr(), B, int(max_q_len), Hq, cache[1], d, bs,
+           cache[0], float(scale), float(k_scale), float(v_scale), _dtype_code(query),
            _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise PaError("pa_prefill_fp4", st)
