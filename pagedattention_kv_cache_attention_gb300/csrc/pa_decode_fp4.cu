@@ -794,10 +794,10 @@ cudaError_t launch_rows(DecodeArgs a, const CUtensorMap &km, const CUtensorMap &
   if (e != cudaSuccess) return e;
   // Longest contexts first where the CTAs are more than run at once and the
   // table leaves room for unequal contexts: 64 sequences of 512 to 4,096 tokens,
-  // 20 rows: 66 us against 78 to 91; 256 of up to 4,096, one query: 118 against
-  // 132.  (256 of up to 300 tokens, 8 rows, under a table of 32,768: 27 against
-  // 26.)  Calls with partitions lose: 256 sequences of up to 16,384 152 us
-  // against 116, since every empty partition's CTA asks for its sequence too.
+  // 20 rows: 66 us against 78 to 91; 256 of up to 4,096, one query: 115 against
+  // 130.  (256 of up to 300 tokens, 8 rows, under a table of 32,768: 27 against
+  // 26.)  Calls with partitions lose: 256 sequences of up to 16,384 128 us
+  // against 117, since every empty partition's CTA asks for its sequence too.
   const int64_t ctas = static_cast<int64_t>(grid_x) * a.num_kv_heads * a.num_seqs;
   a.by_length = !kParts && a.cluster == 1 &&
                 a.num_seqs > 1 && a.num_seqs <= kMaxByLength && ctas > 152 * ctas_per_sm(NT) &&

@@ -79,10 +79,10 @@ constexpr int kMinByLength = 1024;  // tokens of the longest context
 // their context lengths, longest first, in 16 to 32 classes of equal width (in a
 // class by index).  For a whole warp.  A grid of more CTAs than run at once ends
 // with its last CTAs: with the short contexts there it ends earlier.  Where no
-// context reaches kMinByLength the places stay as they are.  (A function of its
-// own: inlined, its registers cost the kernels up to 10 %.)
-static __device__ __noinline__ int seq_by_length(const int32_t *lens, int n, int z, int lane) {
-  constexpr int kWords = kMaxByLength / 32;
+// context reaches kMinByLength the places stay as they are.  (Functions of their
+// own: inlined, their registers cost the kernels up to 10 %.)
+template <int kWords>  // a lane holds the lengths of kWords sequences
+static __device__ __noinline__ int place_by_length(const int32_t *lens, int n, int z, int lane) {
   int c[kWords], top = 0;
 #pragma unroll
   for (int i = 0; i < kWords; ++i) {
@@ -94,32 +94,37 @@ static __device__ __noinline__ int seq_by_length(const int32_t *lens, int n, int
   const int shift = 27 - __clz(top);  // top >> shift is at most 31
 #pragma unroll
   for (int i = 0; i < kWords; ++i) c[i] >>= shift;  // (-1 stays)
-  int cls = 0, rem = z;
+  int cls = 0, rem = z;  // the class, a bit at a time; the place among what is left
 #pragma unroll
   for (int bit = 4; bit >= 0; --bit) {
     const int want = (cls >> bit) | 1;
     int count = 0;
 #pragma unroll
     for (int i = 0; i < kWords; ++i)
-      if (i * 32 < n) count += __popc(__ballot_sync(0xffffffffu, c[i] >> bit == want));
+      count += __popc(__ballot_sync(0xffffffffu, c[i] >> bit == want));
     if (rem < count)
       cls |= 1 << bit;
     else
       rem -= count;
   }
-  int seq = 0;
+  uint32_t in = 0;  // the word of the class that holds place rem
+  int word = 0, first = 0;
 #pragma unroll
-  for (int i = 0; i < kWords; ++i)
-    if (i * 32 < n) {
-      const uint32_t in = __ballot_sync(0xffffffffu, c[i] == cls);
-      const int count = __popc(in);
-      if (rem >= 0 && rem < count)
-        seq = i * 32 + __ffs(__ballot_sync(0xffffffffu, ((in >> lane) & 1u) &&
-                                                            __popc(in & ((1u << lane) - 1)) == rem)) -
-              1;
-      rem -= count;
+  for (int i = 0; i < kWords; ++i) {
+    const uint32_t these = __ballot_sync(0xffffffffu, c[i] == cls);
+    if (first <= rem) {
+      in = these;
+      word = i;
+      z = rem - first;  // among the word's
     }
-  return seq;
+    first += __popc(these);
+  }
+  const bool here = ((in >> lane) & 1u) && __popc(in & ((1u << lane) - 1)) == z;
+  return word * 32 + __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+}
+__device__ __forceinline__ int seq_by_length(const int32_t *lens, int n, int z, int lane) {
+  return n <= 64 ? place_by_length<2>(lens, n, z, lane)
+                 : place_by_length<kMaxByLength / 32>(lens, n, z, lane);
 }
 
 }  // namespace pa
