@@ -254,6 +254,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           *q_unit(lane, c) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
         }
       }
+      // a small cache scale times a small power of two may fall below the normal
+      // numbers, and 0 x -inf would be NaN (what the row's logits lose is below 2^-90)
+      sl2 = fmaxf(sl2, 0x1p-126f);
       fence_proxy_async_smem();
       mbar_arrive(q_ready);
     }
