@@ -428,8 +428,9 @@ pa_status pa_gather_cache_fp4(void *key, void *value, int64_t key_stride, int64_
  * pa_decode_fp4 -- pa_decode over FP4 caches.  s * e2m1(c) is exact in fp16
  * (at most 6 significant bits); both products run in fp16 with fp32
  * accumulation (a group with the NaN scale makes NaN of what attends to it:
- * of a row for K, of the group's dimensions of a row for V), k_scale joins the softmax scale and v_scale multiplies the
- * output; bf16 queries are carried in fp16 as pa_decode_fp8 does.  Other
+ * of a row for K, of the group's dimensions of a row for V), k_scale joins the
+ * softmax scale and v_scale multiplies the output; bf16 queries are carried in
+ * fp16 as pa_decode_fp8 does.  Logits may have any size that fp32 holds.  Other
  * arguments, partitions and workspace as pa_decode; m of a partial is a value
  * that the partition's largest logit passes by at most 4 (base 2) in place of
  * that logit itself, and l and o are relative to it, so that the join is the

@@ -20,8 +20,12 @@
 //    instructions for eight codes, so that a converted pair is already (token,
 //    next token) of one dimension, and its scale pair is shared by the lane's
 //    dimensions.
-//  * fp32 online softmax in base 2 against a reference that moves only when a
-//    score passes it by more than 4.  P is carried as fp16 (11 bits; the output
+//  * fp32 online softmax in base 2 against a reference, a score of the row, that
+//    moves only when another passes it by more than 2^4.  While the reference's
+//    logit is small, a probability's exponent is one fma of the score; one with
+//    a large logit is taken off the score first, which is exact where it matters:
+//    the product alone may be off by more than fp16's range (pa_fp4.cuh).  P is
+//    carried as fp16 (11 bits; the output
 //    has at most 11) times 2^11, so that only probabilities below 2^-25 of the
 //    maximum lose bits and below 2^-35 vanish: a long context's faint tail
 //    keeps its mass.
@@ -71,6 +75,7 @@ namespace {
 // running maximum: below 2^15 then, and in fp16's normal range down to 2^-25 of
 // the maximum.
 constexpr float kPShift = 11.f, kGrowth = 4.f;
+constexpr float kFar = kFp4FarLogit;
 
 // Geometry of a tile in shared memory.  TMA brings it in lines of D bytes (the
 // codes of two tokens; 9 lines for 16 tokens, the last of them scales) with the
@@ -342,6 +347,17 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
       sl[nt][0] = ldexpf(sl[nt][0], -__shfl_sync(kFull, e, 8 * c));      // a lane of column 2c
       sl[nt][1] = ldexpf(sl[nt][1], -__shfl_sync(kFull, e, 8 * c + 4));  // of column 2c + 1
     }
+    sl[nt][0] = fp4_normal_scale(sl[nt][0]);
+    sl[nt][1] = fp4_normal_scale(sl[nt][1]);
+    if (!kChunk && a.scale_log2 < 0.f) {  // a negative scale: the query's sign (order of the scores)
+#pragma unroll
+      for (int i = 0; i < Sh::kQChunks; ++i) {
+        qf[nt][i].x ^= 0x80008000u;
+        qf[nt][i].y ^= 0x80008000u;
+        qf[nt][i].z ^= 0x80008000u;
+        qf[nt][i].w ^= 0x80008000u;
+      }
+    }
   }
 
   // The lane's places in a unit's first half: K row token_of(g), V rows t0 =
@@ -357,13 +373,13 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
   const int vs_1 = t1 * Sh::kScales + (D == 128 ? g : g >> 1);
 
   const float NEG_INF = -INFINITY;
-  // online softmax of the lane's columns 2c and 2c + 1 in base 2: c0 = kPShift -
-  // the reference of the first, so that probabilities are held as 2^(x + c0);
-  // before the first token the reference is far below any score
-  float cr[NT][2], l[NT][2], acc[NT][Sh::kMTiles][4];
+  // online softmax of the lane's columns 2c and 2c + 1 in base 2: xr is the
+  // reference, a score before the softmax scale (-inf before the first token), so
+  // that probabilities are held as 2^((x - xr) sl + kPShift)
+  float xr[NT][2], l[NT][2], acc[NT][Sh::kMTiles][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    cr[nt][0] = cr[nt][1] = 1e30f;
+    xr[nt][0] = xr[nt][1] = NEG_INF;
     l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
     for (int mt = 0; mt < Sh::kMTiles; ++mt)
@@ -437,49 +453,54 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
       const int col = 8 * nt + 2 * c;
       const int own0 = kChunk && masked ? own + col / G : 0;
       const int own1 = kChunk && masked ? own + (col + 1) / G : 0;
-      // z = scores + (b0, b1); tokens that do not count get -inf
-      auto logits = [&](float (&z)[2][4], float b0, float b1) {
+      // tokens that do not count get -inf
+      auto hide = [&](float (&z)[2][4]) {
+        if (!masked) return;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          z[h][0] = fmaf(x[nt][h][0], sl[nt][0], b0);
-          z[h][1] = fmaf(x[nt][h][1], sl[nt][1], b1);
-          z[h][2] = fmaf(x[nt][h][2], sl[nt][0], b0);
-          z[h][3] = fmaf(x[nt][h][3], sl[nt][1], b1);
-          if (masked) {
-            const int ta = 16 * h + kr, tb = ta + 8;
-            const bool va = (mask >> ta) & 1u, vb = (mask >> tb) & 1u;
-            z[h][0] = va && (!kChunk || ta <= own0) ? z[h][0] : NEG_INF;
-            z[h][1] = va && (!kChunk || ta <= own1) ? z[h][1] : NEG_INF;
-            z[h][2] = vb && (!kChunk || tb <= own0) ? z[h][2] : NEG_INF;
-            z[h][3] = vb && (!kChunk || tb <= own1) ? z[h][3] : NEG_INF;
-          }
+          const int ta = 16 * h + kr, tb = ta + 8;
+          const bool va = (mask >> ta) & 1u, vb = (mask >> tb) & 1u;
+          z[h][0] = va && (!kChunk || ta <= own0) ? z[h][0] : NEG_INF;
+          z[h][1] = va && (!kChunk || ta <= own1) ? z[h][1] : NEG_INF;
+          z[h][2] = vb && (!kChunk || tb <= own0) ? z[h][2] : NEG_INF;
+          z[h][3] = vb && (!kChunk || tb <= own1) ? z[h][3] : NEG_INF;
         }
       };
       // 2^y are the probabilities; the reference moves only when one of them
       // passes 2^(kPShift + kGrowth), so most steps need a vote and no shuffles
+      const float s0 = sl[nt][0], s1 = sl[nt][1];
+      const float c0 = fmaf(-xr[nt][0], s0, kPShift), c1 = fmaf(-xr[nt][1], s1, kPShift);
       float y[2][4];
-      logits(y, cr[nt][0], cr[nt][1]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        y[h][0] = fmaf(x[nt][h][0], s0, c0);
+        y[h][1] = fmaf(x[nt][h][1], s1, c1);
+        y[h][2] = fmaf(x[nt][h][2], s0, c0);
+        y[h][3] = fmaf(x[nt][h][3], s1, c1);
+      }
+      hide(y);
       float top = NEG_INF;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         top = fmaxf(top, fmaxf(fmaxf(y[h][0], y[h][1]), fmaxf(y[h][2], y[h][3])));
-      if (__any_sync(kFull, top > kPShift + kGrowth)) {
-        logits(y, 0.f, 0.f);
-        float mx0 = kPShift - cr[nt][0], mx1 = kPShift - cr[nt][1];
+      // (c0, c1 are infinite before the first token)
+      if (__any_sync(kFull, top > kPShift + kGrowth || fmaxf(fabsf(c0), fabsf(c1)) > kFar)) {
+        hide(x[nt]);
+        float mx0 = xr[nt][0], mx1 = xr[nt][1];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          mx0 = fmaxf(mx0, fmaxf(y[h][0], y[h][2]));
-          mx1 = fmaxf(mx1, fmaxf(y[h][1], y[h][3]));
+          mx0 = fmaxf(mx0, fmaxf(x[nt][h][0], x[nt][h][2]));
+          mx1 = fmaxf(mx1, fmaxf(x[nt][h][1], x[nt][h][3]));
         }
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
           mx0 = fmaxf(mx0, __shfl_xor_sync(kFull, mx0, off));
           mx1 = fmaxf(mx1, __shfl_xor_sync(kFull, mx1, off));
         }
-        const float n0 = kPShift - mx0, n1 = kPShift - mx1;
-        const float al0 = ex2_approx(n0 - cr[nt][0]), al1 = ex2_approx(n1 - cr[nt][1]);
-        cr[nt][0] = n0;
-        cr[nt][1] = n1;
+        const float al0 = mx0 == xr[nt][0] ? 1.f : ex2_approx((xr[nt][0] - mx0) * s0);
+        const float al1 = mx1 == xr[nt][1] ? 1.f : ex2_approx((xr[nt][1] - mx1) * s1);
+        xr[nt][0] = mx0;
+        xr[nt][1] = mx1;
         l[nt][0] *= al0;
         l[nt][1] *= al1;
 #pragma unroll
@@ -489,7 +510,15 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
           acc[nt][mt][2] *= al0;
           acc[nt][mt][3] *= al1;
         }
-        logits(y, cr[nt][0], cr[nt][1]);
+        const float r0 = mx0 == NEG_INF ? 0.f : mx0;  // no token yet: any finite reference
+        const float r1 = mx1 == NEG_INF ? 0.f : mx1;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          y[h][0] = fmaf(x[nt][h][0] - r0, s0, kPShift);
+          y[h][1] = fmaf(x[nt][h][1] - r1, s1, kPShift);
+          y[h][2] = fmaf(x[nt][h][2] - r0, s0, kPShift);
+          y[h][3] = fmaf(x[nt][h][3] - r1, s1, kPShift);
+        }
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -617,8 +646,10 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
   for (const int filled = min(k + S, my_n); timed_out && k < filled; ++k)
     (void)mbar_wait_bounded(&my_bars[k % S], (k / S) & 1);
 
-  // row sums over the 8 token rows; l and acc are both held times 2^kPShift
-  const float unshift = exp2f(-kPShift);
+  // row sums over the 8 token rows; l and acc are both held times 2^kPShift,
+  // relative to xr; from here on (to is what brings them there) to m, a float
+  // next to xr's logit
+  float m[NT][2], to[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -626,23 +657,23 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1)
         l[nt][e] += __shfl_xor_sync(kFull, l[nt][e], off);
-      l[nt][e] *= unshift;
-      cr[nt][e] = kPShift - cr[nt][e];  // from here on the reference itself
+      m[nt][e] = fp4_reference(xr[nt][e], sl[nt][e], kPShift, to[nt][e]);
+      l[nt][e] *= to[nt][e];
     }
 
   if constexpr (WP) {
     const int64_t first = static_cast<int64_t>(seq) * a.num_q_heads + kvh * G;
     const int h0 = 2 * c, h1 = 2 * c + 1;
-    const float inv0 = l[0][0] > 0.f ? a.out_scale * unshift / l[0][0] : 0.f;
-    const float inv1 = l[0][1] > 0.f ? a.out_scale * unshift / l[0][1] : 0.f;
+    const float inv0 = l[0][0] > 0.f ? a.out_scale * to[0][0] / l[0][0] : 0.f;
+    const float inv1 = l[0][1] > 0.f ? a.out_scale * to[0][1] / l[0][1] : 0.f;
     const int64_t pr0 = (first + h0) * a.num_parts + part, pr1 = (first + h1) * a.num_parts + part;
     if (g == 0) {
       if (h0 < G) {
-        a.ws_m[pr0] = cr[0][0];
+        a.ws_m[pr0] = m[0][0];
         a.ws_l[pr0] = l[0][0];
       }
       if (h1 < G) {
-        a.ws_m[pr1] = cr[0][1];
+        a.ws_m[pr1] = m[0][1];
         a.ws_l[pr1] = l[0][1];
       }
     }
@@ -672,12 +703,12 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
   for (int nt = 0; nt < NT; ++nt) {
     __syncthreads();
     if (g == 0) {
-      wml[(warp * 8 + 2 * c) * 2 + 0] = cr[nt][0];
+      wml[(warp * 8 + 2 * c) * 2 + 0] = m[nt][0];
       wml[(warp * 8 + 2 * c) * 2 + 1] = l[nt][0];
-      wml[(warp * 8 + 2 * c + 1) * 2 + 0] = cr[nt][1];
+      wml[(warp * 8 + 2 * c + 1) * 2 + 0] = m[nt][1];
       wml[(warp * 8 + 2 * c + 1) * 2 + 1] = l[nt][1];
     }
-    put_acc<D>(wacc + warp * 8 * kAccStride<D>, acc[nt], unshift, unshift, g, c);
+    put_acc<D>(wacc + warp * 8 * kAccStride<D>, acc[nt], to[nt][0], to[nt][1], g, c);
     __syncthreads();
     constexpr int kChunks = D / 8;
     const int cols = min(8, n_rows - 8 * nt);

@@ -67,6 +67,32 @@ __device__ __forceinline__ float e4m3_to_float(uint32_t b) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
 }
 
+// Logits of any size.  A probability is 2^((x - xr) sl + shift): x a score, xr
+// the row's reference (a score, too), sl > 0 the softmax scale in base 2.  As one
+// fma of x, with shift - xr sl rounded to c, its exponent is off by what c lost,
+// the same for all of the row: up to half a unit of xr sl in its last place, 2^-16
+// at 2^8, but more than fp16's range from 2^27 on.  From kFp4FarLogit on xr is
+// therefore taken off x first (exact, or off by 2^-24 of the difference).
+constexpr float kFp4FarLogit = 256.f;
+
+// The softmax scale of a row as a normal number: small cache scales times small
+// powers of two of a bf16 row may fall below, and 0 x -inf would be NaN.  (What
+// the row's logits then lose is below 2^-90: scores are below 2^35.)  Of a
+// negative scale, the magnitude.
+__device__ __forceinline__ float fp4_normal_scale(float sl) {
+  return fminf(fmaxf(fabsf(sl), 0x1p-126f), 0x1.fffffep127f);
+}
+
+// Sums held relative to the score xr, and times 2^shift, are to be joined with
+// others by logits: returns the float next to xr sl, and in `to` what makes them
+// relative to it.  (Bounded: where the rounding of xr sl is larger than 2^6, logits
+// of other parts cannot be told apart any more finely.)
+__device__ __forceinline__ float fp4_reference(float xr, float sl, float shift, float &to) {
+  const float m = fminf(fmaxf(xr * sl, -0x1.fffffep127f), 0x1.fffffep127f);
+  to = exp2f(fminf(fmaxf(fmaf(xr, sl, -m), -64.f), 64.f) - shift);
+  return m;
+}
+
 // fp32 to the nearest E4M3 code (ties to even, at most 448; NaN stays NaN).
 __device__ __forceinline__ uint32_t float_to_e4m3(float x) {
   return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);

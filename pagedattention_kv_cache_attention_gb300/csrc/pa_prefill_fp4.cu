@@ -55,6 +55,7 @@ constexpr int kShare = 32;  // rows of a step that one widening warp has
 // stays below 2^15 and keeps fp16's precision down to 2^-25 of the maximum: a
 // long context's faint tail keeps its mass.
 constexpr float kPShift = 11.f, kGrowth = 4.f;
+constexpr float kFar = kFp4FarLogit;
 
 #ifndef PA_PREFILL_FP4_KSTAGES
 #define PA_PREFILL_FP4_KSTAGES 3
@@ -185,8 +186,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int steps1 = all1 > 0 ? n_steps : 0;
   const int n_sub = (n_keys + 15) / 16;
 
-  // the softmax threads' row, for the join in a cluster
-  float m_ref = -INFINITY, l = 0.f;
+  // the softmax threads' row, for the join in a cluster: its reference, a score
+  // before the softmax scale, and the scale
+  float x_ref = -INFINITY, l = 0.f, sl2 = a.scale_log2;
   bool row_done = false;  // the row's O is in tensor memory
   if (active && warp >= kSoft0 && warp < kSoft0 + 8) {
     // ------------------------------------------------------------ softmax warps
@@ -197,7 +199,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool row_ok = tok <= t_last;
     const int pos = base_pos + tok;     // keys up to pos are attended to
     const int my_steps = t == 0 ? steps0 : steps1;
-    float sl2 = a.scale_log2;           // this row's softmax scale (base 2)
     // Q and the output move in whole rows: lane ch of a group of kLanes holds
     // unit ch of the row, kRowsAt rows at a time; the rows' offsets from the
     // tile pair's first (in rows of D; -1: past the chunk) are asked of their
@@ -254,9 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           *q_unit(lane, c) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
         }
       }
-      // a small cache scale times a small power of two may fall below the normal
-      // numbers, and 0 x -inf would be NaN (what the row's logits lose is below 2^-90)
-      sl2 = fmaxf(sl2, 0x1p-126f);
+      sl2 = fp4_normal_scale(sl2);
       fence_proxy_async_smem();
       mbar_arrive(q_ready);
     }
@@ -314,16 +313,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int j = 0; j < 7; ++j) t8[j] = fmax3(t22[3 * j], t22[3 * j + 1], t22[3 * j + 2]);
       t8[7] = t22[21];
-      const float tmax = sl2 * fmax3(fmax3(t8[0], t8[1], t8[2]), fmax3(t8[3], t8[4], t8[5]),
-                                     fmaxf(t8[6], t8[7]));  // the scale is positive: same order
-      const float m_new = fmaxf(m_ref, tmax);
-      const bool move = m_new > m_ref + kGrowth;  // includes the first finite max
-      const float alpha = !move ? 1.f : (m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m_new));
+      const float xmax = fmax3(fmax3(t8[0], t8[1], t8[2]), fmax3(t8[3], t8[4], t8[5]),
+                               fmaxf(t8[6], t8[7]));  // the scale is positive: same order
+      const float grow = (xmax - x_ref) * sl2;
+      const bool move = grow > kGrowth;  // includes the first finite max
+      const float alpha = move ? ex2_approx(-grow) : 1.f;
       if (move) {
         l *= alpha;
-        m_ref = m_new;
+        x_ref = xmax;
       }
-      const float neg_m = m_ref == -INFINITY ? 0.f : kPShift - m_ref;
+      const float ref = x_ref == -INFINITY ? 0.f : x_ref;
+      float neg_m = fmaf(-ref, sl2, kPShift);
+      if (__any_sync(kFullMask, fabsf(neg_m) > kFar)) {  // a large logit: see kFp4FarLogit
+#pragma unroll
+        for (int c = 0; c < kPairKeys; ++c) sv[c] -= ref;
+        neg_m = kPShift;
+      }
       const uint64_t scale2 = f2_pack(sl2, sl2), negm2 = f2_pack(neg_m, neg_m);
       uint64_t ls2[4] = {0, 0, 0, 0};  // +0.0f pairs
       uint32_t ph[kPairKeys / 2];
@@ -586,6 +591,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * 256 + kOCol;
       float4 *row = reinterpret_cast<float4 *>(smem + (t * kTcRows + r) * D * 4);
       const int pos = base_pos + t_first + (t * kTcRows + r) / G;
+      float to;  // O and l relative to m, and no longer times 2^kPShift
+      const float m = fp4_reference(x_ref, sl2, kPShift, to);
       tc_fence_after();
 #pragma unroll 1
       for (int cb = 0; cb < D / 32; ++cb) {
@@ -596,10 +603,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           row[(cb * 8 + q) ^ (r & 7)] =
-              row_done ? make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3])
+              row_done ? make_float4(o[4 * q] * to, o[4 * q + 1] * to, o[4 * q + 2] * to,
+                                     o[4 * q + 3] * to)
                        : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      ml[t * kTcRows + r] = make_float2(row_done ? m_ref : -INFINITY, row_done ? l : 0.f);
+      ml[t * kTcRows + r] = row_done ? make_float2(m, l * to) : make_float2(-INFINITY, 0.f);
       tc_fence_before();
     }
     cluster_sync();

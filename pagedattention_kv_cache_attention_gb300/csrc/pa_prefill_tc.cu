@@ -516,15 +516,29 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
       t8[7] = t22[21];
       const float tmax_raw = fmax3(fmax3(t8[0], t8[1], t8[2]), fmax3(t8[3], t8[4], t8[5]),
                                    fmaxf(t8[6], t8[7]));
-      const float tmax = tmax_raw * sl2;  // the scale is positive: same order
-      const float m_new = fmaxf(m_ref, tmax);
-      const bool move = m_new > m_ref + kGrowth;  // includes the first finite max
-      const float alpha = !move ? 1.f : (m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m_new));
-      if (move) {
-        l *= alpha;
-        m_ref = m_new;
+      bool move;  // includes the first finite max
+      float alpha, neg_m;
+      if constexpr (F4) {  // m_ref: a score, before the softmax scale
+        const float grow = (tmax_raw - m_ref) * sl2;
+        move = grow > kGrowth;
+        alpha = move ? ex2_approx(-grow) : 1.f;
+        if (move) m_ref = tmax_raw;
+        const float ref = m_ref == -INFINITY ? 0.f : m_ref;
+        neg_m = fmaf(-ref, sl2, kPShift);
+        if (__any_sync(kFullMask, fabsf(neg_m) > kFp4FarLogit)) {  // a large logit
+#pragma unroll
+          for (int c = 0; c < kPairKeys; ++c) sv[c] -= ref;
+          neg_m = kPShift;
+        }
+      } else {
+        const float tmax = tmax_raw * sl2;  // the scale is positive: same order
+        const float m_new = fmaxf(m_ref, tmax);
+        move = m_new > m_ref + kGrowth;
+        alpha = !move ? 1.f : (m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m_new));
+        if (move) m_ref = m_new;
+        neg_m = m_ref == -INFINITY ? 0.f : -m_ref;
       }
-      const float neg_m = m_ref == -INFINITY ? 0.f : kPShift - m_ref;
+      if (move) l *= alpha;
       // P for the whole step in registers first (s scale - m and the row sum on
       // packed fp32 pairs), so the wait for its buffer below overlaps the math
       const uint64_t scale2 = f2_pack(sl2, sl2);

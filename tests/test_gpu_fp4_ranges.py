@@ -69,3 +69,50 @@ def test_small_scales_with_rows_of_zeros(pa, path, ks, d, bs, dtype):  # noqa: F
 def test_tiny_bf16_queries_at_the_ends_of_the_scales(pa, path, ks):  # noqa: F811
     b, ps = constant_keys(path, 83, 128, 16, "bf16", ks, [2.0 ** -110, 0.0, -2.0 ** -126, 1.0])
     run(pa, b, ps)
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("ks", [2.0 ** 100, 2.0 ** 60, 2.0 ** 28, 2.0 ** 10])
+@pytest.mark.parametrize("d,bs,dtype", [(128, 16, "fp16"), (64, 32, "bf16")])
+def test_large_scales(pa, path, ks, d, bs, dtype):  # noqa: F811
+    """Positive and negative logits up to 2^112, rows of zeros (uniform), and
+    rows of ordinary queries, side by side."""
+    b, ps = constant_keys(path, 81, d, bs, dtype, ks, [1.0, -1.0, 0.0, -3.0, 0.5])
+    run(pa, b, ps)
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("rows", [[1e30, -1e30, 1.0, 0.0], [-1e30], [2.0 ** -110, 0.0, -2.0 ** -120],
+                                  [2.0 ** 20, -2.0 ** 20, 1e10]])
+@pytest.mark.parametrize("d,bs", [(128, 32), (64, 16)])
+def test_bf16_queries_of_any_magnitude(pa, path, rows, d, bs):  # noqa: F811
+    b, ps = constant_keys(path, 82, d, bs, "bf16", 1.0, rows)
+    run(pa, b, ps)
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("d,bs,dtype", [(128, 16, "fp16"), (64, 16, "bf16")])
+def test_a_softmax_on_top_of_a_large_common_logit(pa, path, sign, d, bs, dtype):  # noqa: F811
+    """Half of the dimensions add the same 32,000 or so to every logit, 16 others
+    what tells the keys apart: their sums are exact in fp32 (multiples of 0.5
+    below 2^18), so the differences must come out as if the common part were not."""
+    b, ps = constant_keys(path, 84, d, bs, dtype, 1.0, [1.0])
+    rng = np.random.default_rng(85)
+    codes, scales = F.views(b.kc, bs, d)
+    codes[..., : d // 4] = 0x77 if sign > 0 else 0xFF              # 6 or -6 in the first half
+    codes[..., d // 4:] = rng.integers(0, 256, codes[..., d // 4:].shape)
+    q = np.zeros(d)
+    q[: d // 2] = 512 if d == 128 else 1024
+    q[d // 2: d // 2 + 16] = 1
+    b.q[...] = torch.from_numpy(q).to(b.q.dtype)
+    run(pa, b, ps)
+
+
+@pytest.mark.parametrize("path", [p for p in PATHS if p.startswith("decode")])
+@pytest.mark.parametrize("scale", [-0.125, 0.0, -1e-30])
+def test_decode_takes_scales_of_any_sign(pa, path, scale):  # noqa: F811
+    for dtype in ("fp16", "bf16"):
+        b, ps = constant_keys(path, 86, 64, 16, dtype, 1.0, [1.0, -2.0, 0.0])
+        b.scale = scale
+        run(pa, b, ps)
