@@ -377,7 +377,9 @@ pa_status pa_decode_shared_prefix_fp8(void *out, const void *query,
  * it as src and dst.
  * For all calls: k_scale, v_scale between 2^-100 and 2^100 (PA_ERR_INVALID_ARG
  * otherwise); head_dim 64 or 128; block_size 16 or 32; dtype PA_FP16 or
- * PA_BF16 is the type of the 16-bit tensors.
+ * PA_BF16 is the type of the 16-bit tensors.  The attention calls take tables of
+ * less than 2^31 - 2^17 tokens (max_blocks_per_seq * block_size); more are
+ * PA_ERR_UNSUPPORTED.
  */
 
 /*
@@ -451,8 +453,7 @@ pa_status pa_decode_fp4(void *out, const void *query,
  * pa_prefill_fp4 -- pa_prefill over FP4 caches, the values as in pa_decode_fp4.
  * Arguments, shapes and error behaviour as pa_prefill_fp8; max_q_len (or
  * max_blocks_per_seq * block_size, if that is less) above 65535 * (256 / group)
- * tokens, group = num_q_heads / num_kv_heads, or a table of 2^31 tokens or
- * more: PA_ERR_UNSUPPORTED.
+ * tokens, group = num_q_heads / num_kv_heads: PA_ERR_UNSUPPORTED.
  */
 pa_status pa_prefill_fp4(void *out, const void *query, const int32_t *query_start,
                          const void *k_cache, const void *v_cache,

@@ -50,13 +50,14 @@ bool fp4_scales_ok(float k_scale, float v_scale) {
   return k_scale >= lo && k_scale <= hi && v_scale >= lo && v_scale <= hi;
 }
 // TMA row coordinates of an FP4 pool (9 rows for 8 tokens) are 32-bit, and so
-// is the arithmetic on token indexes, a step or two past the table's end.
+// is the arithmetic on token indexes, kFp4LookAhead past the table's end.
 bool fp4_pool_ok(int64_t num_blocks, int32_t num_kv_heads, int32_t block_size,
                  int32_t max_blocks_per_seq) {
   if (num_blocks <= 0 || num_kv_heads <= 0 || block_size <= 0) return true;  // refused elsewhere
   return num_blocks < (int64_t(1) << 31) &&
          num_blocks * num_kv_heads < (int64_t(1) << 31) / (block_size * 9 / 8 + 1) &&
-         static_cast<int64_t>(max_blocks_per_seq) * block_size < (int64_t(1) << 31) - 8192;
+         static_cast<int64_t>(max_blocks_per_seq) * block_size <
+             (int64_t(1) << 31) - pa::kFp4LookAhead;
 }
 bool head_dim_ok(int32_t d) { return d == 64 || d == 128; }
 bool block_size_ok(int32_t b) { return b == 16 || b == 32; }

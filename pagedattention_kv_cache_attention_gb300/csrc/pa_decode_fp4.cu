@@ -819,6 +819,9 @@ cudaError_t launch_rows(DecodeArgs a, const CUtensorMap &km, const CUtensorMap &
   static_assert((static_cast<size_t>(NW) * (kAccStride<D> + 2) + NT * (D + 2)) * 32 + 16 <= stages,
                 "merge buffers and the join flag must fit in the stage area");
   static_assert(smem <= 227 * 1024, "shared memory");
+  static_assert((64 / Fp4Shape<D, BS>::kTiles * NW * (kParts ? 1 : kFp4Cluster) + 1) * 32 <=
+                    kFp4LookAhead,
+                "token indexes past the end of the longest table");
   auto kern = pa_decode_fp4_kernel<T, D, BS, NW, S, ROWS, NT>;
   static SmemLimitOnce smem_limit;
   const cudaError_t e = smem_limit.ensure(kern, smem);
@@ -848,7 +851,7 @@ cudaError_t launch_rows(DecodeArgs a, const CUtensorMap &km, const CUtensorMap &
 int cluster_of(const DecodeArgs &a, int64_t ctas, int warps, int per_sm) {
   const int64_t steps = (static_cast<int64_t>(a.max_blocks_per_seq) << a.bs_log2) / 32;
   int n = 1;
-  while (n < 8 && 2 * n * ctas <= 152 * per_sm && steps >= 4 * n * warps) n *= 2;
+  while (n < kFp4Cluster && 2 * n * ctas <= 152 * per_sm && steps >= 4 * n * warps) n *= 2;
   return n;
 }
 

@@ -205,6 +205,12 @@ cudaError_t launch_prefill_fp4(const PrefillArgs &a, const CUtensorMap &km, cons
                                int head_dim, int dtype, cudaStream_t stream);
 // pa_prefill_fp4 for chunks of at most kMaxChunkRows (token, head) rows a KV head.
 constexpr int kMaxChunkRows = 24;
+// Tokens past a sequence's end whose indexes these two kernels form: two windows
+// of 32 tiles of each warp, a tile or two to a 32-token step, the warps of up to
+// kFp4Cluster CTAs taking the steps in turn (65,536 tokens at block size 32, 8,192
+// where the CTAs are one).  Tables end that far below 2^31 tokens.
+constexpr int64_t kFp4LookAhead = int64_t(1) << 17;
+constexpr int kFp4Cluster = 8;
 cudaError_t launch_chunk_fp4(const DecodeArgs &a, const void *k_cache, const void *v_cache,
                              int head_dim, int dtype, cudaStream_t stream, bool *map_failed);
 cudaError_t launch_reduce(const ReduceArgs &a, int head_dim, int dtype, cudaStream_t stream);
