@@ -163,7 +163,8 @@ size_t pa_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t h
  * partitions; otherwise by pa_decode_reduce on the same stream.
  * max_context_len must be >= every context_lens[i] (sizes the launch).
  * Pointers (out, query, caches) 16-byte aligned; head_dim in {64, 128};
- * block_size in {16, 32}; num_q_heads / num_kv_heads in 1..8.
+ * block_size in {16, 32}; num_q_heads / num_kv_heads in 1..8.  Pools of
+ * num_blocks * num_kv_heads * block_size rows below 2^31 (all attention calls).
  * The caches are read-only here; out must not overlap any input.
  */
 pa_status pa_decode(void *out, const void *query,

@@ -49,18 +49,20 @@ bool fp4_scales_ok(float k_scale, float v_scale) {
   const float lo = 0x1p-100f, hi = 0x1p100f;
   return k_scale >= lo && k_scale <= hi && v_scale >= lo && v_scale <= hi;
 }
-// TMA row coordinates of an FP4 pool (9 rows for 8 tokens) are 32-bit, and so
-// is the arithmetic on token indexes, kFp4LookAhead past the table's end.
-bool fp4_pool_ok(int64_t num_blocks, int32_t num_kv_heads, int32_t block_size,
-                 int32_t max_blocks_per_seq) {
-  if (num_blocks <= 0 || num_kv_heads <= 0 || block_size <= 0) return true;  // refused elsewhere
-  return num_blocks < (int64_t(1) << 31) &&
-         num_blocks * num_kv_heads < (int64_t(1) << 31) / (block_size * 9 / 8 + 1) &&
+bool head_dim_ok(int32_t d) { return d == 64 || d == 128; }
+bool block_size_ok(int32_t b) { return b == 16 || b == 32; }
+// TMA row coordinates are 32-bit: fewer than 2^31 token rows in a pool (of an FP4
+// pool, 9 lines for 16 of them).  block_size: 16 or 32.
+bool pool_ok(int64_t num_blocks, int32_t num_kv_heads, int32_t block_size) {
+  constexpr int64_t kRows = int64_t(1) << 31;
+  return num_blocks < kRows && num_blocks * num_kv_heads < kRows / block_size;
+}
+// FP4 attention forms token indexes kFp4LookAhead past the table's end, in 32 bits.
+bool fp4_table_ok(int32_t block_size, int32_t max_blocks_per_seq) {
+  return !block_size_ok(block_size) ||  // refused elsewhere
          static_cast<int64_t>(max_blocks_per_seq) * block_size <
              (int64_t(1) << 31) - pa::kFp4LookAhead;
 }
-bool head_dim_ok(int32_t d) { return d == 64 || d == 128; }
-bool block_size_ok(int32_t b) { return b == 16 || b == 32; }
 
 int32_t num_partitions(int32_t max_context_len, int32_t partition_size) {
   if (partition_size <= 0 || max_context_len <= partition_size) return 1;
@@ -240,9 +242,8 @@ int32_t pa::decode_check_args(const void *out, const void *query, const void *k_
     return PA_ERR_INVALID_ARG;
   if (!aligned16(out) || !aligned16(query) || !aligned16(k_cache) || !aligned16(v_cache))
     return PA_ERR_INVALID_ARG;
-  // TMA row coordinates are 32-bit; grid y/z are 16-bit
-  const int64_t pool_rows = num_blocks * num_kv_heads * block_size;
-  if (pool_rows >= (int64_t(1) << 31) || num_seqs > 65535 || num_kv_heads > 65535)
+  // grid y/z are 16-bit
+  if (!pool_ok(num_blocks, num_kv_heads, block_size) || num_seqs > 65535 || num_kv_heads > 65535)
     return PA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7fffffff)
     return PA_ERR_UNSUPPORTED;
@@ -482,8 +483,7 @@ pa_status prefill_check_args(const void *out, const void *query, const int32_t *
     return PA_ERR_INVALID_ARG;
   if (!aligned16(out) || !aligned16(query) || !aligned16(k_cache) || !aligned16(v_cache))
     return PA_ERR_INVALID_ARG;
-  if (num_blocks * num_kv_heads * block_size >= (int64_t(1) << 31) || num_seqs > 65535 ||
-      num_kv_heads > 65535)
+  if (!pool_ok(num_blocks, num_kv_heads, block_size) || num_seqs > 65535 || num_kv_heads > 65535)
     return PA_ERR_UNSUPPORTED;
   return PA_OK;
 }
@@ -501,10 +501,9 @@ pa_status prefill_impl(void *out, const void *query, const int32_t *query_start,
   if (st != PA_OK || num_seqs == 0 || max_q_len == 0) return st;
   const int32_t group = num_q_heads / num_kv_heads;
   const int64_t pool_rows = num_blocks * num_kv_heads * block_size;
-  // FP4: positions are 32-bit, and the tiles of a chunk the grid's second dimension
+  // FP4: the tiles of a chunk are the grid's second dimension
   const int64_t room = static_cast<int64_t>(max_blocks_per_seq) * block_size;
-  if (kv == pa::Kv::kFp4 && (room > 0x7fffffff || std::min<int64_t>(max_q_len, room) >
-                                                      int64_t{65535} * (256 / group)))
+  if (kv == pa::Kv::kFp4 && std::min<int64_t>(max_q_len, room) > int64_t{65535} * (256 / group))
     return PA_ERR_UNSUPPORTED;
   unsigned int *err = nullptr;
   if (error_word(&err) != cudaSuccess) return PA_ERR_CUDA;
@@ -643,8 +642,7 @@ pa_status pa_decode_fp4(void *out, const void *query, const void *k_cache, const
                         int32_t max_context_len, int32_t partition_size, void *workspace,
                         size_t workspace_bytes, int32_t dtype, void *stream) {
   if (!fp4_scales_ok(k_scale, v_scale)) return PA_ERR_INVALID_ARG;
-  if (!fp4_pool_ok(num_blocks, num_kv_heads, block_size, max_blocks_per_seq))
-    return PA_ERR_UNSUPPORTED;
+  if (!fp4_table_ok(block_size, max_blocks_per_seq)) return PA_ERR_UNSUPPORTED;
   return decode_impl(out, query, k_cache, v_cache, block_tables, max_blocks_per_seq,
                      context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                      num_blocks, scale, max_context_len, partition_size, workspace,
@@ -659,8 +657,7 @@ pa_status pa_prefill_fp4(void *out, const void *query, const int32_t *query_star
                          int64_t num_blocks, float scale, float k_scale, float v_scale,
                          int32_t dtype, void *stream) {
   if (!fp4_scales_ok(k_scale, v_scale)) return PA_ERR_INVALID_ARG;
-  if (!fp4_pool_ok(num_blocks, num_kv_heads, block_size, max_blocks_per_seq))
-    return PA_ERR_UNSUPPORTED;
+  if (!fp4_table_ok(block_size, max_blocks_per_seq)) return PA_ERR_UNSUPPORTED;
   return prefill_impl(out, query, query_start, k_cache, v_cache, block_tables, max_blocks_per_seq,
                       context_lens, num_seqs, max_q_len, num_q_heads, num_kv_heads, head_dim,
                       block_size, num_blocks, scale, dtype, pa::Kv::kFp4, k_scale, v_scale,

@@ -75,3 +75,17 @@ def test_prefill_windows_stay_within_32_bits(lib):  # noqa: F811
         steps = -(-most // 64)
         last = ((steps - 1) * tiles // 32 * 32 + 31) // tiles
         assert last * 64 + 64 < 2 ** 31
+
+
+@pytest.mark.parametrize("name", ATTENTION)
+@pytest.mark.parametrize("bs", [477218587, 954437175, 2 ** 31 - 1, 2 ** 30, 64, 17, 0, -16])
+def test_any_other_block_size_is_refused(lib, name, bs):  # noqa: F811
+    """The first two are block sizes that a 32-bit product with 9 wraps to a divisor of zero for."""
+    assert status(lib, name, bs=bs) == 2
+
+
+@pytest.mark.parametrize("name", ATTENTION)
+@pytest.mark.parametrize("bs", [16, 32])
+def test_largest_pool(lib, name, bs):  # noqa: F811
+    for nb in (2 ** 31 // (8 * bs), 2 ** 31, 2 ** 59, 2 ** 60, 2 ** 63 - 1):
+        assert status(lib, name, bs=bs, NB=nb, Hkv=8) == 2
