@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(NW * 32)
   // length arrives (entries past the sequence are read from the table row but
   // never used).
   const int t_begin = part * a.part_tokens;
-  const int full_sub = (a.part_tokens + kTile - 1) / kTile;
+  const int full_sub = (a.part_tokens - 1) / kTile + 1;
   const int32_t *bt_row = a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq;
   const int bs_mask = (1 << a.bs_log2) - 1;
   auto sub_of = [&](int l) {
@@ -193,7 +193,8 @@ __global__ void __launch_bounds__(NW * 32)
   auto table_entry = [&](int l) -> int {
     const int u = sub_of(l);
     if (u >= full_sub) return -1;
-    const int lb = (t_begin + u * kTile) >> a.bs_log2;
+    // (max_context_len may be any int: token indexes past a table's end pass 2^31)
+    const int lb = static_cast<int>((static_cast<unsigned>(t_begin) + u * kTile) >> a.bs_log2);
     return lb < a.max_blocks_per_seq ? bt_row[lb] : -1;
   };
   int win = table_entry(lane);
@@ -207,13 +208,13 @@ __global__ void __launch_bounds__(NW * 32)
   if (part > 0 && t_begin >= ctx) return;  // partition past the end: nothing to write
   // partitions of this sequence that have tokens (partition 0 also stands for
   // an empty context)
-  const int np_seq = ctx > 0 ? (ctx + a.part_tokens - 1) / a.part_tokens : 1;
+  const int np_seq = ctx > 0 ? (ctx - 1) / a.part_tokens + 1 : 1;
   // partitions [0, first) lie inside a prefix the sequence shares with its
   // group, and the shared-prefix kernel has written their partials; the last
   // partition always stays here, so some CTA of this grid joins
   const int first = min(max(prefix_len, 0) / a.part_tokens, np_seq - 1);
   if (part < first) return;
-  const int t_end = min(ctx, t_begin + a.part_tokens);
+  const int t_end = t_begin + min(ctx - t_begin, a.part_tokens);
   const int n_sub = t_end > t_begin ? (t_end - t_begin + kTile - 1) / kTile : 0;
   const int n_grp = (n_sub + NSUB - 1) / NSUB;
   // this warp's steps
@@ -615,7 +616,7 @@ __global__ void __launch_bounds__(kReduceWarps * 32) pa_decode_reduce_kernel(con
       if (lane == 0 && j == 0 && row % a.num_q_heads == 0) atomicOr(a.err, kErrBadLen);
       ctx = 0;
     }
-    np = ctx > 0 ? (ctx + a.partition_size - 1) / a.partition_size : 0;
+    np = ctx > 0 ? (ctx - 1) / a.partition_size + 1 : 0;
   }
   const int64_t rr = row_ok ? row : 0;
   const float *m = a.ws_m + rr * a.num_parts;

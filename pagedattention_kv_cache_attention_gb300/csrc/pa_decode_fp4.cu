@@ -231,8 +231,14 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
   const int base = t_begin & ~31;
   const int32_t *bt_row = a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq;
   const int wid = rank * NW + warp, n_warps = NW * cluster;
-  auto step_token = [&](int k) { return base + (WP ? k : wid + k * n_warps) * 32; };
-  auto block_of = [&](int l) { return step_token(l / kTiles) / BS + l % kTiles; };
+  // (unsigned: max_context_len may be any int, and with it a partition past the
+  // table's end may pass 2^31)
+  auto step_token = [&](int k) {
+    return static_cast<unsigned>(base) + (WP ? k : wid + k * n_warps) * 32;
+  };
+  auto block_of = [&](int l) {
+    return static_cast<int>(step_token(l / kTiles) / BS) + l % kTiles;
+  };
   auto table_entry = [&](int l) -> int {
     const int lb = block_of(l);
     return lb < a.max_blocks_per_seq ? bt_row[lb] : -1;
@@ -257,8 +263,8 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
     ctx = 0;
   }
   if (part > 0 && t_begin >= ctx) return;
-  const int np_seq = kParts && ctx > 0 ? (ctx + a.part_tokens - 1) / a.part_tokens : 1;
-  const int t_end = kParts ? min(ctx, t_begin + a.part_tokens) : ctx;
+  const int np_seq = kParts && ctx > 0 ? (ctx - 1) / a.part_tokens + 1 : 1;
+  const int t_end = kParts ? t_begin + min(ctx - t_begin, a.part_tokens) : ctx;
   const int n_step = t_end > base ? (t_end - base + 31) / 32 : 0;
   const int my_n = WP ? n_step : (n_step > wid ? (n_step - wid + n_warps - 1) / n_warps : 0);
 

@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
           int c = a.context_lens[m0 + i];
           // the decode kernel flags a bad length; here it only means "nothing shared"
           if (c < 0 || c > (a.max_blocks_per_seq << a.bs_log2) || c > a.max_context_len) c = 0;
-          const int np = c > 0 ? (c + P - 1) / P : 1;
+          const int np = c > 0 ? (c - 1) / P + 1 : 1;
           const int pl = a.prefix_lens[m0 + i];
           if (pl != a.prefix_lens[g0] && reporter) atomicOr(a.err, kErrPrefix);
           first = min(max(pl, 0) / P, np - 1);
