@@ -167,12 +167,13 @@ constexpr int ctas_per_sm(int tiles) {
 //                partial itself (partitions joined by the reduce kernel), as in
 //                the 16-bit kernel
 //  kWhole        the heads of one query over its whole context, no partitions
-//  kChunk        the rows of a short chunk, (token, head) pairs with token = row /
-//                G, at most 8 NT of them
+//  kChunk        rows of a short chunk, (token, head) pairs with token = row /
+//                G, the CTA's from row 8 NT group on; the warps share the keys
+//                up to its last row's
 // In a call without partitions (kWhole, kChunk) the warps of a.cluster CTAs share
-// the keys, and the CTAs join through one another's shared memory: a long context
-// then takes a cluster's time and not a CTA's, and CTAs of unequal contexts fill
-// the SMs more evenly.
+// the keys, and the CTAs join through one another's
+// shared memory: a long context then takes a cluster's time and not a CTA's,
+// and CTAs of unequal contexts fill the SMs more evenly.
 template <typename T, int D, int BS, int NW, int S, Rows ROWS, int NT>
 __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
     pa_decode_fp4_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -839,14 +840,14 @@ cudaError_t launch_rows(DecodeArgs a, const CUtensorMap &km, const CUtensorMap &
   // against 117, since every empty partition's CTA asks for its sequence too.
   const int64_t ctas = static_cast<int64_t>(grid_x) * a.num_kv_heads * a.num_seqs;
   a.by_length = !kParts && a.cluster == 1 &&
-                a.num_seqs > 1 && a.num_seqs <= kMaxByLength && ctas > kSms * ctas_per_sm(NT) &&
+                a.num_seqs > 1 && a.num_seqs <= kMaxByLength && ctas > 152 * ctas_per_sm(NT) &&
                 (static_cast<int64_t>(a.max_blocks_per_seq) << a.bs_log2) >= kMinByLength &&
                 (ROWS == Rows::kChunk || a.max_context_len >= kMinByLength);
   return launch_clusters(a.cluster, kern, dim3(grid_x, a.num_kv_heads, a.num_seqs),
                          dim3(NW * 32), smem, stream, km, vm, a);
 }
 
-// How many CTAs share the keys of a sequence and KV head in a call without partitions: as many
+// How many CTAs share a row group's keys in a call without partitions: as many
 // as the SMs still have room for, while a warp keeps two steps of the longest
 // context that the table can hold.  Few sequences gain (one of 8,000 tokens and
 // one KV head 20 us, with one CTA 93; eight KV heads of 4,096 tokens 11 against
@@ -856,7 +857,7 @@ cudaError_t launch_rows(DecodeArgs a, const CUtensorMap &km, const CUtensorMap &
 int cluster_of(const DecodeArgs &a, int64_t ctas, int warps, int per_sm) {
   const int64_t steps = (static_cast<int64_t>(a.max_blocks_per_seq) << a.bs_log2) / 32;
   int n = 1;
-  while (n < kFp4Cluster && 2 * n * ctas <= kSms * per_sm && steps >= 4 * n * warps) n *= 2;
+  while (n < kFp4Cluster && 2 * n * ctas <= 152 * per_sm && steps >= 4 * n * warps) n *= 2;
   return n;
 }
 
