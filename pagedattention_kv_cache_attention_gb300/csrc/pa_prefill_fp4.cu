@@ -1,6 +1,8 @@
 // pa_prefill_fp4.cu -- chunked-prefill attention over the FP4 cache on the
-// fifth-generation tensor core, for chunks that fill more than one 128-row tile
-// (pa_prefill_fp4; shorter chunks run in pa_decode_fp4.cu and pa_prefill_tc.cu).
+// fifth-generation tensor core, for chunks of more than 64 (token, head) rows a KV
+// head, and for shorter ones down to 25 rows where the (sequence, KV head) pairs
+// are fewer than two for each SM (pa_prefill_fp4; the others run in
+// pa_prefill_tc.cu, those of at most 24 rows in pa_decode_fp4.cu).
 //
 // The arithmetic is pa_prefill_tc.cu's: two 128-row query tiles of one
 // (sequence, KV head) per CTA, rows (token, head), 64-key steps; S = Q K^T and
@@ -50,7 +52,6 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kShare = 32;  // rows of a step that one widening warp has
 // P is held times 2^11 with the running maximum at most 2^4 behind, so that it
 // stays below 2^15 and keeps fp16's precision down to 2^-25 of the maximum: a
 // long context's faint tail keeps its mass.
@@ -80,6 +81,7 @@ template <int D> struct Layout {
   static constexpr int kQAtom = kTcRows * 128;
   static constexpr int kKAtom = kPairKeys * 128;
   static constexpr int kVAtom = kPairKeys * 128;
+  static_assert(kKAtom == kVAtom, "one widening code for both");
   static constexpr int kRawStep = kPairKeys / 16 * kRawSlot16<D>;
   static constexpr int kKOff = 2 * kAtoms * kQAtom;
   static constexpr int kVOff = kKOff + kSK * kAtoms * kKAtom;
@@ -495,86 +497,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (active) {
     // ------------------------------------------------------------ widening warps
     const bool k_role = (warp & 1) == 0;
-    const int share0 = warp - kLoad0 >= 2 ? kShare : 0;  // the share's first row in a step
-    const int tsh = a.bs_log2 == 4 ? 1 : 0;              // 1 << tsh tiles of a share
-    const uint32_t tile_bytes = fp4_tile_bytes(1 << a.bs_log2, D);
-    const int tile_lines = 9 << (a.bs_log2 - 4);
-    uint64_t *land = raw_land + (warp - kLoad0) * kRaw;
-    uint8_t *raw = smem + L::kRawOff + (k_role ? 0 : kRaw * L::kRawStep) +
-                   (share0 / 16) * kRawSlot16<D>;
-    const CUtensorMap *map = k_role ? &kmap : &vmap;
-    const F4Widen<D> widen(lane, a.bs_log2, k_role ? L::kKAtom : L::kVAtom);
+    uint64_t *full = k_role ? k_full : v_full, *empty = k_role ? k_empty : v_empty;
     const uint64_t policy = l2_policy_evict_normal();  // the chunk's other tiles read it too
-    // block of the warp's tile l (its tiles are numbered over all steps)
-    auto tile_block = [&](int l) -> int {
-      const int key = (step_base + (l >> tsh)) * kPairKeys + share0 + (tsh ? (l & 1) * 16 : 0);
-      if (key >= n_keys) return -1;
-      const int phys = bt_row[key >> a.bs_log2];
-      if (phys < 0 || static_cast<int64_t>(phys) >= a.num_blocks) {
-        atomicOr(a.err, kErrBadBlock);
-        return -1;
-      }
-      return phys;
-    };
-    int win_base = 0, win = tile_block(lane);
-    uint32_t loaded = 0;  // bits 2 rs and up: tiles of the share in raw place rs
-    auto fetch = [&](int m) {
-      const int rs = m % kRaw;
-      if ((m << tsh) >= win_base + 32) {
-        win_base += 32;
-        win = tile_block(win_base + lane);
-      }
-      const int phys = __shfl_sync(kFullMask, win, (m << tsh) + (tsh & lane) - win_base);
-      const uint32_t mask = __ballot_sync(kFullMask, lane < 1 << tsh && phys >= 0);
-      loaded = (loaded & ~(3u << (2 * rs))) | (mask << (2 * rs));
-      if (lane == 0) {
-        if (mask == 0)
-          mbar_arrive(&land[rs]);
-        else
-          mbar_arrive_expect_tx(&land[rs], __popc(mask) * tile_bytes);
-      }
-      __syncwarp();
-      if (lane < 1 << tsh && phys >= 0)
-        tma_load_2d(raw + rs * L::kRawStep + lane * kRawSlot16<D>, map, 0,
-                    (phys * a.num_kv_heads + kvh) * tile_lines, &land[rs], policy);
-    };
-    for (int m = 0; m < min(kRaw, n_steps); ++m) fetch(m);
-    bool ok_run = true;
-    int m = 0;
-    for (; m < n_steps; ++m) {
-      const int rs = m % kRaw;
-      const int S = k_role ? kSK : kSV, s = m % S;
-      uint64_t *full = k_role ? &k_full[s] : &v_full[s];
-      uint64_t *empty = k_role ? &k_empty[s] : &v_empty[s];
-      if (!__all_sync(kFullMask, mbar_wait_bounded(&land[rs], (m / kRaw) & 1) &&
-                                     (m < S || mbar_wait_bounded(empty, ((m / S) - 1) & 1)))) {
-        ok_run = false;
-        break;
-      }
-      const uint32_t ok = (loaded >> (2 * rs)) & 3u;
-      const int past = n_keys - (step_base + m) * kPairKeys - share0;  // the share's first row past the keys
-      uint8_t *st = (k_role ? smem + L::kKOff + s * kAtoms * L::kKAtom
-                            : smem + L::kVOff + s * kAtoms * L::kVAtom) + share0 * 128;
-      const uint8_t *from = raw + rs * L::kRawStep;
-      const int key0 = (step_base + m) * kPairKeys;
-      // V rows that must not contribute become zeros; K's are masked by the softmax
-      if (k_role || (ok == (1u << (1 << tsh)) - 1 && key0 + kPairKeys - 1 <= base_pos + t_first))
-        widen(from, st, [](int, uint32_t sc) { return sc; });
-      else
-        widen(from, st, [&](int r, uint32_t sc) {
-          return r < past && ((ok >> (r >> a.bs_log2)) & 1u)
-                     ? F4Widen<D>::drop_nans(sc, lane, key0 + share0 + r, nan_key)
-                     : 0u;
-        });
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full);
-      if (m + kRaw < n_steps) fetch(m + kRaw);
-    }
-    // after a wait that ran out, copies already in flight land before the CTA
-    // leaves (bounded again)
-    for (int k = m; !ok_run && k < min(m + kRaw, n_steps); ++k)
-      (void)mbar_wait_bounded(&land[k % kRaw], (k / kRaw) & 1);
+    const bool ok_run = f4_widen_share<D, kSK, kSV, kRaw, L::kRawStep, L::kKAtom>(
+        a, k_role ? &kmap : &vmap, bt_row, kvh, lane, k_role,
+        warp - kLoad0 >= 2 ? kF4Share : 0, step_base, n_steps, n_keys, base_pos + t_first + 1, full,
+        empty, raw_land + (warp - kLoad0) * kRaw, smem + (k_role ? L::kKOff : L::kVOff),
+        smem + L::kRawOff + (k_role ? 0 : kRaw * L::kRawStep), nan_key, policy);
     if (!ok_run && lane == 0) atomicOr(a.err, kErrTimeout);
   }
 

@@ -752,8 +752,8 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
     }
   } else if (active && (warp >= kLoad0 || (ROWS == 64 && warp < kIssue0))) {
     // ---------------------------------------------------- TMA producers (K, V)
-    // (and, over FP8 caches at head_dim 128 with two tiles, the K and V
-    // widening helpers)
+    // (and, over FP8 caches at head_dim 128 with two tiles and over FP4 caches,
+    // the K and V widening helpers)
     const bool k_role = (warp & 1) == 0;  // kLoad0 is even
     const bool helper = ROWS == 64 ? warp < kIssue0 : warp - kLoad0 >= 2;
     const int bs_mask = (1 << a.bs_log2) - 1;
@@ -771,97 +771,12 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
     int win = helper || F4 ? -1 : block_of(lane);
     bool ok_run = true;
     if constexpr (F4) {
-      // Each widening warp has its share of every step (64 tokens, or with a
-      // helper 32), which its own copies bring into its part of the raw ring,
-      // kRaw steps ahead; it widens a share into the fp16 stage, hands its
-      // part of the stage over and refills the raw place it has just read.
-      constexpr int kShare = kPairKeys / kWideners, kRaw = L::kRaw;
-      const int share0 = helper ? kShare : 0;  // the share's first row in the step
-      const int tsh = a.bs_log2 == 4 ? (kShare == 64 ? 2 : 1) : (kShare == 64 ? 1 : 0);
-      const int tiles = 1 << tsh;              // tiles of a share
-      const uint32_t tile_bytes = fp4_tile_bytes(1 << a.bs_log2, D);
-      const int tile_lines = 9 << (a.bs_log2 - 4);
-      const int S = k_role ? SK : SV;
-      uint64_t *full = k_role ? k_full : v_full;
-      uint64_t *empty = k_role ? k_empty : v_empty;
-      uint64_t *land = raw_land + ((warp & 1) + (helper ? 2 : 0)) * kRaw;
-      uint8_t *ring = smem + (k_role ? L::kKOff : L::kVOff);
-      uint8_t *raw = smem + L::kRawOff + (k_role ? 0 : kRaw * L::kRawStep);
-      const CUtensorMap *map = k_role ? &kmap : &vmap;
-      // block of the warp's tile l (its tiles are numbered over all steps)
-      auto tile_block = [&](int l) -> int {
-        const int key = (l >> tsh) * kPairKeys + share0 + ((l & (tiles - 1)) << a.bs_log2);
-        if (key >= n_keys) return -1;
-        const int phys = bt_row[key >> a.bs_log2];
-        if (phys < 0 || static_cast<int64_t>(phys) >= a.num_blocks) {
-          atomicOr(a.err, kErrBadBlock);
-          return -1;
-        }
-        return phys;
-      };
-      const F4Widen<D> widen(lane, a.bs_log2, kPairKvAtom);
-      win = tile_block(lane);
-      uint32_t loaded = 0;  // bit 4 rs + i: tile i of the share in raw place rs
-      auto fetch = [&](int m) {
-        const int rs = m % kRaw;
-        if ((m << tsh) >= win_base + 32) {
-          win_base += 32;
-          win = tile_block(win_base + lane);
-        }
-        const int phys = __shfl_sync(kFullMask, win, (m << tsh) + (lane & (tiles - 1)) - win_base);
-        const uint32_t mask = __ballot_sync(kFullMask, lane < tiles && phys >= 0);
-        loaded = (loaded & ~(15u << (4 * rs))) | (mask << (4 * rs));
-        if (lane == 0) {
-          if (mask == 0)
-            mbar_arrive(&land[rs]);
-          else
-            mbar_arrive_expect_tx(&land[rs], __popc(mask) * tile_bytes);
-        }
-        __syncwarp();
-        if (lane < tiles && phys >= 0)
-          tma_load_2d(raw + rs * L::kRawStep + (share0 / 16) * kRawSlot16<D> +
-                          lane * (kRawSlot16<D> << (a.bs_log2 - 4)),
-                      map, 0, (phys * a.num_kv_heads + kvh) * tile_lines, &land[rs], policy);
-      };
-      for (int m = 0; m < min(kRaw, n_steps); ++m) fetch(m);
-      int m = 0;
-      for (; m < n_steps; ++m) {
-        const int rs = m % kRaw, s = m % S;
-        if (!__all_sync(kFullMask, mbar_wait_bounded(&land[rs], (m / kRaw) & 1) &&
-                                       (m < S || mbar_wait_bounded(&empty[s], ((m / S) - 1) & 1)))) {
-          ok_run = false;
-          break;
-        }
-        const uint32_t ok = (loaded >> (4 * rs)) & 15u;
-        const int past = n_keys - m * kPairKeys;  // first row that must not contribute
-        const int key0 = m * kPairKeys;
-        // K rows that must not contribute are masked by the softmax
-        const bool all = k_role || (ok == (1u << tiles) - 1 &&
-                                    key0 + kPairKeys - 1 <= base_pos + t_first);
-        uint8_t *st = ring + s * kAtoms * kPairKvAtom + share0 * 128;
-        const uint8_t *from = raw + rs * L::kRawStep + (share0 / 16) * kRawSlot16<D>;
-#pragma unroll 1
-        for (int r0 = 0; r0 < kShare; r0 += 32) {
-          const int first = r0;
-          if (all)
-            widen(from + (r0 / 16) * kRawSlot16<D>, st + r0 * 128,
-                  [](int, uint32_t sc) { return sc; });
-          else
-            widen(from + (r0 / 16) * kRawSlot16<D>, st + r0 * 128, [&](int r, uint32_t sc) {
-              const int at = share0 + first + r;
-              return at < past && ((ok >> ((first + r) >> a.bs_log2)) & 1u)
-                         ? F4Widen<D>::drop_nans(sc, lane, key0 + at, nan_key)
-                         : 0u;
-            });
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[s]);
-        if (m + kRaw < n_steps) fetch(m + kRaw);
-      }
-      // let copies already in flight land before the CTA leaves (bounded again)
-      for (int k = m; !ok_run && k < min(m + kRaw, n_steps); ++k)
-        (void)mbar_wait_bounded(&land[k % kRaw], (k / kRaw) & 1);
+      ok_run = f4_widen_share<D, SK, SV, L::kRaw, L::kRawStep, kPairKvAtom>(
+          a, k_role ? &kmap : &vmap, bt_row, kvh, lane, k_role, helper ? kF4Share : 0, 0, n_steps,
+          n_keys, base_pos + t_first + 1, k_role ? k_full : v_full, k_role ? k_empty : v_empty,
+          raw_land + ((warp & 1) + (helper ? 2 : 0)) * L::kRaw,
+          smem + (k_role ? L::kKOff : L::kVOff),
+          smem + L::kRawOff + (k_role ? 0 : L::kRaw * L::kRawStep), nan_key, policy);
     } else if constexpr (F8) {
       // A step's copies (16 rows of head_dim codes per sub-tile) land in the
       // upper half of its stage; the warp widens them to fp16 there, clears

@@ -7,6 +7,7 @@
 
 #include "pa_device.cuh"
 #include "pa_fp4.cuh"
+#include "pa_internal.h"
 
 namespace pa {
 
@@ -43,8 +44,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v) {
       : "memory");
 }
 
-// Packed fp32 pairs (sm_100 and later): two IEEE fp32 operations per instruction,
-// each rounded exactly as the scalar one.
 // Non-blocking look at an mbarrier phase (acquire, CTA scope): true once the
 // phase with the given parity has completed.
 __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
@@ -59,6 +58,8 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
   return done != 0;
 }
 
+// Packed fp32 pairs (sm_100 and later): two IEEE fp32 operations per instruction,
+// each rounded exactly as the scalar one.
 __device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
@@ -175,6 +176,94 @@ template <int D> struct F4Widen {
       }
   }
 };
+
+// One widening warp's work: its share, kF4Share rows from share0 on of every 64-key
+// step of K or of V.  Its own copies bring the share's tiles into its part of the
+// raw ring, RAW steps ahead; it widens them into the fp16 stage, hands its part
+// over (full) and refills the raw place that it has just read.  Steps are counted
+// from step_base on.  Of V, rows that must not contribute become zeros (K's are
+// masked by the softmax), and NaNs at keys from all_rows on, which not every row
+// attends to, are noted in nan_key.  False where a wait ran out; copies in flight
+// have then landed or been waited for.
+constexpr int kF4Share = 32;
+template <int D, int SK, int SV, int RAW, int RAW_STEP, int ATOM>
+__device__ __forceinline__ bool f4_widen_share(
+    const PrefillArgs &a, const CUtensorMap *map, const int32_t *bt_row, int kvh, int lane,
+    bool k_role, int share0, int step_base, int n_steps, int n_keys, int all_rows, uint64_t *full,
+    uint64_t *empty, uint64_t *land, uint8_t *ring, uint8_t *raw, int *nan_key, uint64_t policy) {
+  const int tsh = a.bs_log2 == 4 ? 1 : 0;  // 1 << tsh tiles of a share
+  const uint32_t tile_bytes = fp4_tile_bytes(1 << a.bs_log2, D);
+  const int tile_lines = 9 << (a.bs_log2 - 4);
+  const F4Widen<D> widen(lane, a.bs_log2, ATOM);
+  raw += share0 / 16 * kRawSlot16<D>;
+  // block of the warp's tile l (its tiles are numbered over all steps)
+  auto tile_block = [&](int l) -> int {
+    const int key = (step_base + (l >> tsh)) * kPairKeys + share0 + (tsh ? (l & 1) * 16 : 0);
+    if (key >= n_keys) return -1;
+    const int phys = bt_row[key >> a.bs_log2];
+    if (phys < 0 || static_cast<int64_t>(phys) >= a.num_blocks) {
+      atomicOr(a.err, kErrBadBlock);
+      return -1;
+    }
+    return phys;
+  };
+  int win_base = 0, win = tile_block(lane);
+  uint32_t loaded = 0;  // bits 2 rs and up: tiles of the share in raw place rs
+  auto fetch = [&](int m) {
+    const int rs = m % RAW;
+    if ((m << tsh) >= win_base + 32) {
+      win_base += 32;
+      win = tile_block(win_base + lane);
+    }
+    const int phys = __shfl_sync(kFullMask, win, (m << tsh) + (tsh & lane) - win_base);
+    const uint32_t mask = __ballot_sync(kFullMask, lane < 1 << tsh && phys >= 0);
+    loaded = (loaded & ~(3u << (2 * rs))) | (mask << (2 * rs));
+    if (lane == 0) {
+      if (mask == 0)
+        mbar_arrive(&land[rs]);
+      else
+        mbar_arrive_expect_tx(&land[rs], __popc(mask) * tile_bytes);
+    }
+    __syncwarp();
+    if (lane < 1 << tsh && phys >= 0)
+      tma_load_2d(raw + rs * RAW_STEP + lane * kRawSlot16<D>, map, 0,
+                  (phys * a.num_kv_heads + kvh) * tile_lines, &land[rs], policy);
+  };
+  for (int m = 0; m < min(RAW, n_steps); ++m) fetch(m);
+  bool ok_run = true;
+  int m = 0;
+  for (; m < n_steps; ++m) {
+    const int rs = m % RAW;
+    const int S = k_role ? SK : SV, s = m % S;
+    if (!__all_sync(kFullMask, mbar_wait_bounded(&land[rs], (m / RAW) & 1) &&
+                                   (m < S || mbar_wait_bounded(&empty[s], ((m / S) - 1) & 1)))) {
+      ok_run = false;
+      break;
+    }
+    const uint32_t ok = (loaded >> (2 * rs)) & 3u;
+    const int key0 = (step_base + m) * kPairKeys;
+    const int past = n_keys - key0 - share0;  // the share's first row past the keys
+    uint8_t *st = ring + s * (D / 64) * ATOM + share0 * 128;
+    const uint8_t *from = raw + rs * RAW_STEP;
+    if (k_role || (ok == (1u << (1 << tsh)) - 1 && key0 + kPairKeys <= all_rows))
+      widen(from, st, [](int, uint32_t sc) { return sc; });
+    else
+      widen(from, st, [&](int r, uint32_t sc) {
+        return r < past && ((ok >> (r >> a.bs_log2)) & 1u)
+                   ? F4Widen<D>::drop_nans(sc, lane, key0 + share0 + r, nan_key)
+                   : 0u;
+      });
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&full[s]);
+    if (m + RAW < n_steps) fetch(m + RAW);
+  }
+  // after a wait that ran out, copies already in flight land before the CTA
+  // leaves (bounded again)
+  for (int k = m; !ok_run && k < min(m + RAW, n_steps); ++k)
+    (void)mbar_wait_bounded(&land[k % RAW], (k / RAW) & 1);
+  return ok_run;
+}
 
 // 32 output values of a row, from dimension 32 cb on: NaN where the row attends
 // to a key whose V has a NaN scale there (what drop_nans noted; pos: the row's
