@@ -104,14 +104,9 @@ __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Thread-block clusters: the CTA's rank, a barrier over the cluster's CTAs
-// (release / acquire of shared memory), and reads of another CTA's shared
-// memory at the address that `p` has in this one.
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
+// Thread-block clusters: a barrier over the cluster's CTAs (release / acquire of
+// shared memory), and reads of another CTA's shared memory at the address that `p`
+// has in this one.
 __device__ __forceinline__ void cluster_sync() {
   __syncwarp();  // the instructions below are for a converged warp
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");

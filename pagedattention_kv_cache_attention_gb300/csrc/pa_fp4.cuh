@@ -25,7 +25,6 @@
 
 namespace pa {
 
-constexpr int kFp4Group = 16;           // elements that share a scale
 constexpr uint32_t kFp4NanScale = 0x7f;  // E4M3 NaN: the scale of a group with a NaN in it
 
 // Bytes of one (block, KV head) tile, and of its codes.
