@@ -167,13 +167,12 @@ constexpr int ctas_per_sm(int tiles) {
 //                partial itself (partitions joined by the reduce kernel), as in
 //                the 16-bit kernel
 //  kWhole        the heads of one query over its whole context, no partitions
-//  kChunk        rows of a short chunk, (token, head) pairs with token = row /
-//                G, the CTA's from row 8 NT group on; the warps share the keys
-//                up to its last row's
+//  kChunk        the rows of a short chunk, (token, head) pairs with token = row /
+//                G, at most 8 NT of them
 // In a call without partitions (kWhole, kChunk) the warps of a.cluster CTAs share
-// the keys, and the CTAs join through one another's
-// shared memory: a long context then takes a cluster's time and not a CTA's,
-// and CTAs of unequal contexts fill the SMs more evenly.
+// the keys, and the CTAs join through one another's shared memory: a long context
+// then takes a cluster's time and not a CTA's, and CTAs of unequal contexts fill
+// the SMs more evenly.
 template <typename T, int D, int BS, int NW, int S, Rows ROWS, int NT>
 __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
     pa_decode_fp4_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -847,7 +846,7 @@ cudaError_t launch_rows(DecodeArgs a, const CUtensorMap &km, const CUtensorMap &
                          dim3(NW * 32), smem, stream, km, vm, a);
 }
 
-// How many CTAs share a row group's keys in a call without partitions: as many
+// How many CTAs share the keys of a sequence and KV head in a call without partitions: as many
 // as the SMs still have room for, while a warp keeps two steps of the longest
 // context that the table can hold.  Few sequences gain (one of 8,000 tokens and
 // one KV head 20 us, with one CTA 93; eight KV heads of 4,096 tokens 11 against

@@ -199,8 +199,8 @@ cudaError_t launch_decode(const DecodeArgs &a, const void *k_cache, const void *
                           cudaStream_t stream, bool *map_failed);
 cudaError_t launch_decode_fp4(const DecodeArgs &a, const void *k_cache, const void *v_cache,
                               int head_dim, int dtype, cudaStream_t stream, bool *map_failed);
-// pa_prefill_fp4 for chunks of more than one 128-row tile (maps of whole tiles,
-// not swizzled).
+// pa_prefill_fp4 on two 128-row tiles a CTA: chunks of more than 64 rows, or of
+// fewer where there are few of them (maps of whole tiles, not swizzled).
 cudaError_t launch_prefill_fp4(const PrefillArgs &a, const CUtensorMap &km, const CUtensorMap &vm,
                                int head_dim, int dtype, cudaStream_t stream);
 // pa_prefill_fp4 for chunks of at most kMaxChunkRows (token, head) rows a KV head.
