@@ -221,7 +221,7 @@ cudaError_t launch(K kern, const Fp4CacheArgs &a, cudaStream_t stream) {
   const int items = a.num_kv_heads * (a.head_dim / 8);
   const int per_cta = kWarps * (items < 32 ? 32 / items : 1);
   const int64_t ctas = (static_cast<int64_t>(a.num_tokens) + per_cta - 1) / per_cta;
-  const int64_t most = 152 * PA_CACHE_FP4_CTAS;  // then a warp takes several tokens in turn
+  const int64_t most = kSms * PA_CACHE_FP4_CTAS;  // then a warp takes several tokens in turn
   return launch_dependent(kern, dim3(static_cast<unsigned>(ctas < most ? ctas : most)),
                           dim3(kWarps * 32), 0, stream, a);
 }

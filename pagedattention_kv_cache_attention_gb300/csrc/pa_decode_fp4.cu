@@ -839,7 +839,7 @@ cudaError_t launch_rows(DecodeArgs a, const CUtensorMap &km, const CUtensorMap &
   // against 117, since every empty partition's CTA asks for its sequence too.
   const int64_t ctas = static_cast<int64_t>(grid_x) * a.num_kv_heads * a.num_seqs;
   a.by_length = !kParts && a.cluster == 1 &&
-                a.num_seqs > 1 && a.num_seqs <= kMaxByLength && ctas > 152 * ctas_per_sm(NT) &&
+                a.num_seqs > 1 && a.num_seqs <= kMaxByLength && ctas > kSms * ctas_per_sm(NT) &&
                 (static_cast<int64_t>(a.max_blocks_per_seq) << a.bs_log2) >= kMinByLength &&
                 (ROWS == Rows::kChunk || a.max_context_len >= kMinByLength);
   return launch_clusters(a.cluster, kern, dim3(grid_x, a.num_kv_heads, a.num_seqs),
@@ -856,7 +856,7 @@ cudaError_t launch_rows(DecodeArgs a, const CUtensorMap &km, const CUtensorMap &
 int cluster_of(const DecodeArgs &a, int64_t ctas, int warps, int per_sm) {
   const int64_t steps = (static_cast<int64_t>(a.max_blocks_per_seq) << a.bs_log2) / 32;
   int n = 1;
-  while (n < kFp4Cluster && 2 * n * ctas <= 152 * per_sm && steps >= 4 * n * warps) n *= 2;
+  while (n < kFp4Cluster && 2 * n * ctas <= kSms * per_sm && steps >= 4 * n * warps) n *= 2;
   return n;
 }
 

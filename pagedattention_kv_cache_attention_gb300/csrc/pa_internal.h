@@ -12,6 +12,7 @@
 namespace pa {
 
 constexpr int kMaxDevices = 64;
+constexpr int kSms = 152;  // of a GB300
 
 // What the caches hold: fp16 / bf16 elements, E4M3 codes, or FP4 tiles (pa_fp4.cuh).
 enum class Kv { k16, kFp8, kFp4 };

@@ -600,7 +600,7 @@ cudaError_t launch_t(const PrefillArgs &a, const CUtensorMap &km, const CUtensor
   const int64_t tiles = (b.max_q_len - 1) / tpc + 1;
   const int64_t ctas = tiles * a.num_kv_heads * a.num_seqs, steps = room / kPairKeys;
   b.chunks = 1;
-  while (b.chunks < 8 && 2 * b.chunks * ctas <= 152 && steps >= 8 * b.chunks) b.chunks *= 2;
+  while (b.chunks < 8 && 2 * b.chunks * ctas <= kSms && steps >= 8 * b.chunks) b.chunks *= 2;
   return launch_clusters(b.chunks, kern,
                          dim3(a.num_kv_heads * b.chunks, static_cast<unsigned>(tiles), a.num_seqs),
                          dim3(kThreads), smem, stream, km, vm, b);

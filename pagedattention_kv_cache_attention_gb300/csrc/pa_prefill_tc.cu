@@ -1066,7 +1066,7 @@ cudaError_t launch_prefill_tc_d(const PrefillArgs &a, const CUtensorMap &km,
     // whose steps are shorter (80 rows of the same batch 127 us; a one-tile
     // kernel took 176), and which shares a sequence's keys in a cluster.
     if (static_cast<int64_t>(a.max_q_len) * a.group > 64 ||
-        static_cast<int64_t>(a.num_seqs) * a.num_kv_heads < 2 * 152)
+        static_cast<int64_t>(a.num_seqs) * a.num_kv_heads < 2 * kSms)
       return launch_prefill_fp4(a, km, vm, D, dtype, stream);
     return dtype == 0
                ? launch_prefill_tc_pair_t<__half, D, SK, SV, false, 1, false, Kv::kFp4, 64>(
