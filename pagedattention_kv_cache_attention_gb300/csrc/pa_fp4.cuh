@@ -84,11 +84,12 @@ __device__ __forceinline__ float fp4_normal_scale(float sl) {
 
 // Sums held relative to the score xr, and times 2^shift, are to be joined with
 // others by logits: returns the float next to xr sl, and in `to` what makes them
-// relative to it.  (Bounded: where the rounding of xr sl is larger than 2^6, logits
-// of other parts cannot be told apart any more finely.)
+// relative to it.  (Bounded: where the rounding of xr sl is larger than 16, logits
+// of other parts cannot be told apart any more finely, and sums and their
+// reciprocals times a cache scale of 2^100 stay within fp32.)
 __device__ __forceinline__ float fp4_reference(float xr, float sl, float shift, float &to) {
   const float m = fminf(fmaxf(xr * sl, -0x1.fffffep127f), 0x1.fffffep127f);
-  to = exp2f(fminf(fmaxf(fmaf(xr, sl, -m), -64.f), 64.f) - shift);
+  to = exp2f(fminf(fmaxf(fmaf(xr, sl, -m), -16.f), 16.f) - shift);
   return m;
 }
 

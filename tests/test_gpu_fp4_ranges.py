@@ -116,3 +116,16 @@ def test_decode_takes_scales_of_any_sign(pa, path, scale):  # noqa: F811
         b, ps = constant_keys(path, 86, 64, 16, dtype, 1.0, [1.0, -2.0, 0.0])
         b.scale = scale
         run(pa, b, ps)
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("vs", [2.0 ** 100, 2.0 ** -100])
+@pytest.mark.parametrize("ks", [2.0 ** 100, 2.0 ** 40, 1.0])
+def test_v_scales_at_the_ends_of_their_range(pa, path, vs, ks):  # noqa: F811
+    """bf16 holds the outputs; they are compared after the (exact) product with 1 / vs."""
+    b, ps = constant_keys(path, 87, 128, 16, "bf16", ks, [1.0, -1.0, 0.0, -3.0])
+    b.vs = vs
+    out = b.decode(pa, ps) if b.start is None else b.prefill(pa)
+    b.vs = 1.0
+    b.check(out.double() / vs)
+    assert pa.pa_device_errors() == 0
