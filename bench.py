@@ -47,7 +47,7 @@ DEFAULT_WORKLOAD = "llama3_70b_cb"
 # the other decode targets measured beside the default line, in the same run
 DEFAULT_EXTRAS = ("llama3_8b_gqa:fp16", "llama3_70b_cb:bf16", "shared_prefix_cow:shared",
                   "shared_prefix_cow", "llama3_70b_cb:e4m3", "llama3_8b_gqa:e4m3")
-DECODE_SOURCES = ("pa_decode.cu", "pa_device.cuh", "pa_tile.cuh")
+DECODE_SOURCES = ("pa_decode.cu", "pa_device.cuh", "pa_join.cuh", "pa_tile.cuh")
 
 
 def algorithmic_bytes(w) -> dict:
