@@ -594,7 +594,7 @@ def _cache_fp4(name, key, value, k_cache, v_cache, slot_mapping, k_scale, v_scal
     f = _fp4_fns.get(name) or _fp4_fn(name, "cache")
     dev = _device_of("key", key)
     shape, dtype = key.shape, key.dtype
-    if len(shape) != 3 or value.shape != shape:
+    if len(shape) != 3 or not isinstance(value, torch.Tensor) or value.shape != shape:
         raise ValueError("key and value must be [T, Hkv, d], alike")
     T, Hkv, d = shape
     if not value.is_cuda or value.get_device() != dev or value.dtype is not dtype:

@@ -1,6 +1,6 @@
 """FP4 calls as a caller may make them: bounds that are loose, rows and table
 entries behind the batch, blocks that sequences share, captured graphs that share
-a workspace."""
+a workspace, arguments that are no tensors."""
 import numpy as np
 import pytest
 import torch
@@ -113,3 +113,26 @@ def test_one_tensor_as_key_and_value(pa):  # noqa: F811
     for got, c, g in zip(back, want, (1.0, 0.5)):
         v = F.values(c, bs, d, g)[slots // bs, :, slots % bs]
         assert np.array_equal(f64(got), v)
+
+
+def test_what_is_no_tensor_is_named(pa):  # noqa: F811
+    """A missing or foreign argument is a ValueError that names what is wanted."""
+    kc = pa.new_fp4_cache(4, 2, 16, 64)
+    k = torch.zeros(3, 2, 64, dtype=torch.float16, device="cuda")
+    q = torch.zeros(3, 4, 64, dtype=torch.float16, device="cuda")
+    bt = torch.zeros(3, 2, dtype=torch.int32, device="cuda")
+    cl = torch.ones(3, dtype=torch.int32, device="cuda")
+    sm = torch.zeros(3, dtype=torch.int64, device="cuda")
+    qs = torch.tensor([0, 1, 2, 3], dtype=torch.int32, device="cuda")
+    for bad in (None, 3, np.zeros((3, 2, 64), np.float16)):
+        for f in (pa.pa_reshape_and_cache_fp4, pa.pa_gather_cache_fp4):
+            args = [k, k, kc, kc, sm]
+            for i in range(5):
+                with pytest.raises(ValueError):
+                    f(*args[:i], bad, *args[i + 1:])
+        for f, args, tail in ((pa.pa_decode_fp4, [q, q, kc, kc, bt, cl], (0.1, 1.0, 1.0, 10)),
+                              (pa.pa_prefill_fp4, [q, q, qs, kc, kc, bt, cl], (0.1, 1.0, 1.0, 1))):
+            for i in range(len(args)):
+                with pytest.raises(ValueError):
+                    f(*args[:i], bad, *args[i + 1:], *tail)
+    assert pa.pa_device_errors() == 0
