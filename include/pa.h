@@ -392,7 +392,8 @@ pa_status pa_decode_shared_prefix_fp8(void *out, const void *query,
  * beyond 448 and 6 clamped to them.  A group with s = 0 stores zeros; a group
  * with a NaN in it stores the NaN scale (0x7f) and zero codes, so that it
  * reads back as NaN; an infinity is stored as 6 * 448 * g.
- * Other arguments as pa_reshape_and_cache.
+ * Other arguments as pa_reshape_and_cache; of two tokens that write one slot,
+ * which a call must not have, codes and scales of both may stay behind.
  */
 pa_status pa_reshape_and_cache_fp4(const void *key, const void *value,
                                    int64_t key_stride, int64_t value_stride,
@@ -452,6 +453,8 @@ pa_status pa_decode_fp4(void *out, const void *query,
 
 /*
  * pa_prefill_fp4 -- pa_prefill over FP4 caches, the values as in pa_decode_fp4.
+ * max_q_len picks the kernel for the whole call: a batch that mixes prompt chunks
+ * with single tokens takes less time as two calls.
  * Arguments, shapes and error behaviour as pa_prefill_fp8; max_q_len (or
  * max_blocks_per_seq * block_size, if that is less) above 65535 * (256 / group)
  * tokens, group = num_q_heads / num_kv_heads: PA_ERR_UNSUPPORTED.
