@@ -18,6 +18,9 @@
 // warp: with a thread for a group and 64-bit arithmetic of its own the kernels
 // were bound by instructions (a prompt of 16,381 tokens x 8 heads x 128 written
 // and read back in 39 us, 65,536 tokens read in 69 us; these take 33.5 and 55).
+// Apart, the prompt's write takes 20 us and its read-back 16, of 12.7 us each for
+// their bytes: loads in flight bound them (the write has 80 registers and issues in
+// 44 % of the cycles), and on the long read HBM, at 0.92 of the copy rate.
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -32,13 +32,16 @@
 //  * Tokens that must not count get logit -inf and a V scale of zero; a code is
 //    always finite, so nothing a masked slot holds (NaN scales among it)
 //    reaches the output.
-// What bounds it: instructions and their latency.  A warp's 32-token step is
-// about 650 of them (head_dim 128, one tile of 8 rows), issue is at 56 %, the
-// ALU pipe at 48 %.  Measured, 64 sequences of 512 to 4,096 tokens, 32 query / 8
-// KV heads, head_dim 128, fp16, 1,024-token partitions: 42.5 us for 161 MB (3.8
-// TB/s, 0.56 of the copy rate; bytes alone 24 us); 256 sequences of up to 16,384,
-// 64 query heads, bf16: 111 us, 4.9 TB/s; a chunk of 5 tokens x 4 heads for the
-// first batch: 66 to 73 us, its three row tiles' chain of latencies at two CTAs
+// What bounds it: the latency between a step's instructions, and CTAs of unequal
+// length.  A warp's 32-token step is about 650 instructions in a few chains; with
+// 14 warps an SM they fill 45 to 57 % of the issue slots.  Measured, 64 sequences
+// of 512 to 4,096 tokens, 32 query / 8 KV heads, head_dim 128, fp16, 1,024-token
+// partitions: 41 to 45 us for 161 MB by the lengths drawn (3.6 to 3.9 TB/s; bytes
+// alone 24 us, instructions alone some 20); 256 sequences of up to 16,384, 64
+// query heads, bf16: 111 to 117 us, 4.6 to 4.9 TB/s; 8 of 32,768 to 131,072,
+// 512-token partitions: 97.5 us, 4.65 TB/s; unsplit, 256 sequences of 512 to 4,096,
+// 32 / 8 heads, fp16: 126 us (floor 101); a chunk of 5 tokens x 4 heads for the
+// first batch: 63 to 70 us, its three row tiles' chain of latencies at two CTAs
 // an SM.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -832,11 +835,12 @@ cudaError_t launch_rows(DecodeArgs a, const CUtensorMap &km, const CUtensorMap &
   const cudaError_t e = smem_limit.ensure(kern, smem);
   if (e != cudaSuccess) return e;
   // Longest contexts first where the CTAs are more than run at once and the
-  // table leaves room for unequal contexts: 64 sequences of 512 to 4,096 tokens,
-  // 20 rows: 66 us against 78 to 91; 256 of up to 4,096, one query: 115 against
-  // 130.  (256 of up to 300 tokens, 8 rows, under a table of 32,768: 27 against
-  // 26.)  Calls with partitions lose: 256 sequences of up to 16,384 128 us
-  // against 117, since every empty partition's CTA asks for its sequence too.
+  // table leaves room for unequal contexts.  Contexts of 512 to 4,096, 32 / 8 heads:
+  // 64 sequences of 20 rows 68 us against 82, of 16 rows 57 against 63; 128 unsplit
+  // sequences 74 against 87, 256 126 against 140.  (256 of up to 300 tokens, 8 rows,
+  // under a table of 32,768: 27 against 26.)  Calls with partitions lose: 256
+  // sequences of up to 16,384 128 us against 117, since every empty partition's CTA
+  // asks for its sequence too.
   const int64_t ctas = static_cast<int64_t>(grid_x) * a.num_kv_heads * a.num_seqs;
   a.by_length = !kParts && a.cluster == 1 &&
                 a.num_seqs > 1 && a.num_seqs <= kMaxByLength && ctas > kSms * ctas_per_sm(NT) &&

@@ -98,6 +98,9 @@ __device__ __forceinline__ uint32_t float_to_e4m3(float x) {
   return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
 }
 
+// The most sequences that are put in order: a lane holds eight lengths in registers.
+// What the order gives falls with their number, as the last CTAs are a smaller part
+// of the call: of 5-token chunks 17 % at 64 sequences, 4 % at 256.
 constexpr int kMaxByLength = 256;
 constexpr int kMinByLength = 1024;  // tokens of the longest context
 

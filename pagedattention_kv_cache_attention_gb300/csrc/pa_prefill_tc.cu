@@ -1019,8 +1019,8 @@ cudaError_t launch_prefill_tc_pair_t(const PrefillArgs &a, const CUtensorMap &km
   const int tpc = TILES * ROWS / a.group;
   const int tiles = (a.max_q_len + tpc - 1) / tpc;
   if constexpr (KV == Kv::kFp4) {
-    // longest contexts first (64 sequences of 512 to 4,096 tokens, 28 to 64 rows:
-    // 89 us against 107)
+    // longest contexts first (64 sequences of 512 to 4,096 tokens, 28 to 64 rows,
+    // when measured without: 107 us; 89 with)
     PrefillArgs b = a;
     b.by_length = a.num_seqs <= kMaxByLength &&
                   (static_cast<int64_t>(a.max_blocks_per_seq) << a.bs_log2) >= kMinByLength;
@@ -1061,9 +1061,9 @@ cudaError_t launch_prefill_tc_d(const PrefillArgs &a, const CUtensorMap &km,
   constexpr int SK = PA_PREFILL_SOLO_KSTAGES, SV = PA_PREFILL_SOLO_VSTAGES;
   if (kv == Kv::kFp4) {
     // Up to 64 rows run two CTAs to an SM where there are enough of them (64
-    // sequences of 512 to 4,096 tokens, 8 KV heads, 28 to 64 rows: 89 us,
-    // 127 with two tiles); more rows, and few CTAs, in the two-tile kernel,
-    // whose steps are shorter (80 rows of the same batch 127 us; a one-tile
+    // sequences of 512 to 4,096 tokens, 8 KV heads, 28 to 64 rows, fp16: 89 to 91
+    // us, with two tiles 133 to 135); more rows, and few CTAs, in the two-tile
+    // kernel, whose steps are shorter (80 rows of the same batch 135 us; a one-tile
     // kernel took 176), and which shares a sequence's keys in a cluster.
     if (static_cast<int64_t>(a.max_q_len) * a.group > 64 ||
         static_cast<int64_t>(a.num_seqs) * a.num_kv_heads < 2 * kSms)
