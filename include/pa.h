@@ -254,7 +254,9 @@ pa_status pa_decode_shared_prefix(void *out, const void *query,
  * query, out     device, [total_q, num_q_heads, head_dim], dtype; 16-byte aligned
  * query_start    device int32 [num_seqs + 1], non-decreasing, query_start[0] = 0
  * max_q_len      >= every q_len_i (sizes the launch)
- * Softmax and accumulation fp32; out rounded to dtype.  scale > 0.  head_dim
+ * Softmax and accumulation fp32; out rounded to dtype.  scale > 0.  Logits below
+ * 2^28 in magnitude, in units of ln 2 (here, in pa_prefill_fp8 and in the shared
+ * pass of pa_decode_shared_prefix): beyond that a row may come out as NaN.  head_dim
  * in {64, 128}, block_size in {16, 32}, num_q_heads / num_kv_heads in 1..8
  * (every shape runs on the tcgen05 kernel: two 128-row query tiles per CTA
  * when max_q_len * G > 128, one otherwise).  A
@@ -453,6 +455,7 @@ pa_status pa_decode_fp4(void *out, const void *query,
 
 /*
  * pa_prefill_fp4 -- pa_prefill over FP4 caches, the values as in pa_decode_fp4.
+ * Logits of any size that fp32 holds, too.
  * max_q_len picks the kernel for the whole call: a batch that mixes prompt chunks
  * with single tokens takes less time as two calls.
  * Arguments, shapes and error behaviour as pa_prefill_fp8; max_q_len (or
