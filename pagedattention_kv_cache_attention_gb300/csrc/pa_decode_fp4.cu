@@ -21,14 +21,13 @@
 //    next token) of one dimension, and its scale pair is shared by the lane's
 //    dimensions.
 //  * fp32 online softmax in base 2 against a reference, a score of the row, that
-//    moves only when another passes it by more than 2^4.  While the reference's
-//    logit is small, a probability's exponent is one fma of the score; one with
-//    a large logit is taken off the score first, which is exact where it matters:
-//    the product alone may be off by more than fp16's range (pa_fp4.cuh).  P is
-//    carried as fp16 (11 bits; the output
-//    has at most 11) times 2^11, so that only probabilities below 2^-25 of the
-//    maximum lose bits and below 2^-35 vanish: a long context's faint tail
-//    keeps its mass.
+//    moves only when another's probability passes it by more than 2^4.  While the
+//    reference's logit is small, a probability's exponent is one fma of the score;
+//    a reference with a large logit is taken off the score first, since the fma
+//    alone may be off by more than fp16's range (pa_fp4.cuh).  P is carried as fp16
+//    (11 bits; the output has at most 11) times 2^11, so that only probabilities
+//    below 2^-25 of the maximum lose bits and below 2^-35 vanish: a long context's
+//    faint tail keeps its mass.
 //  * Tokens that must not count get logit -inf and a V scale of zero; a code is
 //    always finite, so nothing a masked slot holds (NaN scales among it)
 //    reaches the output.
@@ -850,8 +849,8 @@ cudaError_t launch_rows(DecodeArgs a, const CUtensorMap &km, const CUtensorMap &
                          dim3(NW * 32), smem, stream, km, vm, a);
 }
 
-// How many CTAs share the keys of a sequence and KV head in a call without partitions: as many
-// as the SMs still have room for, while a warp keeps two steps of the longest
+// How many CTAs share the keys of a sequence and KV head in a call without
+// partitions: as many as the SMs still have room for, while a warp keeps two steps of the longest
 // context that the table can hold.  Few sequences gain (one of 8,000 tokens and
 // one KV head 20 us, with one CTA 93; eight KV heads of 4,096 tokens 11 against
 // 33), and beyond that room a CTA's 4 to 6 us of start and join cost more than
