@@ -521,7 +521,8 @@ pa_status prefill_impl(void *out, const void *query, const int32_t *query_start,
   a.bs_log2 = block_size == 16 ? 4 : 5;
   a.max_q_len = max_q_len;
   a.num_blocks = num_blocks;
-  a.scale_log2 = scale * 1.4426950408889634f * k_scale;
+  // (positive; a normal number: 0 x -inf, a masked score, would be NaN)
+  a.scale_log2 = std::max(scale * 1.4426950408889634f * k_scale, 0x1p-126f);
   a.out_scale = v_scale;
   a.err = err;
   bool map_failed = false;

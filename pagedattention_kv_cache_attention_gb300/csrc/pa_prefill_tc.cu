@@ -420,11 +420,11 @@ __global__ void __launch_bounds__(pair_threads<TILES, D, KV>(), TILES == 1 ? 2 :
         const int e = min(120, 14 - ex);
         qf = ldexpf(1.f, e);
         sl2 = ldexpf(sl2, -e);
+        // a small cache scale times a small power of two may fall below the normal
+        // numbers, and 0 x -inf would be NaN (what the row's logits lose is below
+        // 2^-90: scores are below 2^35)
+        sl2 = sl2 < 0.f ? fminf(sl2, -0x1p-126f) : fmaxf(sl2, 0x1p-126f);
       }
-      // a small cache scale times a small power of two may fall below the normal
-      // numbers, and 0 x -inf would be NaN (what the row's logits lose is below
-      // 2^-90: scores are below 2^35)
-      if constexpr (kWide) sl2 = sl2 < 0.f ? fminf(sl2, -0x1p-126f) : fmaxf(sl2, 0x1p-126f);
 #pragma unroll
       for (int ch = 0; ch < D / 8; ++ch) {
         uint4 v = row_ok ? *reinterpret_cast<const uint4 *>(qrow + ch * 8)

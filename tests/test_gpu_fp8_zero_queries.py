@@ -1,4 +1,4 @@
-"""FP8 prefill and shared-prefix decode with bf16 query rows of zeros and of tiny
+"""FP8 prefill and shared-prefix decode with query rows of zeros and of tiny
 numbers over caches of a small scale: a row's softmax scale is carried with the
 power of two that its queries were scaled by, and the product may fall below the
 smallest normal number.  Such rows attend (nearly) uniformly.
@@ -32,9 +32,9 @@ def pool(seed, lens, H, bs, d, vs):
     return rng, tables, kc, vc, kc.double().numpy(), vc.double().numpy() * vs
 
 
-def queries(n, Hq, d):
+def queries(n, Hq, d, dtype=torch.bfloat16):
     at = np.resize(ROWS, n * Hq).reshape(n, Hq, 1)
-    return torch.from_numpy(np.broadcast_to(at, (n, Hq, d)).copy()).to(torch.bfloat16)
+    return torch.from_numpy(np.broadcast_to(at, (n, Hq, d)).copy()).to(dtype)
 
 
 def attend(q, k, v, G, scale):
@@ -57,11 +57,13 @@ def check(got, ref, A):
 
 @pytest.mark.parametrize("q_len,G,d,bs", [(3, 4, 128, 16), (40, 2, 64, 32), (70, 4, 128, 32),
                                           (150, 2, 64, 16)])
-@pytest.mark.parametrize("ks", [2.0 ** -27, 2.0 ** -60, 2.0 ** -120])
-def test_prefill_fp8(pa, q_len, G, d, bs, ks):  # noqa: F811
+@pytest.mark.parametrize("ks,dtype", [(2.0 ** -27, torch.bfloat16), (2.0 ** -60, torch.bfloat16),
+                                      (2.0 ** -120, torch.bfloat16), (2.0 ** -148, torch.bfloat16),
+                                      (2.0 ** -148, torch.float16)])
+def test_prefill_fp8(pa, q_len, G, d, bs, ks, dtype):  # noqa: F811
     H, lens = 2, [q_len + 83, q_len]
     _, tables, kc, vc, k, v = pool(1, lens, H, bs, d, 0.5)
-    q = queries(2 * q_len, H * G, d)
+    q = queries(2 * q_len, H * G, d, dtype)
     out = torch.full_like(q, float("nan"), device="cuda")
     scale = 1 / np.sqrt(d)
     pa.pa_prefill_fp8(out, q.cuda(), dev(np.array([0, q_len, 2 * q_len], np.int32)),
