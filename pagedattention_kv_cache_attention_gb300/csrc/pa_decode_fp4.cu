@@ -35,12 +35,12 @@
 // length.  A warp's 32-token step is about 650 instructions in a few chains; with
 // 14 warps an SM they fill 45 to 57 % of the issue slots.  Measured, 64 sequences
 // of 512 to 4,096 tokens, 32 query / 8 KV heads, head_dim 128, fp16, 1,024-token
-// partitions: 41 to 45 us for 161 MB by the lengths drawn (3.6 to 3.9 TB/s; bytes
+// partitions: 41 to 46 us for 161 MB by the lengths drawn (3.5 to 3.9 TB/s; bytes
 // alone 24 us, instructions alone some 20); 256 sequences of up to 16,384, 64
-// query heads, bf16: 111 to 117 us, 4.6 to 4.9 TB/s; 8 of 32,768 to 131,072,
+// query heads, bf16: 109 to 117 us, 4.6 to 5.0 TB/s; 8 of 32,768 to 131,072,
 // 512-token partitions: 97.5 us, 4.65 TB/s; unsplit, 256 sequences of 512 to 4,096,
 // 32 / 8 heads, fp16: 126 us (floor 101); a chunk of 5 tokens x 4 heads for the
-// first batch: 63 to 70 us, its three row tiles' chain of latencies at two CTAs
+// first batch: 63 to 75 us, its three row tiles' chain of latencies at two CTAs
 // an SM.
 #include <cuda.h>
 #include <cuda_runtime.h>
