@@ -82,6 +82,7 @@ typedef enum pa_dtype {
                                     a group is larger than max_group_size, members of a group
                                     give different prefix lengths, or a member's table names
                                     other blocks than the group's for its shared prefix */
+#define PA_DEVERR_BAD_POS   64u  /* a position was outside [0, max_position) */
 
 /*
  * pa_reshape_and_cache -- write each new token's key and value into its slot
@@ -469,6 +470,196 @@ pa_status pa_prefill_fp4(void *out, const void *query, const int32_t *query_star
                          int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                          int32_t block_size, int64_t num_blocks, float scale,
                          float k_scale, float v_scale, int32_t dtype, void *stream);
+
+/*
+ * Rotated append and sparse attention: a decode step over long contexts.
+ *   1. pa_rope_and_cache rotates the new tokens' queries and keys by their
+ *      positions and writes keys and values to their slots;
+ *   2. pa_update_key_bounds brings the bounds of the blocks that these tokens
+ *      are in up to date;
+ *   3. pa_select_blocks picks, for every query row and KV head, the blocks whose
+ *      bounds promise the largest logits;
+ *   4. pa_decode_sparse attends to those alone.
+ * Each call stands by itself, too: 1 serves dense decode and prefill as well,
+ * and 4 takes tables made in any way.  None needs a workspace; each is one
+ * kernel.  The _fp8 and _fp4 forms are over FP8 and FP4 caches.
+ */
+
+/*
+ * pa_rope_and_cache -- pa_reshape_and_cache with rotary position embedding on
+ * the way.  For every token t with slot_mapping[t] >= 0, with p = positions[t]:
+ *   query_out[t, h, :] = rot(query[t, h, :], p)                       every query head
+ *   k_cache[slot]      = rot(key[t, h, :], p), v_cache[slot] = value[t, h, :]
+ * where rot leaves elements rotary_dim .. head_dim - 1 as they are, and makes of
+ * each pair (x, y), i = 0 .. rotary_dim / 2 - 1,
+ *   x' = x cos_i - y sin_i,   y' = y cos_i + x sin_i,
+ *   cos_i = cos_sin[p, i],    sin_i = cos_sin[p, rotary_dim / 2 + i],
+ * (x, y) being elements (i, i + rotary_dim / 2) of the head, or (2 i, 2 i + 1) if
+ * `interleaved`.  Products and sums are IEEE fp32 operations (no fma), the result
+ * is rounded to dtype; the FP8 and FP4 forms then store what
+ * pa_reshape_and_cache_fp8 and _fp4 would of those rows, bit for bit.
+ *
+ * query, query_out  device, [num_tokens, num_q_heads, head_dim], rows
+ *                   query_stride and query_out_stride elements apart; the same
+ *                   memory for both (one stride, in place), or no overlap
+ * key, value        as for pa_reshape_and_cache
+ * positions         device int64 [num_tokens]
+ * cos_sin           device fp32 [max_position, rotary_dim], 16-byte aligned
+ * A token with a negative slot is left out: its query_out row, too, stays as it
+ * was.  So is one whose slot is past the pool (PA_DEVERR_BAD_SLOT) or whose
+ * position is outside [0, max_position) (PA_DEVERR_BAD_POS).  Slots must be
+ * distinct.  rotary_dim: a multiple of 16, at most head_dim.  Strides in
+ * elements, multiples of 8; pointers 16-byte aligned; num_q_heads is any number.
+ */
+pa_status pa_rope_and_cache(void *query_out, const void *query, const void *key,
+                            const void *value, int64_t query_out_stride, int64_t query_stride,
+                            int64_t key_stride, int64_t value_stride, void *k_cache,
+                            void *v_cache, const int64_t *slot_mapping, const int64_t *positions,
+                            const float *cos_sin, int32_t num_tokens, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t rotary_dim,
+                            int32_t interleaved, int32_t block_size, int64_t num_blocks,
+                            int64_t max_position, int32_t dtype, void *stream);
+/* k_scale, v_scale: as for pa_reshape_and_cache_fp8, pa_reshape_and_cache_fp4. */
+pa_status pa_rope_and_cache_fp8(void *query_out, const void *query, const void *key,
+                                const void *value, int64_t query_out_stride,
+                                int64_t query_stride, int64_t key_stride, int64_t value_stride,
+                                void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                                const int64_t *positions, const float *cos_sin,
+                                int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, int32_t rotary_dim, int32_t interleaved,
+                                int32_t block_size, int64_t num_blocks, int64_t max_position,
+                                int32_t dtype, float k_scale, float v_scale, void *stream);
+pa_status pa_rope_and_cache_fp4(void *query_out, const void *query, const void *key,
+                                const void *value, int64_t query_out_stride,
+                                int64_t query_stride, int64_t key_stride, int64_t value_stride,
+                                void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                                const int64_t *positions, const float *cos_sin,
+                                int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, int32_t rotary_dim, int32_t interleaved,
+                                int32_t block_size, int64_t num_blocks, int64_t max_position,
+                                int32_t dtype, float k_scale, float v_scale, void *stream);
+
+/*
+ * pa_update_key_bounds -- the bounds of every block that holds one of the newest
+ * tokens of a sequence: the last q_len_i = query_start[i+1] - query_start[i] of
+ * sequence i (query_start NULL: the last one).
+ *
+ * bounds        device int8 [num_blocks, num_kv_heads, 2, head_dim], 16-byte aligned
+ * bound_scales  device fp32 [num_blocks, num_kv_heads]
+ * Of a block and KV head, over its tokens below context_lens[i]: with a the
+ * largest magnitude of the keys and e the smallest integer, -126 or more, with
+ * a <= 127 * 2^e,
+ *   bounds[block, h, 0, d] = ceil(max k_d / 2^e),  bounds[block, h, 1, d] =
+ *   floor(min k_d / 2^e),  bound_scales[block, h] = 2^e;
+ * all zeros if a = 0; scale +inf and zeros if one of the keys is an infinity or a
+ * NaN (such a block is always worth a look).  Keys of FP8 and FP4 caches are
+ * taken without k_scale, which changes no order.  The bounds are made from the
+ * block's whole contents each time: nothing has to start at any value, a block may
+ * be given to another sequence or copied (pa_swap_blocks moves the bounds of a block
+ * as block_bytes = num_kv_heads * head_dim * 2, and its scales likewise where
+ * num_kv_heads is a multiple of 4).  Sequences of a call that share such a block
+ * must agree on its tokens.
+ * q_len_i outside [0, max_q_len] or above context_lens[i], or a context longer
+ * than the table, skips that sequence and sets PA_DEVERR_BAD_LEN; a block id
+ * outside [0, num_blocks) sets PA_DEVERR_BAD_BLOCK.  max_q_len is 1 (or 0) without
+ * query_start.  head_dim in {64, 128}, block_size in {16, 32}.
+ */
+pa_status pa_update_key_bounds(int8_t *bounds, float *bound_scales, const void *k_cache,
+                               const int32_t *block_tables, int32_t max_blocks_per_seq,
+                               const int32_t *context_lens, const int32_t *query_start,
+                               int32_t num_seqs, int32_t max_q_len, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                               int32_t dtype, void *stream);
+pa_status pa_update_key_bounds_fp8(int8_t *bounds, float *bound_scales, const void *k_cache,
+                                   const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t *context_lens, const int32_t *query_start,
+                                   int32_t num_seqs, int32_t max_q_len, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                   void *stream);
+pa_status pa_update_key_bounds_fp4(int8_t *bounds, float *bound_scales, const void *k_cache,
+                                   const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t *context_lens, const int32_t *query_start,
+                                   int32_t num_seqs, int32_t max_q_len, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                   void *stream);
+
+/*
+ * pa_select_blocks -- for every query row and KV head, num_selected of the blocks
+ * that the row sees, as a block table for pa_decode_sparse.
+ *
+ * Rows: row i is sequence i's one query and sees its context (query_start NULL);
+ * or, as in pa_prefill, rows query_start[i] .. query_start[i+1]-1 are the last
+ * tokens of sequence i, and each sees the tokens up to itself.
+ * Score of a block for the query heads of a KV head: with a the largest magnitude
+ * of the group's queries, f the smallest integer, -126 or more, with
+ * a <= 4095 * 2^f, and c_hd = rint(q_hd / 2^f),
+ *   I = sum_d (sum_h max(c_hd, 0)) bounds[block, 0, d] + (sum_h min(c_hd, 0)) bounds[block, 1, d]
+ *   score = fp32(I) * bound_scales[block]
+ * (I a whole number, both roundings fp32): a bound on the sum over the group of
+ * q . k, for every key k of the block, in units of 2^f.  A block of scale +inf
+ * scores +inf; a group with an infinity or a NaN has c = 0.
+ * A row that sees at most num_selected blocks gets all of them.  Of more, its
+ * first num_sink and last num_recent blocks are taken, and then those of the
+ * largest scores, of equal ones the first.
+ *
+ * selected_tables  device int32 [rows, num_kv_heads, num_selected]: the physical
+ *                  blocks, in the sequence's order, then -1
+ * selected_lens    device int32 [rows, num_kv_heads]: the tokens in them (the
+ *                  last block of the sequence, if taken, counts its own alone)
+ * max_context_len  >= every context_lens[i]; min(max_context_len / block_size
+ *                  rounded up, max_blocks_per_seq) is at most 49152, or
+ *                  PA_ERR_UNSUPPORTED
+ * num_sink + num_recent <= num_selected.  head_dim in {64, 128}, block_size in
+ * {16, 32}, num_q_heads / num_kv_heads in 1..8, max_q_len 1 (or 0) without query_start.
+ * A context length that is negative or beyond max_context_len or the table sets
+ * PA_DEVERR_BAD_LEN; its row then has length 0 (query_start NULL) or its rows stay
+ * as they were, as they do where q_len_i is outside [0, max_q_len] or above the
+ * context.  Rows behind the last sequence stay as they were.  A block id outside
+ * [0, num_blocks) among more than num_selected sets PA_DEVERR_BAD_BLOCK, and the
+ * block comes after all others.
+ */
+pa_status pa_select_blocks(int32_t *selected_tables, int32_t *selected_lens, const void *query,
+                           const int8_t *bounds, const float *bound_scales,
+                           const int32_t *block_tables, int32_t max_blocks_per_seq,
+                           const int32_t *context_lens, const int32_t *query_start,
+                           int32_t num_seqs, int32_t max_q_len, int32_t num_q_heads,
+                           int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                           int64_t num_blocks, int32_t max_context_len, int32_t num_selected,
+                           int32_t num_sink, int32_t num_recent, int32_t dtype, void *stream);
+
+/*
+ * pa_decode_sparse -- pa_decode with a block table and a length for each (row, KV
+ * head): row r, query head h attends to the tokens
+ *   j < selected_lens[r, h / G],  block selected_tables[r, h / G, j / block_size],
+ * row j mod block_size, G = num_q_heads / num_kv_heads.  Length 0 gives 0.
+ *
+ * query, out        device, [num_rows, num_q_heads, head_dim], dtype
+ * selected_tables   device int32 [num_rows, num_kv_heads, num_selected]
+ * selected_lens     device int32 [num_rows, num_kv_heads]
+ * Rows may be the single queries of a batch or several tokens of a sequence.
+ * num_rows at most 65535.  Accuracy, limits and device errors as for pa_decode
+ * (pa_decode_fp8, pa_decode_fp4) without partitions, selected_lens taking the
+ * place of context_lens and num_selected that of max_blocks_per_seq.
+ */
+pa_status pa_decode_sparse(void *out, const void *query, const void *k_cache, const void *v_cache,
+                           const int32_t *selected_tables, const int32_t *selected_lens,
+                           int32_t num_rows, int32_t num_selected, int32_t num_q_heads,
+                           int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                           int64_t num_blocks, float scale, int32_t dtype, void *stream);
+pa_status pa_decode_sparse_fp8(void *out, const void *query, const void *k_cache,
+                               const void *v_cache, const int32_t *selected_tables,
+                               const int32_t *selected_lens, int32_t num_rows,
+                               int32_t num_selected, int32_t num_q_heads, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                               float scale, float k_scale, float v_scale, int32_t dtype,
+                               void *stream);
+pa_status pa_decode_sparse_fp4(void *out, const void *query, const void *k_cache,
+                               const void *v_cache, const int32_t *selected_tables,
+                               const int32_t *selected_lens, int32_t num_rows,
+                               int32_t num_selected, int32_t num_q_heads, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                               float scale, float k_scale, float v_scale, int32_t dtype,
+                               void *stream);
 
 /*
  * pa_copy_blocks -- copy-on-write fork of whole physical blocks ("Serving

@@ -30,12 +30,17 @@ __all__ = [
     "pa_decode_shared_prefix", "pa_decode_shared_prefix_fp8", "pa_prefill_fp8",
     "pa_copy_blocks_fp8", "new_fp4_cache", "fp4_block_size", "pa_reshape_and_cache_fp4",
     "pa_gather_cache_fp4", "pa_decode_fp4", "pa_prefill_fp4",
+    "new_rope_table", "new_key_bounds", "DEVERR_BAD_POS",
+    "pa_rope_and_cache", "pa_rope_and_cache_fp8", "pa_rope_and_cache_fp4",
+    "pa_update_key_bounds", "pa_update_key_bounds_fp8", "pa_update_key_bounds_fp4",
+    "pa_select_blocks", "pa_decode_sparse", "pa_decode_sparse_fp8", "pa_decode_sparse_fp4",
 ]
 
 PA_FP16, PA_BF16 = 0, 1
 DEVERR_BAD_BLOCK, DEVERR_BAD_SLOT, DEVERR_BAD_LEN, DEVERR_TIMEOUT = 1, 2, 4, 8
 DEVERR_WORKSPACE = 16
 DEVERR_PREFIX = 32
+DEVERR_BAD_POS = 64
 # Bytes of join counters at the start of a split-context workspace
 # (PA_DECODE_COUNTER_BYTES in include/pa.h); they must be zero when a
 # workspace is first used, and every pa_decode call leaves them zero.
@@ -746,6 +751,316 @@ def pa_prefill_fp4(out: torch.Tensor, query: torch.Tensor, query_start: torch.Te
     if st:
         raise PaError("pa_prefill_fp4", st)
     return out
+
+
+def new_rope_table(max_position: int, rotary_dim: int, base: float = 10000.0,
+                   device=None) -> torch.Tensor:
+    """The table that pa_rope_and_cache reads: fp32 [max_position, rotary_dim],
+    cosines and then sines of position * base^(-2 i / rotary_dim), the angles
+    formed in 64 bits.  (Any other table of that form does as well.)"""
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even")
+    dev = device if device is not None else torch.cuda.current_device()
+    freq = float(base) ** (-torch.arange(rotary_dim // 2, dtype=torch.float64, device=dev)
+                           * 2 / rotary_dim)
+    angle = torch.arange(max_position, dtype=torch.float64, device=dev)[:, None] * freq
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def new_key_bounds(num_blocks: int, num_kv_heads: int, head_dim: int, device=None):
+    """(bounds, bound_scales) of zeros for the blocks of a pool: int8
+    [num_blocks, num_kv_heads, 2, head_dim] and fp32 [num_blocks, num_kv_heads]."""
+    dev = device if device is not None else torch.cuda.current_device()
+    return (torch.zeros(num_blocks, num_kv_heads, 2, head_dim, dtype=torch.int8, device=dev),
+            torch.zeros(num_blocks, num_kv_heads, dtype=torch.float32, device=dev))
+
+
+# Their arguments are checked in one pass too, like those of the FP4 calls.
+_I8, _F32 = torch.int8, torch.float32
+_SPARSE_ARGS = {
+    "pa_rope_and_cache": "PPPPllllPPPPPiiiiiiilliP", "pa_update_key_bounds": "PPPPiPPiiiiiliP",
+    "pa_select_blocks": "PPPPPPiPPiiiiiiliiiiiP", "pa_decode_sparse": "PPPPPPiiiiiilfiP",
+    "pa_rope_and_cache_fp8": "PPPPllllPPPPPiiiiiiilliffP",
+    "pa_rope_and_cache_fp4": "PPPPllllPPPPPiiiiiiilliffP",
+    "pa_update_key_bounds_fp8": "PPPPiPPiiiiilP", "pa_update_key_bounds_fp4": "PPPPiPPiiiiilP",
+    "pa_decode_sparse_fp8": "PPPPPPiiiiiilfffiP", "pa_decode_sparse_fp4": "PPPPPPiiiiiilfffiP",
+}
+_sparse_fns = {}
+
+
+def _sparse_fn(name: str):
+    f = getattr(_load(), name)
+    f.argtypes, f.restype = [_CT[c] for c in _SPARSE_ARGS[name]], ctypes.c_int32
+    _sparse_fns[name] = f
+    return f
+
+
+def _dense(dev: int, **tensors) -> None:
+    """Each name=(tensor, dtype), contiguous on device ``dev``: one expression for what
+    fits, and the first that does not named."""
+    for t, dtype in tensors.values():
+        try:
+            if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+                continue
+        except AttributeError:
+            pass
+        _all_fit(dev, **tensors)
+
+
+def _cache_shape(kind: str, cache: torch.Tensor, d: int):
+    """(num_blocks, num_kv_heads, block_size) of a cache for heads of ``d``."""
+    shape = cache.shape
+    if kind == "_fp4":
+        return shape[0], shape[1], fp4_block_size(cache, d)
+    if len(shape) != 4 or shape[3] != d:
+        raise ValueError(f"a cache is [NB, Hkv, block_size, d = {d}], got {tuple(shape)}")
+    return shape[0], shape[1], shape[2]
+
+
+def _rope(kind, query_out, query, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
+          scales, interleaved, stream):
+    name = "pa_rope_and_cache" + kind
+    f = _sparse_fns.get(name) or _sparse_fn(name)
+    dev = _device_of("query", query)
+    dtype = query.dtype
+    strides = []
+    for n, t in (("query_out", query_out), ("query", query), ("key", key), ("value", value)):
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
+            _cuda(n, t, dtype)
+        if t.dim() != 3:
+            raise ValueError(f"{n} must be [T, heads, d]")
+        st, (rows, heads, d) = t.stride(), t.shape
+        if (st[2] != 1 and d > 1) or (st[1] != d and heads > 1):
+            raise ValueError(f"{n}: heads must be contiguous inside a token row")
+        # (the stride of a single row is not looked at)
+        strides.append(st[0] if rows > 1 else heads * d)
+    T, Hq, d = query.shape
+    if query_out.shape != query.shape:
+        raise ValueError("query_out must match query")
+    Hkv = key.shape[1]
+    if key.shape != (T, Hkv, d) or value.shape != key.shape:
+        raise ValueError("key and value must be [T, Hkv, d], with query's T and d")
+    cache = _U8 if kind else dtype
+    _dense(dev, k_cache=(k_cache, cache), v_cache=(v_cache, cache),
+           slot_mapping=(slot_mapping, _I64), positions=(positions, _I64), cos_sin=(cos_sin, _F32))
+    NB, heads, bs = _cache_shape(kind, k_cache, d)
+    if heads != Hkv or v_cache.shape != k_cache.shape:
+        raise ValueError("key/value/cache shapes disagree")
+    if slot_mapping.numel() != T or positions.numel() != T:
+        raise ValueError("slot_mapping and positions must have one entry per token")
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [max_position, rotary_dim]")
+    st = f(query_out.data_ptr(), query.data_ptr(), key.data_ptr(), value.data_ptr(), *strides,
+           k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
+           cos_sin.data_ptr(), T, Hq, Hkv, d, cos_sin.shape[1], 1 if interleaved else 0, bs, NB,
+           cos_sin.shape[0], _dtype_code(query), *scales,
+           _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise PaError(name, st)
+    return query_out
+
+
+def pa_rope_and_cache(query_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
+                      value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                      slot_mapping: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor,
+                      interleaved: bool = False, stream=None) -> torch.Tensor:
+    """Rotate query [T, Hq, d] and key [T, Hkv, d] by positions [T] (int64) with
+    the table cos_sin (new_rope_table); write the queries into ``query_out``
+    (which may be ``query``), and keys and values into the caches at
+    slot_mapping[t] (int64; a token with a negative slot is left out)."""
+    return _rope("", query_out, query, key, value, k_cache, v_cache, slot_mapping, positions,
+                 cos_sin, (), interleaved, stream)
+
+
+def pa_rope_and_cache_fp8(query_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
+                          value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                          slot_mapping: torch.Tensor, positions: torch.Tensor,
+                          cos_sin: torch.Tensor, k_scale: float, v_scale: float,
+                          interleaved: bool = False, stream=None) -> torch.Tensor:
+    """pa_rope_and_cache into uint8 FP8 E4M3 caches."""
+    return _rope("_fp8", query_out, query, key, value, k_cache, v_cache, slot_mapping, positions,
+                 cos_sin, (float(k_scale), float(v_scale)), interleaved, stream)
+
+
+def pa_rope_and_cache_fp4(query_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
+                          value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                          slot_mapping: torch.Tensor, positions: torch.Tensor,
+                          cos_sin: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0,
+                          interleaved: bool = False, stream=None) -> torch.Tensor:
+    """pa_rope_and_cache into FP4 caches (new_fp4_cache)."""
+    return _rope("_fp4", query_out, query, key, value, k_cache, v_cache, slot_mapping, positions,
+                 cos_sin, (float(k_scale), float(v_scale)), interleaved, stream)
+
+
+def _bounds_shape(bounds, bound_scales, NB, Hkv, d):
+    if bounds.shape != (NB, Hkv, 2, d) or bound_scales.shape != (NB, Hkv):
+        raise ValueError(f"bounds must be [{NB}, {Hkv}, 2, {d}] and bound_scales [{NB}, {Hkv}]")
+
+
+def _batch(block_tables, context_lens, query_start):
+    """The number of sequences."""
+    B = context_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be [B, MB] and context_lens [B]")
+    if query_start is not None and query_start.numel() != B + 1:
+        raise ValueError("query_start must have num_seqs + 1 entries")
+    return B
+
+
+def _key_bounds(kind, bounds, bound_scales, k_cache, block_tables, context_lens, query_start,
+                max_q_len, stream):
+    name = "pa_update_key_bounds" + kind
+    f = _sparse_fns.get(name) or _sparse_fn(name)
+    dev = _device_of("bounds", bounds)
+    more = {} if query_start is None else {"query_start": (query_start, _I32)}
+    if not isinstance(k_cache, torch.Tensor):
+        _cuda("k_cache", k_cache)
+    _dense(dev, bounds=(bounds, _I8), bound_scales=(bound_scales, _F32),
+           k_cache=(k_cache, _U8 if kind else k_cache.dtype),
+           block_tables=(block_tables, _I32), context_lens=(context_lens, _I32), **more)
+    if bounds.dim() != 4:
+        raise ValueError("bounds must be [NB, Hkv, 2, d]")
+    d = bounds.shape[3]
+    NB, Hkv, bs = _cache_shape(kind, k_cache, d)
+    _bounds_shape(bounds, bound_scales, NB, Hkv, d)
+    B = _batch(block_tables, context_lens, query_start)
+    st = f(bounds.data_ptr(), bound_scales.data_ptr(), k_cache.data_ptr(), block_tables.data_ptr(),
+           block_tables.shape[1], context_lens.data_ptr(),
+           None if query_start is None else query_start.data_ptr(), B, int(max_q_len), Hkv, d, bs,
+           NB, *(() if kind else (_dtype_code(k_cache),)),
+           _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise PaError(name, st)
+
+
+def pa_update_key_bounds(bounds: torch.Tensor, bound_scales: torch.Tensor, k_cache: torch.Tensor,
+                         block_tables: torch.Tensor, context_lens: torch.Tensor,
+                         query_start: Optional[torch.Tensor] = None, max_q_len: int = 1,
+                         stream=None) -> None:
+    """Bring ``bounds`` and ``bound_scales`` (new_key_bounds) up to date for the
+    blocks that hold the newest tokens of each sequence: the last one, or the
+    last query_start[i + 1] - query_start[i] (at most max_q_len)."""
+    _key_bounds("", bounds, bound_scales, k_cache, block_tables, context_lens, query_start,
+                max_q_len, stream)
+
+
+def pa_update_key_bounds_fp8(bounds: torch.Tensor, bound_scales: torch.Tensor,
+                             k_cache: torch.Tensor, block_tables: torch.Tensor,
+                             context_lens: torch.Tensor,
+                             query_start: Optional[torch.Tensor] = None, max_q_len: int = 1,
+                             stream=None) -> None:
+    """pa_update_key_bounds over a uint8 FP8 E4M3 cache."""
+    _key_bounds("_fp8", bounds, bound_scales, k_cache, block_tables, context_lens, query_start,
+                max_q_len, stream)
+
+
+def pa_update_key_bounds_fp4(bounds: torch.Tensor, bound_scales: torch.Tensor,
+                             k_cache: torch.Tensor, block_tables: torch.Tensor,
+                             context_lens: torch.Tensor,
+                             query_start: Optional[torch.Tensor] = None, max_q_len: int = 1,
+                             stream=None) -> None:
+    """pa_update_key_bounds over an FP4 cache."""
+    _key_bounds("_fp4", bounds, bound_scales, k_cache, block_tables, context_lens, query_start,
+                max_q_len, stream)
+
+
+def pa_select_blocks(selected_tables: torch.Tensor, selected_lens: torch.Tensor,
+                     query: torch.Tensor, bounds: torch.Tensor, bound_scales: torch.Tensor,
+                     block_tables: torch.Tensor, context_lens: torch.Tensor, block_size: int,
+                     max_context_len: int, num_sink: int = 1, num_recent: int = 1,
+                     query_start: Optional[torch.Tensor] = None, max_q_len: int = 1,
+                     stream=None):
+    """For every row of query [R, Hq, d] and KV head, pick the K blocks whose
+    bounds promise the largest logits: their physical ids into
+    ``selected_tables`` (int32 [R, Hkv, K], -1 behind them) and the tokens in
+    them into ``selected_lens`` (int32 [R, Hkv]), for pa_decode_sparse.  Row i
+    is sequence i's query, or rows query_start[i] .. query_start[i + 1] - 1 its
+    last tokens.  The first num_sink and last num_recent blocks that a row
+    sees are always taken.  Returns (selected_tables, selected_lens)."""
+    f = _sparse_fns.get("pa_select_blocks") or _sparse_fn("pa_select_blocks")
+    dev = _device_of("query", query)
+    more = {} if query_start is None else {"query_start": (query_start, _I32)}
+    _dense(dev, query=(query, query.dtype), selected_tables=(selected_tables, _I32),
+           selected_lens=(selected_lens, _I32), bounds=(bounds, _I8),
+           bound_scales=(bound_scales, _F32), block_tables=(block_tables, _I32),
+           context_lens=(context_lens, _I32), **more)
+    if query.dim() != 3 or bounds.dim() != 4 or selected_tables.dim() != 3:
+        raise ValueError("query must be [R, Hq, d], bounds [NB, Hkv, 2, d] and selected_tables "
+                         "[R, Hkv, K]")
+    R, Hq, d = query.shape
+    NB, Hkv = bounds.shape[:2]
+    _bounds_shape(bounds, bound_scales, NB, Hkv, d)
+    K = selected_tables.shape[2]
+    if selected_tables.shape != (R, Hkv, K) or selected_lens.shape != (R, Hkv):
+        raise ValueError("selected_tables must be [R, Hkv, K] and selected_lens [R, Hkv]")
+    B = _batch(block_tables, context_lens, query_start)
+    if query_start is None and R != B:
+        raise ValueError("without query_start there is one query row for each sequence")
+    st = f(selected_tables.data_ptr(), selected_lens.data_ptr(), query.data_ptr(),
+           bounds.data_ptr(), bound_scales.data_ptr(), block_tables.data_ptr(),
+           block_tables.shape[1], context_lens.data_ptr(),
+           None if query_start is None else query_start.data_ptr(), B, int(max_q_len), Hq, Hkv, d,
+           int(block_size), NB, int(max_context_len), K, int(num_sink), int(num_recent),
+           _dtype_code(query), _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise PaError("pa_select_blocks", st)
+    return selected_tables, selected_lens
+
+
+def _decode_sparse(kind, out, query, k_cache, v_cache, selected_tables, selected_lens, scale,
+                   scales, stream):
+    name = "pa_decode_sparse" + kind
+    f = _sparse_fns.get(name) or _sparse_fn(name)
+    dev = _device_of("query", query)
+    dtype = query.dtype
+    cache = _U8 if kind else dtype
+    _dense(dev, query=(query, dtype), out=(out, dtype), k_cache=(k_cache, cache),
+           v_cache=(v_cache, cache), selected_tables=(selected_tables, _I32),
+           selected_lens=(selected_lens, _I32))
+    if query.dim() != 3 or out.shape != query.shape:
+        raise ValueError("query and out must be [R, Hq, d], alike")
+    R, Hq, d = query.shape
+    NB, Hkv, bs = _cache_shape(kind, k_cache, d)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache shapes differ")
+    if (selected_tables.dim() != 3 or selected_tables.shape[:2] != (R, Hkv)
+            or selected_lens.shape != (R, Hkv)):
+        raise ValueError("selected_tables must be [R, Hkv, K] and selected_lens [R, Hkv]")
+    st = f(out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+           selected_tables.data_ptr(), selected_lens.data_ptr(), R, selected_tables.shape[2], Hq,
+           Hkv, d, bs, NB, float(scale), *scales, _dtype_code(query),
+           _raw_stream(dev) if stream is None else _stream(stream))
+    if st:
+        raise PaError(name, st)
+    return out
+
+
+def pa_decode_sparse(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor,
+                     v_cache: torch.Tensor, selected_tables: torch.Tensor,
+                     selected_lens: torch.Tensor, scale: float, stream=None) -> torch.Tensor:
+    """Decode attention of query [R, Hq, d] into ``out``, row r and KV head g
+    over the first selected_lens[r, g] tokens of the blocks
+    selected_tables[r, g, :] (pa_select_blocks)."""
+    return _decode_sparse("", out, query, k_cache, v_cache, selected_tables, selected_lens, scale,
+                          (), stream)
+
+
+def pa_decode_sparse_fp8(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor,
+                         v_cache: torch.Tensor, selected_tables: torch.Tensor,
+                         selected_lens: torch.Tensor, scale: float, k_scale: float,
+                         v_scale: float, stream=None) -> torch.Tensor:
+    """pa_decode_sparse over uint8 FP8 E4M3 caches, fp16 or bf16 queries and output."""
+    return _decode_sparse("_fp8", out, query, k_cache, v_cache, selected_tables, selected_lens,
+                          scale, (float(k_scale), float(v_scale)), stream)
+
+
+def pa_decode_sparse_fp4(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor,
+                         v_cache: torch.Tensor, selected_tables: torch.Tensor,
+                         selected_lens: torch.Tensor, scale: float, k_scale: float,
+                         v_scale: float, stream=None) -> torch.Tensor:
+    """pa_decode_sparse over FP4 caches, fp16 or bf16 queries and output."""
+    return _decode_sparse("_fp4", out, query, k_cache, v_cache, selected_tables, selected_lens,
+                          scale, (float(k_scale), float(v_scale)), stream)
 
 
 def pa_selftest_bounded_wait(stream=None) -> None:

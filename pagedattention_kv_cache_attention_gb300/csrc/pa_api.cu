@@ -265,7 +265,7 @@ pa_status decode_impl(void *out, const void *query, const void *k_cache, const v
                       int64_t num_blocks, float scale, int32_t max_context_len,
                       int32_t partition_size, void *workspace, size_t workspace_bytes,
                       int32_t dtype, pa::Kv kv, float k_scale, float v_scale, void *stream,
-                      const SharedPrefix *sp = nullptr) {
+                      const SharedPrefix *sp = nullptr, bool per_head = false) {
   const int32_t st = pa::decode_check_args(
       out, query, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs,
       num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale, max_context_len,
@@ -320,6 +320,7 @@ pa_status decode_impl(void *out, const void *query, const void *k_cache, const v
   a.ws_o = P > 1 ? reinterpret_cast<float *>(base + w.o_off) : nullptr;
   a.ws_cnt = P > 1 ? reinterpret_cast<unsigned *>(base) : nullptr;
   a.fuse_join = fuse ? 1 : 0;
+  a.per_head = per_head ? 1 : 0;
   a.err = err;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   bool map_failed = false;
@@ -339,6 +340,9 @@ pa_status decode_impl(void *out, const void *query, const void *k_cache, const v
   const cudaError_t launched =
       kv == pa::Kv::kFp4
           ? pa::launch_decode_fp4(a, k_cache, v_cache, head_dim, dtype, cs, &map_failed)
+      : per_head
+          ? pa::launch_decode_sparse(a, k_cache, v_cache, pool_rows, head_dim, dtype,
+                                     kv == pa::Kv::kFp8, cs, &map_failed)
           : pa::launch_decode(a, k_cache, v_cache, pool_rows, head_dim, dtype,
                               kv == pa::Kv::kFp8, cs, &map_failed);
   if (launched != cudaSuccess)
@@ -787,6 +791,312 @@ pa_status pa_device_errors(void *stream, uint32_t *flags) {
   }
   *flags = host;
   return PA_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------- rotated append, sparse attention
+
+namespace {
+
+pa_status rope_impl(void *query_out, const void *query, const void *key, const void *value,
+                    int64_t query_out_stride, int64_t query_stride, int64_t key_stride,
+                    int64_t value_stride, void *k_cache, void *v_cache,
+                    const int64_t *slot_mapping, const int64_t *positions, const float *cos_sin,
+                    int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                    int32_t head_dim, int32_t rotary_dim, int32_t interleaved, int32_t block_size,
+                    int64_t num_blocks, int64_t max_position, int32_t dtype, pa::Kv kv,
+                    float k_scale, float v_scale, void *stream) {
+  if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_blocks <= 0 ||
+      max_position <= 0 || rotary_dim <= 0 || (interleaved != 0 && interleaved != 1) ||
+      !dtype_ok(dtype))
+    return PA_ERR_INVALID_ARG;
+  if (kv == pa::Kv::kFp8 && !fp8_scales_ok(k_scale, v_scale)) return PA_ERR_INVALID_ARG;
+  if (kv == pa::Kv::kFp4 && !fp4_scales_ok(k_scale, v_scale)) return PA_ERR_INVALID_ARG;
+  if (!head_dim_ok(head_dim) || !block_size_ok(block_size)) return PA_ERR_UNSUPPORTED;
+  if (rotary_dim > head_dim || rotary_dim % 16) return PA_ERR_UNSUPPORTED;
+  // a head's place in a row, and the last slot, are formed in 32 and 64 bits
+  constexpr int32_t kMaxHeads = 1 << 20;
+  if (num_q_heads > kMaxHeads || num_kv_heads > kMaxHeads || num_blocks >= int64_t{1} << 32)
+    return PA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return PA_OK;
+  if (!query_out || !query || !key || !value || !k_cache || !v_cache || !slot_mapping ||
+      !positions || !cos_sin)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(query_out) || !aligned16(query) || !aligned16(key) || !aligned16(value) ||
+      !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(cos_sin))
+    return PA_ERR_INVALID_ARG;
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * head_dim;
+  const int64_t kv_row = static_cast<int64_t>(num_kv_heads) * head_dim;
+  if (query_out_stride < q_row || query_stride < q_row || key_stride < kv_row ||
+      value_stride < kv_row || query_out_stride % 8 || query_stride % 8 || key_stride % 8 ||
+      value_stride % 8)
+    return PA_ERR_INVALID_ARG;
+  unsigned int *err = nullptr;
+  if (error_word(&err) != cudaSuccess) return PA_ERR_CUDA;
+  pa::RopeArgs a{};
+  a.query_out = query_out;
+  a.query = query;
+  a.key = key;
+  a.value = value;
+  a.query_out_stride = query_out_stride;
+  a.query_stride = query_stride;
+  a.key_stride = key_stride;
+  a.value_stride = value_stride;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.slot_mapping = slot_mapping;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.max_position = max_position;
+  a.num_tokens = num_tokens;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.rotary_dim = rotary_dim;
+  a.interleaved = interleaved;
+  a.bs_log2 = block_size == 16 ? 4 : 5;
+  a.num_blocks = num_blocks;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.err = err;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = kv == pa::Kv::kFp4
+                            ? pa::launch_rope_fp4(a, head_dim, dtype, cs)
+                            : pa::launch_rope(a, head_dim, dtype, kv == pa::Kv::kFp8, cs);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status bounds_impl(int8_t *bounds, float *bound_scales, const void *k_cache,
+                      const int32_t *block_tables, int32_t max_blocks_per_seq,
+                      const int32_t *context_lens, const int32_t *query_start, int32_t num_seqs,
+                      int32_t max_q_len, int32_t num_kv_heads, int32_t head_dim,
+                      int32_t block_size, int64_t num_blocks, int32_t dtype, pa::Kv kv,
+                      void *stream) {
+  if (num_seqs < 0 || max_q_len < 0 || num_kv_heads <= 0 || num_blocks <= 0 ||
+      max_blocks_per_seq <= 0 || !dtype_ok(dtype) || (!query_start && max_q_len > 1))
+    return PA_ERR_INVALID_ARG;
+  if (!head_dim_ok(head_dim) || !block_size_ok(block_size)) return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || max_q_len == 0) return PA_OK;
+  if (!bounds || !bound_scales || !k_cache || !block_tables || !context_lens ||
+      !aligned16(bounds) || !aligned16(k_cache))
+    return PA_ERR_INVALID_ARG;
+  if (!pool_ok(num_blocks, num_kv_heads, block_size) || num_seqs > 65535 || num_kv_heads > 65535)
+    return PA_ERR_UNSUPPORTED;
+  unsigned int *err = nullptr;
+  if (error_word(&err) != cudaSuccess) return PA_ERR_CUDA;
+  pa::BoundsArgs a{};
+  a.bounds = bounds;
+  a.bound_scales = bound_scales;
+  a.k_cache = k_cache;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.query_start = query_start;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.num_kv_heads = num_kv_heads;
+  a.bs_log2 = block_size == 16 ? 4 : 5;
+  a.max_q_len = max_q_len;
+  a.num_blocks = num_blocks;
+  a.err = err;
+  return pa::launch_key_bounds(a, head_dim, dtype, kv, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+// pa_decode over a table and a length for each (row, KV head), unsplit.
+pa_status sparse_impl(void *out, const void *query, const void *k_cache, const void *v_cache,
+                      const int32_t *selected_tables, const int32_t *selected_lens,
+                      int32_t num_rows, int32_t num_selected, int32_t num_q_heads,
+                      int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                      int64_t num_blocks, float scale, int32_t dtype, pa::Kv kv, float k_scale,
+                      float v_scale, void *stream) {
+  if (num_selected <= 0) return PA_ERR_INVALID_ARG;
+  if (!block_size_ok(block_size)) return PA_ERR_UNSUPPORTED;
+  const int64_t most = static_cast<int64_t>(num_selected) * block_size;
+  if (most > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+  return decode_impl(out, query, k_cache, v_cache, selected_tables, num_selected, selected_lens,
+                     num_rows, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                     static_cast<int32_t>(most), 0, nullptr, 0, dtype, kv, k_scale, v_scale,
+                     stream, nullptr, true);
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_rope_and_cache(void *query_out, const void *query, const void *key,
+                            const void *value, int64_t query_out_stride, int64_t query_stride,
+                            int64_t key_stride, int64_t value_stride, void *k_cache,
+                            void *v_cache, const int64_t *slot_mapping, const int64_t *positions,
+                            const float *cos_sin, int32_t num_tokens, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t rotary_dim,
+                            int32_t interleaved, int32_t block_size, int64_t num_blocks,
+                            int64_t max_position, int32_t dtype, void *stream) {
+  return rope_impl(query_out, query, key, value, query_out_stride, query_stride, key_stride,
+                   value_stride, k_cache, v_cache, slot_mapping, positions, cos_sin, num_tokens,
+                   num_q_heads, num_kv_heads, head_dim, rotary_dim, interleaved, block_size,
+                   num_blocks, max_position, dtype, pa::Kv::k16, 1.f, 1.f, stream);
+}
+
+pa_status pa_rope_and_cache_fp8(void *query_out, const void *query, const void *key,
+                                const void *value, int64_t query_out_stride,
+                                int64_t query_stride, int64_t key_stride, int64_t value_stride,
+                                void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                                const int64_t *positions, const float *cos_sin,
+                                int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, int32_t rotary_dim, int32_t interleaved,
+                                int32_t block_size, int64_t num_blocks, int64_t max_position,
+                                int32_t dtype, float k_scale, float v_scale, void *stream) {
+  return rope_impl(query_out, query, key, value, query_out_stride, query_stride, key_stride,
+                   value_stride, k_cache, v_cache, slot_mapping, positions, cos_sin, num_tokens,
+                   num_q_heads, num_kv_heads, head_dim, rotary_dim, interleaved, block_size,
+                   num_blocks, max_position, dtype, pa::Kv::kFp8, k_scale, v_scale, stream);
+}
+
+pa_status pa_rope_and_cache_fp4(void *query_out, const void *query, const void *key,
+                                const void *value, int64_t query_out_stride,
+                                int64_t query_stride, int64_t key_stride, int64_t value_stride,
+                                void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                                const int64_t *positions, const float *cos_sin,
+                                int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, int32_t rotary_dim, int32_t interleaved,
+                                int32_t block_size, int64_t num_blocks, int64_t max_position,
+                                int32_t dtype, float k_scale, float v_scale, void *stream) {
+  return rope_impl(query_out, query, key, value, query_out_stride, query_stride, key_stride,
+                   value_stride, k_cache, v_cache, slot_mapping, positions, cos_sin, num_tokens,
+                   num_q_heads, num_kv_heads, head_dim, rotary_dim, interleaved, block_size,
+                   num_blocks, max_position, dtype, pa::Kv::kFp4, k_scale, v_scale, stream);
+}
+
+pa_status pa_update_key_bounds(int8_t *bounds, float *bound_scales, const void *k_cache,
+                               const int32_t *block_tables, int32_t max_blocks_per_seq,
+                               const int32_t *context_lens, const int32_t *query_start,
+                               int32_t num_seqs, int32_t max_q_len, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                               int32_t dtype, void *stream) {
+  return bounds_impl(bounds, bound_scales, k_cache, block_tables, max_blocks_per_seq,
+                     context_lens, query_start, num_seqs, max_q_len, num_kv_heads, head_dim,
+                     block_size, num_blocks, dtype, pa::Kv::k16, stream);
+}
+
+pa_status pa_update_key_bounds_fp8(int8_t *bounds, float *bound_scales, const void *k_cache,
+                                   const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t *context_lens, const int32_t *query_start,
+                                   int32_t num_seqs, int32_t max_q_len, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                   void *stream) {
+  return bounds_impl(bounds, bound_scales, k_cache, block_tables, max_blocks_per_seq,
+                     context_lens, query_start, num_seqs, max_q_len, num_kv_heads, head_dim,
+                     block_size, num_blocks, PA_FP16, pa::Kv::kFp8, stream);
+}
+
+pa_status pa_update_key_bounds_fp4(int8_t *bounds, float *bound_scales, const void *k_cache,
+                                   const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t *context_lens, const int32_t *query_start,
+                                   int32_t num_seqs, int32_t max_q_len, int32_t num_kv_heads,
+                                   int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                   void *stream) {
+  return bounds_impl(bounds, bound_scales, k_cache, block_tables, max_blocks_per_seq,
+                     context_lens, query_start, num_seqs, max_q_len, num_kv_heads, head_dim,
+                     block_size, num_blocks, PA_FP16, pa::Kv::kFp4, stream);
+}
+
+pa_status pa_select_blocks(int32_t *selected_tables, int32_t *selected_lens, const void *query,
+                           const int8_t *bounds, const float *bound_scales,
+                           const int32_t *block_tables, int32_t max_blocks_per_seq,
+                           const int32_t *context_lens, const int32_t *query_start,
+                           int32_t num_seqs, int32_t max_q_len, int32_t num_q_heads,
+                           int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                           int64_t num_blocks, int32_t max_context_len, int32_t num_selected,
+                           int32_t num_sink, int32_t num_recent, int32_t dtype, void *stream) {
+  if (num_seqs < 0 || max_q_len < 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+      num_blocks <= 0 || max_blocks_per_seq <= 0 || max_context_len < 0 || num_selected <= 0 ||
+      num_sink < 0 || num_recent < 0 ||
+      static_cast<int64_t>(num_sink) + num_recent > num_selected || !dtype_ok(dtype) ||
+      (!query_start && max_q_len > 1))
+    return PA_ERR_INVALID_ARG;
+  if (num_q_heads % num_kv_heads) return PA_ERR_INVALID_ARG;
+  const int32_t group = num_q_heads / num_kv_heads;
+  if (!head_dim_ok(head_dim) || !block_size_ok(block_size) || group > 8)
+    return PA_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || max_q_len == 0) return PA_OK;
+  if (!selected_tables || !selected_lens || !query || !bounds || !bound_scales ||
+      !block_tables || !context_lens || !aligned16(query) || !aligned16(bounds))
+    return PA_ERR_INVALID_ARG;
+  if (!pool_ok(num_blocks, num_kv_heads, block_size) || num_seqs > 65535 || num_kv_heads > 65535)
+    return PA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_selected) * block_size > 0x7fffffff ||
+      max_q_len > 0x7fffffff / 8)
+    return PA_ERR_UNSUPPORTED;
+  const int64_t most = std::min<int64_t>(
+      (static_cast<int64_t>(max_context_len) + block_size - 1) / block_size, max_blocks_per_seq);
+  if (most > pa::kMaxCandidates) return PA_ERR_UNSUPPORTED;
+  unsigned int *err = nullptr;
+  if (error_word(&err) != cudaSuccess) return PA_ERR_CUDA;
+  pa::SelectArgs a{};
+  a.tables = selected_tables;
+  a.lens = selected_lens;
+  a.query = query;
+  a.bounds = bounds;
+  a.bound_scales = bound_scales;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.query_start = query_start;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.max_q_len = max_q_len;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.group = group;
+  a.bs_log2 = block_size == 16 ? 4 : 5;
+  a.num_blocks = num_blocks;
+  a.max_context_len = max_context_len;
+  a.num_selected = num_selected;
+  a.num_sink = num_sink;
+  a.num_recent = num_recent;
+  a.max_candidates = static_cast<int>(most);
+  a.err = err;
+  return pa::launch_select(a, head_dim, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+pa_status pa_decode_sparse(void *out, const void *query, const void *k_cache, const void *v_cache,
+                           const int32_t *selected_tables, const int32_t *selected_lens,
+                           int32_t num_rows, int32_t num_selected, int32_t num_q_heads,
+                           int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                           int64_t num_blocks, float scale, int32_t dtype, void *stream) {
+  return sparse_impl(out, query, k_cache, v_cache, selected_tables, selected_lens, num_rows,
+                     num_selected, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                     scale, dtype, pa::Kv::k16, 1.f, 1.f, stream);
+}
+
+pa_status pa_decode_sparse_fp8(void *out, const void *query, const void *k_cache,
+                               const void *v_cache, const int32_t *selected_tables,
+                               const int32_t *selected_lens, int32_t num_rows,
+                               int32_t num_selected, int32_t num_q_heads, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                               float scale, float k_scale, float v_scale, int32_t dtype,
+                               void *stream) {
+  if (!fp8_scales_ok(k_scale, v_scale)) return PA_ERR_INVALID_ARG;
+  return sparse_impl(out, query, k_cache, v_cache, selected_tables, selected_lens, num_rows,
+                     num_selected, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                     scale, dtype, pa::Kv::kFp8, k_scale, v_scale, stream);
+}
+
+pa_status pa_decode_sparse_fp4(void *out, const void *query, const void *k_cache,
+                               const void *v_cache, const int32_t *selected_tables,
+                               const int32_t *selected_lens, int32_t num_rows,
+                               int32_t num_selected, int32_t num_q_heads, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                               float scale, float k_scale, float v_scale, int32_t dtype,
+                               void *stream) {
+  if (!fp4_scales_ok(k_scale, v_scale)) return PA_ERR_INVALID_ARG;
+  if (!fp4_table_ok(block_size, num_selected)) return PA_ERR_UNSUPPORTED;
+  return sparse_impl(out, query, k_cache, v_cache, selected_tables, selected_lens, num_rows,
+                     num_selected, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                     scale, dtype, pa::Kv::kFp4, k_scale, v_scale, stream);
 }
 
 }  // extern "C"

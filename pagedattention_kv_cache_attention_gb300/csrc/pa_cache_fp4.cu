@@ -29,6 +29,7 @@
 #include "pa_device.cuh"
 #include "pa_fp4.cuh"
 #include "pa_internal.h"
+#include "pa_rope.cuh"
 
 #ifndef PA_CACHE_FP4_BATCH
 #define PA_CACHE_FP4_BATCH 4
@@ -46,18 +47,21 @@ constexpr int kBatch = PA_CACHE_FP4_BATCH;  // items of K and of V that a lane h
 
 // Calls body(token, slot, item0) for the tokens of this warp: a lane's items
 // are item0, item0 + 32, ... below Hkv * D / 8 (none if item0 is not).
-template <int D, typename F>
-__device__ __forceinline__ void for_tokens(const Fp4CacheArgs &a, F &&body) {
+// (ctas: the CTAs that share the tokens)
+template <int D, typename Args, typename F>
+__device__ __forceinline__ void for_tokens(const Args &a, unsigned ctas, F &&body) {
   const int lane = threadIdx.x & 31, items = a.num_kv_heads * (D / 8);
   const int per_warp = items < 32 ? 32 / items : 1;  // tokens that a warp takes at once
   const int sub = items < 32 ? lane / items : 0;
   const int item0 = sub < per_warp ? lane - sub * items : items;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * per_warp;
+  const int64_t step = static_cast<int64_t>(ctas) * kWarps * per_warp;
   for (int64_t t = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * per_warp;
        t < a.num_tokens; t += step) {
     const int64_t token = t + sub;
     int64_t slot = sub < per_warp && token < a.num_tokens ? a.slot_mapping[token] : -1;
-    if (slot >= (a.num_blocks << a.bs_log2)) {
+    if constexpr (std::is_same<Args, RopeArgs>::value) {
+      if (slot >= 0 && !rope_token(a, slot, a.positions[token], item0 == 0)) slot = -1;
+    } else if (slot >= (a.num_blocks << a.bs_log2)) {
       if (item0 == 0) atomicOr(a.err, kErrBadSlot);
       slot = -1;
     }
@@ -71,7 +75,8 @@ __device__ __forceinline__ void for_tokens(const Fp4CacheArgs &a, F &&body) {
 template <int D> struct Place {
   int codes, scale, step;
   int64_t tile0;
-  __device__ __forceinline__ Place(const Fp4CacheArgs &a, int64_t slot, int item0) {
+  template <typename Args>
+  __device__ __forceinline__ Place(const Args &a, int64_t slot, int item0) {
     constexpr int kPerHead = D / 8;
     const int bs = 1 << a.bs_log2, row = static_cast<int>(slot) & (bs - 1);
     const int h = item0 / kPerHead, b = item0 % kPerHead;
@@ -137,7 +142,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache_fp4_write_kernel(const Fp4C
   grid_launch_dependents();  // the next kernel may start its set-up now
   const int items = a.num_kv_heads * (D / 8);
   const bool odd = threadIdx.x & 1;
-  for_tokens<D>(a, [&](int64_t token, int64_t slot, int item0) {
+  for_tokens<D>(a, gridDim.x, [&](int64_t token, int64_t slot, int item0) {
     const uint4 *key = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.key) +
                                                        token * a.key_stride);
     const uint4 *value = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.value) +
@@ -170,6 +175,94 @@ __global__ void __launch_bounds__(kWarps * 32) cache_fp4_write_kernel(const Fp4C
   });
 }
 
+// pa_rope_and_cache_fp4.  The first `kv_ctas` CTAs write K and V as above, with
+// each lane's chunk of K rotated on the way: it needs the chunk that holds the
+// other elements of its pairs (nothing where pairs are neighbours), which another
+// lane of the warp loads too, so the second load comes out of L1.  The other CTAs
+// rotate the queries.
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32) cache_fp4_rope_kernel(const RopeArgs a,
+                                                                     const unsigned kv_ctas) {
+  constexpr int kTake = 2;   // items of K and of V that a lane has in flight
+  grid_dependency_wait();    // rows and slots may come from the kernel before
+  grid_launch_dependents();  // the next kernel may start its set-up now
+  if (blockIdx.x >= kv_ctas) {
+    const int64_t t = static_cast<int64_t>(blockIdx.x - kv_ctas) * (kWarps * 32 >> a.group_log2) +
+                      (threadIdx.x >> a.group_log2);
+    if (t < a.num_tokens)
+      rope_token_heads<T, D, false>(a, t, threadIdx.x & ((1 << a.group_log2) - 1), a.num_q_heads);
+    return;
+  }
+  const int items = a.num_kv_heads * (D / 8);
+  const bool odd = threadIdx.x & 1;
+  for_tokens<D>(a, kv_ctas, [&](int64_t token, int64_t slot, int item0) {
+    const uint4 *key = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.key) +
+                                                       token * a.key_stride);
+    const uint4 *value = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.value) +
+                                                         token * a.value_stride);
+    const Place<D> at(a, slot, item0);
+    uint8_t *kc = static_cast<uint8_t *>(a.k_cache) + at.tile0;
+    uint8_t *vc = static_cast<uint8_t *>(a.v_cache) + at.tile0;
+    // chunk b of its head: pairs with chunk b + other, cosines and sines of its
+    // 8 elements (negated sines where the element is the pair's first)
+    const int b = item0 % (D / 8), half = a.rotary_dim / 16;
+    const bool turn = item0 < items && b < 2 * half;
+    const int other = a.interleaved || !turn ? 0 : b < half ? half : -half;
+    float c[8], s[8];
+    if (turn) {
+      const float *row = a.cos_sin + a.positions[token] * a.rotary_dim;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int pair = a.interleaved ? 4 * b + i / 2 : 8 * (b < half ? b : b - half) + i;
+        c[i] = row[pair];
+        s[i] = row[a.rotary_dim / 2 + pair];
+      }
+    }
+    // (every lane of the warp runs through: neighbours shuffle)
+    for (int i0 = 0; i0 < items; i0 += 32 * kTake) {
+      uint4 k[kTake], p[kTake], v[kTake];
+#pragma unroll
+      for (int i = 0; i < kTake; ++i) {
+        const int item = item0 + i0 + 32 * i;
+        k[i] = item < items ? key[item] : make_uint4(0, 0, 0, 0);
+        p[i] = item < items ? key[item + other] : make_uint4(0, 0, 0, 0);
+        v[i] = item < items ? value[item] : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kTake; ++i) {
+        if (i0 + 32 * i >= items) break;
+        if (turn) {
+          uint32_t w4[4];
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float2 x = Elem<T>::unpack(word_of(k[i], w)), y = Elem<T>::unpack(word_of(p[i], w));
+            float lo, hi, unused;
+            if (a.interleaved) {
+              rope_pair(x.x, x.y, c[2 * w], s[2 * w], lo, hi);
+            } else if (b < half) {
+              rope_pair(x.x, y.x, c[2 * w], s[2 * w], lo, unused);
+              rope_pair(x.y, y.y, c[2 * w + 1], s[2 * w + 1], hi, unused);
+            } else {
+              rope_pair(y.x, x.x, c[2 * w], s[2 * w], unused, lo);
+              rope_pair(y.y, x.y, c[2 * w + 1], s[2 * w + 1], unused, hi);
+            }
+            w4[w] = Elem<T>::pack(lo, hi);
+          }
+          k[i] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+        }
+        const int off = (i0 / 32 + i) * at.step;
+        uint32_t kq, vq, scale;
+        quantise8<T>(k[i], v[i], odd ? a.v_scale : a.k_scale, kq, vq, scale);
+        if (item0 + i0 + 32 * i < items) {
+          *reinterpret_cast<uint32_t *>(kc + at.codes + off) = kq;
+          *reinterpret_cast<uint32_t *>(vc + at.codes + off) = vq;
+          (odd ? vc : kc)[at.scale + off] = static_cast<uint8_t>(scale);
+        }
+      }
+    }
+  });
+}
+
 // 8 codes times s g, in fp32, rounded to the row's type.
 template <typename T>
 __device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t scale, float g) {
@@ -189,7 +282,7 @@ __global__ void __launch_bounds__(kWarps * 32) cache_fp4_read_kernel(const Fp4Ca
   grid_dependency_wait();  // the pool and the slots may come from the kernel before
   grid_launch_dependents();
   const int items = a.num_kv_heads * (D / 8);
-  for_tokens<D>(a, [&](int64_t token, int64_t slot, int item0) {
+  for_tokens<D>(a, gridDim.x, [&](int64_t token, int64_t slot, int item0) {
     uint4 *key = reinterpret_cast<uint4 *>(static_cast<T *>(a.key) + token * a.key_stride);
     uint4 *value = reinterpret_cast<uint4 *>(static_cast<T *>(a.value) + token * a.value_stride);
     const Place<D> at(a, slot, item0);
@@ -219,14 +312,28 @@ __global__ void __launch_bounds__(kWarps * 32) cache_fp4_read_kernel(const Fp4Ca
   });
 }
 
+// CTAs for the K and V rows of a call.
+unsigned kv_ctas(int num_tokens, int num_kv_heads, int head_dim) {
+  const int items = num_kv_heads * (head_dim / 8);
+  const int per_cta = kWarps * (items < 32 ? 32 / items : 1);
+  const int64_t ctas = (static_cast<int64_t>(num_tokens) + per_cta - 1) / per_cta;
+  const int64_t most = kSms * PA_CACHE_FP4_CTAS;  // then a warp takes several tokens in turn
+  return static_cast<unsigned>(ctas < most ? ctas : most);
+}
+
 template <typename K>
 cudaError_t launch(K kern, const Fp4CacheArgs &a, cudaStream_t stream) {
-  const int items = a.num_kv_heads * (a.head_dim / 8);
-  const int per_cta = kWarps * (items < 32 ? 32 / items : 1);
-  const int64_t ctas = (static_cast<int64_t>(a.num_tokens) + per_cta - 1) / per_cta;
-  const int64_t most = kSms * PA_CACHE_FP4_CTAS;  // then a warp takes several tokens in turn
-  return launch_dependent(kern, dim3(static_cast<unsigned>(ctas < most ? ctas : most)),
+  return launch_dependent(kern, dim3(kv_ctas(a.num_tokens, a.num_kv_heads, a.head_dim)),
                           dim3(kWarps * 32), 0, stream, a);
+}
+
+template <typename T, int D> cudaError_t launch_rope(RopeArgs a, cudaStream_t stream) {
+  a.group_log2 = rope_group_log2(a.num_q_heads * (D / 16));
+  const unsigned per_cta = kWarps * 32 >> a.group_log2;
+  const unsigned kv = kv_ctas(a.num_tokens, a.num_kv_heads, D);
+  return launch_dependent(cache_fp4_rope_kernel<T, D>,
+                          dim3(kv + (a.num_tokens + per_cta - 1) / per_cta), dim3(kWarps * 32), 0,
+                          stream, a, kv);
 }
 
 }  // namespace
@@ -237,6 +344,13 @@ cudaError_t launch_cache_fp4_write(const Fp4CacheArgs &a, int dtype, cudaStream_
                              : launch(cache_fp4_write_kernel<__half, 64>, a, stream);
   return a.head_dim == 128 ? launch(cache_fp4_write_kernel<__nv_bfloat16, 128>, a, stream)
                            : launch(cache_fp4_write_kernel<__nv_bfloat16, 64>, a, stream);
+}
+
+cudaError_t launch_rope_fp4(const RopeArgs &a, int head_dim, int dtype, cudaStream_t stream) {
+  if (dtype == 0)
+    return head_dim == 128 ? launch_rope<__half, 128>(a, stream) : launch_rope<__half, 64>(a, stream);
+  return head_dim == 128 ? launch_rope<__nv_bfloat16, 128>(a, stream)
+                         : launch_rope<__nv_bfloat16, 64>(a, stream);
 }
 
 cudaError_t launch_cache_fp4_read(const Fp4CacheArgs &a, int dtype, cudaStream_t stream) {

@@ -230,7 +230,8 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
   // are numbered l in its own order; 32 lanes hold a window of 32 of them.
   const int t_begin = kParts ? part * a.part_tokens : 0;
   const int base = t_begin & ~31;
-  const int32_t *bt_row = a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq;
+  const int64_t table = a.per_head ? static_cast<int64_t>(seq) * a.num_kv_heads + kvh : seq;
+  const int32_t *bt_row = a.block_tables + table * a.max_blocks_per_seq;
   const int wid = rank * NW + warp, n_warps = NW * cluster;
   // (unsigned: max_context_len may be any int, and with it a partition past the
   // table's end may pass 2^31)
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
   int win = table_entry(lane);  // read before the length arrives; entries past it are not used
 
   const int G = a.group;
-  int ctx = a.context_lens[seq];
+  int ctx = a.context_lens[table];
   int q0 = seq, n_rows = G, base_pos = 0;  // the chunk's first token, its rows, its position
   if constexpr (kChunk) {
     q0 = a.query_start[seq];
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(NW * 32, ctas_per_sm(NT))
     }
     if (n_rows == 0) return;  // (n_rows <= 8 NT: the launch has NT for max_q_len)
   } else if (ctx < 0 || ctx > a.max_blocks_per_seq * BS || ctx > a.max_context_len) {
-    if (threadIdx.x == 0 && part == 0 && kvh == 0) atomicOr(a.err, kErrBadLen);
+    if (threadIdx.x == 0 && part == 0 && (kvh == 0 || a.per_head)) atomicOr(a.err, kErrBadLen);
     ctx = 0;
   }
   if (part > 0 && t_begin >= ctx) return;
@@ -841,7 +842,7 @@ cudaError_t launch_rows(DecodeArgs a, const CUtensorMap &km, const CUtensorMap &
   // sequences of up to 16,384 128 us against 117, since every empty partition's CTA
   // asks for its sequence too.
   const int64_t ctas = static_cast<int64_t>(grid_x) * a.num_kv_heads * a.num_seqs;
-  a.by_length = !kParts && a.cluster == 1 &&
+  a.by_length = !kParts && a.cluster == 1 && !a.per_head &&
                 a.num_seqs > 1 && a.num_seqs <= kMaxByLength && ctas > kSms * ctas_per_sm(NT) &&
                 (static_cast<int64_t>(a.max_blocks_per_seq) << a.bs_log2) >= kMinByLength &&
                 (ROWS == Rows::kChunk || a.max_context_len >= kMinByLength);

@@ -1,0 +1,444 @@
+// pa_decode_sparse.cu -- decode attention over a block table and a length for
+// each (row, KV head), 16-bit and FP8 caches (pa_decode_sparse,
+// pa_decode_sparse_fp8):
+//   out = sum_j softmax_j(scale q . K_j) V_j,   j < lens[row, KV head].
+//
+// How:
+//  * The warps of a cluster of 1 to 8 CTAs share the tokens of one (row, KV
+//    head) and serve its G query heads.  A warp takes steps of NSUB 16-token
+//    sub-tiles in turn, brought in by TMA into its own ring of S stages, and
+//    computes on them as the dense decode kernel does (pa_tile.cuh): S^T = K Q^T
+//    and O^T += V^T P^T on mma.sync, fp32 online softmax, P in two parts.
+//  * The warps' (m, l, o) are merged through shared memory, the CTAs' through one
+//    another's: no workspace, no second kernel.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+#include "pa_tile.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr int kMaxCluster = 8;
+
+// S^T = K Q^T of an FP8 sub-tile: unit c D/64 + j of rows g and g + 8 holds 16
+// dimensions, four k16 steps, widened to fp16 on the way.
+template <int D>
+__device__ __forceinline__ void qk_subtile_8(const uint8_t *Ks, const uint4 (&qf)[D / 32], int g,
+                                             int c, float (&sc)[4]) {
+  sc[0] = sc[1] = sc[2] = sc[3] = 0.f;
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j) {
+    const int u = c * (D / 64) + j;
+    uint32_t ka[8], kb[8];
+    e4m3x16_to_half(*reinterpret_cast<const uint4 *>(f8_unit<D>(Ks, g, u)), ka);
+    e4m3x16_to_half(*reinterpret_cast<const uint4 *>(f8_unit<D>(Ks, g + 8, u)), kb);
+    const uint4 q0 = qf[2 * j], q1 = qf[2 * j + 1];
+    const uint32_t q[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      Elem<__half>::mma(sc, ka[2 * t], kb[2 * t], ka[2 * t + 1], kb[2 * t + 1], q[2 * t],
+                        q[2 * t + 1]);
+  }
+}
+
+// O^T += V^T P^T of an FP8 sub-tile: the lane's dimensions (pv_dim_a, pv_dim_b) of
+// rows 2c, 2c + 1, 2c + 8, 2c + 9; rows from nvalid on are zeros.  Two rows' bytes
+// are interleaved while they are still E4M3: a converted pair is (row, next row).
+template <int D>
+__device__ __forceinline__ void pv_subtile_8(const uint8_t *Vs, int nvalid, int g, int c,
+                                             uint32_t pb0, uint32_t pb1, uint32_t pr0,
+                                             uint32_t pr1, float (&acc)[D / 16][4]) {
+  constexpr int kHi = D == 128 ? 8 : 4;  // byte of pv_dim_b within the lane's dimensions
+  uint4 v[4];
+#pragma unroll
+  for (int ri = 0; ri < 4; ++ri) {
+    const int r = 2 * c + (ri & 1) + 8 * (ri >> 1);
+    v[ri] = make_uint4(0, 0, 0, 0);
+    if constexpr (D == 128) {
+      if (r < nvalid) v[ri] = *reinterpret_cast<const uint4 *>(f8_unit<D>(Vs, r, g));
+    } else {
+      const uint2 half = *reinterpret_cast<const uint2 *>(f8_unit<D>(Vs, r, g >> 1) + (g & 1) * 8);
+      if (r < nvalid) v[ri] = make_uint4(half.x, half.y, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int mt = 0; mt < D / 16; mt += 2) {
+    const uint32_t w0 = interleave_bytes(v[0], v[1], mt), w1 = interleave_bytes(v[0], v[1], kHi + mt);
+    const uint32_t w2 = interleave_bytes(v[2], v[3], mt), w3 = interleave_bytes(v[2], v[3], kHi + mt);
+    const uint32_t a[2][4] = {{e4m3x2_lo_to_f16x2(w0), e4m3x2_lo_to_f16x2(w1),
+                               e4m3x2_lo_to_f16x2(w2), e4m3x2_lo_to_f16x2(w3)},
+                              {e4m3x2_hi_to_f16x2(w0), e4m3x2_hi_to_f16x2(w1),
+                               e4m3x2_hi_to_f16x2(w2), e4m3x2_hi_to_f16x2(w3)}};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      Elem<__half>::mma(acc[mt + i], a[i][0], a[i][1], a[i][2], a[i][3], pb0, pb1);
+      Elem<__half>::mma(acc[mt + i], a[i][0], a[i][1], a[i][2], a[i][3], pr0, pr1);
+    }
+  }
+}
+
+// bf16 queries beside FP8 keys: times the power of two that brings the largest
+// of the warp's into [2^14, 2^15), as fp16 (exact for every value down to 2^-31 of
+// the largest); returns the exponent.
+template <int N> __device__ __forceinline__ int queries_to_half(uint4 (&qf)[N]) {
+  float mx = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float2 v = Elem<__nv_bfloat16>::unpack(word_of(qf[i], w));
+      mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
+    }
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
+  const int ex = static_cast<int>((__float_as_uint(mx) >> 23) & 0xffu) - 127;
+  const int e = min(120, 14 - ex);
+  const float f = ldexpf(1.f, e);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint32_t h[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float2 v = Elem<__nv_bfloat16>::unpack(word_of(qf[i], w));
+      h[w] = Elem<__half>::pack(v.x * f, v.y * f);
+    }
+    qf[i] = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+  return e;
+}
+
+template <typename T, int D, int NW, int S, bool F8, int NSUB>
+__global__ void __launch_bounds__(NW * 32)
+    sparse_decode_kernel(const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap vmap, const DecodeArgs a) {
+  using Sh = Shape<D, F8>;
+  using MT = typename std::conditional<F8, __half, T>::type;  // E4M3 is exact in fp16
+  static_assert(NSUB == 1 || NSUB == 2 || NSUB == 4, "a step's sub-tiles lie in one window");
+  static_assert(S * NSUB <= 32, "stage bits; the first window holds every stage's sub-tiles");
+  constexpr int kStepBytes = 2 * NSUB * Sh::kTileBytes;  // K and V of one step
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + NW * S * kStepBytes);
+
+  const int cluster = a.cluster, rank = static_cast<int>(blockIdx.x);
+  const int kvh = blockIdx.y, row = blockIdx.z;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int wid = rank * NW + warp, n_warps = NW * cluster;
+
+  uint8_t *my_stages = smem + warp * S * kStepBytes;
+  uint64_t *my_bars = bars + warp * S;
+  if (lane == 0) {
+#pragma unroll
+    for (int s = 0; s < S; ++s) mbar_init(&my_bars[s], 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  grid_dependency_wait();  // tables, queries and the pool may come from the kernel before
+
+  // Step k of the warp covers sub-tiles (wid + k n_warps) NSUB + h.  "Local"
+  // sub-tile l = k NSUB + h; the lanes hold the block ids of a window of 32.
+  const int64_t table = static_cast<int64_t>(row) * a.num_kv_heads + kvh;
+  const int32_t *bt_row = a.block_tables + table * a.max_blocks_per_seq;
+  const int bs_mask = (1 << a.bs_log2) - 1;
+  auto sub_of = [&](int l) -> int64_t {
+    return (wid + static_cast<int64_t>(l / NSUB) * n_warps) * NSUB + l % NSUB;
+  };
+  auto table_entry = [&](int l) -> int {
+    const int64_t lb = sub_of(l) * kTile >> a.bs_log2;
+    return lb < a.max_blocks_per_seq ? bt_row[lb] : -1;
+  };
+  int win = table_entry(lane);  // read before the length arrives; entries past it are not used
+  int len = a.context_lens[table];
+  if (len < 0 || len > a.max_context_len) {
+    if (threadIdx.x == 0 && rank == 0) atomicOr(a.err, kErrBadLen);
+    len = 0;
+  }
+  const int n_sub = (len + kTile - 1) / kTile, n_step = (n_sub + NSUB - 1) / NSUB;
+  const int my_n = n_step > wid ? (n_step - wid + n_warps - 1) / n_warps : 0;
+
+  // physical block of local sub-tile l, -1 if past the end or invalid (flagged; its
+  // tokens are masked)
+  auto checked = [&](int l, int phys) -> int {
+    if (l >= my_n * NSUB || sub_of(l) >= n_sub) return -1;
+    if (phys < 0 || static_cast<int64_t>(phys) >= a.num_blocks) {
+      atomicOr(a.err, kErrBadBlock);
+      return -1;
+    }
+    return phys;
+  };
+  const uint64_t policy = l2_policy_evict_first();
+  auto issue = [&](int k, const int (&phys)[NSUB], int s) {  // lane 0
+    uint64_t *bar = &my_bars[s];
+    uint32_t bytes = 0;
+#pragma unroll
+    for (int h = 0; h < NSUB; ++h) bytes += phys[h] >= 0 ? 2 * Sh::kTileBytes : 0;
+    if (bytes == 0) {
+      mbar_arrive(bar);
+      return;
+    }
+    mbar_arrive_expect_tx(bar, bytes);
+    uint8_t *st = my_stages + s * kStepBytes;
+#pragma unroll
+    for (int h = 0; h < NSUB; ++h) {
+      if (phys[h] < 0) continue;
+      const int tok = static_cast<int>(sub_of(k * NSUB + h)) * kTile;
+      const int y = ((phys[h] * a.num_kv_heads + kvh) << a.bs_log2) + (tok & bs_mask);
+#pragma unroll
+      for (int b = 0; b < Sh::kBoxes; ++b) {
+        tma_load_2d(st + h * Sh::kTileBytes + b * Sh::kBoxBytes, &kmap, b * Sh::kBoxElems, y, bar,
+                    policy);
+        tma_load_2d(st + (NSUB + h) * Sh::kTileBytes + b * Sh::kBoxBytes, &vmap,
+                    b * Sh::kBoxElems, y, bar, policy);
+      }
+    }
+  };
+
+  int win_base = 0;
+  win = checked(lane, win);
+  int win_next = my_n * NSUB > 32 ? checked(32 + lane, table_entry(32 + lane)) : -1;
+  uint32_t stage_ok = 0;  // bit s NSUB + h: sub-tile h of the step in stage s is valid
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    if (s < my_n) {
+      int phys[NSUB];
+#pragma unroll
+      for (int h = 0; h < NSUB; ++h) {
+        phys[h] = __shfl_sync(kFull, win, s * NSUB + h);
+        stage_ok |= (phys[h] >= 0 ? 1u : 0u) << (s * NSUB + h);
+      }
+      if (lane == 0) issue(s, phys, s);
+    }
+  }
+
+  // query fragments of head g, in the order in which the keys are read
+  const int G = a.group;
+  uint4 qf[Sh::kQChunks];
+  float scale_log2 = a.scale_log2;
+  {
+    const T *q = static_cast<const T *>(a.query) +
+                 (static_cast<int64_t>(row) * a.num_q_heads + kvh * G + g) * D;
+#pragma unroll
+    for (int i = 0; i < Sh::kQChunks; ++i) {
+      const int ch = F8 ? 2 * (c * (D / 64) + (i >> 1)) + (i & 1) : q_chunk(i, c);
+      qf[i] = g < G ? *reinterpret_cast<const uint4 *>(q + ch * 8) : make_uint4(0, 0, 0, 0);
+    }
+    if constexpr (F8 && !std::is_same<T, __half>::value)
+      scale_log2 = ldexpf(scale_log2, -queries_to_half(qf));
+  }
+
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2c, 2c + 1
+  float acc[Sh::kMTiles][4];
+#pragma unroll
+  for (int mt = 0; mt < Sh::kMTiles; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
+
+  int k = 0;
+  bool timed_out = false;
+#pragma unroll 1
+  for (; k < my_n; ++k) {
+    const int s = k % S;
+    if (!__all_sync(kFull, mbar_wait_bounded(&my_bars[s], (k / S) & 1))) {
+      if (lane == 0) atomicOr(a.err, kErrTimeout);
+      timed_out = true;
+      break;
+    }
+    const uint8_t *stage = my_stages + s * kStepBytes;
+    int nvalid[NSUB];
+    float sc[NSUB][4], p[NSUB][4];
+#pragma unroll
+    for (int h = 0; h < NSUB; ++h) {
+      const bool ok = (stage_ok >> (s * NSUB + h)) & 1u;
+      const int tok = static_cast<int>(sub_of(k * NSUB + h)) * kTile;
+      nvalid[h] = ok ? max(0, min(kTile, len - tok)) : 0;
+      if constexpr (F8)
+        qk_subtile_8<D>(stage + h * Sh::kTileBytes, qf, g, c, sc[h]);
+      else
+        qk_subtile_16<MT, D>(stage + h * Sh::kTileBytes, qf, g, c, sc[h]);
+    }
+    softmax_step<NSUB, Sh::kMTiles>(sc, nvalid, g, scale_log2, m0, m1, l0, l1, acc, p);
+#pragma unroll
+    for (int h = 0; h < NSUB; ++h) {
+      uint32_t pb0, pb1, pr0, pr1;
+      p_operands<MT>(p[h], pb0, pb1, pr0, pr1);
+      const uint8_t *Vs = stage + (NSUB + h) * Sh::kTileBytes;
+      if constexpr (F8)
+        pv_subtile_8<D>(Vs, nvalid[h], g, c, pb0, pb1, pr0, pr1, acc);
+      else
+        pv_subtile_16<MT, D>(Vs, nvalid[h], g, c, pb0, pb1, pr0, pr1, acc);
+    }
+    // refill this stage with step k + S
+    __syncwarp();
+    const int nk = k + S;
+    if (nk < my_n) {
+      if (nk * NSUB >= win_base + 32) {
+        win_base += 32;
+        win = win_next;
+        win_next = checked(win_base + 32 + lane, table_entry(win_base + 32 + lane));
+      }
+      int phys[NSUB];
+#pragma unroll
+      for (int h = 0; h < NSUB; ++h) {
+        phys[h] = __shfl_sync(kFull, win, nk * NSUB + h - win_base);
+        stage_ok = (stage_ok & ~(1u << (s * NSUB + h))) |
+                   ((phys[h] >= 0 ? 1u : 0u) << (s * NSUB + h));
+      }
+      if (lane == 0) {
+        fence_proxy_async_smem();
+        issue(nk, phys, s);
+      }
+    }
+  }
+  // after a wait that ran out, copies already in flight land before the CTA
+  // leaves (bounded again)
+  for (const int filled = min(k + S, my_n); timed_out && k < filled; ++k)
+    (void)mbar_wait_bounded(&my_bars[k % S], (k / S) & 1);
+
+  // row sums over the 8 token rows (lanes differing in g)
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) {
+    l0 += __shfl_xor_sync(kFull, l0, off);
+    l1 += __shfl_xor_sync(kFull, l1, off);
+  }
+  // ---- merge the warps through shared memory (stages are idle now)
+  __syncthreads();
+  float *wacc = reinterpret_cast<float *>(smem);  // [NW][8][D]
+  float *wml = wacc + NW * 8 * D;                 // [NW][8][2]
+  float *cl_o = wml + NW * 8 * 2;                 // [8][D]: the CTA's, for its cluster
+  float *cl_ml = cl_o + 8 * D;                    // [8][2]
+  if (g == 0) {
+    wml[(warp * 8 + 2 * c) * 2 + 0] = m0;
+    wml[(warp * 8 + 2 * c) * 2 + 1] = l0;
+    wml[(warp * 8 + 2 * c + 1) * 2 + 0] = m1;
+    wml[(warp * 8 + 2 * c + 1) * 2 + 1] = l1;
+  }
+  store_partial_o<D, F8>(wacc + (warp * 8 + 2 * c) * D, wacc + (warp * 8 + 2 * c + 1) * D, true,
+                         true, acc, 1.f, 1.f, g);
+  __syncthreads();
+  constexpr int kChunks = D / 8;
+  T *out = static_cast<T *>(a.out) + (static_cast<int64_t>(row) * a.num_q_heads + kvh * G) * D;
+  auto put = [&](int h, int ch, float L, float (&o)[8]) {
+    const float inv = L > 0.f ? a.out_scale / L : 0.f;
+    *reinterpret_cast<uint4 *>(out + h * D + ch * 8) = make_uint4(
+        Elem<T>::pack(o[0] * inv, o[1] * inv), Elem<T>::pack(o[2] * inv, o[3] * inv),
+        Elem<T>::pack(o[4] * inv, o[5] * inv), Elem<T>::pack(o[6] * inv, o[7] * inv));
+  };
+  for (int item = threadIdx.x; item < G * kChunks; item += NW * 32) {
+    const int h = item / kChunks, ch = item % kChunks;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, wml[(w * 8 + h) * 2]);
+    float L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float mw = wml[(w * 8 + h) * 2];
+      const float f = mw == -INFINITY ? 0.f : exp2f(mw - M);
+      L += wml[(w * 8 + h) * 2 + 1] * f;
+      const float *src = wacc + (w * 8 + h) * D + ch * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] += src[e] * f;
+    }
+    if (cluster == 1) {
+      put(h, ch, L, o);
+      continue;
+    }
+    float4 *dst = reinterpret_cast<float4 *>(cl_o + h * D + ch * 8);
+    dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+    if (ch == 0) {
+      cl_ml[h * 2] = M;
+      cl_ml[h * 2 + 1] = L;
+    }
+  }
+  if (cluster > 1) {
+    // the cluster's CTAs share the heads' chunks of the join out
+    cluster_sync();
+    for (int item = threadIdx.x + rank * NW * 32; item < G * kChunks; item += NW * 32 * cluster) {
+      const int h = item / kChunks, ch = item % kChunks;
+      float M = -INFINITY;
+      for (int r = 0; r < cluster; ++r)
+        M = fmaxf(M, ld_cluster_f2(cluster_addr(cl_ml + h * 2, r)).x);
+      float L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int r = 0; r < cluster; ++r) {
+        const float2 ml = ld_cluster_f2(cluster_addr(cl_ml + h * 2, r));
+        const uint32_t src = cluster_addr(cl_o + h * D + ch * 8, r);
+        const float4 x = ld_cluster_f4(src), y = ld_cluster_f4(src + 16);
+        const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+        L += ml.y * f;
+        o[0] += x.x * f;
+        o[1] += x.y * f;
+        o[2] += x.z * f;
+        o[3] += x.w * f;
+        o[4] += y.x * f;
+        o[5] += y.y * f;
+        o[6] += y.z * f;
+        o[7] += y.w * f;
+      }
+      put(h, ch, L, o);
+    }
+    cluster_sync();  // nobody leaves while its memory is read
+  }
+  grid_launch_dependents();
+}
+
+// CTAs that share a row's tokens: as many as the SMs have room for, while a warp
+// keeps two steps of the longest table.
+int cluster_of(const DecodeArgs &a, int64_t ctas, int warps, int per_sm, int step_tokens) {
+  const int64_t steps = a.max_context_len / step_tokens;
+  int n = 1;
+  while (n < kMaxCluster && 2 * n * ctas <= kSms * per_sm && steps >= 4 * n * warps) n *= 2;
+  return n;
+}
+
+template <typename T, int D, int NW, int S, bool F8, int NSUB>
+cudaError_t launch_t(DecodeArgs a, const CUtensorMap &km, const CUtensorMap &vm,
+                     cudaStream_t stream) {
+  using Sh = Shape<D, F8>;
+  constexpr size_t stages = static_cast<size_t>(NW) * S * 2 * NSUB * Sh::kTileBytes;
+  constexpr size_t smem = 1024 + stages + NW * S * 8;
+  static_assert((static_cast<size_t>(NW) + 1) * 8 * (D + 2) * 4 <= stages,
+                "merge buffers must fit in the stage area");
+  auto kern = sparse_decode_kernel<T, D, NW, S, F8, NSUB>;
+  static SmemLimitOnce smem_limit;
+  const cudaError_t e = smem_limit.ensure(kern, smem);
+  if (e != cudaSuccess) return e;
+  constexpr int per_sm = static_cast<int>(227 * 1024 / (smem + 1024));
+  a.cluster = cluster_of(a, static_cast<int64_t>(a.num_seqs) * a.num_kv_heads, NW, per_sm,
+                         NSUB * kTile);
+  return launch_clusters(a.cluster, kern, dim3(a.cluster, a.num_kv_heads, a.num_seqs),
+                         dim3(NW * 32), smem, stream, km, vm, a);
+}
+
+template <typename T, int D>
+cudaError_t launch_d(const DecodeArgs &a, bool kv_fp8, const CUtensorMap &km,
+                     const CUtensorMap &vm, cudaStream_t stream) {
+  // 64 KB of stages a CTA, three CTAs an SM
+  if (kv_fp8) return launch_t<T, D, 4, D == 64 ? 4 : 2, true, 2>(a, km, vm, stream);
+  return launch_t<T, D, 4, 2, false, D == 64 ? 2 : 1>(a, km, vm, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_sparse(const DecodeArgs &a, const void *k_cache, const void *v_cache,
+                                 int64_t pool_rows, int head_dim, int dtype, bool kv_fp8,
+                                 cudaStream_t stream, bool *map_failed) {
+  CUtensorMap km, vm;
+  *map_failed = !encode_pool_map(&km, k_cache, pool_rows, head_dim, dtype, kv_fp8) ||
+                !encode_pool_map(&vm, v_cache, pool_rows, head_dim, dtype, kv_fp8);
+  if (*map_failed) return cudaErrorInvalidValue;
+  if (dtype == 0)
+    return head_dim == 128 ? launch_d<__half, 128>(a, kv_fp8, km, vm, stream)
+                           : launch_d<__half, 64>(a, kv_fp8, km, vm, stream);
+  return head_dim == 128 ? launch_d<__nv_bfloat16, 128>(a, kv_fp8, km, vm, stream)
+                         : launch_d<__nv_bfloat16, 64>(a, kv_fp8, km, vm, stream);
+}
+
+}  // namespace pa

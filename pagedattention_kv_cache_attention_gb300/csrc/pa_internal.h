@@ -77,6 +77,9 @@ struct DecodeArgs {
   // CTAs of a cluster that share the keys of an unsplit call over FP4 caches
   int cluster;
   int by_length;  // FP4: CTAs take the longest contexts first (seq_by_length)
+  // pa_decode_sparse: block_tables [B, Hkv, max_blocks_per_seq] and context_lens [B, Hkv]
+  // (read by pa_decode_sparse.cu and pa_decode_fp4.cu)
+  int per_head;
 };
 
 struct ReduceArgs {
@@ -117,6 +120,60 @@ struct Fp4CacheArgs {
   float k_scale, v_scale;
   unsigned *err;
 };
+
+// The rotating writes (pa_rope.cuh).
+struct RopeArgs {
+  void *query_out;
+  const void *query, *key, *value;
+  int64_t query_out_stride, query_stride, key_stride, value_stride;  // elements
+  void *k_cache, *v_cache;
+  const int64_t *slot_mapping, *positions;
+  const float *cos_sin;              // [max_position, rotary_dim]
+  int64_t max_position;
+  int num_tokens, num_q_heads, num_kv_heads, rotary_dim, interleaved, bs_log2;
+  int64_t num_blocks;
+  float k_scale, v_scale;            // FP8 and FP4 caches
+  int group_log2;                    // threads that share a token, in rope_token_heads
+  unsigned *err;
+};
+
+// Threads (a power of two, at most a CTA of 256) that share a token with `items`
+// items of 16 elements, so that a thread has at most four of them where it can.
+inline int rope_group_log2(int items) {
+  int g = 5;
+  while (g < 8 && (items >> (g + 2)) > 0) ++g;
+  return g;
+}
+
+// The bounds of a block's keys (pa_sparse.cu).
+struct BoundsArgs {
+  int8_t *bounds;               // [num_blocks, Hkv, 2, D]: largest, smallest
+  float *bound_scales;          // [num_blocks, Hkv]
+  const void *k_cache;
+  const int32_t *block_tables, *context_lens;
+  const int32_t *query_start;   // [B + 1], or nullptr: one new token a sequence
+  int max_blocks_per_seq, num_seqs, num_kv_heads, bs_log2, max_q_len;
+  int64_t num_blocks;
+  unsigned *err;
+};
+
+struct SelectArgs {
+  int32_t *tables;              // [rows, Hkv, num_selected]
+  int32_t *lens;                // [rows, Hkv]
+  const void *query;            // [rows, Hq, D]
+  const int8_t *bounds;
+  const float *bound_scales;
+  const int32_t *block_tables, *context_lens;
+  const int32_t *query_start;   // [B + 1], or nullptr: row i is sequence i
+  int max_blocks_per_seq, num_seqs, max_q_len, num_q_heads, num_kv_heads, group, bs_log2;
+  int64_t num_blocks;
+  int max_context_len, num_selected, num_sink, num_recent;
+  int cluster;                  // CTAs that share a row's blocks
+  int max_candidates;           // blocks of the longest context
+  unsigned *err;
+};
+// Blocks of one sequence that a selection can choose from: their keys lie in shared memory.
+constexpr int64_t kMaxCandidates = 49152;
 
 struct PrefillArgs {
   void *out;                    // [total_q, Hq, D]
@@ -200,6 +257,10 @@ cudaError_t launch_decode(const DecodeArgs &a, const void *k_cache, const void *
                           cudaStream_t stream, bool *map_failed);
 cudaError_t launch_decode_fp4(const DecodeArgs &a, const void *k_cache, const void *v_cache,
                               int head_dim, int dtype, cudaStream_t stream, bool *map_failed);
+// pa_decode_sparse over 16-bit and FP8 caches (launch_decode_fp4 takes a.per_head itself).
+cudaError_t launch_decode_sparse(const DecodeArgs &a, const void *k_cache, const void *v_cache,
+                                 int64_t pool_rows, int head_dim, int dtype, bool kv_fp8,
+                                 cudaStream_t stream, bool *map_failed);
 // pa_prefill_fp4 on two 128-row tiles a CTA: chunks of more than 64 rows, or of
 // fewer where there are few of them (maps of whole tiles, not swizzled).
 cudaError_t launch_prefill_fp4(const PrefillArgs &a, const CUtensorMap &km, const CUtensorMap &vm,
@@ -223,6 +284,12 @@ cudaError_t launch_shared_prefix(const DecodeArgs &a, const void *k_cache, const
 // Sequences of one group that a shared-prefix CTA serves at query group size G.
 int shared_prefix_members_per_cta(int group);
 cudaError_t launch_reshape(const ReshapeArgs &a, cudaStream_t stream);
+cudaError_t launch_rope(const RopeArgs &a, int head_dim, int dtype, bool to_fp8,
+                        cudaStream_t stream);
+cudaError_t launch_rope_fp4(const RopeArgs &a, int head_dim, int dtype, cudaStream_t stream);
+cudaError_t launch_key_bounds(const BoundsArgs &a, int head_dim, int dtype, Kv kv,
+                              cudaStream_t stream);
+cudaError_t launch_select(const SelectArgs &a, int head_dim, int dtype, cudaStream_t stream);
 cudaError_t launch_cache_fp4_write(const Fp4CacheArgs &a, int dtype, cudaStream_t stream);
 cudaError_t launch_cache_fp4_read(const Fp4CacheArgs &a, int dtype, cudaStream_t stream);
 cudaError_t launch_block_copy(const BlockCopyArgs &a, int num_tensors, cudaStream_t stream);
