@@ -236,8 +236,6 @@ cudaError_t launch_bounds_kv(const BoundsArgs &a, Kv kv, cudaStream_t stream) {
 
 // ---------------------------------------------------------------- selection
 
-constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048, kBinBits = 11;
 constexpr uint32_t kForced = 0xffffffffu;  // above the key of every score
 
 // An unsigned key in the order of the floats (no NaN).
@@ -246,53 +244,361 @@ __device__ __forceinline__ uint32_t key_of(float x) {
   return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-__device__ __forceinline__ int dp2a_lo(uint32_t a, uint32_t b, int c) {
-  return __dp2a_lo(static_cast<int>(a), static_cast<int>(b), c);
-}
-__device__ __forceinline__ int dp2a_hi(uint32_t a, uint32_t b, int c) {
-  return __dp2a_hi(static_cast<int>(a), static_cast<int>(b), c);
-}
-
 __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// Shared memory of a CTA, after the keys [max_candidates].
+// A sequence's rows and the tokens that they see.
+struct SelectRows {
+  int64_t row0;  // its first row
+  int rows;      // how many
+  int base;      // tokens that row t sees, less t
+  // false if there is nothing to do for the sequence (a bad length is flagged by
+  // one thread of the grid)
+  __device__ __forceinline__ bool load(const SelectArgs &a, int seq, bool tell) {
+    const int ctx = a.context_lens[seq];
+    const bool fine = ctx >= 0 && ctx <= a.max_context_len &&
+                      ctx <= static_cast<int64_t>(a.max_blocks_per_seq) << a.bs_log2;
+    if (!a.query_start) {
+      if (!fine && tell) atomicOr(a.err, kErrBadLen);
+      row0 = seq;
+      rows = 1;
+      base = fine ? ctx : 0;
+      return true;
+    }
+    const int q0 = a.query_start[seq], q_len = a.query_start[seq + 1] - q0;
+    row0 = q0;
+    rows = q_len;
+    base = ctx - q_len + 1;
+    if (fine && q_len >= 0 && q_len <= ctx && q_len <= a.max_q_len) return true;
+    if (tell) atomicOr(a.err, kErrBadLen);
+    return false;
+  }
+};
+
+// I of 16 blocks and up to 4 rows is a product on the tensor cores: the blocks'
+// codes as fp16 integers times 2^-24 (a byte in the low bits of a half is that
+// subnormal number; with 128 added codes are unsigned), the weights P and N of a
+// row as two columns, their low bytes (0 to 255) and high ones (-128 to 127).  A
+// column's sum is below 255 * 255 * 256 < 2^24 units of 2^-24, so fp32 holds every
+// partial sum exactly.  I = low + 256 high - 128 (sum of the weights).
+// (By integer dot products a row takes 64 of them for 16 blocks, at half rate, and
+// sums over lanes; the codes' three instructions for 4 of them here are shared by
+// the rows.  5 drafted tokens of 64 sequences, contexts of 512 to 4,096, 32 / 8
+// heads: PLACE_DRAFT.)
+//
+// The order of the 2 D codes in the product is one that lets a lane take 16
+// consecutive codes of a block: code 64 i + 16 c + 4 w + e is column c's e-th of
+// step 4 i + w.
+template <int D> struct Weights {
+  static constexpr int kSteps = 2 * D / 16;
+  uint2 frag[kSteps][32];  // the B operand of a step in each lane: columns 2 r, 2 r + 1 are row r's
+  int bias[4];             // 128 times the sum of a row's weights
+
+  // Row r of the tile, from the row's group of queries; nullptr: zeros.  For a
+  // whole warp; a lane takes D / 32 channels of all heads.
+  template <typename T>
+  __device__ __forceinline__ void put(const T *q, int group, int r, int lane) {
+    constexpr int kPer = D / 32;
+    int p[kPer], m[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) p[i] = m[i] = 0;
+    if (q) {
+      float x[8][kPer];
+      uint32_t top = 0;  // magnitudes are ordered like their bits; a NaN is above infinity
+#pragma unroll
+      for (int h = 0; h < 8; ++h) {
+        if (h >= group) break;
+#pragma unroll
+        for (int i = 0; i < kPer; i += 2) {
+          const float2 v = Elem<T>::unpack(
+              *reinterpret_cast<const uint32_t *>(q + h * D + lane * kPer + i));
+          x[h][i] = v.x;
+          x[h][i + 1] = v.y;
+          top = max(top, max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y))));
+        }
+      }
+      top = __reduce_max_sync(kAll, top);
+      if (top > 0 && top < 0x7f800000u) {
+        const float inv = pow2(-exponent_for(__uint_as_float(top), 12));
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+          if (h >= group) break;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int c = __float2int_rn(x[h][i] * inv);
+            p[i] += max(c, 0);
+            m[i] += min(c, 0);
+            sum += c;
+          }
+        }
+      }
+    }
+    sum = __reduce_add_sync(kAll, sum);
+    if (lane == 0) bias[r] = 128 * sum;
+    // kPer consecutive codes are part of one lane's four of a step
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int code = n * D + lane * kPer;
+      const int step = code / 64 * 4 + code % 16 / 4, c = code % 64 / 16;
+#pragma unroll
+      for (int high = 0; high < 2; ++high) {
+        uint32_t h[kPer / 2];
+#pragma unroll
+        for (int i = 0; i < kPer; i += 2) {
+          const int a = n ? m[i] : p[i], b = n ? m[i + 1] : p[i + 1];
+          h[i / 2] = high ? Elem<__half>::pack(static_cast<float>(a >> 8), static_cast<float>(b >> 8))
+                          : Elem<__half>::pack(static_cast<float>(a & 255), static_cast<float>(b & 255));
+        }
+        uint32_t *dst = reinterpret_cast<uint32_t *>(&frag[step][(2 * r + high) * 4 + c]) +
+                        code % 4 / 2;
+#pragma unroll
+        for (int i = 0; i < kPer / 2; ++i) dst[i] = h[i];
+      }
+    }
+  }
+};
+
+// 16 blocks of a row's table, in one warp: lane (g, c) holds codes 64 i + 16 c ..
+// of blocks g and g + 8, and their scales.
+template <int D> struct Unit {
+  static constexpr int kBlocks = 16;
+  static constexpr int kLoads = 2 * D / 64;
+  uint4 x[2][kLoads];
+  float scale[2];
+  bool ok[2];
+
+  // phys: blocks g and g + 8, -1 for none
+  __device__ __forceinline__ void load(const SelectArgs &a, int kvh, const int (&phys)[2], int c) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      ok[b] = phys[b] >= 0;
+      const int64_t cell = static_cast<int64_t>(phys[b]) * a.num_kv_heads + kvh;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        x[b][i] = make_uint4(0, 0, 0, 0);
+        if (ok[b])
+          x[b][i] = *reinterpret_cast<const uint4 *>(a.bounds + cell * (2 * D) + 64 * i + 16 * c);
+      }
+      scale[b] = ok[b] ? a.bound_scales[cell] : 0.f;
+    }
+  }
+  // The keys of blocks g and g + 8 for rows c of kTiles tiles.
+  template <int kTiles>
+  __device__ __forceinline__ void keys(const Weights<D> *w, int lane, uint32_t (&key)[kTiles][2]) const {
+    float acc[kTiles][4];
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+#pragma unroll
+    for (int s = 0; s < Weights<D>::kSteps; ++s) {
+      const uint32_t u0 = word_of(x[0][s / 4], s % 4) ^ 0x80808080u;
+      const uint32_t u1 = word_of(x[1][s / 4], s % 4) ^ 0x80808080u;
+      const uint32_t a0 = __byte_perm(u0, 0, 0x4140), a2 = __byte_perm(u0, 0, 0x4342);
+      const uint32_t a1 = __byte_perm(u1, 0, 0x4140), a3 = __byte_perm(u1, 0, 0x4342);
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n) {
+        const uint2 f = w[n].frag[s][lane];
+        Elem<__half>::mma(acc[n], a0, a1, a2, a3, f.x, f.y);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) {
+      const int bias = w[n].bias[lane & 3];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int total = __float2int_rn(acc[n][2 * b] * 0x1p24f) +
+                          256 * __float2int_rn(acc[n][2 * b + 1] * 0x1p24f) - bias;
+        key[n][b] = 0;
+        if (ok[b])
+          key[n][b] = key_of(scale[b] < INFINITY ? __fmul_rn(__int2float_rn(total), scale[b]) : INFINITY);
+      }
+    }
+  }
+};
+
+// Block j of a sequence's table, -1 (and flagged) if it is none.
+__device__ __forceinline__ int block_of(const SelectArgs &a, const int32_t *bt_row, int j, int n) {
+  const int phys = j < n ? bt_row[j] : -1;
+  if (phys >= 0 && phys < a.num_blocks) return phys;
+  if (j < n) atomicOr(a.err, kErrBadBlock);
+  return -1;
+}
+
+// Short contexts: at most 32 KPL blocks.  A CTA takes up to 4 TILES rows of a
+// sequence and one KV head: its warps score 16 blocks at a time for all rows, so
+// that bounds are read once for them; then a warp a row picks, with the row's keys
+// in registers and no barrier.
+// The keys of a row (key i * 32 + lane of n in k[i]; 0 past n): calls take(i, place)
+// in the lanes of the `want` largest, ties to the first; want <= n.
+template <int KPL, typename F>
+__device__ __forceinline__ void pick(const uint32_t (&k)[KPL], int n, int want, int lane, F &&take) {
+  uint32_t lo = 0xffffffffu, hi = 0;
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) {
+    if (i * 32 + lane < n) {
+      lo = min(lo, k[i]);
+      hi = max(hi, k[i]);
+    }
+  }
+  lo = __reduce_min_sync(kAll, lo);
+  hi = __reduce_max_sync(kAll, hi);
+  // the largest t with at least `want` keys >= t, a bit at a time from the first
+  // in which keys differ; done early where they are just `want`
+  uint32_t t = lo;
+  int count = n;
+  if (lo != hi && count != want) {
+    const int top = 31 - __clz(lo ^ hi);
+    t = hi & ~((2u << top) - 1);
+    for (int bit = top; bit >= 0; --bit) {
+      const uint32_t c = t | (1u << bit);
+      int here = 0;
+#pragma unroll
+      for (int i = 0; i < KPL; ++i) here += k[i] >= c ? 1 : 0;
+      here = __reduce_add_sync(kAll, here);
+      if (here >= want) {
+        t = c;
+        count = here;
+        if (here == want) break;
+      }
+    }
+  }
+  // keys above t are taken, and of those equal to it (the count has count - want
+  // too many) the first
+  int equal = 0;
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) equal += i * 32 + lane < n && k[i] == t ? 1 : 0;
+  equal = __reduce_add_sync(kAll, equal);
+  int left = equal - (count - want), place = 0;
+  const uint32_t below = (1u << lane) - 1;
+#pragma unroll
+  for (int i = 0; i < KPL; ++i) {
+    if (i * 32 >= n) break;
+    const bool in = i * 32 + lane < n;
+    const uint32_t eqs = __ballot_sync(kAll, in && k[i] == t);
+    const bool mine = in && (k[i] > t || (k[i] == t && __popc(eqs & below) < left));
+    const uint32_t all = __ballot_sync(kAll, mine);
+    if (mine) take(i, place + __popc(all & below));
+    place += __popc(all);
+    left -= __popc(eqs);
+  }
+}
+
+template <typename T, int D, int KPL, int TILES, int NW>
+__global__ void __launch_bounds__(NW * 32) select_short_kernel(const SelectArgs a) {
+  using U = Unit<D>;
+  constexpr int kRows = 4 * TILES;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Weights<D> *weights = reinterpret_cast<Weights<D> *>(smem_raw);
+  uint32_t *keys = reinterpret_cast<uint32_t *>(smem_raw + TILES * sizeof(Weights<D>));  // [rows][stride]
+  const int stride = a.max_candidates;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int kvh = blockIdx.y, seq = blockIdx.z;
+  const int bs = 1 << a.bs_log2, K = a.num_selected;
+  grid_dependency_wait();  // queries, bounds and lengths may come from the kernel before
+  grid_launch_dependents();
+  const int32_t *bt_row = a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq;
+  SelectRows rows;
+  if (!rows.load(a, seq, tid == 0 && blockIdx.x == 0 && kvh == 0)) return;
+  const int t0 = blockIdx.x * kRows, count = min(kRows, rows.rows - t0);
+  if (count <= 0) return;
+  const int most = (rows.base + t0 + count - 1 + bs - 1) >> a.bs_log2;  // blocks of the last row
+  if (most > K) {
+    for (int r = warp; r < kRows; r += NW)
+      weights[r / 4].put(r < count ? static_cast<const T *>(a.query) +
+                                         ((rows.row0 + t0 + r) * a.num_q_heads + kvh * a.group) * D
+                                   : nullptr,
+                         a.group, r % 4, lane);
+    __syncthreads();
+    for (int j0 = warp * U::kBlocks; j0 < most; j0 += NW * U::kBlocks) {
+      const int phys[2] = {block_of(a, bt_row, j0 + g, most), block_of(a, bt_row, j0 + 8 + g, most)};
+      U unit;
+      unit.load(a, kvh, phys, c);
+      uint32_t key[TILES][2];
+      unit.template keys<TILES>(weights, lane, key);
+#pragma unroll
+      for (int n = 0; n < TILES; ++n)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          if (4 * n + c < count && j0 + 8 * b + g < most)
+            keys[(4 * n + c) * stride + j0 + 8 * b + g] = key[n][b];
+    }
+    __syncthreads();
+  }
+  for (int r = warp; r < count; r += NW) {
+    const int seen = rows.base + t0 + r, n = (seen + bs - 1) >> a.bs_log2;
+    const int64_t at = (rows.row0 + t0 + r) * a.num_kv_heads + kvh;
+    int32_t *out = a.tables + at * K;
+    if (n <= K) {  // all of them
+      for (int i = lane; i < K; i += 32) out[i] = i < n ? bt_row[i] : -1;
+      if (lane == 0) a.lens[at] = seen;
+      continue;
+    }
+    uint32_t k[KPL];
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) {
+      const int j = i * 32 + lane;
+      k[i] = j < n ? keys[r * stride + j] : 0;
+      if (j < n && (j < a.num_sink || j >= n - a.num_recent)) k[i] = kForced;
+    }
+    bool last = false;
+    pick<KPL>(k, n, K, lane, [&](int i, int place) {
+      out[place] = bt_row[i * 32 + lane];
+      last = last || i * 32 + lane == n - 1;
+    });
+    const bool any = __any_sync(kAll, last);
+    if (lane == 0) a.lens[at] = K * bs - (any ? n * bs - seen : 0);
+  }
+}
+
+// Long contexts: the CTAs of a cluster score a share of a row's blocks each, into
+// the keys of the first one, which then picks.  A thread of that one takes runs of
+// 32 keys; a word between two runs puts the lanes' keys into different banks.
+constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048, kBinBits = 11;
+__host__ __device__ constexpr int64_t key_place(int64_t j) { return j + (j >> 5); }
+
+// Shared memory of a CTA, after the keys.
 template <int D> struct SelectShared {
+  Weights<D> weights;
   uint32_t bins[kBins];
-  int16_t w[2][D];              // P, N
-  uint16_t q[8][D];             // the group's queries
   uint32_t part[3][kSelWarps];
   uint32_t chosen_bin, chosen_above, chosen_count;
 };
-
-// Sum over lanes of a warp of R values held by R lanes each ... in a butterfly
-// that halves the values as it goes: lane r of a group of R ends with the sum of
-// v[r] over its group.
-template <int R> __device__ __forceinline__ int transpose_sum(int (&v)[R], int lane) {
-#pragma unroll
-  for (int half = R / 2; half > 0; half >>= 1) {
-    const bool up = lane & half;
-#pragma unroll
-    for (int i = 0; i < half; ++i) {
-      const int keep = up ? v[i + half] : v[i], give = up ? v[i] : v[i + half];
-      v[i] = keep + __shfl_xor_sync(kAll, give, half);
-    }
-  }
-  return v[0];
+__host__ __device__ constexpr size_t key_bytes(int64_t n) {
+  return (static_cast<size_t>(key_place(n)) * 4 + 15) & ~static_cast<size_t>(15);
 }
 
-// The cluster's CTAs score a share of the row's blocks each, into the keys of the
-// first one, which then picks and writes.
+// Sum over the CTA's threads before this one; `all`: over all of them.
+__device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t *part, uint32_t &all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t incl = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t x = __shfl_up_sync(kAll, incl, off);
+    if (lane >= off) incl += x;
+  }
+  if (lane == 31) part[warp] = incl;
+  __syncthreads();
+  uint32_t before = 0;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) {
+    const uint32_t x = part[w];
+    before += w < warp ? x : 0;
+    all += x;
+  }
+  return before + incl - v;
+}
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a) {
-  constexpr int kLanes = 2 * D / 16;      // lanes that hold a block's bounds, 16 codes each
-  constexpr int kSteps = kLanes;          // blocks of a warp's window of 32 that a lane sees
+__global__ void __launch_bounds__(kSelThreads, 2) select_long_kernel(const SelectArgs a) {
+  using U = Unit<D>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   uint32_t *keys = reinterpret_cast<uint32_t *>(smem_raw);
-  SelectShared<D> &sh = *reinterpret_cast<SelectShared<D> *>(
-      smem_raw + ((static_cast<size_t>(a.max_candidates) * 4 + 15) & ~static_cast<size_t>(15)));
+  SelectShared<D> &sh = *reinterpret_cast<SelectShared<D> *>(smem_raw + key_bytes(a.max_candidates));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, c = lane & 3;
   const int cluster = a.cluster, rank = static_cast<int>(blockIdx.x) % cluster;
   const int t = static_cast<int>(blockIdx.x) / cluster;  // row of the sequence's chunk
   const int kvh = blockIdx.y, seq = blockIdx.z;
@@ -300,25 +606,22 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
   grid_dependency_wait();  // queries, bounds and lengths may come from the kernel before
   grid_launch_dependents();
 
-  // the row, and the tokens that it sees
-  const int ctx = a.context_lens[seq];
-  int64_t row = seq;
-  int seen = ctx;
-  bool fine = ctx >= 0 && ctx <= a.max_context_len &&
-              ctx <= static_cast<int64_t>(a.max_blocks_per_seq) << a.bs_log2;
-  if (a.query_start) {
-    const int q0 = a.query_start[seq], q_len = a.query_start[seq + 1] - q0;
-    fine = fine && q_len >= 0 && q_len <= ctx && q_len <= a.max_q_len;
-    if (!fine && tid == 0 && blockIdx.x == 0 && kvh == 0) atomicOr(a.err, kErrBadLen);
-    if (!fine || t >= q_len) return;  // (the whole cluster)
-    row = q0 + t;
-    seen = ctx - q_len + t + 1;
-  } else if (!fine) {
-    if (tid == 0 && blockIdx.x == 0 && kvh == 0) atomicOr(a.err, kErrBadLen);
-    seen = 0;
-  }
-  const int n = (seen + bs - 1) >> a.bs_log2;
+  // the warp's first units' blocks, read before the length is known
   const int32_t *bt_row = a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq;
+  const int step = cluster * kSelWarps * U::kBlocks;
+  int j0 = (rank * kSelWarps + warp) * U::kBlocks;
+  auto entries = [&](int j, int (&e)[2]) {
+    e[0] = j + g < a.max_blocks_per_seq ? bt_row[j + g] : -1;
+    e[1] = j + 8 + g < a.max_blocks_per_seq ? bt_row[j + 8 + g] : -1;
+  };
+  int ahead[2][2];
+  entries(j0, ahead[0]);
+  entries(j0 + step, ahead[1]);
+  SelectRows rows;
+  if (!rows.load(a, seq, tid == 0 && blockIdx.x == 0 && kvh == 0) || t >= rows.rows)
+    return;  // (the whole cluster)
+  const int64_t row = rows.row0 + t;
+  const int seen = rows.base + t, n = (seen + bs - 1) >> a.bs_log2;
   int32_t *out = a.tables + (row * a.num_kv_heads + kvh) * K;
   int32_t *out_len = a.lens + row * a.num_kv_heads + kvh;
   if (n <= K) {  // all of them
@@ -328,118 +631,76 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
     }
     return;  // (the whole cluster)
   }
-
-  // the group's queries as integers, and their sums by sign
-  const int G = a.group;
-  const T *q = static_cast<const T *>(a.query) + (row * a.num_q_heads + kvh * G) * D;
-  {
-    float top = 0.f;
-    for (int i = tid; i < G * (D / 8); i += kSelThreads) {
-      const uint4 x = reinterpret_cast<const uint4 *>(q)[i];
-      *reinterpret_cast<uint4 *>(&sh.q[0][0] + i * 8) = x;
+  // units in turn, the loads of the next one under way while one is worked on
+  auto fetch = [&](U &u, int j, const int (&e)[2]) {
+    int phys[2];
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float2 v = Elem<T>::unpack(word_of(x, w));
-        // (a NaN becomes an infinity: both are left out)
-        const float m0 = fabsf(v.x), m1 = fabsf(v.y);
-        top = fmaxf(top, fmaxf(m0 == m0 ? m0 : INFINITY, m1 == m1 ? m1 : INFINITY));
-      }
+    for (int b = 0; b < 2; ++b) {
+      const bool in = j + 8 * b + g < n, good = e[b] >= 0 && e[b] < a.num_blocks;
+      if (in && !good) atomicOr(a.err, kErrBadBlock);
+      phys[b] = in && good ? e[b] : -1;
     }
-    // (magnitudes are ordered like their bits)
-    const uint32_t most = __reduce_max_sync(kAll, __float_as_uint(top));
-    if (lane == 0) sh.part[0][warp] = most;
-    __syncthreads();
-    uint32_t all = 0;
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) all = max(all, sh.part[0][w]);
-    top = __uint_as_float(all);
-    if (tid < D) {
-      int p = 0, m = 0;
-      if (top > 0.f && top < INFINITY) {
-        const float inv = pow2(-exponent_for(top, 12));
-        for (int h = 0; h < G; ++h) {
-          const uint16_t b = sh.q[h][tid];
-          const float x = Elem<T>::unpack(b).x;
-          const int c = __float2int_rn(x * inv);
-          p += max(c, 0);
-          m += min(c, 0);
-        }
-      }
-      sh.w[0][tid] = static_cast<int16_t>(p);
-      sh.w[1][tid] = static_cast<int16_t>(m);
-    }
-    __syncthreads();
-  }
-  uint32_t w[8];  // the 16 sums that the lane's codes meet
-  {
-    const uint4 *src = reinterpret_cast<const uint4 *>(&sh.w[0][0] + (lane % kLanes) * 16);
-    const uint4 x = src[0], y = src[1];
-    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-    w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
-  }
-
-  if (cluster > 1) cluster_sync();  // the first CTA has started: its shared memory is there
+    u.load(a, kvh, phys, c);
+  };
+  U u[2];
+  fetch(u[0], j0, ahead[0]);
+  if (warp < 4)
+    sh.weights.put(warp == 0 ? static_cast<const T *>(a.query) +
+                                   (row * a.num_q_heads + kvh * a.group) * D
+                             : nullptr,
+                   a.group, warp, lane);
+  // the first CTA of the cluster has started: its shared memory is there
+  if (cluster > 1) cluster_sync(); else __syncthreads();
   const uint32_t keys_at = cluster > 1 ? cluster_addr(keys, 0) : 0;
-  // windows of 32 blocks, one warp's each: lane l ends with the score of block l
-  for (int j0 = (rank * kSelWarps + warp) * 32; j0 < n; j0 += cluster * kSelWarps * 32) {
-    const int j = j0 + lane;
-    int phys = j < n ? bt_row[j] : -1;
-    if (phys >= a.num_blocks || phys < 0) {
-      if (j < n) atomicOr(a.err, kErrBadBlock);
-      phys = -1;
-    }
-    const int64_t mine = static_cast<int64_t>(phys) * a.num_kv_heads + kvh;
-    const float scale = phys >= 0 ? a.bound_scales[mine] : 0.f;
-    uint4 x[kSteps];
+  auto score = [&](const U &unit, int j) {
+    uint32_t key[1][2];
+    unit.template keys<1>(&sh.weights, lane, key);
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int p = __shfl_sync(kAll, phys, (lane / kLanes) * kSteps + i);
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (p >= 0)
-        x[i] = *reinterpret_cast<const uint4 *>(
-            a.bounds + (static_cast<int64_t>(p) * a.num_kv_heads + kvh) * (2 * D) + (lane % kLanes) * 16);
+    for (int b = 0; b < 2; ++b) {
+      const int at = j + 8 * b + g;
+      if (c == 0 && at < n) {
+        const uint32_t k = at < a.num_sink || at >= n - a.num_recent ? kForced : key[0][b];
+        if (cluster > 1)
+          st_cluster_u32(keys_at + static_cast<uint32_t>(key_place(at)) * 4, k);
+        else
+          keys[key_place(at)] = k;
+      }
     }
-    int v[kSteps];
+  };
+  while (j0 < n) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      int s = dp2a_lo(w[0], x[i].x, 0);
-      s = dp2a_hi(w[1], x[i].x, s);
-      s = dp2a_lo(w[2], x[i].y, s);
-      s = dp2a_hi(w[3], x[i].y, s);
-      s = dp2a_lo(w[4], x[i].z, s);
-      s = dp2a_hi(w[5], x[i].z, s);
-      s = dp2a_lo(w[6], x[i].w, s);
-      v[i] = dp2a_hi(w[7], x[i].w, s);
-    }
-    const int total = transpose_sum<kSteps>(v, lane % kLanes);
-    uint32_t key = 0;
-    if (phys >= 0)
-      key = key_of(scale < INFINITY ? __fmul_rn(__int2float_rn(total), scale) : INFINITY);
-    if (j < a.num_sink || j >= n - a.num_recent) key = kForced;
-    if (j < n) {
-      if (cluster > 1)
-        st_cluster_u32(keys_at + j * 4, key);
-      else
-        keys[j] = key;
+    for (int s = 0; s < 2; ++s) {
+      if (j0 >= n) break;
+      // (entries of the unit after the next one: read now, used a turn later)
+      if (j0 + step < n) fetch(u[s ^ 1], j0 + step, ahead[s ^ 1]);
+      if (j0 + 2 * step < n) entries(j0 + 2 * step, ahead[s]);
+      score(u[s], j0);
+      j0 += step;
     }
   }
   if (cluster > 1) cluster_sync(); else __syncthreads();
   if (rank != 0) return;
 
+  // f(key, j) for the keys of run r
+  auto run = [&](int r, auto &&f) {
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i)
+      if (r * 32 + i < n) f(keys[r * 33 + i], i);
+  };
   // The K-th largest key: the range [lo, hi] that holds it is cut into kBins
   // equal parts, their keys counted, and the part that holds it taken, until
   // what is left of the range is taken whole or is one value.
   uint32_t lo = 0xffffffffu, hi = 0;
   int forced = 0;
-  for (int i = tid; i < n; i += kSelThreads) {
-    const uint32_t k = keys[i];
-    if (k == kForced) {
-      ++forced;
-    } else {
-      lo = min(lo, k);
-      hi = max(hi, k);
-    }
-  }
+  for (int r = tid; r * 32 < n; r += kSelThreads)
+    run(r, [&](uint32_t k, int) {
+      if (k == kForced) {
+        ++forced;
+      } else {
+        lo = min(lo, k);
+        hi = max(hi, k);
+      }
+    });
   lo = __reduce_min_sync(kAll, lo);
   hi = __reduce_max_sync(kAll, hi);
   forced = __reduce_add_sync(kAll, forced);
@@ -460,30 +721,21 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
     __syncthreads();
     for (int i = tid; i < kBins; i += kSelThreads) sh.bins[i] = 0;
     __syncthreads();
-    for (int i = tid; i < n; i += kSelThreads) {
-      const uint32_t k = keys[i];
-      if (k >= lo && k <= hi) atomicAdd(&sh.bins[(k - lo) >> shift], 1u);
-    }
+    for (int r = tid; r * 32 < n; r += kSelThreads)
+      run(r, [&](uint32_t k, int) {
+        if (k >= lo && k <= hi) atomicAdd(&sh.bins[(k - lo) >> shift], 1u);
+      });
     __syncthreads();
     // the part with the need-th largest key: sums over the parts from the top;
     // thread i holds 8 parts, from part kBins - 1 - 8 i down
     constexpr int kPer = kBins / kSelThreads;
-    uint32_t mine[kPer], sum = 0;
+    uint32_t mine[kPer], sum = 0, all;
 #pragma unroll
     for (int b = 0; b < kPer; ++b) {
       mine[b] = sh.bins[kBins - 1 - tid * kPer - b];
       sum += mine[b];
     }
-    uint32_t before = sum;  // inclusive over the lanes
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t x = __shfl_up_sync(kAll, before, off);
-      if (lane >= off) before += x;
-    }
-    if (lane == 31) sh.part[0][warp] = before;
-    __syncthreads();
-    before -= sum;
-    for (int i = 0; i < warp; ++i) before += sh.part[0][i];
+    uint32_t before = sum_before(sum, sh.part[0], all);
 #pragma unroll
     for (int b = 0; b < kPer; ++b) {
       if (before < static_cast<uint32_t>(need) && before + mine[b] >= static_cast<uint32_t>(need)) {
@@ -499,53 +751,47 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs a)
     lo += sh.chosen_bin << shift;
     hi = min(hi, lo + ((1u << shift) - 1));
   }
-  // keys above hi are taken, those of [lo, hi] too if `whole`; otherwise they
-  // are one value, and the first `need` of them are.  A warp takes a run of
-  // the blocks, so that places and ties follow the blocks' order.
-  const int per = ((n + kSelThreads - 1) / kSelThreads) * 32;  // blocks of a warp
-  const int begin = min(warp * per, n), end = min(begin + per, n);
-  int above = 0, equal = 0;
-  for (int i0 = begin; i0 < end; i0 += 32) {
-    const uint32_t k = i0 + lane < end ? keys[i0 + lane] : 0;
-    const bool in = i0 + lane < end;
-    above += __popc(__ballot_sync(kAll, in && (whole ? k >= lo : k > lo)));
-    equal += __popc(__ballot_sync(kAll, in && !whole && k == lo));
-  }
-  __syncthreads();
-  if (lane == 0) sh.part[0][warp] = above, sh.part[1][warp] = equal;
-  __syncthreads();
-  int place = 0, ties = 0;  // taken, and equal ones, before this warp's blocks
-  for (int i = 0; i < warp; ++i) {
-    place += sh.part[0][i] + min(static_cast<int>(sh.part[1][i]), max(0, need - ties));
-    ties += sh.part[1][i];
-  }
-  bool last = false;
-  for (int i0 = begin; i0 < end; i0 += 32) {
-    const int j = i0 + lane;
-    const bool in = j < end;
-    const uint32_t k = in ? keys[j] : 0;
-    const bool eq = in && !whole && k == lo;
-    const uint32_t eqs = __ballot_sync(kAll, eq);
-    const int tie = ties + __popc(eqs & ((1u << lane) - 1));
-    const bool take = in && ((whole ? k >= lo : k > lo) || (eq && tie < need));
-    const uint32_t takes = __ballot_sync(kAll, take);
-    if (take) {
-      out[place + __popc(takes & ((1u << lane) - 1))] = bt_row[j];
-      last = last || j == n - 1;
+  // Keys above hi are taken, those of [lo, hi] too if `whole`; otherwise they are
+  // one value, and the first `need` of them are.  Blocks taken are written over
+  // the keys, in order (the place of block j is at most j), and then looked up.
+  int place0 = 0;  // taken before this turn's keys
+  for (int r0 = 0; r0 * 32 < n; r0 += kSelThreads) {
+    uint32_t above = 0, equal = 0;
+    run(r0 + tid, [&](uint32_t k, int i) {
+      above |= (whole ? k >= lo : k > lo) ? 1u << i : 0;
+      equal |= !whole && k == lo ? 1u << i : 0;
+    });
+    uint32_t all;
+    __syncthreads();  // sh.part
+    const uint32_t before = sum_before(__popc(above) | (__popc(equal) << 16), sh.part[0], all);
+    // (every thread has read its keys of this turn, too)
+    const int ties = before >> 16;
+    int place = place0 + static_cast<int>(before & 0xffff) + min(ties, need);
+    int left = max(0, need - ties);
+    uint32_t todo = above | equal;
+    while (todo) {
+      const int i = __ffs(todo) - 1;
+      todo &= todo - 1;
+      if ((equal >> i) & 1u) {
+        if (left == 0) continue;
+        --left;
+      }
+      keys[key_place(place++)] = (r0 + tid) * 32 + i;
     }
-    place += __popc(takes);
-    ties += __popc(eqs);
+    place0 += static_cast<int>(all & 0xffff) + min(static_cast<int>(all >> 16), need);
+    need -= min(static_cast<int>(all >> 16), need);
   }
-  const int any = __syncthreads_or(last ? 1 : 0);
-  if (tid == 0) *out_len = K * bs - (any ? n * bs - seen : 0);
+  __syncthreads();
+  for (int i = tid; i < K; i += kSelThreads) out[i] = bt_row[keys[key_place(i)]];
+  if (tid == 0)
+    *out_len = K * bs - (keys[key_place(K - 1)] == static_cast<uint32_t>(n - 1) ? n * bs - seen : 0);
 }
 
-template <typename T, int D> cudaError_t launch_select_t(SelectArgs a, cudaStream_t stream) {
-  const size_t smem = ((static_cast<size_t>(a.max_candidates) * 4 + 15) & ~static_cast<size_t>(15)) +
-                      sizeof(SelectShared<D>);
-  constexpr size_t most = kMaxCandidates * 4 + sizeof(SelectShared<D>);
+template <typename T, int D> cudaError_t launch_long(SelectArgs a, cudaStream_t stream) {
+  const size_t smem = key_bytes(a.max_candidates) + sizeof(SelectShared<D>);
+  constexpr size_t most = key_bytes(kMaxCandidates) + sizeof(SelectShared<D>);
   static_assert(most <= 227 * 1024, "shared memory");
-  auto kern = select_kernel<T, D>;
+  auto kern = select_long_kernel<T, D>;
   static SmemLimitOnce smem_limit;
   const cudaError_t e = smem_limit.ensure(kern, most);
   if (e != cudaSuccess) return e;
@@ -556,6 +802,28 @@ template <typename T, int D> cudaError_t launch_select_t(SelectArgs a, cudaStrea
   return launch_clusters(a.cluster, kern,
                          dim3(static_cast<unsigned>(a.cluster * a.max_q_len), a.num_kv_heads, a.num_seqs),
                          dim3(kSelThreads), smem, stream, a);
+}
+
+template <typename T, int D, int KPL, int TILES, int NW>
+cudaError_t launch_short(const SelectArgs &a, cudaStream_t stream) {
+  constexpr int kRows = 4 * TILES;
+  const int rows = a.max_q_len < kRows ? a.max_q_len : kRows;
+  constexpr size_t fixed = TILES * sizeof(Weights<D>);
+  const size_t smem = fixed + static_cast<size_t>(rows) * a.max_candidates * 4;
+  static_assert(fixed + static_cast<size_t>(kRows) * 32 * KPL * 4 <= 48 * 1024,
+                "shared memory that needs no leave");
+  const unsigned tiles = (static_cast<unsigned>(a.max_q_len) + kRows - 1) / kRows;
+  return launch_dependent(select_short_kernel<T, D, KPL, TILES, NW>,
+                          dim3(tiles, a.num_kv_heads, a.num_seqs), dim3(NW * 32), smem, stream, a);
+}
+
+template <typename T, int D> cudaError_t launch_select_t(const SelectArgs &a, cudaStream_t stream) {
+  if (a.max_candidates > 1024) return launch_long<T, D>(a, stream);
+  if (a.max_q_len > 4)
+    return a.max_candidates > 256 ? launch_short<T, D, 32, 2, 8>(a, stream)
+                                  : launch_short<T, D, 8, 2, 8>(a, stream);
+  return a.max_candidates > 256 ? launch_short<T, D, 32, 1, 4>(a, stream)
+                                : launch_short<T, D, 8, 1, 4>(a, stream);
 }
 
 }  // namespace

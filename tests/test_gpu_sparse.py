@@ -219,6 +219,33 @@ def test_select_among_few_different_scores(pa, blocks, keep):  # noqa: F811
                 assert n[r, h] == len(got) * 16 - (m * 16 - b.lens[r] if got[-1] == m - 1 else 0)
 
 
+@pytest.mark.parametrize("lens", [[16 * 60] * 4, [16 * 1500] * 4])
+@pytest.mark.parametrize("d", [64, 128])
+def test_select_with_the_largest_sums(pa, lens, d):  # noqa: F811
+    """Codes and weights at the ends of their ranges: 8 heads that add up to the
+    largest weights, weights with full low bytes, codes of 127 and -127, with
+    scores that differ by one."""
+    b = Batch(40, [16 * 3] * 4, 1, 8, d, 16, "fp16", extra=80)
+    b.bounds[:] = np.where(b.rng.random(b.bounds.shape) < 0.9, 127, -127)
+    b.bounds[: b.NB // 2, :, 1] = -127
+    b.bounds[:, :, :, 0] = b.rng.integers(-127, 128, b.bounds[:, :, :, 0].shape)
+    b.scales[:] = 1
+    blocks = -(-lens[0] // 16)
+    b.tables = np.stack([b.rng.permutation(b.NB)[np.arange(blocks) % b.NB] for _ in lens]).astype(np.int32)
+    b.lens = b.seen = np.asarray(lens, np.int32)
+    q = np.zeros((4, 8, d))
+    q[0] = 4095                             # weights of 32760
+    q[1] = np.where(np.arange(d) % 2, 255, -1)  # low bytes of 255, high ones of -1
+    q[1, 0, 3] = 4095
+    q[2], q[2, :4], q[2, 0] = -4095, 4095, 1
+    q[3] = b.rng.integers(-4095, 4096, (8, d))
+    b.q = torch.from_numpy(q).to(torch.float16)
+    for keep in (1, 7, 40):
+        t, n = b.select(pa, keep, 0, 0)
+        wt, wn = b.want(keep, 0, 0)
+        assert np.array_equal(t, wt) and np.array_equal(n, wn)
+
+
 def test_select_with_odd_scores(pa):  # noqa: F811
     """Blocks of infinite scale first (in order), zeros, scores of both signs, queries that are zero or not finite."""
     b = Batch(7, [16 * 60] * 6, 2, 4, 128, 16, "fp16", mean=0.0)
