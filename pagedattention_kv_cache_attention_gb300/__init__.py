@@ -795,65 +795,79 @@ def _sparse_fn(name: str):
     return f
 
 
-def _dense(dev: int, **tensors) -> None:
-    """Each name=(tensor, dtype), contiguous on device ``dev``: one expression for what
-    fits, and the first that does not named."""
-    for t, dtype in tensors.values():
-        try:
-            if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
-                continue
-        except AttributeError:
-            pass
-        _all_fit(dev, **tensors)
-
-
-def _cache_shape(kind: str, cache: torch.Tensor, d: int):
+def _cache_shape(name: str, cache: torch.Tensor, d: int):
     """(num_blocks, num_kv_heads, block_size) of a cache for heads of ``d``."""
     shape = cache.shape
-    if kind == "_fp4":
+    if name.endswith("_fp4"):
         return shape[0], shape[1], fp4_block_size(cache, d)
     if len(shape) != 4 or shape[3] != d:
         raise ValueError(f"a cache is [NB, Hkv, block_size, d = {d}], got {tuple(shape)}")
     return shape[0], shape[1], shape[2]
 
 
-def _rope(kind, query_out, query, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
+def _rows_fit(dtype, dev, **rows) -> None:
+    """Names the first of the row tensors that a rotated append cannot take."""
+    for n, t in rows.items():
+        _cuda(n, t, dtype)
+        if t.dim() != 3:
+            raise ValueError(f"{n} must be [T, heads, d]")
+        st, (_, heads, d) = t.stride(), t.shape
+        if (st[2] != 1 and d > 1) or (st[1] != d and heads > 1):
+            raise ValueError(f"{n}: heads must be contiguous inside a token row")
+
+
+def _rope(name, query_out, query, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
           scales, interleaved, stream):
-    name = "pa_rope_and_cache" + kind
     f = _sparse_fns.get(name) or _sparse_fn(name)
     dev = _device_of("query", query)
     dtype = query.dtype
-    strides = []
-    for n, t in (("query_out", query_out), ("query", query), ("key", key), ("value", value)):
-        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
-            _cuda(n, t, dtype)
-        if t.dim() != 3:
-            raise ValueError(f"{n} must be [T, heads, d]")
-        st, (rows, heads, d) = t.stride(), t.shape
-        if (st[2] != 1 and d > 1) or (st[1] != d and heads > 1):
-            raise ValueError(f"{n}: heads must be contiguous inside a token row")
-        # (the stride of a single row is not looked at)
-        strides.append(st[0] if rows > 1 else heads * d)
-    T, Hq, d = query.shape
-    if query_out.shape != query.shape:
-        raise ValueError("query_out must match query")
-    Hkv = key.shape[1]
-    if key.shape != (T, Hkv, d) or value.shape != key.shape:
-        raise ValueError("key and value must be [T, Hkv, d], with query's T and d")
-    cache = _U8 if kind else dtype
-    _dense(dev, k_cache=(k_cache, cache), v_cache=(v_cache, cache),
-           slot_mapping=(slot_mapping, _I64), positions=(positions, _I64), cos_sin=(cos_sin, _F32))
-    NB, heads, bs = _cache_shape(kind, k_cache, d)
-    if heads != Hkv or v_cache.shape != k_cache.shape:
+    cache = _U8 if scales else dtype
+    try:
+        fit = (query_out.dtype is dtype and key.dtype is dtype and value.dtype is dtype
+               and k_cache.dtype is cache and v_cache.dtype is cache
+               and slot_mapping.dtype is _I64 and positions.dtype is _I64 and cos_sin.dtype is _F32
+               and query_out.get_device() == dev == key.get_device() == value.get_device()
+               and k_cache.get_device() == dev == v_cache.get_device() == cos_sin.get_device()
+               and slot_mapping.get_device() == dev == positions.get_device()
+               and k_cache.is_contiguous() and v_cache.is_contiguous()
+               and slot_mapping.is_contiguous() and positions.is_contiguous()
+               and cos_sin.is_contiguous())
+        shape = query.shape
+        T, Hq, d = shape
+        _, Hkv, _ = kv = key.shape
+        qo, q, k, v = query_out.stride(), query.stride(), key.stride(), value.stride()
+        rows = (query_out.shape == shape and value.shape == kv and kv[0] == T and kv[2] == d
+                and qo[2] == 1 and q[2] == 1 and k[2] == 1 and v[2] == 1
+                and qo[1] == d and q[1] == d and k[1] == d and v[1] == d)
+    except (AttributeError, ValueError, IndexError):
+        fit = rows = False
+    if not (fit and rows):
+        # (a single head may have any stride, and name what does not fit)
+        _rows_fit(dtype, dev, query_out=query_out, query=query, key=key, value=value)
+        _all_fit(dev, k_cache=(k_cache, cache), v_cache=(v_cache, cache),
+                 slot_mapping=(slot_mapping, _I64), positions=(positions, _I64),
+                 cos_sin=(cos_sin, _F32))
+        if query_out.shape != shape:
+            raise ValueError("query_out must match query")
+        if kv[0] != T or kv[2] != d or value.shape != kv:
+            raise ValueError("key and value must be [T, Hkv, d], with query's T and d")
+    caches, table = k_cache.shape, cos_sin.shape
+    NB, heads, bs = _cache_shape(name, k_cache, d)
+    if heads != Hkv or v_cache.shape != caches:
         raise ValueError("key/value/cache shapes disagree")
     if slot_mapping.numel() != T or positions.numel() != T:
         raise ValueError("slot_mapping and positions must have one entry per token")
-    if cos_sin.dim() != 2:
+    if len(table) != 2:
         raise ValueError("cos_sin must be [max_position, rotary_dim]")
-    st = f(query_out.data_ptr(), query.data_ptr(), key.data_ptr(), value.data_ptr(), *strides,
+    if T > 1:
+        qo, q, k, v = qo[0], q[0], k[0], v[0]
+    else:  # the stride of a single row is not looked at
+        qo = q = Hq * d
+        k = v = Hkv * d
+    st = f(query_out.data_ptr(), query.data_ptr(), key.data_ptr(), value.data_ptr(), qo, q, k, v,
            k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
-           cos_sin.data_ptr(), T, Hq, Hkv, d, cos_sin.shape[1], 1 if interleaved else 0, bs, NB,
-           cos_sin.shape[0], _dtype_code(query), *scales,
+           cos_sin.data_ptr(), T, Hq, Hkv, d, table[1], 1 if interleaved else 0, bs, NB, table[0],
+           _dtype_code(query), *scales,
            _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise PaError(name, st)
@@ -868,8 +882,8 @@ def pa_rope_and_cache(query_out: torch.Tensor, query: torch.Tensor, key: torch.T
     the table cos_sin (new_rope_table); write the queries into ``query_out``
     (which may be ``query``), and keys and values into the caches at
     slot_mapping[t] (int64; a token with a negative slot is left out)."""
-    return _rope("", query_out, query, key, value, k_cache, v_cache, slot_mapping, positions,
-                 cos_sin, (), interleaved, stream)
+    return _rope("pa_rope_and_cache", query_out, query, key, value, k_cache, v_cache,
+                 slot_mapping, positions, cos_sin, (), interleaved, stream)
 
 
 def pa_rope_and_cache_fp8(query_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
@@ -878,8 +892,9 @@ def pa_rope_and_cache_fp8(query_out: torch.Tensor, query: torch.Tensor, key: tor
                           cos_sin: torch.Tensor, k_scale: float, v_scale: float,
                           interleaved: bool = False, stream=None) -> torch.Tensor:
     """pa_rope_and_cache into uint8 FP8 E4M3 caches."""
-    return _rope("_fp8", query_out, query, key, value, k_cache, v_cache, slot_mapping, positions,
-                 cos_sin, (float(k_scale), float(v_scale)), interleaved, stream)
+    return _rope("pa_rope_and_cache_fp8", query_out, query, key, value, k_cache, v_cache,
+                 slot_mapping, positions, cos_sin, (float(k_scale), float(v_scale)), interleaved,
+                 stream)
 
 
 def pa_rope_and_cache_fp4(query_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
@@ -888,49 +903,58 @@ def pa_rope_and_cache_fp4(query_out: torch.Tensor, query: torch.Tensor, key: tor
                           cos_sin: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0,
                           interleaved: bool = False, stream=None) -> torch.Tensor:
     """pa_rope_and_cache into FP4 caches (new_fp4_cache)."""
-    return _rope("_fp4", query_out, query, key, value, k_cache, v_cache, slot_mapping, positions,
-                 cos_sin, (float(k_scale), float(v_scale)), interleaved, stream)
+    return _rope("pa_rope_and_cache_fp4", query_out, query, key, value, k_cache, v_cache,
+                 slot_mapping, positions, cos_sin, (float(k_scale), float(v_scale)), interleaved,
+                 stream)
 
 
-def _bounds_shape(bounds, bound_scales, NB, Hkv, d):
-    if bounds.shape != (NB, Hkv, 2, d) or bound_scales.shape != (NB, Hkv):
-        raise ValueError(f"bounds must be [{NB}, {Hkv}, 2, {d}] and bound_scales [{NB}, {Hkv}]")
-
-
-def _batch(block_tables, context_lens, query_start):
-    """The number of sequences."""
-    B = context_lens.numel()
-    if block_tables.dim() != 2 or block_tables.shape[0] != B:
-        raise ValueError("block_tables must be [B, MB] and context_lens [B]")
-    if query_start is not None and query_start.numel() != B + 1:
-        raise ValueError("query_start must have num_seqs + 1 entries")
-    return B
-
-
-def _key_bounds(kind, bounds, bound_scales, k_cache, block_tables, context_lens, query_start,
+def _key_bounds(name, bounds, bound_scales, k_cache, block_tables, context_lens, query_start,
                 max_q_len, stream):
-    name = "pa_update_key_bounds" + kind
     f = _sparse_fns.get(name) or _sparse_fn(name)
-    dev = _device_of("bounds", bounds)
-    more = {} if query_start is None else {"query_start": (query_start, _I32)}
-    if not isinstance(k_cache, torch.Tensor):
-        _cuda("k_cache", k_cache)
-    _dense(dev, bounds=(bounds, _I8), bound_scales=(bound_scales, _F32),
-           k_cache=(k_cache, _U8 if kind else k_cache.dtype),
-           block_tables=(block_tables, _I32), context_lens=(context_lens, _I32), **more)
-    if bounds.dim() != 4:
-        raise ValueError("bounds must be [NB, Hkv, 2, d]")
-    d = bounds.shape[3]
-    NB, Hkv, bs = _cache_shape(kind, k_cache, d)
-    _bounds_shape(bounds, bound_scales, NB, Hkv, d)
-    B = _batch(block_tables, context_lens, query_start)
+    dev = _device_of("k_cache", k_cache)
+    plain = name == "pa_update_key_bounds"
+    cache = k_cache.dtype if plain else _U8
+    try:
+        fit = (bounds.dtype is _I8 and bound_scales.dtype is _F32 and k_cache.dtype is cache
+               and block_tables.dtype is _I32 and context_lens.dtype is _I32
+               and bounds.get_device() == dev == bound_scales.get_device()
+               and block_tables.get_device() == dev == context_lens.get_device()
+               and bounds.is_contiguous() and bound_scales.is_contiguous()
+               and k_cache.is_contiguous() and block_tables.is_contiguous()
+               and context_lens.is_contiguous())
+    except AttributeError:
+        fit = False
+    if not fit:
+        _all_fit(dev, bounds=(bounds, _I8), bound_scales=(bound_scales, _F32),
+                 k_cache=(k_cache, cache), block_tables=(block_tables, _I32),
+                 context_lens=(context_lens, _I32))
+    start = _start(query_start, dev, context_lens)
+    shape, table = bounds.shape, block_tables.shape
+    if len(shape) != 4 or shape[2] != 2 or bound_scales.shape != shape[:2]:
+        raise ValueError("bounds must be [NB, Hkv, 2, d] and bound_scales [NB, Hkv]")
+    d = shape[3]
+    NB, Hkv, bs = _cache_shape(name, k_cache, d)
+    if shape[0] != NB or shape[1] != Hkv:
+        raise ValueError("bounds and k_cache differ in blocks or heads")
+    B = context_lens.numel()
+    if len(table) != 2 or table[0] != B:
+        raise ValueError("block_tables must be [B, MB] and context_lens [B]")
     st = f(bounds.data_ptr(), bound_scales.data_ptr(), k_cache.data_ptr(), block_tables.data_ptr(),
-           block_tables.shape[1], context_lens.data_ptr(),
-           None if query_start is None else query_start.data_ptr(), B, int(max_q_len), Hkv, d, bs,
-           NB, *(() if kind else (_dtype_code(k_cache),)),
+           table[1], context_lens.data_ptr(), start, B, int(max_q_len), Hkv, d, bs, NB,
+           *((_dtype_code(k_cache),) if plain else ()),
            _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise PaError(name, st)
+
+
+def _start(query_start, dev, context_lens):
+    """The address of query_start, checked; None for none."""
+    if query_start is None:
+        return None
+    _fits("query_start", query_start, _I32, dev)
+    if query_start.numel() != context_lens.numel() + 1:
+        raise ValueError("query_start must have num_seqs + 1 entries")
+    return query_start.data_ptr()
 
 
 def pa_update_key_bounds(bounds: torch.Tensor, bound_scales: torch.Tensor, k_cache: torch.Tensor,
@@ -940,8 +964,8 @@ def pa_update_key_bounds(bounds: torch.Tensor, bound_scales: torch.Tensor, k_cac
     """Bring ``bounds`` and ``bound_scales`` (new_key_bounds) up to date for the
     blocks that hold the newest tokens of each sequence: the last one, or the
     last query_start[i + 1] - query_start[i] (at most max_q_len)."""
-    _key_bounds("", bounds, bound_scales, k_cache, block_tables, context_lens, query_start,
-                max_q_len, stream)
+    _key_bounds("pa_update_key_bounds", bounds, bound_scales, k_cache, block_tables,
+                context_lens, query_start, max_q_len, stream)
 
 
 def pa_update_key_bounds_fp8(bounds: torch.Tensor, bound_scales: torch.Tensor,
@@ -950,8 +974,8 @@ def pa_update_key_bounds_fp8(bounds: torch.Tensor, bound_scales: torch.Tensor,
                              query_start: Optional[torch.Tensor] = None, max_q_len: int = 1,
                              stream=None) -> None:
     """pa_update_key_bounds over a uint8 FP8 E4M3 cache."""
-    _key_bounds("_fp8", bounds, bound_scales, k_cache, block_tables, context_lens, query_start,
-                max_q_len, stream)
+    _key_bounds("pa_update_key_bounds_fp8", bounds, bound_scales, k_cache, block_tables,
+                context_lens, query_start, max_q_len, stream)
 
 
 def pa_update_key_bounds_fp4(bounds: torch.Tensor, bound_scales: torch.Tensor,
@@ -960,8 +984,8 @@ def pa_update_key_bounds_fp4(bounds: torch.Tensor, bound_scales: torch.Tensor,
                              query_start: Optional[torch.Tensor] = None, max_q_len: int = 1,
                              stream=None) -> None:
     """pa_update_key_bounds over an FP4 cache."""
-    _key_bounds("_fp4", bounds, bound_scales, k_cache, block_tables, context_lens, query_start,
-                max_q_len, stream)
+    _key_bounds("pa_update_key_bounds_fp4", bounds, bound_scales, k_cache, block_tables,
+                context_lens, query_start, max_q_len, stream)
 
 
 def pa_select_blocks(selected_tables: torch.Tensor, selected_lens: torch.Tensor,
@@ -979,56 +1003,83 @@ def pa_select_blocks(selected_tables: torch.Tensor, selected_lens: torch.Tensor,
     sees are always taken.  Returns (selected_tables, selected_lens)."""
     f = _sparse_fns.get("pa_select_blocks") or _sparse_fn("pa_select_blocks")
     dev = _device_of("query", query)
-    more = {} if query_start is None else {"query_start": (query_start, _I32)}
-    _dense(dev, query=(query, query.dtype), selected_tables=(selected_tables, _I32),
-           selected_lens=(selected_lens, _I32), bounds=(bounds, _I8),
-           bound_scales=(bound_scales, _F32), block_tables=(block_tables, _I32),
-           context_lens=(context_lens, _I32), **more)
-    if query.dim() != 3 or bounds.dim() != 4 or selected_tables.dim() != 3:
-        raise ValueError("query must be [R, Hq, d], bounds [NB, Hkv, 2, d] and selected_tables "
-                         "[R, Hkv, K]")
-    R, Hq, d = query.shape
-    NB, Hkv = bounds.shape[:2]
-    _bounds_shape(bounds, bound_scales, NB, Hkv, d)
-    K = selected_tables.shape[2]
-    if selected_tables.shape != (R, Hkv, K) or selected_lens.shape != (R, Hkv):
+    try:
+        fit = (selected_tables.dtype is _I32 and selected_lens.dtype is _I32
+               and bounds.dtype is _I8 and bound_scales.dtype is _F32
+               and block_tables.dtype is _I32 and context_lens.dtype is _I32
+               and selected_tables.get_device() == dev == selected_lens.get_device()
+               and bounds.get_device() == dev == bound_scales.get_device()
+               and block_tables.get_device() == dev == context_lens.get_device()
+               and query.is_contiguous() and selected_tables.is_contiguous()
+               and selected_lens.is_contiguous() and bounds.is_contiguous()
+               and bound_scales.is_contiguous() and block_tables.is_contiguous()
+               and context_lens.is_contiguous())
+    except AttributeError:
+        fit = False
+    if not fit:
+        _all_fit(dev, query=(query, query.dtype), selected_tables=(selected_tables, _I32),
+                 selected_lens=(selected_lens, _I32), bounds=(bounds, _I8),
+                 bound_scales=(bound_scales, _F32), block_tables=(block_tables, _I32),
+                 context_lens=(context_lens, _I32))
+    start = _start(query_start, dev, context_lens)
+    rows, shape, picked, table = (query.shape, bounds.shape, selected_tables.shape,
+                                  block_tables.shape)
+    if len(rows) != 3 or len(picked) != 3:
+        raise ValueError("query must be [R, Hq, d] and selected_tables [R, Hkv, K]")
+    R, Hq, d = rows
+    if len(shape) != 4 or shape[2] != 2 or shape[3] != d or bound_scales.shape != shape[:2]:
+        raise ValueError("bounds must be [NB, Hkv, 2, d] and bound_scales [NB, Hkv]")
+    Hkv = shape[1]
+    if picked[0] != R or picked[1] != Hkv or selected_lens.shape != picked[:2]:
         raise ValueError("selected_tables must be [R, Hkv, K] and selected_lens [R, Hkv]")
-    B = _batch(block_tables, context_lens, query_start)
-    if query_start is None and R != B:
+    B = context_lens.numel()
+    if len(table) != 2 or table[0] != B:
+        raise ValueError("block_tables must be [B, MB] and context_lens [B]")
+    if start is None and R != B:
         raise ValueError("without query_start there is one query row for each sequence")
     st = f(selected_tables.data_ptr(), selected_lens.data_ptr(), query.data_ptr(),
-           bounds.data_ptr(), bound_scales.data_ptr(), block_tables.data_ptr(),
-           block_tables.shape[1], context_lens.data_ptr(),
-           None if query_start is None else query_start.data_ptr(), B, int(max_q_len), Hq, Hkv, d,
-           int(block_size), NB, int(max_context_len), K, int(num_sink), int(num_recent),
+           bounds.data_ptr(), bound_scales.data_ptr(), block_tables.data_ptr(), table[1],
+           context_lens.data_ptr(), start, B, int(max_q_len), Hq, Hkv, d, int(block_size),
+           shape[0], int(max_context_len), picked[2], int(num_sink), int(num_recent),
            _dtype_code(query), _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise PaError("pa_select_blocks", st)
     return selected_tables, selected_lens
 
 
-def _decode_sparse(kind, out, query, k_cache, v_cache, selected_tables, selected_lens, scale,
+def _decode_sparse(name, out, query, k_cache, v_cache, selected_tables, selected_lens, scale,
                    scales, stream):
-    name = "pa_decode_sparse" + kind
     f = _sparse_fns.get(name) or _sparse_fn(name)
     dev = _device_of("query", query)
     dtype = query.dtype
-    cache = _U8 if kind else dtype
-    _dense(dev, query=(query, dtype), out=(out, dtype), k_cache=(k_cache, cache),
-           v_cache=(v_cache, cache), selected_tables=(selected_tables, _I32),
-           selected_lens=(selected_lens, _I32))
-    if query.dim() != 3 or out.shape != query.shape:
+    cache = _U8 if scales else dtype
+    try:
+        fit = (out.dtype is dtype and k_cache.dtype is cache and v_cache.dtype is cache
+               and selected_tables.dtype is _I32 and selected_lens.dtype is _I32
+               and out.get_device() == dev == k_cache.get_device() == v_cache.get_device()
+               and selected_tables.get_device() == dev == selected_lens.get_device()
+               and query.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous()
+               and v_cache.is_contiguous() and selected_tables.is_contiguous()
+               and selected_lens.is_contiguous())
+    except AttributeError:
+        fit = False
+    if not fit:
+        _all_fit(dev, query=(query, dtype), out=(out, dtype), k_cache=(k_cache, cache),
+                 v_cache=(v_cache, cache), selected_tables=(selected_tables, _I32),
+                 selected_lens=(selected_lens, _I32))
+    rows, picked = query.shape, selected_tables.shape
+    if len(rows) != 3 or out.shape != rows:
         raise ValueError("query and out must be [R, Hq, d], alike")
-    R, Hq, d = query.shape
-    NB, Hkv, bs = _cache_shape(kind, k_cache, d)
+    R, Hq, d = rows
+    NB, Hkv, bs = _cache_shape(name, k_cache, d)
     if v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache shapes differ")
-    if (selected_tables.dim() != 3 or selected_tables.shape[:2] != (R, Hkv)
-            or selected_lens.shape != (R, Hkv)):
+    if (len(picked) != 3 or picked[0] != R or picked[1] != Hkv
+            or selected_lens.shape != picked[:2]):
         raise ValueError("selected_tables must be [R, Hkv, K] and selected_lens [R, Hkv]")
     st = f(out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-           selected_tables.data_ptr(), selected_lens.data_ptr(), R, selected_tables.shape[2], Hq,
-           Hkv, d, bs, NB, float(scale), *scales, _dtype_code(query),
+           selected_tables.data_ptr(), selected_lens.data_ptr(), R, picked[2], Hq, Hkv, d, bs, NB,
+           float(scale), *scales, _dtype_code(query),
            _raw_stream(dev) if stream is None else _stream(stream))
     if st:
         raise PaError(name, st)
@@ -1041,8 +1092,8 @@ def pa_decode_sparse(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tens
     """Decode attention of query [R, Hq, d] into ``out``, row r and KV head g
     over the first selected_lens[r, g] tokens of the blocks
     selected_tables[r, g, :] (pa_select_blocks)."""
-    return _decode_sparse("", out, query, k_cache, v_cache, selected_tables, selected_lens, scale,
-                          (), stream)
+    return _decode_sparse("pa_decode_sparse", out, query, k_cache, v_cache, selected_tables,
+                          selected_lens, scale, (), stream)
 
 
 def pa_decode_sparse_fp8(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor,
@@ -1050,8 +1101,8 @@ def pa_decode_sparse_fp8(out: torch.Tensor, query: torch.Tensor, k_cache: torch.
                          selected_lens: torch.Tensor, scale: float, k_scale: float,
                          v_scale: float, stream=None) -> torch.Tensor:
     """pa_decode_sparse over uint8 FP8 E4M3 caches, fp16 or bf16 queries and output."""
-    return _decode_sparse("_fp8", out, query, k_cache, v_cache, selected_tables, selected_lens,
-                          scale, (float(k_scale), float(v_scale)), stream)
+    return _decode_sparse("pa_decode_sparse_fp8", out, query, k_cache, v_cache, selected_tables,
+                          selected_lens, scale, (float(k_scale), float(v_scale)), stream)
 
 
 def pa_decode_sparse_fp4(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tensor,
@@ -1059,8 +1110,8 @@ def pa_decode_sparse_fp4(out: torch.Tensor, query: torch.Tensor, k_cache: torch.
                          selected_lens: torch.Tensor, scale: float, k_scale: float,
                          v_scale: float, stream=None) -> torch.Tensor:
     """pa_decode_sparse over FP4 caches, fp16 or bf16 queries and output."""
-    return _decode_sparse("_fp4", out, query, k_cache, v_cache, selected_tables, selected_lens,
-                          scale, (float(k_scale), float(v_scale)), stream)
+    return _decode_sparse("pa_decode_sparse_fp4", out, query, k_cache, v_cache, selected_tables,
+                          selected_lens, scale, (float(k_scale), float(v_scale)), stream)
 
 
 def pa_selftest_bounded_wait(stream=None) -> None:

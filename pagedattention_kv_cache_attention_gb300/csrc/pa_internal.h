@@ -168,7 +168,8 @@ struct SelectArgs {
   int max_blocks_per_seq, num_seqs, max_q_len, num_q_heads, num_kv_heads, group, bs_log2;
   int64_t num_blocks;
   int max_context_len, num_selected, num_sink, num_recent;
-  int cluster;                  // CTAs that share a row's blocks
+  int cluster;                  // CTAs that may share a row's blocks
+  int units_per_cta;            // at least, where they are more than one
   int max_candidates;           // blocks of the longest context
   unsigned *err;
 };

@@ -416,52 +416,88 @@ template <int D> struct Unit {
   }
 };
 
-// Block j of a sequence's table, -1 (and flagged) if it is none.
-__device__ __forceinline__ int block_of(const SelectArgs &a, const int32_t *bt_row, int j, int n) {
-  const int phys = j < n ? bt_row[j] : -1;
-  if (phys >= 0 && phys < a.num_blocks) return phys;
-  if (j < n) atomicOr(a.err, kErrBadBlock);
-  return -1;
-}
+// A sequence's table, 16 blocks (g and g + 8 of a lane) at a time: entries may be
+// read before the length is known, blocks are what is left of them then.
+struct Table {
+  const int32_t *row;
+  int width;
+  __device__ __forceinline__ Table(const SelectArgs &a, int seq)
+      : row(a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq),
+        width(a.max_blocks_per_seq) {}
+  __device__ __forceinline__ void entries(int j, int (&e)[2]) const {
+    e[0] = j < width ? row[j] : -1;
+    e[1] = j + 8 < width ? row[j + 8] : -1;
+  }
+  // -1 for entry e of block j >= n, or (flagged) for one that is no block
+  static __device__ __forceinline__ int block(const SelectArgs &a, int e, int j, int n) {
+    if (j >= n) return -1;
+    if (e >= 0 && e < a.num_blocks) return e;
+    atomicOr(a.err, kErrBadBlock);
+    return -1;
+  }
+};
 
 // Short contexts: at most 32 KPL blocks.  A CTA takes up to 4 TILES rows of a
 // sequence and one KV head: its warps score 16 blocks at a time for all rows, so
 // that bounds are read once for them; then a warp a row picks, with the row's keys
 // in registers and no barrier.
+// The largest t in [lo, hi] with at_least(t) >= want, where at_least(c) counts the
+// keys >= c, at_least(lo) = count >= want, and no key is above hi; count becomes
+// at_least(t).  Every second guess is where t would lie if the keys were spread
+// evenly, the others halve the range; done early where the count is just `want`
+// (some five guesses among 256 keys, in place of twenty bits one by one).
+template <typename F>
+__device__ __forceinline__ uint32_t threshold(uint32_t lo, uint32_t hi, int &count, int want,
+                                              F &&at_least) {
+  int above = 0;  // keys > hi
+  bool even = true;
+  while (lo != hi && count != want) {
+    const uint32_t room = hi - lo;  // c - lo is 1 .. room
+    uint32_t off = room / 2;
+    if (even)
+      off = static_cast<uint32_t>(static_cast<float>(room) * static_cast<float>(count - want) /
+                                  static_cast<float>(count - above));
+    even = !even;
+    const uint32_t c = lo + 1 + min(off, room - 1);
+    const int here = at_least(c);
+    if (here >= want) {
+      lo = c;
+      count = here;
+    } else {
+      hi = c - 1;
+      above = here;
+    }
+  }
+  return lo;
+}
+
 // The keys of a row (key i * 32 + lane of n in k[i]; 0 past n): calls take(i, place)
-// in the lanes of the `want` largest, ties to the first; want <= n.
+// in the lanes of the `want` largest, ties to the first; want < n, and more than
+// the forced ones or as many.
 template <int KPL, typename F>
-__device__ __forceinline__ void pick(const uint32_t (&k)[KPL], int n, int want, int lane, F &&take) {
+__device__ __forceinline__ void pick(const uint32_t (&k)[KPL], int n, int forced, int want, int lane,
+                                     F &&take) {
   uint32_t lo = 0xffffffffu, hi = 0;
 #pragma unroll
   for (int i = 0; i < KPL; ++i) {
-    if (i * 32 + lane < n) {
+    if (i * 32 + lane < n && k[i] != kForced) {
       lo = min(lo, k[i]);
       hi = max(hi, k[i]);
     }
   }
   lo = __reduce_min_sync(kAll, lo);
   hi = __reduce_max_sync(kAll, hi);
-  // the largest t with at least `want` keys >= t, a bit at a time from the first
-  // in which keys differ; done early where they are just `want`
-  uint32_t t = lo;
   int count = n;
-  if (lo != hi && count != want) {
-    const int top = 31 - __clz(lo ^ hi);
-    t = hi & ~((2u << top) - 1);
-    for (int bit = top; bit >= 0; --bit) {
-      const uint32_t c = t | (1u << bit);
+  uint32_t t = kForced;
+  if (want == forced)
+    count = want;
+  else
+    t = threshold(lo, hi, count, want, [&](uint32_t c) {
       int here = 0;
 #pragma unroll
       for (int i = 0; i < KPL; ++i) here += k[i] >= c ? 1 : 0;
-      here = __reduce_add_sync(kAll, here);
-      if (here >= want) {
-        t = c;
-        count = here;
-        if (here == want) break;
-      }
-    }
-  }
+      return static_cast<int>(__reduce_add_sync(kAll, here));
+    });
   // keys above t are taken, and of those equal to it (the count has count - want
   // too many) the first
   int equal = 0;
@@ -497,7 +533,10 @@ __global__ void __launch_bounds__(NW * 32) select_short_kernel(const SelectArgs 
   const int bs = 1 << a.bs_log2, K = a.num_selected;
   grid_dependency_wait();  // queries, bounds and lengths may come from the kernel before
   grid_launch_dependents();
-  const int32_t *bt_row = a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq;
+  const Table table(a, seq);
+  const int32_t *bt_row = table.row;
+  int j0 = warp * U::kBlocks, e[2];
+  table.entries(j0 + g, e);
   SelectRows rows;
   if (!rows.load(a, seq, tid == 0 && blockIdx.x == 0 && kvh == 0)) return;
   const int t0 = blockIdx.x * kRows, count = min(kRows, rows.rows - t0);
@@ -510,10 +549,11 @@ __global__ void __launch_bounds__(NW * 32) select_short_kernel(const SelectArgs 
                                    : nullptr,
                          a.group, r % 4, lane);
     __syncthreads();
-    for (int j0 = warp * U::kBlocks; j0 < most; j0 += NW * U::kBlocks) {
-      const int phys[2] = {block_of(a, bt_row, j0 + g, most), block_of(a, bt_row, j0 + 8 + g, most)};
+    for (; j0 < most; j0 += NW * U::kBlocks) {
+      const int phys[2] = {Table::block(a, e[0], j0 + g, most), Table::block(a, e[1], j0 + 8 + g, most)};
       U unit;
       unit.load(a, kvh, phys, c);
+      if (j0 + NW * U::kBlocks < most) table.entries(j0 + NW * U::kBlocks + g, e);
       uint32_t key[TILES][2];
       unit.template keys<TILES>(weights, lane, key);
 #pragma unroll
@@ -542,7 +582,7 @@ __global__ void __launch_bounds__(NW * 32) select_short_kernel(const SelectArgs 
       if (j < n && (j < a.num_sink || j >= n - a.num_recent)) k[i] = kForced;
     }
     bool last = false;
-    pick<KPL>(k, n, K, lane, [&](int i, int place) {
+    pick<KPL>(k, n, a.num_sink + a.num_recent, K, lane, [&](int i, int place) {
       out[place] = bt_row[i * 32 + lane];
       last = last || i * 32 + lane == n - 1;
     });
@@ -552,22 +592,20 @@ __global__ void __launch_bounds__(NW * 32) select_short_kernel(const SelectArgs 
 }
 
 // Long contexts: the CTAs of a cluster score a share of a row's blocks each, into
-// the keys of the first one, which then picks.  A thread of that one takes runs of
-// 32 keys; a word between two runs puts the lanes' keys into different banks.
-constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
+// the keys of the first one, which then picks.
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048, kBinBits = 11;
-__host__ __device__ constexpr int64_t key_place(int64_t j) { return j + (j >> 5); }
 
-// Shared memory of a CTA, after the keys.
+// Shared memory of a CTA, before the keys.
 template <int D> struct SelectShared {
   Weights<D> weights;
   uint32_t bins[kBins];
-  uint32_t part[3][kSelWarps];
+  uint32_t part[kSelWarps];
+  uint32_t lo, hi;  // of the keys that are not forced
   uint32_t chosen_bin, chosen_above, chosen_count;
+  uint32_t few[32], few_count;
+  uint32_t few_keys[kSelThreads], few_at[kSelThreads];  // keys that may be taken, and where they are
 };
-__host__ __device__ constexpr size_t key_bytes(int64_t n) {
-  return (static_cast<size_t>(key_place(n)) * 4 + 15) & ~static_cast<size_t>(15);
-}
 
 // Sum over the CTA's threads before this one; `all`: over all of them.
 __device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t *part, uint32_t &all) {
@@ -591,32 +629,219 @@ __device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t *part, uint3
   return before + incl - v;
 }
 
+// The two halves of cluster_sync.
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void red_cluster_min(uint32_t addr, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.min.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void red_cluster_max(uint32_t addr, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// The K largest of n > K keys, ties to the first; the keys' indexes take their
+// places in order from keys[0] on.  For a whole CTA.  In a turn thread i takes
+// keys L i .. L i + L - 1, from one of its own on around (different lanes,
+// different banks).  ONE: one turn does (n <= 512 L), the keys stay in registers.
+template <int D, int L, bool ONE>
+__device__ __forceinline__ void pick_long(const SelectArgs &a, SelectShared<D> &sh, uint32_t *keys,
+                                          int n) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  constexpr int kTurn = kSelThreads * L;
+  const int first = lane * L / 32;
+  uint32_t k[L];  // k[i] is key (first + i) % L of the run; 0 past n
+  auto load = [&](int j0) {
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      const int j = j0 + tid * L + ((first + i) & (L - 1));
+      k[i] = j < n ? keys[j] : 0;
+    }
+  };
+  if (ONE) load(0);
+  // f() with every turn's keys in k
+  auto turns = [&](auto &&f) {
+    if (ONE) {
+      f();
+    } else {
+      for (int j0 = 0; j0 < n; j0 += kTurn) {
+        load(j0);
+        f();
+      }
+    }
+  };
+  uint32_t lo = sh.lo, hi = sh.hi;
+  const int forced = a.num_sink + a.num_recent;
+  int need = a.num_selected - forced;  // fewer than the keys not forced
+  if (ONE && need > 0 && need <= n / L) {
+    // As many whole runs as are wanted: the need-th largest of the runs' largest
+    // keys is a bound that the need-th largest key is not below, and few keys pass
+    // it (of 8,192 in 512 runs some 145 for the 128 largest).  Among these a thread
+    // a key picks.
+    uint32_t top = lo;
+#pragma unroll
+    for (int i = 0; i < L; ++i) top = max(top, k[i] == kForced ? 0 : k[i]);
+    int count = n / L;
+    const uint32_t least = threshold(lo, hi, count, need, [&](uint32_t c) {
+      return __syncthreads_count(tid < n / L && top >= c);
+    });
+    uint32_t mine = 0, all;
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      const int at = (first + i) & (L - 1);
+      mine |= (tid * L + at < n && k[i] >= least ? 1u : 0u) << at;
+    }
+    int place = sum_before(__popc(mine), sh.part, all);
+    if (all <= kSelThreads) {
+      while (mine) {
+        const int i = __ffs(mine) - 1;
+        mine &= mine - 1;
+        sh.few_keys[place] = keys[tid * L + i];
+        sh.few_at[place++] = tid * L + i;
+      }
+      __syncthreads();
+      const bool real = tid < static_cast<int>(all);
+      const uint32_t x = real ? sh.few_keys[tid] : 0;
+      count = all;
+      const uint32_t t = threshold(least, hi, count, a.num_selected, [&](uint32_t c) {
+        return __syncthreads_count(real && x >= c);
+      });
+      // keys above t are taken, and of those equal to it the first
+      const bool eq = real && x == t;
+      const int left = a.num_selected - __syncthreads_count(real && x > t);
+      const uint32_t before = sum_before((real && x > t ? 1u : 0u) | (eq ? 0x10000u : 0u), sh.part, all);
+      const int ties = before >> 16;
+      if ((real && x > t) || (eq && ties < left))
+        keys[(before & 0xffff) + min(ties, left)] = sh.few_at[tid];
+      __syncthreads();
+      return;
+    }
+    __syncthreads();
+  }
+  bool whole = need == 0;  // every key of [lo, hi] is taken
+  if (whole) lo = hi = kForced;
+  // The need-th largest key: the range [lo, hi] that holds it is cut into kBins
+  // equal parts, their keys counted, and the part that holds it taken, until
+  // what is left of the range is taken whole, is one value or holds few keys.
+  while (!whole && lo != hi) {
+    const int shift = max(0, 32 - __clz(hi - lo) - kBinBits);
+#pragma unroll
+    for (int i = 0; i < kBins; i += kSelThreads) sh.bins[i + tid] = 0;
+    if (tid == 0) sh.few_count = 0;
+    __syncthreads();
+    turns([&] {
+#pragma unroll
+      for (int i = 0; i < L; ++i)
+        if (k[i] >= lo && k[i] <= hi) atomicAdd(&sh.bins[(k[i] - lo) >> shift], 1u);
+    });
+    __syncthreads();
+    // the part with the need-th largest key: sums over the parts from the top;
+    // thread i holds some parts, from part kBins - 1 - kPer i down
+    constexpr int kPer = kBins / kSelThreads;
+    uint32_t mine[kPer], sum = 0, all;
+#pragma unroll
+    for (int b = 0; b < kPer; ++b) {
+      mine[b] = sh.bins[kBins - 1 - tid * kPer - b];
+      sum += mine[b];
+    }
+    uint32_t before = sum_before(sum, sh.part, all);
+#pragma unroll
+    for (int b = 0; b < kPer; ++b) {
+      if (before < static_cast<uint32_t>(need) && before + mine[b] >= static_cast<uint32_t>(need)) {
+        sh.chosen_bin = kBins - 1 - tid * kPer - b;
+        sh.chosen_above = before;
+        sh.chosen_count = mine[b];
+      }
+      before += mine[b];
+    }
+    __syncthreads();
+    const int count = sh.chosen_count;
+    need -= sh.chosen_above;
+    whole = count == need;
+    lo += sh.chosen_bin << shift;
+    hi = min(hi, lo + ((1u << shift) - 1));
+    if (!whole && lo != hi && count <= 32) {
+      // the need-th largest of them: its rank is the number of larger ones, and of
+      // equal ones before it
+      turns([&] {
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+          if (k[i] >= lo && k[i] <= hi) sh.few[atomicAdd(&sh.few_count, 1u)] = k[i];
+      });
+      __syncthreads();
+      const uint32_t x = lane < count ? sh.few[lane] : 0;
+      int rank = 0, above = 0;
+      for (int i = 0; i < count; ++i) {
+        const uint32_t other = __shfl_sync(kAll, x, i);
+        rank += other > x || (other == x && i < lane) ? 1 : 0;
+        above += other > x ? 1 : 0;
+      }
+      const int who = __ffs(__ballot_sync(kAll, lane < count && rank == need - 1)) - 1;
+      lo = hi = __shfl_sync(kAll, x, who);
+      need -= __shfl_sync(kAll, above, who);
+    }
+  }
+  // Keys above hi are taken, those of [lo, hi] too if `whole`; otherwise they are
+  // one value, and the first `need` of them are.  (A key's index is at least its
+  // place: written over the keys, it meets none that is still to be read.)
+  int place0 = 0, j0 = 0;  // taken before this turn's keys, which begin at j0
+  turns([&] {
+    uint32_t above = 0, equal = 0;
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      const int at = (first + i) & (L - 1);
+      const bool in = j0 + tid * L + at < n;
+      above |= (in && (whole ? k[i] >= lo : k[i] > lo) ? 1u : 0u) << at;
+      equal |= (in && !whole && k[i] == lo ? 1u : 0u) << at;
+    }
+    uint32_t all;
+    __syncthreads();  // sh.part is free
+    const uint32_t before = sum_before(__popc(above) | (__popc(equal) << 16), sh.part, all);
+    const int ties = before >> 16;
+    int place = place0 + static_cast<int>(before & 0xffff) + min(ties, need);
+    int left = max(0, need - ties);
+    uint32_t todo = above | equal;
+    while (todo) {
+      const int i = __ffs(todo) - 1;
+      todo &= todo - 1;
+      if ((equal >> i) & 1u) {
+        if (left == 0) continue;
+        --left;
+      }
+      keys[place++] = j0 + tid * L + i;
+    }
+    place0 += static_cast<int>(all & 0xffff) + min(static_cast<int>(all >> 16), need);
+    need -= min(static_cast<int>(all >> 16), need);
+    j0 += kTurn;
+  });
+  __syncthreads();
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kSelThreads, 2) select_long_kernel(const SelectArgs a) {
   using U = Unit<D>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  uint32_t *keys = reinterpret_cast<uint32_t *>(smem_raw);
-  SelectShared<D> &sh = *reinterpret_cast<SelectShared<D> *>(smem_raw + key_bytes(a.max_candidates));
+  SelectShared<D> &sh = *reinterpret_cast<SelectShared<D> *>(smem_raw);
+  uint32_t *keys = reinterpret_cast<uint32_t *>(smem_raw + sizeof(SelectShared<D>));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
-  const int cluster = a.cluster, rank = static_cast<int>(blockIdx.x) % cluster;
-  const int t = static_cast<int>(blockIdx.x) / cluster;  // row of the sequence's chunk
-  const int kvh = blockIdx.y, seq = blockIdx.z;
+  const int rank = static_cast<int>(blockIdx.x) % a.cluster;
+  const int t = static_cast<int>(blockIdx.x) / a.cluster;  // row of the sequence's chunk
+  // (heads last: neighbouring clusters are of different sequences, so that the
+  // long ones do not meet on the same SMs)
+  const int seq = blockIdx.y, kvh = blockIdx.z;
   const int bs = 1 << a.bs_log2, K = a.num_selected;
+  if (tid == 0) sh.lo = 0xffffffffu, sh.hi = 0;
   grid_dependency_wait();  // queries, bounds and lengths may come from the kernel before
   grid_launch_dependents();
 
-  // the warp's first units' blocks, read before the length is known
-  const int32_t *bt_row = a.block_tables + static_cast<int64_t>(seq) * a.max_blocks_per_seq;
-  const int step = cluster * kSelWarps * U::kBlocks;
-  int j0 = (rank * kSelWarps + warp) * U::kBlocks;
-  auto entries = [&](int j, int (&e)[2]) {
-    e[0] = j + g < a.max_blocks_per_seq ? bt_row[j + g] : -1;
-    e[1] = j + 8 + g < a.max_blocks_per_seq ? bt_row[j + 8 + g] : -1;
-  };
-  int ahead[2][2];
-  entries(j0, ahead[0]);
-  entries(j0 + step, ahead[1]);
+  const Table table(a, seq);
+  const int32_t *bt_row = table.row;
   SelectRows rows;
   if (!rows.load(a, seq, tid == 0 && blockIdx.x == 0 && kvh == 0) || t >= rows.rows)
     return;  // (the whole cluster)
@@ -631,165 +856,77 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_long_kernel(const Selec
     }
     return;  // (the whole cluster)
   }
-  // units in turn, the loads of the next one under way while one is worked on
-  auto fetch = [&](U &u, int j, const int (&e)[2]) {
-    int phys[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const bool in = j + 8 * b + g < n, good = e[b] >= 0 && e[b] < a.num_blocks;
-      if (in && !good) atomicOr(a.err, kErrBadBlock);
-      phys[b] = in && good ? e[b] : -1;
-    }
-    u.load(a, kvh, phys, c);
-  };
-  U u[2];
-  fetch(u[0], j0, ahead[0]);
+  // CTAs that have work; the others make room (a CTA that has left counts as
+  // arrived at the cluster's barriers)
+  const int units = (n + U::kBlocks - 1) / U::kBlocks;
+  const int ctas = min(a.cluster, (units + a.units_per_cta - 1) / a.units_per_cta);
+  if (rank >= ctas) return;
+  if (ctas > 1) cluster_arrive();
+  // the warp's units, `step` blocks apart; the next one's entries are read while one
+  // is worked on
+  const int step = ctas * kSelWarps * U::kBlocks;
+  int j0 = (rank * kSelWarps + warp) * U::kBlocks, e[2];
+  table.entries(j0 + g, e);
   if (warp < 4)
     sh.weights.put(warp == 0 ? static_cast<const T *>(a.query) +
                                    (row * a.num_q_heads + kvh * a.group) * D
                              : nullptr,
                    a.group, warp, lane);
-  // the first CTA of the cluster has started: its shared memory is there
-  if (cluster > 1) cluster_sync(); else __syncthreads();
-  const uint32_t keys_at = cluster > 1 ? cluster_addr(keys, 0) : 0;
-  auto score = [&](const U &unit, int j) {
+  __syncthreads();
+  if (ctas > 1) cluster_wait();  // the first CTA has started: its shared memory is there
+  const uint32_t keys_at = ctas > 1 ? cluster_addr(keys, 0) : 0;
+  uint32_t lo = 0xffffffffu, hi = 0;  // of the keys that are not forced
+  for (; j0 < n; j0 += step) {
+    const int phys[2] = {Table::block(a, e[0], j0 + g, n), Table::block(a, e[1], j0 + 8 + g, n)};
+    U unit;
+    unit.load(a, kvh, phys, c);
+    if (j0 + step < n) table.entries(j0 + step + g, e);
     uint32_t key[1][2];
     unit.template keys<1>(&sh.weights, lane, key);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const int at = j + 8 * b + g;
-      if (c == 0 && at < n) {
-        const uint32_t k = at < a.num_sink || at >= n - a.num_recent ? kForced : key[0][b];
-        if (cluster > 1)
-          st_cluster_u32(keys_at + static_cast<uint32_t>(key_place(at)) * 4, k);
+      const int j = j0 + 8 * b + g;
+      if (c == 0 && j < n) {
+        uint32_t k = key[0][b];
+        if (j < a.num_sink || j >= n - a.num_recent) {
+          k = kForced;
+        } else {
+          lo = min(lo, k);
+          hi = max(hi, k);
+        }
+        if (ctas > 1)
+          st_cluster_u32(keys_at + j * 4, k);
         else
-          keys[key_place(at)] = k;
+          keys[j] = k;
       }
-    }
-  };
-  while (j0 < n) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (j0 >= n) break;
-      // (entries of the unit after the next one: read now, used a turn later)
-      if (j0 + step < n) fetch(u[s ^ 1], j0 + step, ahead[s ^ 1]);
-      if (j0 + 2 * step < n) entries(j0 + 2 * step, ahead[s]);
-      score(u[s], j0);
-      j0 += step;
     }
   }
-  if (cluster > 1) cluster_sync(); else __syncthreads();
-  if (rank != 0) return;
-
-  // f(key, j) for the keys of run r
-  auto run = [&](int r, auto &&f) {
-#pragma unroll 8
-    for (int i = 0; i < 32; ++i)
-      if (r * 32 + i < n) f(keys[r * 33 + i], i);
-  };
-  // The K-th largest key: the range [lo, hi] that holds it is cut into kBins
-  // equal parts, their keys counted, and the part that holds it taken, until
-  // what is left of the range is taken whole or is one value.
-  uint32_t lo = 0xffffffffu, hi = 0;
-  int forced = 0;
-  for (int r = tid; r * 32 < n; r += kSelThreads)
-    run(r, [&](uint32_t k, int) {
-      if (k == kForced) {
-        ++forced;
-      } else {
-        lo = min(lo, k);
-        hi = max(hi, k);
-      }
-    });
   lo = __reduce_min_sync(kAll, lo);
   hi = __reduce_max_sync(kAll, hi);
-  forced = __reduce_add_sync(kAll, forced);
-  if (lane == 0) sh.part[0][warp] = lo, sh.part[1][warp] = hi, sh.part[2][warp] = forced;
-  __syncthreads();
-  forced = 0;
-#pragma unroll
-  for (int i = 0; i < kSelWarps; ++i) {
-    lo = min(lo, sh.part[0][i]);
-    hi = max(hi, sh.part[1][i]);
-    forced += sh.part[2][i];
-  }
-  int need = K - forced;  // >= 0: the call's checks; fewer than n - forced
-  bool whole = need == 0;  // every key of [lo, hi] is taken
-  if (whole) lo = kForced, hi = kForced;
-  while (!whole && lo != hi) {
-    const int shift = max(0, 32 - __clz(hi - lo) - kBinBits);
-    __syncthreads();
-    for (int i = tid; i < kBins; i += kSelThreads) sh.bins[i] = 0;
-    __syncthreads();
-    for (int r = tid; r * 32 < n; r += kSelThreads)
-      run(r, [&](uint32_t k, int) {
-        if (k >= lo && k <= hi) atomicAdd(&sh.bins[(k - lo) >> shift], 1u);
-      });
-    __syncthreads();
-    // the part with the need-th largest key: sums over the parts from the top;
-    // thread i holds 8 parts, from part kBins - 1 - 8 i down
-    constexpr int kPer = kBins / kSelThreads;
-    uint32_t mine[kPer], sum = 0, all;
-#pragma unroll
-    for (int b = 0; b < kPer; ++b) {
-      mine[b] = sh.bins[kBins - 1 - tid * kPer - b];
-      sum += mine[b];
+  if (lane == 0) {
+    if (ctas > 1) {
+      red_cluster_min(cluster_addr(&sh.lo, 0), lo);
+      red_cluster_max(cluster_addr(&sh.hi, 0), hi);
+    } else {
+      atomicMin(&sh.lo, lo);
+      atomicMax(&sh.hi, hi);
     }
-    uint32_t before = sum_before(sum, sh.part[0], all);
-#pragma unroll
-    for (int b = 0; b < kPer; ++b) {
-      if (before < static_cast<uint32_t>(need) && before + mine[b] >= static_cast<uint32_t>(need)) {
-        sh.chosen_bin = kBins - 1 - tid * kPer - b;
-        sh.chosen_above = before;
-        sh.chosen_count = mine[b];
-      }
-      before += mine[b];
-    }
-    __syncthreads();
-    need -= sh.chosen_above;
-    whole = sh.chosen_count == static_cast<uint32_t>(need);
-    lo += sh.chosen_bin << shift;
-    hi = min(hi, lo + ((1u << shift) - 1));
   }
-  // Keys above hi are taken, those of [lo, hi] too if `whole`; otherwise they are
-  // one value, and the first `need` of them are.  Blocks taken are written over
-  // the keys, in order (the place of block j is at most j), and then looked up.
-  int place0 = 0;  // taken before this turn's keys
-  for (int r0 = 0; r0 * 32 < n; r0 += kSelThreads) {
-    uint32_t above = 0, equal = 0;
-    run(r0 + tid, [&](uint32_t k, int i) {
-      above |= (whole ? k >= lo : k > lo) ? 1u << i : 0;
-      equal |= !whole && k == lo ? 1u << i : 0;
-    });
-    uint32_t all;
-    __syncthreads();  // sh.part
-    const uint32_t before = sum_before(__popc(above) | (__popc(equal) << 16), sh.part[0], all);
-    // (every thread has read its keys of this turn, too)
-    const int ties = before >> 16;
-    int place = place0 + static_cast<int>(before & 0xffff) + min(ties, need);
-    int left = max(0, need - ties);
-    uint32_t todo = above | equal;
-    while (todo) {
-      const int i = __ffs(todo) - 1;
-      todo &= todo - 1;
-      if ((equal >> i) & 1u) {
-        if (left == 0) continue;
-        --left;
-      }
-      keys[key_place(place++)] = (r0 + tid) * 32 + i;
-    }
-    place0 += static_cast<int>(all & 0xffff) + min(static_cast<int>(all >> 16), need);
-    need -= min(static_cast<int>(all >> 16), need);
-  }
-  __syncthreads();
-  for (int i = tid; i < K; i += kSelThreads) out[i] = bt_row[keys[key_place(i)]];
-  if (tid == 0)
-    *out_len = K * bs - (keys[key_place(K - 1)] == static_cast<uint32_t>(n - 1) ? n * bs - seen : 0);
+  if (ctas > 1) cluster_sync(); else __syncthreads();
+  if (rank != 0) return;
+  if (n <= kSelThreads * 4)
+    pick_long<D, 4, true>(a, sh, keys, n);
+  else if (n <= kSelThreads * 16)
+    pick_long<D, 16, true>(a, sh, keys, n);
+  else
+    pick_long<D, 16, false>(a, sh, keys, n);
+  for (int i = tid; i < K; i += kSelThreads) out[i] = bt_row[keys[i]];
+  if (tid == 0) *out_len = K * bs - (keys[K - 1] == static_cast<uint32_t>(n - 1) ? n * bs - seen : 0);
 }
 
 template <typename T, int D> cudaError_t launch_long(SelectArgs a, cudaStream_t stream) {
-  const size_t smem = key_bytes(a.max_candidates) + sizeof(SelectShared<D>);
-  constexpr size_t most = key_bytes(kMaxCandidates) + sizeof(SelectShared<D>);
+  const size_t smem = sizeof(SelectShared<D>) + static_cast<size_t>(a.max_candidates) * 4;
+  constexpr size_t most = sizeof(SelectShared<D>) + kMaxCandidates * 4;
   static_assert(most <= 227 * 1024, "shared memory");
   auto kern = select_long_kernel<T, D>;
   static SmemLimitOnce smem_limit;
@@ -799,8 +936,9 @@ template <typename T, int D> cudaError_t launch_long(SelectArgs a, cudaStream_t 
   a.cluster = 1;
   while (a.cluster < 8 && 2 * a.cluster * rows <= 4 * kSms && a.max_candidates >= 512 * a.cluster)
     a.cluster *= 2;
+  a.units_per_cta = kSelWarps * (a.cluster * rows <= 2 * kSms ? 1 : 4);
   return launch_clusters(a.cluster, kern,
-                         dim3(static_cast<unsigned>(a.cluster * a.max_q_len), a.num_kv_heads, a.num_seqs),
+                         dim3(static_cast<unsigned>(a.cluster * a.max_q_len), a.num_seqs, a.num_kv_heads),
                          dim3(kSelThreads), smem, stream, a);
 }
 
