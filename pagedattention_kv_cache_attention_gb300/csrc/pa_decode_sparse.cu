@@ -11,6 +11,11 @@
 //    and O^T += V^T P^T on mma.sync, fp32 online softmax, P in two parts.
 //  * The warps' (m, l, o) are merged through shared memory, the CTAs' through one
 //    another's: no workspace, no second kernel.
+// What bounds it: HBM, and of small calls the chain of latencies from the table
+// over the first tiles to the join.  Measured (32 / 8 heads x 128, fp16 or bf16):
+// 64 rows of 512 tokens 23.1 us for 135 MB, 5.9 TB/s; 8 rows of 2,048 tokens 15.0 us
+// for 67 MB, 4.5 TB/s; FP8, 256 rows of up to 1,024 tokens, 64 / 8 heads: 67 us for
+// 420 MB, 6.2 TB/s.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -389,40 +394,53 @@ __global__ void __launch_bounds__(NW * 32)
   grid_launch_dependents();
 }
 
-// CTAs that share a row's tokens: as many as the SMs have room for, while a warp
-// keeps two steps of the longest table.
-int cluster_of(const DecodeArgs &a, int64_t ctas, int warps, int per_sm, int step_tokens) {
-  const int64_t steps = a.max_context_len / step_tokens;
-  int n = 1;
-  while (n < kMaxCluster && 2 * n * ctas <= kSms * per_sm && steps >= 4 * n * warps) n *= 2;
-  return n;
-}
-
-template <typename T, int D, int NW, int S, bool F8, int NSUB>
-cudaError_t launch_t(DecodeArgs a, const CUtensorMap &km, const CUtensorMap &vm,
-                     cudaStream_t stream) {
-  using Sh = Shape<D, F8>;
-  constexpr size_t stages = static_cast<size_t>(NW) * S * 2 * NSUB * Sh::kTileBytes;
-  constexpr size_t smem = 1024 + stages + NW * S * 8;
-  static_assert((static_cast<size_t>(NW) + 1) * 8 * (D + 2) * 4 <= stages,
+// One instance of the kernel: its shared memory, and how many CTAs of it an SM
+// takes at least (by shared memory, and at most 136 registers a thread).
+template <typename T, int D, int NW, int S, bool F8, int NSUB> struct Instance {
+  static constexpr int kWarps = NW, kStepTokens = NSUB * kTile;
+  static constexpr size_t kStages = static_cast<size_t>(NW) * S * 2 * NSUB * Shape<D, F8>::kTileBytes;
+  static constexpr size_t kSmem = 1024 + kStages + NW * S * 8;
+  static constexpr int kPerSm = static_cast<int>(227 * 1024 / (kSmem + 1024));
+  static_assert((static_cast<size_t>(NW) + 1) * 8 * (D + 2) * 4 <= kStages,
                 "merge buffers must fit in the stage area");
-  auto kern = sparse_decode_kernel<T, D, NW, S, F8, NSUB>;
-  static SmemLimitOnce smem_limit;
-  const cudaError_t e = smem_limit.ensure(kern, smem);
-  if (e != cudaSuccess) return e;
-  constexpr int per_sm = static_cast<int>(227 * 1024 / (smem + 1024));
-  a.cluster = cluster_of(a, static_cast<int64_t>(a.num_seqs) * a.num_kv_heads, NW, per_sm,
-                         NSUB * kTile);
-  return launch_clusters(a.cluster, kern, dim3(a.cluster, a.num_kv_heads, a.num_seqs),
-                         dim3(NW * 32), smem, stream, km, vm, a);
-}
 
+  // CTAs that share a row's tokens: as many as the SMs have room for, while a warp
+  // keeps four steps of the longest table.
+  static int cluster_of(const DecodeArgs &a) {
+    const int64_t ctas = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
+    const int64_t steps = a.max_context_len / kStepTokens;
+    int n = 1;
+    while (n < kMaxCluster && 2 * n * ctas <= kSms * kPerSm && steps >= 4 * n * NW) n *= 2;
+    return n;
+  }
+  static cudaError_t launch(DecodeArgs a, const CUtensorMap &km, const CUtensorMap &vm,
+                            cudaStream_t stream) {
+    auto kern = sparse_decode_kernel<T, D, NW, S, F8, NSUB>;
+    static SmemLimitOnce smem_limit;
+    const cudaError_t e = smem_limit.ensure(kern, kSmem);
+    if (e != cudaSuccess) return e;
+    a.cluster = cluster_of(a);
+    return launch_clusters(a.cluster, kern, dim3(a.cluster, a.num_kv_heads, a.num_seqs),
+                           dim3(NW * 32), kSmem, stream, km, vm, a);
+  }
+};
+
+// Warps of a CTA.  16-bit caches: four where they share a row in clusters (8 rows of
+// 2,048 tokens, 32 / 8 heads x 128: 15.0 us; 16.0 with two), else two, of whose CTAs
+// an SM takes six (64 rows of 512 tokens: 23.1 us; 27.9 with four, whose 512 CTAs
+// are more than the 456 that run at once; 23.6 with three, 24.3 with one).  FP8
+// caches: four (256 rows of up to 1,024 tokens, 64 / 8 heads x 128: 67 us; 72 with
+// two or three, 79 with one, 98 with eight).  Three stages in place of two:
+// 23.5 and 77 us with two warps, 24.8 and 76 with four.
 template <typename T, int D>
 cudaError_t launch_d(const DecodeArgs &a, bool kv_fp8, const CUtensorMap &km,
                      const CUtensorMap &vm, cudaStream_t stream) {
-  // 64 KB of stages a CTA, three CTAs an SM
-  if (kv_fp8) return launch_t<T, D, 4, D == 64 ? 4 : 2, true, 2>(a, km, vm, stream);
-  return launch_t<T, D, 4, 2, false, D == 64 ? 2 : 1>(a, km, vm, stream);
+  using Wide = Instance<T, D, 4, 2, false, D == 64 ? 2 : 1>;
+  using Narrow = Instance<T, D, 2, 2, false, D == 64 ? 2 : 1>;
+  using Fp8 = Instance<T, D, 4, D == 64 ? 4 : 2, true, 2>;
+  if (kv_fp8) return Fp8::launch(a, km, vm, stream);
+  return Wide::cluster_of(a) > 1 ? Wide::launch(a, km, vm, stream)
+                                 : Narrow::launch(a, km, vm, stream);
 }
 
 }  // namespace

@@ -138,10 +138,10 @@ struct RopeArgs {
 };
 
 // Threads (a power of two, at most a CTA of 256) that share a token with `items`
-// items of 16 elements, so that a thread has at most four of them where it can.
+// items of 16 elements, so that a thread has at most three of them where it can.
 inline int rope_group_log2(int items) {
   int g = 5;
-  while (g < 8 && (items >> (g + 2)) > 0) ++g;
+  while (g < 8 && items > 3 << g) ++g;
   return g;
 }
 

@@ -2,6 +2,14 @@
 // tokens' queries and keys, write the queries out and the keys and values to
 // their slots, in one pass over the rows.  (The rotation: pa_rope.cuh; the FP4
 // form: pa_cache_fp4.cu, beside the cache's quantising write.)
+//
+// HBM bounds a prompt's append, latency a step's: a thread waits for its token's
+// slot, position and row of the table and has its items' rows in flight
+// meanwhile.  16,381 tokens x (32 + 2 x 8) heads x 128, fp16: 59.6 us for 386 MB,
+// 0.95 of the copy rate; 256 tokens x (64 + 2 x 8) x 128 into FP8 caches 3.2 us.
+// Three items a thread in flight and four CTAs an SM: with four items and 80
+// registers (three CTAs) the prompt takes 65.0 us, with two items 63.7, with four
+// items and as many registers as they want (90, two CTAs) 80.5.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -17,7 +25,7 @@ namespace {
 constexpr int kThreads = 256;
 
 template <typename T, int D, bool F8>
-__global__ void __launch_bounds__(kThreads) rope_and_cache_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) rope_and_cache_kernel(const RopeArgs a) {
   grid_dependency_wait();    // the rows may come from the kernel before
   grid_launch_dependents();  // the next kernel may start its set-up now
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads >> a.group_log2) +

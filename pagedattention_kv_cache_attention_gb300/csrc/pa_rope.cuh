@@ -106,7 +106,7 @@ template <typename T> __device__ __forceinline__ uint2 quantise8_e4m3(const uint
 template <typename T, int D, bool F8>
 __device__ __forceinline__ void rope_token_heads(const RopeArgs &a, int64_t token, int me,
                                                  int heads) {
-  constexpr int kItems = D / 16, kBatch = 4;
+  constexpr int kItems = D / 16, kBatch = 3;
   const int64_t slot = a.slot_mapping[token], pos = a.positions[token];
   const int u = me % kItems, step = (1 << a.group_log2) / kItems;
   const int hq = a.num_q_heads, hkv = a.num_kv_heads;
