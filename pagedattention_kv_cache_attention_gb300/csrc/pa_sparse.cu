@@ -520,7 +520,7 @@ __device__ __forceinline__ void pick(const uint32_t (&k)[KPL], int n, int forced
 }
 
 template <typename T, int D, int KPL, int TILES, int NW>
-__global__ void __launch_bounds__(NW * 32) select_short_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(NW * 32, KPL == 8 ? 4 : 1) select_short_kernel(const SelectArgs a) {
   using U = Unit<D>;
   constexpr int kRows = 4 * TILES;
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -867,20 +867,26 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_long_kernel(const Selec
   const int step = ctas * kSelWarps * U::kBlocks;
   int j0 = (rank * kSelWarps + warp) * U::kBlocks, e[2];
   table.entries(j0 + g, e);
+  U unit;
+  auto fetch = [&] {
+    const int phys[2] = {Table::block(a, e[0], j0 + g, n), Table::block(a, e[1], j0 + 8 + g, n)};
+    unit.load(a, kvh, phys, c);
+    if (j0 + step < n) table.entries(j0 + step + g, e);
+  };
+  // (four warps make the weights, the others' first loads are under way meanwhile)
   if (warp < 4)
     sh.weights.put(warp == 0 ? static_cast<const T *>(a.query) +
                                    (row * a.num_q_heads + kvh * a.group) * D
                              : nullptr,
                    a.group, warp, lane);
+  else if (j0 < n)
+    fetch();
   __syncthreads();
   if (ctas > 1) cluster_wait();  // the first CTA has started: its shared memory is there
   const uint32_t keys_at = ctas > 1 ? cluster_addr(keys, 0) : 0;
   uint32_t lo = 0xffffffffu, hi = 0;  // of the keys that are not forced
-  for (; j0 < n; j0 += step) {
-    const int phys[2] = {Table::block(a, e[0], j0 + g, n), Table::block(a, e[1], j0 + 8 + g, n)};
-    U unit;
-    unit.load(a, kvh, phys, c);
-    if (j0 + step < n) table.entries(j0 + step + g, e);
+  for (bool there = warp >= 4; j0 < n; j0 += step, there = false) {
+    if (!there) fetch();
     uint32_t key[1][2];
     unit.template keys<1>(&sh.weights, lane, key);
 #pragma unroll
