@@ -441,22 +441,24 @@ struct Table {
 // sequence and one KV head: its warps score 16 blocks at a time for all rows, so
 // that bounds are read once for them; then a warp a row picks, with the row's keys
 // in registers and no barrier.
-// The largest t in [lo, hi] with at_least(t) >= want, where at_least(c) counts the
-// keys >= c, at_least(lo) = count >= want, and no key is above hi; count becomes
+// The largest t in [lo, hi] with at_least(t) >= want, or one with at_least(t) <=
+// enough (>= want) too.  at_least(c) counts the keys >= c, at_least(lo) = count >=
+// want, and no key that can be told from others is above hi; count becomes
 // at_least(t).  Every second guess is where t would lie if the keys were spread
-// evenly, the others halve the range; done early where the count is just `want`
-// (some five guesses among 256 keys, in place of twenty bits one by one).
+// evenly, the others halve the range (some five to nine guesses for exactly `want`
+// of 256 keys, in place of twenty bits one by one).
 template <typename F>
 __device__ __forceinline__ uint32_t threshold(uint32_t lo, uint32_t hi, int &count, int want,
-                                              F &&at_least) {
+                                              int enough, F &&at_least) {
   int above = 0;  // keys > hi
   bool even = true;
-  while (lo != hi && count != want) {
+  while (lo != hi && count > enough) {
     const uint32_t room = hi - lo;  // c - lo is 1 .. room
     uint32_t off = room / 2;
     if (even)
-      off = static_cast<uint32_t>(static_cast<float>(room) * static_cast<float>(count - want) /
-                                  static_cast<float>(count - above));
+      off = static_cast<uint32_t>(static_cast<float>(room) *
+                                  __fdividef(static_cast<float>(count - want),
+                                             static_cast<float>(count - above)));
     even = !even;
     const uint32_t c = lo + 1 + min(off, room - 1);
     const int here = at_least(c);
@@ -492,7 +494,7 @@ __device__ __forceinline__ void pick(const uint32_t (&k)[KPL], int n, int forced
   if (want == forced)
     count = want;
   else
-    t = threshold(lo, hi, count, want, [&](uint32_t c) {
+    t = threshold(lo, hi, count, want, want, [&](uint32_t c) {
       int here = 0;
 #pragma unroll
       for (int i = 0; i < KPL; ++i) here += k[i] >= c ? 1 : 0;
@@ -679,15 +681,15 @@ __device__ __forceinline__ void pick_long(const SelectArgs &a, SelectShared<D> &
   const int forced = a.num_sink + a.num_recent;
   int need = a.num_selected - forced;  // fewer than the keys not forced
   if (ONE && need > 0 && need <= n / L) {
-    // As many whole runs as are wanted: the need-th largest of the runs' largest
-    // keys is a bound that the need-th largest key is not below, and few keys pass
-    // it (of 8,192 in 512 runs some 145 for the 128 largest).  Among these a thread
-    // a key picks.
+    // As many whole runs as are wanted: what `need` of the runs' largest keys reach,
+    // the need-th largest key does, too.  With a bound that half as many more of
+    // them reach some 240 keys of 8,192 in 512 runs are left for the 128 largest;
+    // among these a thread a key picks.
     uint32_t top = lo;
 #pragma unroll
     for (int i = 0; i < L; ++i) top = max(top, k[i] == kForced ? 0 : k[i]);
     int count = n / L;
-    const uint32_t least = threshold(lo, hi, count, need, [&](uint32_t c) {
+    const uint32_t least = threshold(lo, hi, count, need, need + need / 2, [&](uint32_t c) {
       return __syncthreads_count(tid < n / L && top >= c);
     });
     uint32_t mine = 0, all;
@@ -708,7 +710,7 @@ __device__ __forceinline__ void pick_long(const SelectArgs &a, SelectShared<D> &
       const bool real = tid < static_cast<int>(all);
       const uint32_t x = real ? sh.few_keys[tid] : 0;
       count = all;
-      const uint32_t t = threshold(least, hi, count, a.num_selected, [&](uint32_t c) {
+      const uint32_t t = threshold(least, hi, count, a.num_selected, a.num_selected, [&](uint32_t c) {
         return __syncthreads_count(real && x >= c);
       });
       // keys above t are taken, and of those equal to it the first
@@ -721,6 +723,7 @@ __device__ __forceinline__ void pick_long(const SelectArgs &a, SelectShared<D> &
       __syncthreads();
       return;
     }
+    lo = least;  // the general way
     __syncthreads();
   }
   bool whole = need == 0;  // every key of [lo, hi] is taken
