@@ -580,10 +580,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
+# (asked only where a CUDA tensor is at hand, so CUDA is initialised)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _device_of(name: str, t) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     if t.get_device() != dev:
         _cuda(name, t)
     return dev

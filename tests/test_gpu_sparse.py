@@ -132,6 +132,22 @@ def test_bounds_of_odd_values(pa, dtype, d):  # noqa: F811
     assert np.isinf(s[13:16]).all() and (s[:2] == 0).all()
 
 
+@pytest.mark.parametrize("kv", ["fp8", "fp4"])
+def test_bounds_of_nan_codes(pa, kv):  # noqa: F811
+    """A NaN among a block's tokens gives the infinite scale; past the context it does not count."""
+    b = Batch(50, [20, 20, 20], 2, 1, 64, 16, "fp16", kv)
+    x = b.rng.standard_normal((b.NB, 2, 16, 64))
+    x[b.tables[0, 1], 0, 3, 40] = math.nan   # token 19 of sequence 0: the newest
+    x[b.tables[1, 1], 1, 4:, :] = math.nan   # past sequence 1's context
+    b.kc, b.kvals = pool(b.rng, x, kv, "fp16", 16, 64)
+    want, s = np.zeros_like(b.bounds), np.zeros_like(b.scales)
+    S.update_bounds(want, s, b.kvals, b.tables, b.lens, [1, 1, 1])
+    gb, gs = pa.new_key_bounds(b.NB, 2, 64)
+    getattr(pa, "pa_update_key_bounds" + END[kv])(gb, gs, b.kc, dev(b.tables), dev(b.lens))
+    assert np.array_equal(gb.cpu().numpy(), want) and np.array_equal(gs.cpu().numpy(), s)
+    assert np.isinf(s[b.tables[0, 1], 0]) and np.isfinite(s[b.tables[1, 1]]).all()
+
+
 def test_bounds_of_bad_lengths_and_blocks(pa):  # noqa: F811
     b = Batch(3, [40, 20, 33, 7], 2, 1, 64, 16, "fp16", q_lens=[3, 3, 3, 3])
     want, s = np.zeros_like(b.bounds), np.zeros_like(b.scales)
@@ -195,6 +211,27 @@ def test_select_of_long_contexts(pa, lens, keep, bs, d):  # noqa: F811
     t, n = b.select(pa, keep, 1, 1)
     wt, wn = b.want(keep, 1, 1)
     assert np.array_equal(t, wt) and np.array_equal(n, wn)
+
+
+@pytest.mark.parametrize("n,keep", [(3000, 600), (2000, 700), (8192, 128), (8192, 500), (5000, 90), (1500, 1499)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_select_where_large_scores_are_neighbours(pa, n, keep, d):  # noqa: F811
+    """Runs of blocks with nearly the same large scores, among many that are small or
+    negative, and more blocks wanted than there are runs."""
+    b = Batch(41, [16 * 3] * 3, 2, 2, d, 16, "bf16", extra=n)
+    b.bounds = b.rng.integers(-20, 21, b.bounds.shape).astype(np.int8)
+    b.bounds[:, :, 1] = np.minimum(b.bounds[:, :, 0], b.bounds[:, :, 1])
+    b.scales[:] = 2.0 ** -4
+    b.tables = np.stack([b.rng.permutation(b.NB)[:n] for _ in range(3)]).astype(np.int32)
+    b.lens = b.seen = np.full(3, 16 * n - 5, np.int32)
+    for r in range(3):
+        for at in (0, n // 3, n - 300 if n > 1800 else n // 2):
+            b.bounds[b.tables[r, at:at + 250], :, 0] = np.clip(
+                b.bounds[b.tables[r, at:at + 250], :, 0].astype(int) + 100, -127, 127)
+    for sink, recent in ((0, 0), (3, 5)):
+        t, m = b.select(pa, keep, sink, recent)
+        wt, wm = b.want(keep, sink, recent)
+        assert np.array_equal(t, wt) and np.array_equal(m, wm)
 
 
 @pytest.mark.parametrize("blocks,keep", [(49152, 300), (49151, 49000), (700, 699), (257, 8)])
@@ -535,6 +572,41 @@ def test_all_blocks_kept_is_dense_decode(pa):  # noqa: F811
         pair = () if kv == "16" else (1.0, 1.0)
         getattr(pa, "pa_decode" + END[kv])(dense, b.q.cuda(), b.kc, vc, dev(b.tables), dev(b.lens), 0.09, *pair, 2000)
         check(b, dense, vvals, t, n, 0.09, 1.0, 1.0)
+
+
+def test_offsets_past_32_bits(pa):  # noqa: F811
+    """The last blocks of a pool of more than 2^31 elements a cache, through all calls."""
+    H, bs, d, NB = 8, 32, 128, (1 << 31) // (8 * 32 * 128) + 9
+    kc, vc = (torch.empty(NB, H, bs, d, dtype=torch.float16, device="cuda") for _ in range(2))
+    gb, gs = pa.new_key_bounds(NB, H, d)
+    rng = np.random.default_rng(60)
+    ids = np.array([NB - 1, 0, NB - 2, 3, NB - 5, NB - 7], np.int32)
+    n = 6 * bs - 7
+    j = np.arange(n)
+    slots = ids[j // bs].astype(np.int64) * bs + j % bs
+    q, k, v = (torch.from_numpy(rng.standard_normal((n, h, d))).half() for h in (2 * H, H, H))
+    table = pa.new_rope_table(n, d)
+    out = torch.zeros_like(q, device="cuda")
+    pa.pa_rope_and_cache(out, q.cuda(), k.cuda(), v.cuda(), kc, vc, dev(slots), dev(j.astype(np.int64)), table)
+    tables, lens, start = ids[None], np.array([n], np.int32), np.array([0, n], np.int32)
+    pa.pa_update_key_bounds(gb, gs, kc, dev(tables), dev(lens), dev(start), n)
+    at = torch.from_numpy(ids.astype(np.int64)).cuda()
+    keys, vals = f64(kc[at]), f64(vc[at])
+    bounds, scales = np.zeros((6, H, 2, d), np.int8), np.zeros((6, H), np.float32)
+    small = np.arange(6, dtype=np.int32)[None]
+    S.update_bounds(bounds, scales, keys, small, lens, [n])
+    assert np.array_equal(gb[at].cpu().numpy(), bounds) and np.array_equal(gs[at].cpu().numpy(), scales)
+    last = out[-1:].contiguous()
+    t = torch.zeros(1, H, 3, dtype=torch.int32, device="cuda")
+    m = torch.zeros(1, H, dtype=torch.int32, device="cuda")
+    pa.pa_select_blocks(t, m, last, gb, gs, dev(tables), dev(lens), bs, n)
+    wt, wm = S.select(f64(last), bounds, scales, small, [0], [n], bs, 3, 1, 1)
+    assert np.array_equal(t.cpu().numpy(), ids[wt]) and np.array_equal(m.cpu().numpy(), wm)
+    o = torch.zeros_like(last)
+    pa.pa_decode_sparse(o, last, kc, vc, t, m, 0.08)
+    ref, mag = S.attend(f64(last), keys, vals, wt, wm, 0.08)
+    assert (np.abs(f64(o) - ref) <= mag * (2.0 ** -11 + 2.0 ** -14) + np.abs(ref) * 2.0 ** -11 + 2.0 ** -24).all()
+    assert pa.pa_device_errors() == 0
 
 
 def test_refused_arguments(pa):  # noqa: F811
