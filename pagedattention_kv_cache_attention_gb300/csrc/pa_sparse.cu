@@ -285,7 +285,7 @@ struct SelectRows {
 // (By integer dot products a row takes 64 of them for 16 blocks, at half rate, and
 // sums over lanes; the codes' three instructions for 4 of them here are shared by
 // the rows.  5 drafted tokens of 64 sequences, contexts of 512 to 4,096, 32 / 8
-// heads: PLACE_DRAFT.)
+// heads: 12.7 us, by dot products 16.8.)
 //
 // The order of the 2 D codes in the product is one that lets a lane take 16
 // consecutive codes of a block: code 64 i + 16 c + 4 w + e is column c's e-th of
@@ -594,22 +594,27 @@ __global__ void __launch_bounds__(NW * 32, KPL == 8 ? 4 : 1) select_short_kernel
 }
 
 // Long contexts: the CTAs of a cluster score a share of a row's blocks each, into
-// the keys of the first one, which then picks.
-constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+// the keys of the first one, which then picks.  What bounds it: HBM while blocks are
+// scored (8 contexts of 32,768 to 131,072 tokens, 32 / 8 heads x 128: 51 MB, 9 to 10
+// of 21 us), and the chain of latencies around that: the length, the queries'
+// weights and the cluster's start 3 us, the pick 4 us in some 15 barriers.
 constexpr int kBins = 2048, kBinBits = 11;
+constexpr int kMaxSelCluster = 8;
+constexpr int kRunKeys = 16;  // keys that a thread holds in registers at most
 
 // Shared memory of a CTA, before the keys.
-template <int D> struct SelectShared {
+template <int D, int NT> struct SelectShared {
   Weights<D> weights;
   uint32_t bins[kBins];
-  uint32_t part[kSelWarps];
+  uint32_t part[NT / 32];
   uint32_t lo, hi;  // of the keys that are not forced
   uint32_t chosen_bin, chosen_above, chosen_count;
   uint32_t few[32], few_count;
-  uint32_t few_keys[kSelThreads], few_at[kSelThreads];  // keys that may be taken, and where they are
+  uint32_t few_keys[NT], few_at[NT];  // keys that may be taken, and where they are
 };
 
 // Sum over the CTA's threads before this one; `all`: over all of them.
+template <int NT>
 __device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t *part, uint32_t &all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t incl = v;
@@ -623,7 +628,7 @@ __device__ __forceinline__ uint32_t sum_before(uint32_t v, uint32_t *part, uint3
   uint32_t before = 0;
   all = 0;
 #pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) {
+  for (int w = 0; w < NT / 32; ++w) {
     const uint32_t x = part[w];
     before += w < warp ? x : 0;
     all += x;
@@ -650,12 +655,12 @@ __device__ __forceinline__ void red_cluster_max(uint32_t addr, uint32_t v) {
 // The K largest of n > K keys, ties to the first; the keys' indexes take their
 // places in order from keys[0] on.  For a whole CTA.  In a turn thread i takes
 // keys L i .. L i + L - 1, from one of its own on around (different lanes,
-// different banks).  ONE: one turn does (n <= 512 L), the keys stay in registers.
-template <int D, int L, bool ONE>
-__device__ __forceinline__ void pick_long(const SelectArgs &a, SelectShared<D> &sh, uint32_t *keys,
+// different banks).  ONE: one turn does (n <= NT L), the keys stay in registers.
+template <int D, int NT, int L, bool ONE>
+__device__ __forceinline__ void pick_long(const SelectArgs &a, SelectShared<D, NT> &sh, uint32_t *keys,
                                           int n) {
   const int tid = threadIdx.x, lane = tid & 31;
-  constexpr int kTurn = kSelThreads * L;
+  constexpr int kTurn = NT * L;
   const int first = lane * L / 32;
   uint32_t k[L];  // k[i] is key (first + i) % L of the run; 0 past n
   auto load = [&](int j0) {
@@ -684,7 +689,8 @@ __device__ __forceinline__ void pick_long(const SelectArgs &a, SelectShared<D> &
     // As many whole runs as are wanted: what `need` of the runs' largest keys reach,
     // the need-th largest key does, too.  With a bound that half as many more of
     // them reach some 240 keys of 8,192 in 512 runs are left for the 128 largest;
-    // among these a thread a key picks.
+    // among these a thread a key picks.  (Cutting the whole range instead, as below:
+    // 4.8 us for 8,192 keys in 256 runs, against 4.)
     uint32_t top = lo;
 #pragma unroll
     for (int i = 0; i < L; ++i) top = max(top, k[i] == kForced ? 0 : k[i]);
@@ -698,8 +704,8 @@ __device__ __forceinline__ void pick_long(const SelectArgs &a, SelectShared<D> &
       const int at = (first + i) & (L - 1);
       mine |= (tid * L + at < n && k[i] >= least ? 1u : 0u) << at;
     }
-    int place = sum_before(__popc(mine), sh.part, all);
-    if (all <= kSelThreads) {
+    int place = sum_before<NT>(__popc(mine), sh.part, all);
+    if (all <= NT) {
       while (mine) {
         const int i = __ffs(mine) - 1;
         mine &= mine - 1;
@@ -716,7 +722,7 @@ __device__ __forceinline__ void pick_long(const SelectArgs &a, SelectShared<D> &
       // keys above t are taken, and of those equal to it the first
       const bool eq = real && x == t;
       const int left = a.num_selected - __syncthreads_count(real && x > t);
-      const uint32_t before = sum_before((real && x > t ? 1u : 0u) | (eq ? 0x10000u : 0u), sh.part, all);
+      const uint32_t before = sum_before<NT>((real && x > t ? 1u : 0u) | (eq ? 0x10000u : 0u), sh.part, all);
       const int ties = before >> 16;
       if ((real && x > t) || (eq && ties < left))
         keys[(before & 0xffff) + min(ties, left)] = sh.few_at[tid];
@@ -734,7 +740,7 @@ __device__ __forceinline__ void pick_long(const SelectArgs &a, SelectShared<D> &
   while (!whole && lo != hi) {
     const int shift = max(0, 32 - __clz(hi - lo) - kBinBits);
 #pragma unroll
-    for (int i = 0; i < kBins; i += kSelThreads) sh.bins[i + tid] = 0;
+    for (int i = 0; i < kBins; i += NT) sh.bins[i + tid] = 0;
     if (tid == 0) sh.few_count = 0;
     __syncthreads();
     turns([&] {
@@ -745,14 +751,14 @@ __device__ __forceinline__ void pick_long(const SelectArgs &a, SelectShared<D> &
     __syncthreads();
     // the part with the need-th largest key: sums over the parts from the top;
     // thread i holds some parts, from part kBins - 1 - kPer i down
-    constexpr int kPer = kBins / kSelThreads;
+    constexpr int kPer = kBins / NT;
     uint32_t mine[kPer], sum = 0, all;
 #pragma unroll
     for (int b = 0; b < kPer; ++b) {
       mine[b] = sh.bins[kBins - 1 - tid * kPer - b];
       sum += mine[b];
     }
-    uint32_t before = sum_before(sum, sh.part, all);
+    uint32_t before = sum_before<NT>(sum, sh.part, all);
 #pragma unroll
     for (int b = 0; b < kPer; ++b) {
       if (before < static_cast<uint32_t>(need) && before + mine[b] >= static_cast<uint32_t>(need)) {
@@ -804,7 +810,7 @@ __device__ __forceinline__ void pick_long(const SelectArgs &a, SelectShared<D> &
     }
     uint32_t all;
     __syncthreads();  // sh.part is free
-    const uint32_t before = sum_before(__popc(above) | (__popc(equal) << 16), sh.part, all);
+    const uint32_t before = sum_before<NT>(__popc(above) | (__popc(equal) << 16), sh.part, all);
     const int ties = before >> 16;
     int place = place0 + static_cast<int>(before & 0xffff) + min(ties, need);
     int left = max(0, need - ties);
@@ -825,12 +831,12 @@ __device__ __forceinline__ void pick_long(const SelectArgs &a, SelectShared<D> &
   __syncthreads();
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kSelThreads, 2) select_long_kernel(const SelectArgs a) {
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) select_long_kernel(const SelectArgs a) {
   using U = Unit<D>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  SelectShared<D> &sh = *reinterpret_cast<SelectShared<D> *>(smem_raw);
-  uint32_t *keys = reinterpret_cast<uint32_t *>(smem_raw + sizeof(SelectShared<D>));
+  SelectShared<D, NT> &sh = *reinterpret_cast<SelectShared<D, NT> *>(smem_raw);
+  uint32_t *keys = reinterpret_cast<uint32_t *>(smem_raw + sizeof(SelectShared<D, NT>));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   const int rank = static_cast<int>(blockIdx.x) % a.cluster;
@@ -854,7 +860,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_long_kernel(const Selec
   int32_t *out_len = a.lens + row * a.num_kv_heads + kvh;
   if (n <= K) {  // all of them
     if (rank == 0) {
-      for (int i = tid; i < K; i += kSelThreads) out[i] = i < n ? bt_row[i] : -1;
+      for (int i = tid; i < K; i += NT) out[i] = i < n ? bt_row[i] : -1;
       if (tid == 0) *out_len = seen;
     }
     return;  // (the whole cluster)
@@ -867,8 +873,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_long_kernel(const Selec
   if (ctas > 1) cluster_arrive();
   // the warp's units, `step` blocks apart; the next one's entries are read while one
   // is worked on
-  const int step = ctas * kSelWarps * U::kBlocks;
-  int j0 = (rank * kSelWarps + warp) * U::kBlocks, e[2];
+  const int step = ctas * (NT / 32) * U::kBlocks;
+  int j0 = (rank * (NT / 32) + warp) * U::kBlocks, e[2];
   table.entries(j0 + g, e);
   U unit;
   auto fetch = [&] {
@@ -923,32 +929,45 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_long_kernel(const Selec
   }
   if (ctas > 1) cluster_sync(); else __syncthreads();
   if (rank != 0) return;
-  if (n <= kSelThreads * 4)
-    pick_long<D, 4, true>(a, sh, keys, n);
-  else if (n <= kSelThreads * 16)
-    pick_long<D, 16, true>(a, sh, keys, n);
+  if (n <= NT * 4)
+    pick_long<D, NT, 4, true>(a, sh, keys, n);
+  else if (n <= NT * kRunKeys)
+    pick_long<D, NT, kRunKeys, true>(a, sh, keys, n);
   else
-    pick_long<D, 16, false>(a, sh, keys, n);
-  for (int i = tid; i < K; i += kSelThreads) out[i] = bt_row[keys[i]];
+    pick_long<D, NT, kRunKeys, false>(a, sh, keys, n);
+  for (int i = tid; i < K; i += NT) out[i] = bt_row[keys[i]];
   if (tid == 0) *out_len = K * bs - (keys[K - 1] == static_cast<uint32_t>(n - 1) ? n * bs - seen : 0);
 }
 
-template <typename T, int D> cudaError_t launch_long(SelectArgs a, cudaStream_t stream) {
-  const size_t smem = sizeof(SelectShared<D>) + static_cast<size_t>(a.max_candidates) * 4;
-  constexpr size_t most = sizeof(SelectShared<D>) + kMaxCandidates * 4;
+template <typename T, int D, int NT> cudaError_t launch_long(SelectArgs a, cudaStream_t stream) {
+  const size_t smem = sizeof(SelectShared<D, NT>) + static_cast<size_t>(a.max_candidates) * 4;
+  constexpr size_t most = sizeof(SelectShared<D, NT>) + kMaxCandidates * 4;
   static_assert(most <= 227 * 1024, "shared memory");
-  auto kern = select_long_kernel<T, D>;
+  auto kern = select_long_kernel<T, D, NT>;
   static SmemLimitOnce smem_limit;
   const cudaError_t e = smem_limit.ensure(kern, most);
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * a.max_q_len;
+  // CTAs that may share a row: as many as run at once (2 kSms), each with 128 blocks
+  // at least; twice as many where each has 512, since those of the shorter
+  // contexts then leave at once.  (32 / 8 heads x 128, one row a sequence, in all
+  // that this gives and in one: 1 x 16,000 tokens 6.7 and 12.2 us, 16 x 1,000 to
+  // 16,000 10.8 and 12.7, 16 x 16,000 to 65,000 25.9 and 44.9; with twice as many
+  // from 128 blocks on 8 x 16,000 take 16.9 us in place of 9.0, with only as many
+  // as run at once 16 x 16,000 to 65,000 take 30.8 in place of 25.9.)
   a.cluster = 1;
-  while (a.cluster < 8 && 2 * a.cluster * rows <= 4 * kSms && a.max_candidates >= 512 * a.cluster)
-    a.cluster *= 2;
-  a.units_per_cta = kSelWarps * (a.cluster * rows <= 2 * kSms ? 1 : 4);
+  for (int c = 1; c < kMaxSelCluster; c *= 2) {
+    const int64_t ctas = 2 * c * rows;
+    if (!(ctas <= 2 * kSms && a.max_candidates >= 128 * c) &&
+        !(ctas <= 4 * kSms && a.max_candidates >= 512 * c))
+      break;
+    a.cluster = 2 * c;
+  }
+  // where they are more than run at once, four units a warp
+  a.units_per_cta = NT / 32 * (a.cluster * rows <= 2 * kSms ? 1 : 4);
   return launch_clusters(a.cluster, kern,
                          dim3(static_cast<unsigned>(a.cluster * a.max_q_len), a.num_seqs, a.num_kv_heads),
-                         dim3(kSelThreads), smem, stream, a);
+                         dim3(NT), smem, stream, a);
 }
 
 template <typename T, int D, int KPL, int TILES, int NW>
@@ -964,8 +983,18 @@ cudaError_t launch_short(const SelectArgs &a, cudaStream_t stream) {
                           dim3(tiles, a.num_kv_heads, a.num_seqs), dim3(NW * 32), smem, stream, a);
 }
 
+// Which kernel (32 / 8 heads x 128, GPU time of a call).  Up to 256 candidates the
+// short one: 64 x 512 to 4,096 tokens 10.0 us (long, 256 threads: 10.7), 5 drafted
+// rows each 12.8 (35.7).  Up to 1,024 it keeps the calls with several rows a
+// sequence, for which it reads the bounds once: 64 x 5 rows, 2,000 to 8,000 tokens,
+// 32 us (53); single rows take the long one: 64 x 2,000 to 8,000 16.4 us (21.5),
+// 256 of them 45 (55).  That one has 256 threads, four CTAs an SM, while their
+// registers hold the keys of the longest context, and else 512: 64 x 2,000 to 8,000
+// tokens 16.4 us (22.8), 200 x 8,000 to 30,000 96 (113); 131,072 tokens 12.6 us
+// with 512 and 15.7 with 256, 4 x 5 rows of up to 131,072 51 and 76.
 template <typename T, int D> cudaError_t launch_select_t(const SelectArgs &a, cudaStream_t stream) {
-  if (a.max_candidates > 1024) return launch_long<T, D>(a, stream);
+  if (a.max_candidates > 256 * kRunKeys) return launch_long<T, D, 512>(a, stream);
+  if (a.max_candidates > (a.max_q_len > 1 ? 1024 : 256)) return launch_long<T, D, 256>(a, stream);
   if (a.max_q_len > 4)
     return a.max_candidates > 256 ? launch_short<T, D, 32, 2, 8>(a, stream)
                                   : launch_short<T, D, 8, 2, 8>(a, stream);
