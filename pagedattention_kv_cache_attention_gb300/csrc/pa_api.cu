@@ -1026,9 +1026,7 @@ pa_status pa_select_blocks(int32_t *selected_tables, int32_t *selected_lens, con
     return PA_ERR_INVALID_ARG;
   if (!pool_ok(num_blocks, num_kv_heads, block_size) || num_seqs > 65535 || num_kv_heads > 65535)
     return PA_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(num_selected) * block_size > 0x7fffffff ||
-      max_q_len > 0x7fffffff / 8)
-    return PA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_selected) * block_size > 0x7fffffff) return PA_ERR_UNSUPPORTED;
   const int64_t most = std::min<int64_t>(
       (static_cast<int64_t>(max_context_len) + block_size - 1) / block_size, max_blocks_per_seq);
   if (most > pa::kMaxCandidates) return PA_ERR_UNSUPPORTED;
@@ -1045,7 +1043,8 @@ pa_status pa_select_blocks(int32_t *selected_tables, int32_t *selected_lens, con
   a.query_start = query_start;
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.num_seqs = num_seqs;
-  a.max_q_len = max_q_len;
+  // (no sequence has more rows than tokens)
+  a.max_q_len = static_cast<int32_t>(std::min<int64_t>(max_q_len, std::max<int64_t>(most, 1) * block_size));
   a.num_q_heads = num_q_heads;
   a.num_kv_heads = num_kv_heads;
   a.group = group;

@@ -279,6 +279,20 @@ struct SelectRows {
   }
 };
 
+// A row's group of queries, in one warp: lane l holds channels D / 32 l .. of all heads.
+template <typename T, int D> struct Queries {
+  static constexpr int kPer = D / 32;
+  uint32_t w[8][kPer / 2];
+  __device__ __forceinline__ void load(const SelectArgs &a, int64_t row, int kvh, int lane) {
+    const T *q = static_cast<const T *>(a.query) + (row * a.num_q_heads + kvh * a.group) * D + lane * kPer;
+#pragma unroll
+    for (int h = 0; h < 8; ++h)
+#pragma unroll
+      for (int i = 0; i < kPer / 2; ++i)
+        w[h][i] = h < a.group ? reinterpret_cast<const uint32_t *>(q + h * D)[i] : 0;
+  }
+};
+
 // I of 16 blocks and up to 4 rows is a product on the tensor cores: the blocks'
 // codes as fp16 integers times 2^-24 (a byte in the low bits of a half is that
 // subnormal number; with 128 added codes are unsigned), the weights P and N of a
@@ -298,43 +312,35 @@ template <int D> struct Weights {
   uint2 frag[kSteps][32];  // the B operand of a step in each lane: columns 2 r, 2 r + 1 are row r's
   int bias[4];             // 128 times the sum of a row's weights
 
-  // Row r of the tile, from the row's group of queries; nullptr: zeros.  For a
-  // whole warp; a lane takes D / 32 channels of all heads.
+  // Row r of the tile, from its group of queries (nullptr: zeros).  For a whole warp.
   template <typename T>
-  __device__ __forceinline__ void put(const T *q, int group, int r, int lane) {
+  __device__ __forceinline__ void put(const Queries<T, D> *q, int r, int lane) {
     constexpr int kPer = D / 32;
     int p[kPer], m[kPer], sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) p[i] = m[i] = 0;
     if (q) {
-      float x[8][kPer];
       uint32_t top = 0;  // magnitudes are ordered like their bits; a NaN is above infinity
 #pragma unroll
-      for (int h = 0; h < 8; ++h) {
-        if (h >= group) break;
+      for (int h = 0; h < 8; ++h)
 #pragma unroll
-        for (int i = 0; i < kPer; i += 2) {
-          const float2 v = Elem<T>::unpack(
-              *reinterpret_cast<const uint32_t *>(q + h * D + lane * kPer + i));
-          x[h][i] = v.x;
-          x[h][i + 1] = v.y;
+        for (int i = 0; i < kPer / 2; ++i) {
+          const float2 v = Elem<T>::unpack(q->w[h][i]);
           top = max(top, max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y))));
         }
-      }
       top = __reduce_max_sync(kAll, top);
       if (top > 0 && top < 0x7f800000u) {
         const float inv = pow2(-exponent_for(__uint_as_float(top), 12));
 #pragma unroll
-        for (int h = 0; h < 8; ++h) {
-          if (h >= group) break;
+        for (int h = 0; h < 8; ++h)
 #pragma unroll
           for (int i = 0; i < kPer; ++i) {
-            const int c = __float2int_rn(x[h][i] * inv);
+            const float2 v = Elem<T>::unpack(q->w[h][i / 2]);
+            const int c = __float2int_rn((i & 1 ? v.y : v.x) * inv);
             p[i] += max(c, 0);
             m[i] += min(c, 0);
             sum += c;
           }
-        }
       }
     }
     sum = __reduce_add_sync(kAll, sum);
@@ -440,10 +446,6 @@ struct Table {
   }
 };
 
-// Short contexts: at most 32 KPL blocks.  A CTA takes up to 4 TILES rows of a
-// sequence and one KV head: its warps score 16 blocks at a time for all rows, so
-// that bounds are read once for them; then a warp a row picks, with the row's keys
-// in registers and no barrier.
 // The largest t in [lo, hi] with at_least(t) >= want, or one with at_least(t) <=
 // enough (>= want) too.  at_least(c) counts the keys >= c, at_least(lo) = count >=
 // want, and no key that can be told from others is above hi; count becomes
@@ -524,6 +526,10 @@ __device__ __forceinline__ void pick(const uint32_t (&k)[KPL], int n, int forced
   }
 }
 
+// Short contexts: at most 32 KPL blocks.  A CTA takes up to 4 TILES rows of a
+// sequence and one KV head: its warps score 16 blocks at a time for all rows, so
+// that bounds are read once for them; then a warp a row picks, with the row's keys
+// in registers and no barrier.
 template <typename T, int D, int KPL, int TILES, int NW>
 __global__ void __launch_bounds__(NW * 32, KPL == 8 ? 4 : 1) select_short_kernel(const SelectArgs a) {
   using U = Unit<D>;
@@ -542,17 +548,19 @@ __global__ void __launch_bounds__(NW * 32, KPL == 8 ? 4 : 1) select_short_kernel
   const int32_t *bt_row = table.row;
   int j0 = warp * U::kBlocks, e[2];
   table.entries(j0 + g, e);
+  Queries<T, D> q;  // (a row of its own needs no length to be found)
+  if (!a.query_start && warp == 0) q.load(a, seq, kvh, lane);
   SelectRows rows;
   if (!rows.load(a, seq, tid == 0 && blockIdx.x == 0 && kvh == 0)) return;
   const int t0 = blockIdx.x * kRows, count = min(kRows, rows.rows - t0);
   if (count <= 0) return;
   const int most = (rows.base + t0 + count - 1 + bs - 1) >> a.bs_log2;  // blocks of the last row
   if (most > K) {
-    for (int r = warp; r < kRows; r += NW)
-      weights[r / 4].put(r < count ? static_cast<const T *>(a.query) +
-                                         ((rows.row0 + t0 + r) * a.num_q_heads + kvh * a.group) * D
-                                   : nullptr,
-                         a.group, r % 4, lane);
+    static_assert(kRows <= NW, "a warp a row");
+    if (warp < kRows) {
+      if (a.query_start && warp < count) q.load(a, rows.row0 + t0 + warp, kvh, lane);
+      weights[warp / 4].put(warp < count ? &q : nullptr, warp % 4, lane);
+    }
     __syncthreads();
     for (; j0 < most; j0 += NW * U::kBlocks) {
       const int phys[2] = {Table::block(a, e[0], j0 + g, most), Table::block(a, e[1], j0 + 8 + g, most)};
@@ -854,6 +862,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_long_kernel(const Select
 
   const Table table(a, seq);
   const int32_t *bt_row = table.row;
+  Queries<T, D> q;  // (a row of its own needs no length to be found)
+  if (!a.query_start && warp == 0) q.load(a, seq, kvh, lane);
   SelectRows rows;
   if (!rows.load(a, seq, tid == 0 && blockIdx.x == 0 && kvh == 0) || t >= rows.rows)
     return;  // (the whole cluster)
@@ -886,13 +896,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_long_kernel(const Select
     if (j0 + step < n) table.entries(j0 + step + g, e);
   };
   // (four warps make the weights, the others' first loads are under way meanwhile)
-  if (warp < 4)
-    sh.weights.put(warp == 0 ? static_cast<const T *>(a.query) +
-                                   (row * a.num_q_heads + kvh * a.group) * D
-                             : nullptr,
-                   a.group, warp, lane);
-  else if (j0 < n)
+  if (warp < 4) {
+    if (a.query_start && warp == 0) q.load(a, row, kvh, lane);
+    sh.weights.put(warp == 0 ? &q : nullptr, warp, lane);
+  } else if (j0 < n) {
     fetch();
+  }
   __syncthreads();
   if (ctas > 1) cluster_wait();  // the first CTA has started: its shared memory is there
   const uint32_t keys_at = ctas > 1 ? cluster_addr(keys, 0) : 0;

@@ -199,6 +199,9 @@ def test_select_for_chunks(pa, keep, sink, recent, G, dtype):  # noqa: F811
     t, n = b.select(pa, keep, sink, recent, q=q, most=1 << 18)
     assert np.array_equal(t[:-3], wt) and np.array_equal(n[:-3], wn)
     assert (t[-3:] == 77).all() and (n[-3:] == 77).all()
+    b.q_lens[4] = 2 ** 31 - 1  # a bound far above what any context holds
+    t, n = b.select(pa, keep, sink, recent, q=q)
+    assert np.array_equal(t[:-3], wt) and np.array_equal(n[:-3], wn)
     assert pa.pa_device_errors() == 0
 
 
