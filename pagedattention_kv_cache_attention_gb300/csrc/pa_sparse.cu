@@ -302,7 +302,7 @@ template <typename T, int D> struct Queries {
 // (By integer dot products a row takes 64 of them for 16 blocks, at half rate, and
 // sums over lanes; the codes' three instructions for 4 of them here are shared by
 // the rows.  5 drafted tokens of 64 sequences, contexts of 512 to 4,096, 32 / 8
-// heads: 12.7 us, by dot products 16.8.)
+// heads: 12.4 us, by dot products 16.8.)
 //
 // The order of the 2 D codes in the product is one that lets a lane take 16
 // consecutive codes of a block: code 64 i + 16 c + 4 w + e is column c's e-th of
@@ -607,8 +607,8 @@ __global__ void __launch_bounds__(NW * 32, KPL == 8 ? 4 : 1) select_short_kernel
 // Long contexts: the CTAs of a cluster score a share of a row's blocks each, into
 // the keys of the first one, which then picks.  What bounds it: HBM while blocks are
 // scored (8 contexts of 32,768 to 131,072 tokens, 32 / 8 heads x 128: 51 MB, 9 to 10
-// of 21 us), and the chain of latencies around that: the length, the queries'
-// weights and the cluster's start 3 us, the pick 4 us in some 15 barriers.
+// of 20.7 us), and the chain of latencies around that: the length, the queries'
+// weights and the cluster's start 2.5 us, the pick 4 us in some 15 barriers.
 constexpr int kBins = 2048, kBinBits = 11;
 constexpr int kMaxSelCluster = 8;
 constexpr int kRunKeys = 16;  // keys that a thread holds in registers at most
@@ -962,11 +962,11 @@ template <typename T, int D, int NT> cudaError_t launch_long(SelectArgs a, cudaS
   const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * a.max_q_len;
   // CTAs that may share a row: as many as run at once (2 kSms), each with 128 blocks
   // at least; twice as many where each has 512, since those of the shorter
-  // contexts then leave at once.  (32 / 8 heads x 128, one row a sequence, in all
-  // that this gives and in one: 1 x 16,000 tokens 6.7 and 12.2 us, 16 x 1,000 to
-  // 16,000 10.8 and 12.7, 16 x 16,000 to 65,000 25.9 and 44.9; with twice as many
-  // from 128 blocks on 8 x 16,000 take 16.9 us in place of 9.0, with only as many
-  // as run at once 16 x 16,000 to 65,000 take 30.8 in place of 25.9.)
+  // contexts then leave at once.  (32 / 8 heads x 128, one row a sequence, with this
+  // rule and with one CTA: 16,000 tokens 6.2 and 11.5 us, 131,072 tokens 12.2 and 44,
+  // 16 x 1,000 to 16,000 10.3 and 12.0, 16 x 16,000 to 65,000 25.4 and 43.6; with twice
+  // as many from 128 blocks on 8 x 16,000 take 16.3 us in place of 8.5, with only as
+  // many as run at once 16 x 16,000 to 65,000 29.8 in place of 25.4.)
   a.cluster = 1;
   for (int c = 1; c < kMaxSelCluster; c *= 2) {
     const int64_t ctas = 2 * c * rows;
@@ -996,14 +996,15 @@ cudaError_t launch_short(const SelectArgs &a, cudaStream_t stream) {
 }
 
 // Which kernel (32 / 8 heads x 128, GPU time of a call).  Up to 256 candidates the
-// short one: 64 x 512 to 4,096 tokens 10.0 us (long, 256 threads: 10.7), 5 drafted
-// rows each 12.8 (35.7).  Up to 1,024 it keeps the calls with several rows a
+// short one: 64 x 512 to 4,096 tokens 9.5 us (long, 256 threads: 10.2), 5 drafted
+// rows each 12.6 (34.5).  Up to 1,024 it keeps the calls with several rows a
 // sequence, for which it reads the bounds once: 64 x 5 rows, 2,000 to 8,000 tokens,
-// 32 us (53); single rows take the long one: 64 x 2,000 to 8,000 16.4 us (21.5),
-// 256 of them 45 (55).  That one has 256 threads, four CTAs an SM, while their
-// registers hold the keys of the longest context, and else 512: 64 x 2,000 to 8,000
-// tokens 16.4 us (22.8), 200 x 8,000 to 30,000 96 (113); 131,072 tokens 12.6 us
-// with 512 and 15.7 with 256, 4 x 5 rows of up to 131,072 51 and 76.
+// 29 us (49); single rows take the long one: 64 x 2,000 to 8,000 15.3 us (20.6),
+// 256 of them 44 (56), one of 16,000 6.2 (20.9).  That one has 256 threads, four CTAs
+// an SM, while their registers hold the keys of the longest context, and else 512:
+// 64 x 2,000 to 8,000 tokens 15.3 us (512: 20.6), 200 x 8,000 to 30,000 95 (106);
+// 131,072 tokens 12.2 us with 512 and 15.0 with 256, 4 x 5 rows of up to 131,072 49
+// and 75.
 template <typename T, int D> cudaError_t launch_select_t(const SelectArgs &a, cudaStream_t stream) {
   if (a.max_candidates > 256 * kRunKeys) return launch_long<T, D, 512>(a, stream);
   if (a.max_candidates > (a.max_q_len > 1 ? 1024 : 256)) return launch_long<T, D, 256>(a, stream);
