@@ -561,6 +561,69 @@ def test_steps_on_two_streams_at_once(pa):  # noqa: F811
         s.check()
 
 
+@pytest.mark.parametrize("kv,dtype,d,bs,keep", STEPS)
+def test_drafted_rows_through_all_calls(pa, kv, dtype, d, bs, keep):  # noqa: F811
+    """Several new tokens a sequence, none for one: rotated and written, their blocks
+    bounded, blocks chosen for each row by the tokens up to it, and attended to."""
+    H, G, q_lens = 2, 4, [5, 1, 0, 3]
+    lens = [700, 2 * bs + 1, 90, 3]
+    b = Batch(24, lens, H, G, d, bs, dtype, kv, q_lens)
+    ks, vs = (1.0, 1.0) if kv == "16" else (0.5, 0.25)
+    pair = () if kv == "16" else (ks, vs)
+    vc, _ = pool(b.rng, b.rng.standard_normal((b.NB, H, bs, d)), kv, dtype, bs, d)
+    b.all_bounds()
+    gb, gs = dev(b.bounds), dev(b.scales)
+    new = torch.from_numpy(b.rng.standard_normal((9, (G + 2) * H, d))).to(TYPES[dtype]).cuda()
+    q, k, v = new.split([G * H, H, H], 1)
+    pos = (b.seen - 1).astype(np.int64)
+    slots = b.tables[b.seqs, pos // bs].astype(np.int64) * bs + pos % bs
+    table = pa.new_rope_table(700, d)
+    getattr(pa, "pa_rope_and_cache" + END[kv])(q, q, k, v, b.kc, vc, dev(slots), dev(pos), table, *pair)
+    bt, cl, start = dev(b.tables), dev(b.lens), dev(b.start)
+    getattr(pa, "pa_update_key_bounds" + END[kv])(gb, gs, b.kc, bt, cl, start, 5)
+    query = q.contiguous()
+    t = torch.zeros(9, H, keep, dtype=torch.int32, device="cuda")
+    n = torch.zeros(9, H, dtype=torch.int32, device="cuda")
+    pa.pa_select_blocks(t, n, query, gb, gs, bt, cl, bs, 700, 1, 1, start, 5)
+    out = torch.zeros_like(query)
+    getattr(pa, "pa_decode_sparse" + END[kv])(out, query, b.kc, vc, t, n, 1 / math.sqrt(d), *pair)
+    assert pa.pa_device_errors() == 0
+
+    def values(cache):
+        if kv == "16":
+            return f64(cache)
+        if kv == "fp8":
+            return oracle.e4m3_to_f64(cache.cpu().numpy()).reshape(b.NB, H, bs, d)
+        return F.values(cache.cpu().numpy(), bs, d, 1.0)
+
+    b.kvals, vvals = values(b.kc), values(vc)  # (what append writes: test_gpu_rope.py)
+    S.update_bounds(b.bounds, b.scales, b.kvals, b.tables, b.lens, q_lens)
+    assert np.array_equal(gb.cpu().numpy(), b.bounds) and np.array_equal(gs.cpu().numpy(), b.scales)
+    wt, wn = S.select(f64(query), b.bounds, b.scales, b.tables, b.seqs, b.seen, bs, keep, 1, 1)
+    assert np.array_equal(t.cpu().numpy(), wt) and np.array_equal(n.cpu().numpy(), wn)
+    ref, mag = S.attend(f64(query), b.kvals * ks, vvals * vs, wt, wn, 1 / math.sqrt(d))
+    eps = torch.finfo(TYPES[dtype]).eps / 2
+    # (keys have a mean of their own: as in Step.check)
+    assert (np.abs(f64(out) - ref) <= mag * (2.0 ** -9 + 2.0 ** -11) + np.abs(ref) * eps + 2.0 ** -24).all()
+
+
+def test_bounds_move_with_blocks(pa):  # noqa: F811
+    """A fork: blocks, bounds and scales copied within their pools, and a sequence that goes on in the copy."""
+    b = Batch(25, [100, 100], 4, 2, 64, 16, "fp16", extra=0)
+    b.all_bounds()
+    gb, gs = dev(b.bounds), dev(b.scales)
+    pairs = np.stack([b.tables[0], b.tables[1]], 1).astype(np.int64)
+    for pool_ in (b.kc, gb, gs):
+        pa.pa_swap_blocks(pool_, pool_, dev(pairs))
+    b.kvals[b.tables[1]] = b.kvals[b.tables[0]]
+    b.bounds[b.tables[1]], b.scales[b.tables[1]] = b.bounds[b.tables[0]], b.scales[b.tables[0]]
+    assert np.array_equal(gb.cpu().numpy(), b.bounds) and np.array_equal(gs.cpu().numpy(), b.scales)
+    b.lens[:] = 97, 100  # the first sequence gives up three tokens
+    S.update_bounds(b.bounds, b.scales, b.kvals, b.tables, b.lens, [1, 1])
+    pa.pa_update_key_bounds(gb, gs, b.kc, dev(b.tables), dev(b.lens))
+    assert np.array_equal(gb.cpu().numpy(), b.bounds) and np.array_equal(gs.cpu().numpy(), b.scales)
+
+
 def test_all_blocks_kept_is_dense_decode(pa):  # noqa: F811
     """Where every block is kept, the dense call of the same cache agrees within both calls' rounding."""
     for kv in ("16", "fp8", "fp4"):
