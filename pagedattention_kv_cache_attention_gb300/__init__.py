@@ -5,13 +5,16 @@ argument marshalling only: they check tensor devices, dtypes, shapes and
 contiguity, pass ``data_ptr()`` values, sizes and the current CUDA stream to
 the library, and turn a non-zero status into an exception.  Every step of the
 computation runs in the library's CUDA kernels; there is no fallback path, and
-importing a function fails loudly when ``libpa.so`` has not been built.
+importing a function fails loudly when ``libpa.so`` has not been built.  (The
+calls of rotated append and sparse attention make their checks in C++,
+``csrc/pa_bind.cpp``.)
 
 PyTorch supplies device memory and streams only.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 from typing import Optional
@@ -779,7 +782,23 @@ def new_key_bounds(num_blocks: int, num_kv_heads: int, head_dim: int, device=Non
             torch.zeros(num_blocks, num_kv_heads, dtype=torch.float32, device=dev))
 
 
-# Their arguments are checked in one pass too, like those of the FP4 calls.
+# These calls go through pa_bind.cpp, which makes the checks below and the C call
+# in C++; only what does not fit there is gone through here, to name it.
+_bind = None
+
+
+def _native():
+    """The module built from pa_bind.cpp."""
+    global _bind
+    _load()  # (fails loudly where nothing is built)
+    spec = importlib.util.spec_from_file_location("pa_bind", _build.BIND)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.set_raw_stream(_raw_stream)
+    _bind = module
+    return module
+
+
 _I8, _F32 = torch.int8, torch.float32
 _SPARSE_ARGS = {
     "pa_rope_and_cache": "PPPPllllPPPPPiiiiiiilliP", "pa_update_key_bounds": "PPPPiPPiiiiiliP",
@@ -789,13 +808,11 @@ _SPARSE_ARGS = {
     "pa_update_key_bounds_fp8": "PPPPiPPiiiiilP", "pa_update_key_bounds_fp4": "PPPPiPPiiiiilP",
     "pa_decode_sparse_fp8": "PPPPPPiiiiiilfffiP", "pa_decode_sparse_fp4": "PPPPPPiiiiiilfffiP",
 }
-_sparse_fns = {}
 
 
 def _sparse_fn(name: str):
     f = getattr(_load(), name)
     f.argtypes, f.restype = [_CT[c] for c in _SPARSE_ARGS[name]], ctypes.c_int32
-    _sparse_fns[name] = f
     return f
 
 
@@ -809,72 +826,42 @@ def _cache_shape(name: str, cache: torch.Tensor, d: int):
     return shape[0], shape[1], shape[2]
 
 
-def _rows_fit(dtype, dev, **rows) -> None:
-    """Names the first of the row tensors that a rotated append cannot take."""
-    for n, t in rows.items():
+def _rope(name, query_out, query, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
+          scales, interleaved, stream):
+    dev = _device_of("query", query)
+    dtype = query.dtype
+    strides = []
+    for n, t in (("query_out", query_out), ("query", query), ("key", key), ("value", value)):
         _cuda(n, t, dtype)
         if t.dim() != 3:
             raise ValueError(f"{n} must be [T, heads, d]")
-        st, (_, heads, d) = t.stride(), t.shape
+        st, (rows, heads, d) = t.stride(), t.shape
         if (st[2] != 1 and d > 1) or (st[1] != d and heads > 1):
             raise ValueError(f"{n}: heads must be contiguous inside a token row")
-
-
-def _rope(name, query_out, query, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
-          scales, interleaved, stream):
-    f = _sparse_fns.get(name) or _sparse_fn(name)
-    dev = _device_of("query", query)
-    dtype = query.dtype
+        # (the stride of a single row is not looked at)
+        strides.append(st[0] if rows > 1 else heads * d)
     cache = _U8 if scales else dtype
-    try:
-        fit = (query_out.dtype is dtype and key.dtype is dtype and value.dtype is dtype
-               and k_cache.dtype is cache and v_cache.dtype is cache
-               and slot_mapping.dtype is _I64 and positions.dtype is _I64 and cos_sin.dtype is _F32
-               and query_out.get_device() == dev == key.get_device() == value.get_device()
-               and k_cache.get_device() == dev == v_cache.get_device() == cos_sin.get_device()
-               and slot_mapping.get_device() == dev == positions.get_device()
-               and k_cache.is_contiguous() and v_cache.is_contiguous()
-               and slot_mapping.is_contiguous() and positions.is_contiguous()
-               and cos_sin.is_contiguous())
-        shape = query.shape
-        T, Hq, d = shape
-        _, Hkv, _ = kv = key.shape
-        qo, q, k, v = query_out.stride(), query.stride(), key.stride(), value.stride()
-        rows = (query_out.shape == shape and value.shape == kv and kv[0] == T and kv[2] == d
-                and qo[2] == 1 and q[2] == 1 and k[2] == 1 and v[2] == 1
-                and qo[1] == d and q[1] == d and k[1] == d and v[1] == d)
-    except (AttributeError, ValueError, IndexError):
-        fit = rows = False
-    if not (fit and rows):
-        # (a single head may have any stride, and name what does not fit)
-        _rows_fit(dtype, dev, query_out=query_out, query=query, key=key, value=value)
-        _all_fit(dev, k_cache=(k_cache, cache), v_cache=(v_cache, cache),
-                 slot_mapping=(slot_mapping, _I64), positions=(positions, _I64),
-                 cos_sin=(cos_sin, _F32))
-        if query_out.shape != shape:
-            raise ValueError("query_out must match query")
-        if kv[0] != T or kv[2] != d or value.shape != kv:
-            raise ValueError("key and value must be [T, Hkv, d], with query's T and d")
-    caches, table = k_cache.shape, cos_sin.shape
+    _all_fit(dev, k_cache=(k_cache, cache), v_cache=(v_cache, cache),
+             slot_mapping=(slot_mapping, _I64), positions=(positions, _I64),
+             cos_sin=(cos_sin, _F32))
+    T, Hq, d = query.shape
+    Hkv = key.shape[1]
+    if query_out.shape != query.shape:
+        raise ValueError("query_out must match query")
+    if key.shape != (T, Hkv, d) or value.shape != key.shape:
+        raise ValueError("key and value must be [T, Hkv, d], with query's T and d")
     NB, heads, bs = _cache_shape(name, k_cache, d)
-    if heads != Hkv or v_cache.shape != caches:
+    if heads != Hkv or v_cache.shape != k_cache.shape:
         raise ValueError("key/value/cache shapes disagree")
     if slot_mapping.numel() != T or positions.numel() != T:
         raise ValueError("slot_mapping and positions must have one entry per token")
-    if len(table) != 2:
+    if cos_sin.dim() != 2:
         raise ValueError("cos_sin must be [max_position, rotary_dim]")
-    if T > 1:
-        qo, q, k, v = qo[0], q[0], k[0], v[0]
-    else:  # the stride of a single row is not looked at
-        qo = q = Hq * d
-        k = v = Hkv * d
-    st = f(query_out.data_ptr(), query.data_ptr(), key.data_ptr(), value.data_ptr(), qo, q, k, v,
-           k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
-           cos_sin.data_ptr(), T, Hq, Hkv, d, table[1], 1 if interleaved else 0, bs, NB, table[0],
-           _dtype_code(query), *scales,
-           _raw_stream(dev) if stream is None else _stream(stream))
-    if st:
-        raise PaError(name, st)
+    _check(name, _sparse_fn(name)(
+        query_out.data_ptr(), query.data_ptr(), key.data_ptr(), value.data_ptr(), *strides,
+        k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
+        cos_sin.data_ptr(), T, Hq, Hkv, d, cos_sin.shape[1], 1 if interleaved else 0, bs, NB,
+        cos_sin.shape[0], _dtype_code(query), *scales, _stream(stream)))
     return query_out
 
 
@@ -886,6 +873,13 @@ def pa_rope_and_cache(query_out: torch.Tensor, query: torch.Tensor, key: torch.T
     the table cos_sin (new_rope_table); write the queries into ``query_out``
     (which may be ``query``), and keys and values into the caches at
     slot_mapping[t] (int64; a token with a negative slot is left out)."""
+    st = (_bind or _native()).rope(0, query_out, query, key, value, k_cache, v_cache,
+                                   slot_mapping, positions, cos_sin, 1.0, 1.0, interleaved,
+                                   stream)
+    if st == 0:
+        return query_out
+    if st > 0:
+        raise PaError("pa_rope_and_cache", st)
     return _rope("pa_rope_and_cache", query_out, query, key, value, k_cache, v_cache,
                  slot_mapping, positions, cos_sin, (), interleaved, stream)
 
@@ -896,6 +890,13 @@ def pa_rope_and_cache_fp8(query_out: torch.Tensor, query: torch.Tensor, key: tor
                           cos_sin: torch.Tensor, k_scale: float, v_scale: float,
                           interleaved: bool = False, stream=None) -> torch.Tensor:
     """pa_rope_and_cache into uint8 FP8 E4M3 caches."""
+    st = (_bind or _native()).rope(1, query_out, query, key, value, k_cache, v_cache,
+                                   slot_mapping, positions, cos_sin, k_scale, v_scale, interleaved,
+                                   stream)
+    if st == 0:
+        return query_out
+    if st > 0:
+        raise PaError("pa_rope_and_cache_fp8", st)
     return _rope("pa_rope_and_cache_fp8", query_out, query, key, value, k_cache, v_cache,
                  slot_mapping, positions, cos_sin, (float(k_scale), float(v_scale)), interleaved,
                  stream)
@@ -907,6 +908,13 @@ def pa_rope_and_cache_fp4(query_out: torch.Tensor, query: torch.Tensor, key: tor
                           cos_sin: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0,
                           interleaved: bool = False, stream=None) -> torch.Tensor:
     """pa_rope_and_cache into FP4 caches (new_fp4_cache)."""
+    st = (_bind or _native()).rope(2, query_out, query, key, value, k_cache, v_cache,
+                                   slot_mapping, positions, cos_sin, k_scale, v_scale, interleaved,
+                                   stream)
+    if st == 0:
+        return query_out
+    if st > 0:
+        raise PaError("pa_rope_and_cache_fp4", st)
     return _rope("pa_rope_and_cache_fp4", query_out, query, key, value, k_cache, v_cache,
                  slot_mapping, positions, cos_sin, (float(k_scale), float(v_scale)), interleaved,
                  stream)
@@ -914,26 +922,13 @@ def pa_rope_and_cache_fp4(query_out: torch.Tensor, query: torch.Tensor, key: tor
 
 def _key_bounds(name, bounds, bound_scales, k_cache, block_tables, context_lens, query_start,
                 max_q_len, stream):
-    f = _sparse_fns.get(name) or _sparse_fn(name)
     dev = _device_of("k_cache", k_cache)
     plain = name == "pa_update_key_bounds"
-    cache = k_cache.dtype if plain else _U8
-    try:
-        fit = (bounds.dtype is _I8 and bound_scales.dtype is _F32 and k_cache.dtype is cache
-               and block_tables.dtype is _I32 and context_lens.dtype is _I32
-               and bounds.get_device() == dev == bound_scales.get_device()
-               and block_tables.get_device() == dev == context_lens.get_device()
-               and bounds.is_contiguous() and bound_scales.is_contiguous()
-               and k_cache.is_contiguous() and block_tables.is_contiguous()
-               and context_lens.is_contiguous())
-    except AttributeError:
-        fit = False
-    if not fit:
-        _all_fit(dev, bounds=(bounds, _I8), bound_scales=(bound_scales, _F32),
-                 k_cache=(k_cache, cache), block_tables=(block_tables, _I32),
-                 context_lens=(context_lens, _I32))
+    _all_fit(dev, bounds=(bounds, _I8), bound_scales=(bound_scales, _F32),
+             k_cache=(k_cache, k_cache.dtype if plain else _U8),
+             block_tables=(block_tables, _I32), context_lens=(context_lens, _I32))
     start = _start(query_start, dev, context_lens)
-    shape, table = bounds.shape, block_tables.shape
+    shape = bounds.shape
     if len(shape) != 4 or shape[2] != 2 or bound_scales.shape != shape[:2]:
         raise ValueError("bounds must be [NB, Hkv, 2, d] and bound_scales [NB, Hkv]")
     d = shape[3]
@@ -941,14 +936,12 @@ def _key_bounds(name, bounds, bound_scales, k_cache, block_tables, context_lens,
     if shape[0] != NB or shape[1] != Hkv:
         raise ValueError("bounds and k_cache differ in blocks or heads")
     B = context_lens.numel()
-    if len(table) != 2 or table[0] != B:
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
         raise ValueError("block_tables must be [B, MB] and context_lens [B]")
-    st = f(bounds.data_ptr(), bound_scales.data_ptr(), k_cache.data_ptr(), block_tables.data_ptr(),
-           table[1], context_lens.data_ptr(), start, B, int(max_q_len), Hkv, d, bs, NB,
-           *((_dtype_code(k_cache),) if plain else ()),
-           _raw_stream(dev) if stream is None else _stream(stream))
-    if st:
-        raise PaError(name, st)
+    _check(name, _sparse_fn(name)(
+        bounds.data_ptr(), bound_scales.data_ptr(), k_cache.data_ptr(), block_tables.data_ptr(),
+        block_tables.shape[1], context_lens.data_ptr(), start, B, int(max_q_len), Hkv, d, bs, NB,
+        *((_dtype_code(k_cache),) if plain else ()), _stream(stream)))
 
 
 def _start(query_start, dev, context_lens):
@@ -968,6 +961,12 @@ def pa_update_key_bounds(bounds: torch.Tensor, bound_scales: torch.Tensor, k_cac
     """Bring ``bounds`` and ``bound_scales`` (new_key_bounds) up to date for the
     blocks that hold the newest tokens of each sequence: the last one, or the
     last query_start[i + 1] - query_start[i] (at most max_q_len)."""
+    st = (_bind or _native()).key_bounds(0, bounds, bound_scales, k_cache, block_tables,
+                                         context_lens, query_start, max_q_len, stream)
+    if st == 0:
+        return
+    if st > 0:
+        raise PaError("pa_update_key_bounds", st)
     _key_bounds("pa_update_key_bounds", bounds, bound_scales, k_cache, block_tables,
                 context_lens, query_start, max_q_len, stream)
 
@@ -978,6 +977,12 @@ def pa_update_key_bounds_fp8(bounds: torch.Tensor, bound_scales: torch.Tensor,
                              query_start: Optional[torch.Tensor] = None, max_q_len: int = 1,
                              stream=None) -> None:
     """pa_update_key_bounds over a uint8 FP8 E4M3 cache."""
+    st = (_bind or _native()).key_bounds(1, bounds, bound_scales, k_cache, block_tables,
+                                         context_lens, query_start, max_q_len, stream)
+    if st == 0:
+        return
+    if st > 0:
+        raise PaError("pa_update_key_bounds_fp8", st)
     _key_bounds("pa_update_key_bounds_fp8", bounds, bound_scales, k_cache, block_tables,
                 context_lens, query_start, max_q_len, stream)
 
@@ -988,6 +993,12 @@ def pa_update_key_bounds_fp4(bounds: torch.Tensor, bound_scales: torch.Tensor,
                              query_start: Optional[torch.Tensor] = None, max_q_len: int = 1,
                              stream=None) -> None:
     """pa_update_key_bounds over an FP4 cache."""
+    st = (_bind or _native()).key_bounds(2, bounds, bound_scales, k_cache, block_tables,
+                                         context_lens, query_start, max_q_len, stream)
+    if st == 0:
+        return
+    if st > 0:
+        raise PaError("pa_update_key_bounds_fp4", st)
     _key_bounds("pa_update_key_bounds_fp4", bounds, bound_scales, k_cache, block_tables,
                 context_lens, query_start, max_q_len, stream)
 
@@ -1005,88 +1016,63 @@ def pa_select_blocks(selected_tables: torch.Tensor, selected_lens: torch.Tensor,
     is sequence i's query, or rows query_start[i] .. query_start[i + 1] - 1 its
     last tokens.  The first num_sink and last num_recent blocks that a row
     sees are always taken.  Returns (selected_tables, selected_lens)."""
-    f = _sparse_fns.get("pa_select_blocks") or _sparse_fn("pa_select_blocks")
+    st = (_bind or _native()).select(selected_tables, selected_lens, query, bounds, bound_scales,
+                                     block_tables, context_lens, block_size, max_context_len,
+                                     num_sink, num_recent, query_start, max_q_len, stream)
+    if st == 0:
+        return selected_tables, selected_lens
+    if st > 0:
+        raise PaError("pa_select_blocks", st)
     dev = _device_of("query", query)
-    try:
-        fit = (selected_tables.dtype is _I32 and selected_lens.dtype is _I32
-               and bounds.dtype is _I8 and bound_scales.dtype is _F32
-               and block_tables.dtype is _I32 and context_lens.dtype is _I32
-               and selected_tables.get_device() == dev == selected_lens.get_device()
-               and bounds.get_device() == dev == bound_scales.get_device()
-               and block_tables.get_device() == dev == context_lens.get_device()
-               and query.is_contiguous() and selected_tables.is_contiguous()
-               and selected_lens.is_contiguous() and bounds.is_contiguous()
-               and bound_scales.is_contiguous() and block_tables.is_contiguous()
-               and context_lens.is_contiguous())
-    except AttributeError:
-        fit = False
-    if not fit:
-        _all_fit(dev, query=(query, query.dtype), selected_tables=(selected_tables, _I32),
-                 selected_lens=(selected_lens, _I32), bounds=(bounds, _I8),
-                 bound_scales=(bound_scales, _F32), block_tables=(block_tables, _I32),
-                 context_lens=(context_lens, _I32))
+    _all_fit(dev, query=(query, query.dtype), selected_tables=(selected_tables, _I32),
+             selected_lens=(selected_lens, _I32), bounds=(bounds, _I8),
+             bound_scales=(bound_scales, _F32), block_tables=(block_tables, _I32),
+             context_lens=(context_lens, _I32))
     start = _start(query_start, dev, context_lens)
-    rows, shape, picked, table = (query.shape, bounds.shape, selected_tables.shape,
-                                  block_tables.shape)
-    if len(rows) != 3 or len(picked) != 3:
+    shape, picked = bounds.shape, selected_tables.shape
+    if query.dim() != 3 or len(picked) != 3:
         raise ValueError("query must be [R, Hq, d] and selected_tables [R, Hkv, K]")
-    R, Hq, d = rows
+    R, Hq, d = query.shape
     if len(shape) != 4 or shape[2] != 2 or shape[3] != d or bound_scales.shape != shape[:2]:
         raise ValueError("bounds must be [NB, Hkv, 2, d] and bound_scales [NB, Hkv]")
-    Hkv = shape[1]
-    if picked[0] != R or picked[1] != Hkv or selected_lens.shape != picked[:2]:
+    NB, Hkv = shape[:2]
+    if picked[:2] != (R, Hkv) or selected_lens.shape != picked[:2]:
         raise ValueError("selected_tables must be [R, Hkv, K] and selected_lens [R, Hkv]")
     B = context_lens.numel()
-    if len(table) != 2 or table[0] != B:
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
         raise ValueError("block_tables must be [B, MB] and context_lens [B]")
     if start is None and R != B:
         raise ValueError("without query_start there is one query row for each sequence")
-    st = f(selected_tables.data_ptr(), selected_lens.data_ptr(), query.data_ptr(),
-           bounds.data_ptr(), bound_scales.data_ptr(), block_tables.data_ptr(), table[1],
-           context_lens.data_ptr(), start, B, int(max_q_len), Hq, Hkv, d, int(block_size),
-           shape[0], int(max_context_len), picked[2], int(num_sink), int(num_recent),
-           _dtype_code(query), _raw_stream(dev) if stream is None else _stream(stream))
-    if st:
-        raise PaError("pa_select_blocks", st)
+    _check("pa_select_blocks", _sparse_fn("pa_select_blocks")(
+        selected_tables.data_ptr(), selected_lens.data_ptr(), query.data_ptr(), bounds.data_ptr(),
+        bound_scales.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+        context_lens.data_ptr(), start, B, int(max_q_len), Hq, Hkv, d, int(block_size), NB,
+        int(max_context_len), picked[2], int(num_sink), int(num_recent), _dtype_code(query),
+        _stream(stream)))
     return selected_tables, selected_lens
 
 
 def _decode_sparse(name, out, query, k_cache, v_cache, selected_tables, selected_lens, scale,
                    scales, stream):
-    f = _sparse_fns.get(name) or _sparse_fn(name)
     dev = _device_of("query", query)
     dtype = query.dtype
     cache = _U8 if scales else dtype
-    try:
-        fit = (out.dtype is dtype and k_cache.dtype is cache and v_cache.dtype is cache
-               and selected_tables.dtype is _I32 and selected_lens.dtype is _I32
-               and out.get_device() == dev == k_cache.get_device() == v_cache.get_device()
-               and selected_tables.get_device() == dev == selected_lens.get_device()
-               and query.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous()
-               and v_cache.is_contiguous() and selected_tables.is_contiguous()
-               and selected_lens.is_contiguous())
-    except AttributeError:
-        fit = False
-    if not fit:
-        _all_fit(dev, query=(query, dtype), out=(out, dtype), k_cache=(k_cache, cache),
-                 v_cache=(v_cache, cache), selected_tables=(selected_tables, _I32),
-                 selected_lens=(selected_lens, _I32))
-    rows, picked = query.shape, selected_tables.shape
-    if len(rows) != 3 or out.shape != rows:
+    _all_fit(dev, query=(query, dtype), out=(out, dtype), k_cache=(k_cache, cache),
+             v_cache=(v_cache, cache), selected_tables=(selected_tables, _I32),
+             selected_lens=(selected_lens, _I32))
+    picked = selected_tables.shape
+    if query.dim() != 3 or out.shape != query.shape:
         raise ValueError("query and out must be [R, Hq, d], alike")
-    R, Hq, d = rows
+    R, Hq, d = query.shape
     NB, Hkv, bs = _cache_shape(name, k_cache, d)
     if v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache shapes differ")
-    if (len(picked) != 3 or picked[0] != R or picked[1] != Hkv
-            or selected_lens.shape != picked[:2]):
+    if len(picked) != 3 or picked[:2] != (R, Hkv) or selected_lens.shape != picked[:2]:
         raise ValueError("selected_tables must be [R, Hkv, K] and selected_lens [R, Hkv]")
-    st = f(out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-           selected_tables.data_ptr(), selected_lens.data_ptr(), R, picked[2], Hq, Hkv, d, bs, NB,
-           float(scale), *scales, _dtype_code(query),
-           _raw_stream(dev) if stream is None else _stream(stream))
-    if st:
-        raise PaError(name, st)
+    _check(name, _sparse_fn(name)(
+        out.data_ptr(), query.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        selected_tables.data_ptr(), selected_lens.data_ptr(), R, picked[2], Hq, Hkv, d, bs, NB,
+        float(scale), *scales, _dtype_code(query), _stream(stream)))
     return out
 
 
@@ -1096,6 +1082,12 @@ def pa_decode_sparse(out: torch.Tensor, query: torch.Tensor, k_cache: torch.Tens
     """Decode attention of query [R, Hq, d] into ``out``, row r and KV head g
     over the first selected_lens[r, g] tokens of the blocks
     selected_tables[r, g, :] (pa_select_blocks)."""
+    st = (_bind or _native()).sparse(0, out, query, k_cache, v_cache, selected_tables,
+                                     selected_lens, scale, 1.0, 1.0, stream)
+    if st == 0:
+        return out
+    if st > 0:
+        raise PaError("pa_decode_sparse", st)
     return _decode_sparse("pa_decode_sparse", out, query, k_cache, v_cache, selected_tables,
                           selected_lens, scale, (), stream)
 
@@ -1105,6 +1097,12 @@ def pa_decode_sparse_fp8(out: torch.Tensor, query: torch.Tensor, k_cache: torch.
                          selected_lens: torch.Tensor, scale: float, k_scale: float,
                          v_scale: float, stream=None) -> torch.Tensor:
     """pa_decode_sparse over uint8 FP8 E4M3 caches, fp16 or bf16 queries and output."""
+    st = (_bind or _native()).sparse(1, out, query, k_cache, v_cache, selected_tables,
+                                     selected_lens, scale, k_scale, v_scale, stream)
+    if st == 0:
+        return out
+    if st > 0:
+        raise PaError("pa_decode_sparse_fp8", st)
     return _decode_sparse("pa_decode_sparse_fp8", out, query, k_cache, v_cache, selected_tables,
                           selected_lens, scale, (float(k_scale), float(v_scale)), stream)
 
@@ -1114,6 +1112,12 @@ def pa_decode_sparse_fp4(out: torch.Tensor, query: torch.Tensor, k_cache: torch.
                          selected_lens: torch.Tensor, scale: float, k_scale: float,
                          v_scale: float, stream=None) -> torch.Tensor:
     """pa_decode_sparse over FP4 caches, fp16 or bf16 queries and output."""
+    st = (_bind or _native()).sparse(2, out, query, k_cache, v_cache, selected_tables,
+                                     selected_lens, scale, k_scale, v_scale, stream)
+    if st == 0:
+        return out
+    if st > 0:
+        raise PaError("pa_decode_sparse_fp4", st)
     return _decode_sparse("pa_decode_sparse_fp4", out, query, k_cache, v_cache, selected_tables,
                           selected_lens, scale, (float(k_scale), float(v_scale)), stream)
 

@@ -2,7 +2,9 @@
 
 Each translation unit under csrc/ is compiled by its own nvcc process, in
 parallel, then linked into one shared library with the CUDA runtime linked
-statically.  Output: <package>/_build/libpa.so (git-ignored).
+statically.  Beside it the C++ part of the Python binding (pa_bind.cpp) is
+compiled with g++ against the installed torch's headers.  Outputs (git-ignored):
+<package>/_build/libpa.so and <package>/_build/pa_bind.so.
 """
 from __future__ import annotations
 
@@ -10,12 +12,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libpa.so")
+BIND = os.path.join(OUT_DIR, "pa_bind.so")
 SOURCES = ("pa_api.cu", "pa_blocks.cu", "pa_cache.cu", "pa_cache_fp4.cu", "pa_decode.cu",
            "pa_decode_fp4.cu", "pa_decode_sparse.cu", "pa_prefill_fp4.cu", "pa_prefill_tc.cu",
            "pa_rope.cu", "pa_sparse.cu", "pa_static_ws.cu")
@@ -31,12 +35,36 @@ def nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BIND)):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
     deps.append(os.path.join(os.path.dirname(HERE), "include", "pa.h"))
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _run(what: str, cmd) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(torch.__file__)
+
+
+def _compile_bind() -> str:
+    import torch
+    obj = os.path.join(OUT_DIR, "pa_bind.o")
+    inc = os.path.join(_torch_dir(), "include")
+    _run("g++ on pa_bind.cpp", [
+        "g++", "-std=c++17", "-O2", "-fPIC", "-Wall",
+        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", inc,
+        "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+        "-isystem", sysconfig.get_paths()["include"],
+        "-c", os.path.join(CSRC, "pa_bind.cpp"), "-o", obj])
+    return obj
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -57,14 +85,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        bind = ex.submit(_compile_bind)
         objs = list(ex.map(compile_one, SOURCES))
+        bind_obj = bind.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [cc, "-shared", *ARCH, "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _run("link of pa_bind.so", ["g++", "-shared", "-o", tmp, bind_obj, "-L" + OUT_DIR, "-l:libpa.so",
+                                "-L" + os.path.join(_torch_dir(), "lib"), "-lc10", "-ltorch_cpu",
+                                "-ltorch_python", "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, BIND)
     return LIB
 
 

@@ -640,6 +640,46 @@ def test_all_blocks_kept_is_dense_decode(pa):  # noqa: F811
         check(b, dense, vvals, t, n, 0.09, 1.0, 1.0)
 
 
+def test_arguments_of_other_kinds(pa):  # noqa: F811
+    """numpy numbers, a stream's handle, a stream object, single heads of any stride, one row of any
+    stride: what the native binding leaves to the checks in Python."""
+    b = Batch(32, [40, 33], 1, 2, 64, 16, "fp16", mean=0.0)
+    vc, vvals = pool(b.rng, b.rng.standard_normal((b.NB, 1, 16, 64)), "16", "fp16", 16, 64)
+    b.all_bounds()
+    gb, gs = pa.new_key_bounds(b.NB, 1, 64)
+    st = torch.cuda.Stream()
+    handle = torch.cuda.current_stream().cuda_stream
+    torch.cuda.synchronize()
+    one = dev(np.array([0, 40, 73], np.int32))
+    pa.pa_update_key_bounds(gb, gs, b.kc, dev(b.tables), dev(b.lens), one, np.int64(40), stream=st)
+    st.synchronize()
+    assert np.array_equal(gb.cpu().numpy(), b.bounds)
+    t = torch.zeros(2, 1, 2, dtype=torch.int32, device="cuda")
+    n = torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+    pa.pa_select_blocks(t, n, b.q.cuda(), gb, gs, dev(b.tables), dev(b.lens), np.int32(16), np.int64(40), np.int64(1),
+                        stream=handle)
+    wt, wn = b.want(2, 1, 1)
+    assert np.array_equal(t.cpu().numpy(), wt) and np.array_equal(n.cpu().numpy(), wn)
+    out = torch.zeros_like(b.q, device="cuda")
+    pa.pa_decode_sparse(out, b.q.cuda(), b.kc, vc, t, n, np.float32(0.1))
+    check(b, out, vvals, wt, wn, float(np.float32(0.1)), 1.0, 1.0)
+    # K of one head in rows whose heads are 200 apart; one token in a row of any length
+    wide = torch.from_numpy(b.rng.standard_normal((3, 2, 200))).half().cuda()
+    k = wide[:, :1, :64]
+    q = torch.from_numpy(b.rng.standard_normal((3, 2, 64))).half().cuda()
+    table = pa.new_rope_table(5, 64)
+    slots, pos = dev(np.array([0, 1, 2])), dev(np.array([4, 0, 3]))
+    res = torch.zeros_like(q)
+    pa.pa_rope_and_cache(res, q, k, k, b.kc, vc, slots, pos, table)
+    want = S.rotate(k.cpu().float().numpy(), [4, 0, 3], table.cpu().numpy(), False)
+    assert np.array_equal(f64(b.kc[0, :, :3].transpose(0, 1)), torch.from_numpy(want).half().double().numpy())
+    assert torch.equal(vc[0, 0, :3], k[:, 0])
+    pa.pa_rope_and_cache(res[:1], q[:1], wide[:1, 1:, 3:67].clone(), k[:1], b.kc, vc, slots[:1], pos[:1], table)
+    want = S.rotate(wide[:1, 1:, 3:67].cpu().float().numpy(), [4], table.cpu().numpy(), False)
+    assert np.array_equal(f64(b.kc[0, :, :1].transpose(0, 1)), torch.from_numpy(want).half().double().numpy())
+    assert pa.pa_device_errors() == 0
+
+
 def test_offsets_past_32_bits(pa):  # noqa: F811
     """The last blocks of a pool of more than 2^31 elements a cache, through all calls."""
     H, bs, d, NB = 8, 32, 128, (1 << 31) // (8 * 32 * 128) + 9

@@ -204,6 +204,17 @@ def test_what_is_no_cuda_tensor_is_named(pa):
             pa.pa_decode_sparse(x, bad, x, x, i32, i32, 0.1)
 
 
+def test_native_binding_leaves_what_does_not_fit(pa):
+    """-1 for a wrong number of arguments, for what is no tensor, and for host tensors."""
+    native = pa._native()
+    x, i32 = torch.zeros(2, 4, 64, dtype=torch.float16), torch.zeros(2, dtype=torch.int32)
+    for f, n in ((native.rope, 14), (native.key_bounds, 9), (native.select, 14), (native.sparse, 11)):
+        assert f() == -1 and f(1, 2, 3) == -1
+        for bad in (None, 0, x, i32, "", 2 ** 70):
+            assert f(*[bad] * n) == -1
+            assert f(0, *[bad] * (n - 1)) == -1
+
+
 def test_rope_table_holds_far_angles(pa):
     t = pa.new_rope_table(100001, 32, base=500000.0, device="cpu")
     assert t.shape == (100001, 32) and t.dtype == torch.float32
