@@ -106,24 +106,34 @@ template <int D, Kv KV> struct KeyShare {
   }
 };
 
-constexpr int kBoundsWarps = 4;
+// Elementwise larger of two pairs, NaN if either is.
+template <typename T> __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
+  uint32_t unused = y;
+  extremes2<T>(x, y, unused);
+  return y;
+}
 
-// A warp for a (block, KV head): every lane keeps the extremes of its channels
-// over the rows that it reads, lanes of the same channels are joined by shuffles.
+// A CTA for a block, a warp for a KV head of it (more heads in turn): every lane
+// keeps the extremes of its channels over the rows that it reads.  The lanes that
+// hold the same channels then share these out in a butterfly, largest ones to the
+// lower half of the warp and the negated smallest to the upper one, so that all
+// that is left is a maximum.
 // Latency bounds it (length, table entry, keys: three loads one after another): a
-// step's 256 sequences x 8 heads x 32 tokens x 128, bf16, 3.7 us for 9 MB; 16 chunks
-// of 1,031 tokens, 8 heads x 128, fp16 9.8 us for 36 MB, FP8 7.1, FP4 7.3.
+// step's 256 sequences x 8 heads x 32 tokens x 128, bf16, 2.9 us for 9 MB; 16 chunks
+// of 1,031 tokens, 8 heads x 128, fp16 7.5 us for 36 MB, FP8 5.5, FP4 5.8 (with all
+// lanes of a channel taking all of its maxima 3.7, 9.8, 7.1 and 7.3: instructions).
+constexpr int kBoundsWarps = 8;
+
 template <typename T, int D, Kv KV>
 __global__ void __launch_bounds__(kBoundsWarps * 32) key_bounds_kernel(const BoundsArgs a) {
   using Share = KeyShare<D, KV>;
   using MT = typename std::conditional<KV == Kv::k16, T, __half>::type;
   constexpr int W = Share::kWords, kLanes = Share::kLanes, kRows = Share::kRows;
   constexpr int kTake = KV == Kv::k16 ? 8 : 4;  // rows that a lane has in flight
+  constexpr int kKeep = 2 * W * kLanes / 32;    // words that a lane ends with
   grid_dependency_wait();  // the keys may come from the kernel before
   grid_launch_dependents();
   const int seq = blockIdx.y, lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kBoundsWarps + (threadIdx.x >> 5);
-  const int h = static_cast<int>(item % a.num_kv_heads);
   const int bs = 1 << a.bs_log2;
   const int ctx = a.context_lens[seq];
   int new_tokens = min(ctx, 1);
@@ -134,86 +144,87 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) key_bounds_kernel(const Bou
     return;
   }
   if (new_tokens == 0) return;
-  const int64_t j = ((ctx - new_tokens) >> a.bs_log2) + item / a.num_kv_heads;
+  const int64_t j = ((ctx - new_tokens) >> a.bs_log2) + static_cast<int64_t>(blockIdx.x);
   if (j > (ctx - 1) >> a.bs_log2) return;
   const int phys = a.block_tables[static_cast<int64_t>(seq) * a.max_blocks_per_seq + j];
   if (phys < 0 || phys >= a.num_blocks) {
-    if (lane == 0) atomicOr(a.err, kErrBadBlock);
+    if (threadIdx.x == 0) atomicOr(a.err, kErrBadBlock);
     return;
   }
   const int rows = min(bs, static_cast<int>(ctx - (j << a.bs_log2)));
-  const int64_t cell = static_cast<int64_t>(phys) * a.num_kv_heads + h;
   const int block_bytes = KV == Kv::kFp4 ? fp4_tile_bytes(bs, D) : bs * D * (KV == Kv::k16 ? 2 : 1);
-  const uint8_t *block = static_cast<const uint8_t *>(a.k_cache) + cell * block_bytes;
-
   const int share = lane % kLanes, r0 = lane / kLanes;
-  // (row 0 counts always: rows past the end are read as that one)
-  uint32_t hi[W], lo[W];
-  Share::widen(Share::load(block, bs, 0, share), hi);
+  for (int h = threadIdx.x >> 5; h < a.num_kv_heads; h += blockDim.x >> 5) {
+    const int64_t cell = static_cast<int64_t>(phys) * a.num_kv_heads + h;
+    const uint8_t *block = static_cast<const uint8_t *>(a.k_cache) + cell * block_bytes;
+    // (row 0 counts always: rows past the end are read as that one)
+    uint32_t v[2 * W];  // the largest, then the smallest
+    for (int r = r0; r < bs; r += kRows * kTake) {
+      typename Share::Raw raw[kTake];
 #pragma unroll
-  for (int w = 0; w < W; ++w) lo[w] = hi[w];
-  for (int r = r0; r < bs; r += kRows * kTake) {
-    typename Share::Raw raw[kTake];
+      for (int i = 0; i < kTake; ++i) {
+        const int at = r + i * kRows;
+        raw[i] = Share::load(block, bs, at < rows ? at : 0, share);
+      }
 #pragma unroll
-    for (int i = 0; i < kTake; ++i) {
-      const int at = r + i * kRows;
-      raw[i] = Share::load(block, bs, at < rows ? at : 0, share);
+      for (int i = 0; i < kTake; ++i) {
+        uint32_t x[W];
+        Share::widen(raw[i], x);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          if (i == 0 && r == r0) v[w] = v[W + w] = x[w];
+          extremes2<MT>(x[w], v[w], v[W + w]);
+        }
+      }
     }
 #pragma unroll
-    for (int i = 0; i < kTake; ++i) {
-      uint32_t x[W];
-      Share::widen(raw[i], x);
+    for (int w = 0; w < W; ++w) v[W + w] ^= 0x80008000u;
 #pragma unroll
-      for (int w = 0; w < W; ++w) extremes2<MT>(x[w], hi[w], lo[w]);
+    for (int off = 16, n = W; off >= kLanes; off >>= 1, n >>= 1) {
+      const bool up = lane & off;
+#pragma unroll
+      for (int w = 0; w < n; ++w) {
+        const uint32_t keep = up ? v[n + w] : v[w], give = up ? v[w] : v[n + w];
+        v[w] = max2<MT>(__shfl_xor_sync(kAll, give, off), keep);
+      }
     }
-  }
-  float top = 0.f;
-  bool odd = false;  // an infinity or a NaN
-  float up[2 * W], down[2 * W];
+    // the largest magnitude is the largest of all that is left; an infinity or a NaN
+    // is one of those, too
+    float x[2 * kKeep], top = 0.f;
 #pragma unroll
-  for (int w = 0; w < W; ++w) {
-#pragma unroll
-    for (int off = kLanes; off < 32; off <<= 1) {
-      const uint32_t oh = __shfl_xor_sync(kAll, hi[w], off), ol = __shfl_xor_sync(kAll, lo[w], off);
-      uint32_t unused = ol;
-      extremes2<MT>(oh, hi[w], unused);
-      unused = oh;
-      extremes2<MT>(ol, unused, lo[w]);
+    for (int w = 0; w < kKeep; ++w) {
+      const float2 p = Elem<MT>::unpack(v[w]);
+      x[2 * w] = p.x, x[2 * w + 1] = p.y;
+      top = p.x < INFINITY ? fmaxf(top, p.x) : INFINITY;
+      top = p.y < INFINITY ? fmaxf(top, p.y) : INFINITY;
     }
-    const float2 x = Elem<MT>::unpack(hi[w]), y = Elem<MT>::unpack(lo[w]);
-    up[2 * w] = x.x, up[2 * w + 1] = x.y, down[2 * w] = y.x, down[2 * w + 1] = y.y;
+    top = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(top)));
+    const bool odd = top == INFINITY, none = odd || top == 0.f;
+    const int e = none ? 0 : exponent_for(top, 7);
+    const float inv = none ? 0.f : pow2(-e);
+    const bool smallest = lane & 16;
+    uint32_t out[kKeep / 2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float m = fmaxf(fabsf(up[2 * w + e]), fabsf(down[2 * w + e]));
-      odd = odd || !(fabsf(up[2 * w + e]) < INFINITY) || !(fabsf(down[2 * w + e]) < INFINITY);
-      top = fmaxf(top, m);
-    }
-  }
-#pragma unroll
-  for (int off = 1; off < kLanes; off <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
-  odd = __any_sync(kAll, odd);
-  const bool none = odd || top == 0.f;
-  const int e = none ? 0 : exponent_for(top, 7);
-  const float inv = none ? 0.f : pow2(-e);
-  // group 0 of the lanes writes the largest, group 1 the smallest
-  if (r0 < 2) {
-    uint32_t out[Share::kElems / 4];
-#pragma unroll
-    for (int q = 0; q < Share::kElems / 4; ++q) {
+    for (int q = 0; q < kKeep / 2; ++q) {
       uint32_t word = 0;
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const int i = 4 * q + b;
         // (2^-e is exact, and so is the product but for results below 2^-149)
-        const int code = none ? 0 : r0 == 0 ? __float2int_ru(up[i] * inv) : __float2int_rd(down[i] * inv);
-        word |= static_cast<uint32_t>(code & 0xff) << (8 * b);
+        const int c = none ? 0 : __float2int_ru(x[4 * q + b] * inv);
+        word |= static_cast<uint32_t>((smallest ? -c : c) & 0xff) << (8 * b);
       }
       out[q] = word;
     }
-    uint32_t *dst = reinterpret_cast<uint32_t *>(a.bounds + (cell * 2 + r0) * D + share * Share::kElems);
+    // the lane's words: the part of its share that its place among the lanes of
+    // equal channels in its half of the warp stands for
+    int first = 0;
 #pragma unroll
-    for (int q = 0; q < Share::kElems / 4; q += 2)
-      *reinterpret_cast<uint2 *>(dst + q) = make_uint2(out[q], out[q + 1]);
+    for (int off = 8, n = W / 2; off >= kLanes; off >>= 1, n >>= 1) first += lane & off ? n : 0;
+    int8_t *dst = a.bounds + (cell * 2 + (smallest ? 1 : 0)) * D + share * Share::kElems + 2 * first;
+    if constexpr (kKeep == 4)
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(out[0], out[1]);
+    else
+      *reinterpret_cast<uint32_t *>(dst) = out[0];
     if (lane == 0) a.bound_scales[cell] = odd ? INFINITY : none ? 0.f : pow2(e);
   }
 }
@@ -224,10 +235,9 @@ cudaError_t launch_bounds(const BoundsArgs &a, cudaStream_t stream) {
   int64_t blocks = ((static_cast<int64_t>(a.max_q_len) - 1) >> a.bs_log2) + 2;
   blocks = blocks < a.max_blocks_per_seq ? blocks : a.max_blocks_per_seq;
   if (a.max_q_len == 1) blocks = 1;
-  const int64_t ctas = (blocks * a.num_kv_heads + kBoundsWarps - 1) / kBoundsWarps;
-  if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  return launch_dependent(key_bounds_kernel<T, D, KV>, dim3(static_cast<unsigned>(ctas), a.num_seqs),
-                          dim3(kBoundsWarps * 32), 0, stream, a);
+  const int warps = a.num_kv_heads < kBoundsWarps ? a.num_kv_heads : kBoundsWarps;
+  return launch_dependent(key_bounds_kernel<T, D, KV>, dim3(static_cast<unsigned>(blocks), a.num_seqs),
+                          dim3(warps * 32), 0, stream, a);
 }
 
 template <typename T, int D>
