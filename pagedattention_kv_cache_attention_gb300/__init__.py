@@ -790,7 +790,10 @@ _bind = None
 def _native():
     """The module built from pa_bind.cpp."""
     global _bind
-    _load()  # (fails loudly where nothing is built)
+    _load()
+    if not os.path.exists(_build.BIND):
+        raise ImportError(f"{_build.BIND} is missing (it belongs to one version of torch): run "
+                          "`python -c 'import __graft_entry__ as g; g.build()'` first")
     spec = importlib.util.spec_from_file_location("pa_bind", _build.BIND)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)

@@ -4,7 +4,7 @@ Each translation unit under csrc/ is compiled by its own nvcc process, in
 parallel, then linked into one shared library with the CUDA runtime linked
 statically.  Beside it the C++ part of the Python binding (pa_bind.cpp) is
 compiled with g++ against the installed torch's headers.  Outputs (git-ignored):
-<package>/_build/libpa.so and <package>/_build/pa_bind.so.
+<package>/_build/libpa.so and <package>/_build/pa_bind-<torch's version>.so.
 """
 from __future__ import annotations
 
@@ -15,11 +15,14 @@ import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
+import torch
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libpa.so")
-BIND = os.path.join(OUT_DIR, "pa_bind.so")
+# (of one torch: another one's tensors may be laid out otherwise)
+BIND = os.path.join(OUT_DIR, f"pa_bind-{torch.__version__}.so")
 SOURCES = ("pa_api.cu", "pa_blocks.cu", "pa_cache.cu", "pa_cache_fp4.cu", "pa_decode.cu",
            "pa_decode_fp4.cu", "pa_decode_sparse.cu", "pa_prefill_fp4.cu", "pa_prefill_tc.cu",
            "pa_rope.cu", "pa_sparse.cu", "pa_static_ws.cu")
@@ -50,12 +53,10 @@ def _run(what: str, cmd) -> None:
 
 
 def _torch_dir() -> str:
-    import torch
     return os.path.dirname(torch.__file__)
 
 
 def _compile_bind() -> str:
-    import torch
     obj = os.path.join(OUT_DIR, "pa_bind.o")
     inc = os.path.join(_torch_dir(), "include")
     _run("g++ on pa_bind.cpp", [
@@ -95,7 +96,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _run("link of pa_bind.so", ["g++", "-shared", "-o", tmp, bind_obj, "-L" + OUT_DIR, "-l:libpa.so",
+    _run("link of the binding", ["g++", "-shared", "-o", tmp, bind_obj, "-L" + OUT_DIR, "-l:libpa.so",
                                 "-L" + os.path.join(_torch_dir(), "lib"), "-lc10", "-ltorch_cpu",
                                 "-ltorch_python", "-Wl,-rpath,$ORIGIN"])
     os.replace(tmp, BIND)

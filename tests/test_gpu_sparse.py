@@ -640,6 +640,30 @@ def test_all_blocks_kept_is_dense_decode(pa):  # noqa: F811
         check(b, dense, vvals, t, n, 0.09, 1.0, 1.0)
 
 
+@pytest.mark.parametrize("kv", ["16", "fp8", "fp4"])
+def test_native_binding_takes_what_fits(pa, kv):  # noqa: F811
+    """Not by way of the checks in Python."""
+    kind, native = list(END).index(kv), pa._native()
+    b = Batch(33, [40, 33], 2, 2, 64, 16, "bf16", kv)
+    gb, gs = pa.new_key_bounds(b.NB, 2, 64)
+    q = b.q.cuda()
+    both = torch.cat([q, q], 1)
+    slots, pos, table = dev(np.array([3, 20])), dev(np.array([0, 1])), pa.new_rope_table(4, 64)
+    vc = b.kc.clone()
+    assert native.rope(kind, q, both[:, :4], both[:, 4:6], both[:, 6:], b.kc, vc, slots, pos, table, 1, 0.5, False, None) == 0
+    bt, cl = dev(b.tables), dev(b.lens)
+    start = dev(np.array([0, 40, 73], np.int32))
+    assert native.key_bounds(kind, gb, gs, b.kc, bt, cl, None, 1, None) == 0
+    assert native.key_bounds(kind, gb, gs, b.kc, bt, cl, start, 40, torch.cuda.current_stream()) == 0
+    t = torch.zeros(2, 2, 2, dtype=torch.int32, device="cuda")
+    n = torch.zeros(2, 2, dtype=torch.int32, device="cuda")
+    assert native.select(t, n, q, gb, gs, bt, cl, 16, 40, 1, 1, None, 1, None) == 0
+    assert native.select(t, n, q, gb, gs, bt, cl, 16, 40, 2, 1, None, 1, None) == 1  # the call's own refusal
+    out = torch.zeros_like(q)
+    assert native.sparse(kind, out, q, b.kc, vc, t, n, 0.1, 1.0, 1, torch.cuda.current_stream().cuda_stream) == 0
+    assert pa.pa_device_errors() == 0
+
+
 def test_arguments_of_other_kinds(pa):  # noqa: F811
     """numpy numbers, a stream's handle, a stream object, single heads of any stride, one row of any
     stride: what the native binding leaves to the checks in Python."""
