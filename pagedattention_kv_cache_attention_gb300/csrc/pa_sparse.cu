@@ -132,7 +132,6 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) key_bounds_kernel(const Bou
   constexpr int kTake = KV == Kv::k16 ? 8 : 4;  // rows that a lane has in flight
   constexpr int kKeep = 2 * W * kLanes / 32;    // words that a lane ends with
   grid_dependency_wait();  // the keys may come from the kernel before
-  grid_launch_dependents();
   const int seq = blockIdx.y, lane = threadIdx.x & 31;
   const int bs = 1 << a.bs_log2;
   const int ctx = a.context_lens[seq];
@@ -312,7 +311,7 @@ template <typename T, int D> struct Queries {
 // (By integer dot products a row takes 64 of them for 16 blocks, at half rate, and
 // sums over lanes; the codes' three instructions for 4 of them here are shared by
 // the rows.  5 drafted tokens of 64 sequences, contexts of 512 to 4,096, 32 / 8
-// heads: 12.4 us, by dot products 16.8.)
+// heads: 12.4 us, by dot products 16.8, at the time.)
 //
 // The order of the 2 D codes in the product is one that lets a lane take 16
 // consecutive codes of a block: code 64 i + 16 c + 4 w + e is column c's e-th of
@@ -540,6 +539,8 @@ __device__ __forceinline__ void pick(const uint32_t (&k)[KPL], int n, int forced
 // sequence and one KV head: its warps score 16 blocks at a time for all rows, so
 // that bounds are read once for them; then a warp a row picks, with the row's keys
 // in registers and no barrier.
+// (Neither selection kernel lets the next one start early: its CTAs would wait on
+// the SMs that this one's are on; drafted rows back to back 12.6 us, 11.5 without.)
 template <typename T, int D, int KPL, int TILES, int NW>
 __global__ void __launch_bounds__(NW * 32, KPL == 8 ? 4 : 1) select_short_kernel(const SelectArgs a) {
   using U = Unit<D>;
@@ -553,7 +554,6 @@ __global__ void __launch_bounds__(NW * 32, KPL == 8 ? 4 : 1) select_short_kernel
   const int kvh = blockIdx.y, seq = blockIdx.z;
   const int bs = 1 << a.bs_log2, K = a.num_selected;
   grid_dependency_wait();  // queries, bounds and lengths may come from the kernel before
-  grid_launch_dependents();
   const Table table(a, seq);
   const int32_t *bt_row = table.row;
   int j0 = warp * U::kBlocks, e[2];
@@ -868,7 +868,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_long_kernel(const Select
   const int bs = 1 << a.bs_log2, K = a.num_selected;
   if (tid == 0) sh.lo = 0xffffffffu, sh.hi = 0;
   grid_dependency_wait();  // queries, bounds and lengths may come from the kernel before
-  grid_launch_dependents();
 
   const Table table(a, seq);
   const int32_t *bt_row = table.row;
@@ -1007,7 +1006,7 @@ cudaError_t launch_short(const SelectArgs &a, cudaStream_t stream) {
 
 // Which kernel (32 / 8 heads x 128, GPU time of a call).  Up to 256 candidates the
 // short one: 64 x 512 to 4,096 tokens 9.5 us (long, 256 threads: 10.2), 5 drafted
-// rows each 12.6 (34.5).  Up to 1,024 it keeps the calls with several rows a
+// rows each 11.5 (34.5).  Up to 1,024 it keeps the calls with several rows a
 // sequence, for which it reads the bounds once: 64 x 5 rows, 2,000 to 8,000 tokens,
 // 29 us (49); single rows take the long one: 64 x 2,000 to 8,000 15.3 us (20.6),
 // 256 of them 44 (56), one of 16,000 6.2 (20.9).  That one has 256 threads, four CTAs
