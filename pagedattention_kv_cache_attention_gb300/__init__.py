@@ -1049,9 +1049,10 @@ def pa_select_blocks(selected_tables: torch.Tensor, selected_lens: torch.Tensor,
     _check("pa_select_blocks", _sparse_fn("pa_select_blocks")(
         selected_tables.data_ptr(), selected_lens.data_ptr(), query.data_ptr(), bounds.data_ptr(),
         bound_scales.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
-        context_lens.data_ptr(), start, B, int(max_q_len), Hq, Hkv, d, int(block_size), NB,
-        int(max_context_len), picked[2], int(num_sink), int(num_recent), _dtype_code(query),
-        _stream(stream)))
+        # (no rows: empty tensors have no address)
+        context_lens.data_ptr(), start, B, int(max_q_len) if R else 0, Hq, Hkv, d,
+        int(block_size), NB, int(max_context_len), picked[2], int(num_sink), int(num_recent),
+        _dtype_code(query), _stream(stream)))
     return selected_tables, selected_lens
 
 

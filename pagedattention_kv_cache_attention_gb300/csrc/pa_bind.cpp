@@ -228,11 +228,12 @@ PyObject *select(PyObject *, PyObject *const *argv, Py_ssize_t n) {
     const at::Tensor *tables = a.tensor(5, at::kInt, 2), *lens = a.tensor(6, at::kInt, -1);
     const int32_t bs = a.integer(7), most = a.integer(8), sink = a.integer(9), recent = a.integer(10);
     const at::Tensor *start = a.none(11) ? nullptr : a.tensor(11, at::kInt, -1);
-    const int32_t max_q = a.integer(12);
+    int32_t max_q = a.integer(12);
     void *stream = a.stream(13);
     if (!a.ok) return kNoFit;
     const int64_t R = q->size(0), hq = q->size(1), d = q->size(2), B = lens->numel();
     const int64_t nb = bounds->size(0), hkv = bounds->size(1), K = picked->size(2);
+    if (R == 0) max_q = 0;  // no rows: empty tensors have no address
     a.want(bounds->size(2) == 2 && bounds->size(3) == d && scales->size(0) == nb &&
            scales->size(1) == hkv && picked->size(0) == R && picked->size(1) == hkv &&
            plens->size(0) == R && plens->size(1) == hkv && tables->size(0) == B &&

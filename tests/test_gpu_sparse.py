@@ -205,6 +205,24 @@ def test_select_for_chunks(pa, keep, sink, recent, G, dtype):  # noqa: F811
     assert pa.pa_device_errors() == 0
 
 
+def test_no_rows(pa):  # noqa: F811
+    """Sequences without new tokens alone, and no sequences."""
+    b = Batch(42, [40, 0], 2, 2, 64, 16, "fp16", q_lens=[0, 0])
+    b.all_bounds()
+    for most in (0, 5, np.int64(5)):
+        b.q_lens[0] = most
+        t, n = b.select(pa, 2, 1, 1)
+        assert t.shape == (0, 2, 2) and n.shape == (0, 2)
+        pa.pa_update_key_bounds(*pa.new_key_bounds(b.NB, 2, 64), b.kc, dev(b.tables), dev(b.lens), dev(b.start), most)
+    none = torch.zeros(0, 4, 64, dtype=torch.float16, device="cuda")
+    t = torch.zeros(0, 2, 2, dtype=torch.int32, device="cuda")
+    assert pa.pa_decode_sparse(none, none, b.kc, b.kc, t, t[..., 0], 0.1) is none
+    lens = torch.zeros(0, dtype=torch.int32, device="cuda")
+    pa.pa_select_blocks(t, t[..., 0], none, dev(b.bounds), dev(b.scales), t[:, 0], lens, 16, 40)
+    pa.pa_update_key_bounds(dev(b.bounds), dev(b.scales), b.kc, t[:, 0], lens)
+    assert pa.pa_device_errors() == 0
+
+
 @pytest.mark.parametrize("lens,keep", [([70000, 16, 33333], 128), ([16 * 9000], 1000), ([131072], 2), ([20001] * 3, 77)])
 @pytest.mark.parametrize("bs,d", [(16, 128), (32, 64)])
 def test_select_of_long_contexts(pa, lens, keep, bs, d):  # noqa: F811
@@ -539,6 +557,34 @@ def test_captured_steps_of_two_batches(pa):  # noqa: F811
             s.call()
         graphs.append(g)
     for _ in range(3):
+        for s, g in zip(steps, graphs):
+            s.draw()
+            s.out.zero_()
+            g.replay()
+            s.check()
+
+
+@pytest.mark.parametrize("longest", [9000, 70000])
+def test_long_steps_on_two_streams_and_captured(pa, longest):  # noqa: F811
+    """The selection in clusters: two batches at once, then each replayed."""
+    steps = [Step(pa, 27 + i, [longest - 700 * i, 60, 4300], 2, 4, 128, 16, "bf16", kv, 12, 2, 3)
+             for i, kv in enumerate(("16", "fp8"))]
+    streams = [torch.cuda.Stream() for _ in steps]
+    for s in steps:
+        s.draw()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, st in zip(steps, streams):
+            with torch.cuda.stream(st):
+                s.call()
+    torch.cuda.synchronize()
+    graphs = []
+    for s in steps:
+        s.check()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            s.call()
+    for _ in range(2):
         for s, g in zip(steps, graphs):
             s.draw()
             s.out.zero_()
