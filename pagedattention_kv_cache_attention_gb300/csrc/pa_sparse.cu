@@ -428,7 +428,9 @@ template <int D> struct Unit {
                           256 * __float2int_rn(acc[n][2 * b + 1] * 0x1p24f) - bias;
         key[n][b] = 0;
         if (ok[b])
-          key[n][b] = key_of(scale[b] < INFINITY ? __fmul_rn(__int2float_rn(total), scale[b]) : INFINITY);
+          // (+ 0: a scale of 0 gives 0, not -0, whose key is another)
+          key[n][b] = key_of(
+              scale[b] < INFINITY ? __fmul_rn(__int2float_rn(total), scale[b]) + 0.f : INFINITY);
       }
     }
   }

@@ -325,6 +325,18 @@ def test_select_with_odd_scores(pa):  # noqa: F811
         assert np.array_equal(t, wt) and np.array_equal(n, wn)
 
 
+@pytest.mark.parametrize("lens", [[16 * 60, 16 * 200], [16 * 1500]])
+def test_select_with_scales_of_zero(pa, lens):  # noqa: F811
+    b = Batch(19, lens, 2, 2, 64, 16, "fp16")
+    b.all_bounds()
+    b.scales[:] = 0  # scores 0 and -0 are equal: the first blocks
+    got, n = b.select(pa, 9, 1, 1)
+    want, wn = b.want(9, 1, 1)
+    assert np.array_equal(want[..., :8], np.broadcast_to(b.tables[:, None, :8], want[..., :8].shape))
+    assert np.array_equal(got, want) and np.array_equal(n, wn)
+    assert pa.pa_device_errors() == 0
+
+
 def test_select_of_bad_lengths_and_blocks(pa):  # noqa: F811
     b = Batch(8, [200, 300, 150], 2, 2, 64, 16, "bf16")
     b.all_bounds()
