@@ -501,7 +501,7 @@ pa_status pa_prefill_fp4(void *out, const void *query, const int32_t *query_star
  *
  * query, query_out  device, [num_tokens, num_q_heads, head_dim], rows
  *                   query_stride and query_out_stride elements apart; the same
- *                   memory for both (one stride, in place), or no overlap
+ *                   memory for both (in place; two strides are refused), or no overlap
  * key, value        as for pa_reshape_and_cache
  * positions         device int64 [num_tokens]
  * cos_sin           device fp32 [max_position, rotary_dim], 16-byte aligned

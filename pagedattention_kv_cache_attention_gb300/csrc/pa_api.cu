@@ -832,6 +832,9 @@ pa_status rope_impl(void *query_out, const void *query, const void *key, const v
       value_stride < kv_row || query_out_stride % 8 || query_stride % 8 || key_stride % 8 ||
       value_stride % 8)
     return PA_ERR_INVALID_ARG;
+  // (in place a token's row is its own alone)
+  if (query_out == query && query_out_stride != query_stride && num_tokens > 1)
+    return PA_ERR_INVALID_ARG;
   unsigned int *err = nullptr;
   if (error_word(&err) != cudaSuccess) return PA_ERR_CUDA;
   pa::RopeArgs a{};

@@ -152,6 +152,11 @@ def test_append_refusals(pa, over, want, end):
     assert status(pa, "pa_rope_and_cache" + end, ROPE, over, (1.0, 1.0) if end else None) == want
 
 
+@pytest.mark.parametrize("end", ["", "_fp8", "_fp4"])
+def test_append_in_place_has_one_stride(pa, end):
+    assert status(pa, "pa_rope_and_cache" + end, ROPE, dict(qs=520), (1.0, 1.0) if end else None) == 1
+
+
 @pytest.mark.parametrize("scales", [(0.0, 1.0), (1.0, -1.0), (math.nan, 1.0), (1.0, math.inf)])
 @pytest.mark.parametrize("end", ["_fp8", "_fp4"])
 def test_cache_scales_are_checked(pa, scales, end):
