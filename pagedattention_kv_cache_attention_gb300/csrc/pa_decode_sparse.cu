@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(NW * 32)
 // One instance of the kernel: its shared memory, and how many CTAs of it an SM
 // takes at least (by shared memory, and at most 136 registers a thread).
 template <typename T, int D, int NW, int S, bool F8, int NSUB> struct Instance {
-  static constexpr int kWarps = NW, kStepTokens = NSUB * kTile;
+  static constexpr int kStepTokens = NSUB * kTile;
   static constexpr size_t kStages = static_cast<size_t>(NW) * S * 2 * NSUB * Shape<D, F8>::kTileBytes;
   static constexpr size_t kSmem = 1024 + kStages + NW * S * 8;
   static constexpr int kPerSm = static_cast<int>(227 * 1024 / (kSmem + 1024));
