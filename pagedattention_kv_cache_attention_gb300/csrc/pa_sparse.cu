@@ -679,9 +679,8 @@ __device__ __forceinline__ void red_cluster_max(uint32_t addr, uint32_t v) {
 // places in order from keys[0] on.  For a whole CTA.  In a turn thread i takes
 // keys L i .. L i + L - 1, from one of its own on around (different lanes,
 // different banks).  ONE: one turn does (n <= NT L), the keys stay in registers.
-template <int D, int NT, int L, bool ONE>
-__device__ __forceinline__ void pick_long(const SelectArgs &a, SelectShared<D, NT> &sh, uint32_t *keys,
-                                          int n) {
+template <int NT, int L, bool ONE, typename Shared>
+__device__ __forceinline__ void pick_long(const SelectArgs &a, Shared &sh, uint32_t *keys, int n) {
   const int tid = threadIdx.x, lane = tid & 31;
   constexpr int kTurn = NT * L;
   const int first = lane * L / 32;
@@ -854,16 +853,23 @@ __device__ __forceinline__ void pick_long(const SelectArgs &a, SelectShared<D, N
   __syncthreads();
 }
 
-template <typename T, int D, int NT>
+// ROWS: rows of a sequence that a cluster scores at once, 1 or 4 (four rows are one
+// product); row r's keys gather in CTA r, which picks for it.  (4 rows of 4 contexts
+// of 32,768 to 131,072 tokens 20.0 us, 5 rows 33, where a cluster for each row took
+// 42.6 and 49.  Eight rows in two products: 25 us for the 5 rows, but as slow or up to
+// 12 % slower where more clusters are to be served than run at once.)
+template <typename T, int D, int NT, int ROWS>
 __global__ void __launch_bounds__(NT, 1024 / NT) select_long_kernel(const SelectArgs a) {
   using U = Unit<D>;
+  static_assert(ROWS == 1 || ROWS == 4, "of one product");
+  using Shared = SelectShared<D, NT>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  SelectShared<D, NT> &sh = *reinterpret_cast<SelectShared<D, NT> *>(smem_raw);
-  uint32_t *keys = reinterpret_cast<uint32_t *>(smem_raw + sizeof(SelectShared<D, NT>));
+  Shared &sh = *reinterpret_cast<Shared *>(smem_raw);
+  uint32_t *keys = reinterpret_cast<uint32_t *>(smem_raw + sizeof(Shared));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   const int rank = static_cast<int>(blockIdx.x) % a.cluster;
-  const int t = static_cast<int>(blockIdx.x) / a.cluster;  // row of the sequence's chunk
+  const int t0 = static_cast<int>(blockIdx.x) / a.cluster * ROWS;  // first row of the sequence's
   // (heads last: neighbouring clusters are of different sequences, so that the
   // long ones do not meet on the same SMs)
   const int seq = blockIdx.y, kvh = blockIdx.z;
@@ -876,23 +882,27 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_long_kernel(const Select
   Queries<T, D> q;  // (a row of its own needs no length to be found)
   if (!a.query_start && warp == 0) q.load(a, seq, kvh, lane);
   SelectRows rows;
-  if (!rows.load(a, seq, tid == 0 && blockIdx.x == 0 && kvh == 0) || t >= rows.rows)
+  if (!rows.load(a, seq, tid == 0 && blockIdx.x == 0 && kvh == 0) || t0 >= rows.rows)
     return;  // (the whole cluster)
-  const int64_t row = rows.row0 + t;
-  const int seen = rows.base + t, n = (seen + bs - 1) >> a.bs_log2;
-  int32_t *out = a.tables + (row * a.num_kv_heads + kvh) * K;
-  int32_t *out_len = a.lens + row * a.num_kv_heads + kvh;
-  if (n <= K) {  // all of them
-    if (rank == 0) {
-      for (int i = tid; i < K; i += NT) out[i] = i < n ? bt_row[i] : -1;
-      if (tid == 0) *out_len = seen;
-    }
+  const int count = ROWS == 1 ? 1 : min(ROWS, rows.rows - t0);
+  // of row r < count: the tokens and blocks that it sees, more than the row before
+  auto seen_by = [&](int r) { return rows.base + t0 + r; };
+  auto blocks_of = [&](int r) { return (seen_by(r) + bs - 1) >> a.bs_log2; };
+  auto cell_of = [&](int r) { return (rows.row0 + t0 + r) * a.num_kv_heads + kvh; };
+  auto take_all = [&](int r) {
+    const int n = blocks_of(r);
+    for (int i = tid; i < K; i += NT) a.tables[cell_of(r) * K + i] = i < n ? bt_row[i] : -1;
+    if (tid == 0) a.lens[cell_of(r)] = seen_by(r);
+  };
+  const int most = blocks_of(count - 1);
+  if (most <= K) {
+    for (int r = rank; r < count; r += a.cluster) take_all(r);
     return;  // (the whole cluster)
   }
   // CTAs that have work; the others make room (a CTA that has left counts as
   // arrived at the cluster's barriers)
-  const int units = (n + U::kBlocks - 1) / U::kBlocks;
-  const int ctas = min(a.cluster, (units + a.units_per_cta - 1) / a.units_per_cta);
+  const int units = (most + U::kBlocks - 1) / U::kBlocks;
+  const int ctas = max(count, min(a.cluster, (units + a.units_per_cta - 1) / a.units_per_cta));
   if (rank >= ctas) return;
   if (ctas > 1) cluster_arrive();
   // the warp's units, `step` blocks apart; the next one's entries are read while one
@@ -902,31 +912,33 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_long_kernel(const Select
   table.entries(j0 + g, e);
   U unit;
   auto fetch = [&] {
-    const int phys[2] = {Table::block(a, e[0], j0 + g, n), Table::block(a, e[1], j0 + 8 + g, n)};
+    const int phys[2] = {Table::block(a, e[0], j0 + g, most), Table::block(a, e[1], j0 + 8 + g, most)};
     unit.load(a, kvh, phys, c);
-    if (j0 + step < n) table.entries(j0 + step + g, e);
+    if (j0 + step < most) table.entries(j0 + step + g, e);
   };
   // (four warps make the weights, the others' first loads are under way meanwhile)
   if (warp < 4) {
-    if (a.query_start && warp == 0) q.load(a, row, kvh, lane);
-    sh.weights.put(warp == 0 ? &q : nullptr, warp, lane);
-  } else if (j0 < n) {
+    if (a.query_start && warp < count) q.load(a, rows.row0 + t0 + warp, kvh, lane);
+    sh.weights.put(warp < count ? &q : nullptr, warp, lane);
+  } else if (j0 < most) {
     fetch();
   }
   __syncthreads();
-  if (ctas > 1) cluster_wait();  // the first CTA has started: its shared memory is there
-  const uint32_t keys_at = ctas > 1 ? cluster_addr(keys, 0) : 0;
+  if (ctas > 1) cluster_wait();  // the CTAs that pick have started: their shared memory is there
+  // the lane's row c: its blocks (none if there is no such row), where its keys go
+  const int n_of = c < count ? blocks_of(c) : 0;
+  const uint32_t keys_at = ctas > 1 ? cluster_addr(keys, c < count ? c : 0) : 0;
   uint32_t lo = 0xffffffffu, hi = 0;  // of the keys that are not forced
-  for (bool there = warp >= 4; j0 < n; j0 += step, there = false) {
+  for (bool there = warp >= 4; j0 < most; j0 += step, there = false) {
     if (!there) fetch();
     uint32_t key[1][2];
     unit.template keys<1>(&sh.weights, lane, key);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const int j = j0 + 8 * b + g;
-      if (c == 0 && j < n) {
+      if (j < n_of) {
         uint32_t k = key[0][b];
-        if (j < a.num_sink || j >= n - a.num_recent) {
+        if (j < a.num_sink || j >= n_of - a.num_recent) {
           k = kForced;
         } else {
           lo = min(lo, k);
@@ -939,38 +951,55 @@ __global__ void __launch_bounds__(NT, 1024 / NT) select_long_kernel(const Select
       }
     }
   }
-  lo = __reduce_min_sync(kAll, lo);
-  hi = __reduce_max_sync(kAll, hi);
-  if (lane == 0) {
+  if constexpr (ROWS == 1) {
+    lo = __reduce_min_sync(kAll, lo);
+    hi = __reduce_max_sync(kAll, hi);
+  } else {
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      lo = min(lo, __shfl_xor_sync(kAll, lo, off));
+      hi = max(hi, __shfl_xor_sync(kAll, hi, off));
+    }
+  }
+  if (lane < count) {
     if (ctas > 1) {
-      red_cluster_min(cluster_addr(&sh.lo, 0), lo);
-      red_cluster_max(cluster_addr(&sh.hi, 0), hi);
+      red_cluster_min(cluster_addr(&sh.lo, lane), lo);
+      red_cluster_max(cluster_addr(&sh.hi, lane), hi);
     } else {
       atomicMin(&sh.lo, lo);
       atomicMax(&sh.hi, hi);
     }
   }
   if (ctas > 1) cluster_sync(); else __syncthreads();
-  if (rank != 0) return;
+  if (rank >= count) return;
+  const int r = ROWS == 1 ? 0 : rank, n = blocks_of(r);
+  if (ROWS > 1 && n <= K) {
+    take_all(r);
+    return;
+  }
   if (n <= NT * 4)
-    pick_long<D, NT, 4, true>(a, sh, keys, n);
+    pick_long<NT, 4, true>(a, sh, keys, n);
   else if (n <= NT * kRunKeys)
-    pick_long<D, NT, kRunKeys, true>(a, sh, keys, n);
+    pick_long<NT, kRunKeys, true>(a, sh, keys, n);
   else
-    pick_long<D, NT, kRunKeys, false>(a, sh, keys, n);
+    pick_long<NT, kRunKeys, false>(a, sh, keys, n);
+  int32_t *out = a.tables + cell_of(r) * K;
   for (int i = tid; i < K; i += NT) out[i] = bt_row[keys[i]];
-  if (tid == 0) *out_len = K * bs - (keys[K - 1] == static_cast<uint32_t>(n - 1) ? n * bs - seen : 0);
+  if (tid == 0)
+    a.lens[cell_of(r)] =
+        K * bs - (keys[K - 1] == static_cast<uint32_t>(n - 1) ? n * bs - seen_by(r) : 0);
 }
 
-template <typename T, int D, int NT> cudaError_t launch_long(SelectArgs a, cudaStream_t stream) {
+template <typename T, int D, int NT, int ROWS> cudaError_t launch_long(SelectArgs a, cudaStream_t stream) {
   const size_t smem = sizeof(SelectShared<D, NT>) + static_cast<size_t>(a.max_candidates) * 4;
   constexpr size_t most = sizeof(SelectShared<D, NT>) + kMaxCandidates * 4;
   static_assert(most <= 227 * 1024, "shared memory");
-  auto kern = select_long_kernel<T, D, NT>;
+  auto kern = select_long_kernel<T, D, NT, ROWS>;
   static SmemLimitOnce smem_limit;
   const cudaError_t e = smem_limit.ensure(kern, most);
   if (e != cudaSuccess) return e;
-  const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * a.max_q_len;
+  const int tiles = (a.max_q_len - 1) / ROWS + 1;
+  const int64_t clusters = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * tiles;
   // CTAs that may share a row: as many as run at once (2 kSms), each with 128 blocks
   // at least; twice as many where each has 512, since those of the shorter
   // contexts then leave at once.  (32 / 8 heads x 128, one row a sequence, with this
@@ -978,18 +1007,18 @@ template <typename T, int D, int NT> cudaError_t launch_long(SelectArgs a, cudaS
   // 16 x 1,000 to 16,000 10.3 and 12.0, 16 x 16,000 to 65,000 25.4 and 43.6; with twice
   // as many from 128 blocks on 8 x 16,000 take 16.3 us in place of 8.5, with only as
   // many as run at once 16 x 16,000 to 65,000 29.8 in place of 25.4.)
-  a.cluster = 1;
-  for (int c = 1; c < kMaxSelCluster; c *= 2) {
-    const int64_t ctas = 2 * c * rows;
+  a.cluster = ROWS;  // a CTA for each row that a cluster picks for
+  for (int c = a.cluster; c < kMaxSelCluster; c *= 2) {
+    const int64_t ctas = 2 * c * clusters;
     if (!(ctas <= 2 * kSms && a.max_candidates >= 128 * c) &&
         !(ctas <= 4 * kSms && a.max_candidates >= 512 * c))
       break;
     a.cluster = 2 * c;
   }
   // where they are more than run at once, four units a warp
-  a.units_per_cta = NT / 32 * (a.cluster * rows <= 2 * kSms ? 1 : 4);
+  a.units_per_cta = NT / 32 * (a.cluster * clusters <= 2 * kSms ? 1 : 4);
   return launch_clusters(a.cluster, kern,
-                         dim3(static_cast<unsigned>(a.cluster * a.max_q_len), a.num_seqs, a.num_kv_heads),
+                         dim3(static_cast<unsigned>(a.cluster * tiles), a.num_seqs, a.num_kv_heads),
                          dim3(NT), smem, stream, a);
 }
 
@@ -1006,24 +1035,40 @@ cudaError_t launch_short(const SelectArgs &a, cudaStream_t stream) {
                           dim3(tiles, a.num_kv_heads, a.num_seqs), dim3(NW * 32), smem, stream, a);
 }
 
-// Which kernel (32 / 8 heads x 128, GPU time of a call).  Up to 256 candidates the
-// short one: 64 x 512 to 4,096 tokens 9.5 us (long, 256 threads: 10.2), 5 drafted
-// rows each 11.5 (34.5).  Up to 1,024 it keeps the calls with several rows a
-// sequence, for which it reads the bounds once: 64 x 5 rows, 2,000 to 8,000 tokens,
-// 29 us (49); single rows take the long one: 64 x 2,000 to 8,000 15.3 us (20.6),
-// 256 of them 44 (56), one of 16,000 6.2 (20.9).  That one has 256 threads, four CTAs
-// an SM, while their registers hold the keys of the longest context, and else 512:
-// 64 x 2,000 to 8,000 tokens 15.3 us (512: 20.6), 200 x 8,000 to 30,000 95 (106);
-// 131,072 tokens 12.2 us with 512 and 15.0 with 256, 4 x 5 rows of up to 131,072 49
-// and 75.
+// Which kernel (32 / 8 heads x 128, GPU time of a call).
+// Single rows: up to 256 candidates the short one, 64 x 512 to 4,096 tokens 9.5 us
+// (long, 256 threads: 10.2); above, the long one, 64 x 2,000 to 8,000 tokens 15.3 us
+// (20.6), 256 of them 44 (56), one of 16,000 6.2 (20.9).
+// The long one has 256 threads, four CTAs an SM, while their registers hold the keys
+// of the longest context, and else 512: 64 x 2,000 to 8,000 tokens 15.3 us (512:
+// 20.6), 200 x 8,000 to 30,000 95 (106); 131,072 tokens 12.2 us with 512 and 15.0
+// with 256.
+// Several rows a sequence: up to 256 candidates the short one, 5 rows of 64 x 512 to
+// 4,096 tokens 11.5 us (34.5 with a cluster for each row); up to 1,024 too, where
+// there are so many tiles of four rows that the long one's clusters would wait for
+// one another: 64 x 2,000 to 8,000 tokens, 4 rows 22.4 us (long 34), 5 rows 27.3 (55);
+// 200 x 4,000 to 9,000, 4 rows 69 (100); 16 x 4,000 to 16,000, 5 rows 18.2 (22.4).
+// The long one for fewer: 8 x 2,000 to 8,000, 2 rows 7.8 us (short 12.9); 8 x 4,000
+// to 16,000, 8 rows 13.1 (18.4); 32 x 8,000 to 16,000, 4 rows 25.3 (38.3).
 template <typename T, int D> cudaError_t launch_select_t(const SelectArgs &a, cudaStream_t stream) {
-  if (a.max_candidates > 256 * kRunKeys) return launch_long<T, D, 512>(a, stream);
-  if (a.max_candidates > (a.max_q_len > 1 ? 1024 : 256)) return launch_long<T, D, 256>(a, stream);
-  if (a.max_q_len > 4)
-    return a.max_candidates > 256 ? launch_short<T, D, 32, 2, 8>(a, stream)
-                                  : launch_short<T, D, 8, 2, 8>(a, stream);
-  return a.max_candidates > 256 ? launch_short<T, D, 32, 1, 4>(a, stream)
-                                : launch_short<T, D, 8, 1, 4>(a, stream);
+  if (a.max_q_len == 1) {
+    if (a.max_candidates > 256 * kRunKeys) return launch_long<T, D, 512, 1>(a, stream);
+    if (a.max_candidates > 256) return launch_long<T, D, 256, 1>(a, stream);
+    return launch_short<T, D, 8, 1, 4>(a, stream);
+  }
+  if (a.max_candidates > 256 * kRunKeys) return launch_long<T, D, 512, 4>(a, stream);
+  const int64_t tiles = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * ((a.max_q_len - 1) / 4 + 1);
+  const int few = a.max_candidates <= 512 ? kSms / 2 : a.max_q_len > 4 ? kSms : 2 * kSms;
+  if (a.max_candidates > 1024 || (a.max_candidates > 256 && tiles <= few))
+    return launch_long<T, D, 256, 4>(a, stream);
+  if (a.max_q_len > 4) {
+    if (a.max_candidates > 512) return launch_short<T, D, 32, 2, 8>(a, stream);
+    if (a.max_candidates > 256) return launch_short<T, D, 16, 2, 8>(a, stream);
+    return launch_short<T, D, 8, 2, 8>(a, stream);
+  }
+  if (a.max_candidates > 512) return launch_short<T, D, 32, 1, 4>(a, stream);
+  if (a.max_candidates > 256) return launch_short<T, D, 16, 1, 4>(a, stream);
+  return launch_short<T, D, 8, 1, 4>(a, stream);
 }
 
 }  // namespace

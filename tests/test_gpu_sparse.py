@@ -234,6 +234,31 @@ def test_select_of_long_contexts(pa, lens, keep, bs, d):  # noqa: F811
     assert np.array_equal(t, wt) and np.array_equal(n, wn)
 
 
+@pytest.mark.parametrize("lens,q_lens,keep", [
+    ([20000, 70, 30017], [5, 3, 4], 128), ([40000, 33, 17000, 0], [9, 1, 0, 0], 70), ([66000], [2], 500),
+    ([16 * 1100 + 2] * 3, [4, 3, 8], 1100), ([70001] * 2, [1, 7], 9)])
+@pytest.mark.parametrize("bs,d,G,dtype", [(16, 128, 4, "bf16"), (32, 64, 1, "fp16")])
+def test_select_for_drafts_of_long_contexts(pa, lens, q_lens, keep, bs, d, G, dtype):  # noqa: F811
+    b = Batch(23, lens, 2, G, d, bs, dtype, "16", q_lens)
+    b.all_bounds()
+    got, n = b.select(pa, keep, 1, 4)
+    want, wn = b.want(keep, 1, 4)
+    assert np.array_equal(got, want) and np.array_equal(n, wn)
+    assert pa.pa_device_errors() == 0
+
+
+@pytest.mark.parametrize("seqs,q", [(3, 3), (3, 7), (40, 3), (40, 7), (160, 4)])
+@pytest.mark.parametrize("longest,bs", [(16 * 400 + 3, 16), (16 * 513, 16), (16 * 1024 - 9, 16), (32 * 700 + 1, 32)])
+def test_select_for_drafts_of_many_and_few_sequences(pa, seqs, q, longest, bs):  # noqa: F811
+    lens = [longest, longest - 1000] + [70 + 11 * i % 300 for i in range(seqs - 2)]
+    b = Batch(29, lens, 2, 2, 64, bs, "bf16", "16", [1 + (i + q) % q for i in range(1, seqs)] + [q])
+    b.all_bounds()
+    got, n = b.select(pa, 9, 1, 2)
+    want, wn = b.want(9, 1, 2)
+    assert np.array_equal(got, want) and np.array_equal(n, wn)
+    assert pa.pa_device_errors() == 0
+
+
 @pytest.mark.parametrize("n,keep", [(3000, 600), (2000, 700), (8192, 128), (8192, 500), (5000, 90), (1500, 1499)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_select_where_large_scores_are_neighbours(pa, n, keep, d):  # noqa: F811
