@@ -56,16 +56,20 @@ def _torch_dir() -> str:
     return os.path.dirname(torch.__file__)
 
 
-def _compile_bind() -> str:
-    obj = os.path.join(OUT_DIR, "pa_bind.o")
+def _compile_bind(src: str, obj: str) -> None:
     inc = os.path.join(_torch_dir(), "include")
     _run("g++ on pa_bind.cpp", [
         "g++", "-std=c++17", "-O2", "-fPIC", "-Wall",
         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", inc,
         "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
-        "-isystem", sysconfig.get_paths()["include"],
-        "-c", os.path.join(CSRC, "pa_bind.cpp"), "-o", obj])
-    return obj
+        "-isystem", sysconfig.get_paths()["include"], "-I", CSRC, "-c", src, "-o", obj])
+
+
+def _link_bind(obj: str, lib_dir: str, out: str) -> None:
+    """`out` from `obj` and the libpa.so of lib_dir, which it looks for beside itself."""
+    _run("link of the binding", ["g++", "-shared", "-o", out, obj, "-L" + lib_dir, "-l:libpa.so",
+                                "-L" + os.path.join(_torch_dir(), "lib"), "-lc10", "-ltorch_cpu",
+                                "-ltorch_python", "-Wl,-rpath,$ORIGIN"])
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -87,18 +91,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        bind = ex.submit(_compile_bind)
+        bind_obj = os.path.join(OUT_DIR, "pa_bind.o")
+        bind = ex.submit(_compile_bind, os.path.join(CSRC, "pa_bind.cpp"), bind_obj)
         objs = list(ex.map(compile_one, SOURCES))
-        bind_obj = bind.result()
+        bind.result()
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [cc, "-shared", *ARCH, "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _run("link of the binding", ["g++", "-shared", "-o", tmp, bind_obj, "-L" + OUT_DIR, "-l:libpa.so",
-                                "-L" + os.path.join(_torch_dir(), "lib"), "-lc10", "-ltorch_cpu",
-                                "-ltorch_python", "-Wl,-rpath,$ORIGIN"])
+    _link_bind(bind_obj, OUT_DIR, tmp)
     os.replace(tmp, BIND)
     return LIB
 

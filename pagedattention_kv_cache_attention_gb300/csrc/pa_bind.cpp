@@ -133,12 +133,18 @@ template <typename F> PyObject *call(PyObject *const *a, Py_ssize_t n, Py_ssize_
   return PyLong_FromLong(st);
 }
 
-template <typename F> long launch(F &&f) {
-  pa_status st;
-  Py_BEGIN_ALLOW_THREADS
-  st = f();
-  Py_END_ALLOW_THREADS
-  return static_cast<long>(st);
+// The GIL is given up for its life, and taken again however that ends.
+struct Unlocked {
+  PyThreadState *state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// The C call.  Its arguments are values by now: what asks a tensor for something
+// (its address: a tensor without memory of its own throws) is done by the caller,
+// with the GIL.
+template <typename... P, typename... A> long launch(pa_status (*f)(P...), A... args) {
+  const Unlocked unlocked;
+  return static_cast<long>(f(args...));
 }
 
 // kind, query_out, query, key, value, k_cache, v_cache, slot_mapping, positions, cos_sin,
@@ -168,18 +174,16 @@ PyObject *rope(PyObject *, PyObject *const *argv, Py_ssize_t n) {
     if (!a.ok) return kNoFit;
     // (the stride of a single row is not looked at)
     auto stride = [&](const at::Tensor *t) { return T > 1 ? t->stride(0) : t->size(1) * d; };
-    return launch([&] {
-      auto with = [&](auto f, auto... scales) {
-        return f(qo->data_ptr(), q->data_ptr(), k->data_ptr(), v->data_ptr(), stride(qo), stride(q),
-                 stride(k), stride(v), kc->data_ptr(), vc->data_ptr(),
-                 static_cast<const int64_t *>(slots->data_ptr()),
-                 static_cast<const int64_t *>(pos->data_ptr()),
-                 static_cast<const float *>(table->data_ptr()), T, hq, hkv, d, table->size(1),
-                 inter ? 1 : 0, bs, nb, table->size(0), code_of(type), scales..., stream);
-      };
-      return kind == k16 ? with(pa_rope_and_cache)
-                         : with(kind == kFp8 ? pa_rope_and_cache_fp8 : pa_rope_and_cache_fp4, ks, vs);
-    });
+    auto with = [&](auto f, auto... scales) {
+      return launch(f, qo->data_ptr(), q->data_ptr(), k->data_ptr(), v->data_ptr(), stride(qo),
+                    stride(q), stride(k), stride(v), kc->data_ptr(), vc->data_ptr(),
+                    static_cast<const int64_t *>(slots->data_ptr()),
+                    static_cast<const int64_t *>(pos->data_ptr()),
+                    static_cast<const float *>(table->data_ptr()), T, hq, hkv, d, table->size(1),
+                    inter ? 1 : 0, bs, nb, table->size(0), code_of(type), scales..., stream);
+    };
+    return kind == k16 ? with(pa_rope_and_cache)
+                       : with(kind == kFp8 ? pa_rope_and_cache_fp8 : pa_rope_and_cache_fp4, ks, vs);
   });
 }
 
@@ -203,17 +207,16 @@ PyObject *key_bounds(PyObject *, PyObject *const *argv, Py_ssize_t n) {
            (!start || start->numel() == B + 1) && fits32(B) && fits32(heads) && fits32(d) &&
            fits32(bs) && fits32(tables->size(1)));
     if (!a.ok) return kNoFit;
-    return launch([&] {
-      auto with = [&](auto f, auto... type_code) {
-        return f(static_cast<int8_t *>(bounds->data_ptr()), static_cast<float *>(scales->data_ptr()),
-                 kc->data_ptr(), static_cast<const int32_t *>(tables->data_ptr()), tables->size(1),
-                 static_cast<const int32_t *>(lens->data_ptr()),
-                 start ? static_cast<const int32_t *>(start->data_ptr()) : nullptr, B, max_q, heads,
-                 d, bs, nb, type_code..., stream);
-      };
-      return kind == k16 ? with(pa_update_key_bounds, code_of(type))
-                         : with(kind == kFp8 ? pa_update_key_bounds_fp8 : pa_update_key_bounds_fp4);
-    });
+    auto with = [&](auto f, auto... type_code) {
+      return launch(f, static_cast<int8_t *>(bounds->data_ptr()),
+                    static_cast<float *>(scales->data_ptr()), kc->data_ptr(),
+                    static_cast<const int32_t *>(tables->data_ptr()), tables->size(1),
+                    static_cast<const int32_t *>(lens->data_ptr()),
+                    start ? static_cast<const int32_t *>(start->data_ptr()) : nullptr, B, max_q,
+                    heads, d, bs, nb, type_code..., stream);
+    };
+    return kind == k16 ? with(pa_update_key_bounds, code_of(type))
+                       : with(kind == kFp8 ? pa_update_key_bounds_fp8 : pa_update_key_bounds_fp4);
   });
 }
 
@@ -240,17 +243,14 @@ PyObject *select(PyObject *, PyObject *const *argv, Py_ssize_t n) {
            (start ? start->numel() == B + 1 : R == B) && fits32(B) && fits32(hq) && fits32(hkv) &&
            fits32(d) && fits32(K) && fits32(tables->size(1)));
     if (!a.ok) return kNoFit;
-    return launch([&] {
-      return pa_select_blocks(static_cast<int32_t *>(picked->data_ptr()),
-                              static_cast<int32_t *>(plens->data_ptr()), q->data_ptr(),
-                              static_cast<const int8_t *>(bounds->data_ptr()),
-                              static_cast<const float *>(scales->data_ptr()),
-                              static_cast<const int32_t *>(tables->data_ptr()), tables->size(1),
-                              static_cast<const int32_t *>(lens->data_ptr()),
-                              start ? static_cast<const int32_t *>(start->data_ptr()) : nullptr, B,
-                              max_q, hq, hkv, d, bs, nb, most, K, sink, recent, code_of(type),
-                              stream);
-    });
+    return launch(pa_select_blocks, static_cast<int32_t *>(picked->data_ptr()),
+                  static_cast<int32_t *>(plens->data_ptr()), q->data_ptr(),
+                  static_cast<const int8_t *>(bounds->data_ptr()),
+                  static_cast<const float *>(scales->data_ptr()),
+                  static_cast<const int32_t *>(tables->data_ptr()), tables->size(1),
+                  static_cast<const int32_t *>(lens->data_ptr()),
+                  start ? static_cast<const int32_t *>(start->data_ptr()) : nullptr, B, max_q, hq,
+                  hkv, d, bs, nb, most, K, sink, recent, code_of(type), stream);
   });
 }
 
@@ -274,16 +274,14 @@ PyObject *sparse(PyObject *, PyObject *const *argv, Py_ssize_t n) {
            picked->size(1) == hkv && plens->size(0) == R && plens->size(1) == hkv && fits32(R) &&
            fits32(hq) && fits32(hkv) && fits32(d) && fits32(K) && fits32(bs));
     if (!a.ok) return kNoFit;
-    return launch([&] {
-      auto with = [&](auto f, auto... scales) {
-        return f(out->data_ptr(), q->data_ptr(), kc->data_ptr(), vc->data_ptr(),
-                 static_cast<const int32_t *>(picked->data_ptr()),
-                 static_cast<const int32_t *>(plens->data_ptr()), R, K, hq, hkv, d, bs, nb, scale,
-                 scales..., code_of(type), stream);
-      };
-      return kind == k16 ? with(pa_decode_sparse)
-                         : with(kind == kFp8 ? pa_decode_sparse_fp8 : pa_decode_sparse_fp4, ks, vs);
-    });
+    auto with = [&](auto f, auto... scales) {
+      return launch(f, out->data_ptr(), q->data_ptr(), kc->data_ptr(), vc->data_ptr(),
+                    static_cast<const int32_t *>(picked->data_ptr()),
+                    static_cast<const int32_t *>(plens->data_ptr()), R, K, hq, hkv, d, bs, nb,
+                    scale, scales..., code_of(type), stream);
+    };
+    return kind == k16 ? with(pa_decode_sparse)
+                       : with(kind == kFp8 ? pa_decode_sparse_fp8 : pa_decode_sparse_fp4, ks, vs);
   });
 }
 
