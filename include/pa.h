@@ -509,7 +509,8 @@ pa_status pa_prefill_fp4(void *out, const void *query, const int32_t *query_star
  * was.  So is one whose slot is past the pool (PA_DEVERR_BAD_SLOT) or whose
  * position is outside [0, max_position) (PA_DEVERR_BAD_POS).  Slots must be
  * distinct.  rotary_dim: a multiple of 16, at most head_dim.  Strides in
- * elements, multiples of 8; pointers 16-byte aligned; num_q_heads is any number.
+ * elements, multiples of 8; pointers 16-byte aligned; num_q_heads need be no
+ * multiple of num_kv_heads, both at most 2^20 (num_kv_heads of FP4 caches 65535).
  */
 pa_status pa_rope_and_cache(void *query_out, const void *query, const void *key,
                             const void *value, int64_t query_out_stride, int64_t query_stride,

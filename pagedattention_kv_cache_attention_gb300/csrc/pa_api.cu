@@ -819,6 +819,8 @@ pa_status rope_impl(void *query_out, const void *query, const void *key, const v
   constexpr int32_t kMaxHeads = 1 << 20;
   if (num_q_heads > kMaxHeads || num_kv_heads > kMaxHeads || num_blocks >= int64_t{1} << 32)
     return PA_ERR_UNSUPPORTED;
+  // (FP4 caches: offsets within a block, all heads, are 32-bit)
+  if (kv == pa::Kv::kFp4 && num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
   if (num_tokens == 0) return PA_OK;
   if (!query_out || !query || !key || !value || !k_cache || !v_cache || !slot_mapping ||
       !positions || !cos_sin)

@@ -157,6 +157,14 @@ def test_append_in_place_has_one_stride(pa, end):
     assert status(pa, "pa_rope_and_cache" + end, ROPE, dict(qs=520), (1.0, 1.0) if end else None) == 1
 
 
+@pytest.mark.parametrize("heads", [65536, 2 ** 20])
+def test_append_of_more_heads_than_an_fp4_block_has_offsets_for(pa, heads):
+    """The heads of an FP4 block lie 2,304 bytes apart at most, and offsets within it are 32-bit: 2^20 heads
+    pass 2^31 bytes.  The limit is that of pa_reshape_and_cache_fp4."""
+    over = dict(Hkv=heads, ks=heads * 128, vs=heads * 128)
+    assert status(pa, "pa_rope_and_cache_fp4", ROPE, over, (1.0, 1.0)) == 2
+
+
 @pytest.mark.parametrize("scales", [(0.0, 1.0), (1.0, -1.0), (math.nan, 1.0), (1.0, math.inf)])
 @pytest.mark.parametrize("end", ["_fp8", "_fp4"])
 def test_cache_scales_are_checked(pa, scales, end):
