@@ -208,8 +208,9 @@ __global__ void __launch_bounds__(kBoundsWarps * 32) key_bounds_kernel(const Bou
       uint32_t word = 0;
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        // (2^-e is exact, and so is the product but for results below 2^-149)
-        const int c = none ? 0 : __float2int_ru(x[4 * q + b] * inv);
+        // (2^-e is exact, and so is the product but for one below 2^-126, which, rounded
+        // up, stays above 0 if it is above 0)
+        const int c = none ? 0 : __float2int_ru(__fmul_ru(x[4 * q + b], inv));
         word |= static_cast<uint32_t>((smallest ? -c : c) & 0xff) << (8 * b);
       }
       out[q] = word;

@@ -132,6 +132,26 @@ def test_bounds_of_odd_values(pa, dtype, d):  # noqa: F811
     assert np.isinf(s[13:16]).all() and (s[:2] == 0).all()
 
 
+@pytest.mark.parametrize("d,bs", [(64, 16), (128, 32)])
+def test_bounds_of_tiny_keys_beside_large_ones(pa, d, bs):  # noqa: F811
+    """Whatever is above zero has a bound above zero: keys whose quotient by the scale is below every fp32 number."""
+    x = np.zeros((3, 2, bs, d))
+    tiny = 2.0 ** np.arange(-133, -60)  # from bf16's smallest number on
+    rng = np.random.default_rng(77)
+    x[...] = rng.choice(tiny, x.shape) * rng.choice([-1.0, 0.0, 1.0], x.shape)
+    x[:, :, :, 5] = np.abs(x[:, :, :, 5]) + tiny[0]
+    x[:, :, :, 6] = -np.abs(x[:, :, :, 6]) - tiny[0]
+    x[0, :, 3, 9], x[1, :, 0, 9], x[2, :, bs - 1, 9] = 2.0 ** 127, -2.0 ** 120, 1.9 * 2.0 ** 126
+    t = torch.from_numpy(x).bfloat16()
+    tables, lens = np.arange(3, dtype=np.int32)[:, None], np.full(3, bs, np.int32)
+    b, s = np.zeros((3, 2, 2, d), np.int8), np.zeros((3, 2), np.float32)
+    S.update_bounds(b, s, t.double().numpy(), tables, lens, [bs] * 3)
+    gb, gs = pa.new_key_bounds(3, 2, d)
+    pa.pa_update_key_bounds(gb, gs, t.cuda(), dev(tables), dev(lens))
+    assert np.array_equal(gs.cpu().numpy(), s) and np.array_equal(gb.cpu().numpy(), b)
+    assert (b[:, :, :, 5] == [1, 0]).all() and (b[:, :, :, 6] == [0, -1]).all()
+
+
 @pytest.mark.parametrize("kv", ["fp8", "fp4"])
 def test_bounds_of_nan_codes(pa, kv):  # noqa: F811
     """A NaN among a block's tokens gives the infinite scale; past the context it does not count."""
