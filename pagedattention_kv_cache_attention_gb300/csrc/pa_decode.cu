@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(NW * 32)
     // ---- online softmax in base 2 (log2(e) folded into the scale), one
     // reduction over all NSUB x 16 tokens of the step
     float p[NSUB][4];
-    softmax_step<NSUB, Sh::kMTiles>(sc, nvalid, g, scale_log2, m0, m1, l0, l1, acc, p);
+    softmax_step<NSUB, Sh::kMTiles>(sc, nvalid, g, scale_log2, scale_log2, m0, m1, l0, l1, acc, p);
 
 #pragma unroll
     for (int h = 0; h < NSUB; ++h) {

@@ -90,36 +90,6 @@ __device__ __forceinline__ void pv_subtile_8(const uint8_t *Vs, int nvalid, int 
   }
 }
 
-// bf16 queries beside FP8 keys: times the power of two that brings the largest
-// of the warp's into [2^14, 2^15), as fp16 (exact for every value down to 2^-31 of
-// the largest); returns the exponent.
-template <int N> __device__ __forceinline__ int queries_to_half(uint4 (&qf)[N]) {
-  float mx = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float2 v = Elem<__nv_bfloat16>::unpack(word_of(qf[i], w));
-      mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
-    }
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
-  const int ex = static_cast<int>((__float_as_uint(mx) >> 23) & 0xffu) - 127;
-  const int e = min(120, 14 - ex);
-  const float f = ldexpf(1.f, e);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    uint32_t h[4];
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float2 v = Elem<__nv_bfloat16>::unpack(word_of(qf[i], w));
-      h[w] = Elem<__half>::pack(v.x * f, v.y * f);
-    }
-    qf[i] = make_uint4(h[0], h[1], h[2], h[3]);
-  }
-  return e;
-}
-
 template <typename T, int D, int NW, int S, bool F8, int NSUB>
 __global__ void __launch_bounds__(NW * 32)
     sparse_decode_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -228,7 +198,7 @@ __global__ void __launch_bounds__(NW * 32)
   // query fragments of head g, in the order in which the keys are read
   const int G = a.group;
   uint4 qf[Sh::kQChunks];
-  float scale_log2 = a.scale_log2;
+  float scale0 = a.scale_log2, scale1 = a.scale_log2;  // of heads 2c, 2c + 1
   {
     const T *q = static_cast<const T *>(a.query) +
                  (static_cast<int64_t>(row) * a.num_q_heads + kvh * G + g) * D;
@@ -238,7 +208,7 @@ __global__ void __launch_bounds__(NW * 32)
       qf[i] = g < G ? *reinterpret_cast<const uint4 *>(q + ch * 8) : make_uint4(0, 0, 0, 0);
     }
     if constexpr (F8 && !std::is_same<T, __half>::value)
-      scale_log2 = ldexpf(scale_log2, -queries_to_half(qf));
+      column_scales(a.scale_log2, queries_to_half(qf), c, scale0, scale1);
   }
 
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2c, 2c + 1
@@ -269,7 +239,7 @@ __global__ void __launch_bounds__(NW * 32)
       else
         qk_subtile_16<MT, D>(stage + h * Sh::kTileBytes, qf, g, c, sc[h]);
     }
-    softmax_step<NSUB, Sh::kMTiles>(sc, nvalid, g, scale_log2, m0, m1, l0, l1, acc, p);
+    softmax_step<NSUB, Sh::kMTiles>(sc, nvalid, g, scale0, scale1, m0, m1, l0, l1, acc, p);
 #pragma unroll
     for (int h = 0; h < NSUB; ++h) {
       uint32_t pb0, pb1, pr0, pr1;

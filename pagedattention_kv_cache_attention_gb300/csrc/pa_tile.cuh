@@ -88,16 +88,53 @@ __device__ __forceinline__ void qk_subtile_16(const uint8_t *Ks, const uint4 (&q
 // dropped, far below what the fp32 accumulation resolves).  2^-inf = 0.
 __device__ __forceinline__ float softmax_exp2(float x) { return ex2_approx(x); }
 
-// One online-softmax step in base 2 (log2(e) is folded into scale_log2) over
-// the NSUB sub-tiles of a pipeline step, for the lane's columns 2c (m0, l0)
-// and 2c + 1 (m1, l1): tokens at or past nvalid[h] of sub-tile h get logit
+// bf16 queries beside FP8 keys, which are fp16 in the product: the lane's share of
+// column g times 2^e, as fp16, with e such that the column's largest magnitude lies
+// in [2^14, 2^15) (exact for every value down to 2^-31 of that: bf16 carries 8
+// significant bits, and fp16 holds 8 bits at every magnitude from 2^-17 up).
+// Returns e.  A column's own e: whatever another head of the group holds, an
+// infinity among it, leaves this one's queries as they are.
+template <int N> __device__ __forceinline__ int queries_to_half(uint4 (&qf)[N]) {
+  float mx = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float2 v = Elem<__nv_bfloat16>::unpack(word_of(qf[i], w));
+      mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
+    }
+  mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+  mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+  const int e = min(120, 14 + 127 - static_cast<int>((__float_as_uint(mx) >> 23) & 0xffu));
+  const float f = ldexpf(1.f, e);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint32_t h[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float2 v = Elem<__nv_bfloat16>::unpack(word_of(qf[i], w));
+      h[w] = Elem<__half>::pack(v.x * f, v.y * f);
+    }
+    qf[i] = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+  return e;
+}
+// The softmax scales of the lane's columns 2c and 2c + 1, with 2^-e of each.
+__device__ __forceinline__ void column_scales(float scale_log2, int e, int c, float &s0, float &s1) {
+  s0 = ldexpf(scale_log2, -__shfl_sync(kFull, e, 8 * c));      // a lane of column 2c
+  s1 = ldexpf(scale_log2, -__shfl_sync(kFull, e, 8 * c + 4));  // of column 2c + 1
+}
+
+// One online-softmax step in base 2 (log2(e) is folded into the scales) over
+// the NSUB sub-tiles of a pipeline step, for the lane's columns 2c (s0, m0, l0)
+// and 2c + 1 (s1, m1, l1): tokens at or past nvalid[h] of sub-tile h get logit
 // -inf; the running maxima take one butterfly reduction over the step's token
 // rows; the accumulator is rescaled only when some maximum grew.  The running
 // sums stay per lane (summed over the token rows at the end).  p receives the
 // step's probabilities 2^(x - m) in the S^T fragment layout.
 template <int NSUB, int MTILES>
 __device__ __forceinline__ void softmax_step(const float (&sc)[NSUB][4], const int (&nvalid)[NSUB],
-                                             int g, float scale_log2, float &m0, float &m1,
+                                             int g, float s0, float s1, float &m0, float &m1,
                                              float &l0, float &l1, float (&acc)[MTILES][4],
                                              float (&p)[NSUB][4]) {
   const float NEG_INF = -INFINITY;
@@ -106,10 +143,10 @@ __device__ __forceinline__ void softmax_step(const float (&sc)[NSUB][4], const i
 #pragma unroll
   for (int h = 0; h < NSUB; ++h) {
     const bool v_lo = g < nvalid[h], v_hi = g + 8 < nvalid[h];
-    x[h][0] = v_lo ? sc[h][0] * scale_log2 : NEG_INF;
-    x[h][1] = v_lo ? sc[h][1] * scale_log2 : NEG_INF;
-    x[h][2] = v_hi ? sc[h][2] * scale_log2 : NEG_INF;
-    x[h][3] = v_hi ? sc[h][3] * scale_log2 : NEG_INF;
+    x[h][0] = v_lo ? sc[h][0] * s0 : NEG_INF;
+    x[h][1] = v_lo ? sc[h][1] * s1 : NEG_INF;
+    x[h][2] = v_hi ? sc[h][2] * s0 : NEG_INF;
+    x[h][3] = v_hi ? sc[h][3] * s1 : NEG_INF;
     mx0 = fmaxf(mx0, fmaxf(x[h][0], x[h][2]));
     mx1 = fmaxf(mx1, fmaxf(x[h][1], x[h][3]));
   }
