@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(NW * 32)
   // chunks q_chunk(i, c); FP8 caches use 16-dim units 2c + j (two chunks each)
   const int G = a.group;
   uint4 qf[Sh::kQChunks];
-  float scale_log2 = a.scale_log2;
+  float scale0 = a.scale_log2, scale1 = a.scale_log2;  // of heads 2c, 2c + 1
   {
     const T *qrow = static_cast<const T *>(a.query) +
                     (static_cast<int64_t>(seq) * a.num_q_heads + kvh * G + g) * D;
@@ -292,37 +292,8 @@ __global__ void __launch_bounds__(NW * 32)
       const int ch = F8 ? 2 * (c * (D / 64) + (i >> 1)) + (i & 1) : q_chunk(i, c);
       qf[i] = g < G ? *reinterpret_cast<const uint4 *>(qrow + ch * 8) : make_uint4(0, 0, 0, 0);
     }
-    if constexpr (F8 && !std::is_same<T, __half>::value) {
-      // bf16 queries over FP8 caches: the warp holds all G x D query values;
-      // scale them by 2^e so the largest magnitude lands in [2^14, 2^15),
-      // then round to fp16 (exact for every value down to 2^-31 of the
-      // largest: bf16 carries 8 significant bits, and fp16 holds 8 bits at
-      // every magnitude from 2^-17 up), and fold 2^-e into the softmax scale
-      float mx = 0.f;
-#pragma unroll
-      for (int i = 0; i < Sh::kQChunks; ++i)
-#pragma unroll
-        for (int w2 = 0; w2 < 4; ++w2) {
-          const float2 v = Elem<T>::unpack(word_of(qf[i], w2));
-          mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
-        }
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
-      const int ex = static_cast<int>((__float_as_uint(mx) >> 23) & 0xffu) - 127;
-      const int e = min(120, 14 - ex);
-      const float f = ldexpf(1.f, e);
-#pragma unroll
-      for (int i = 0; i < Sh::kQChunks; ++i) {
-        uint32_t w4[4];
-#pragma unroll
-        for (int w2 = 0; w2 < 4; ++w2) {
-          const float2 v = Elem<T>::unpack(word_of(qf[i], w2));
-          w4[w2] = Elem<__half>::pack(v.x * f, v.y * f);
-        }
-        qf[i] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-      }
-      scale_log2 = ldexpf(scale_log2, -e);
-    }
+    if constexpr (F8 && !std::is_same<T, __half>::value)
+      column_scales(a.scale_log2, queries_to_half(qf), c, scale0, scale1);
   }
 
   const float NEG_INF = -INFINITY;
@@ -384,7 +355,7 @@ __global__ void __launch_bounds__(NW * 32)
     // ---- online softmax in base 2 (log2(e) folded into the scale), one
     // reduction over all NSUB x 16 tokens of the step
     float p[NSUB][4];
-    softmax_step<NSUB, Sh::kMTiles>(sc, nvalid, g, scale_log2, scale_log2, m0, m1, l0, l1, acc, p);
+    softmax_step<NSUB, Sh::kMTiles>(sc, nvalid, g, scale0, scale1, m0, m1, l0, l1, acc, p);
 
 #pragma unroll
     for (int h = 0; h < NSUB; ++h) {
