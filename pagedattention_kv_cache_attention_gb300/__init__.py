@@ -792,7 +792,7 @@ def _native():
     global _bind
     _load()
     if not os.path.exists(_build.BIND):
-        raise ImportError(f"{_build.BIND} is missing (it belongs to one version of torch): run "
+        raise ImportError(f"{_build.BIND} is missing (it belongs to one torch and one Python): run "
                           "`python -c 'import __graft_entry__ as g; g.build()'` first")
     spec = importlib.util.spec_from_file_location("pa_bind", _build.BIND)
     module = importlib.util.module_from_spec(spec)

@@ -4,7 +4,8 @@ Each translation unit under csrc/ is compiled by its own nvcc process, in
 parallel, then linked into one shared library with the CUDA runtime linked
 statically.  Beside it the C++ part of the Python binding (pa_bind.cpp) is
 compiled with g++ against the installed torch's headers.  Outputs (git-ignored):
-<package>/_build/libpa.so and <package>/_build/pa_bind-<torch's version>.so.
+<package>/_build/libpa.so and <package>/_build/pa_bind-<torch's version><Python's suffix
+of extension modules>, .cpython-312-x86_64-linux-gnu.so for instance.
 """
 from __future__ import annotations
 
@@ -21,8 +22,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libpa.so")
-# (of one torch: another one's tensors may be laid out otherwise)
-BIND = os.path.join(OUT_DIR, f"pa_bind-{torch.__version__}.so")
+# (of one torch, whose tensors it looks into, and of one Python: it is loaded by this path,
+# which the import system's own check of the suffix does not see)
+BIND = os.path.join(OUT_DIR, f"pa_bind-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
 SOURCES = ("pa_api.cu", "pa_blocks.cu", "pa_cache.cu", "pa_cache_fp4.cu", "pa_decode.cu",
            "pa_decode_fp4.cu", "pa_decode_sparse.cu", "pa_prefill_fp4.cu", "pa_prefill_tc.cu",
            "pa_rope.cu", "pa_sparse.cu", "pa_static_ws.cu")
