@@ -92,19 +92,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
+    bind_obj = os.path.join(OUT_DIR, "pa_bind.o")
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        bind_obj = os.path.join(OUT_DIR, "pa_bind.o")
         bind = ex.submit(_compile_bind, os.path.join(CSRC, "pa_bind.cpp"), bind_obj)
         objs = list(ex.map(compile_one, SOURCES))
-        bind.result()
-    tmp = LIB + f".{os.getpid()}.tmp"
-    cmd = [cc, "-shared", *ARCH, "-o", tmp, *objs, "-cudart", "static"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    _link_bind(bind_obj, OUT_DIR, tmp)
-    os.replace(tmp, BIND)
+        tmp = LIB + f".{os.getpid()}.tmp"
+        _run("link", [cc, "-shared", *ARCH, "-o", tmp, *objs, "-cudart", "static"])
+        os.replace(tmp, LIB)
+        try:  # (what follows needs the headers of Python and torch, which libpa.so does not)
+            bind.result()
+            _link_bind(bind_obj, OUT_DIR, tmp)
+        except (OSError, RuntimeError) as e:
+            raise RuntimeError(f"{LIB} is built; the Python binding of rotated append and sparse "
+                               f"attention is not: {e}") from e
+        os.replace(tmp, BIND)
     return LIB
 
 
