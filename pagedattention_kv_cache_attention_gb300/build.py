@@ -39,13 +39,13 @@ def nvcc() -> str:
     return path
 
 
-def _stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(BIND)):
+def _stale(out: str, *endings: str) -> bool:
+    """Whether `out` is missing, or older than pa.h or a file of csrc/ with one of the endings."""
+    if not os.path.exists(out):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
+    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(endings)]
     deps.append(os.path.join(os.path.dirname(HERE), "include", "pa.h"))
-    return any(os.path.getmtime(d) > t for d in deps)
+    return any(os.path.getmtime(d) > os.path.getmtime(out) for d in deps)
 
 
 def _run(what: str, cmd) -> None:
@@ -74,10 +74,7 @@ def _link_bind(obj: str, lib_dir: str, out: str) -> None:
                                 "-ltorch_python", "-Wl,-rpath,$ORIGIN"])
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
-        return LIB
-    os.makedirs(OUT_DIR, exist_ok=True)
+def _build_lib(verbose: bool) -> None:
     cc = nvcc()
 
     def compile_one(src: str) -> str:
@@ -92,20 +89,34 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    bind_obj = os.path.join(OUT_DIR, "pa_bind.o")
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        bind = ex.submit(_compile_bind, os.path.join(CSRC, "pa_bind.cpp"), bind_obj)
+    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
-        tmp = LIB + f".{os.getpid()}.tmp"
-        _run("link", [cc, "-shared", *ARCH, "-o", tmp, *objs, "-cudart", "static"])
-        os.replace(tmp, LIB)
-        try:  # (what follows needs the headers of Python and torch, which libpa.so does not)
-            bind.result()
-            _link_bind(bind_obj, OUT_DIR, tmp)
-        except (OSError, RuntimeError) as e:
-            raise RuntimeError(f"{LIB} is built; the Python binding of rotated append and sparse "
-                               f"attention is not: {e}") from e
-        os.replace(tmp, BIND)
+    tmp = LIB + f".{os.getpid()}.tmp"
+    _run("link", [cc, "-shared", *ARCH, "-o", tmp, *objs, "-cudart", "static"])
+    os.replace(tmp, LIB)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Makes what is missing or older than its sources: the library, and the binding,
+    which links against it but holds nothing of it."""
+    lib = force or _stale(LIB, ".cu", ".cuh", ".h")
+    bind = force or _stale(BIND, ".cpp")
+    os.makedirs(OUT_DIR, exist_ok=True)
+    bind_obj = os.path.join(OUT_DIR, "pa_bind.o")
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        if bind:
+            compiled = ex.submit(_compile_bind, os.path.join(CSRC, "pa_bind.cpp"), bind_obj)
+        if lib:
+            _build_lib(verbose)
+        if bind:
+            tmp = BIND + f".{os.getpid()}.tmp"
+            try:  # (what follows needs the headers of Python and torch, which libpa.so does not)
+                compiled.result()
+                _link_bind(bind_obj, OUT_DIR, tmp)
+            except (OSError, RuntimeError) as e:
+                raise RuntimeError(f"{LIB} is built; the Python binding of rotated append and sparse "
+                                   f"attention is not: {e}") from e
+            os.replace(tmp, BIND)
     return LIB
 
 
