@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(NW * 32)
       qf[i] = g < G ? *reinterpret_cast<const uint4 *>(qrow + ch * 8) : make_uint4(0, 0, 0, 0);
     }
     if constexpr (F8 && !std::is_same<T, __half>::value)
-      column_scales(a.scale_log2, queries_to_half(qf), c, scale0, scale1);
+      column_scales(a.scale_log2 * queries_to_half(qf), c, scale0, scale1);
   }
 
   const float NEG_INF = -INFINITY;
@@ -331,24 +331,7 @@ __global__ void __launch_bounds__(NW * 32)
       if constexpr (!F8) {
         qk_subtile_16<MT, D>(Ks, qf, g, c, sc[h]);
       } else {
-        sc[h][0] = sc[h][1] = sc[h][2] = sc[h][3] = 0.f;
-        // unit c D/64 + j of rows g and g+8 holds 16 dims: four k16 steps
-        // (rows g and g+8 share their swizzle, so each quarter-warp hits 8
-        // distinct 16-byte units of one 128-byte span)
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-          const int u = c * (D / 64) + j;
-          uint32_t ka[8], kb[8];
-          e4m3x16_to_half(*reinterpret_cast<const uint4 *>(f8_unit<D>(Ks, g, u)), ka);
-          e4m3x16_to_half(*reinterpret_cast<const uint4 *>(f8_unit<D>(Ks, g + 8, u)), kb);
-          const uint32_t q[8] = {qf[2 * j].x, qf[2 * j].y, qf[2 * j].z, qf[2 * j].w,
-                                 qf[2 * j + 1].x, qf[2 * j + 1].y, qf[2 * j + 1].z,
-                                 qf[2 * j + 1].w};
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-            Elem<MT>::mma(sc[h], ka[2 * t], kb[2 * t], ka[2 * t + 1], kb[2 * t + 1], q[2 * t],
-                         q[2 * t + 1]);
-        }
+        qk_subtile_8<D>(Ks, qf, g, c, sc[h]);
       }
     }
 
@@ -368,45 +351,7 @@ __global__ void __launch_bounds__(NW * 32)
       if constexpr (!F8) {
         pv_subtile_16<MT, D>(Vs, nvalid[h], g, c, pb0, pb1, pr0, pr1, acc);
       } else {
-        // MMA row g of m-tile mt is dim dA = pv_dim_a(g, mt), row g+8 is dB:
-        // at head_dim 128 the 16 dims 16g .. 16g+15 (unit g of each row), at
-        // 64 the 8 dims 8g .. 8g+7 (half g % 2 of unit g / 2); each byte
-        // interleave of two rows yields the (token 2c, token 2c+1) pairs of
-        // two m-tiles, still E4M3
-        constexpr int kHi = D == 128 ? 8 : 4;  // byte of dB within the lane's dims
-        uint4 v8[4];
-#pragma unroll
-        for (int ri = 0; ri < 4; ++ri) {
-          const int r = 2 * c + (ri & 1) + 8 * (ri >> 1);
-          uint4 xv;
-          if constexpr (D == 128) {
-            xv = *reinterpret_cast<const uint4 *>(f8_unit<D>(Vs, r, g));
-          } else {
-            const uint2 half_unit =
-                *reinterpret_cast<const uint2 *>(f8_unit<D>(Vs, r, g >> 1) + (g & 1) * 8);
-            xv = make_uint4(half_unit.x, half_unit.y, 0u, 0u);
-          }
-          v8[ri] = r < nvalid[h] ? xv : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int mt = 0; mt < Sh::kMTiles; mt += 2) {
-          const uint32_t w0 = interleave_bytes(v8[0], v8[1], mt);
-          const uint32_t w1 = interleave_bytes(v8[0], v8[1], kHi + mt);
-          const uint32_t w2 = interleave_bytes(v8[2], v8[3], mt);
-          const uint32_t w3 = interleave_bytes(v8[2], v8[3], kHi + mt);
-          {
-            const uint32_t a0 = e4m3x2_lo_to_f16x2(w0), a1 = e4m3x2_lo_to_f16x2(w1);
-            const uint32_t a2 = e4m3x2_lo_to_f16x2(w2), a3 = e4m3x2_lo_to_f16x2(w3);
-            Elem<MT>::mma(acc[mt], a0, a1, a2, a3, pb0, pb1);
-            Elem<MT>::mma(acc[mt], a0, a1, a2, a3, pr0, pr1);
-          }
-          {
-            const uint32_t a0 = e4m3x2_hi_to_f16x2(w0), a1 = e4m3x2_hi_to_f16x2(w1);
-            const uint32_t a2 = e4m3x2_hi_to_f16x2(w2), a3 = e4m3x2_hi_to_f16x2(w3);
-            Elem<MT>::mma(acc[mt + 1], a0, a1, a2, a3, pb0, pb1);
-            Elem<MT>::mma(acc[mt + 1], a0, a1, a2, a3, pr0, pr1);
-          }
-        }
+        pv_subtile_8<D>(Vs, nvalid[h], g, c, pb0, pb1, pr0, pr1, acc);
       }
     }
 

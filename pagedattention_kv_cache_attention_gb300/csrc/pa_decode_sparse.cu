@@ -33,63 +33,6 @@ namespace {
 
 constexpr int kMaxCluster = 8;
 
-// S^T = K Q^T of an FP8 sub-tile: unit c D/64 + j of rows g and g + 8 holds 16
-// dimensions, four k16 steps, widened to fp16 on the way.
-template <int D>
-__device__ __forceinline__ void qk_subtile_8(const uint8_t *Ks, const uint4 (&qf)[D / 32], int g,
-                                             int c, float (&sc)[4]) {
-  sc[0] = sc[1] = sc[2] = sc[3] = 0.f;
-#pragma unroll
-  for (int j = 0; j < D / 64; ++j) {
-    const int u = c * (D / 64) + j;
-    uint32_t ka[8], kb[8];
-    e4m3x16_to_half(*reinterpret_cast<const uint4 *>(f8_unit<D>(Ks, g, u)), ka);
-    e4m3x16_to_half(*reinterpret_cast<const uint4 *>(f8_unit<D>(Ks, g + 8, u)), kb);
-    const uint4 q0 = qf[2 * j], q1 = qf[2 * j + 1];
-    const uint32_t q[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      Elem<__half>::mma(sc, ka[2 * t], kb[2 * t], ka[2 * t + 1], kb[2 * t + 1], q[2 * t],
-                        q[2 * t + 1]);
-  }
-}
-
-// O^T += V^T P^T of an FP8 sub-tile: the lane's dimensions (pv_dim_a, pv_dim_b) of
-// rows 2c, 2c + 1, 2c + 8, 2c + 9; rows from nvalid on are zeros.  Two rows' bytes
-// are interleaved while they are still E4M3: a converted pair is (row, next row).
-template <int D>
-__device__ __forceinline__ void pv_subtile_8(const uint8_t *Vs, int nvalid, int g, int c,
-                                             uint32_t pb0, uint32_t pb1, uint32_t pr0,
-                                             uint32_t pr1, float (&acc)[D / 16][4]) {
-  constexpr int kHi = D == 128 ? 8 : 4;  // byte of pv_dim_b within the lane's dimensions
-  uint4 v[4];
-#pragma unroll
-  for (int ri = 0; ri < 4; ++ri) {
-    const int r = 2 * c + (ri & 1) + 8 * (ri >> 1);
-    v[ri] = make_uint4(0, 0, 0, 0);
-    if constexpr (D == 128) {
-      if (r < nvalid) v[ri] = *reinterpret_cast<const uint4 *>(f8_unit<D>(Vs, r, g));
-    } else {
-      const uint2 half = *reinterpret_cast<const uint2 *>(f8_unit<D>(Vs, r, g >> 1) + (g & 1) * 8);
-      if (r < nvalid) v[ri] = make_uint4(half.x, half.y, 0, 0);
-    }
-  }
-#pragma unroll
-  for (int mt = 0; mt < D / 16; mt += 2) {
-    const uint32_t w0 = interleave_bytes(v[0], v[1], mt), w1 = interleave_bytes(v[0], v[1], kHi + mt);
-    const uint32_t w2 = interleave_bytes(v[2], v[3], mt), w3 = interleave_bytes(v[2], v[3], kHi + mt);
-    const uint32_t a[2][4] = {{e4m3x2_lo_to_f16x2(w0), e4m3x2_lo_to_f16x2(w1),
-                               e4m3x2_lo_to_f16x2(w2), e4m3x2_lo_to_f16x2(w3)},
-                              {e4m3x2_hi_to_f16x2(w0), e4m3x2_hi_to_f16x2(w1),
-                               e4m3x2_hi_to_f16x2(w2), e4m3x2_hi_to_f16x2(w3)}};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      Elem<__half>::mma(acc[mt + i], a[i][0], a[i][1], a[i][2], a[i][3], pb0, pb1);
-      Elem<__half>::mma(acc[mt + i], a[i][0], a[i][1], a[i][2], a[i][3], pr0, pr1);
-    }
-  }
-}
-
 template <typename T, int D, int NW, int S, bool F8, int NSUB>
 __global__ void __launch_bounds__(NW * 32)
     sparse_decode_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -208,7 +151,7 @@ __global__ void __launch_bounds__(NW * 32)
       qf[i] = g < G ? *reinterpret_cast<const uint4 *>(q + ch * 8) : make_uint4(0, 0, 0, 0);
     }
     if constexpr (F8 && !std::is_same<T, __half>::value)
-      column_scales(a.scale_log2, queries_to_half(qf), c, scale0, scale1);
+      column_scales(a.scale_log2 * queries_to_half(qf), c, scale0, scale1);
   }
 
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // heads 2c, 2c + 1

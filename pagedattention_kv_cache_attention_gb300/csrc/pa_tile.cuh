@@ -1,6 +1,5 @@
-// pa_tile.cuh -- the per-sub-tile arithmetic of the paged decode kernel over
-// a 16-bit KV cache, and the sub-tile geometry and softmax step it shares with
-// the FP8 path.
+// pa_tile.cuh -- the per-sub-tile arithmetic of the paged decode kernels (dense
+// and sparse) over 16-bit and FP8 caches, the sub-tile geometry and the softmax step.
 //
 // A sub-tile is 16 consecutive rows of one physical block, K or V, staged in
 // shared memory by 2-D TMA copies in 128-byte boxes of 16 rows with the
@@ -91,10 +90,10 @@ __device__ __forceinline__ float softmax_exp2(float x) { return ex2_approx(x); }
 // bf16 queries beside FP8 keys, which are fp16 in the product: the lane's share of
 // column g times 2^e, as fp16, with e such that the column's largest magnitude lies
 // in [2^14, 2^15) (exact for every value down to 2^-31 of that: bf16 carries 8
-// significant bits, and fp16 holds 8 bits at every magnitude from 2^-17 up).
-// Returns e.  A column's own e: whatever another head of the group holds, an
-// infinity among it, leaves this one's queries as they are.
-template <int N> __device__ __forceinline__ int queries_to_half(uint4 (&qf)[N]) {
+// significant bits, and fp16 holds 8 bits at every magnitude from 2^-17 up), and 120
+// at most.  Returns 2^-e.  A column's own e: whatever another head of the group
+// holds, an infinity among it, leaves this one's queries as they are.
+template <int N> __device__ __forceinline__ float queries_to_half(uint4 (&qf)[N]) {
   float mx = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i)
@@ -105,8 +104,8 @@ template <int N> __device__ __forceinline__ int queries_to_half(uint4 (&qf)[N]) 
     }
   mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
   mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-  const int e = min(120, 14 + 127 - static_cast<int>((__float_as_uint(mx) >> 23) & 0xffu));
-  const float f = ldexpf(1.f, e);
+  const int ex = static_cast<int>(__float_as_uint(mx) >> 23);  // e = min(120, 14 + 127 - ex)
+  const float f = __int_as_float(min(127 + 120, 268 - ex) << 23);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     uint32_t h[4];
@@ -117,12 +116,12 @@ template <int N> __device__ __forceinline__ int queries_to_half(uint4 (&qf)[N]) 
     }
     qf[i] = make_uint4(h[0], h[1], h[2], h[3]);
   }
-  return e;
+  return __int_as_float(max(127 - 120, ex - 14) << 23);
 }
-// The softmax scales of the lane's columns 2c and 2c + 1, with 2^-e of each.
-__device__ __forceinline__ void column_scales(float scale_log2, int e, int c, float &s0, float &s1) {
-  s0 = ldexpf(scale_log2, -__shfl_sync(kFull, e, 8 * c));      // a lane of column 2c
-  s1 = ldexpf(scale_log2, -__shfl_sync(kFull, e, 8 * c + 4));  // of column 2c + 1
+// The softmax scales of the lane's columns 2c and 2c + 1, from that of its column g.
+__device__ __forceinline__ void column_scales(float scale_log2, int c, float &s0, float &s1) {
+  s0 = __shfl_sync(kFull, scale_log2, 8 * c);      // a lane of column 2c
+  s1 = __shfl_sync(kFull, scale_log2, 8 * c + 4);  // of column 2c + 1
 }
 
 // One online-softmax step in base 2 (log2(e) is folded into the scales) over
@@ -234,6 +233,64 @@ __device__ __forceinline__ void pv_subtile_16(const uint8_t *Vs, int nvalid, int
     const uint32_t a3 = pair_of(v[2][bB], v[3][bB], eB);
     Elem<MT>::mma(acc[mt], a0, a1, a2, a3, pb0, pb1);
     Elem<MT>::mma(acc[mt], a0, a1, a2, a3, pr0, pr1);
+  }
+}
+
+// S^T = K Q^T of an FP8 sub-tile: unit c D/64 + j of rows g and g + 8 holds 16
+// dimensions, four k16 steps, widened to fp16 on the way (rows g and g + 8 share their
+// swizzle, so that a quarter-warp reads 8 different units of a 128-byte span).
+template <int D>
+__device__ __forceinline__ void qk_subtile_8(const uint8_t *Ks, const uint4 (&qf)[D / 32], int g,
+                                             int c, float (&sc)[4]) {
+  sc[0] = sc[1] = sc[2] = sc[3] = 0.f;
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j) {
+    const int u = c * (D / 64) + j;
+    uint32_t ka[8], kb[8];
+    e4m3x16_to_half(*reinterpret_cast<const uint4 *>(f8_unit<D>(Ks, g, u)), ka);
+    e4m3x16_to_half(*reinterpret_cast<const uint4 *>(f8_unit<D>(Ks, g + 8, u)), kb);
+    const uint4 q0 = qf[2 * j], q1 = qf[2 * j + 1];
+    const uint32_t q[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      Elem<__half>::mma(sc, ka[2 * t], kb[2 * t], ka[2 * t + 1], kb[2 * t + 1], q[2 * t],
+                        q[2 * t + 1]);
+  }
+}
+
+// O^T += V^T P^T of an FP8 sub-tile: the lane's dimensions (pv_dim_a, pv_dim_b) of
+// rows 2c, 2c + 1, 2c + 8, 2c + 9; rows from nvalid on are zeros.  Two rows' bytes
+// are interleaved while they are still E4M3: a converted pair is (row, next row).
+template <int D>
+__device__ __forceinline__ void pv_subtile_8(const uint8_t *Vs, int nvalid, int g, int c,
+                                             uint32_t pb0, uint32_t pb1, uint32_t pr0,
+                                             uint32_t pr1, float (&acc)[D / 16][4]) {
+  constexpr int kHi = D == 128 ? 8 : 4;  // byte of pv_dim_b within the lane's dimensions
+  uint4 v[4];
+#pragma unroll
+  for (int ri = 0; ri < 4; ++ri) {
+    const int r = 2 * c + (ri & 1) + 8 * (ri >> 1);
+    v[ri] = make_uint4(0, 0, 0, 0);
+    if constexpr (D == 128) {
+      if (r < nvalid) v[ri] = *reinterpret_cast<const uint4 *>(f8_unit<D>(Vs, r, g));
+    } else {
+      const uint2 half = *reinterpret_cast<const uint2 *>(f8_unit<D>(Vs, r, g >> 1) + (g & 1) * 8);
+      if (r < nvalid) v[ri] = make_uint4(half.x, half.y, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int mt = 0; mt < D / 16; mt += 2) {
+    const uint32_t w0 = interleave_bytes(v[0], v[1], mt), w1 = interleave_bytes(v[0], v[1], kHi + mt);
+    const uint32_t w2 = interleave_bytes(v[2], v[3], mt), w3 = interleave_bytes(v[2], v[3], kHi + mt);
+    const uint32_t a[2][4] = {{e4m3x2_lo_to_f16x2(w0), e4m3x2_lo_to_f16x2(w1),
+                               e4m3x2_lo_to_f16x2(w2), e4m3x2_lo_to_f16x2(w3)},
+                              {e4m3x2_hi_to_f16x2(w0), e4m3x2_hi_to_f16x2(w1),
+                               e4m3x2_hi_to_f16x2(w2), e4m3x2_hi_to_f16x2(w3)}};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      Elem<__half>::mma(acc[mt + i], a[i][0], a[i][1], a[i][2], a[i][3], pb0, pb1);
+      Elem<__half>::mma(acc[mt + i], a[i][0], a[i][1], a[i][2], a[i][3], pr0, pr1);
+    }
   }
 }
 
