@@ -596,9 +596,13 @@ pa_status pa_update_key_bounds_fp4(int8_t *bounds, float *bound_scales, const vo
  * a <= 4095 * 2^f, and c_hd = rint(q_hd / 2^f),
  *   I = sum_d (sum_h max(c_hd, 0)) bounds[block, 0, d] + (sum_h min(c_hd, 0)) bounds[block, 1, d]
  *   score = fp32(I) * bound_scales[block]
- * (I a whole number, both roundings fp32): a bound on the sum over the group of
- * q . k, for every key k of the block, in units of 2^f.  A block of scale +inf
- * scores +inf; a group with an infinity or a NaN has c = 0.
+ * (I a whole number, both roundings fp32).  I * bound_scales bounds the sum over the
+ * group of c . k, for every key k of the block: of q . k in units of 2^f, but for the
+ * queries' rounding, up to half a unit for each element of a query times that
+ * channel of the key.  (What is below 2^f / 2 counts for nothing, a whole head that
+ * is 2^13 times smaller than the group's largest, too.)  A block of scale +inf
+ * scores +inf; a group with an infinity or a NaN has c = 0, so that all its heads,
+ * the finite ones too, get the first blocks there are and not those of their queries.
  * A row that sees at most num_selected blocks gets all of them.  Of more, its
  * first num_sink and last num_recent blocks are taken, and then those of the
  * largest scores, of equal ones the first.

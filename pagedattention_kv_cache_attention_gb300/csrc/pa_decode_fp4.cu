@@ -856,7 +856,10 @@ cudaError_t launch_rows(DecodeArgs a, const CUtensorMap &km, const CUtensorMap &
 // one KV head 20 us, with one CTA 93; eight KV heads of 4,096 tokens 11 against
 // 33), and beyond that room a CTA's 4 to 6 us of start and join cost more than
 // the evener load gives (64 sequences of 512 to 4,096 tokens, 20 rows, taken
-// as they come: 82 us alone, 88 in pairs, 115 in fours).
+// as they come: 82 us alone, 88 in pairs, 115 in fours).  Tables per head, 32 / 8
+// heads x 128: 8 rows of 2,048 tokens 11.3 us, 16.5 without clusters; 64 of 512 12.5
+// (two warps a CTA 11.0 and 12.3, but 256 rows of up to 1,024, 64 / 8 heads, 62 us
+// against 53.7 with four).
 int cluster_of(const DecodeArgs &a, int64_t ctas, int warps, int per_sm) {
   const int64_t steps = (static_cast<int64_t>(a.max_blocks_per_seq) << a.bs_log2) / 32;
   int n = 1;

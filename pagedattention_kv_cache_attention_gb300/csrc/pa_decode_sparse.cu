@@ -342,9 +342,11 @@ template <typename T, int D, int NW, int S, bool F8, int NSUB> struct Instance {
 // 2,048 tokens, 32 / 8 heads x 128: 15.0 us; 16.0 with two), else two, of whose CTAs
 // an SM takes six (64 rows of 512 tokens: 23.1 us; 27.9 with four, whose 512 CTAs
 // are more than the 456 that run at once; 23.6 with three, 24.3 with one).  FP8
-// caches: four (256 rows of up to 1,024 tokens, 64 / 8 heads x 128: 67 us; 72 with
-// two or three, 79 with one, 98 with eight).  Three stages in place of two:
-// 23.5 and 77 us with two warps, 24.8 and 76 with four.
+// caches: four (256 rows of up to 1,024 tokens, 64 / 8 heads x 128: 67 us; 71 with
+// two, 72 with three, 79 with one, 98 with eight; 8 rows of 2,048 tokens, 32 / 8 heads
+// 11.1 us, 12.1 with two).  For 64 rows of 512 tokens two would be better, for the
+// reason above: 14.1 us, 17.6 with four.  Three stages in place of two: 23.5 and 77 us
+// with two warps, 24.8 and 76 with four.
 template <typename T, int D>
 cudaError_t launch_d(const DecodeArgs &a, bool kv_fp8, const CUtensorMap &km,
                      const CUtensorMap &vm, cudaStream_t stream) {

@@ -77,8 +77,9 @@ struct DecodeArgs {
   // CTAs of a cluster that share the keys of an unsplit call over FP4 caches
   int cluster;
   int by_length;  // FP4: CTAs take the longest contexts first (seq_by_length)
-  // pa_decode_sparse: block_tables [B, Hkv, max_blocks_per_seq] and context_lens [B, Hkv]
-  // (read by pa_decode_sparse.cu and pa_decode_fp4.cu)
+  // pa_decode_sparse: block_tables [B, Hkv, max_blocks_per_seq] and context_lens [B, Hkv].
+  // (Read by pa_decode_fp4.cu, whose kernel takes both kinds; pa_decode_sparse.cu takes
+  // no other.)
   int per_head;
 };
 

@@ -9,7 +9,7 @@
 //
 // Score of a block for a KV head's group of queries.  The queries become
 // integers c = rint(q / 2^f), 2^f the least power of two with the group's
-// largest magnitude <= 4095 2^f.  The bounds of the group's heads add up to
+// largest magnitude <= 4095 2^f.  The bounds of c 2^f, all heads, add up to
 //   2^f 2^e I,   I = sum_d P_d hi_d + N_d lo_d,
 //   P_d, N_d = the sums of the group's positive, of its negative c_d,
 // one integer product of 2 D terms for the whole group: |P_d| + |N_d| <= 8 * 4095,
